@@ -395,6 +395,73 @@ KV_API int kv_unpack_blocks_signal(const kv_cache_desc *dst, int32_t dst_slice_o
 KV_API int kv_wait_signal(const kv_signal *signal, uint64_t expected, uint32_t timeout_us, int32_t *status_out,
                           kv_stream_t stream);
 
+/* Element types of the attention calls. */
+enum { KV_BF16 = 0, KV_F16 = 1 };
+
+/*
+ * The new tokens of a ragged batch and the paged rows they attend to.  All pointers are device memory.
+ * Request r's new tokens are rows [q_offsets[r], q_offsets[r + 1]) of q (q_offsets[0] = 0), and its cache
+ * holds kv_lens[r] tokens, the new ones last: new token i of request r stands at position
+ * kv_lens[r] - q_len + i, and token j of the cache is slot j % block_size of page
+ * block_table[r * bt_row_stride + j / block_size].  The lengths are read on the device, so a captured
+ * graph follows them.  n_tokens is the capacity of q in tokens; rows at and past q_offsets[n_reqs] are
+ * not read and their outputs not written.  A request may have no new tokens, or no cached ones.
+ */
+typedef struct {
+    const int32_t *block_table; /* [n_reqs, max_blocks_per_req], row stride bt_row_stride (elements) */
+    int32_t n_reqs;
+    int32_t max_blocks_per_req;
+    int64_t bt_row_stride;
+    const int32_t *q_offsets; /* [n_reqs + 1] */
+    const int32_t *kv_lens;   /* [n_reqs] */
+    int64_t n_tokens;
+} kv_attn_batch;
+
+/*
+ * Softmax attention.  Query head h uses key head h / (n_heads / n_kv_heads).  causal: a token sees keys
+ * at positions <= its own; otherwise all kv_lens[r].  window > 0 (causal only): of these only the last
+ * `window`, and pages wholly before them are never read, so their table entries may be stale.  scale > 0
+ * multiplies the products.
+ */
+typedef struct {
+    int32_t dtype; /* KV_BF16 or KV_F16: of q, the cache and out */
+    int32_t n_heads;
+    int32_t n_kv_heads;
+    int32_t head_dim;   /* of q and the keys: a multiple of 8, <= 192 */
+    int32_t head_dim_v; /* of the values and out: a multiple of 8, <= 128 */
+    int32_t causal;
+    int32_t window;
+    float scale;
+} kv_attn_desc;
+
+/* Device workspace bytes that one kv_attention or kv_latent_attention call needs on the current device,
+ * whatever its sizes.  Calls sharing a workspace must be ordered. */
+KV_API int kv_attention_workspace_bytes(int64_t *bytes_out);
+
+/*
+ * kv_attention [S "batch tensor 组装" and "Paged kv cache": the model's forward reads the cache through the
+ * block table]: attention of new tokens, one or a chunk of each request, over the paged cache,
+ *     out[t, h] = sum_j p_j V[j],  p = softmax over the keys j that t sees of scale * q[t, h] . K[j],
+ * for rows already written to the cache (kv_write_tokens).  Keys are plane k_plane of tensor k_tensor of
+ * *k, rows of n_kv_heads * head_dim elements; values likewise of *v (k and v may be one descriptor; their
+ * block sizes are equal).  q: [n_tokens, n_heads, head_dim] and out: [n_tokens, n_heads, head_dim_v] with
+ * byte strides of tokens and heads.  lse (float [n_tokens, n_heads], may be NULL): the natural logarithm
+ * of the sum of the exponentials.  A row that sees nothing gets out 0 and lse -inf.  Products and sums are
+ * held in 32 bits; the weights p are rounded to the element type before they multiply the values.
+ * Slots at and past kv_lens[r], and before every window, are not used whatever they hold; the
+ * tokens a request does hold must be finite.
+ *  - q_offsets that decrease or leave [0, n_tokens] are clamped and set KV_DERR_LIST; a kv_len outside
+ *    [0, max_blocks_per_req * block_size] is clamped, and a table entry outside the cache reads as a
+ *    page of zeros: both set KV_DERR_TABLE.
+ *  - out must not overlap q, the cache or the workspace.
+ * Limits: n_tokens * n_heads and max_blocks_per_req * block_size <= 2^30 (KV_ERR_UNSUPPORTED).
+ * The result does not depend on timing: the same call gives the same bits.
+ */
+KV_API int kv_attention(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_cache_desc *k, int32_t k_tensor,
+                        int32_t k_plane, const kv_cache_desc *v, int32_t v_tensor, int32_t v_plane, const void *q,
+                        int64_t q_token_stride, int64_t q_head_stride, void *out, int64_t out_token_stride,
+                        int64_t out_head_stride, float *lse, void *workspace, int64_t workspace_bytes, kv_stream_t stream);
+
 /*
  * kv_get_last_error: copies the current device's sticky error word (KV_DERR_* bits) to
  * *host_out after the work queued on `stream` so far, clears it when clear != 0, and

@@ -1,0 +1,676 @@
+// kv_attention: softmax attention of a ragged batch of new tokens over paged keys and values.
+//
+// out = softmax(scale q K^T) V, one pass over the keys: a row keeps the running maximum m and the
+// running sum l of 2^(c (s - m)) (c = scale log2 e), and the accumulator O is multiplied by
+// 2^(c (m_old - m_new)) when m moves.  Partial results of disjoint key ranges join the same way.
+//
+// One persistent CTA per SM walks its piece of the batch's line of key tiles (kv_plan.cuh).  A unit
+// is up to 256 query rows (tokens x heads of one key head's group) and its key tiles of 128 keys:
+//   warp 0        loads: one tiled TMA per (64-element panel, run of slots inside a page) into rings of
+//                 K and V tiles, the page ids looked up one tile ahead
+//   warp 1        one thread issues every tcgen05.mma: S = Q K^T and O += P V, accumulators in TMEM
+//   warps 4-7, 8-11   two softmax groups, a thread per row: S from TMEM, maximum, exponentials, P back to
+//                 TMEM (over S) as the A operand of the second product, O rescaled only when the
+//                 maximum has grown by more than 2^8 (P stays below 2^8, far inside 16-bit range, so
+//                 most tiles touch O not at all)
+// TMEM: S0, S1 (128 columns each) and O0, O1 (128 columns each).  With more than 128 rows the two groups
+// own 128 rows each and share every K and V tile; with fewer (decoding) they take the even and the odd
+// key tiles of the same rows and are joined through TMEM, so both ways keep two tiles in flight between
+// the tensor core and the exponentials.
+#include <cmath>
+
+#include "kv_attention.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kRows = 256;  // rows of a unit
+constexpr uint32_t kPanel = 128 * 128;  // bytes of a 64-element panel of 128 rows
+
+template <int DK, int DV>
+struct Shape {
+    static constexpr uint32_t kQ = 128 * DK * 2, kK = 128 * DK * 2, kV = 128 * DV * 2;
+    static constexpr int kNK = DK == 64 ? 5 : DK == 128 ? 3 : 2;  // ring depths: what 227 KB holds
+    static constexpr int kNV = DK == 64 ? 5 : DK == 128 ? 2 : 1;
+    static constexpr uint32_t kOffK = 2 * kQ, kOffV = kOffK + kNK * kK, kOffAux = kOffV + kNV * kV;
+    static constexpr uint32_t kBytes = kOffAux + 2048;
+};
+
+struct Params {
+    Batch b;
+    const int32_t *table;
+    int64_t table_stride;
+    int32_t num_blocks;
+    FastDiv block;       // slots of a page
+    int32_t piece_rows;  // slots one TMA brings: gcd(block, 128), so it never leaves a page
+    int32_t dk, dv, heads;
+    float scale, c;  // c = scale * log2 e
+    const char *q;
+    int64_t q_token, q_head;
+    char *out;
+    int64_t out_token, out_head;
+    float *lse;
+    float *ws;
+    Place *places;
+};
+
+// Bookkeeping at the end of shared memory.
+struct Aux {
+    uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
+    uint64_t s_full[2], p_ready[2], o_done[2], q_full[2], q_empty, merge_ready, merge_free;
+    long long scan[33];
+    Place place;
+    float m[128], l[128];  // the odd tiles' group, for the join
+    uint32_t tmem;
+    int gave_up;
+};
+static_assert(sizeof(Aux) <= 2048, "bookkeeping");
+
+// One row of the output from its accumulator: 32 columns of it.
+template <bool Bf16>
+__device__ __forceinline__ void store_row32(char *to, const float (&o)[32], float inv, int col, int dv)
+{
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        if (col + 8 * i < dv) {
+            uint4 v;
+            v.x = pack2<Bf16>(o[8 * i] * inv, o[8 * i + 1] * inv);
+            v.y = pack2<Bf16>(o[8 * i + 2] * inv, o[8 * i + 3] * inv);
+            v.z = pack2<Bf16>(o[8 * i + 4] * inv, o[8 * i + 5] * inv);
+            v.w = pack2<Bf16>(o[8 * i + 6] * inv, o[8 * i + 7] * inv);
+            *reinterpret_cast<uint4 *>(to + (col + 8 * i) * 2) = v;
+        }
+    }
+}
+
+template <int DK, int DV, bool Bf16>
+__global__ void __launch_bounds__(kThreads, 1)
+attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const Params p)
+{
+    using S = Shape<DK, DV>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const uint32_t base = smem_addr(smem);
+    Aux &aux = *reinterpret_cast<Aux *>(smem + S::kOffAux);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Batch &b = p.b;
+    const Waiter wait{&aux.gave_up, b.err};
+
+    if (tid == 0) {
+        aux.gave_up = 0;
+        for (int i = 0; i < S::kNK; i++) mbar_init(smem_addr(&aux.k_full[i]), 1), mbar_init(smem_addr(&aux.k_empty[i]), 1);
+        for (int i = 0; i < S::kNV; i++) mbar_init(smem_addr(&aux.v_full[i]), 1), mbar_init(smem_addr(&aux.v_empty[i]), 1);
+        for (int i = 0; i < 2; i++) {
+            mbar_init(smem_addr(&aux.s_full[i]), 1);
+            mbar_init(smem_addr(&aux.p_ready[i]), 128);
+            mbar_init(smem_addr(&aux.o_done[i]), 1);
+            mbar_init(smem_addr(&aux.q_full[i]), 128);
+        }
+        mbar_init(smem_addr(&aux.q_empty), 1);
+        mbar_init(smem_addr(&aux.merge_ready), 128);
+        mbar_init(smem_addr(&aux.merge_free), 128);
+        mbar_init_fence();
+        tma_prefetch_map(&k_map);
+        tma_prefetch_map(&v_map);
+    }
+    if (warp == 2) tmem_alloc(smem_addr(&aux.tmem), 512);
+    grid_dep_entry();
+    const int tiles = find_piece<kThreads>(b, blockIdx.x, gridDim.x, aux.scan, &aux.place, blockIdx.x == 0);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = aux.tmem;
+    if (tid == 0) {
+        Place pl = aux.place;
+        if (tiles <= 0) pl.req = -1;
+        p.places[blockIdx.x] = pl;
+    }
+
+    Walk w;
+    const bool any = w.start(b, aux.place, tiles);
+    if (!any) {
+        // nothing to do: on to the common exit
+    } else if (warp == 0) {
+        // ---- loads ----
+        const int pr = p.piece_rows, pieces = kTile / pr;
+        int it = 0;
+        do {
+            if (w.u.tiles == 0) continue;
+            const int32_t *row = p.table + (int64_t)w.at.req * p.table_stride;
+            const int kt0 = w.u.tile0 + w.at.off;
+            bool ok = true;
+            for (int t = 0; t < w.n; t++, it++) {
+                const int kb = (kt0 + t) * kTile;
+                const int p0 = max(0, w.u.lo - kb) / pr, p1 = (min(w.u.hi - kb, kTile) + pr - 1) / pr;
+                const int sk = it % S::kNK, sv = it % S::kNV;
+                const uint32_t kbar = smem_addr(&aux.k_full[sk]), vbar = smem_addr(&aux.v_full[sv]);
+                // this lane's first page, looked up before the waits
+                int page = 0, slot = 0;
+                const auto find = [&](int i) {
+                    const uint32_t key = (uint32_t)(kb + i * pr), col = fdiv(key, p.block);
+                    slot = (int)(key - col * p.block.d);
+                    page = __ldg(row + col);
+                    if (page < 0 || page >= p.num_blocks) {
+                        set_error(b.err, KV_DERR_TABLE);
+                        page = p.num_blocks;  // outside the map: reads zeros
+                    }
+                };
+                if (p0 + lane < p1) find(p0 + lane);
+                const int page0 = page, slot0 = slot;
+                if (it >= S::kNK && !wait.warp(smem_addr(&aux.k_empty[sk]), ((it / S::kNK) - 1) & 1)) { ok = false; break; }
+                if (lane == 0) mbar_arrive_expect_tx(kbar, (uint32_t)((p1 - p0) * pr) * DK * 2);
+                __syncwarp();
+                for (int i = p0 + lane; i < p1; i += 32) {
+                    if (i >= p0 + 32) find(i);
+#pragma unroll
+                    for (int h = 0; h < DK / 64; h++)
+                        tma_load_4d(base + S::kOffK + sk * S::kK + h * kPanel + i * pr * 128, &k_map, kbar, h * 64, w.at.head, slot, page);
+                }
+                page = page0, slot = slot0;
+                if (it >= S::kNV && !wait.warp(smem_addr(&aux.v_empty[sv]), ((it / S::kNV) - 1) & 1)) { ok = false; break; }
+                if (lane == 0) mbar_arrive_expect_tx(vbar, (uint32_t)((p1 - p0) * pr) * DV * 2);
+                __syncwarp();
+                for (int i = p0 + lane; i < p1; i += 32) {
+                    if (i >= p0 + 32) find(i);
+#pragma unroll
+                    for (int h = 0; h < DV / 64; h++)
+                        tma_load_4d(base + S::kOffV + sv * S::kV + h * kPanel + i * pr * 128, &v_map, vbar, h * 64, w.at.head, slot, page);
+                }
+                (void)pieces;
+            }
+            if (!ok) break;
+        } while (w.next(b));
+    } else if (warp == 1) {
+        // ---- matrix products: one thread ----
+        if (lane == 0) {
+            constexpr uint32_t qk_desc = mma_desc(Bf16, 128, 128, false), pv_desc = mma_desc(Bf16, 128, DV, true);
+            int it = 0, steps[2] = {0, 0}, qs[2] = {0, 0};
+            bool ok = true;
+            do {
+                if (w.u.tiles == 0) continue;
+                const bool both = w.u.rows > 128;
+                const int n = both ? 2 * w.n : w.n;
+                ok = wait.one(smem_addr(&aux.q_full[0]), qs[0]++ & 1) && (!both || wait.one(smem_addr(&aux.q_full[1]), qs[1]++ & 1));
+                if (!ok) break;
+                tc_fence_after();
+                const auto qk = [&](int i) {
+                    const int s = i & 1, kt = it + (both ? i >> 1 : i), slot = kt % S::kNK;
+                    if ((!both || s == 0) && !wait.one(smem_addr(&aux.k_full[slot]), (kt / S::kNK) & 1)) return false;
+                    const uint32_t qa = base + (both && s ? S::kQ : 0), ka = base + S::kOffK + slot * S::kK;
+#pragma unroll
+                    for (int kk = 0; kk < DK / 16; kk++) {
+                        const uint32_t o = (kk / 4) * kPanel + (kk % 4) * 32;
+                        mma_ss(tmem + s * 128, smem_desc(qa + o, 16, 1024), smem_desc(ka + o, 16, 1024), qk_desc, kk > 0);
+                    }
+                    tc_commit(smem_addr(&aux.s_full[s]));
+                    if (!both || s == 1) tc_commit(smem_addr(&aux.k_empty[slot]));
+                    if (i == n - 1) tc_commit(smem_addr(&aux.q_empty));
+                    return true;
+                };
+                ok = qk(0) && (n < 2 || qk(1));
+                for (int i = 0; ok && i < n; i++) {
+                    const int s = i & 1, vt = it + (both ? i >> 1 : i), slot = vt % S::kNV;
+                    ok = wait.one(smem_addr(&aux.p_ready[s]), steps[s]++ & 1) &&
+                         ((both && s) || wait.one(smem_addr(&aux.v_full[slot]), (vt / S::kNV) & 1));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t va = base + S::kOffV + slot * S::kV;
+#pragma unroll
+                    for (int kk = 0; kk < 8; kk++)
+                        mma_ts(tmem + 256 + s * 128, tmem + s * 128 + kk * 8, smem_desc(va + kk * 2048, kPanel, 1024), pv_desc,
+                               i >= 2 || kk > 0);
+                    if (!both || s == 1) tc_commit(smem_addr(&aux.v_empty[slot]));
+                    tc_commit(smem_addr(&aux.o_done[s]));  // last: the groups wait for it before the CTA ends
+                    if (i + 2 < n) ok = qk(i + 2);
+                }
+                it += w.n;
+            } while (ok && w.next(b));
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ---- softmax: group g, a thread per row ----
+        const int g = (warp - 4) >> 2, t = tid & 127;
+        const uint32_t mine = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_at = tmem + g * 128 + mine, o_at = tmem + 256 + g * 128 + mine;
+        const float slack = 8.0f / p.c;  // how far the maximum may grow before O is rescaled
+        int it = 0, steps = 0, loads = 0, joins = 0;
+        bool owes_free = false;  // the even group may still be reading this (odd) group's O
+        bool ok = true;
+        do {
+            const bool both = w.u.rows > 128;
+            const int row = both ? g * 128 + t : t;            // row of the unit
+            const bool live = row < w.u.rows;
+            const int r = w.u.row0 + min(row, w.u.rows - 1);   // row of the request; spare rows repeat the last
+            const int tok = (int)fdiv((uint32_t)r, b.group), head = w.at.head * (int)b.group.d + r - tok * (int)b.group.d;
+            const int64_t out_row = (int64_t)(w.q.q0 + tok);
+            char *to = p.out + out_row * p.out_token + (int64_t)head * p.out_head;
+            if (w.u.tiles == 0) {  // nothing is seen
+                if (live && (both || g == 0)) {
+                    for (int col = 0; col < p.dv; col += 8) *reinterpret_cast<uint4 *>(to + col * 2) = make_uint4(0, 0, 0, 0);
+                    if (p.lse) p.lse[out_row * p.heads + head] = -INFINITY;
+                }
+                continue;
+            }
+            // Q
+            if (both || g == 0) {
+                if (loads && !wait.warp(smem_addr(&aux.q_empty), (loads - 1) & 1)) { ok = false; break; }
+                const uint32_t qa = base + g * S::kQ;
+                constexpr int kChunks = DK / 8;
+#pragma unroll 8
+                for (int i = t; i < 128 * kChunks; i += 128) {
+                    const int rr = i / kChunks, cc = i % kChunks, ur = w.u.row0 + (both ? g * 128 : 0) + rr;
+                    if (ur < w.u.row0 + w.u.rows) {
+                        const int tt = (int)fdiv((uint32_t)ur, b.group), hh = w.at.head * (int)b.group.d + ur - tt * (int)b.group.d;
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (cc * 8 < p.dk)
+                            v = *reinterpret_cast<const uint4 *>(p.q + (int64_t)(w.q.q0 + tt) * p.q_token + (int64_t)hh * p.q_head + cc * 16);
+                        st_smem16(qa + (cc / 8) * kPanel + panel_off(rr, cc & 7), v);
+                    }
+                }
+                fence_async_smem();
+                mbar_arrive(smem_addr(&aux.q_full[g]));
+            }
+            loads++;
+            // key tiles
+            int lo, hi;
+            sees(b, w.q, tok, lo, hi);
+            const bool warp_live = __any_sync(0xffffffffu, live);
+            float m = -INFINITY, l = 0.0f;
+            const int first = both ? 0 : g, step = both ? 1 : 2, kt0 = w.u.tile0 + w.at.off;
+            for (int k = first; k < w.n; k += step) {
+                const int kb = (kt0 + k) * kTile, vt = it + k;
+                if (!wait.warp(smem_addr(&aux.s_full[g]), steps & 1)) { ok = false; break; }
+                tc_fence_after();
+                if (warp_live) {
+                    uint32_t x[4][32];
+#pragma unroll
+                    for (int q = 0; q < 4; q++) tmem_ld32(s_at + q * 32, x[q]);
+                    tc_wait_ld();
+                    if (__any_sync(0xffffffffu, kb < lo || kb + kTile > hi)) {
+                        const int a = lo - kb, z = hi - kb;
+#pragma unroll
+                        for (int q = 0; q < 4; q++)
+#pragma unroll
+                            for (int i = 0; i < 32; i++)
+                                if (q * 32 + i < a || q * 32 + i >= z) x[q][i] = 0xff800000u;
+                    }
+                    float mx[4];
+#pragma unroll
+                    for (int q = 0; q < 4; q++) {
+                        mx[q] = __uint_as_float(x[q][0]);
+#pragma unroll
+                        for (int i = 1; i < 32; i++) mx[q] = fmaxf(mx[q], __uint_as_float(x[q][i]));
+                    }
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    const bool grow = top > m + slack;  // -inf + slack: the first finite score
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float to_m = grow ? top : m;
+                        const float alpha = grow ? exp2_fast((m - to_m) * p.c) : 1.0f;
+                        l *= alpha;
+                        m = to_m;
+                        if (k > first) {
+                            if (!wait.warp(smem_addr(&aux.o_done[g]), (steps - 1) & 1)) { ok = false; break; }
+                            tc_fence_after();
+#pragma unroll
+                            for (int q = 0; q < DV / 32; q++) {
+                                uint32_t o[32];
+                                tmem_ld32(o_at + q * 32, o);
+                                tc_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                                tmem_st32(o_at + q * 32, o);
+                            }
+                        }
+                    }
+                    const float mc = m == -INFINITY ? 0.0f : m * p.c;
+                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int q = 0; q < 4; q += 2) {
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int i = 0; i < 64; i += 2) {
+                            const float e0 = exp2_fast(fmaf(__uint_as_float(x[q + i / 32][i % 32]), p.c, -mc));
+                            const float e1 = exp2_fast(fmaf(__uint_as_float(x[q + i / 32][i % 32 + 1]), p.c, -mc));
+                            sum[i / 2 % 4] += e0 + e1;
+                            pk[i / 2] = pack2<Bf16>(e0, e1);
+                        }
+                        tmem_st32(s_at + q * 16, pk);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tc_wait_st();
+                }
+                // rows of V that no query sees must not reach the product: they may hold anything
+                if (kb < w.u.lo || kb + kTile > w.u.hi) {
+                    if (!wait.warp(smem_addr(&aux.v_full[vt % S::kNV]), (vt / S::kNV) & 1)) { ok = false; break; }
+                    if (kb + t < w.u.lo || kb + t >= w.u.hi) {
+                        const uint32_t va = base + S::kOffV + (vt % S::kNV) * S::kV + t * 128;
+#pragma unroll
+                        for (int h = 0; h < DV / 64; h++)
+#pragma unroll
+                            for (int c = 0; c < 8; c++) st_smem16(va + h * kPanel + c * 16, make_uint4(0, 0, 0, 0));
+                    }
+                    fence_async_smem();
+                }
+                if (owes_free) {  // this step's product overwrites O
+                    if (!wait.warp(smem_addr(&aux.merge_free), (joins - 1) & 1)) { ok = false; break; }
+                    owes_free = false;
+                }
+                tc_fence_before();
+                mbar_arrive(smem_addr(&aux.p_ready[g]));
+                steps++;
+            }
+            if (!ok) break;
+            it += w.n;
+            const bool had = first < w.n;
+            if (had && !wait.warp(smem_addr(&aux.o_done[g]), (steps - 1) & 1)) { ok = false; break; }
+            tc_fence_after();
+            if (!both) joins++;
+            if (!both && g == 1) {
+                // the even tiles' group joins and writes
+                if (owes_free) {  // it had no step in this unit: the last join must be over before its m, l go
+                    if (!wait.warp(smem_addr(&aux.merge_free), (joins - 2) & 1)) { ok = false; break; }
+                }
+                aux.m[t] = m;
+                aux.l[t] = l;
+                tc_fence_before();
+                mbar_arrive(smem_addr(&aux.merge_ready));
+                owes_free = true;
+                continue;
+            }
+            float a0 = 1.0f, a1 = 0.0f;
+            const bool join = !both && w.n > 1;
+            if (!both) {
+                if (!wait.warp(smem_addr(&aux.merge_ready), (joins - 1) & 1)) { ok = false; break; }
+                tc_fence_after();
+                const float m1 = aux.m[t], l1 = aux.l[t], top = fmaxf(m, m1);
+                if (top > -INFINITY) {
+                    a0 = exp2_fast((m - top) * p.c);
+                    a1 = exp2_fast((m1 - top) * p.c);
+                }
+                l = l * a0 + l1 * a1;
+                m = top;
+            }
+            const bool whole = w.whole();
+            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+            const int slot = 2 * blockIdx.x + (w.at.off == 0 ? 1 : 0);
+            float *part = p.ws + (int64_t)slot * (kRows * (DV + 2));
+            if (warp_live) {
+#pragma unroll
+                for (int q = 0; q < DV / 32; q++) {
+                    uint32_t o[32];
+                    tmem_ld32(o_at + q * 32, o);
+                    float f[32];
+                    if (join) {
+                        uint32_t o1[32];
+                        tmem_ld32(o_at + 128 + q * 32, o1);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; i++) f[i] = __uint_as_float(o[i]) * a0 + __uint_as_float(o1[i]) * a1;
+                    } else {
+                        tc_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; i++) f[i] = __uint_as_float(o[i]);
+                    }
+                    if (l == 0.0f) {
+#pragma unroll
+                        for (int i = 0; i < 32; i++) f[i] = 0.0f;
+                    }
+                    if (live) {
+                        if (whole) {
+                            store_row32<Bf16>(to, f, inv, q * 32, p.dv);
+                        } else {
+                            float4 *d = reinterpret_cast<float4 *>(part + row * DV + q * 32);
+#pragma unroll
+                            for (int i = 0; i < 8; i++) d[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                        }
+                    }
+                }
+                if (live) {
+                    if (whole) {
+                        if (p.lse) p.lse[out_row * p.heads + head] = l > 0.0f ? fmaf(m, p.scale, logf(l)) : -INFINITY;
+                    } else {
+                        part[kRows * DV + row] = m;
+                        part[kRows * DV + kRows + row] = l;
+                    }
+                }
+            }
+            if (!both) {
+                tc_fence_before();
+                mbar_arrive(smem_addr(&aux.merge_free));
+            }
+        } while (w.next(b));
+        (void)ok;
+    }
+    // common exit
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (aux.gave_up) {  // let copies in flight land before the shared memory is given back
+        const unsigned long long t0 = now_ns();
+        while (now_ns() - t0 < 10000000ull) {}
+    }
+    if (warp == 2) tmem_free(tmem, 512);
+}
+
+// Joins the fragments of the units that were cut: block (c, y) looks whether the cut before CTA c is the
+// first one inside its unit, and joins rows y, y + gridDim.y, ... of it.  A row's fragments are read in
+// the order of their keys, so the result does not depend on timing.
+template <int DV, bool Bf16>
+__global__ void __launch_bounds__(256) join_kernel(const Params p, int parts, int ws_rows)
+{
+    grid_dep_entry();
+    const Batch &b = p.b;
+    const int c = blockIdx.x + 1;
+    const Place pl = p.places[c];
+    if (pl.req < 0 || pl.off == 0) return;
+    const Place before = p.places[c - 1];
+    const auto same = [&](const Place &o) { return o.req == pl.req && o.head == pl.head && o.unit == pl.unit; };
+    if (same(before) && before.off != 0) return;  // an earlier cut of the unit joins it
+    int last = c;
+    while (last + 1 < parts) {
+        const Place nx = p.places[last + 1];
+        if (!same(nx) || nx.off == 0) break;
+        last++;
+    }
+    const Request q = load_request(b, pl.req);
+    const Unit u = make_unit(b, q, pl.unit);
+    const int64_t stride = (int64_t)ws_rows * (DV + 2);
+    constexpr int kLanes = DV / 8, kRowsPerPass = 256 / kLanes;
+    const int col = (threadIdx.x % kLanes) * 8;
+    for (int row = blockIdx.y * kRowsPerPass + threadIdx.x / kLanes; row < u.rows; row += gridDim.y * kRowsPerPass) {
+        float top = -INFINITY;
+        for (int x = c - 1; x <= last; x++) {
+            const float *part = p.ws + (2 * x + (x == c - 1)) * stride;
+            top = fmaxf(top, part[(int64_t)ws_rows * DV + row]);
+        }
+        float o[8] = {0, 0, 0, 0, 0, 0, 0, 0}, l = 0.0f;
+        if (top > -INFINITY) {
+#pragma unroll 4
+            for (int x = c - 1; x <= last; x++) {
+                const float *part = p.ws + (2 * x + (x == c - 1)) * stride;
+                const float a = exp2_fast((part[(int64_t)ws_rows * DV + row] - top) * p.c);
+                l += part[(int64_t)ws_rows * (DV + 1) + row] * a;
+                const float4 v0 = *reinterpret_cast<const float4 *>(part + (int64_t)row * DV + col);
+                const float4 v1 = *reinterpret_cast<const float4 *>(part + (int64_t)row * DV + col + 4);
+                o[0] += v0.x * a, o[1] += v0.y * a, o[2] += v0.z * a, o[3] += v0.w * a;
+                o[4] += v1.x * a, o[5] += v1.y * a, o[6] += v1.z * a, o[7] += v1.w * a;
+            }
+        }
+        const int r = u.row0 + row, tok = (int)fdiv((uint32_t)r, b.group);
+        const int head = pl.head * (int)b.group.d + r - tok * (int)b.group.d;
+        const int64_t out_row = (int64_t)(q.q0 + tok);
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        if (col < p.dv) {
+            uint4 v;
+            v.x = pack2<Bf16>(o[0] * inv, o[1] * inv);
+            v.y = pack2<Bf16>(o[2] * inv, o[3] * inv);
+            v.z = pack2<Bf16>(o[4] * inv, o[5] * inv);
+            v.w = pack2<Bf16>(o[6] * inv, o[7] * inv);
+            *reinterpret_cast<uint4 *>(p.out + out_row * p.out_token + (int64_t)head * p.out_head + col * 2) = v;
+        }
+        if (col == 0 && p.lse) p.lse[out_row * p.heads + head] = l > 0.0f ? fmaf(top, p.scale, logf(l)) : -INFINITY;
+    }
+}
+
+template <int DK, int DV, bool Bf16>
+int launch_attention(const CUtensorMap &km, const CUtensorMap &vm, const Params &p, int parts, cudaStream_t s, bool prepare)
+{
+    const auto kernel = attention_kernel<DK, DV, Bf16>;
+    if (prepare)
+        return cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<DK, DV>::kBytes));
+    int st = cuda_status(launch(kernel, dim3(parts), dim3(kThreads), Shape<DK, DV>::kBytes, s, km, vm, p));
+    if (st != KV_OK || parts < 2) return st;
+    return cuda_status(launch(join_kernel<DV, Bf16>, dim3(parts - 1, 8), dim3(256), 0, s, p, parts, kRows));
+}
+
+template <bool Bf16>
+int pick_attention(int dk, int dv, const CUtensorMap &km, const CUtensorMap &vm, const Params &p, int parts, cudaStream_t s, bool prepare)
+{
+    if (dk <= 64 && dv <= 64) return launch_attention<64, 64, Bf16>(km, vm, p, parts, s, prepare);
+    if (dk <= 128) return launch_attention<128, 128, Bf16>(km, vm, p, parts, s, prepare);
+    return launch_attention<192, 128, Bf16>(km, vm, p, parts, s, prepare);
+}
+
+}  // namespace
+
+int check_batch(const kv_attn_batch *t)
+{
+    if (t == nullptr || t->n_reqs < 0 || t->n_tokens < 0 || t->max_blocks_per_req < 0 || t->bt_row_stride < 0) return KV_ERR_INVALID_ARG;
+    if (t->n_reqs > 0 && (t->q_offsets == nullptr || t->kv_lens == nullptr || (t->block_table == nullptr && t->max_blocks_per_req > 0)))
+        return KV_ERR_INVALID_ARG;
+    if (t->n_reqs > 1 && t->bt_row_stride < t->max_blocks_per_req) return KV_ERR_INVALID_ARG;
+    return KV_OK;
+}
+
+// Fills the batch a kernel works on; lengths are held in 32 bits.
+int fill_batch(Batch *b, const kv_attn_batch *t, int heads, int kv_heads, int block_size, int unit_rows, int causal, int window, int *err)
+{
+    const int64_t max_tokens = (int64_t)t->max_blocks_per_req * block_size;
+    if (max_tokens > (1ll << 30) || t->n_tokens * (int64_t)heads > (1ll << 30)) return KV_ERR_UNSUPPORTED;
+    b->q_offsets = t->q_offsets;
+    b->kv_lens = t->kv_lens;
+    b->n_reqs = t->n_reqs;
+    b->n_tokens = (int32_t)t->n_tokens;
+    b->max_tokens = (int32_t)max_tokens;
+    b->kv_heads = kv_heads;
+    b->unit_rows = unit_rows;
+    b->causal = causal ? 1 : 0;
+    b->window = window;
+    b->group = make_fastdiv((uint32_t)(heads / kv_heads));
+    b->err = err;
+    return KV_OK;
+}
+
+// One plane of one tensor as rows of `heads` heads of `dim` 16-bit elements.
+int check_plane(const kv_cache_desc *c, int tensor, int plane, int heads, int dim)
+{
+    const int st = check_cache(c);
+    if (st != KV_OK) return st;
+    if (tensor < 0 || tensor >= c->n_tensors || plane < 0 || plane >= c->n_planes) return KV_ERR_INVALID_ARG;
+    if ((int64_t)heads * dim * 2 != c->row_bytes) return KV_ERR_INVALID_ARG;
+    if (c->num_blocks >= (1ll << 31) || c->token_stride >= (1ll << 40) || c->block_stride >= (1ll << 40)) return KV_ERR_UNSUPPORTED;
+    if (c->num_blocks == 0) return KV_ERR_INVALID_ARG;
+    return KV_OK;
+}
+
+int piece_rows(int block_size)
+{
+    int n = 1;
+    while (n < kTile && block_size % (2 * n) == 0) n *= 2;
+    return n;
+}
+
+int check_rows(const void *p, int64_t token_stride, int64_t head_stride)
+{
+    if (p == nullptr || token_stride < 0 || head_stride < 0) return KV_ERR_INVALID_ARG;
+    if (!aligned16(p) || !aligned16(token_stride) || !aligned16(head_stride)) return KV_ERR_ALIGN;
+    return KV_OK;
+}
+
+int preload_attention_kernels()
+{
+    Params p = {};
+    CUtensorMap m;
+    for (int dk : {64, 128, 192})
+        for (bool bf : {false, true}) {
+            const int st = bf ? pick_attention<true>(dk, dk == 64 ? 64 : 128, m, m, p, 0, nullptr, true)
+                              : pick_attention<false>(dk, dk == 64 ? 64 : 128, m, m, p, 0, nullptr, true);
+            if (st != KV_OK) return st;
+        }
+    return load_kernels(attention_kernel<64, 64, false>, attention_kernel<64, 64, true>, attention_kernel<128, 128, false>,
+                        attention_kernel<128, 128, true>, attention_kernel<192, 128, false>, attention_kernel<192, 128, true>,
+                        join_kernel<64, false>, join_kernel<64, true>, join_kernel<128, false>, join_kernel<128, true>);
+}
+
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" {
+
+int kv_attention_workspace_bytes(int64_t *bytes_out)
+{
+    if (bytes_out == nullptr) return KV_ERR_INVALID_ARG;
+    const DeviceInfo *d = current_device();
+    if (d == nullptr) return KV_ERR_CUDA;
+    *bytes_out = attention_workspace(d->num_sms);
+    return KV_OK;
+}
+
+int kv_attention(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_cache_desc *k, int32_t k_tensor, int32_t k_plane,
+                 const kv_cache_desc *v, int32_t v_tensor, int32_t v_plane, const void *q, int64_t q_token_stride,
+                 int64_t q_head_stride, void *out, int64_t out_token_stride, int64_t out_head_stride, float *lse, void *workspace,
+                 int64_t workspace_bytes, kv_stream_t stream)
+{
+    if (d == nullptr || d->n_heads <= 0 || d->n_kv_heads <= 0 || d->n_heads % d->n_kv_heads != 0 || d->head_dim <= 0 ||
+        d->head_dim_v <= 0 || d->window < 0 || !(d->scale > 0.0f) || !std::isfinite(d->scale) ||
+        (d->dtype != KV_BF16 && d->dtype != KV_F16))
+        return KV_ERR_INVALID_ARG;
+    int st = check_batch(batch);
+    if (st != KV_OK) return st;
+    if (d->head_dim % 8 || d->head_dim_v % 8) return KV_ERR_ALIGN;
+    if (d->head_dim > 192 || d->head_dim_v > 128 || (d->window && !d->causal)) return KV_ERR_UNSUPPORTED;
+    if ((st = check_plane(k, k_tensor, k_plane, d->n_kv_heads, d->head_dim)) != KV_OK) return st;
+    if ((st = check_plane(v, v_tensor, v_plane, d->n_kv_heads, d->head_dim_v)) != KV_OK) return st;
+    if (k->block_size != v->block_size) return KV_ERR_INVALID_ARG;
+    if (batch->n_reqs == 0 || batch->n_tokens == 0) return KV_OK;
+    if ((st = check_rows(q, q_token_stride, q_head_stride)) != KV_OK) return st;
+    if ((st = check_rows(out, out_token_stride, out_head_stride)) != KV_OK) return st;
+    if (workspace == nullptr) return KV_ERR_INVALID_ARG;
+    if (!aligned16(workspace) || ((uintptr_t)lse & 3u)) return KV_ERR_ALIGN;
+    Params p = {};
+    if ((st = fill_batch(&p.b, batch, d->n_heads, d->n_kv_heads, k->block_size, kRows, d->causal, d->window, nullptr)) != KV_OK) return st;
+    const DeviceInfo *dev = current_device();
+    if (dev == nullptr) return KV_ERR_CUDA;
+    if (workspace_bytes < attention_workspace(dev->num_sms)) return KV_ERR_RANGE;
+    if ((st = prepare_attention(*dev)) != KV_OK) return st;
+    p.b.err = dev->err_word;
+    p.table = batch->block_table;
+    p.table_stride = batch->bt_row_stride;
+    p.num_blocks = (int32_t)(k->num_blocks < v->num_blocks ? k->num_blocks : v->num_blocks);
+    p.block = make_fastdiv((uint32_t)k->block_size);
+    p.piece_rows = piece_rows(k->block_size);
+    p.dk = d->head_dim;
+    p.dv = d->head_dim_v;
+    p.heads = d->n_heads;
+    p.scale = d->scale;
+    p.c = d->scale * 1.44269504088896340736f;
+    p.q = (const char *)q;
+    p.q_token = q_token_stride;
+    p.q_head = q_head_stride;
+    p.out = (char *)out;
+    p.out_token = out_token_stride;
+    p.out_head = out_head_stride;
+    p.lse = lse;
+    p.places = (Place *)workspace;
+    p.ws = (float *)((char *)workspace + kPlaceBytes);
+    CUtensorMap km, vm;
+    if ((st = make_cache_map(&km, k, k_tensor, k_plane, d->n_kv_heads, d->head_dim, p.piece_rows)) != KV_OK) return st;
+    if ((st = make_cache_map(&vm, v, v_tensor, v_plane, d->n_kv_heads, d->head_dim_v, p.piece_rows)) != KV_OK) return st;
+    cudaStream_t s = (cudaStream_t)stream;
+    return d->dtype == KV_BF16 ? pick_attention<true>(p.dk, p.dv, km, vm, p, dev->num_sms, s, false)
+                               : pick_attention<false>(p.dk, p.dv, km, vm, p, dev->num_sms, s, false);
+}
+
+}  // extern "C"

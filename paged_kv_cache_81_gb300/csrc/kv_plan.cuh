@@ -1,0 +1,198 @@
+// How the attention kernels cut a ragged batch into work, on the device, from the lengths alone.
+//
+// A request's query rows are its (token, head of the group) pairs, token-major: row = token * group +
+// head.  Rows are cut into units of `unit_rows`; a unit of one key head needs the key tiles of
+// kTile keys between the first key that its first token sees and the last that its last token sees.
+// Laid end to end (request, key head, unit), all units' tiles form one line; CTA c of `parts` takes
+// the c-th equal piece of it.  A piece may begin and end inside a unit: those two fragments go to the
+// workspace and are joined by a second kernel.  So the split follows the lengths, not the launch: one
+// grid serves a captured graph whatever the lengths become, and long contexts and few rows fill the
+// GPU as well as many short requests do.
+#pragma once
+
+#include <cstdint>
+
+#include "kv_common.cuh"
+
+namespace pkv {
+
+constexpr int kTile = 128;  // keys of one tile
+
+struct Batch {
+    const int32_t *q_offsets;  // [n_reqs + 1]
+    const int32_t *kv_lens;    // [n_reqs]
+    int32_t n_reqs;
+    int32_t n_tokens;    // capacity: q_offsets entries are clamped to it
+    int32_t max_tokens;  // capacity of a table row in tokens: kv_lens entries are clamped to it
+    int32_t kv_heads;
+    int32_t unit_rows;
+    int32_t causal;
+    int32_t window;  // 0: none
+    FastDiv group;   // query heads of a key head
+    int *err;
+};
+
+struct Request {
+    int32_t q0, q_len, len;
+    int32_t rows, units;
+};
+
+struct Unit {
+    int32_t row0, rows;  // rows of the request
+    int32_t lo, hi;      // keys that some row sees
+    int32_t tile0, tiles;  // key tiles (absolute index of the first, count)
+};
+
+__device__ __forceinline__ Request load_request(const Batch &b, int r, bool report = false)
+{
+    Request q;
+    const int a = __ldg(b.q_offsets + r), e = __ldg(b.q_offsets + r + 1), n = __ldg(b.kv_lens + r);
+    q.q0 = min(max(a, 0), b.n_tokens);
+    const int end = min(max(e, q.q0), b.n_tokens);
+    q.q_len = end - q.q0;
+    q.len = min(max(n, 0), b.max_tokens);
+    q.rows = q.q_len * (int)b.group.d;
+    q.units = (q.rows + b.unit_rows - 1) / b.unit_rows;
+    if (report && (a != q.q0 || e != end || (r == 0 && a != 0))) set_error(b.err, KV_DERR_LIST);
+    if (report && n != q.len) set_error(b.err, KV_DERR_TABLE);
+    return q;
+}
+
+// Keys [lo, hi) that query token t of the request sees.
+__device__ __forceinline__ void sees(const Batch &b, const Request &q, int t, int &lo, int &hi)
+{
+    const int pos = q.len - q.q_len + t;
+    hi = b.causal ? min(q.len, pos + 1) : q.len;
+    hi = max(hi, 0);
+    lo = b.window ? min(max(pos - b.window + 1, 0), hi) : 0;
+}
+
+__device__ __forceinline__ Unit make_unit(const Batch &b, const Request &q, int j)
+{
+    Unit u;
+    u.row0 = j * b.unit_rows;
+    u.rows = min(b.unit_rows, q.rows - u.row0);
+    int x;
+    sees(b, q, (int)fdiv((uint32_t)u.row0, b.group), u.lo, x);
+    sees(b, q, (int)fdiv((uint32_t)(u.row0 + u.rows - 1), b.group), x, u.hi);
+    u.tile0 = u.lo / kTile;
+    u.tiles = u.hi > u.lo ? (u.hi + kTile - 1) / kTile - u.tile0 : 0;
+    return u;
+}
+
+// A unit that sees nothing still takes one step of the line: its rows have to be written.
+__device__ __forceinline__ int unit_cost(const Unit &u) { return max(1, u.tiles); }
+
+__device__ __forceinline__ long long head_cost(const Batch &b, const Request &q)
+{
+    long long n = 0;
+    for (int j = 0; j < q.units; j++) n += unit_cost(make_unit(b, q, j));
+    return n;
+}
+
+// A place on the line: tile `off` of unit (request, head, j).
+struct Place {
+    int32_t req, head, unit, off;
+};
+
+// Finds this CTA's piece of the line; every thread of the block calls it.  `scratch`: 33 words of 8
+// bytes; `place`: where the piece begins.  Returns the tiles in the piece (0: none).
+template <int Threads>
+__device__ int find_piece(const Batch &b, int part, int parts, long long *scratch, Place *place, bool report)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int kWarps = Threads / 32;
+    const int per = (b.n_reqs + Threads - 1) / Threads;
+    const int r0 = min(tid * per, b.n_reqs), r1 = min(r0 + per, b.n_reqs);
+    long long mine = 0;
+    for (int r = r0; r < r1; r++) mine += head_cost(b, load_request(b, r, report)) * b.kv_heads;
+    long long upto = mine;  // inclusive scan
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += o;
+    }
+    if (lane == 31) scratch[warp] = upto;
+    __syncthreads();
+    long long before = 0, total = 0;
+    for (int w = 0; w < kWarps; w++) {
+        if (w < warp) before += scratch[w];
+        total += scratch[w];
+    }
+    upto += before;
+    const long long used = min((long long)parts, total);  // no piece is empty but the last ones
+    long long w0 = 0, w1 = 0;
+    if (part < used) {
+        w0 = total * part / used;
+        w1 = total * (part + 1) / used;
+        if (w0 >= upto - mine && w0 < upto) {
+            long long rest = w0 - (upto - mine);
+            for (int r = r0; r < r1; r++) {
+                const Request q = load_request(b, r);
+                const long long h = head_cost(b, q), all = h * b.kv_heads;
+                if (rest >= all) {
+                    rest -= all;
+                    continue;
+                }
+                Place p;
+                p.req = r;
+                p.head = (int)(rest / h);
+                rest -= p.head * h;
+                int j = 0;
+                for (;; j++) {
+                    const int n = unit_cost(make_unit(b, q, j));
+                    if (rest < n) break;
+                    rest -= n;
+                }
+                p.unit = j;
+                p.off = (int)rest;
+                *place = p;
+                break;
+            }
+        }
+    }
+    __syncthreads();
+    return (int)(w1 - w0);
+}
+
+// Walks a piece unit by unit.
+struct Walk {
+    Place at;
+    int left;
+    Request q;
+    Unit u;
+    int n;  // tiles of the current fragment
+
+    __device__ __forceinline__ bool start(const Batch &b, const Place &p, int tiles)
+    {
+        at = p;
+        left = tiles;
+        if (left <= 0) return false;
+        q = load_request(b, at.req);
+        u = make_unit(b, q, at.unit);
+        n = min(left, unit_cost(u) - at.off);
+        return true;
+    }
+    // The fragment is the unit as a whole.
+    __device__ __forceinline__ bool whole() const { return at.off == 0 && n == unit_cost(u); }
+    __device__ __forceinline__ bool next(const Batch &b)
+    {
+        left -= n;
+        if (left <= 0) return false;
+        at.off = 0;
+        if (++at.unit == q.units) {
+            at.unit = 0;
+            if (++at.head == b.kv_heads) {
+                at.head = 0;
+                do {
+                    q = load_request(b, ++at.req);
+                } while (q.units == 0);  // `left` tiles remain, so a later request has rows
+            }
+        }
+        u = make_unit(b, q, at.unit);
+        n = min(left, unit_cost(u));
+        return true;
+    }
+};
+
+}  // namespace pkv

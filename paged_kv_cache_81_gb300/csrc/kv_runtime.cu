@@ -3,6 +3,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "kv_attention.cuh"
 #include "kv_common.cuh"
 
 namespace {
@@ -79,6 +80,22 @@ int preload_all_kernels(const DeviceInfo &dev)
     if (done[dev.device]) return KV_OK;
     for (int (*load)() : {preload_write_kernels, preload_xfer_kernels, preload_copy_kernels, preload_bulk_kernels,
                           preload_clip_kernels, preload_hash_kernels, preload_signal_kernels}) {
+        const int st = load();
+        if (st != KV_OK) return st;
+    }
+    const int st = prepare_attention(dev);
+    if (st != KV_OK) return st;
+    done[dev.device] = true;
+    return KV_OK;
+}
+
+int prepare_attention(const DeviceInfo &dev)
+{
+    static std::mutex mu;
+    static bool done[kMaxDevices];
+    std::lock_guard<std::mutex> lock(mu);
+    if (done[dev.device]) return KV_OK;
+    for (int (*load)() : {preload_attention_kernels}) {
         const int st = load();
         if (st != KV_OK) return st;
     }

@@ -22,11 +22,15 @@ KV_OK, KV_ERR_INVALID_ARG, KV_ERR_ALIGN, KV_ERR_RANGE, KV_ERR_CUDA, KV_ERR_TIMEO
 KV_DERR_TABLE, KV_DERR_SLOT, KV_DERR_BLOCK, KV_DERR_LIST = 0x01, 0x02, 0x04, 0x08
 KV_DERR_CAPACITY, KV_DERR_STAGE, KV_DERR_DST_TABLE, KV_DERR_TIMEOUT = 0x10, 0x20, 0x40, 0x80
 
+KV_BF16, KV_F16 = 0, 1
+_DTYPES = {torch.bfloat16: KV_BF16, torch.float16: KV_F16}
+
 RUN_WORDS = 6  # a kv_xfer_run is 24 bytes: six int32 words (the last two hold the int64 stage_block)
 EXPORTS = ("kv_version", "kv_status_string", "kv_last_cuda_error", "kv_slot_mapping", "kv_reshape_and_cache",
            "kv_xfer_workspace_bytes", "kv_build_xfer_list", "kv_pack_blocks", "kv_unpack_blocks",
            "kv_get_last_error", "kv_build_xfer_list_static", "kv_unpack_blocks_signal", "kv_wait_signal",
-           "kv_clip_block_lists", "kv_block_hashes", "kv_block_hashes_workspace_bytes", "kv_write_tokens")
+           "kv_clip_block_lists", "kv_block_hashes", "kv_block_hashes_workspace_bytes", "kv_write_tokens",
+           "kv_attention", "kv_attention_workspace_bytes")
 
 
 class KvError(RuntimeError):
@@ -59,6 +63,31 @@ class KvStageDesc(ctypes.Structure):
     ]
 
 
+class KvAttnBatch(ctypes.Structure):
+    _fields_ = [
+        ("block_table", ctypes.c_void_p),
+        ("n_reqs", ctypes.c_int32),
+        ("max_blocks_per_req", ctypes.c_int32),
+        ("bt_row_stride", ctypes.c_int64),
+        ("q_offsets", ctypes.c_void_p),
+        ("kv_lens", ctypes.c_void_p),
+        ("n_tokens", ctypes.c_int64),
+    ]
+
+
+class KvAttnDesc(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32),
+        ("n_heads", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("head_dim_v", ctypes.c_int32),
+        ("causal", ctypes.c_int32),
+        ("window", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -75,6 +104,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         P, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
         D = ctypes.POINTER(KvCacheDesc)
         S = ctypes.POINTER(KvStageDesc)
+        A, B = ctypes.POINTER(KvAttnDesc), ctypes.POINTER(KvAttnBatch)
         sig = {
             "kv_version": ([], ctypes.c_char_p),
             "kv_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -93,6 +123,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             "kv_clip_block_lists": ([P, i32, P, i64, P, i32, i32, P, P, i64, P], ctypes.c_int),
             "kv_block_hashes": ([P, i32, P, i64, i32, ctypes.c_uint64, P, P, i64, P, i64, P], ctypes.c_int),
             "kv_block_hashes_workspace_bytes": ([i64, i32, ctypes.POINTER(ctypes.c_int64)], ctypes.c_int),
+            "kv_attention_workspace_bytes": ([ctypes.POINTER(i64)], ctypes.c_int),
+            "kv_attention": ([A, B, D, i32, i32, D, i32, i32, P, i64, i64, P, i64, i64, P, P, i64, P], ctypes.c_int),
             "kv_write_tokens": ([D, P, i64, P, i32, i32, i64, P, P, i64, P, P], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
@@ -437,6 +469,89 @@ def kv_get_last_error(clear: bool = True, stream=None) -> int:
     out = ctypes.c_int32(0)
     _check("kv_get_last_error", load().kv_get_last_error(ctypes.byref(out), 1 if clear else 0, _stream(stream)))
     return out.value
+
+
+# ---------------------------------------------------------------------------
+# attention over the paged cache
+# ---------------------------------------------------------------------------
+def kv_attention_workspace_bytes() -> int:
+    out = ctypes.c_int64(0)
+    _check("kv_attention_workspace_bytes", load().kv_attention_workspace_bytes(ctypes.byref(out)))
+    return out.value
+
+
+def kv_attention_workspace(device="cuda") -> torch.Tensor:
+    """A workspace for kv_attention and kv_latent_attention calls of any size on `device`; calls that
+    share one must be ordered."""
+    with torch.cuda.device(device):
+        return torch.empty(kv_attention_workspace_bytes(), dtype=torch.uint8, device=device)
+
+
+def _attn_batch(block_table: torch.Tensor, q_offsets: torch.Tensor, kv_lens: torch.Tensor, n_tokens: int) -> KvAttnBatch:
+    _i32(q_offsets, "q_offsets"), _i32(kv_lens, "kv_lens")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.stride(1) != 1:
+        raise ValueError("block_table must be a row-major int32 [n_reqs, max_blocks] CUDA tensor")
+    n = kv_lens.shape[0]
+    if block_table.shape[0] != n or q_offsets.shape[0] != n + 1:
+        raise ValueError("block_table, q_offsets and kv_lens are of different numbers of requests")
+    return KvAttnBatch(_ptr(block_table), n, block_table.shape[1], block_table.stride(0), _ptr(q_offsets), _ptr(kv_lens), n_tokens)
+
+
+def _rows3(t: torch.Tensor, name: str) -> torch.Tensor:
+    if t.dim() != 3 or t.dtype not in _DTYPES or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} must be a bf16 or fp16 CUDA tensor [tokens, heads, dim] with contiguous rows")
+    return t
+
+
+def _like_cache(cache: PagedCache, dtype: torch.dtype, name: str):
+    t = cache.tensors[0]
+    if t.dtype != dtype:
+        raise ValueError(f"{name} holds {t.dtype}, the queries are {dtype}")
+
+
+def _strides(t: torch.Tensor):
+    return t.stride(0) * t.element_size(), t.stride(1) * t.element_size()
+
+
+def kv_attention(q: torch.Tensor, cache: PagedCache, block_table: torch.Tensor, q_offsets: torch.Tensor,
+                 kv_lens: torch.Tensor, scale: float, *, v_cache: Optional[PagedCache] = None, k_tensor: int = 0,
+                 v_tensor: Optional[int] = None, causal: bool = True, window: int = 0, out: Optional[torch.Tensor] = None,
+                 lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of new tokens q [tokens, heads, dim] over the paged cache; returns (out, lse float32 [tokens, heads]).
+
+    Keys are tensor `k_tensor` of `cache` (plane 0).  Values are tensor `v_tensor` of `v_cache`, or, without a
+    `v_cache`, plane 1 of the same tensor (two-plane caches) or tensor `v_tensor` of `cache`."""
+    _rows3(q, "q")
+    _like_cache(cache, q.dtype, "cache")
+    values = cache if v_cache is None else v_cache
+    _like_cache(values, q.dtype, "v_cache")
+    v_plane = 1 if values.n_planes == 2 else 0
+    if v_tensor is None:
+        v_tensor = k_tensor if v_cache is None else 0
+        if v_cache is None and cache.n_planes == 1:
+            raise ValueError("a one-plane cache holds the values in another tensor: give v_tensor or v_cache")
+    T, H, dk = q.shape
+    kv_heads, left = divmod(cache.row_bytes, dk * q.element_size())
+    if left or not kv_heads or values.row_bytes % (kv_heads * q.element_size()):
+        raise ValueError("the cache's rows are not whole heads of q's width")
+    dv = values.row_bytes // (kv_heads * q.element_size())
+    batch = _attn_batch(block_table, q_offsets, kv_lens, T)
+    if out is None:
+        out = torch.empty((T, H, dv), dtype=q.dtype, device=q.device)
+    elif _rows3(out, "out").shape != (T, H, dv) or out.dtype != q.dtype:
+        raise ValueError("out must be [tokens, heads, value dim] of q's type")
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+    elif lse.shape != (T, H) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 [tokens, heads] tensor")
+    if workspace is None:
+        workspace = kv_attention_workspace(q.device)
+    desc = KvAttnDesc(_DTYPES[q.dtype], H, kv_heads, dk, dv, int(causal), int(window), float(scale))
+    _check("kv_attention", load().kv_attention(
+        ctypes.byref(desc), ctypes.byref(batch), ctypes.byref(cache.desc()), int(k_tensor), 0, ctypes.byref(values.desc()),
+        int(v_tensor), v_plane, _ptr(q), *_strides(q), _ptr(out), *_strides(out), _ptr(lse), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out, lse
 
 
 def default_max_run_blocks(stage_block_bytes: int, target_bytes: int = 16 * 1024) -> int:
