@@ -463,6 +463,76 @@ KV_API int kv_attention(const kv_attn_desc *d, const kv_attn_batch *batch, const
                         int64_t out_head_stride, float *lse, void *workspace, int64_t workspace_bytes, kv_stream_t stream);
 
 /*
+ * kv_latent_attention: kv_attention over a latent cache, one row of 576 elements a token shared by every
+ * head (the MLA latent layout above): keys are whole rows, values their first 512 elements.
+ *     out[t, h] = sum_j p_j row[j][0:512],  p = softmax over the j that t sees of scale * q[t, h] . row[j]
+ * This is the absorbed form: q holds the up-projection of the keys already, and out is multiplied by that
+ * of the values afterwards.  d->n_kv_heads is 1, head_dim 576 and head_dim_v 512 (KV_ERR_UNSUPPORTED
+ * otherwise).  Everything else as for kv_attention.
+ */
+KV_API int kv_latent_attention(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_cache_desc *cache, int32_t tensor,
+                               const void *q, int64_t q_token_stride, int64_t q_head_stride, void *out,
+                               int64_t out_token_stride, int64_t out_head_stride, float *lse, void *workspace,
+                               int64_t workspace_bytes, kv_stream_t stream);
+
+/*
+ * kv_latent_expand: the expanded form's keys and values.  For every request r, token j < kv_lens[r] and head h,
+ * with row = the latent row of token j (512 latent elements c, 64 rotary ones),
+ *     K[j, h] = [ weight[h, 0:128] c ; row[512:576] ]  (192 elements)    V[j, h] = weight[h, 128:256] c
+ * rounded once to the element type and written to token j of request r in the caches k_out (rows of
+ * n_heads * 192) and v_out (rows of n_heads * 128) through out_table; kv_attention with head_dim 192 and
+ * head_dim_v 128 then attends to them.  weight: contiguous [n_heads, 256, 512], 16-byte aligned.  The two
+ * tables may have different block sizes.  A kv_len beyond either table is clamped and an entry
+ * outside its cache reads as zeros (source) or is skipped (output): both set KV_DERR_TABLE.  Slots past
+ * the lengths are left as they were.  The outputs must not overlap the latent cache.
+ */
+KV_API int kv_latent_expand(int32_t dtype, int32_t n_heads, const kv_cache_desc *cache, int32_t tensor,
+                            const int32_t *block_table, int32_t n_reqs, int32_t max_blocks_per_req, int64_t bt_row_stride,
+                            const int32_t *kv_lens, const void *weight, const kv_cache_desc *k_out, int32_t k_tensor,
+                            const kv_cache_desc *v_out, int32_t v_tensor, const int32_t *out_table,
+                            int32_t out_blocks_per_req, int64_t out_row_stride, kv_stream_t stream);
+
+/*
+ * kv_attention_mass: the attention weight that each cached token receives from the new ones,
+ *     score[r, j] = prev[r, j] + sum over new tokens t of r that see j, and over heads h, of
+ *                   exp(scale * q[t, h] . K[j] - lse[t, h])          for j < min(kv_lens[r], width),
+ *     score[r, j] = prev[r, j]                                       for the other j < width,
+ * with lse as kv_attention wrote it ([n_tokens, n_heads]; a row of -inf adds nothing).  prev (NULL: zeros)
+ * and score are float [n_reqs, width] with row strides in elements; they may be the same buffer.  Adding layer
+ * by layer and step by step gives the accumulated weights that kv_evict ranks by.  d->head_dim_v is
+ * ignored; at most 128 query heads a key head.  The sum of a token is formed in a fixed order, so the same call
+ * gives the same bits.  workspace: kv_attention_mass_workspace_bytes(), 16-byte aligned; calls sharing it must
+ * be ordered.  Lengths and tables as for kv_attention.
+ */
+KV_API int kv_attention_mass_workspace_bytes(int64_t *bytes_out);
+KV_API int kv_attention_mass(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_cache_desc *k, int32_t k_tensor,
+                             int32_t k_plane, const void *q, int64_t q_token_stride, int64_t q_head_stride, const float *lse,
+                             const float *prev, int64_t prev_stride, float *score, int64_t score_stride, int32_t width,
+                             void *workspace, int64_t workspace_bytes, kv_stream_t stream);
+
+/*
+ * kv_evict: trims every request to at most `budget` tokens.  Of a request with more, the first `sinks`, the
+ * last `recent` and, of the others, the ones of highest score[r, j] stay (equal scores: the lowest j; NaN
+ * below everything), in their order: kept[r, i] is the old index of new token i.  Every tensor's and plane's
+ * rows are gathered to slot i % block_size of page out_table[r * out_row_stride + i / block_size].
+ * Outputs (device): new_lens [n_reqs] = min(kv_lens[r], budget); kept int32 [n_reqs, budget], -1 past
+ * new_lens[r]; out_score (may be NULL) float [n_reqs, budget], the kept tokens' scores, 0 past them.
+ *  - out_table == block_table (the same pointer): in place; the pages past new_lens[r] are then free.  The
+ *    pages of a request must then belong to it alone.  Otherwise the pages out_table lists must not be
+ *    among those block_table lists; shared prefix pages stay as they are.
+ *  - out_score may be score itself (row strides equal).
+ *  - kv_lens outside [0, min(max_blocks_per_req * block_size, width)] are clamped, an out_table too short for
+ *    the kept tokens truncates their rows, a table entry outside the cache skips its rows: each sets
+ *    KV_DERR_TABLE.
+ * sinks + recent <= budget (KV_ERR_INVALID_ARG).  Limits: n_reqs <= 65535, 2^30 tokens a table row.
+ */
+KV_API int kv_evict(const kv_cache_desc *cache, const int32_t *block_table, int32_t n_reqs, int32_t max_blocks_per_req,
+                    int64_t bt_row_stride, const int32_t *kv_lens, const float *score, int64_t score_stride, int32_t width,
+                    int32_t budget, int32_t sinks, int32_t recent, const int32_t *out_table, int32_t out_blocks_per_req,
+                    int64_t out_row_stride, int32_t *new_lens, int32_t *kept, int64_t kept_stride, float *out_score,
+                    int64_t out_score_stride, kv_stream_t stream);
+
+/*
  * kv_get_last_error: copies the current device's sticky error word (KV_DERR_* bits) to
  * *host_out after the work queued on `stream` so far, clears it when clear != 0, and
  * SYNCHRONISES `stream`.  Work on other streams is not waited for.

@@ -27,6 +27,7 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kRows = 256;  // rows of a unit
+constexpr int kTile = 128;  // keys of a tile
 constexpr uint32_t kPanel = 128 * 128;  // bytes of a 64-element panel of 128 rows
 
 template <int DK, int DV>
@@ -68,23 +69,6 @@ struct Aux {
 };
 static_assert(sizeof(Aux) <= 2048, "bookkeeping");
 
-// One row of the output from its accumulator: 32 columns of it.
-template <bool Bf16>
-__device__ __forceinline__ void store_row32(char *to, const float (&o)[32], float inv, int col, int dv)
-{
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        if (col + 8 * i < dv) {
-            uint4 v;
-            v.x = pack2<Bf16>(o[8 * i] * inv, o[8 * i + 1] * inv);
-            v.y = pack2<Bf16>(o[8 * i + 2] * inv, o[8 * i + 3] * inv);
-            v.z = pack2<Bf16>(o[8 * i + 4] * inv, o[8 * i + 5] * inv);
-            v.w = pack2<Bf16>(o[8 * i + 6] * inv, o[8 * i + 7] * inv);
-            *reinterpret_cast<uint4 *>(to + (col + 8 * i) * 2) = v;
-        }
-    }
-}
-
 template <int DK, int DV, bool Bf16>
 __global__ void __launch_bounds__(kThreads, 1)
 attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const Params p)
@@ -116,7 +100,7 @@ attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
     }
     if (warp == 2) tmem_alloc(smem_addr(&aux.tmem), 512);
     grid_dep_entry();
-    const int tiles = find_piece<kThreads>(b, blockIdx.x, gridDim.x, aux.scan, &aux.place, blockIdx.x == 0);
+    const int tiles = find_place<kThreads>(b, blockIdx.x, gridDim.x, aux.scan, &aux.place, blockIdx.x == 0);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -453,66 +437,6 @@ attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
     if (warp == 2) tmem_free(tmem, 512);
 }
 
-// Joins the fragments of the units that were cut: block (c, y) looks whether the cut before CTA c is the
-// first one inside its unit, and joins rows y, y + gridDim.y, ... of it.  A row's fragments are read in
-// the order of their keys, so the result does not depend on timing.
-template <int DV, bool Bf16>
-__global__ void __launch_bounds__(256) join_kernel(const Params p, int parts, int ws_rows)
-{
-    grid_dep_entry();
-    const Batch &b = p.b;
-    const int c = blockIdx.x + 1;
-    const Place pl = p.places[c];
-    if (pl.req < 0 || pl.off == 0) return;
-    const Place before = p.places[c - 1];
-    const auto same = [&](const Place &o) { return o.req == pl.req && o.head == pl.head && o.unit == pl.unit; };
-    if (same(before) && before.off != 0) return;  // an earlier cut of the unit joins it
-    int last = c;
-    while (last + 1 < parts) {
-        const Place nx = p.places[last + 1];
-        if (!same(nx) || nx.off == 0) break;
-        last++;
-    }
-    const Request q = load_request(b, pl.req);
-    const Unit u = make_unit(b, q, pl.unit);
-    const int64_t stride = (int64_t)ws_rows * (DV + 2);
-    constexpr int kLanes = DV / 8, kRowsPerPass = 256 / kLanes;
-    const int col = (threadIdx.x % kLanes) * 8;
-    for (int row = blockIdx.y * kRowsPerPass + threadIdx.x / kLanes; row < u.rows; row += gridDim.y * kRowsPerPass) {
-        float top = -INFINITY;
-        for (int x = c - 1; x <= last; x++) {
-            const float *part = p.ws + (2 * x + (x == c - 1)) * stride;
-            top = fmaxf(top, part[(int64_t)ws_rows * DV + row]);
-        }
-        float o[8] = {0, 0, 0, 0, 0, 0, 0, 0}, l = 0.0f;
-        if (top > -INFINITY) {
-#pragma unroll 4
-            for (int x = c - 1; x <= last; x++) {
-                const float *part = p.ws + (2 * x + (x == c - 1)) * stride;
-                const float a = exp2_fast((part[(int64_t)ws_rows * DV + row] - top) * p.c);
-                l += part[(int64_t)ws_rows * (DV + 1) + row] * a;
-                const float4 v0 = *reinterpret_cast<const float4 *>(part + (int64_t)row * DV + col);
-                const float4 v1 = *reinterpret_cast<const float4 *>(part + (int64_t)row * DV + col + 4);
-                o[0] += v0.x * a, o[1] += v0.y * a, o[2] += v0.z * a, o[3] += v0.w * a;
-                o[4] += v1.x * a, o[5] += v1.y * a, o[6] += v1.z * a, o[7] += v1.w * a;
-            }
-        }
-        const int r = u.row0 + row, tok = (int)fdiv((uint32_t)r, b.group);
-        const int head = pl.head * (int)b.group.d + r - tok * (int)b.group.d;
-        const int64_t out_row = (int64_t)(q.q0 + tok);
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-        if (col < p.dv) {
-            uint4 v;
-            v.x = pack2<Bf16>(o[0] * inv, o[1] * inv);
-            v.y = pack2<Bf16>(o[2] * inv, o[3] * inv);
-            v.z = pack2<Bf16>(o[4] * inv, o[5] * inv);
-            v.w = pack2<Bf16>(o[6] * inv, o[7] * inv);
-            *reinterpret_cast<uint4 *>(p.out + out_row * p.out_token + (int64_t)head * p.out_head + col * 2) = v;
-        }
-        if (col == 0 && p.lse) p.lse[out_row * p.heads + head] = l > 0.0f ? fmaf(top, p.scale, logf(l)) : -INFINITY;
-    }
-}
-
 template <int DK, int DV, bool Bf16>
 int launch_attention(const CUtensorMap &km, const CUtensorMap &vm, const Params &p, int parts, cudaStream_t s, bool prepare)
 {
@@ -521,7 +445,7 @@ int launch_attention(const CUtensorMap &km, const CUtensorMap &vm, const Params 
         return cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<DK, DV>::kBytes));
     int st = cuda_status(launch(kernel, dim3(parts), dim3(kThreads), Shape<DK, DV>::kBytes, s, km, vm, p));
     if (st != KV_OK || parts < 2) return st;
-    return cuda_status(launch(join_kernel<DV, Bf16>, dim3(parts - 1, 8), dim3(256), 0, s, p, parts, kRows));
+    return join_fragments<DV, Bf16>(Join{p.b, p.places, p.ws, p.out, p.out_token, p.out_head, p.lse, p.heads, p.dv, kRows, 1, parts, p.scale, p.c}, s);
 }
 
 template <bool Bf16>
@@ -544,7 +468,7 @@ int check_batch(const kv_attn_batch *t)
 }
 
 // Fills the batch a kernel works on; lengths are held in 32 bits.
-int fill_batch(Batch *b, const kv_attn_batch *t, int heads, int kv_heads, int block_size, int unit_rows, int causal, int window, int *err)
+int fill_batch(Batch *b, const kv_attn_batch *t, int heads, int kv_heads, int block_size, int unit_rows, int tile, int causal, int window)
 {
     const int64_t max_tokens = (int64_t)t->max_blocks_per_req * block_size;
     if (max_tokens > (1ll << 30) || t->n_tokens * (int64_t)heads > (1ll << 30)) return KV_ERR_UNSUPPORTED;
@@ -555,10 +479,11 @@ int fill_batch(Batch *b, const kv_attn_batch *t, int heads, int kv_heads, int bl
     b->max_tokens = (int32_t)max_tokens;
     b->kv_heads = kv_heads;
     b->unit_rows = unit_rows;
+    b->tile = tile;
     b->causal = causal ? 1 : 0;
     b->window = window;
     b->group = make_fastdiv((uint32_t)(heads / kv_heads));
-    b->err = err;
+    b->err = nullptr;
     return KV_OK;
 }
 
@@ -574,10 +499,10 @@ int check_plane(const kv_cache_desc *c, int tensor, int plane, int heads, int di
     return KV_OK;
 }
 
-int piece_rows(int block_size)
+int piece_rows(int block_size, int tile)
 {
     int n = 1;
-    while (n < kTile && block_size % (2 * n) == 0) n *= 2;
+    while (n < tile && block_size % (2 * n) == 0) n *= 2;
     return n;
 }
 
@@ -640,7 +565,7 @@ int kv_attention(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_cac
     if (workspace == nullptr) return KV_ERR_INVALID_ARG;
     if (!aligned16(workspace) || ((uintptr_t)lse & 3u)) return KV_ERR_ALIGN;
     Params p = {};
-    if ((st = fill_batch(&p.b, batch, d->n_heads, d->n_kv_heads, k->block_size, kRows, d->causal, d->window, nullptr)) != KV_OK) return st;
+    if ((st = fill_batch(&p.b, batch, d->n_heads, d->n_kv_heads, k->block_size, kRows, kTile, d->causal, d->window)) != KV_OK) return st;
     const DeviceInfo *dev = current_device();
     if (dev == nullptr) return KV_ERR_CUDA;
     if (workspace_bytes < attention_workspace(dev->num_sms)) return KV_ERR_RANGE;
@@ -650,7 +575,7 @@ int kv_attention(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_cac
     p.table_stride = batch->bt_row_stride;
     p.num_blocks = (int32_t)(k->num_blocks < v->num_blocks ? k->num_blocks : v->num_blocks);
     p.block = make_fastdiv((uint32_t)k->block_size);
-    p.piece_rows = piece_rows(k->block_size);
+    p.piece_rows = piece_rows(k->block_size, kTile);
     p.dk = d->head_dim;
     p.dv = d->head_dim_v;
     p.heads = d->n_heads;

@@ -1,0 +1,439 @@
+// kv_latent_attention: attention over one shared latent row a token (the absorbed form).
+//
+// Keys are whole rows of 576 elements, values their first 512.  The accumulator of 128 query rows by 512
+// values would fill tensor memory by itself, so two CTAs share a part of the batch's line
+// (kv_plan.cuh): each forms the products S = Q K^T over all 576 elements and accumulates 256 of the 512
+// values.  The scores are computed twice (576 + 256 multiply-adds a key, row and CTA instead of 544), but
+// nothing has to be exchanged, and every operand stays on chip:
+//   TMEM           O 256 columns, S twice 64, Q's first four panels 128 (A operand from TMEM)
+//   shared memory  Q's other five panels 80 KB; two tiles of 64 keys, 72 KB each: the four panels that
+//                  are this CTA's values, and the five that the scores alone use and free earlier
+//   warp 0 loads, warp 1 issues the products, warps 4-7 hold a row a thread (maximum, exponentials, P
+//   over S, lazy rescaling as in kv_attention.cu).  S of the next tile is formed before O += P V of
+//   this one, so the tensor core works while the exponentials run.
+#include "kv_attention.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRows = 128;
+constexpr int kKeys = 64;      // keys of a tile
+constexpr int kD = 576, kDV = 512, kHalf = 256;
+constexpr int kQT = 4;         // panels of Q in tensor memory
+constexpr uint32_t kQPanel = 128 * 128, kPanel = kKeys * 128;
+constexpr uint32_t kOffV = 5 * kQPanel, kOffX = kOffV + 2 * 4 * kPanel, kOffAux = kOffX + 2 * 5 * kPanel;
+constexpr uint32_t kBytes = kOffAux + 1024;
+constexpr uint32_t kTmO = 0, kTmS = 256, kTmQ = 384;
+
+struct Params {
+    Batch b;
+    const int32_t *table;
+    int64_t table_stride;
+    int32_t num_blocks;
+    FastDiv block;
+    int32_t piece_rows, heads;
+    float scale, c;
+    const char *q;
+    int64_t q_token, q_head;
+    char *out;
+    int64_t out_token, out_head;
+    float *lse;
+    float *ws;
+    Place *places;
+};
+
+struct Aux {
+    uint64_t v_full[2], v_empty[2], x_full[2], x_empty[2], s_full[2], p_ready[2], o_done[2], q_full;
+    long long scan[8];
+    Place place;
+    uint32_t tmem;
+    int gave_up;
+};
+static_assert(sizeof(Aux) <= 1024, "bookkeeping");
+
+template <bool Bf16>
+__global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_constant__ CUtensorMap map, const Params p)
+{
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const uint32_t base = smem_addr(smem);
+    Aux &aux = *reinterpret_cast<Aux *>(smem + kOffAux);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int part = blockIdx.x >> 1, half = blockIdx.x & 1;
+    const Batch &b = p.b;
+    const Waiter wait{&aux.gave_up, b.err};
+
+    if (tid == 0) {
+        aux.gave_up = 0;
+        for (int i = 0; i < 2; i++) {
+            mbar_init(smem_addr(&aux.v_full[i]), 1);
+            mbar_init(smem_addr(&aux.v_empty[i]), 1);
+            mbar_init(smem_addr(&aux.x_full[i]), 1);
+            mbar_init(smem_addr(&aux.x_empty[i]), 1);
+            mbar_init(smem_addr(&aux.s_full[i]), 1);
+            mbar_init(smem_addr(&aux.p_ready[i]), 128);
+            // by the tile's parity: the softmax warps look at it only now and then, and when they do the
+            // product two tiles before has completed (its scores' successor is out) but the last may not have
+            mbar_init(smem_addr(&aux.o_done[i]), 1);
+        }
+        mbar_init(smem_addr(&aux.q_full), 128);
+        mbar_init_fence();
+        tma_prefetch_map(&map);
+    }
+    if (warp == 2) tmem_alloc(smem_addr(&aux.tmem), 512);
+    grid_dep_entry();
+    const int tiles = find_place<kThreads>(b, part, gridDim.x >> 1, aux.scan, &aux.place, blockIdx.x == 0);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = aux.tmem;
+    if (tid == 0 && half == 0) {
+        Place pl = aux.place;
+        if (tiles <= 0) pl.req = -1;
+        p.places[part] = pl;
+    }
+
+    Walk w;
+    if (!w.start(b, aux.place, tiles)) {
+        // nothing to do: on to the common exit
+    } else if (warp == 0) {
+        // ---- loads: the five other panels, then the four of this CTA's values ----
+        const int pr = p.piece_rows;
+        int it = 0;
+        bool ok = true;
+        do {
+            if (w.u.tiles == 0) continue;
+            const int32_t *row = p.table + (int64_t)w.at.req * p.table_stride;
+            const int kt0 = w.u.tile0 + w.at.off;
+            for (int t = 0; t < w.n; t++, it++) {
+                const int kb = (kt0 + t) * kKeys;
+                const int p0 = max(0, w.u.lo - kb) / pr, p1 = (min(w.u.hi - kb, kKeys) + pr - 1) / pr;
+                const int s = it & 1;
+                const uint32_t xbar = smem_addr(&aux.x_full[s]), vbar = smem_addr(&aux.v_full[s]);
+                int page = 0, slot = 0;
+                const auto find = [&](int i) {
+                    const uint32_t key = (uint32_t)(kb + i * pr), col = fdiv(key, p.block);
+                    slot = (int)(key - col * p.block.d);
+                    page = __ldg(row + col);
+                    if (page < 0 || page >= p.num_blocks) {
+                        set_error(b.err, KV_DERR_TABLE);
+                        page = p.num_blocks;  // outside the map: reads zeros
+                    }
+                };
+                if (p0 + lane < p1) find(p0 + lane);
+                const int page0 = page, slot0 = slot;
+                if (it >= 2 && !wait.warp(smem_addr(&aux.x_empty[s]), ((it >> 1) - 1) & 1)) { ok = false; break; }
+                if (lane == 0) mbar_arrive_expect_tx(xbar, (uint32_t)((p1 - p0) * pr) * 5 * 128);
+                __syncwarp();
+                for (int i = p0 + lane; i < p1; i += 32) {
+                    if (i >= p0 + 32) find(i);
+#pragma unroll
+                    for (int h = 0; h < 5; h++) {
+                        const int panel = h == 4 ? 8 : h + 4 - 4 * half;  // the other half's values, then the rotary part
+                        tma_load_4d(base + kOffX + (s * 5 + h) * kPanel + i * pr * 128, &map, xbar, panel * 64, 0, slot, page);
+                    }
+                }
+                page = page0, slot = slot0;
+                if (it >= 2 && !wait.warp(smem_addr(&aux.v_empty[s]), ((it >> 1) - 1) & 1)) { ok = false; break; }
+                if (lane == 0) mbar_arrive_expect_tx(vbar, (uint32_t)((p1 - p0) * pr) * 4 * 128);
+                __syncwarp();
+                for (int i = p0 + lane; i < p1; i += 32) {
+                    if (i >= p0 + 32) find(i);
+#pragma unroll
+                    for (int h = 0; h < 4; h++)
+                        tma_load_4d(base + kOffV + (s * 4 + h) * kPanel + i * pr * 128, &map, vbar, (h + 4 * half) * 64, 0, slot, page);
+                }
+            }
+        } while (ok && w.next(b));
+    } else if (warp == 1) {
+        // ---- matrix products: one thread ----
+        if (lane == 0) {
+            constexpr uint32_t qk_desc = mma_desc(Bf16, 128, kKeys, false), pv_desc = mma_desc(Bf16, 128, kHalf, true);
+            int it = 0, units = 0;
+            bool ok = true;
+            do {
+                if (w.u.tiles == 0) continue;
+                ok = wait.one(smem_addr(&aux.q_full), units++ & 1);
+                if (!ok) break;
+                tc_fence_after();
+                // Q's panels stand in the order of the key panels as this CTA holds them: the five others
+                // (shared memory), the four of its values (tensor memory)
+                const auto qk = [&](int i) {
+                    const int n = it + i, s = n & 1;
+                    const uint32_t d = tmem + kTmS + s * kKeys;
+                    if (!wait.one(smem_addr(&aux.x_full[s]), (n >> 1) & 1)) return false;
+#pragma unroll
+                    for (int kk = 0; kk < 20; kk++) {
+                        const uint32_t o = (kk % 4) * 32;
+                        mma_ss(d, smem_desc(base + (kk / 4) * kQPanel + o, 16, 1024), smem_desc(base + kOffX + (s * 5 + kk / 4) * kPanel + o, 16, 1024),
+                               qk_desc, kk > 0);
+                    }
+                    tc_commit(smem_addr(&aux.x_empty[s]));
+                    if (!wait.one(smem_addr(&aux.v_full[s]), (n >> 1) & 1)) return false;
+#pragma unroll
+                    for (int kk = 0; kk < 16; kk++)
+                        mma_ts(d, tmem + kTmQ + kk * 8, smem_desc(base + kOffV + (s * 4 + kk / 4) * kPanel + (kk % 4) * 32, 16, 1024), qk_desc, true);
+                    tc_commit(smem_addr(&aux.s_full[s]));
+                    return true;
+                };
+                ok = qk(0);
+                for (int i = 0; ok && i < w.n; i++) {
+                    if (i + 1 < w.n && !(ok = qk(i + 1))) break;
+                    const int n = it + i, s = n & 1;
+                    ok = wait.one(smem_addr(&aux.p_ready[s]), (n >> 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < kKeys / 16; kk++)
+                        mma_ts(tmem + kTmO, tmem + kTmS + s * kKeys + kk * 8, smem_desc(base + kOffV + s * 4 * kPanel + kk * 2048, kPanel, 1024), pv_desc,
+                               i > 0 || kk > 0);
+                    tc_commit(smem_addr(&aux.v_empty[s]));
+                    tc_commit(smem_addr(&aux.o_done[s]));  // last: the softmax warps wait for it before the CTA ends
+                }
+                it += w.n;
+            } while (ok && w.next(b));
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ---- softmax: a thread per row ----
+        const int t = tid & 127;
+        const uint32_t mine = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t o_at = tmem + kTmO + mine;
+        const float slack = 8.0f / p.c;
+        int it = 0;
+        bool ok = true;
+        do {
+            const bool live = t < w.u.rows;
+            const int r = w.u.row0 + min(t, w.u.rows - 1);
+            const int tok = (int)fdiv((uint32_t)r, b.group), head = r - tok * (int)b.group.d;
+            const int64_t out_row = (int64_t)(w.q.q0 + tok);
+            char *to = p.out + out_row * p.out_token + (int64_t)head * p.out_head + half * kHalf * 2;
+            if (w.u.tiles == 0) {
+                if (live) {
+                    for (int col = 0; col < kHalf; col += 8) *reinterpret_cast<uint4 *>(to + col * 2) = make_uint4(0, 0, 0, 0);
+                    if (p.lse && half == 0) p.lse[out_row * p.heads + head] = -INFINITY;
+                }
+                continue;
+            }
+            const bool warp_live = __any_sync(0xffffffffu, live);
+            // Q: the last tile's scores are out, so the tensor core has done with the previous one
+            {
+                const int q_row0 = w.u.row0;
+#pragma unroll 4
+                for (int i = t; i < 128 * 40; i += 128) {
+                    const int rr = i / 40, cc = i % 40, ur = q_row0 + rr;
+                    if (rr < w.u.rows) {
+                        const int tt = (int)fdiv((uint32_t)ur, b.group), hh = ur - tt * (int)b.group.d;
+                        const int panel = cc / 8 == 4 ? 8 : cc / 8 + 4 - 4 * half;
+                        const uint4 v = *reinterpret_cast<const uint4 *>(p.q + (int64_t)(w.q.q0 + tt) * p.q_token + (int64_t)hh * p.q_head + panel * 128 + (cc & 7) * 16);
+                        st_smem16(base + (cc / 8) * kQPanel + panel_off(rr, cc & 7), v);
+                    }
+                }
+                if (warp_live) {
+                    const char *from = p.q + out_row * p.q_token + (int64_t)head * p.q_head + half * kHalf * 2;
+#pragma unroll
+                    for (int q = 0; q < kQT; q++) {
+                        uint32_t v[32];
+#pragma unroll
+                        for (int i = 0; i < 8; i++) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(from + q * 128 + i * 16);
+                            v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+                        }
+                        tmem_st32(tmem + kTmQ + q * 32 + mine, v);
+                    }
+                    tc_wait_st();
+                }
+                fence_async_smem();
+                tc_fence_before();
+                mbar_arrive(smem_addr(&aux.q_full));
+            }
+            int lo, hi;
+            sees(b, w.q, tok, lo, hi);
+            float m = -INFINITY, l = 0.0f;
+            const int kt0 = w.u.tile0 + w.at.off;
+            for (int k = 0; k < w.n; k++) {
+                const int kb = (kt0 + k) * kKeys, n = it + k, s = n & 1;
+                const uint32_t s_at = tmem + kTmS + s * kKeys + mine;
+                if (!wait.warp(smem_addr(&aux.s_full[s]), (n >> 1) & 1)) { ok = false; break; }
+                tc_fence_after();
+                if (warp_live) {
+                    uint32_t x[2][32];
+                    tmem_ld32(s_at, x[0]);
+                    tmem_ld32(s_at + 32, x[1]);
+                    tc_wait_ld();
+                    if (__any_sync(0xffffffffu, kb < lo || kb + kKeys > hi)) {
+                        const int a = lo - kb, z = hi - kb;
+#pragma unroll
+                        for (int q = 0; q < 2; q++)
+#pragma unroll
+                            for (int i = 0; i < 32; i++)
+                                if (q * 32 + i < a || q * 32 + i >= z) x[q][i] = 0xff800000u;
+                    }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int i = 0; i < 64; i++) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(x[i >> 5][i & 31]));
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    const bool grow = top > m + slack;
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float to_m = grow ? top : m;
+                        const float alpha = grow ? exp2_fast((m - to_m) * p.c) : 1.0f;
+                        l *= alpha;
+                        m = to_m;
+                        if (k > 0) {
+                            if (!wait.warp(smem_addr(&aux.o_done[s ^ 1]), ((n - 1) >> 1) & 1)) { ok = false; break; }
+                            tc_fence_after();
+#pragma unroll
+                            for (int q = 0; q < kHalf / 32; q++) {
+                                uint32_t o[32];
+                                tmem_ld32(o_at + q * 32, o);
+                                tc_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                                tmem_st32(o_at + q * 32, o);
+                            }
+                        }
+                    }
+                    const float mc = m == -INFINITY ? 0.0f : m * p.c;
+                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int i = 0; i < 64; i += 2) {
+                        const float e0 = exp2_fast(fmaf(__uint_as_float(x[i / 32][i % 32]), p.c, -mc));
+                        const float e1 = exp2_fast(fmaf(__uint_as_float(x[i / 32][i % 32 + 1]), p.c, -mc));
+                        sum[i / 2 % 4] += e0 + e1;
+                        pk[i / 2] = pack2<Bf16>(e0, e1);
+                    }
+                    tmem_st32(s_at, pk);
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tc_wait_st();
+                }
+                // rows that no query sees must not reach the second product (the scores of this tile are out)
+                if (kb < w.u.lo || kb + kKeys > w.u.hi) {
+                    const int key = kb + (t & 63);
+                    if (key < w.u.lo || key >= w.u.hi) {
+                        const uint32_t va = base + kOffV + s * 4 * kPanel + (t & 63) * 128 + (t >> 6) * 2 * kPanel;
+#pragma unroll
+                        for (int i = 0; i < 16; i++) st_smem16(va + (i >> 3) * kPanel + (i & 7) * 16, make_uint4(0, 0, 0, 0));
+                    }
+                    fence_async_smem();
+                }
+                tc_fence_before();
+                mbar_arrive(smem_addr(&aux.p_ready[s]));
+            }
+            if (!ok) break;
+            it += w.n;
+            if (!wait.warp(smem_addr(&aux.o_done[(it - 1) & 1]), ((it - 1) >> 1) & 1)) { ok = false; break; }
+            tc_fence_after();
+            const bool whole = w.whole();
+            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+            float *frag = p.ws + (int64_t)(2 * blockIdx.x + (w.at.off == 0 ? 1 : 0)) * (kRows * (kHalf + 2));
+            if (warp_live) {
+#pragma unroll
+                for (int q = 0; q < kHalf / 32; q++) {
+                    uint32_t o[32];
+                    tmem_ld32(o_at + q * 32, o);
+                    tc_wait_ld();
+                    float f[32];
+#pragma unroll
+                    for (int i = 0; i < 32; i++) f[i] = l == 0.0f ? 0.0f : __uint_as_float(o[i]);
+                    if (live) {
+                        if (whole) {
+                            store_row32<Bf16>(to, f, inv, q * 32, kHalf);
+                        } else {
+                            float4 *d = reinterpret_cast<float4 *>(frag + t * kHalf + q * 32);
+#pragma unroll
+                            for (int i = 0; i < 8; i++) d[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                        }
+                    }
+                }
+                if (live) {
+                    if (whole) {
+                        if (p.lse && half == 0) p.lse[out_row * p.heads + head] = l > 0.0f ? fmaf(m, p.scale, logf(l)) : -INFINITY;
+                    } else {
+                        frag[kRows * kHalf + t] = m;
+                        frag[kRows * (kHalf + 1) + t] = l;
+                    }
+                }
+            }
+        } while (w.next(b));
+        (void)ok;
+    }
+    // common exit
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (aux.gave_up) {  // let copies in flight land before the shared memory is given back
+        const unsigned long long t0 = now_ns();
+        while (now_ns() - t0 < 10000000ull) {}
+    }
+    if (warp == 2) tmem_free(tmem, 512);
+}
+
+template <bool Bf16>
+int run_latent(const CUtensorMap &map, const Params &p, int parts, cudaStream_t s)
+{
+    const int st = cuda_status(launch(latent_kernel<Bf16>, dim3(2 * parts), dim3(kThreads), kBytes, s, map, p));
+    if (st != KV_OK || parts < 2) return st;
+    return join_fragments<kHalf, Bf16>(
+        Join{p.b, p.places, p.ws, p.out, p.out_token, p.out_head, p.lse, p.heads, kDV, kRows, 2, parts, p.scale, p.c}, s);
+}
+
+}  // namespace
+
+int preload_latent_kernels()
+{
+    int st = cuda_status(cudaFuncSetAttribute(latent_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes));
+    if (st == KV_OK) st = cuda_status(cudaFuncSetAttribute(latent_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes));
+    return st != KV_OK ? st : load_kernels(latent_kernel<false>, latent_kernel<true>, join_kernel<kHalf, false>, join_kernel<kHalf, true>);
+}
+
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" int kv_latent_attention(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_cache_desc *cache, int32_t tensor,
+                                   const void *q, int64_t q_token_stride, int64_t q_head_stride, void *out, int64_t out_token_stride,
+                                   int64_t out_head_stride, float *lse, void *workspace, int64_t workspace_bytes, kv_stream_t stream)
+{
+    if (d == nullptr || d->n_heads <= 0 || d->n_kv_heads != 1 || d->window < 0 || !(d->scale > 0.0f) || !std::isfinite(d->scale) ||
+        (d->dtype != KV_BF16 && d->dtype != KV_F16))
+        return KV_ERR_INVALID_ARG;
+    int st = check_batch(batch);
+    if (st != KV_OK) return st;
+    if (d->head_dim != kD || d->head_dim_v != kDV || (d->window && !d->causal)) return KV_ERR_UNSUPPORTED;
+    if ((st = check_plane(cache, tensor, 0, 1, kD)) != KV_OK) return st;
+    if (batch->n_reqs == 0 || batch->n_tokens == 0) return KV_OK;
+    if ((st = check_rows(q, q_token_stride, q_head_stride)) != KV_OK) return st;
+    if ((st = check_rows(out, out_token_stride, out_head_stride)) != KV_OK) return st;
+    if (workspace == nullptr) return KV_ERR_INVALID_ARG;
+    if (!aligned16(workspace) || ((uintptr_t)lse & 3u)) return KV_ERR_ALIGN;
+    Params p = {};
+    if ((st = fill_batch(&p.b, batch, d->n_heads, 1, cache->block_size, kRows, kKeys, d->causal, d->window)) != KV_OK) return st;
+    const DeviceInfo *dev = current_device();
+    if (dev == nullptr) return KV_ERR_CUDA;
+    if (workspace_bytes < attention_workspace(dev->num_sms)) return KV_ERR_RANGE;
+    if ((st = prepare_attention(*dev)) != KV_OK) return st;
+    p.b.err = dev->err_word;
+    p.table = batch->block_table;
+    p.table_stride = batch->bt_row_stride;
+    p.num_blocks = (int32_t)cache->num_blocks;
+    p.block = make_fastdiv((uint32_t)cache->block_size);
+    p.piece_rows = piece_rows(cache->block_size, kKeys);
+    p.heads = d->n_heads;
+    p.scale = d->scale;
+    p.c = d->scale * 1.44269504088896340736f;
+    p.q = (const char *)q;
+    p.q_token = q_token_stride;
+    p.q_head = q_head_stride;
+    p.out = (char *)out;
+    p.out_token = out_token_stride;
+    p.out_head = out_head_stride;
+    p.lse = lse;
+    p.places = (Place *)workspace;
+    p.ws = (float *)((char *)workspace + kPlaceBytes);
+    CUtensorMap map;
+    if ((st = make_cache_map(&map, cache, tensor, 0, 1, kD, p.piece_rows)) != KV_OK) return st;
+    const int parts = dev->num_sms / 2;
+    return d->dtype == KV_BF16 ? run_latent<true>(map, p, parts, (cudaStream_t)stream) : run_latent<false>(map, p, parts, (cudaStream_t)stream);
+}

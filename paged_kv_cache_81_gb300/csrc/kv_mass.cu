@@ -1,0 +1,502 @@
+// kv_attention_mass: the attention weight that every cached token receives.
+//
+//   score[r, j] = prev[r, j] + sum over the request's new tokens t that see j, and over the query heads h,
+//                 of exp(scale q[t, h] . K[j] - lse[t, h])
+//
+// The products are formed with keys as the rows of the accumulator, S^T = K Q^T: a thread owns a key and adds
+// the exponentials of its row, column by column in a fixed order, so nothing is shared and nothing atomic.
+// The line (as in kv_plan.cuh) runs over requests, tiles of 128 keys, key heads and tiles of up to 128
+// (token, head of the group) rows; a CTA takes an equal piece of it, and a key tile that was cut is summed
+// from its pieces' partial sums by a second kernel, in their order.
+//   warp 0 loads (K once a head, Q a step), warp 1 issues the products, warps 4-7 and 8-11 take the even
+//   and the odd steps; warps 2 and 3 carry over what lies past the requests' lengths.
+#include "kv_attention.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kTile = 128;
+constexpr uint32_t kPanel = 128 * 128;
+
+template <int DK>
+struct Shape {
+    static constexpr uint32_t kOperand = 128 * DK * 2;
+    static constexpr int kNK = DK == 192 ? 2 : 3, kNQ = kNK;
+    static constexpr uint32_t kOffQ = kNK * kOperand, kOffAux = kOffQ + kNQ * kOperand, kBytes = kOffAux + 3072;
+};
+
+struct Params {
+    Batch b;
+    const int32_t *table;
+    int64_t table_stride;
+    int32_t num_blocks;
+    FastDiv block;
+    int32_t piece_rows, dk, heads;
+    int32_t step_tokens;  // tokens of one step: 128 / group
+    float c;
+    const float *lse;
+    const float *prev;
+    int64_t prev_stride;
+    float *score;
+    int64_t score_stride;
+    int32_t width;
+    float *ws;
+    Place *places;
+};
+
+struct Aux {
+    uint64_t k_full[3], k_empty[3], q_full[3], q_empty[3], s_full[2], s_empty[2], l_ready[2], sum_ready, sum_free;
+    long long scan[12];
+    Place place;
+    float neg[2][128];  // -lse log2 e of a step's rows
+    float odd[128];     // the odd steps' sums
+    uint32_t tmem;
+    int gave_up;
+};
+static_assert(sizeof(Aux) <= 3072, "bookkeeping");
+
+// The steps of one key tile: a key head's query rows, in steps of step_tokens tokens.
+struct KeyTile {
+    int t0, t1;     // tokens that see some key of the tile
+    int per_head;   // steps of a key head
+    int steps;      // of the tile (at least one: its scores have to be written)
+    int lo;         // first key that some token sees
+};
+
+__device__ __forceinline__ KeyTile key_tile(const Params &p, const Request &q, int tile)
+{
+    const Batch &b = p.b;
+    const int kb = tile * kTile, end = min(kb + kTile, q.len), base = q.len - q.q_len;
+    KeyTile k;
+    k.t0 = b.causal ? max(0, kb - base) : 0;
+    k.t1 = b.window ? min(q.q_len, max(0, end - 1 + b.window - base)) : q.q_len;
+    k.per_head = k.t1 > k.t0 ? (k.t1 - k.t0 + p.step_tokens - 1) / p.step_tokens : 0;
+    k.steps = max(1, k.per_head * b.kv_heads);
+    k.lo = b.window ? max(0, base - b.window + 1) : 0;
+    return k;
+}
+
+// The request's first key tiles that all take the same number of steps: without a window those that every
+// new token sees from their first key on, with one those that no token sees.
+__device__ __forceinline__ int even_tiles(const Params &p, const Request &q)
+{
+    const Batch &b = p.b;
+    const int tiles = (q.len + kTile - 1) / kTile, base = q.len - q.q_len;
+    if (b.window) return min(tiles, max(0, base - b.window + 1) / kTile);
+    if (!b.causal) return tiles;
+    return base < 0 ? 0 : min(tiles, base / kTile + 1);
+}
+
+__device__ __forceinline__ long long request_cost(const Params &p, int r)
+{
+    const Request q = load_request(p.b, r);
+    int t = even_tiles(p, q);
+    long long n = t > 0 ? (long long)t * key_tile(p, q, 0).steps : 0;
+    for (; t * kTile < q.len; t++) n += key_tile(p, q, t).steps;
+    return n;
+}
+
+// Walks a piece key tile by key tile.  place.unit: the key tile; place.off: the step inside it.
+struct Walk2 {
+    Place at;
+    int left, n;
+    Request q;
+    KeyTile k;
+    __device__ __forceinline__ bool start(const Params &p, const Place &pl, int steps)
+    {
+        at = pl;
+        left = steps;
+        if (left <= 0) return false;
+        q = load_request(p.b, at.req);
+        k = key_tile(p, q, at.unit);
+        n = min(left, k.steps - at.off);
+        return true;
+    }
+    __device__ __forceinline__ bool next(const Params &p)
+    {
+        left -= n;
+        if (left <= 0) return false;
+        at.off = 0;
+        at.unit++;
+        while (at.unit * kTile >= q.len) {
+            at.unit = 0;
+            q = load_request(p.b, ++at.req);
+        }
+        k = key_tile(p, q, at.unit);
+        n = min(left, k.steps);
+        return true;
+    }
+};
+
+template <int DK, bool Bf16>
+__global__ void __launch_bounds__(kThreads, 1)
+mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap q_map, const Params p)
+{
+    using S = Shape<DK>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const uint32_t base = smem_addr(smem);
+    Aux &aux = *reinterpret_cast<Aux *>(smem + S::kOffAux);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Batch &b = p.b;
+    const Waiter wait{&aux.gave_up, b.err};
+    const int group = (int)b.group.d;
+
+    if (tid == 0) {
+        aux.gave_up = 0;
+        for (int i = 0; i < 3; i++) {
+            mbar_init(smem_addr(&aux.k_full[i]), 1);
+            mbar_init(smem_addr(&aux.k_empty[i]), 1);
+            mbar_init(smem_addr(&aux.q_full[i]), 1);
+            mbar_init(smem_addr(&aux.q_empty[i]), 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            mbar_init(smem_addr(&aux.s_full[i]), 1);
+            mbar_init(smem_addr(&aux.s_empty[i]), 128);
+            mbar_init(smem_addr(&aux.l_ready[i]), 128);
+        }
+        mbar_init(smem_addr(&aux.sum_ready), 128);
+        mbar_init(smem_addr(&aux.sum_free), 128);
+        mbar_init_fence();
+        tma_prefetch_map(&k_map);
+        tma_prefetch_map(&q_map);
+    }
+    if (warp == 2) tmem_alloc(smem_addr(&aux.tmem), 256);
+    grid_dep_entry();
+    const int steps = find_piece<kThreads>(
+        b.n_reqs, blockIdx.x, gridDim.x, aux.scan,
+        [&](int r) {
+            if (blockIdx.x == 0) load_request(b, r, true);
+            return request_cost(p, r);
+        },
+        [&](int r, long long rest) {
+            const Request q = load_request(b, r);
+            Place pl{r, 0, 0, 0};
+            const int even = even_tiles(p, q);
+            if (even > 0) {
+                const int n = key_tile(p, q, 0).steps;
+                pl.unit = (int)min((long long)even, rest / n);
+                rest -= (long long)pl.unit * n;
+            }
+            for (;; pl.unit++) {
+                const int n = key_tile(p, q, pl.unit).steps;
+                if (rest < n) break;
+                rest -= n;
+            }
+            pl.off = (int)rest;
+            aux.place = pl;
+        });
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = aux.tmem;
+    if (tid == 0) {
+        Place pl = aux.place;
+        if (steps <= 0) pl.req = -1;
+        p.places[blockIdx.x] = pl;
+    }
+
+    Walk2 w;
+    if (warp == 2 || warp == 3) {
+        // what lies past every request's length is carried over
+        const int me = blockIdx.x * 64 + (tid & 63), all = gridDim.x * 64;
+        for (int r = 0; r < b.n_reqs; r++) {
+            const int len = min(max(__ldg(b.kv_lens + r), 0), b.max_tokens);
+            for (int j = len + me; j < p.width; j += all)
+                p.score[(int64_t)r * p.score_stride + j] = p.prev ? p.prev[(int64_t)r * p.prev_stride + j] : 0.0f;
+        }
+    } else if (!w.start(p, aux.place, steps)) {
+        // nothing to do: on to the common exit
+    } else if (warp == 0) {
+        const int pr = p.piece_rows;
+        int kt = 0, it = 0;
+        bool ok = true;
+        do {
+            if (w.k.per_head == 0) continue;
+            const int kb = w.at.unit * kTile, p0 = max(0, w.k.lo - kb) / pr, p1 = (min(w.q.len - kb, kTile) + pr - 1) / pr;
+            const int32_t *row = p.table + (int64_t)w.at.req * p.table_stride;
+            for (int i = 0; ok && i < w.n; i++, it++) {
+                const int step = w.at.off + i, head = step / w.k.per_head, qi = step - head * w.k.per_head;
+                if (i == 0 || qi == 0) {
+                    const int s = kt % S::kNK;
+                    const uint32_t bar = smem_addr(&aux.k_full[s]);
+                    if (kt >= S::kNK && !wait.warp(smem_addr(&aux.k_empty[s]), ((kt / S::kNK) - 1) & 1)) { ok = false; break; }
+                    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)((p1 - p0) * pr) * DK * 2);
+                    __syncwarp();
+                    for (int j = p0 + lane; j < p1; j += 32) {
+                        const uint32_t key = (uint32_t)(kb + j * pr), col = fdiv(key, p.block);
+                        int page = __ldg(row + col);
+                        if (page < 0 || page >= p.num_blocks) {
+                            set_error(b.err, KV_DERR_TABLE);
+                            page = p.num_blocks;  // outside the map: reads zeros
+                        }
+#pragma unroll
+                        for (int h = 0; h < DK / 64; h++)
+                            tma_load_4d(base + s * S::kOperand + h * kPanel + j * pr * 128, &k_map, bar, h * 64, head, (int)(key - col * p.block.d), page);
+                    }
+                    kt++;
+                }
+                const int s = it % S::kNQ;
+                if (it >= S::kNQ && !wait.warp(smem_addr(&aux.q_empty[s]), ((it / S::kNQ) - 1) & 1)) { ok = false; break; }
+                if (lane == 0) {
+                    const uint32_t bar = smem_addr(&aux.q_full[s]);
+                    mbar_arrive_expect_tx(bar, (uint32_t)(p.step_tokens * group) * DK * 2);
+#pragma unroll
+                    for (int h = 0; h < DK / 64; h++)
+                        tma_load_3d(base + S::kOffQ + s * S::kOperand + h * kPanel, &q_map, bar, h * 64, head * group,
+                                    w.q.q0 + w.k.t0 + qi * p.step_tokens);
+                }
+                __syncwarp();
+            }
+        } while (ok && w.next(p));
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t desc = mma_desc(Bf16, 128, (uint32_t)((p.step_tokens * group + 15) / 16 * 16), false);
+            int kt = -1, it = 0;
+            bool ok = true;
+            do {
+                if (w.k.per_head == 0) continue;
+                for (int i = 0; ok && i < w.n; i++, it++) {
+                    const int qi = (w.at.off + i) % w.k.per_head, g = it & 1, s = it % S::kNQ;
+                    if (i == 0 || qi == 0) {
+                        kt++;
+                        ok = wait.one(smem_addr(&aux.k_full[kt % S::kNK]), (kt / S::kNK) & 1);
+                    }
+                    ok = ok && wait.one(smem_addr(&aux.q_full[s]), (it / S::kNQ) & 1) &&
+                         (it < 2 || wait.one(smem_addr(&aux.s_empty[g]), ((it >> 1) - 1) & 1));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t ka = base + (kt % S::kNK) * S::kOperand, qa = base + S::kOffQ + s * S::kOperand;
+#pragma unroll
+                    for (int kk = 0; kk < DK / 16; kk++) {
+                        const uint32_t o = (kk / 4) * kPanel + (kk % 4) * 32;
+                        mma_ss(tmem + g * 128, smem_desc(ka + o, 16, 1024), smem_desc(qa + o, 16, 1024), desc, kk > 0);
+                    }
+                    tc_commit(smem_addr(&aux.q_empty[s]));
+                    if (i + 1 == w.n || qi + 1 == w.k.per_head) tc_commit(smem_addr(&aux.k_empty[kt % S::kNK]));
+                    tc_commit(smem_addr(&aux.s_full[g]));  // last: the groups wait for it before the CTA ends
+                }
+            } while (ok && w.next(p));
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        const int g = (warp - 4) >> 2, t = tid & 127;
+        const uint32_t s_at = tmem + g * 128 + ((uint32_t)((warp & 3) * 32) << 16);
+        int it = 0, mine = 0, tiles = 0;
+        bool ok = true;
+        do {
+            const int key = w.at.unit * kTile + t;
+            float sum = 0.0f;
+            if (w.k.per_head) {
+                const int kt0 = w.q.q0 + w.k.t0, ntok = w.k.t1 - w.k.t0, base_pos = w.q.len - w.q.q_len + w.k.t0;
+                // tokens (counted from t0) that see this key: [va, vb)
+                const int va = b.causal ? max(0, key - base_pos) : 0, vb = key >= w.q.len ? 0 : b.window ? min(ntok, max(0, key + b.window - base_pos)) : ntok;
+                for (int i = 0; i < w.n; i++, it++) {
+                    if ((it & 1) != g) continue;
+                    const int step = w.at.off + i, head = step / w.k.per_head, tok0 = (step - head * w.k.per_head) * p.step_tokens;
+                    const int cols = min(p.step_tokens, ntok - tok0) * group;
+                    float v = -INFINITY;
+                    if (t < cols) {
+                        const int tt = (int)fdiv((uint32_t)t, b.group);
+                        v = -p.lse[(int64_t)(kt0 + tok0 + tt) * p.heads + head * group + t - tt * group] * 1.44269504088896340736f;
+                        if (v == INFINITY) v = -INFINITY;  // a row that saw nothing weighs nothing
+                    }
+                    // these scores are out, so the whole group has done with the previous step's row of `neg`
+                    if (!wait.warp(smem_addr(&aux.s_full[g]), mine & 1)) { ok = false; break; }
+                    aux.neg[g][t] = v;
+                    mbar_arrive(smem_addr(&aux.l_ready[g]));
+                    if (!wait.warp(smem_addr(&aux.l_ready[g]), mine & 1)) { ok = false; break; }
+                    tc_fence_after();
+                    const int c0 = (va - tok0) * group, c1 = min(cols, (vb - tok0) * group);
+                    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    for (int q = 0; q < cols; q += 32) {
+                        uint32_t x[32];
+                        tmem_ld32(s_at + q, x);
+                        tc_wait_ld();
+                        const float4 *neg = reinterpret_cast<const float4 *>(&aux.neg[g][q]);
+                        if (__any_sync(0xffffffffu, c0 > q || c1 < q + 32)) {
+#pragma unroll
+                            for (int j = 0; j < 32; j++)
+                                if (q + j < c0 || q + j >= c1) x[j] = 0xff800000u;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 8; j++) {
+                            const float4 e = neg[j];
+                            part[0] += exp2_fast(fmaf(__uint_as_float(x[4 * j]), p.c, e.x));
+                            part[1] += exp2_fast(fmaf(__uint_as_float(x[4 * j + 1]), p.c, e.y));
+                            part[2] += exp2_fast(fmaf(__uint_as_float(x[4 * j + 2]), p.c, e.z));
+                            part[3] += exp2_fast(fmaf(__uint_as_float(x[4 * j + 3]), p.c, e.w));
+                        }
+                    }
+                    sum += (part[0] + part[1]) + (part[2] + part[3]);
+                    tc_fence_before();
+                    mbar_arrive(smem_addr(&aux.s_empty[g]));
+                    mine++;
+                }
+                if (!ok) break;
+            }
+            // the odd steps' group hands its sums over
+            if (g == 1) {
+                if (tiles && !wait.warp(smem_addr(&aux.sum_free), (tiles - 1) & 1)) { ok = false; break; }
+                aux.odd[t] = sum;
+                mbar_arrive(smem_addr(&aux.sum_ready));
+            } else {
+                if (!wait.warp(smem_addr(&aux.sum_ready), tiles & 1)) { ok = false; break; }
+                sum += aux.odd[t];
+                mbar_arrive(smem_addr(&aux.sum_free));
+                if (w.at.off == 0 && w.n == w.k.steps) {
+                    if (key < w.q.len && key < p.width)
+                        p.score[(int64_t)w.at.req * p.score_stride + key] = sum + (p.prev ? p.prev[(int64_t)w.at.req * p.prev_stride + key] : 0.0f);
+                } else {
+                    p.ws[(2 * blockIdx.x + (w.at.off == 0 ? 1 : 0)) * kTile + t] = sum;
+                }
+            }
+            tiles++;
+        } while (w.next(p));
+        (void)ok;
+    }
+    // common exit
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (aux.gave_up) {  // let copies in flight land before the shared memory is given back
+        const unsigned long long t0 = now_ns();
+        while (now_ns() - t0 < 10000000ull) {}
+    }
+    if (warp == 2) tmem_free(tmem, 256);
+}
+
+// Sums the pieces of the key tiles that were cut, in their order.
+__global__ void __launch_bounds__(kTile) mass_join_kernel(const Params p, int parts)
+{
+    grid_dep_entry();
+    const int c = blockIdx.x + 1, t = threadIdx.x;
+    const Place pl = p.places[c];
+    if (pl.req < 0 || pl.off == 0) return;
+    const Place before = p.places[c - 1];
+    if (before.req == pl.req && before.unit == pl.unit && before.off != 0) return;  // an earlier cut of the tile joins it
+    float sum = p.ws[(2 * (c - 1) + 1) * kTile + t];
+    for (int x = c; x < parts; x++) {
+        const Place at = p.places[x];
+        if (at.req != pl.req || at.unit != pl.unit || at.off == 0) break;
+        sum += p.ws[2 * x * kTile + t];
+    }
+    const int key = pl.unit * kTile + t;
+    if (key < load_request(p.b, pl.req).len && key < p.width)
+        p.score[(int64_t)pl.req * p.score_stride + key] = sum + (p.prev ? p.prev[(int64_t)pl.req * p.prev_stride + key] : 0.0f);
+}
+
+template <int DK, bool Bf16>
+int run_mass(const CUtensorMap &km, const CUtensorMap &qm, const Params &p, int parts, cudaStream_t s, bool prepare)
+{
+    if (prepare)
+        return cuda_status(cudaFuncSetAttribute(mass_kernel<DK, Bf16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<DK>::kBytes));
+    const int st = cuda_status(launch(mass_kernel<DK, Bf16>, dim3(parts), dim3(kThreads), Shape<DK>::kBytes, s, km, qm, p));
+    if (st != KV_OK || parts < 2) return st;
+    return cuda_status(launch(mass_join_kernel, dim3(parts - 1), dim3(kTile), 0, s, p, parts));
+}
+
+template <bool Bf16>
+int pick_mass(int dk, const CUtensorMap &km, const CUtensorMap &qm, const Params &p, int parts, cudaStream_t s, bool prepare)
+{
+    if (dk <= 64) return run_mass<64, Bf16>(km, qm, p, parts, s, prepare);
+    if (dk <= 128) return run_mass<128, Bf16>(km, qm, p, parts, s, prepare);
+    return run_mass<192, Bf16>(km, qm, p, parts, s, prepare);
+}
+
+int64_t mass_workspace(int num_sms) { return kPlaceBytes + (int64_t)num_sms * 2 * kTile * 4; }
+
+}  // namespace
+
+int preload_mass_kernels()
+{
+    Params p = {};
+    CUtensorMap m;
+    for (int dk : {64, 128, 192})
+        for (bool bf : {false, true}) {
+            const int st = bf ? pick_mass<true>(dk, m, m, p, 0, nullptr, true) : pick_mass<false>(dk, m, m, p, 0, nullptr, true);
+            if (st != KV_OK) return st;
+        }
+    return load_kernels(mass_kernel<64, false>, mass_kernel<64, true>, mass_kernel<128, false>, mass_kernel<128, true>,
+                        mass_kernel<192, false>, mass_kernel<192, true>, mass_join_kernel);
+}
+
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" {
+
+int kv_attention_mass_workspace_bytes(int64_t *bytes_out)
+{
+    if (bytes_out == nullptr) return KV_ERR_INVALID_ARG;
+    const DeviceInfo *d = current_device();
+    if (d == nullptr) return KV_ERR_CUDA;
+    *bytes_out = mass_workspace(d->num_sms);
+    return KV_OK;
+}
+
+int kv_attention_mass(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_cache_desc *k, int32_t k_tensor, int32_t k_plane,
+                      const void *q, int64_t q_token_stride, int64_t q_head_stride, const float *lse, const float *prev,
+                      int64_t prev_stride, float *score, int64_t score_stride, int32_t width, void *workspace, int64_t workspace_bytes,
+                      kv_stream_t stream)
+{
+    if (d == nullptr || d->n_heads <= 0 || d->n_kv_heads <= 0 || d->n_heads % d->n_kv_heads != 0 || d->head_dim <= 0 || d->window < 0 ||
+        !(d->scale > 0.0f) || !std::isfinite(d->scale) || (d->dtype != KV_BF16 && d->dtype != KV_F16) || width < 0)
+        return KV_ERR_INVALID_ARG;
+    int st = check_batch(batch);
+    if (st != KV_OK) return st;
+    if (d->head_dim % 8) return KV_ERR_ALIGN;
+    if (d->head_dim > 192 || d->n_heads / d->n_kv_heads > 128 || (d->window && !d->causal)) return KV_ERR_UNSUPPORTED;
+    if ((st = check_plane(k, k_tensor, k_plane, d->n_kv_heads, d->head_dim)) != KV_OK) return st;
+    if (batch->n_reqs == 0 || width == 0) return KV_OK;
+    if (batch->n_tokens > 0) {
+        if ((st = check_rows(q, q_token_stride, q_head_stride)) != KV_OK) return st;
+        if (lse == nullptr) return KV_ERR_INVALID_ARG;
+        if (q_token_stride >= (1ll << 40) || q_head_stride >= (1ll << 40)) return KV_ERR_UNSUPPORTED;
+    }
+    if (score == nullptr || workspace == nullptr || score_stride < 0 || prev_stride < 0) return KV_ERR_INVALID_ARG;
+    if (batch->n_reqs > 1 && (score_stride < width || (prev != nullptr && prev_stride < width))) return KV_ERR_INVALID_ARG;
+    if (!aligned16(workspace) || ((uintptr_t)lse & 3u) || ((uintptr_t)prev & 3u) || ((uintptr_t)score & 3u)) return KV_ERR_ALIGN;
+    Params p = {};
+    if ((st = fill_batch(&p.b, batch, d->n_heads, d->n_kv_heads, k->block_size, 128, kTile, d->causal, d->window)) != KV_OK) return st;
+    const DeviceInfo *dev = current_device();
+    if (dev == nullptr) return KV_ERR_CUDA;
+    if (workspace_bytes < mass_workspace(dev->num_sms)) return KV_ERR_RANGE;
+    if ((st = prepare_attention(*dev)) != KV_OK) return st;
+    p.b.err = dev->err_word;
+    p.table = batch->block_table;
+    p.table_stride = batch->bt_row_stride;
+    p.num_blocks = (int32_t)k->num_blocks;
+    p.block = make_fastdiv((uint32_t)k->block_size);
+    p.piece_rows = piece_rows(k->block_size, kTile);
+    p.dk = d->head_dim;
+    p.heads = d->n_heads;
+    const int group = d->n_heads / d->n_kv_heads;
+    p.step_tokens = 128 / group;
+    if (batch->n_tokens > 0 && p.step_tokens > batch->n_tokens) p.step_tokens = (int32_t)batch->n_tokens;
+    p.c = d->scale * 1.44269504088896340736f;
+    p.lse = lse;
+    p.prev = prev;
+    p.prev_stride = prev_stride;
+    p.score = score;
+    p.score_stride = score_stride;
+    p.width = width;
+    p.places = (Place *)workspace;
+    p.ws = (float *)((char *)workspace + kPlaceBytes);
+    CUtensorMap km, qm;
+    if ((st = make_cache_map(&km, k, k_tensor, k_plane, d->n_kv_heads, d->head_dim, p.piece_rows)) != KV_OK) return st;
+    if (batch->n_tokens > 0) {
+        const uint64_t dims[3] = {(uint64_t)d->head_dim, (uint64_t)d->n_heads, (uint64_t)batch->n_tokens};
+        const uint64_t strides[2] = {(uint64_t)q_head_stride, (uint64_t)q_token_stride};
+        const uint32_t box[3] = {64, (uint32_t)group, (uint32_t)p.step_tokens};
+        if ((st = make_map(&qm, (uint64_t)q, 3, dims, strides, box)) != KV_OK) return st;
+    } else {
+        qm = km;  // never used: no request has new tokens
+    }
+    return d->dtype == KV_BF16 ? pick_mass<true>(p.dk, km, qm, p, dev->num_sms, (cudaStream_t)stream, false)
+                               : pick_mass<false>(p.dk, km, qm, p, dev->num_sms, (cudaStream_t)stream, false);
+}
+
+}  // extern "C"

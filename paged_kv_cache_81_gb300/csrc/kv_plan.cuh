@@ -2,7 +2,7 @@
 //
 // A request's query rows are its (token, head of the group) pairs, token-major: row = token * group +
 // head.  Rows are cut into units of `unit_rows`; a unit of one key head needs the key tiles of
-// kTile keys between the first key that its first token sees and the last that its last token sees.
+// `tile` keys between the first key that its first token sees and the last that its last token sees.
 // Laid end to end (request, key head, unit), all units' tiles form one line; CTA c of `parts` takes
 // the c-th equal piece of it.  A piece may begin and end inside a unit: those two fragments go to the
 // workspace and are joined by a second kernel.  So the split follows the lengths, not the launch: one
@@ -16,8 +16,6 @@
 
 namespace pkv {
 
-constexpr int kTile = 128;  // keys of one tile
-
 struct Batch {
     const int32_t *q_offsets;  // [n_reqs + 1]
     const int32_t *kv_lens;    // [n_reqs]
@@ -26,6 +24,7 @@ struct Batch {
     int32_t max_tokens;  // capacity of a table row in tokens: kv_lens entries are clamped to it
     int32_t kv_heads;
     int32_t unit_rows;
+    int32_t tile;  // keys of one tile
     int32_t causal;
     int32_t window;  // 0: none
     FastDiv group;   // query heads of a key head
@@ -75,8 +74,8 @@ __device__ __forceinline__ Unit make_unit(const Batch &b, const Request &q, int 
     int x;
     sees(b, q, (int)fdiv((uint32_t)u.row0, b.group), u.lo, x);
     sees(b, q, (int)fdiv((uint32_t)(u.row0 + u.rows - 1), b.group), x, u.hi);
-    u.tile0 = u.lo / kTile;
-    u.tiles = u.hi > u.lo ? (u.hi + kTile - 1) / kTile - u.tile0 : 0;
+    u.tile0 = u.lo / b.tile;
+    u.tiles = u.hi > u.lo ? (u.hi + b.tile - 1) / b.tile - u.tile0 : 0;
     return u;
 }
 
@@ -95,17 +94,18 @@ struct Place {
     int32_t req, head, unit, off;
 };
 
-// Finds this CTA's piece of the line; every thread of the block calls it.  `scratch`: 33 words of 8
-// bytes; `place`: where the piece begins.  Returns the tiles in the piece (0: none).
-template <int Threads>
-__device__ int find_piece(const Batch &b, int part, int parts, long long *scratch, Place *place, bool report)
+// Finds a CTA's piece of a line made of n_reqs stretches, the r-th cost(r) steps long; every thread of
+// the block calls it.  scratch: one 8-byte word a warp.  Returns the steps of piece `part` of `parts` (0:
+// none) and calls found(request, step inside its stretch) in the one thread that holds its beginning.
+template <int Threads, typename Cost, typename Found>
+__device__ __forceinline__ int find_piece(int n_reqs, int part, int parts, long long *scratch, const Cost &cost, const Found &found)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kWarps = Threads / 32;
-    const int per = (b.n_reqs + Threads - 1) / Threads;
-    const int r0 = min(tid * per, b.n_reqs), r1 = min(r0 + per, b.n_reqs);
+    const int per = (n_reqs + Threads - 1) / Threads;
+    const int r0 = min(tid * per, n_reqs), r1 = min(r0 + per, n_reqs);
     long long mine = 0;
-    for (int r = r0; r < r1; r++) mine += head_cost(b, load_request(b, r, report)) * b.kv_heads;
+    for (int r = r0; r < r1; r++) mine += cost(r);
     long long upto = mine;  // inclusive scan
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -128,31 +128,40 @@ __device__ int find_piece(const Batch &b, int part, int parts, long long *scratc
         if (w0 >= upto - mine && w0 < upto) {
             long long rest = w0 - (upto - mine);
             for (int r = r0; r < r1; r++) {
-                const Request q = load_request(b, r);
-                const long long h = head_cost(b, q), all = h * b.kv_heads;
-                if (rest >= all) {
-                    rest -= all;
-                    continue;
+                const long long all = cost(r);
+                if (rest < all) {
+                    found(r, rest);
+                    break;
                 }
-                Place p;
-                p.req = r;
-                p.head = (int)(rest / h);
-                rest -= p.head * h;
-                int j = 0;
-                for (;; j++) {
-                    const int n = unit_cost(make_unit(b, q, j));
-                    if (rest < n) break;
-                    rest -= n;
-                }
-                p.unit = j;
-                p.off = (int)rest;
-                *place = p;
-                break;
+                rest -= all;
             }
         }
     }
     __syncthreads();
     return (int)(w1 - w0);
+}
+
+// This CTA's piece of an attention batch's line.
+template <int Threads>
+__device__ __forceinline__ int find_place(const Batch &b, int part, int parts, long long *scratch, Place *place, bool report)
+{
+    return find_piece<Threads>(
+        b.n_reqs, part, parts, scratch, [&](int r) { return head_cost(b, load_request(b, r, report)) * b.kv_heads; },
+        [&](int r, long long rest) {
+            const Request q = load_request(b, r);
+            const long long h = head_cost(b, q);
+            Place p;
+            p.req = r;
+            p.head = (int)(rest / h);
+            rest -= p.head * h;
+            for (p.unit = 0;; p.unit++) {
+                const int n = unit_cost(make_unit(b, q, p.unit));
+                if (rest < n) break;
+                rest -= n;
+            }
+            p.off = (int)rest;
+            *place = p;
+        });
 }
 
 // Walks a piece unit by unit.

@@ -95,7 +95,8 @@ int prepare_attention(const DeviceInfo &dev)
     static bool done[kMaxDevices];
     std::lock_guard<std::mutex> lock(mu);
     if (done[dev.device]) return KV_OK;
-    for (int (*load)() : {preload_attention_kernels}) {
+    for (int (*load)() : {preload_attention_kernels, preload_latent_kernels, preload_expand_kernels, preload_mass_kernels,
+                          preload_evict_kernels}) {
         const int st = load();
         if (st != KV_OK) return st;
     }

@@ -30,7 +30,8 @@ EXPORTS = ("kv_version", "kv_status_string", "kv_last_cuda_error", "kv_slot_mapp
            "kv_xfer_workspace_bytes", "kv_build_xfer_list", "kv_pack_blocks", "kv_unpack_blocks",
            "kv_get_last_error", "kv_build_xfer_list_static", "kv_unpack_blocks_signal", "kv_wait_signal",
            "kv_clip_block_lists", "kv_block_hashes", "kv_block_hashes_workspace_bytes", "kv_write_tokens",
-           "kv_attention", "kv_attention_workspace_bytes")
+           "kv_attention", "kv_attention_workspace_bytes", "kv_latent_attention", "kv_latent_expand", "kv_attention_mass",
+           "kv_attention_mass_workspace_bytes", "kv_evict")
 
 
 class KvError(RuntimeError):
@@ -125,6 +126,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             "kv_block_hashes_workspace_bytes": ([i64, i32, ctypes.POINTER(ctypes.c_int64)], ctypes.c_int),
             "kv_attention_workspace_bytes": ([ctypes.POINTER(i64)], ctypes.c_int),
             "kv_attention": ([A, B, D, i32, i32, D, i32, i32, P, i64, i64, P, i64, i64, P, P, i64, P], ctypes.c_int),
+            "kv_latent_attention": ([A, B, D, i32, P, i64, i64, P, i64, i64, P, P, i64, P], ctypes.c_int),
+            "kv_latent_expand": ([i32, i32, D, i32, P, i32, i32, i64, P, P, D, i32, D, i32, P, i32, i64, P], ctypes.c_int),
+            "kv_attention_mass_workspace_bytes": ([ctypes.POINTER(i64)], ctypes.c_int),
+            "kv_attention_mass": ([A, B, D, i32, i32, P, i64, i64, P, P, i64, P, i64, i32, P, i64, P], ctypes.c_int),
+            "kv_evict": ([D, P, i32, i32, i64, P, P, i64, i32, i32, i32, i32, P, i32, i64, P, P, i64, P, i64, P],
+                         ctypes.c_int),
             "kv_write_tokens": ([D, P, i64, P, i32, i32, i64, P, P, i64, P, P], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
@@ -513,6 +520,19 @@ def _strides(t: torch.Tensor):
     return t.stride(0) * t.element_size(), t.stride(1) * t.element_size()
 
 
+def _attn_outputs(q: torch.Tensor, dv: int, out: Optional[torch.Tensor], lse: Optional[torch.Tensor]):
+    T, H, _ = q.shape
+    if out is None:
+        out = torch.empty((T, H, dv), dtype=q.dtype, device=q.device)
+    elif _rows3(out, "out").shape != (T, H, dv) or out.dtype != q.dtype:
+        raise ValueError("out must be [tokens, heads, value dim] of q's type")
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+    elif lse.shape != (T, H) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 [tokens, heads] tensor")
+    return out, lse
+
+
 def kv_attention(q: torch.Tensor, cache: PagedCache, block_table: torch.Tensor, q_offsets: torch.Tensor,
                  kv_lens: torch.Tensor, scale: float, *, v_cache: Optional[PagedCache] = None, k_tensor: int = 0,
                  v_tensor: Optional[int] = None, causal: bool = True, window: int = 0, out: Optional[torch.Tensor] = None,
@@ -536,14 +556,7 @@ def kv_attention(q: torch.Tensor, cache: PagedCache, block_table: torch.Tensor, 
         raise ValueError("the cache's rows are not whole heads of q's width")
     dv = values.row_bytes // (kv_heads * q.element_size())
     batch = _attn_batch(block_table, q_offsets, kv_lens, T)
-    if out is None:
-        out = torch.empty((T, H, dv), dtype=q.dtype, device=q.device)
-    elif _rows3(out, "out").shape != (T, H, dv) or out.dtype != q.dtype:
-        raise ValueError("out must be [tokens, heads, value dim] of q's type")
-    if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    elif lse.shape != (T, H) or lse.dtype != torch.float32 or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous float32 [tokens, heads] tensor")
+    out, lse = _attn_outputs(q, dv, out, lse)
     if workspace is None:
         workspace = kv_attention_workspace(q.device)
     desc = KvAttnDesc(_DTYPES[q.dtype], H, kv_heads, dk, dv, int(causal), int(window), float(scale))
@@ -552,6 +565,128 @@ def kv_attention(q: torch.Tensor, cache: PagedCache, block_table: torch.Tensor, 
         int(v_tensor), v_plane, _ptr(q), *_strides(q), _ptr(out), *_strides(out), _ptr(lse), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream)))
     return out, lse
+
+
+LATENT_DIM, LATENT_RANK = 576, 512  # elements of a latent row, and of its latent part
+
+
+def kv_latent_attention(q: torch.Tensor, cache: PagedCache, block_table: torch.Tensor, q_offsets: torch.Tensor,
+                        kv_lens: torch.Tensor, scale: float, *, tensor: int = 0, causal: bool = True, window: int = 0,
+                        out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of new tokens q [tokens, heads, 576] over a latent cache (the absorbed form); returns
+    (out [tokens, heads, 512], lse float32 [tokens, heads])."""
+    _rows3(q, "q")
+    _like_cache(cache, q.dtype, "cache")
+    T, H, dk = q.shape
+    batch = _attn_batch(block_table, q_offsets, kv_lens, T)
+    out, lse = _attn_outputs(q, LATENT_RANK, out, lse)
+    if workspace is None:
+        workspace = kv_attention_workspace(q.device)
+    desc = KvAttnDesc(_DTYPES[q.dtype], H, 1, dk, LATENT_RANK, int(causal), int(window), float(scale))
+    _check("kv_latent_attention", load().kv_latent_attention(
+        ctypes.byref(desc), ctypes.byref(batch), ctypes.byref(cache.desc()), int(tensor), _ptr(q), *_strides(q), _ptr(out),
+        *_strides(out), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out, lse
+
+
+def _table(t: torch.Tensor, name: str) -> torch.Tensor:
+    if t.dtype != torch.int32 or t.dim() != 2 or t.stride(1) != 1:
+        raise ValueError(f"{name} must be a row-major int32 [n_reqs, max_blocks] CUDA tensor")
+    return t
+
+
+def kv_latent_expand(cache: PagedCache, block_table: torch.Tensor, kv_lens: torch.Tensor, weight: torch.Tensor,
+                     k_out: PagedCache, v_out: PagedCache, out_table: torch.Tensor, *, tensor: int = 0, k_tensor: int = 0,
+                     v_tensor: int = 0, stream=None):
+    """The latent rows of every request multiplied out by weight [heads, 256, 512] into per-head keys (192) and
+    values (128) of the caches k_out and v_out, at the same tokens of out_table."""
+    _table(block_table, "block_table"), _table(out_table, "out_table"), _i32(kv_lens, "kv_lens")
+    if weight.dim() != 3 or tuple(weight.shape[1:]) != (256, LATENT_RANK) or not weight.is_contiguous() or weight.dtype not in _DTYPES:
+        raise ValueError("weight must be a contiguous bf16 or fp16 [heads, 256, 512] CUDA tensor")
+    for c, name in ((cache, "cache"), (k_out, "k_out"), (v_out, "v_out")):
+        _like_cache(c, weight.dtype, name)
+    n = kv_lens.shape[0]
+    if block_table.shape[0] != n or out_table.shape[0] != n:
+        raise ValueError("block_table, out_table and kv_lens are of different numbers of requests")
+    _check("kv_latent_expand", load().kv_latent_expand(
+        _DTYPES[weight.dtype], weight.shape[0], ctypes.byref(cache.desc()), int(tensor), _ptr(block_table), n,
+        block_table.shape[1], block_table.stride(0), _ptr(kv_lens), _ptr(weight), ctypes.byref(k_out.desc()), int(k_tensor),
+        ctypes.byref(v_out.desc()), int(v_tensor), _ptr(out_table), out_table.shape[1], out_table.stride(0), _stream(stream)))
+
+
+def kv_attention_mass_workspace_bytes() -> int:
+    out = ctypes.c_int64(0)
+    _check("kv_attention_mass_workspace_bytes", load().kv_attention_mass_workspace_bytes(ctypes.byref(out)))
+    return out.value
+
+
+def kv_attention_mass(q: torch.Tensor, cache: PagedCache, block_table: torch.Tensor, q_offsets: torch.Tensor,
+                      kv_lens: torch.Tensor, lse: torch.Tensor, scale: float, *, k_tensor: int = 0, causal: bool = True,
+                      window: int = 0, prev: Optional[torch.Tensor] = None, score: Optional[torch.Tensor] = None,
+                      width: Optional[int] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The attention weight every cached token receives from q, added to prev (float32 [n_reqs, width], or None);
+    returns score [n_reqs, width].  width: prev's or score's columns, else a table row's slots."""
+    _rows3(q, "q")
+    _like_cache(cache, q.dtype, "cache")
+    T, H, dk = q.shape
+    kv_heads, left = divmod(cache.row_bytes, dk * q.element_size())
+    if left or not kv_heads:
+        raise ValueError("the cache's rows are not whole heads of q's width")
+    batch = _attn_batch(block_table, q_offsets, kv_lens, T)
+    if lse.shape != (T, H) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 [tokens, heads] tensor")
+    n = kv_lens.shape[0]
+    if width is None:
+        width = prev.shape[1] if prev is not None else score.shape[1] if score is not None else batch.max_blocks_per_req * cache.block_size
+    if score is None:
+        score = torch.empty((n, width), dtype=torch.float32, device=q.device)
+    for t, name in ((prev, "prev"), (score, "score")):
+        if t is not None and (t.dtype != torch.float32 or t.dim() != 2 or t.shape[0] != n or t.shape[1] < width or t.stride(1) != 1):
+            raise ValueError(f"{name} must be a row-major float32 [n_reqs, width] CUDA tensor")
+    if workspace is None:
+        with torch.cuda.device(q.device):
+            workspace = torch.empty(kv_attention_mass_workspace_bytes(), dtype=torch.uint8, device=q.device)
+    desc = KvAttnDesc(_DTYPES[q.dtype], H, kv_heads, dk, dk, int(causal), int(window), float(scale))
+    _check("kv_attention_mass", load().kv_attention_mass(
+        ctypes.byref(desc), ctypes.byref(batch), ctypes.byref(cache.desc()), int(k_tensor), 0, _ptr(q), *_strides(q), _ptr(lse),
+        _ptr(prev), prev.stride(0) if prev is not None else 0, _ptr(score), score.stride(0), int(width), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+    return score
+
+
+def kv_evict(cache: PagedCache, block_table: torch.Tensor, kv_lens: torch.Tensor, score: torch.Tensor, budget: int, *,
+             sinks: int = 0, recent: int = 0, out_table: Optional[torch.Tensor] = None, new_lens: Optional[torch.Tensor] = None,
+             kept: Optional[torch.Tensor] = None, out_score: Optional[torch.Tensor] = None, stream=None):
+    """Trims every request to `budget` tokens: the first `sinks`, the last `recent` and the highest scores between, in
+    their order; rows of every tensor and plane are gathered to out_table's pages (None: in place).  Returns
+    (new_lens int32 [n_reqs], kept int32 [n_reqs, budget], out_score float32 [n_reqs, budget])."""
+    _table(block_table, "block_table"), _i32(kv_lens, "kv_lens")
+    if out_table is None:
+        out_table = block_table
+    _table(out_table, "out_table")
+    n = kv_lens.shape[0]
+    if block_table.shape[0] != n or out_table.shape[0] != n:
+        raise ValueError("block_table, out_table and kv_lens are of different numbers of requests")
+    if score.dtype != torch.float32 or score.dim() != 2 or score.shape[0] != n or score.stride(1) != 1:
+        raise ValueError("score must be a row-major float32 [n_reqs, width] CUDA tensor")
+    dev = kv_lens.device
+    if new_lens is None:
+        new_lens = torch.empty(n, dtype=torch.int32, device=dev)
+    if kept is None:
+        kept = torch.empty((n, max(0, budget)), dtype=torch.int32, device=dev)
+    if out_score is None:
+        out_score = torch.empty((n, max(0, budget)), dtype=torch.float32, device=dev)
+    _i32(new_lens, "new_lens")
+    if new_lens.shape[0] != n or kept.dtype != torch.int32 or kept.shape != (n, budget) or (budget > 1 and kept.stride(1) != 1):
+        raise ValueError("new_lens must be int32 [n_reqs] and kept a row-major int32 [n_reqs, budget]")
+    if out_score.dtype != torch.float32 or out_score.shape[0] != n or out_score.shape[1] < budget or (budget > 1 and out_score.stride(1) != 1):
+        raise ValueError("out_score must be a row-major float32 [n_reqs, budget] CUDA tensor")
+    _check("kv_evict", load().kv_evict(
+        ctypes.byref(cache.desc()), _ptr(block_table), n, block_table.shape[1], block_table.stride(0), _ptr(kv_lens), _ptr(score),
+        score.stride(0), score.shape[1], int(budget), int(sinks), int(recent), _ptr(out_table), out_table.shape[1],
+        out_table.stride(0), _ptr(new_lens), _ptr(kept), kept.stride(0), _ptr(out_score), out_score.stride(0), _stream(stream)))
+    return new_lens, kept, out_score
 
 
 def default_max_run_blocks(stage_block_bytes: int, target_bytes: int = 16 * 1024) -> int:
