@@ -6,9 +6,9 @@
 //
 // One persistent CTA per SM walks its piece of the batch's line of key tiles (kv_plan.cuh).  A unit
 // is up to 256 query rows (tokens x heads of one key head's group) and its key tiles of 128 keys:
-//   warp 0        loads: one tiled TMA per (64-element panel, run of slots inside a page) into rings of
-//                 K and V tiles, the page ids looked up one tile ahead
-//   warp 1        one thread issues every tcgen05.mma: S = Q K^T and O += P V, accumulators in TMEM
+//   warps 0, 2    load K and V: one tiled TMA per (64-element panel, run of slots inside a page) into a
+//                 ring of tiles each, the page ids looked up before the wait for a slot; warp 3 loads Q
+//   warp 1        issues every tcgen05.mma: S = Q K^T and O += P V, accumulators in TMEM
 //   warps 4-7, 8-11   two softmax groups, a thread per row: S from TMEM, maximum, exponentials, P back to
 //                 TMEM (over S) as the A operand of the second product, O rescaled only when the
 //                 maximum has grown by more than 2^8 (P stays below 2^8, far inside 16-bit range, so
@@ -26,7 +26,7 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kRows = 256;  // rows of a unit
+constexpr int kRows = 256;  // rows of a unit, at most: 2 * floor(128 / group) tokens of a group
 constexpr int kTile = 128;  // keys of a tile
 constexpr uint32_t kPanel = 128 * 128;  // bytes of a 64-element panel of 128 rows
 
@@ -46,10 +46,9 @@ struct Params {
     int32_t num_blocks;
     FastDiv block;       // slots of a page
     int32_t piece_rows;  // slots one TMA brings: gcd(block, 128), so it never leaves a page
-    int32_t dk, dv, heads;
+    int32_t q_box;       // tokens one TMA brings of q
+    int32_t dv, heads;
     float scale, c;  // c = scale * log2 e
-    const char *q;
-    int64_t q_token, q_head;
     char *out;
     int64_t out_token, out_head;
     float *lse;
@@ -60,7 +59,7 @@ struct Params {
 // Bookkeeping at the end of shared memory.
 struct Aux {
     uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
-    uint64_t s_full[2], p_ready[2], o_done[2], q_full[2], q_empty, merge_ready, merge_free;
+    uint64_t s_full[2], p_ready[2], o_done[2], q_full, q_empty, merge_ready, merge_free;
     long long scan[33];
     Place place;
     float m[128], l[128];  // the odd tiles' group, for the join
@@ -69,15 +68,47 @@ struct Aux {
 };
 static_assert(sizeof(Aux) <= 2048, "bookkeeping");
 
+// One tile of K or V rows into its slot: a TMA per (run of slots inside a page, panel), spread over the
+// lanes.  The first page a lane needs is looked up before `ready` waits for the slot.
+template <int Panels, typename Ready>
+__device__ __forceinline__ bool load_tile(const Params &p, const CUtensorMap *map, const int32_t *row, int kb, int lo, int hi, int head,
+                                          uint32_t to, uint32_t bar, const Ready &ready)
+{
+    const int lane = threadIdx.x & 31, pr = p.piece_rows;
+    const int p0 = max(0, lo - kb) / pr, p1 = (min(hi - kb, kTile) + pr - 1) / pr;
+    int page = 0, slot = 0;
+    const auto find = [&](int i) {
+        const uint32_t key = (uint32_t)(kb + i * pr), col = fdiv(key, p.block);
+        slot = (int)(key - col * p.block.d);
+        page = __ldg(row + col);
+        if (page < 0 || page >= p.num_blocks) {
+            set_error(p.b.err, KV_DERR_TABLE);
+            page = p.num_blocks;  // outside the map: reads zeros
+        }
+    };
+    if (p0 + lane < p1) find(p0 + lane);
+    if (!ready()) return false;
+    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)((p1 - p0) * pr) * Panels * 128);
+    __syncwarp();
+    for (int i = p0 + lane; i < p1; i += 32) {
+        if (i >= p0 + 32) find(i);
+#pragma unroll
+        for (int h = 0; h < Panels; h++) tma_load_4d(to + h * kPanel + i * pr * 128, map, bar, h * 64, head, slot, page);
+    }
+    __syncwarp();
+    return true;
+}
+
 template <int DK, int DV, bool Bf16>
 __global__ void __launch_bounds__(kThreads, 1)
-attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const Params p)
+attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                 const __grid_constant__ CUtensorMap v_map, const Params p)
 {
     using S = Shape<DK, DV>;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t base = smem_addr(smem);
     Aux &aux = *reinterpret_cast<Aux *>(smem + S::kOffAux);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const Batch &b = p.b;
     const Waiter wait{&aux.gave_up, b.err};
 
@@ -87,144 +118,153 @@ attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
         for (int i = 0; i < S::kNV; i++) mbar_init(smem_addr(&aux.v_full[i]), 1), mbar_init(smem_addr(&aux.v_empty[i]), 1);
         for (int i = 0; i < 2; i++) {
             mbar_init(smem_addr(&aux.s_full[i]), 1);
-            mbar_init(smem_addr(&aux.p_ready[i]), 128);
+            mbar_init(smem_addr(&aux.p_ready[i]), 4);
             mbar_init(smem_addr(&aux.o_done[i]), 1);
-            mbar_init(smem_addr(&aux.q_full[i]), 128);
         }
+        mbar_init(smem_addr(&aux.q_full), 1);
         mbar_init(smem_addr(&aux.q_empty), 1);
-        mbar_init(smem_addr(&aux.merge_ready), 128);
-        mbar_init(smem_addr(&aux.merge_free), 128);
+        mbar_init(smem_addr(&aux.merge_ready), 4);
+        mbar_init(smem_addr(&aux.merge_free), 4);
         mbar_init_fence();
+        tma_prefetch_map(&q_map);
         tma_prefetch_map(&k_map);
         tma_prefetch_map(&v_map);
     }
-    if (warp == 2) tmem_alloc(smem_addr(&aux.tmem), 512);
+    if (warp == 3) tmem_alloc(smem_addr(&aux.tmem), 512);
     grid_dep_entry();
     const int tiles = find_place<kThreads>(b, blockIdx.x, gridDim.x, aux.scan, &aux.place, blockIdx.x == 0);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = aux.tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, aux.tmem, 0);
     if (tid == 0) {
         Place pl = aux.place;
         if (tiles <= 0) pl.req = -1;
         p.places[blockIdx.x] = pl;
     }
 
+    const int half = b.unit_rows / 2;  // rows of a softmax group
     Walk w;
     const bool any = w.start(b, aux.place, tiles);
     if (!any) {
         // nothing to do: on to the common exit
     } else if (warp == 0) {
-        // ---- loads ----
-        const int pr = p.piece_rows, pieces = kTile / pr;
+        // ---- keys ----
         int it = 0;
+        bool ok = true;
         do {
             if (w.u.tiles == 0) continue;
             const int32_t *row = p.table + (int64_t)w.at.req * p.table_stride;
-            const int kt0 = w.u.tile0 + w.at.off;
-            bool ok = true;
-            for (int t = 0; t < w.n; t++, it++) {
-                const int kb = (kt0 + t) * kTile;
-                const int p0 = max(0, w.u.lo - kb) / pr, p1 = (min(w.u.hi - kb, kTile) + pr - 1) / pr;
-                const int sk = it % S::kNK, sv = it % S::kNV;
-                const uint32_t kbar = smem_addr(&aux.k_full[sk]), vbar = smem_addr(&aux.v_full[sv]);
-                // this lane's first page, looked up before the waits
-                int page = 0, slot = 0;
-                const auto find = [&](int i) {
-                    const uint32_t key = (uint32_t)(kb + i * pr), col = fdiv(key, p.block);
-                    slot = (int)(key - col * p.block.d);
-                    page = __ldg(row + col);
-                    if (page < 0 || page >= p.num_blocks) {
-                        set_error(b.err, KV_DERR_TABLE);
-                        page = p.num_blocks;  // outside the map: reads zeros
-                    }
-                };
-                if (p0 + lane < p1) find(p0 + lane);
-                const int page0 = page, slot0 = slot;
-                if (it >= S::kNK && !wait.warp(smem_addr(&aux.k_empty[sk]), ((it / S::kNK) - 1) & 1)) { ok = false; break; }
-                if (lane == 0) mbar_arrive_expect_tx(kbar, (uint32_t)((p1 - p0) * pr) * DK * 2);
-                __syncwarp();
-                for (int i = p0 + lane; i < p1; i += 32) {
-                    if (i >= p0 + 32) find(i);
-#pragma unroll
-                    for (int h = 0; h < DK / 64; h++)
-                        tma_load_4d(base + S::kOffK + sk * S::kK + h * kPanel + i * pr * 128, &k_map, kbar, h * 64, w.at.head, slot, page);
-                }
-                page = page0, slot = slot0;
-                if (it >= S::kNV && !wait.warp(smem_addr(&aux.v_empty[sv]), ((it / S::kNV) - 1) & 1)) { ok = false; break; }
-                if (lane == 0) mbar_arrive_expect_tx(vbar, (uint32_t)((p1 - p0) * pr) * DV * 2);
-                __syncwarp();
-                for (int i = p0 + lane; i < p1; i += 32) {
-                    if (i >= p0 + 32) find(i);
-#pragma unroll
-                    for (int h = 0; h < DV / 64; h++)
-                        tma_load_4d(base + S::kOffV + sv * S::kV + h * kPanel + i * pr * 128, &v_map, vbar, h * 64, w.at.head, slot, page);
-                }
-                (void)pieces;
+            for (int t = 0; ok && t < w.n; t++, it++) {
+                const int s = it % S::kNK;
+                ok = load_tile<DK / 64>(p, &k_map, row, (w.u.tile0 + w.at.off + t) * kTile, w.u.lo, w.u.hi, w.at.head, base + S::kOffK + s * S::kK,
+                                        smem_addr(&aux.k_full[s]), [&] { return it < S::kNK || wait.warp(smem_addr(&aux.k_empty[s]), ((it / S::kNK) - 1) & 1); });
             }
-            if (!ok) break;
-        } while (w.next(b));
+        } while (ok && w.next(b));
+    } else if (warp == 2) {
+        // ---- values ----
+        int it = 0;
+        bool ok = true;
+        do {
+            if (w.u.tiles == 0) continue;
+            const int32_t *row = p.table + (int64_t)w.at.req * p.table_stride;
+            for (int t = 0; ok && t < w.n; t++, it++) {
+                const int s = it % S::kNV;
+                ok = load_tile<DV / 64>(p, &v_map, row, (w.u.tile0 + w.at.off + t) * kTile, w.u.lo, w.u.hi, w.at.head, base + S::kOffV + s * S::kV,
+                                        smem_addr(&aux.v_full[s]), [&] { return it < S::kNV || wait.warp(smem_addr(&aux.v_empty[s]), ((it / S::kNV) - 1) & 1); });
+            }
+        } while (ok && w.next(b));
+    } else if (warp == 3) {
+        // ---- queries: as soon as the last scores of the unit before are out ----
+        int units = 0;
+        bool ok = true;
+        do {
+            if (w.u.tiles == 0) continue;
+            if (units && !wait.warp(smem_addr(&aux.q_empty), (units - 1) & 1)) break;
+            units++;
+            const int group = (int)b.group.d, tok0 = (int)fdiv((uint32_t)w.u.row0, b.group), toks = w.u.rows / group, per_half = half / group;
+            // boxes of q_box tokens; a box that begins in the first half ends there
+            const int n0 = (min(toks, per_half) + p.q_box - 1) / p.q_box, n1 = toks > per_half ? (toks - per_half + p.q_box - 1) / p.q_box : 0;
+            if (lane == 0) mbar_arrive_expect_tx(smem_addr(&aux.q_full), (uint32_t)((n0 + n1) * p.q_box * group) * DK * 2);
+            __syncwarp();
+            for (int i = lane; i < n0 + n1; i += 32) {
+                const int g = i >= n0, t = (i - (g ? n0 : 0)) * p.q_box;
+#pragma unroll
+                for (int h = 0; h < DK / 64; h++)
+                    tma_load_3d(base + g * S::kQ + h * kPanel + t * group * 128, &q_map, smem_addr(&aux.q_full), h * 64, w.at.head * group,
+                                w.q.q0 + tok0 + g * per_half + t);
+            }
+            __syncwarp();
+        } while (ok && w.next(b));
     } else if (warp == 1) {
-        // ---- matrix products: one thread ----
-        if (lane == 0) {
-            constexpr uint32_t qk_desc = mma_desc(Bf16, 128, 128, false), pv_desc = mma_desc(Bf16, 128, DV, true);
-            int it = 0, steps[2] = {0, 0}, qs[2] = {0, 0};
-            bool ok = true;
-            do {
-                if (w.u.tiles == 0) continue;
-                const bool both = w.u.rows > 128;
-                const int n = both ? 2 * w.n : w.n;
-                ok = wait.one(smem_addr(&aux.q_full[0]), qs[0]++ & 1) && (!both || wait.one(smem_addr(&aux.q_full[1]), qs[1]++ & 1));
-                if (!ok) break;
-                tc_fence_after();
-                const auto qk = [&](int i) {
-                    const int s = i & 1, kt = it + (both ? i >> 1 : i), slot = kt % S::kNK;
-                    if ((!both || s == 0) && !wait.one(smem_addr(&aux.k_full[slot]), (kt / S::kNK) & 1)) return false;
-                    const uint32_t qa = base + (both && s ? S::kQ : 0), ka = base + S::kOffK + slot * S::kK;
+        // ---- matrix products ----
+        constexpr uint32_t qk_desc = mma_desc(Bf16, 128, 128, false), pv_desc = mma_desc(Bf16, 128, DV, true);
+        const uint32_t elected = elect_one();
+        const uint64_t qd = smem_desc(base, 16, 1024), kd = smem_desc(base + S::kOffK, 16, 1024), vd = smem_desc(base + S::kOffV, kPanel, 1024);
+        int it = 0, steps[2] = {0, 0}, units = 0;
+        bool ok = true;
+        do {
+            if (w.u.tiles == 0) continue;
+            const bool both = w.u.rows > half;
+            const int n = both ? 2 * w.n : w.n;
+            ok = wait.warp(smem_addr(&aux.q_full), units++ & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const auto qk = [&](int i) {
+                const int s = i & 1, kt = it + (both ? i >> 1 : i), slot = kt % S::kNK;
+                if ((!both || s == 0) && !wait.warp(smem_addr(&aux.k_full[slot]), (kt / S::kNK) & 1)) return false;
+                const uint64_t qa = qd + (both && s ? S::kQ >> 4 : 0), ka = kd + slot * (S::kK >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < DK / 16; kk++) {
-                        const uint32_t o = (kk / 4) * kPanel + (kk % 4) * 32;
-                        mma_ss(tmem + s * 128, smem_desc(qa + o, 16, 1024), smem_desc(ka + o, 16, 1024), qk_desc, kk > 0);
-                    }
-                    tc_commit(smem_addr(&aux.s_full[s]));
-                    if (!both || s == 1) tc_commit(smem_addr(&aux.k_empty[slot]));
-                    if (i == n - 1) tc_commit(smem_addr(&aux.q_empty));
-                    return true;
-                };
-                ok = qk(0) && (n < 2 || qk(1));
-                for (int i = 0; ok && i < n; i++) {
-                    const int s = i & 1, vt = it + (both ? i >> 1 : i), slot = vt % S::kNV;
-                    ok = wait.one(smem_addr(&aux.p_ready[s]), steps[s]++ & 1) &&
-                         ((both && s) || wait.one(smem_addr(&aux.v_full[slot]), (vt / S::kNV) & 1));
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t va = base + S::kOffV + slot * S::kV;
-#pragma unroll
-                    for (int kk = 0; kk < 8; kk++)
-                        mma_ts(tmem + 256 + s * 128, tmem + s * 128 + kk * 8, smem_desc(va + kk * 2048, kPanel, 1024), pv_desc,
-                               i >= 2 || kk > 0);
-                    if (!both || s == 1) tc_commit(smem_addr(&aux.v_empty[slot]));
-                    tc_commit(smem_addr(&aux.o_done[s]));  // last: the groups wait for it before the CTA ends
-                    if (i + 2 < n) ok = qk(i + 2);
+                for (int kk = 0; kk < DK / 16; kk++) {
+                    const uint32_t o = ((kk / 4) * kPanel + (kk % 4) * 32) >> 4;
+                    mma_ss(tmem + s * 128, qa + o, ka + o, qk_desc, kk > 0, elected);
                 }
-                it += w.n;
-            } while (ok && w.next(b));
-        }
-        __syncwarp();
-    } else if (warp >= 4) {
+                if (!both || s == 1) tc_commit(smem_addr(&aux.k_empty[slot]), elected);
+                if (i == n - 1) tc_commit(smem_addr(&aux.q_empty), elected);
+                tc_commit(smem_addr(&aux.s_full[s]), elected);
+                return true;
+            };
+            ok = qk(0) && (n < 2 || qk(1));
+            for (int i = 0; ok && i < n; i++) {
+                const int s = i & 1, vt = it + (both ? i >> 1 : i), slot = vt % S::kNV;
+                ok = wait.warp(smem_addr(&aux.p_ready[s]), steps[s]++ & 1) &&
+                     ((both && s) || wait.warp(smem_addr(&aux.v_full[slot]), (vt / S::kNV) & 1));
+                if (!ok) break;
+                // rows of V that no query sees must not reach the product: they may hold anything
+                const int kb = (w.u.tile0 + w.at.off + vt - it) * kTile;
+                if (!(both && s) && (kb < w.u.lo || kb + kTile > w.u.hi)) {
+                    for (int r = lane >> 3; r < kTile; r += 4)
+                        if (kb + r < w.u.lo || kb + r >= w.u.hi)
+#pragma unroll
+                            for (int h = 0; h < DV / 64; h++)
+                                st_smem16(base + S::kOffV + slot * S::kV + h * kPanel + r * 128 + (lane & 7) * 16, make_uint4(0, 0, 0, 0));
+                    fence_async_smem();
+                    __syncwarp();
+                }
+                tc_fence_after();
+                const uint64_t va = vd + slot * (S::kV >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 8; kk++)
+                    mma_ts(tmem + 256 + s * 128, tmem + s * 128 + 64 + kk * 8, va + kk * (2048 >> 4), pv_desc, i >= 2 || kk > 0, elected);
+                if (!both || s == 1) tc_commit(smem_addr(&aux.v_empty[slot]), elected);
+                tc_commit(smem_addr(&aux.o_done[s]), elected);  // last: the groups wait for it before the CTA ends
+                if (i + 2 < n) ok = qk(i + 2);
+            }
+            it += w.n;
+        } while (ok && w.next(b));
+    } else {
         // ---- softmax: group g, a thread per row ----
         const int g = (warp - 4) >> 2, t = tid & 127;
         const uint32_t mine = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_at = tmem + g * 128 + mine, o_at = tmem + 256 + g * 128 + mine;
         const float slack = 8.0f / p.c;  // how far the maximum may grow before O is rescaled
-        int it = 0, steps = 0, loads = 0, joins = 0;
+        int steps = 0, joins = 0;
         bool owes_free = false;  // the even group may still be reading this (odd) group's O
         bool ok = true;
         do {
-            const bool both = w.u.rows > 128;
-            const int row = both ? g * 128 + t : t;            // row of the unit
-            const bool live = row < w.u.rows;
+            const bool both = w.u.rows > half;
+            const int row = (both ? g * half : 0) + t;         // row of the unit
+            const bool live = t < half && row < w.u.rows;
             const int r = w.u.row0 + min(row, w.u.rows - 1);   // row of the request; spare rows repeat the last
             const int tok = (int)fdiv((uint32_t)r, b.group), head = w.at.head * (int)b.group.d + r - tok * (int)b.group.d;
             const int64_t out_row = (int64_t)(w.q.q0 + tok);
@@ -236,26 +276,6 @@ attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                 }
                 continue;
             }
-            // Q
-            if (both || g == 0) {
-                if (loads && !wait.warp(smem_addr(&aux.q_empty), (loads - 1) & 1)) { ok = false; break; }
-                const uint32_t qa = base + g * S::kQ;
-                constexpr int kChunks = DK / 8;
-#pragma unroll 8
-                for (int i = t; i < 128 * kChunks; i += 128) {
-                    const int rr = i / kChunks, cc = i % kChunks, ur = w.u.row0 + (both ? g * 128 : 0) + rr;
-                    if (ur < w.u.row0 + w.u.rows) {
-                        const int tt = (int)fdiv((uint32_t)ur, b.group), hh = w.at.head * (int)b.group.d + ur - tt * (int)b.group.d;
-                        uint4 v = make_uint4(0, 0, 0, 0);
-                        if (cc * 8 < p.dk)
-                            v = *reinterpret_cast<const uint4 *>(p.q + (int64_t)(w.q.q0 + tt) * p.q_token + (int64_t)hh * p.q_head + cc * 16);
-                        st_smem16(qa + (cc / 8) * kPanel + panel_off(rr, cc & 7), v);
-                    }
-                }
-                fence_async_smem();
-                mbar_arrive(smem_addr(&aux.q_full[g]));
-            }
-            loads++;
             // key tiles
             int lo, hi;
             sees(b, w.q, tok, lo, hi);
@@ -263,30 +283,24 @@ attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
             float m = -INFINITY, l = 0.0f;
             const int first = both ? 0 : g, step = both ? 1 : 2, kt0 = w.u.tile0 + w.at.off;
             for (int k = first; k < w.n; k += step) {
-                const int kb = (kt0 + k) * kTile, vt = it + k;
+                const int kb = (kt0 + k) * kTile;
                 if (!wait.warp(smem_addr(&aux.s_full[g]), steps & 1)) { ok = false; break; }
                 tc_fence_after();
                 if (warp_live) {
-                    uint32_t x[4][32];
-#pragma unroll
-                    for (int q = 0; q < 4; q++) tmem_ld32(s_at + q * 32, x[q]);
+                    // the maximum over all 128 scores; the upper 64 stay in registers, the lower 64 are read again
+                    const int from = lo - kb, to_key = hi - kb;
+                    const bool hide = __any_sync(0xffffffffu, from > 0 || to_key < kTile);
+                    uint32_t x0[32], x1[32], x2[32], x3[32];
+                    tmem_ld32(s_at, x0);
+                    tmem_ld32(s_at + 32, x1);
                     tc_wait_ld();
-                    if (__any_sync(0xffffffffu, kb < lo || kb + kTile > hi)) {
-                        const int a = lo - kb, z = hi - kb;
-#pragma unroll
-                        for (int q = 0; q < 4; q++)
-#pragma unroll
-                            for (int i = 0; i < 32; i++)
-                                if (q * 32 + i < a || q * 32 + i >= z) x[q][i] = 0xff800000u;
-                    }
-                    float mx[4];
-#pragma unroll
-                    for (int q = 0; q < 4; q++) {
-                        mx[q] = __uint_as_float(x[q][0]);
-#pragma unroll
-                        for (int i = 1; i < 32; i++) mx[q] = fmaxf(mx[q], __uint_as_float(x[q][i]));
-                    }
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    tmem_ld32(s_at + 64, x2);
+                    tmem_ld32(s_at + 96, x3);
+                    if (hide) hide32(x0, 0, from, to_key), hide32(x1, 32, from, to_key);
+                    float top = max32(x1, max32(x0, -INFINITY));
+                    tc_wait_ld();
+                    if (hide) hide32(x2, 64, from, to_key), hide32(x3, 96, from, to_key);
+                    top = max32(x3, max32(x2, top));
                     const bool grow = top > m + slack;  // -inf + slack: the first finite score
                     if (__any_sync(0xffffffffu, grow)) {
                         const float to_m = grow ? top : m;
@@ -308,44 +322,35 @@ attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                         }
                     }
                     const float mc = m == -INFINITY ? 0.0f : m * p.c;
-                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int q = 0; q < 4; q += 2) {
-                        uint32_t pk[32];
-#pragma unroll
-                        for (int i = 0; i < 64; i += 2) {
-                            const float e0 = exp2_fast(fmaf(__uint_as_float(x[q + i / 32][i % 32]), p.c, -mc));
-                            const float e1 = exp2_fast(fmaf(__uint_as_float(x[q + i / 32][i % 32 + 1]), p.c, -mc));
-                            sum[i / 2 % 4] += e0 + e1;
-                            pk[i / 2] = pack2<Bf16>(e0, e1);
-                        }
-                        tmem_st32(s_at + q * 16, pk);
-                    }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                    uint32_t pk[16];
+                    // P takes the columns of the upper 64 scores, which are in registers
+                    weights32<Bf16>(x2, p.c, mc, sum, pk);
+                    tmem_ld32(s_at, x0);
+                    tmem_st16(s_at + 96, pk);
+                    weights32<Bf16>(x3, p.c, mc, sum, pk);
+                    tc_wait_ld();
+                    tmem_ld32(s_at + 32, x1);
+                    tmem_st16(s_at + 112, pk);
+                    if (hide) hide32(x0, 0, from, to_key);
+                    weights32<Bf16>(x0, p.c, mc, sum, pk);
+                    tc_wait_ld();
+                    tmem_st16(s_at + 64, pk);
+                    if (hide) hide32(x1, 32, from, to_key);
+                    weights32<Bf16>(x1, p.c, mc, sum, pk);
+                    tmem_st16(s_at + 80, pk);
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tc_wait_st();
-                }
-                // rows of V that no query sees must not reach the product: they may hold anything
-                if (kb < w.u.lo || kb + kTile > w.u.hi) {
-                    if (!wait.warp(smem_addr(&aux.v_full[vt % S::kNV]), (vt / S::kNV) & 1)) { ok = false; break; }
-                    if (kb + t < w.u.lo || kb + t >= w.u.hi) {
-                        const uint32_t va = base + S::kOffV + (vt % S::kNV) * S::kV + t * 128;
-#pragma unroll
-                        for (int h = 0; h < DV / 64; h++)
-#pragma unroll
-                            for (int c = 0; c < 8; c++) st_smem16(va + h * kPanel + c * 16, make_uint4(0, 0, 0, 0));
-                    }
-                    fence_async_smem();
                 }
                 if (owes_free) {  // this step's product overwrites O
                     if (!wait.warp(smem_addr(&aux.merge_free), (joins - 1) & 1)) { ok = false; break; }
                     owes_free = false;
                 }
                 tc_fence_before();
-                mbar_arrive(smem_addr(&aux.p_ready[g]));
+                warp_arrive(smem_addr(&aux.p_ready[g]));
                 steps++;
             }
             if (!ok) break;
-            it += w.n;
             const bool had = first < w.n;
             if (had && !wait.warp(smem_addr(&aux.o_done[g]), (steps - 1) & 1)) { ok = false; break; }
             tc_fence_after();
@@ -358,7 +363,7 @@ attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                 aux.m[t] = m;
                 aux.l[t] = l;
                 tc_fence_before();
-                mbar_arrive(smem_addr(&aux.merge_ready));
+                warp_arrive(smem_addr(&aux.merge_ready));
                 owes_free = true;
                 continue;
             }
@@ -421,7 +426,7 @@ attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
             }
             if (!both) {
                 tc_fence_before();
-                mbar_arrive(smem_addr(&aux.merge_free));
+                warp_arrive(smem_addr(&aux.merge_free));
             }
         } while (w.next(b));
         (void)ok;
@@ -434,26 +439,26 @@ attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
         const unsigned long long t0 = now_ns();
         while (now_ns() - t0 < 10000000ull) {}
     }
-    if (warp == 2) tmem_free(tmem, 512);
+    if (warp == 3) tmem_free(tmem, 512);
 }
 
 template <int DK, int DV, bool Bf16>
-int launch_attention(const CUtensorMap &km, const CUtensorMap &vm, const Params &p, int parts, cudaStream_t s, bool prepare)
+int launch_attention(const CUtensorMap &qm, const CUtensorMap &km, const CUtensorMap &vm, const Params &p, int parts, cudaStream_t s, bool prepare)
 {
     const auto kernel = attention_kernel<DK, DV, Bf16>;
     if (prepare)
         return cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<DK, DV>::kBytes));
-    int st = cuda_status(launch(kernel, dim3(parts), dim3(kThreads), Shape<DK, DV>::kBytes, s, km, vm, p));
+    int st = cuda_status(launch(kernel, dim3(parts), dim3(kThreads), Shape<DK, DV>::kBytes, s, qm, km, vm, p));
     if (st != KV_OK || parts < 2) return st;
     return join_fragments<DV, Bf16>(Join{p.b, p.places, p.ws, p.out, p.out_token, p.out_head, p.lse, p.heads, p.dv, kRows, 1, parts, p.scale, p.c}, s);
 }
 
 template <bool Bf16>
-int pick_attention(int dk, int dv, const CUtensorMap &km, const CUtensorMap &vm, const Params &p, int parts, cudaStream_t s, bool prepare)
+int pick_attention(int dk, int dv, const CUtensorMap &qm, const CUtensorMap &km, const CUtensorMap &vm, const Params &p, int parts, cudaStream_t s, bool prepare)
 {
-    if (dk <= 64 && dv <= 64) return launch_attention<64, 64, Bf16>(km, vm, p, parts, s, prepare);
-    if (dk <= 128) return launch_attention<128, 128, Bf16>(km, vm, p, parts, s, prepare);
-    return launch_attention<192, 128, Bf16>(km, vm, p, parts, s, prepare);
+    if (dk <= 64 && dv <= 64) return launch_attention<64, 64, Bf16>(qm, km, vm, p, parts, s, prepare);
+    if (dk <= 128) return launch_attention<128, 128, Bf16>(qm, km, vm, p, parts, s, prepare);
+    return launch_attention<192, 128, Bf16>(qm, km, vm, p, parts, s, prepare);
 }
 
 }  // namespace
@@ -499,6 +504,16 @@ int check_plane(const kv_cache_desc *c, int tensor, int plane, int heads, int di
     return KV_OK;
 }
 
+int make_q_map(CUtensorMap *map, const void *q, int64_t token_stride, int64_t head_stride, int head_dim, int heads, int64_t tokens, int group,
+               int box_tokens)
+{
+    if (token_stride >= (1ll << 40) || head_stride >= (1ll << 40)) return KV_ERR_UNSUPPORTED;
+    const uint64_t dims[3] = {(uint64_t)head_dim, (uint64_t)heads, (uint64_t)tokens};
+    const uint64_t strides[2] = {(uint64_t)head_stride, (uint64_t)token_stride};
+    const uint32_t box[3] = {64, (uint32_t)group, (uint32_t)box_tokens};
+    return make_map(map, (uint64_t)q, 3, dims, strides, box);
+}
+
 int piece_rows(int block_size, int tile)
 {
     int n = 1;
@@ -519,8 +534,8 @@ int preload_attention_kernels()
     CUtensorMap m;
     for (int dk : {64, 128, 192})
         for (bool bf : {false, true}) {
-            const int st = bf ? pick_attention<true>(dk, dk == 64 ? 64 : 128, m, m, p, 0, nullptr, true)
-                              : pick_attention<false>(dk, dk == 64 ? 64 : 128, m, m, p, 0, nullptr, true);
+            const int st = bf ? pick_attention<true>(dk, dk == 64 ? 64 : 128, m, m, m, p, 0, nullptr, true)
+                              : pick_attention<false>(dk, dk == 64 ? 64 : 128, m, m, m, p, 0, nullptr, true);
             if (st != KV_OK) return st;
         }
     return load_kernels(attention_kernel<64, 64, false>, attention_kernel<64, 64, true>, attention_kernel<128, 128, false>,
@@ -555,7 +570,8 @@ int kv_attention(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_cac
     int st = check_batch(batch);
     if (st != KV_OK) return st;
     if (d->head_dim % 8 || d->head_dim_v % 8) return KV_ERR_ALIGN;
-    if (d->head_dim > 192 || d->head_dim_v > 128 || (d->window && !d->causal)) return KV_ERR_UNSUPPORTED;
+    const int group = d->n_heads / d->n_kv_heads;
+    if (d->head_dim > 192 || d->head_dim_v > 128 || group > 128 || (d->window && !d->causal)) return KV_ERR_UNSUPPORTED;
     if ((st = check_plane(k, k_tensor, k_plane, d->n_kv_heads, d->head_dim)) != KV_OK) return st;
     if ((st = check_plane(v, v_tensor, v_plane, d->n_kv_heads, d->head_dim_v)) != KV_OK) return st;
     if (k->block_size != v->block_size) return KV_ERR_INVALID_ARG;
@@ -565,7 +581,7 @@ int kv_attention(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_cac
     if (workspace == nullptr) return KV_ERR_INVALID_ARG;
     if (!aligned16(workspace) || ((uintptr_t)lse & 3u)) return KV_ERR_ALIGN;
     Params p = {};
-    if ((st = fill_batch(&p.b, batch, d->n_heads, d->n_kv_heads, k->block_size, kRows, kTile, d->causal, d->window)) != KV_OK) return st;
+    if ((st = fill_batch(&p.b, batch, d->n_heads, d->n_kv_heads, k->block_size, 2 * (128 / group) * group, kTile, d->causal, d->window)) != KV_OK) return st;
     const DeviceInfo *dev = current_device();
     if (dev == nullptr) return KV_ERR_CUDA;
     if (workspace_bytes < attention_workspace(dev->num_sms)) return KV_ERR_RANGE;
@@ -576,26 +592,28 @@ int kv_attention(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_cac
     p.num_blocks = (int32_t)(k->num_blocks < v->num_blocks ? k->num_blocks : v->num_blocks);
     p.block = make_fastdiv((uint32_t)k->block_size);
     p.piece_rows = piece_rows(k->block_size, kTile);
-    p.dk = d->head_dim;
     p.dv = d->head_dim_v;
     p.heads = d->n_heads;
     p.scale = d->scale;
     p.c = d->scale * 1.44269504088896340736f;
-    p.q = (const char *)q;
-    p.q_token = q_token_stride;
-    p.q_head = q_head_stride;
     p.out = (char *)out;
     p.out_token = out_token_stride;
     p.out_head = out_head_stride;
     p.lse = lse;
     p.places = (Place *)workspace;
     p.ws = (float *)((char *)workspace + kPlaceBytes);
-    CUtensorMap km, vm;
+    // a box of q: the smallest divisor of a softmax group's tokens that holds a request's on average (a
+    // divisor, so that the last box of a half ends with it)
+    const int per_half = 128 / group;
+    for (p.q_box = 1; p.q_box < per_half; p.q_box++)
+        if (per_half % p.q_box == 0 && (int64_t)p.q_box * batch->n_reqs >= batch->n_tokens) break;
+    CUtensorMap qm, km, vm;
+    if ((st = make_q_map(&qm, q, q_token_stride, q_head_stride, d->head_dim, d->n_heads, batch->n_tokens, group, p.q_box)) != KV_OK) return st;
     if ((st = make_cache_map(&km, k, k_tensor, k_plane, d->n_kv_heads, d->head_dim, p.piece_rows)) != KV_OK) return st;
     if ((st = make_cache_map(&vm, v, v_tensor, v_plane, d->n_kv_heads, d->head_dim_v, p.piece_rows)) != KV_OK) return st;
     cudaStream_t s = (cudaStream_t)stream;
-    return d->dtype == KV_BF16 ? pick_attention<true>(p.dk, p.dv, km, vm, p, dev->num_sms, s, false)
-                               : pick_attention<false>(p.dk, p.dv, km, vm, p, dev->num_sms, s, false);
+    return d->dtype == KV_BF16 ? pick_attention<true>(d->head_dim, p.dv, qm, km, vm, p, dev->num_sms, s, false)
+                               : pick_attention<false>(d->head_dim, p.dv, qm, km, vm, p, dev->num_sms, s, false);
 }
 
 }  // extern "C"

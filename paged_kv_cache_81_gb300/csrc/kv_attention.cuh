@@ -18,6 +18,9 @@ int check_batch(const kv_attn_batch *t);
 int fill_batch(Batch *b, const kv_attn_batch *t, int heads, int kv_heads, int block_size, int unit_rows, int tile, int causal, int window);
 int check_plane(const kv_cache_desc *c, int tensor, int plane, int heads, int dim);
 int check_rows(const void *p, int64_t token_stride, int64_t head_stride);
+// A map of q [tokens, heads, head_dim]; a load brings 64 elements of `group` heads of box_tokens tokens.
+int make_q_map(CUtensorMap *map, const void *q, int64_t token_stride, int64_t head_stride, int head_dim, int heads, int64_t tokens, int group,
+               int box_tokens);
 // Slots that one TMA brings: the largest power of two that divides the block, at most a tile, so that a
 // piece never leaves its page.
 int piece_rows(int block_size, int tile);

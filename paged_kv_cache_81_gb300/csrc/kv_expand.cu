@@ -85,7 +85,7 @@ expand_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t base = smem_addr(smem);
     Aux &aux = *reinterpret_cast<Aux *>(smem + kOffAux);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const Waiter wait{&aux.gave_up, p.err};
 
     if (tid == 0) {
@@ -93,7 +93,7 @@ expand_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__
         mbar_init(smem_addr(&aux.a_full), 1);
         mbar_init(smem_addr(&aux.a_empty), 1);
         for (int i = 0; i < kStages; i++) mbar_init(smem_addr(&aux.b_full[i]), 1), mbar_init(smem_addr(&aux.b_empty[i]), 1);
-        for (int i = 0; i < 2; i++) mbar_init(smem_addr(&aux.d_full[i]), 1), mbar_init(smem_addr(&aux.d_empty[i]), 128);
+        for (int i = 0; i < 2; i++) mbar_init(smem_addr(&aux.d_full[i]), 1), mbar_init(smem_addr(&aux.d_empty[i]), 4);
         mbar_init_fence();
         tma_prefetch_map(&a_map);
         tma_prefetch_map(&w_map);
@@ -111,7 +111,7 @@ expand_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = aux.tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, aux.tmem, 0);
 
     Walk w;
     if (!w.start(p, aux, steps)) {
@@ -151,34 +151,31 @@ expand_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__
                 }
         } while (ok && w.next(p));
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t desc = mma_desc(Bf16, 128, kN, false);
-            int frag = 0, it = 0, heads = 0;
-            bool ok = true;
-            do {
-                ok = wait.one(smem_addr(&aux.a_full), frag++ & 1);
-                for (int h = 0; ok && h < w.n; h++, heads++) {
-                    const int d = heads & 1;
-                    ok = heads < 2 || wait.one(smem_addr(&aux.d_empty[d]), ((heads >> 1) - 1) & 1);
+        constexpr uint32_t desc = mma_desc(Bf16, 128, kN, false);
+        const uint32_t elected = elect_one();
+        const uint64_t ad = smem_desc(base, 16, 1024), bd = smem_desc(base + kOffB, 16, 1024);
+        int frag = 0, it = 0, heads = 0;
+        bool ok = true;
+        do {
+            ok = wait.warp(smem_addr(&aux.a_full), frag++ & 1);
+            for (int h = 0; ok && h < w.n; h++, heads++) {
+                const int d = heads & 1;
+                ok = heads < 2 || wait.warp(smem_addr(&aux.d_empty[d]), ((heads >> 1) - 1) & 1);
+                for (int kk = 0; ok && kk < 8; kk++, it++) {
+                    const int s = it % kStages;
+                    ok = wait.warp(smem_addr(&aux.b_full[s]), (it / kStages) & 1);
                     if (!ok) break;
                     tc_fence_after();
-                    for (int kk = 0; kk < 8; kk++, it++) {
-                        const int s = it % kStages;
-                        ok = wait.one(smem_addr(&aux.b_full[s]), (it / kStages) & 1);
-                        if (!ok) break;
-                        tc_fence_after();
+                    const uint64_t aa = ad + kk * (kAPanel >> 4), bb = bd + s * (kBPanel >> 4);
 #pragma unroll
-                        for (int j = 0; j < 4; j++)
-                            mma_ss(tmem + d * kN, smem_desc(base + kk * kAPanel + j * 32, 16, 1024), smem_desc(base + kOffB + s * kBPanel + j * 32, 16, 1024),
-                                   desc, kk > 0 || j > 0);
-                        tc_commit(smem_addr(&aux.b_empty[s]));
-                    }
-                    if (h + 1 == w.n) tc_commit(smem_addr(&aux.a_empty));
-                    tc_commit(smem_addr(&aux.d_full[d]));  // last: the writing warps wait for it before the CTA ends
+                    for (int j = 0; j < 4; j++) mma_ss(tmem + d * kN, aa + j * 2, bb + j * 2, desc, kk > 0 || j > 0, elected);
+                    tc_commit(smem_addr(&aux.b_empty[s]), elected);
                 }
-            } while (ok && w.next(p));
-        }
-        __syncwarp();
+                if (!ok) break;
+                if (h + 1 == w.n) tc_commit(smem_addr(&aux.a_empty), elected);
+                tc_commit(smem_addr(&aux.d_full[d]), elected);  // last: the writing warps wait for it before the CTA ends
+            }
+        } while (ok && w.next(p));
     } else if (warp >= 4) {
         const int t = tid & 127;
         const uint32_t mine = (uint32_t)((warp & 3) * 32) << 16;
@@ -227,7 +224,7 @@ expand_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__
                     }
                 }
                 tc_fence_before();
-                mbar_arrive(smem_addr(&aux.d_empty[d]));
+                warp_arrive(smem_addr(&aux.d_empty[d]));
                 if (live) {
 #pragma unroll
                     for (int i = 0; i < kRope / 8; i++) *reinterpret_cast<uint4 *>(k + (head * (kNope + kRope) + kNope + i * 8) * 2) = rope[i];

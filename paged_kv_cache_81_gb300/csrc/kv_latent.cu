@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t base = smem_addr(smem);
     Aux &aux = *reinterpret_cast<Aux *>(smem + kOffAux);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int part = blockIdx.x >> 1, half = blockIdx.x & 1;
     const Batch &b = p.b;
     const Waiter wait{&aux.gave_up, b.err};
@@ -72,12 +72,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
             mbar_init(smem_addr(&aux.x_full[i]), 1);
             mbar_init(smem_addr(&aux.x_empty[i]), 1);
             mbar_init(smem_addr(&aux.s_full[i]), 1);
-            mbar_init(smem_addr(&aux.p_ready[i]), 128);
+            mbar_init(smem_addr(&aux.p_ready[i]), 4);
             // by the tile's parity: the softmax warps look at it only now and then, and when they do the
             // product two tiles before has completed (its scores' successor is out) but the last may not have
             mbar_init(smem_addr(&aux.o_done[i]), 1);
         }
-        mbar_init(smem_addr(&aux.q_full), 128);
+        mbar_init(smem_addr(&aux.q_full), 4);
         mbar_init_fence();
         tma_prefetch_map(&map);
     }
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = aux.tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, aux.tmem, 0);
     if (tid == 0 && half == 0) {
         Place pl = aux.place;
         if (tiles <= 0) pl.req = -1;
@@ -147,54 +147,52 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
             }
         } while (ok && w.next(b));
     } else if (warp == 1) {
-        // ---- matrix products: one thread ----
-        if (lane == 0) {
-            constexpr uint32_t qk_desc = mma_desc(Bf16, 128, kKeys, false), pv_desc = mma_desc(Bf16, 128, kHalf, true);
-            int it = 0, units = 0;
-            bool ok = true;
-            do {
-                if (w.u.tiles == 0) continue;
-                ok = wait.one(smem_addr(&aux.q_full), units++ & 1);
+        // ---- matrix products ----
+        constexpr uint32_t qk_desc = mma_desc(Bf16, 128, kKeys, false), pv_desc = mma_desc(Bf16, 128, kHalf, true);
+        const uint32_t elected = elect_one();
+        const uint64_t qd = smem_desc(base, 16, 1024), xd = smem_desc(base + kOffX, 16, 1024), kd = smem_desc(base + kOffV, 16, 1024),
+                       vd = smem_desc(base + kOffV, kPanel, 1024);
+        int it = 0, units = 0;
+        bool ok = true;
+        do {
+            if (w.u.tiles == 0) continue;
+            ok = wait.warp(smem_addr(&aux.q_full), units++ & 1);
+            if (!ok) break;
+            tc_fence_after();
+            // Q's panels stand in the order of the key panels as this CTA holds them: the five others
+            // (shared memory), the four of its values (tensor memory)
+            const auto qk = [&](int i) {
+                const int n = it + i, s = n & 1;
+                const uint32_t d = tmem + kTmS + s * kKeys;
+                if (!wait.warp(smem_addr(&aux.x_full[s]), (n >> 1) & 1)) return false;
+                const uint64_t xs = xd + s * (5 * kPanel >> 4), ks = kd + s * (4 * kPanel >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 20; kk++)
+                    mma_ss(d, qd + (((kk / 4) * kQPanel + (kk % 4) * 32) >> 4), xs + (((kk / 4) * kPanel + (kk % 4) * 32) >> 4), qk_desc, kk > 0, elected);
+                tc_commit(smem_addr(&aux.x_empty[s]), elected);
+                if (!wait.warp(smem_addr(&aux.v_full[s]), (n >> 1) & 1)) return false;
+#pragma unroll
+                for (int kk = 0; kk < 16; kk++)
+                    mma_ts(d, tmem + kTmQ + kk * 8, ks + (((kk / 4) * kPanel + (kk % 4) * 32) >> 4), qk_desc, true, elected);
+                tc_commit(smem_addr(&aux.s_full[s]), elected);
+                return true;
+            };
+            ok = qk(0);
+            for (int i = 0; ok && i < w.n; i++) {
+                if (i + 1 < w.n && !(ok = qk(i + 1))) break;
+                const int n = it + i, s = n & 1;
+                ok = wait.warp(smem_addr(&aux.p_ready[s]), (n >> 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
-                // Q's panels stand in the order of the key panels as this CTA holds them: the five others
-                // (shared memory), the four of its values (tensor memory)
-                const auto qk = [&](int i) {
-                    const int n = it + i, s = n & 1;
-                    const uint32_t d = tmem + kTmS + s * kKeys;
-                    if (!wait.one(smem_addr(&aux.x_full[s]), (n >> 1) & 1)) return false;
+                const uint64_t vs = vd + s * (4 * kPanel >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < 20; kk++) {
-                        const uint32_t o = (kk % 4) * 32;
-                        mma_ss(d, smem_desc(base + (kk / 4) * kQPanel + o, 16, 1024), smem_desc(base + kOffX + (s * 5 + kk / 4) * kPanel + o, 16, 1024),
-                               qk_desc, kk > 0);
-                    }
-                    tc_commit(smem_addr(&aux.x_empty[s]));
-                    if (!wait.one(smem_addr(&aux.v_full[s]), (n >> 1) & 1)) return false;
-#pragma unroll
-                    for (int kk = 0; kk < 16; kk++)
-                        mma_ts(d, tmem + kTmQ + kk * 8, smem_desc(base + kOffV + (s * 4 + kk / 4) * kPanel + (kk % 4) * 32, 16, 1024), qk_desc, true);
-                    tc_commit(smem_addr(&aux.s_full[s]));
-                    return true;
-                };
-                ok = qk(0);
-                for (int i = 0; ok && i < w.n; i++) {
-                    if (i + 1 < w.n && !(ok = qk(i + 1))) break;
-                    const int n = it + i, s = n & 1;
-                    ok = wait.one(smem_addr(&aux.p_ready[s]), (n >> 1) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int kk = 0; kk < kKeys / 16; kk++)
-                        mma_ts(tmem + kTmO, tmem + kTmS + s * kKeys + kk * 8, smem_desc(base + kOffV + s * 4 * kPanel + kk * 2048, kPanel, 1024), pv_desc,
-                               i > 0 || kk > 0);
-                    tc_commit(smem_addr(&aux.v_empty[s]));
-                    tc_commit(smem_addr(&aux.o_done[s]));  // last: the softmax warps wait for it before the CTA ends
-                }
-                it += w.n;
-            } while (ok && w.next(b));
-        }
-        __syncwarp();
+                for (int kk = 0; kk < kKeys / 16; kk++)
+                    mma_ts(tmem + kTmO, tmem + kTmS + s * kKeys + kk * 8, vs + kk * (2048 >> 4), pv_desc, i > 0 || kk > 0, elected);
+                tc_commit(smem_addr(&aux.v_empty[s]), elected);
+                tc_commit(smem_addr(&aux.o_done[s]), elected);  // last: the softmax warps wait for it before the CTA ends
+            }
+            it += w.n;
+        } while (ok && w.next(b));
     } else if (warp >= 4) {
         // ---- softmax: a thread per row ----
         const int t = tid & 127;
@@ -246,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                 }
                 fence_async_smem();
                 tc_fence_before();
-                mbar_arrive(smem_addr(&aux.q_full));
+                warp_arrive(smem_addr(&aux.q_full));
             }
             int lo, hi;
             sees(b, w.q, tok, lo, hi);
@@ -319,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                     fence_async_smem();
                 }
                 tc_fence_before();
-                mbar_arrive(smem_addr(&aux.p_ready[s]));
+                warp_arrive(smem_addr(&aux.p_ready[s]));
             }
             if (!ok) break;
             it += w.n;

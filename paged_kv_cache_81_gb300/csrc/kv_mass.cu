@@ -138,7 +138,7 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t base = smem_addr(smem);
     Aux &aux = *reinterpret_cast<Aux *>(smem + S::kOffAux);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const Batch &b = p.b;
     const Waiter wait{&aux.gave_up, b.err};
     const int group = (int)b.group.d;
@@ -153,11 +153,11 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(smem_addr(&aux.s_full[i]), 1);
-            mbar_init(smem_addr(&aux.s_empty[i]), 128);
-            mbar_init(smem_addr(&aux.l_ready[i]), 128);
+            mbar_init(smem_addr(&aux.s_empty[i]), 4);
+            mbar_init(smem_addr(&aux.l_ready[i]), 4);
         }
-        mbar_init(smem_addr(&aux.sum_ready), 128);
-        mbar_init(smem_addr(&aux.sum_free), 128);
+        mbar_init(smem_addr(&aux.sum_ready), 4);
+        mbar_init(smem_addr(&aux.sum_free), 4);
         mbar_init_fence();
         tma_prefetch_map(&k_map);
         tma_prefetch_map(&q_map);
@@ -190,7 +190,7 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = aux.tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, aux.tmem, 0);
     if (tid == 0) {
         Place pl = aux.place;
         if (steps <= 0) pl.req = -1;
@@ -251,35 +251,36 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
             }
         } while (ok && w.next(p));
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t desc = mma_desc(Bf16, 128, (uint32_t)((p.step_tokens * group + 15) / 16 * 16), false);
-            int kt = -1, it = 0;
-            bool ok = true;
-            do {
-                if (w.k.per_head == 0) continue;
-                for (int i = 0; ok && i < w.n; i++, it++) {
-                    const int qi = (w.at.off + i) % w.k.per_head, g = it & 1, s = it % S::kNQ;
-                    if (i == 0 || qi == 0) {
-                        kt++;
-                        ok = wait.one(smem_addr(&aux.k_full[kt % S::kNK]), (kt / S::kNK) & 1);
-                    }
-                    ok = ok && wait.one(smem_addr(&aux.q_full[s]), (it / S::kNQ) & 1) &&
-                         (it < 2 || wait.one(smem_addr(&aux.s_empty[g]), ((it >> 1) - 1) & 1));
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t ka = base + (kt % S::kNK) * S::kOperand, qa = base + S::kOffQ + s * S::kOperand;
-#pragma unroll
-                    for (int kk = 0; kk < DK / 16; kk++) {
-                        const uint32_t o = (kk / 4) * kPanel + (kk % 4) * 32;
-                        mma_ss(tmem + g * 128, smem_desc(ka + o, 16, 1024), smem_desc(qa + o, 16, 1024), desc, kk > 0);
-                    }
-                    tc_commit(smem_addr(&aux.q_empty[s]));
-                    if (i + 1 == w.n || qi + 1 == w.k.per_head) tc_commit(smem_addr(&aux.k_empty[kt % S::kNK]));
-                    tc_commit(smem_addr(&aux.s_full[g]));  // last: the groups wait for it before the CTA ends
+        const uint32_t desc = mma_desc(Bf16, 128, (uint32_t)((p.step_tokens * group + 15) / 16 * 16), false);
+        const uint32_t elected = elect_one();
+        const uint64_t kd = smem_desc(base, 16, 1024), qd = smem_desc(base + S::kOffQ, 16, 1024);
+        int kt = -1, it = 0;
+        bool ok = true;
+        do {
+            if (w.k.per_head == 0) continue;
+            int qi = w.at.off % w.k.per_head;
+            for (int i = 0; ok && i < w.n; i++, it++) {
+                const int g = it & 1, s = it % S::kNQ;
+                if (i == 0 || qi == 0) {
+                    kt++;
+                    ok = wait.warp(smem_addr(&aux.k_full[kt % S::kNK]), (kt / S::kNK) & 1);
                 }
-            } while (ok && w.next(p));
-        }
-        __syncwarp();
+                ok = ok && wait.warp(smem_addr(&aux.q_full[s]), (it / S::kNQ) & 1) &&
+                     (it < 2 || wait.warp(smem_addr(&aux.s_empty[g]), ((it >> 1) - 1) & 1));
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t ka = kd + (kt % S::kNK) * (S::kOperand >> 4), qa = qd + s * (S::kOperand >> 4);
+#pragma unroll
+                for (int kk = 0; kk < DK / 16; kk++) {
+                    const uint32_t o = ((kk / 4) * kPanel + (kk % 4) * 32) >> 4;
+                    mma_ss(tmem + g * 128, ka + o, qa + o, desc, kk > 0, elected);
+                }
+                tc_commit(smem_addr(&aux.q_empty[s]), elected);
+                if (++qi == w.k.per_head) qi = 0;
+                if (i + 1 == w.n || qi == 0) tc_commit(smem_addr(&aux.k_empty[kt % S::kNK]), elected);
+                tc_commit(smem_addr(&aux.s_full[g]), elected);  // last: the groups wait for it before the CTA ends
+            }
+        } while (ok && w.next(p));
     } else if (warp >= 4) {
         const int g = (warp - 4) >> 2, t = tid & 127;
         const uint32_t s_at = tmem + g * 128 + ((uint32_t)((warp & 3) * 32) << 16);
@@ -305,7 +306,7 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
                     // these scores are out, so the whole group has done with the previous step's row of `neg`
                     if (!wait.warp(smem_addr(&aux.s_full[g]), mine & 1)) { ok = false; break; }
                     aux.neg[g][t] = v;
-                    mbar_arrive(smem_addr(&aux.l_ready[g]));
+                    warp_arrive(smem_addr(&aux.l_ready[g]));
                     if (!wait.warp(smem_addr(&aux.l_ready[g]), mine & 1)) { ok = false; break; }
                     tc_fence_after();
                     const int c0 = (va - tok0) * group, c1 = min(cols, (vb - tok0) * group);
@@ -331,7 +332,7 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
                     }
                     sum += (part[0] + part[1]) + (part[2] + part[3]);
                     tc_fence_before();
-                    mbar_arrive(smem_addr(&aux.s_empty[g]));
+                    warp_arrive(smem_addr(&aux.s_empty[g]));
                     mine++;
                 }
                 if (!ok) break;
@@ -340,11 +341,11 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
             if (g == 1) {
                 if (tiles && !wait.warp(smem_addr(&aux.sum_free), (tiles - 1) & 1)) { ok = false; break; }
                 aux.odd[t] = sum;
-                mbar_arrive(smem_addr(&aux.sum_ready));
+                warp_arrive(smem_addr(&aux.sum_ready));
             } else {
                 if (!wait.warp(smem_addr(&aux.sum_ready), tiles & 1)) { ok = false; break; }
                 sum += aux.odd[t];
-                mbar_arrive(smem_addr(&aux.sum_free));
+                warp_arrive(smem_addr(&aux.sum_free));
                 if (w.at.off == 0 && w.n == w.k.steps) {
                     if (key < w.q.len && key < p.width)
                         p.score[(int64_t)w.at.req * p.score_stride + key] = sum + (p.prev ? p.prev[(int64_t)w.at.req * p.prev_stride + key] : 0.0f);
@@ -454,7 +455,6 @@ int kv_attention_mass(const kv_attn_desc *d, const kv_attn_batch *batch, const k
     if (batch->n_tokens > 0) {
         if ((st = check_rows(q, q_token_stride, q_head_stride)) != KV_OK) return st;
         if (lse == nullptr) return KV_ERR_INVALID_ARG;
-        if (q_token_stride >= (1ll << 40) || q_head_stride >= (1ll << 40)) return KV_ERR_UNSUPPORTED;
     }
     if (score == nullptr || workspace == nullptr || score_stride < 0 || prev_stride < 0) return KV_ERR_INVALID_ARG;
     if (batch->n_reqs > 1 && (score_stride < width || (prev != nullptr && prev_stride < width))) return KV_ERR_INVALID_ARG;
@@ -488,10 +488,8 @@ int kv_attention_mass(const kv_attn_desc *d, const kv_attn_batch *batch, const k
     CUtensorMap km, qm;
     if ((st = make_cache_map(&km, k, k_tensor, k_plane, d->n_kv_heads, d->head_dim, p.piece_rows)) != KV_OK) return st;
     if (batch->n_tokens > 0) {
-        const uint64_t dims[3] = {(uint64_t)d->head_dim, (uint64_t)d->n_heads, (uint64_t)batch->n_tokens};
-        const uint64_t strides[2] = {(uint64_t)q_head_stride, (uint64_t)q_token_stride};
-        const uint32_t box[3] = {64, (uint32_t)group, (uint32_t)p.step_tokens};
-        if ((st = make_map(&qm, (uint64_t)q, 3, dims, strides, box)) != KV_OK) return st;
+        if ((st = make_q_map(&qm, q, q_token_stride, q_head_stride, d->head_dim, d->n_heads, batch->n_tokens, group, p.step_tokens)) != KV_OK)
+            return st;
     } else {
         qm = km;  // never used: no request has new tokens
     }

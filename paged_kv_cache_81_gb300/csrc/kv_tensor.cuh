@@ -6,6 +6,7 @@
 // tiled TMA load with a 64-element box writes.  Panels start on 1024-byte boundaries.
 #pragma once
 
+#include <cmath>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -55,6 +56,14 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar)
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// One arrival for a whole warp, after what all its lanes did before (32 arrivals on one barrier would be
+// taken one after another).
+__device__ __forceinline__ void warp_arrive(uint32_t bar)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 __device__ __forceinline__ void mbar_init_fence() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
 
 // Orders this thread's shared-memory writes before later reads by the tensor core and TMA.
@@ -102,10 +111,25 @@ __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence:
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// The barrier is arrived on once every tcgen05.mma that this thread issued so far has completed.
-__device__ __forceinline__ void tc_commit(uint32_t bar)
+// True in one lane of the warp, the same one every time.  A warp that issues products runs its loops as a
+// whole, with operands the same in all lanes, and predicates only the instructions: the descriptors then
+// stay in uniform registers (issued from inside a one-lane branch, each product cost about 95 cycles of
+// moving them there, one and a half times what the tensor core takes for it).
+__device__ __forceinline__ uint32_t elect_one()
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e;
+}
+
+// The barrier is arrived on once every tcgen05.mma that the elected thread issued so far has completed.
+__device__ __forceinline__ void tc_commit(uint32_t bar, uint32_t elected)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(elected)
+        : "memory");
 }
 
 // 32 columns of this warp's 32 lanes: register i of a thread is column i of its lane.
@@ -133,6 +157,15 @@ __device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t (&v)[32])
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(v[0]),
+        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]),
+        "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(t)
+        : "memory");
+}
+
 // Shared-memory operand descriptor: 128-byte swizzle, version 1; stride = bytes between groups of
 // eight rows, lead = bytes between 64-element panels of an operand whose rows are the K axis.
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride)
@@ -148,22 +181,22 @@ __host__ __device__ constexpr uint32_t mma_desc(bool bf16, uint32_t m, uint32_t 
            ((m >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate, uint32_t elected)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(elected)
         : "memory");
 }
 
 // A from tensor memory (16-bit pairs packed in 32-bit columns).
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate, uint32_t elected)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(elected)
         : "memory");
 }
 
@@ -177,6 +210,27 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
+// (a x + b) of two values at once.
+__device__ __forceinline__ float2 fma2(float2 x, float2 a, float2 b)
+{
+    float2 r;
+    asm("{\n\t.reg .b64 x, a, b, r;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 a, {%4, %5};\n\tmov.b64 b, {%6, %7};\n\t"
+        "fma.rn.f32x2 r, x, a, b;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 r, a, b;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
 template <bool Bf16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi)  // lo in the low half, round to nearest even
 {
@@ -186,6 +240,37 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)  // lo in the low 
     else
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// Scores of 32 keys, the first of them key `at` of its tile: those outside [a, z) become -inf.
+__device__ __forceinline__ void hide32(uint32_t (&x)[32], int at, int a, int z)
+{
+#pragma unroll
+    for (int i = 0; i < 32; i++)
+        if (at + i < a || at + i >= z) x[i] = 0xff800000u;
+}
+
+__device__ __forceinline__ float max32(const uint32_t (&x)[32], float top)
+{
+    float t[4] = {top, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < 32; i++) t[i & 3] = fmaxf(t[i & 3], __uint_as_float(x[i]));
+    return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+}
+
+// Weights 2^(c s - mc) of 32 scores, added to two partial sums and rounded to pairs of the element type.
+template <bool Bf16>
+__device__ __forceinline__ void weights32(const uint32_t (&x)[32], float c, float mc, float2 (&sum)[2], uint32_t (&pk)[16])
+{
+    const float2 cc = make_float2(c, c), nn = make_float2(-mc, -mc);
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+        float2 e = fma2(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), cc, nn);
+        e.x = exp2_fast(e.x);
+        e.y = exp2_fast(e.y);
+        sum[i & 1] = add2(sum[i & 1], e);
+        pk[i] = pack2<Bf16>(e.x, e.y);
+    }
 }
 
 // Byte offset of 16-byte chunk c (0 .. 7) of row r in a panel.
