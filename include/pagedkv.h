@@ -435,7 +435,8 @@ typedef struct {
 } kv_attn_desc;
 
 /* Device workspace bytes that one kv_attention or kv_latent_attention call needs on the current device,
- * whatever its sizes.  Calls sharing a workspace must be ordered. */
+ * whatever its sizes.  The caller zeroes the workspace once; every call leaves its counters zero again
+ * (after KV_DERR_TIMEOUT, zero it anew).  Calls sharing a workspace must be ordered. */
 KV_API int kv_attention_workspace_bytes(int64_t *bytes_out);
 
 /*
@@ -501,8 +502,8 @@ KV_API int kv_latent_expand(int32_t dtype, int32_t n_heads, const kv_cache_desc 
  * and score are float [n_reqs, width] with row strides in elements; they may be the same buffer.  Adding layer
  * by layer and step by step gives the accumulated weights that kv_evict ranks by.  d->head_dim_v is
  * ignored; at most 128 query heads a key head.  The sum of a token is formed in a fixed order, so the same call
- * gives the same bits.  workspace: kv_attention_mass_workspace_bytes(), 16-byte aligned; calls sharing it must
- * be ordered.  Lengths and tables as for kv_attention.
+ * gives the same bits.  workspace: kv_attention_mass_workspace_bytes(), 16-byte aligned, zeroed once
+ * by the caller as for kv_attention (whose workspace serves too); calls sharing it must be ordered.  Lengths and tables as for kv_attention.
  */
 KV_API int kv_attention_mass_workspace_bytes(int64_t *bytes_out);
 KV_API int kv_attention_mass(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_cache_desc *k, int32_t k_tensor,

@@ -25,6 +25,10 @@ namespace pkv {
 
 namespace {
 
+#ifndef KL
+#define KL 1
+#endif
+constexpr int kLeast = KL;  // steps of a piece, at least
 constexpr int kThreads = 384;
 constexpr int kRows = 256;  // rows of a unit, at most: 2 * floor(128 / group) tokens of a group
 constexpr int kTile = 128;  // keys of a tile
@@ -47,23 +51,20 @@ struct Params {
     FastDiv block;       // slots of a page
     int32_t piece_rows;  // slots one TMA brings: gcd(block, 128), so it never leaves a page
     int32_t q_box;       // tokens one TMA brings of q
-    int32_t dv, heads;
-    float scale, c;  // c = scale * log2 e
-    char *out;
-    int64_t out_token, out_head;
-    float *lse;
+    Output o;
     float *ws;
-    Place *places;
+    int *counters;
 };
 
 // Bookkeeping at the end of shared memory.
 struct Aux {
     uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
-    uint64_t s_full[2], p_ready[2], o_done[2], q_full, q_empty, merge_ready, merge_free;
+    uint64_t s_full[2], p_ready[2], o_done[2], q_full, q_empty, merge_ready, merge_free, join[2];
     long long scan[33];
     Place place;
     float m[128], l[128];  // the odd tiles' group, for the join
     uint32_t tmem;
+    int answer[2];
     int gave_up;
 };
 static_assert(sizeof(Aux) <= 2048, "bookkeeping");
@@ -120,6 +121,7 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
             mbar_init(smem_addr(&aux.s_full[i]), 1);
             mbar_init(smem_addr(&aux.p_ready[i]), 4);
             mbar_init(smem_addr(&aux.o_done[i]), 1);
+            mbar_init(smem_addr(&aux.join[i]), 4);
         }
         mbar_init(smem_addr(&aux.q_full), 1);
         mbar_init(smem_addr(&aux.q_empty), 1);
@@ -132,20 +134,14 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
     }
     if (warp == 3) tmem_alloc(smem_addr(&aux.tmem), 512);
     grid_dep_entry();
-    const int tiles = find_place<kThreads>(b, blockIdx.x, gridDim.x, aux.scan, &aux.place, blockIdx.x == 0);
+    const Line line = find_place<kThreads>(b, blockIdx.x, gridDim.x, kLeast, aux.scan, &aux.place, blockIdx.x == 0);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, aux.tmem, 0);
-    if (tid == 0) {
-        Place pl = aux.place;
-        if (tiles <= 0) pl.req = -1;
-        p.places[blockIdx.x] = pl;
-    }
-
     const int half = b.unit_rows / 2;  // rows of a softmax group
     Walk w;
-    const bool any = w.start(b, aux.place, tiles);
+    const bool any = w.start(b, aux.place, line);
     if (!any) {
         // nothing to do: on to the common exit
     } else if (warp == 0) {
@@ -257,8 +253,8 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         const int g = (warp - 4) >> 2, t = tid & 127;
         const uint32_t mine = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_at = tmem + g * 128 + mine, o_at = tmem + 256 + g * 128 + mine;
-        const float slack = 8.0f / p.c;  // how far the maximum may grow before O is rescaled
-        int steps = 0, joins = 0;
+        const float slack = 8.0f / p.o.c;  // how far the maximum may grow before O is rescaled
+        int steps = 0, joins = 0, cuts = 0;
         bool owes_free = false;  // the even group may still be reading this (odd) group's O
         bool ok = true;
         do {
@@ -268,11 +264,11 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
             const int r = w.u.row0 + min(row, w.u.rows - 1);   // row of the request; spare rows repeat the last
             const int tok = (int)fdiv((uint32_t)r, b.group), head = w.at.head * (int)b.group.d + r - tok * (int)b.group.d;
             const int64_t out_row = (int64_t)(w.q.q0 + tok);
-            char *to = p.out + out_row * p.out_token + (int64_t)head * p.out_head;
+            char *to = p.o.out + out_row * p.o.out_token + (int64_t)head * p.o.out_head;
             if (w.u.tiles == 0) {  // nothing is seen
                 if (live && (both || g == 0)) {
-                    for (int col = 0; col < p.dv; col += 8) *reinterpret_cast<uint4 *>(to + col * 2) = make_uint4(0, 0, 0, 0);
-                    if (p.lse) p.lse[out_row * p.heads + head] = -INFINITY;
+                    for (int col = 0; col < p.o.dv; col += 8) *reinterpret_cast<uint4 *>(to + col * 2) = make_uint4(0, 0, 0, 0);
+                    if (p.o.lse) p.o.lse[out_row * p.o.heads + head] = -INFINITY;
                 }
                 continue;
             }
@@ -304,7 +300,7 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                     const bool grow = top > m + slack;  // -inf + slack: the first finite score
                     if (__any_sync(0xffffffffu, grow)) {
                         const float to_m = grow ? top : m;
-                        const float alpha = grow ? exp2_fast((m - to_m) * p.c) : 1.0f;
+                        const float alpha = grow ? exp2_fast((m - to_m) * p.o.c) : 1.0f;
                         l *= alpha;
                         m = to_m;
                         if (k > first) {
@@ -321,23 +317,23 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                             }
                         }
                     }
-                    const float mc = m == -INFINITY ? 0.0f : m * p.c;
+                    const float mc = m == -INFINITY ? 0.0f : m * p.o.c;
                     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                     uint32_t pk[16];
                     // P takes the columns of the upper 64 scores, which are in registers
-                    weights32<Bf16>(x2, p.c, mc, sum, pk);
+                    weights32<Bf16>(x2, p.o.c, mc, sum, pk);
                     tmem_ld32(s_at, x0);
                     tmem_st16(s_at + 96, pk);
-                    weights32<Bf16>(x3, p.c, mc, sum, pk);
+                    weights32<Bf16>(x3, p.o.c, mc, sum, pk);
                     tc_wait_ld();
                     tmem_ld32(s_at + 32, x1);
                     tmem_st16(s_at + 112, pk);
                     if (hide) hide32(x0, 0, from, to_key);
-                    weights32<Bf16>(x0, p.c, mc, sum, pk);
+                    weights32<Bf16>(x0, p.o.c, mc, sum, pk);
                     tc_wait_ld();
                     tmem_st16(s_at + 64, pk);
                     if (hide) hide32(x1, 32, from, to_key);
-                    weights32<Bf16>(x1, p.c, mc, sum, pk);
+                    weights32<Bf16>(x1, p.o.c, mc, sum, pk);
                     tmem_st16(s_at + 80, pk);
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tc_wait_st();
@@ -374,8 +370,8 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                 tc_fence_after();
                 const float m1 = aux.m[t], l1 = aux.l[t], top = fmaxf(m, m1);
                 if (top > -INFINITY) {
-                    a0 = exp2_fast((m - top) * p.c);
-                    a1 = exp2_fast((m1 - top) * p.c);
+                    a0 = exp2_fast((m - top) * p.o.c);
+                    a1 = exp2_fast((m1 - top) * p.o.c);
                 }
                 l = l * a0 + l1 * a1;
                 m = top;
@@ -407,7 +403,7 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                     }
                     if (live) {
                         if (whole) {
-                            store_row32<Bf16>(to, f, inv, q * 32, p.dv);
+                            store_row32<Bf16>(to, f, inv, q * 32, p.o.dv);
                         } else {
                             float4 *d = reinterpret_cast<float4 *>(part + row * DV + q * 32);
 #pragma unroll
@@ -417,7 +413,7 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                 }
                 if (live) {
                     if (whole) {
-                        if (p.lse) p.lse[out_row * p.heads + head] = l > 0.0f ? fmaf(m, p.scale, logf(l)) : -INFINITY;
+                        if (p.o.lse) p.o.lse[out_row * p.o.heads + head] = l > 0.0f ? fmaf(m, p.o.scale, logf(l)) : -INFINITY;
                     } else {
                         part[kRows * DV + row] = m;
                         part[kRows * DV + kRows + row] = l;
@@ -427,6 +423,15 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
             if (!both) {
                 tc_fence_before();
                 warp_arrive(smem_addr(&aux.merge_free));
+            }
+            if (!whole) {
+                const Cut cut(line, w.pos - w.at.off, unit_cost(w.u));
+                if (last_of(p.counters + 2 * cut.c0 + g, cut.count, smem_addr(&aux.join[g]), cuts, &aux.answer[g], wait, ok)) {
+                    const int row0 = both ? g * half : 0;
+                    join_rows<DV, Bf16>(p.o, p.ws, cut.c0, cut.count, 1, 0, kRows * (DV + 2), row0, min(half, w.u.rows - row0), kRows, w.u.row0, w.q.q0,
+                                        w.at.head * (int)b.group.d, b.group);
+                }
+                if (!ok) break;
             }
         } while (w.next(b));
         (void)ok;
@@ -448,9 +453,7 @@ int launch_attention(const CUtensorMap &qm, const CUtensorMap &km, const CUtenso
     const auto kernel = attention_kernel<DK, DV, Bf16>;
     if (prepare)
         return cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<DK, DV>::kBytes));
-    int st = cuda_status(launch(kernel, dim3(parts), dim3(kThreads), Shape<DK, DV>::kBytes, s, qm, km, vm, p));
-    if (st != KV_OK || parts < 2) return st;
-    return join_fragments<DV, Bf16>(Join{p.b, p.places, p.ws, p.out, p.out_token, p.out_head, p.lse, p.heads, p.dv, kRows, 1, parts, p.scale, p.c}, s);
+    return cuda_status(launch(kernel, dim3(parts), dim3(kThreads), Shape<DK, DV>::kBytes, s, qm, km, vm, p));
 }
 
 template <bool Bf16>
@@ -539,8 +542,7 @@ int preload_attention_kernels()
             if (st != KV_OK) return st;
         }
     return load_kernels(attention_kernel<64, 64, false>, attention_kernel<64, 64, true>, attention_kernel<128, 128, false>,
-                        attention_kernel<128, 128, true>, attention_kernel<192, 128, false>, attention_kernel<192, 128, true>,
-                        join_kernel<64, false>, join_kernel<64, true>, join_kernel<128, false>, join_kernel<128, true>);
+                        attention_kernel<128, 128, true>, attention_kernel<192, 128, false>, attention_kernel<192, 128, true>);
 }
 
 }  // namespace pkv
@@ -592,16 +594,9 @@ int kv_attention(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_cac
     p.num_blocks = (int32_t)(k->num_blocks < v->num_blocks ? k->num_blocks : v->num_blocks);
     p.block = make_fastdiv((uint32_t)k->block_size);
     p.piece_rows = piece_rows(k->block_size, kTile);
-    p.dv = d->head_dim_v;
-    p.heads = d->n_heads;
-    p.scale = d->scale;
-    p.c = d->scale * 1.44269504088896340736f;
-    p.out = (char *)out;
-    p.out_token = out_token_stride;
-    p.out_head = out_head_stride;
-    p.lse = lse;
-    p.places = (Place *)workspace;
-    p.ws = (float *)((char *)workspace + kPlaceBytes);
+    p.o = Output{(char *)out, out_token_stride, out_head_stride, lse, d->n_heads, d->head_dim_v, d->scale, d->scale * kLog2e};
+    p.counters = (int *)workspace;
+    p.ws = (float *)((char *)workspace + kCounterBytes);
     // a box of q: the smallest divisor of a softmax group's tokens that holds a request's on average (a
     // divisor, so that the last box of a half ends with it)
     const int per_half = 128 / group;
@@ -612,8 +607,8 @@ int kv_attention(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_cac
     if ((st = make_cache_map(&km, k, k_tensor, k_plane, d->n_kv_heads, d->head_dim, p.piece_rows)) != KV_OK) return st;
     if ((st = make_cache_map(&vm, v, v_tensor, v_plane, d->n_kv_heads, d->head_dim_v, p.piece_rows)) != KV_OK) return st;
     cudaStream_t s = (cudaStream_t)stream;
-    return d->dtype == KV_BF16 ? pick_attention<true>(d->head_dim, p.dv, qm, km, vm, p, dev->num_sms, s, false)
-                               : pick_attention<false>(d->head_dim, p.dv, qm, km, vm, p, dev->num_sms, s, false);
+    return d->dtype == KV_BF16 ? pick_attention<true>(d->head_dim, p.o.dv, qm, km, vm, p, dev->num_sms, s, false)
+                               : pick_attention<false>(d->head_dim, p.o.dv, qm, km, vm, p, dev->num_sms, s, false);
 }
 
 }  // extern "C"

@@ -100,8 +100,8 @@ expand_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__
     }
     if (warp == 2) tmem_alloc(smem_addr(&aux.tmem), 512);
     grid_dep_entry();
-    const int steps = find_piece<kThreads>(
-        p.n_reqs, blockIdx.x, gridDim.x, aux.scan,
+    const Line line = find_piece<kThreads>(
+        p.n_reqs, blockIdx.x, gridDim.x, 1, aux.scan,
         [&](int r) { return (long long)((request_len(p, r, blockIdx.x == 0) + kTile - 1) / kTile) * p.heads; },
         [&](int r, long long rest) {
             aux.req = r;
@@ -114,7 +114,7 @@ expand_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__
     const uint32_t tmem = __shfl_sync(0xffffffffu, aux.tmem, 0);
 
     Walk w;
-    if (!w.start(p, aux, steps)) {
+    if (!w.start(p, aux, line.steps)) {
         // nothing to do: on to the common exit
     } else if (warp == 0) {
         const int pr = p.piece_rows;

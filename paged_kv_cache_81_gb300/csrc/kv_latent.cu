@@ -17,6 +17,10 @@ namespace pkv {
 
 namespace {
 
+#ifndef KL
+#define KL 2
+#endif
+constexpr int kLeast = KL;  // steps of a piece, at least
 constexpr int kThreads = 256;
 constexpr int kRows = 128;
 constexpr int kKeys = 64;      // keys of a tile
@@ -33,22 +37,20 @@ struct Params {
     int64_t table_stride;
     int32_t num_blocks;
     FastDiv block;
-    int32_t piece_rows, heads;
-    float scale, c;
+    int32_t piece_rows;
     const char *q;
     int64_t q_token, q_head;
-    char *out;
-    int64_t out_token, out_head;
-    float *lse;
+    Output o;
     float *ws;
-    Place *places;
+    int *counters;
 };
 
 struct Aux {
-    uint64_t v_full[2], v_empty[2], x_full[2], x_empty[2], s_full[2], p_ready[2], o_done[2], q_full;
+    uint64_t v_full[2], v_empty[2], x_full[2], x_empty[2], s_full[2], p_ready[2], o_done[2], q_full, join;
     long long scan[8];
     Place place;
     uint32_t tmem;
+    int answer;
     int gave_up;
 };
 static_assert(sizeof(Aux) <= 1024, "bookkeeping");
@@ -78,24 +80,19 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
             mbar_init(smem_addr(&aux.o_done[i]), 1);
         }
         mbar_init(smem_addr(&aux.q_full), 4);
+        mbar_init(smem_addr(&aux.join), 4);
         mbar_init_fence();
         tma_prefetch_map(&map);
     }
     if (warp == 2) tmem_alloc(smem_addr(&aux.tmem), 512);
     grid_dep_entry();
-    const int tiles = find_place<kThreads>(b, part, gridDim.x >> 1, aux.scan, &aux.place, blockIdx.x == 0);
+    const Line line = find_place<kThreads>(b, part, gridDim.x >> 1, kLeast, aux.scan, &aux.place, blockIdx.x == 0);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, aux.tmem, 0);
-    if (tid == 0 && half == 0) {
-        Place pl = aux.place;
-        if (tiles <= 0) pl.req = -1;
-        p.places[part] = pl;
-    }
-
     Walk w;
-    if (!w.start(b, aux.place, tiles)) {
+    if (!w.start(b, aux.place, line)) {
         // nothing to do: on to the common exit
     } else if (warp == 0) {
         // ---- loads: the five other panels, then the four of this CTA's values ----
@@ -198,19 +195,19 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
         const int t = tid & 127;
         const uint32_t mine = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t o_at = tmem + kTmO + mine;
-        const float slack = 8.0f / p.c;
-        int it = 0;
+        const float slack = 8.0f / p.o.c;
+        int it = 0, cuts = 0;
         bool ok = true;
         do {
             const bool live = t < w.u.rows;
             const int r = w.u.row0 + min(t, w.u.rows - 1);
             const int tok = (int)fdiv((uint32_t)r, b.group), head = r - tok * (int)b.group.d;
             const int64_t out_row = (int64_t)(w.q.q0 + tok);
-            char *to = p.out + out_row * p.out_token + (int64_t)head * p.out_head + half * kHalf * 2;
+            char *to = p.o.out + out_row * p.o.out_token + (int64_t)head * p.o.out_head + half * kHalf * 2;
             if (w.u.tiles == 0) {
                 if (live) {
                     for (int col = 0; col < kHalf; col += 8) *reinterpret_cast<uint4 *>(to + col * 2) = make_uint4(0, 0, 0, 0);
-                    if (p.lse && half == 0) p.lse[out_row * p.heads + head] = -INFINITY;
+                    if (p.o.lse && half == 0) p.o.lse[out_row * p.o.heads + head] = -INFINITY;
                 }
                 continue;
             }
@@ -275,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                     const bool grow = top > m + slack;
                     if (__any_sync(0xffffffffu, grow)) {
                         const float to_m = grow ? top : m;
-                        const float alpha = grow ? exp2_fast((m - to_m) * p.c) : 1.0f;
+                        const float alpha = grow ? exp2_fast((m - to_m) * p.o.c) : 1.0f;
                         l *= alpha;
                         m = to_m;
                         if (k > 0) {
@@ -292,13 +289,13 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                             }
                         }
                     }
-                    const float mc = m == -INFINITY ? 0.0f : m * p.c;
+                    const float mc = m == -INFINITY ? 0.0f : m * p.o.c;
                     float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                     uint32_t pk[32];
 #pragma unroll
                     for (int i = 0; i < 64; i += 2) {
-                        const float e0 = exp2_fast(fmaf(__uint_as_float(x[i / 32][i % 32]), p.c, -mc));
-                        const float e1 = exp2_fast(fmaf(__uint_as_float(x[i / 32][i % 32 + 1]), p.c, -mc));
+                        const float e0 = exp2_fast(fmaf(__uint_as_float(x[i / 32][i % 32]), p.o.c, -mc));
+                        const float e1 = exp2_fast(fmaf(__uint_as_float(x[i / 32][i % 32 + 1]), p.o.c, -mc));
                         sum[i / 2 % 4] += e0 + e1;
                         pk[i / 2] = pack2<Bf16>(e0, e1);
                     }
@@ -347,12 +344,18 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                 }
                 if (live) {
                     if (whole) {
-                        if (p.lse && half == 0) p.lse[out_row * p.heads + head] = l > 0.0f ? fmaf(m, p.scale, logf(l)) : -INFINITY;
+                        if (p.o.lse && half == 0) p.o.lse[out_row * p.o.heads + head] = l > 0.0f ? fmaf(m, p.o.scale, logf(l)) : -INFINITY;
                     } else {
                         frag[kRows * kHalf + t] = m;
                         frag[kRows * (kHalf + 1) + t] = l;
                     }
                 }
+            }
+            if (!whole) {
+                const Cut cut(line, w.pos - w.at.off, unit_cost(w.u));
+                if (last_of(p.counters + 2 * cut.c0 + half, cut.count, smem_addr(&aux.join), cuts, &aux.answer, wait, ok))
+                    join_rows<kHalf, Bf16>(p.o, p.ws, cut.c0, cut.count, 2, half, kRows * (kHalf + 2), 0, w.u.rows, kRows, w.u.row0, w.q.q0, 0, b.group);
+                if (!ok) break;
             }
         } while (w.next(b));
         (void)ok;
@@ -368,22 +371,13 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
     if (warp == 2) tmem_free(tmem, 512);
 }
 
-template <bool Bf16>
-int run_latent(const CUtensorMap &map, const Params &p, int parts, cudaStream_t s)
-{
-    const int st = cuda_status(launch(latent_kernel<Bf16>, dim3(2 * parts), dim3(kThreads), kBytes, s, map, p));
-    if (st != KV_OK || parts < 2) return st;
-    return join_fragments<kHalf, Bf16>(
-        Join{p.b, p.places, p.ws, p.out, p.out_token, p.out_head, p.lse, p.heads, kDV, kRows, 2, parts, p.scale, p.c}, s);
-}
-
 }  // namespace
 
 int preload_latent_kernels()
 {
     int st = cuda_status(cudaFuncSetAttribute(latent_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes));
     if (st == KV_OK) st = cuda_status(cudaFuncSetAttribute(latent_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes));
-    return st != KV_OK ? st : load_kernels(latent_kernel<false>, latent_kernel<true>, join_kernel<kHalf, false>, join_kernel<kHalf, true>);
+    return st != KV_OK ? st : load_kernels(latent_kernel<false>, latent_kernel<true>);
 }
 
 }  // namespace pkv
@@ -418,20 +412,14 @@ extern "C" int kv_latent_attention(const kv_attn_desc *d, const kv_attn_batch *b
     p.num_blocks = (int32_t)cache->num_blocks;
     p.block = make_fastdiv((uint32_t)cache->block_size);
     p.piece_rows = piece_rows(cache->block_size, kKeys);
-    p.heads = d->n_heads;
-    p.scale = d->scale;
-    p.c = d->scale * 1.44269504088896340736f;
     p.q = (const char *)q;
     p.q_token = q_token_stride;
     p.q_head = q_head_stride;
-    p.out = (char *)out;
-    p.out_token = out_token_stride;
-    p.out_head = out_head_stride;
-    p.lse = lse;
-    p.places = (Place *)workspace;
-    p.ws = (float *)((char *)workspace + kPlaceBytes);
+    p.o = Output{(char *)out, out_token_stride, out_head_stride, lse, d->n_heads, kDV, d->scale, d->scale * kLog2e};
+    p.counters = (int *)workspace;
+    p.ws = (float *)((char *)workspace + kCounterBytes);
     CUtensorMap map;
     if ((st = make_cache_map(&map, cache, tensor, 0, 1, kD, p.piece_rows)) != KV_OK) return st;
-    const int parts = dev->num_sms / 2;
-    return d->dtype == KV_BF16 ? run_latent<true>(map, p, parts, (cudaStream_t)stream) : run_latent<false>(map, p, parts, (cudaStream_t)stream);
+    return cuda_status(launch(d->dtype == KV_BF16 ? latent_kernel<true> : latent_kernel<false>, dim3(dev->num_sms / 2 * 2), dim3(kThreads), kBytes,
+                              (cudaStream_t)stream, map, p));
 }

@@ -7,7 +7,7 @@
 // the exponentials of its row, column by column in a fixed order, so nothing is shared and nothing atomic.
 // The line (as in kv_plan.cuh) runs over requests, tiles of 128 keys, key heads and tiles of up to 128
 // (token, head of the group) rows; a CTA takes an equal piece of it, and a key tile that was cut is summed
-// from its pieces' partial sums by a second kernel, in their order.
+// from its pieces' partial sums, in their order, by whichever CTA finishes the last of them.
 //   warp 0 loads (K once a head, Q a step), warp 1 issues the products, warps 4-7 and 8-11 take the even
 //   and the odd steps; warps 2 and 3 carry over what lies past the requests' lengths.
 #include "kv_attention.cuh"
@@ -16,6 +16,10 @@ namespace pkv {
 
 namespace {
 
+#ifndef KL
+#define KL 2
+#endif
+constexpr int kLeast = KL;  // steps of a piece, at least
 constexpr int kThreads = 384;
 constexpr int kTile = 128;
 constexpr uint32_t kPanel = 128 * 128;
@@ -43,16 +47,17 @@ struct Params {
     int64_t score_stride;
     int32_t width;
     float *ws;
-    Place *places;
+    int *counters;
 };
 
 struct Aux {
-    uint64_t k_full[3], k_empty[3], q_full[3], q_empty[3], s_full[2], s_empty[2], l_ready[2], sum_ready, sum_free;
+    uint64_t k_full[3], k_empty[3], q_full[3], q_empty[3], s_full[2], s_empty[2], l_ready[2], sum_ready, sum_free, join;
     long long scan[12];
     Place place;
-    float neg[2][128];  // -lse log2 e of a step's rows
+    alignas(16) float neg[2][128];  // read four at a time: -lse log2 e of a step's rows
     float odd[128];     // the odd steps' sums
     uint32_t tmem;
+    int answer;
     int gave_up;
 };
 static_assert(sizeof(Aux) <= 3072, "bookkeeping");
@@ -102,12 +107,14 @@ __device__ __forceinline__ long long request_cost(const Params &p, int r)
 struct Walk2 {
     Place at;
     int left, n;
+    long long pos;  // the fragment's first step on the line
     Request q;
     KeyTile k;
-    __device__ __forceinline__ bool start(const Params &p, const Place &pl, int steps)
+    __device__ __forceinline__ bool start(const Params &p, const Place &pl, const Line &line)
     {
         at = pl;
-        left = steps;
+        left = line.steps;
+        pos = line.begin;
         if (left <= 0) return false;
         q = load_request(p.b, at.req);
         k = key_tile(p, q, at.unit);
@@ -117,6 +124,7 @@ struct Walk2 {
     __device__ __forceinline__ bool next(const Params &p)
     {
         left -= n;
+        pos += n;
         if (left <= 0) return false;
         at.off = 0;
         at.unit++;
@@ -158,14 +166,15 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
         }
         mbar_init(smem_addr(&aux.sum_ready), 4);
         mbar_init(smem_addr(&aux.sum_free), 4);
+        mbar_init(smem_addr(&aux.join), 4);
         mbar_init_fence();
         tma_prefetch_map(&k_map);
         tma_prefetch_map(&q_map);
     }
     if (warp == 2) tmem_alloc(smem_addr(&aux.tmem), 256);
     grid_dep_entry();
-    const int steps = find_piece<kThreads>(
-        b.n_reqs, blockIdx.x, gridDim.x, aux.scan,
+    const Line line = find_piece<kThreads>(
+        b.n_reqs, blockIdx.x, gridDim.x, kLeast, aux.scan,
         [&](int r) {
             if (blockIdx.x == 0) load_request(b, r, true);
             return request_cost(p, r);
@@ -191,12 +200,6 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, aux.tmem, 0);
-    if (tid == 0) {
-        Place pl = aux.place;
-        if (steps <= 0) pl.req = -1;
-        p.places[blockIdx.x] = pl;
-    }
-
     Walk2 w;
     if (warp == 2 || warp == 3) {
         // what lies past every request's length is carried over
@@ -206,7 +209,7 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
             for (int j = len + me; j < p.width; j += all)
                 p.score[(int64_t)r * p.score_stride + j] = p.prev ? p.prev[(int64_t)r * p.prev_stride + j] : 0.0f;
         }
-    } else if (!w.start(p, aux.place, steps)) {
+    } else if (!w.start(p, aux.place, line)) {
         // nothing to do: on to the common exit
     } else if (warp == 0) {
         const int pr = p.piece_rows;
@@ -284,7 +287,7 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
     } else if (warp >= 4) {
         const int g = (warp - 4) >> 2, t = tid & 127;
         const uint32_t s_at = tmem + g * 128 + ((uint32_t)((warp & 3) * 32) << 16);
-        int it = 0, mine = 0, tiles = 0;
+        int it = 0, mine = 0, tiles = 0, cuts = 0;
         bool ok = true;
         do {
             const int key = w.at.unit * kTile + t;
@@ -300,7 +303,7 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
                     float v = -INFINITY;
                     if (t < cols) {
                         const int tt = (int)fdiv((uint32_t)t, b.group);
-                        v = -p.lse[(int64_t)(kt0 + tok0 + tt) * p.heads + head * group + t - tt * group] * 1.44269504088896340736f;
+                        v = -p.lse[(int64_t)(kt0 + tok0 + tt) * p.heads + head * group + t - tt * group] * kLog2e;
                         if (v == INFINITY) v = -INFINITY;  // a row that saw nothing weighs nothing
                     }
                     // these scores are out, so the whole group has done with the previous step's row of `neg`
@@ -346,12 +349,20 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
                 if (!wait.warp(smem_addr(&aux.sum_ready), tiles & 1)) { ok = false; break; }
                 sum += aux.odd[t];
                 warp_arrive(smem_addr(&aux.sum_free));
-                if (w.at.off == 0 && w.n == w.k.steps) {
-                    if (key < w.q.len && key < p.width)
-                        p.score[(int64_t)w.at.req * p.score_stride + key] = sum + (p.prev ? p.prev[(int64_t)w.at.req * p.prev_stride + key] : 0.0f);
-                } else {
+                bool mine_to_write = true;
+                if (w.n < w.k.steps) {  // cut: the group that comes last adds the fragments in their order
+                    const Cut cut(line, w.pos - w.at.off, w.k.steps);
                     p.ws[(2 * blockIdx.x + (w.at.off == 0 ? 1 : 0)) * kTile + t] = sum;
+                    mine_to_write = last_of(p.counters + cut.c0, cut.count, smem_addr(&aux.join), cuts, &aux.answer, wait, ok);
+                    if (!ok) break;
+                    if (mine_to_write) {
+                        sum = 0.0f;
+#pragma unroll 4
+                        for (int i = 0; i < cut.count; i++) sum += __ldcg(p.ws + cut.slot(i) * kTile + t);
+                    }
                 }
+                if (mine_to_write && key < w.q.len && key < p.width)
+                    p.score[(int64_t)w.at.req * p.score_stride + key] = sum + (p.prev ? p.prev[(int64_t)w.at.req * p.prev_stride + key] : 0.0f);
             }
             tiles++;
         } while (w.next(p));
@@ -368,34 +379,12 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
     if (warp == 2) tmem_free(tmem, 256);
 }
 
-// Sums the pieces of the key tiles that were cut, in their order.
-__global__ void __launch_bounds__(kTile) mass_join_kernel(const Params p, int parts)
-{
-    grid_dep_entry();
-    const int c = blockIdx.x + 1, t = threadIdx.x;
-    const Place pl = p.places[c];
-    if (pl.req < 0 || pl.off == 0) return;
-    const Place before = p.places[c - 1];
-    if (before.req == pl.req && before.unit == pl.unit && before.off != 0) return;  // an earlier cut of the tile joins it
-    float sum = p.ws[(2 * (c - 1) + 1) * kTile + t];
-    for (int x = c; x < parts; x++) {
-        const Place at = p.places[x];
-        if (at.req != pl.req || at.unit != pl.unit || at.off == 0) break;
-        sum += p.ws[2 * x * kTile + t];
-    }
-    const int key = pl.unit * kTile + t;
-    if (key < load_request(p.b, pl.req).len && key < p.width)
-        p.score[(int64_t)pl.req * p.score_stride + key] = sum + (p.prev ? p.prev[(int64_t)pl.req * p.prev_stride + key] : 0.0f);
-}
-
 template <int DK, bool Bf16>
 int run_mass(const CUtensorMap &km, const CUtensorMap &qm, const Params &p, int parts, cudaStream_t s, bool prepare)
 {
     if (prepare)
         return cuda_status(cudaFuncSetAttribute(mass_kernel<DK, Bf16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<DK>::kBytes));
-    const int st = cuda_status(launch(mass_kernel<DK, Bf16>, dim3(parts), dim3(kThreads), Shape<DK>::kBytes, s, km, qm, p));
-    if (st != KV_OK || parts < 2) return st;
-    return cuda_status(launch(mass_join_kernel, dim3(parts - 1), dim3(kTile), 0, s, p, parts));
+    return cuda_status(launch(mass_kernel<DK, Bf16>, dim3(parts), dim3(kThreads), Shape<DK>::kBytes, s, km, qm, p));
 }
 
 template <bool Bf16>
@@ -406,7 +395,7 @@ int pick_mass(int dk, const CUtensorMap &km, const CUtensorMap &qm, const Params
     return run_mass<192, Bf16>(km, qm, p, parts, s, prepare);
 }
 
-int64_t mass_workspace(int num_sms) { return kPlaceBytes + (int64_t)num_sms * 2 * kTile * 4; }
+int64_t mass_workspace(int num_sms) { return kCounterBytes + (int64_t)num_sms * 2 * kTile * 4; }
 
 }  // namespace
 
@@ -420,7 +409,7 @@ int preload_mass_kernels()
             if (st != KV_OK) return st;
         }
     return load_kernels(mass_kernel<64, false>, mass_kernel<64, true>, mass_kernel<128, false>, mass_kernel<128, true>,
-                        mass_kernel<192, false>, mass_kernel<192, true>, mass_join_kernel);
+                        mass_kernel<192, false>, mass_kernel<192, true>);
 }
 
 }  // namespace pkv
@@ -476,15 +465,15 @@ int kv_attention_mass(const kv_attn_desc *d, const kv_attn_batch *batch, const k
     const int group = d->n_heads / d->n_kv_heads;
     p.step_tokens = 128 / group;
     if (batch->n_tokens > 0 && p.step_tokens > batch->n_tokens) p.step_tokens = (int32_t)batch->n_tokens;
-    p.c = d->scale * 1.44269504088896340736f;
+    p.c = d->scale * kLog2e;
     p.lse = lse;
     p.prev = prev;
     p.prev_stride = prev_stride;
     p.score = score;
     p.score_stride = score_stride;
     p.width = width;
-    p.places = (Place *)workspace;
-    p.ws = (float *)((char *)workspace + kPlaceBytes);
+    p.counters = (int *)workspace;
+    p.ws = (float *)((char *)workspace + kCounterBytes);
     CUtensorMap km, qm;
     if ((st = make_cache_map(&km, k, k_tensor, k_plane, d->n_kv_heads, d->head_dim, p.piece_rows)) != KV_OK) return st;
     if (batch->n_tokens > 0) {

@@ -5,7 +5,7 @@
 // `tile` keys between the first key that its first token sees and the last that its last token sees.
 // Laid end to end (request, key head, unit), all units' tiles form one line; CTA c of `parts` takes
 // the c-th equal piece of it.  A piece may begin and end inside a unit: those two fragments go to the
-// workspace and are joined by a second kernel.  So the split follows the lengths, not the launch: one
+// workspace, and whichever CTA finishes the unit's last one joins them.  So the split follows the lengths, not the launch: one
 // grid serves a captured graph whatever the lengths become, and long contexts and few rows fill the
 // GPU as well as many short requests do.
 #pragma once
@@ -94,11 +94,22 @@ struct Place {
     int32_t req, head, unit, off;
 };
 
+// How the line is cut: part p of `used` takes the steps [total p / used, total (p + 1) / used).
+struct Line {
+    long long begin;  // this CTA's first step
+    long long total;
+    long long used;
+    int steps;  // this CTA's; 0: none
+
+    // The part that takes step x.
+    __device__ __forceinline__ int part_of(long long x) const { return (int)(((x + 1) * used - 1) / total); }
+};
+
 // Finds a CTA's piece of a line made of n_reqs stretches, the r-th cost(r) steps long; every thread of
-// the block calls it.  scratch: one 8-byte word a warp.  Returns the steps of piece `part` of `parts` (0:
-// none) and calls found(request, step inside its stretch) in the one thread that holds its beginning.
+// the block calls it.  scratch: one 8-byte word a warp.  Calls found(request, step inside its stretch) in
+// the one thread that holds the piece's beginning.
 template <int Threads, typename Cost, typename Found>
-__device__ __forceinline__ int find_piece(int n_reqs, int part, int parts, long long *scratch, const Cost &cost, const Found &found)
+__device__ __forceinline__ Line find_piece(int n_reqs, int part, int parts, int least, long long *scratch, const Cost &cost, const Found &found)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kWarps = Threads / 32;
@@ -120,13 +131,13 @@ __device__ __forceinline__ int find_piece(int n_reqs, int part, int parts, long 
         total += scratch[w];
     }
     upto += before;
-    const long long used = min((long long)parts, total);  // no piece is empty but the last ones
-    long long w0 = 0, w1 = 0;
-    if (part < used) {
-        w0 = total * part / used;
-        w1 = total * (part + 1) / used;
-        if (w0 >= upto - mine && w0 < upto) {
-            long long rest = w0 - (upto - mine);
+    // pieces of at least `least` steps; none is empty but the last ones
+    Line line{0, total, min((long long)parts, (total + least - 1) / least), 0};
+    if (part < line.used) {
+        line.begin = total * part / line.used;
+        line.steps = (int)(total * (part + 1) / line.used - line.begin);
+        if (line.begin >= upto - mine && line.begin < upto) {
+            long long rest = line.begin - (upto - mine);
             for (int r = r0; r < r1; r++) {
                 const long long all = cost(r);
                 if (rest < all) {
@@ -138,15 +149,15 @@ __device__ __forceinline__ int find_piece(int n_reqs, int part, int parts, long 
         }
     }
     __syncthreads();
-    return (int)(w1 - w0);
+    return line;
 }
 
 // This CTA's piece of an attention batch's line.
 template <int Threads>
-__device__ __forceinline__ int find_place(const Batch &b, int part, int parts, long long *scratch, Place *place, bool report)
+__device__ __forceinline__ Line find_place(const Batch &b, int part, int parts, int least, long long *scratch, Place *place, bool report)
 {
     return find_piece<Threads>(
-        b.n_reqs, part, parts, scratch, [&](int r) { return head_cost(b, load_request(b, r, report)) * b.kv_heads; },
+        b.n_reqs, part, parts, least, scratch, [&](int r) { return head_cost(b, load_request(b, r, report)) * b.kv_heads; },
         [&](int r, long long rest) {
             const Request q = load_request(b, r);
             const long long h = head_cost(b, q);
@@ -171,11 +182,13 @@ struct Walk {
     Request q;
     Unit u;
     int n;  // tiles of the current fragment
+    long long pos;  // its first step on the line
 
-    __device__ __forceinline__ bool start(const Batch &b, const Place &p, int tiles)
+    __device__ __forceinline__ bool start(const Batch &b, const Place &p, const Line &line)
     {
         at = p;
-        left = tiles;
+        left = line.steps;
+        pos = line.begin;
         if (left <= 0) return false;
         q = load_request(b, at.req);
         u = make_unit(b, q, at.unit);
@@ -187,6 +200,7 @@ struct Walk {
     __device__ __forceinline__ bool next(const Batch &b)
     {
         left -= n;
+        pos += n;
         if (left <= 0) return false;
         at.off = 0;
         if (++at.unit == q.units) {

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from contextlib import nullcontext as _no_context
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -481,55 +482,112 @@ def kv_get_last_error(clear: bool = True, stream=None) -> int:
 # ---------------------------------------------------------------------------
 # attention over the paged cache
 # ---------------------------------------------------------------------------
+# These calls run once a layer and step, so the marshalling is kept short: plain integers for pointers, the
+# raw stream handle, one device check a tensor.
+LATENT_DIM, LATENT_RANK = 576, 512  # elements of a latent row, and of its latent part
+
+
 def kv_attention_workspace_bytes() -> int:
     out = ctypes.c_int64(0)
     _check("kv_attention_workspace_bytes", load().kv_attention_workspace_bytes(ctypes.byref(out)))
     return out.value
 
 
+def kv_attention_mass_workspace_bytes() -> int:
+    out = ctypes.c_int64(0)
+    _check("kv_attention_mass_workspace_bytes", load().kv_attention_mass_workspace_bytes(ctypes.byref(out)))
+    return out.value
+
+
 def kv_attention_workspace(device="cuda") -> torch.Tensor:
-    """A workspace for kv_attention and kv_latent_attention calls of any size on `device`; calls that
-    share one must be ordered."""
+    """A workspace for kv_attention, kv_latent_attention and kv_attention_mass calls of any size on `device`,
+    zeroed on the current stream; calls that share one must be ordered."""
     with torch.cuda.device(device):
-        return torch.empty(kv_attention_workspace_bytes(), dtype=torch.uint8, device=device)
+        return torch.zeros(kv_attention_workspace_bytes(), dtype=torch.uint8, device=device)
 
 
-def _attn_batch(block_table: torch.Tensor, q_offsets: torch.Tensor, kv_lens: torch.Tensor, n_tokens: int) -> KvAttnBatch:
-    _i32(q_offsets, "q_offsets"), _i32(kv_lens, "kv_lens")
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.stride(1) != 1:
-        raise ValueError("block_table must be a row-major int32 [n_reqs, max_blocks] CUDA tensor")
+_workspaces = {}  # (bytes function, device, stream handle) -> the workspace of calls without one on that stream
+
+
+def _own_workspace(nbytes, dev: int, handle: int) -> torch.Tensor:
+    """The workspace of calls that bring none: one a stream, whose calls are in order.  A call that is being captured
+    gets one of its own, in the graph's memory and zeroed by the graph, as replays are not in that order."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(nbytes(), dtype=torch.uint8, device=f"cuda:{dev}")
+    key = (nbytes, dev, handle)
+    ws = _workspaces.get(key)
+    if ws is None:
+        with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev)) if handle else _no_context():
+            ws = _workspaces[key] = torch.zeros(nbytes(), dtype=torch.uint8, device=f"cuda:{dev}")
+    return ws
+
+
+def _begin(t: torch.Tensor, stream):
+    """(device index, raw stream handle) of a call whose first tensor is `t`."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("libpagedkv takes CUDA tensors")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{dev}, which is not the current device")
+    return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _on(dev: int, *tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"every tensor must be on cuda:{dev}")
+
+
+def _outputs_on(stream):
+    """Outputs made here belong to the stream that writes them."""
+    return _no_context() if stream is None else torch.cuda.stream(stream)
+
+
+def _attn_batch(dev: int, block_table: torch.Tensor, q_offsets: torch.Tensor, kv_lens: torch.Tensor, n_tokens: int) -> KvAttnBatch:
+    _i32(q_offsets, "q_offsets"), _i32(kv_lens, "kv_lens"), _table(block_table, "block_table")
+    _on(dev, block_table, q_offsets, kv_lens)
     n = kv_lens.shape[0]
-    if block_table.shape[0] != n or q_offsets.shape[0] != n + 1:
+    rows, cols = block_table.shape
+    if rows != n or q_offsets.shape[0] != n + 1:
         raise ValueError("block_table, q_offsets and kv_lens are of different numbers of requests")
-    return KvAttnBatch(_ptr(block_table), n, block_table.shape[1], block_table.stride(0), _ptr(q_offsets), _ptr(kv_lens), n_tokens)
+    return KvAttnBatch(block_table.data_ptr(), n, cols, block_table.stride(0), q_offsets.data_ptr(), kv_lens.data_ptr(), n_tokens)
 
 
-def _rows3(t: torch.Tensor, name: str) -> torch.Tensor:
-    if t.dim() != 3 or t.dtype not in _DTYPES or (t.shape[2] > 1 and t.stride(2) != 1):
-        raise ValueError(f"{name} must be a bf16 or fp16 CUDA tensor [tokens, heads, dim] with contiguous rows")
+def _table(t: torch.Tensor, name: str) -> torch.Tensor:
+    if t.dtype != torch.int32 or t.dim() != 2 or t.stride(1) != 1:
+        raise ValueError(f"{name} must be a row-major int32 [n_reqs, max_blocks] CUDA tensor")
     return t
 
 
-def _like_cache(cache: PagedCache, dtype: torch.dtype, name: str):
+def _rows3(t: torch.Tensor, name: str) -> int:
+    """The KV_BF16 / KV_F16 code of [tokens, heads, dim] rows."""
+    code = _DTYPES.get(t.dtype)
+    if code is None or t.dim() != 3 or t.stride(2) != 1:
+        raise ValueError(f"{name} must be a bf16 or fp16 CUDA tensor [tokens, heads, dim] with contiguous rows")
+    return code
+
+
+def _like_cache(dev: int, cache: PagedCache, dtype: torch.dtype, name: str) -> KvCacheDesc:
     t = cache.tensors[0]
     if t.dtype != dtype:
-        raise ValueError(f"{name} holds {t.dtype}, the queries are {dtype}")
+        raise ValueError(f"{name} holds {t.dtype}, not {dtype}")
+    _on(dev, t)
+    return cache.desc()
 
 
-def _strides(t: torch.Tensor):
-    return t.stride(0) * t.element_size(), t.stride(1) * t.element_size()
-
-
-def _attn_outputs(q: torch.Tensor, dv: int, out: Optional[torch.Tensor], lse: Optional[torch.Tensor]):
+def _attn_outputs(dev: int, q: torch.Tensor, dv: int, out: Optional[torch.Tensor], lse: Optional[torch.Tensor], stream):
     T, H, _ = q.shape
     if out is None:
-        out = torch.empty((T, H, dv), dtype=q.dtype, device=q.device)
-    elif _rows3(out, "out").shape != (T, H, dv) or out.dtype != q.dtype:
+        with _outputs_on(stream):
+            out = q.new_empty((T, H, dv))
+    elif _rows3(out, "out") < 0 or out.shape != (T, H, dv) or out.dtype != q.dtype:
         raise ValueError("out must be [tokens, heads, value dim] of q's type")
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        with _outputs_on(stream):
+            lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
     elif lse.shape != (T, H) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 [tokens, heads] tensor")
+    _on(dev, out, lse)
     return out, lse
 
 
@@ -541,33 +599,30 @@ def kv_attention(q: torch.Tensor, cache: PagedCache, block_table: torch.Tensor, 
 
     Keys are tensor `k_tensor` of `cache` (plane 0).  Values are tensor `v_tensor` of `v_cache`, or, without a
     `v_cache`, plane 1 of the same tensor (two-plane caches) or tensor `v_tensor` of `cache`."""
-    _rows3(q, "q")
-    _like_cache(cache, q.dtype, "cache")
+    code = _rows3(q, "q")
+    dev, handle = _begin(q, stream)
+    k_desc = _like_cache(dev, cache, q.dtype, "cache")
     values = cache if v_cache is None else v_cache
-    _like_cache(values, q.dtype, "v_cache")
-    v_plane = 1 if values.n_planes == 2 else 0
+    v_desc = k_desc if v_cache is None else _like_cache(dev, v_cache, q.dtype, "v_cache")
     if v_tensor is None:
-        v_tensor = k_tensor if v_cache is None else 0
         if v_cache is None and cache.n_planes == 1:
             raise ValueError("a one-plane cache holds the values in another tensor: give v_tensor or v_cache")
+        v_tensor = k_tensor if v_cache is None else 0
     T, H, dk = q.shape
-    kv_heads, left = divmod(cache.row_bytes, dk * q.element_size())
-    if left or not kv_heads or values.row_bytes % (kv_heads * q.element_size()):
+    kv_heads, left = divmod(cache.row_bytes, dk * 2) if dk else (0, 0)
+    if left or not kv_heads or values.row_bytes % (kv_heads * 2):
         raise ValueError("the cache's rows are not whole heads of q's width")
-    dv = values.row_bytes // (kv_heads * q.element_size())
-    batch = _attn_batch(block_table, q_offsets, kv_lens, T)
-    out, lse = _attn_outputs(q, dv, out, lse)
+    dv = values.row_bytes // (kv_heads * 2)
+    batch = _attn_batch(dev, block_table, q_offsets, kv_lens, T)
+    out, lse = _attn_outputs(dev, q, dv, out, lse, stream)
     if workspace is None:
-        workspace = kv_attention_workspace(q.device)
-    desc = KvAttnDesc(_DTYPES[q.dtype], H, kv_heads, dk, dv, int(causal), int(window), float(scale))
+        workspace = _own_workspace(kv_attention_workspace_bytes, dev, handle)
+    _on(dev, workspace)
+    desc = KvAttnDesc(code, H, kv_heads, dk, dv, causal, window, scale)
     _check("kv_attention", load().kv_attention(
-        ctypes.byref(desc), ctypes.byref(batch), ctypes.byref(cache.desc()), int(k_tensor), 0, ctypes.byref(values.desc()),
-        int(v_tensor), v_plane, _ptr(q), *_strides(q), _ptr(out), *_strides(out), _ptr(lse), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+        desc, batch, k_desc, k_tensor, 0, v_desc, v_tensor, values.n_planes - 1, q.data_ptr(), q.stride(0) * 2, q.stride(1) * 2,
+        out.data_ptr(), out.stride(0) * 2, out.stride(1) * 2, lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, handle))
     return out, lse
-
-
-LATENT_DIM, LATENT_RANK = 576, 512  # elements of a latent row, and of its latent part
 
 
 def kv_latent_attention(q: torch.Tensor, cache: PagedCache, block_table: torch.Tensor, q_offsets: torch.Tensor,
@@ -576,24 +631,20 @@ def kv_latent_attention(q: torch.Tensor, cache: PagedCache, block_table: torch.T
                         workspace: Optional[torch.Tensor] = None, stream=None):
     """Attention of new tokens q [tokens, heads, 576] over a latent cache (the absorbed form); returns
     (out [tokens, heads, 512], lse float32 [tokens, heads])."""
-    _rows3(q, "q")
-    _like_cache(cache, q.dtype, "cache")
+    code = _rows3(q, "q")
+    dev, handle = _begin(q, stream)
+    c_desc = _like_cache(dev, cache, q.dtype, "cache")
     T, H, dk = q.shape
-    batch = _attn_batch(block_table, q_offsets, kv_lens, T)
-    out, lse = _attn_outputs(q, LATENT_RANK, out, lse)
+    batch = _attn_batch(dev, block_table, q_offsets, kv_lens, T)
+    out, lse = _attn_outputs(dev, q, LATENT_RANK, out, lse, stream)
     if workspace is None:
-        workspace = kv_attention_workspace(q.device)
-    desc = KvAttnDesc(_DTYPES[q.dtype], H, 1, dk, LATENT_RANK, int(causal), int(window), float(scale))
+        workspace = _own_workspace(kv_attention_workspace_bytes, dev, handle)
+    _on(dev, workspace)
+    desc = KvAttnDesc(code, H, 1, dk, LATENT_RANK, causal, window, scale)
     _check("kv_latent_attention", load().kv_latent_attention(
-        ctypes.byref(desc), ctypes.byref(batch), ctypes.byref(cache.desc()), int(tensor), _ptr(q), *_strides(q), _ptr(out),
-        *_strides(out), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+        desc, batch, c_desc, tensor, q.data_ptr(), q.stride(0) * 2, q.stride(1) * 2, out.data_ptr(), out.stride(0) * 2,
+        out.stride(1) * 2, lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, handle))
     return out, lse
-
-
-def _table(t: torch.Tensor, name: str) -> torch.Tensor:
-    if t.dtype != torch.int32 or t.dim() != 2 or t.stride(1) != 1:
-        raise ValueError(f"{name} must be a row-major int32 [n_reqs, max_blocks] CUDA tensor")
-    return t
 
 
 def kv_latent_expand(cache: PagedCache, block_table: torch.Tensor, kv_lens: torch.Tensor, weight: torch.Tensor,
@@ -601,24 +652,25 @@ def kv_latent_expand(cache: PagedCache, block_table: torch.Tensor, kv_lens: torc
                      v_tensor: int = 0, stream=None):
     """The latent rows of every request multiplied out by weight [heads, 256, 512] into per-head keys (192) and
     values (128) of the caches k_out and v_out, at the same tokens of out_table."""
-    _table(block_table, "block_table"), _table(out_table, "out_table"), _i32(kv_lens, "kv_lens")
-    if weight.dim() != 3 or tuple(weight.shape[1:]) != (256, LATENT_RANK) or not weight.is_contiguous() or weight.dtype not in _DTYPES:
+    code = _DTYPES.get(weight.dtype)
+    if code is None or weight.dim() != 3 or tuple(weight.shape[1:]) != (256, LATENT_RANK) or not weight.is_contiguous():
         raise ValueError("weight must be a contiguous bf16 or fp16 [heads, 256, 512] CUDA tensor")
-    for c, name in ((cache, "cache"), (k_out, "k_out"), (v_out, "v_out")):
-        _like_cache(c, weight.dtype, name)
+    dev, handle = _begin(weight, stream)
+    _table(block_table, "block_table"), _table(out_table, "out_table"), _i32(kv_lens, "kv_lens")
+    _on(dev, block_table, out_table, kv_lens)
+    descs = [_like_cache(dev, c, weight.dtype, name) for c, name in ((cache, "cache"), (k_out, "k_out"), (v_out, "v_out"))]
     n = kv_lens.shape[0]
     if block_table.shape[0] != n or out_table.shape[0] != n:
         raise ValueError("block_table, out_table and kv_lens are of different numbers of requests")
     _check("kv_latent_expand", load().kv_latent_expand(
-        _DTYPES[weight.dtype], weight.shape[0], ctypes.byref(cache.desc()), int(tensor), _ptr(block_table), n,
-        block_table.shape[1], block_table.stride(0), _ptr(kv_lens), _ptr(weight), ctypes.byref(k_out.desc()), int(k_tensor),
-        ctypes.byref(v_out.desc()), int(v_tensor), _ptr(out_table), out_table.shape[1], out_table.stride(0), _stream(stream)))
+        code, weight.shape[0], descs[0], tensor, block_table.data_ptr(), n, block_table.shape[1], block_table.stride(0),
+        kv_lens.data_ptr(), weight.data_ptr(), descs[1], k_tensor, descs[2], v_tensor, out_table.data_ptr(), out_table.shape[1],
+        out_table.stride(0), handle))
 
 
-def kv_attention_mass_workspace_bytes() -> int:
-    out = ctypes.c_int64(0)
-    _check("kv_attention_mass_workspace_bytes", load().kv_attention_mass_workspace_bytes(ctypes.byref(out)))
-    return out.value
+def _score_rows(t: torch.Tensor, n: int, width: int, name: str):
+    if t.dtype != torch.float32 or t.dim() != 2 or t.shape[0] != n or t.shape[1] < width or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a row-major float32 [n_reqs, {width} or more] CUDA tensor")
 
 
 def kv_attention_mass(q: torch.Tensor, cache: PagedCache, block_table: torch.Tensor, q_offsets: torch.Tensor,
@@ -627,31 +679,34 @@ def kv_attention_mass(q: torch.Tensor, cache: PagedCache, block_table: torch.Ten
                       width: Optional[int] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The attention weight every cached token receives from q, added to prev (float32 [n_reqs, width], or None);
     returns score [n_reqs, width].  width: prev's or score's columns, else a table row's slots."""
-    _rows3(q, "q")
-    _like_cache(cache, q.dtype, "cache")
+    code = _rows3(q, "q")
+    dev, handle = _begin(q, stream)
+    k_desc = _like_cache(dev, cache, q.dtype, "cache")
     T, H, dk = q.shape
-    kv_heads, left = divmod(cache.row_bytes, dk * q.element_size())
+    kv_heads, left = divmod(cache.row_bytes, dk * 2) if dk else (0, 0)
     if left or not kv_heads:
         raise ValueError("the cache's rows are not whole heads of q's width")
-    batch = _attn_batch(block_table, q_offsets, kv_lens, T)
+    batch = _attn_batch(dev, block_table, q_offsets, kv_lens, T)
     if lse.shape != (T, H) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 [tokens, heads] tensor")
     n = kv_lens.shape[0]
     if width is None:
         width = prev.shape[1] if prev is not None else score.shape[1] if score is not None else batch.max_blocks_per_req * cache.block_size
     if score is None:
-        score = torch.empty((n, width), dtype=torch.float32, device=q.device)
-    for t, name in ((prev, "prev"), (score, "score")):
-        if t is not None and (t.dtype != torch.float32 or t.dim() != 2 or t.shape[0] != n or t.shape[1] < width or t.stride(1) != 1):
-            raise ValueError(f"{name} must be a row-major float32 [n_reqs, width] CUDA tensor")
+        with _outputs_on(stream):
+            score = torch.empty((n, width), dtype=torch.float32, device=q.device)
+    else:
+        _score_rows(score, n, width, "score")
+    if prev is not None:
+        _score_rows(prev, n, width, "prev")
     if workspace is None:
-        with torch.cuda.device(q.device):
-            workspace = torch.empty(kv_attention_mass_workspace_bytes(), dtype=torch.uint8, device=q.device)
-    desc = KvAttnDesc(_DTYPES[q.dtype], H, kv_heads, dk, dk, int(causal), int(window), float(scale))
+        workspace = _own_workspace(kv_attention_mass_workspace_bytes, dev, handle)
+    _on(dev, lse, score, prev, workspace)
+    desc = KvAttnDesc(code, H, kv_heads, dk, dk, causal, window, scale)
     _check("kv_attention_mass", load().kv_attention_mass(
-        ctypes.byref(desc), ctypes.byref(batch), ctypes.byref(cache.desc()), int(k_tensor), 0, _ptr(q), *_strides(q), _ptr(lse),
-        _ptr(prev), prev.stride(0) if prev is not None else 0, _ptr(score), score.stride(0), int(width), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+        desc, batch, k_desc, k_tensor, 0, q.data_ptr(), q.stride(0) * 2, q.stride(1) * 2, lse.data_ptr(),
+        prev.data_ptr() if prev is not None else None, prev.stride(0) if prev is not None else 0, score.data_ptr(), score.stride(0),
+        width, workspace.data_ptr(), workspace.nbytes, handle))
     return score
 
 
@@ -661,6 +716,7 @@ def kv_evict(cache: PagedCache, block_table: torch.Tensor, kv_lens: torch.Tensor
     """Trims every request to `budget` tokens: the first `sinks`, the last `recent` and the highest scores between, in
     their order; rows of every tensor and plane are gathered to out_table's pages (None: in place).  Returns
     (new_lens int32 [n_reqs], kept int32 [n_reqs, budget], out_score float32 [n_reqs, budget])."""
+    dev, handle = _begin(kv_lens, stream)
     _table(block_table, "block_table"), _i32(kv_lens, "kv_lens")
     if out_table is None:
         out_table = block_table
@@ -668,24 +724,25 @@ def kv_evict(cache: PagedCache, block_table: torch.Tensor, kv_lens: torch.Tensor
     n = kv_lens.shape[0]
     if block_table.shape[0] != n or out_table.shape[0] != n:
         raise ValueError("block_table, out_table and kv_lens are of different numbers of requests")
-    if score.dtype != torch.float32 or score.dim() != 2 or score.shape[0] != n or score.stride(1) != 1:
-        raise ValueError("score must be a row-major float32 [n_reqs, width] CUDA tensor")
-    dev = kv_lens.device
-    if new_lens is None:
-        new_lens = torch.empty(n, dtype=torch.int32, device=dev)
-    if kept is None:
-        kept = torch.empty((n, max(0, budget)), dtype=torch.int32, device=dev)
-    if out_score is None:
-        out_score = torch.empty((n, max(0, budget)), dtype=torch.float32, device=dev)
+    if budget < 0:
+        raise ValueError("budget must not be negative")
+    _score_rows(score, n, 0, "score")
+    with _outputs_on(stream):
+        if new_lens is None:
+            new_lens = torch.empty(n, dtype=torch.int32, device=kv_lens.device)
+        if kept is None:
+            kept = torch.empty((n, budget), dtype=torch.int32, device=kv_lens.device)
+        if out_score is None:
+            out_score = torch.empty((n, budget), dtype=torch.float32, device=kv_lens.device)
     _i32(new_lens, "new_lens")
     if new_lens.shape[0] != n or kept.dtype != torch.int32 or kept.shape != (n, budget) or (budget > 1 and kept.stride(1) != 1):
         raise ValueError("new_lens must be int32 [n_reqs] and kept a row-major int32 [n_reqs, budget]")
-    if out_score.dtype != torch.float32 or out_score.shape[0] != n or out_score.shape[1] < budget or (budget > 1 and out_score.stride(1) != 1):
-        raise ValueError("out_score must be a row-major float32 [n_reqs, budget] CUDA tensor")
+    _score_rows(out_score, n, budget, "out_score")
+    _on(dev, block_table, out_table, kv_lens, score, new_lens, kept, out_score, cache.tensors[0])
     _check("kv_evict", load().kv_evict(
-        ctypes.byref(cache.desc()), _ptr(block_table), n, block_table.shape[1], block_table.stride(0), _ptr(kv_lens), _ptr(score),
-        score.stride(0), score.shape[1], int(budget), int(sinks), int(recent), _ptr(out_table), out_table.shape[1],
-        out_table.stride(0), _ptr(new_lens), _ptr(kept), kept.stride(0), _ptr(out_score), out_score.stride(0), _stream(stream)))
+        cache.desc(), block_table.data_ptr(), n, block_table.shape[1], block_table.stride(0), kv_lens.data_ptr(), score.data_ptr(),
+        score.stride(0), score.shape[1], budget, sinks, recent, out_table.data_ptr(), out_table.shape[1], out_table.stride(0),
+        new_lens.data_ptr(), kept.data_ptr(), kept.stride(0), out_score.data_ptr(), out_score.stride(0), handle))
     return new_lens, kept, out_score
 
 
