@@ -283,20 +283,33 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                 if (!wait.warp(smem_addr(&aux.s_full[g]), steps & 1)) { ok = false; break; }
                 tc_fence_after();
                 if (warp_live) {
-                    // the maximum over all 128 scores; the upper 64 stay in registers, the lower 64 are read again
+                    // the maximum over all 128 scores.  A tile that some row sees in part (the first and last of a
+                    // request, the diagonal) goes through a short loop, all others through straight code that
+                    // keeps the upper 64 scores in registers and reads the lower 64 again: a call of one or two
+                    // tiles a CTA is bound by fetching instructions
                     const int from = lo - kb, to_key = hi - kb;
                     const bool hide = __any_sync(0xffffffffu, from > 0 || to_key < kTile);
                     uint32_t x0[32], x1[32], x2[32], x3[32];
-                    tmem_ld32(s_at, x0);
-                    tmem_ld32(s_at + 32, x1);
-                    tc_wait_ld();
-                    tmem_ld32(s_at + 64, x2);
-                    tmem_ld32(s_at + 96, x3);
-                    if (hide) hide32(x0, 0, from, to_key), hide32(x1, 32, from, to_key);
-                    float top = max32(x1, max32(x0, -INFINITY));
-                    tc_wait_ld();
-                    if (hide) hide32(x2, 64, from, to_key), hide32(x3, 96, from, to_key);
-                    top = max32(x3, max32(x2, top));
+                    float top;
+                    if (hide) {
+                        top = -INFINITY;
+#pragma unroll 1
+                        for (int q = 0; q < 4; q++) {
+                            tmem_ld32(s_at + q * 32, x0);
+                            tc_wait_ld();
+                            hide32(x0, from - q * 32, to_key - q * 32);
+                            top = max32(x0, top);
+                        }
+                    } else {
+                        tmem_ld32(s_at, x0);
+                        tmem_ld32(s_at + 32, x1);
+                        tc_wait_ld();
+                        tmem_ld32(s_at + 64, x2);
+                        tmem_ld32(s_at + 96, x3);
+                        top = max32(x1, max32(x0, -INFINITY));
+                        tc_wait_ld();
+                        top = max32(x3, max32(x2, top));
+                    }
                     const bool grow = top > m + slack;  // -inf + slack: the first finite score
                     if (__any_sync(0xffffffffu, grow)) {
                         const float to_m = grow ? top : m;
@@ -306,7 +319,7 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                         if (k > first) {
                             if (!wait.warp(smem_addr(&aux.o_done[g]), (steps - 1) & 1)) { ok = false; break; }
                             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                             for (int q = 0; q < DV / 32; q++) {
                                 uint32_t o[32];
                                 tmem_ld32(o_at + q * 32, o);
@@ -320,21 +333,31 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                     const float mc = m == -INFINITY ? 0.0f : m * p.o.c;
                     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                     uint32_t pk[16];
-                    // P takes the columns of the upper 64 scores, which are in registers
-                    weights32<Bf16>(x2, p.o.c, mc, sum, pk);
-                    tmem_ld32(s_at, x0);
-                    tmem_st16(s_at + 96, pk);
-                    weights32<Bf16>(x3, p.o.c, mc, sum, pk);
-                    tc_wait_ld();
-                    tmem_ld32(s_at + 32, x1);
-                    tmem_st16(s_at + 112, pk);
-                    if (hide) hide32(x0, 0, from, to_key);
-                    weights32<Bf16>(x0, p.o.c, mc, sum, pk);
-                    tc_wait_ld();
-                    tmem_st16(s_at + 64, pk);
-                    if (hide) hide32(x1, 32, from, to_key);
-                    weights32<Bf16>(x1, p.o.c, mc, sum, pk);
-                    tmem_st16(s_at + 80, pk);
+                    // P takes the columns of the upper 64 scores: 32 keys' weights stand in 16 columns from 64 on, so
+                    // going down no score is overwritten before it has been read
+                    if (hide) {
+#pragma unroll 1
+                        for (int q = 3; q >= 0; q--) {
+                            tmem_ld32(s_at + q * 32, x0);
+                            tc_wait_ld();
+                            hide32(x0, from - q * 32, to_key - q * 32);
+                            weights32<Bf16>(x0, p.o.c, mc, sum, pk);
+                            tmem_st16(s_at + 64 + q * 16, pk);
+                        }
+                    } else {
+                        weights32<Bf16>(x2, p.o.c, mc, sum, pk);
+                        tmem_ld32(s_at, x0);
+                        tmem_st16(s_at + 96, pk);
+                        weights32<Bf16>(x3, p.o.c, mc, sum, pk);
+                        tc_wait_ld();
+                        tmem_ld32(s_at + 32, x1);
+                        tmem_st16(s_at + 112, pk);
+                        weights32<Bf16>(x0, p.o.c, mc, sum, pk);
+                        tc_wait_ld();
+                        tmem_st16(s_at + 64, pk);
+                        weights32<Bf16>(x1, p.o.c, mc, sum, pk);
+                        tmem_st16(s_at + 80, pk);
+                    }
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tc_wait_st();
                 }
@@ -381,7 +404,7 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
             const int slot = 2 * blockIdx.x + (w.at.off == 0 ? 1 : 0);
             float *part = p.ws + (int64_t)slot * (kRows * (DV + 2));
             if (warp_live) {
-#pragma unroll
+#pragma unroll 1
                 for (int q = 0; q < DV / 32; q++) {
                     uint32_t o[32];
                     tmem_ld32(o_at + q * 32, o);

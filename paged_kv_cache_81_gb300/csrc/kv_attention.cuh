@@ -78,7 +78,7 @@ __device__ __noinline__ void join_rows(const Output p, const float *ws, int c0, 
     constexpr int kLanes = DV / 8, kRowsPerPass = 128 / kLanes, kBatch = 4;
     const int t = threadIdx.x & 127, col = (t % kLanes) * 8;
     for (int r0 = row0 + t / kLanes; r0 < row0 + rows; r0 += kRowsPerPass * kBatch) {
-        // four rows at a time, two fragments ahead: the loads, not the arithmetic, take the time
+        // four rows at a time: the loads, not the arithmetic, take the time
         float o[kBatch][8], m[kBatch], l[kBatch];
 #pragma unroll
         for (int k = 0; k < kBatch; k++) {
@@ -86,7 +86,7 @@ __device__ __noinline__ void join_rows(const Output p, const float *ws, int c0, 
 #pragma unroll
             for (int j = 0; j < 8; j++) o[k][j] = 0.0f;
         }
-#pragma unroll 2
+#pragma unroll 1
         for (int i = 0; i < count; i++) {
             const float *part = ws + (2 * ((c0 + i) * halves + half) + (i == 0)) * (int64_t)stride;
             float pm[kBatch], pl[kBatch];

@@ -105,8 +105,8 @@ expand_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__
         [&](int r) { return (long long)((request_len(p, r, blockIdx.x == 0) + kTile - 1) / kTile) * p.heads; },
         [&](int r, long long rest) {
             aux.req = r;
-            aux.tile = (int)(rest / p.heads);
-            aux.head = (int)(rest % p.heads);
+            aux.tile = (int)line_div(rest, p.heads);
+            aux.head = (int)(rest - (long long)aux.tile * p.heads);
         });
     tc_fence_before();
     __syncthreads();
@@ -208,7 +208,7 @@ expand_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__
                 const int d = heads & 1, head = w.head + h;
                 if (!wait.warp(smem_addr(&aux.d_full[d]), (heads >> 1) & 1)) { ok = false; break; }
                 tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                 for (int q = 0; q < kN / 32; q++) {
                     uint32_t x[32];
                     tmem_ld32(tmem + d * kN + q * 32 + mine, x);

@@ -258,17 +258,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                     tmem_ld32(s_at + 32, x[1]);
                     tc_wait_ld();
                     if (__any_sync(0xffffffffu, kb < lo || kb + kKeys > hi)) {
-                        const int a = lo - kb, z = hi - kb;
-#pragma unroll
-                        for (int q = 0; q < 2; q++)
-#pragma unroll
-                            for (int i = 0; i < 32; i++)
-                                if (q * 32 + i < a || q * 32 + i >= z) x[q][i] = 0xff800000u;
+                        hide32(x[0], lo - kb, hi - kb);
+                        hide32(x[1], lo - kb - 32, hi - kb - 32);
                     }
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int i = 0; i < 64; i++) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(x[i >> 5][i & 31]));
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    const float top = max32(x[1], max32(x[0], -INFINITY));
                     const bool grow = top > m + slack;
                     if (__any_sync(0xffffffffu, grow)) {
                         const float to_m = grow ? top : m;
@@ -278,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                         if (k > 0) {
                             if (!wait.warp(smem_addr(&aux.o_done[s ^ 1]), ((n - 1) >> 1) & 1)) { ok = false; break; }
                             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                             for (int q = 0; q < kHalf / 32; q++) {
                                 uint32_t o[32];
                                 tmem_ld32(o_at + q * 32, o);
@@ -290,17 +283,13 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                         }
                     }
                     const float mc = m == -INFINITY ? 0.0f : m * p.o.c;
-                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    uint32_t pk[32];
-#pragma unroll
-                    for (int i = 0; i < 64; i += 2) {
-                        const float e0 = exp2_fast(fmaf(__uint_as_float(x[i / 32][i % 32]), p.o.c, -mc));
-                        const float e1 = exp2_fast(fmaf(__uint_as_float(x[i / 32][i % 32 + 1]), p.o.c, -mc));
-                        sum[i / 2 % 4] += e0 + e1;
-                        pk[i / 2] = pack2<Bf16>(e0, e1);
-                    }
-                    tmem_st32(s_at, pk);
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                    uint32_t pk[16];
+                    weights32<Bf16>(x[0], p.o.c, mc, sum, pk);
+                    tmem_st16(s_at, pk);
+                    weights32<Bf16>(x[1], p.o.c, mc, sum, pk);
+                    tmem_st16(s_at + 16, pk);
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tc_wait_st();
                 }
                 // rows that no query sees must not reach the second product (the scores of this tile are out)
@@ -324,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
             const float inv = l > 0.0f ? 1.0f / l : 0.0f;
             float *frag = p.ws + (int64_t)(2 * blockIdx.x + (w.at.off == 0 ? 1 : 0)) * (kRows * (kHalf + 2));
             if (warp_live) {
-#pragma unroll
+#pragma unroll 1
                 for (int q = 0; q < kHalf / 32; q++) {
                     uint32_t o[32];
                     tmem_ld32(o_at + q * 32, o);

@@ -314,16 +314,13 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
                     tc_fence_after();
                     const int c0 = (va - tok0) * group, c1 = min(cols, (vb - tok0) * group);
                     float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
                     for (int q = 0; q < cols; q += 32) {
                         uint32_t x[32];
                         tmem_ld32(s_at + q, x);
                         tc_wait_ld();
                         const float4 *neg = reinterpret_cast<const float4 *>(&aux.neg[g][q]);
-                        if (__any_sync(0xffffffffu, c0 > q || c1 < q + 32)) {
-#pragma unroll
-                            for (int j = 0; j < 32; j++)
-                                if (q + j < c0 || q + j >= c1) x[j] = 0xff800000u;
-                        }
+                        if (__any_sync(0xffffffffu, c0 > q || c1 < q + 32)) hide32(x, c0 - q, c1 - q);
 #pragma unroll
                         for (int j = 0; j < 8; j++) {
                             const float4 e = neg[j];

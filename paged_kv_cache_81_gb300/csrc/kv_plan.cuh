@@ -85,6 +85,7 @@ __device__ __forceinline__ int unit_cost(const Unit &u) { return max(1, u.tiles)
 __device__ __forceinline__ long long head_cost(const Batch &b, const Request &q)
 {
     long long n = 0;
+#pragma unroll 1
     for (int j = 0; j < q.units; j++) n += unit_cost(make_unit(b, q, j));
     return n;
 }
@@ -94,6 +95,14 @@ struct Place {
     int32_t req, head, unit, off;
 };
 
+// Quotients of the line's places.  Its length fits 32 bits but for very large batches, and a 64-bit
+// division is a few hundred instructions of code that a short call would fetch for nothing else.
+__device__ __forceinline__ long long line_div(long long a, long long b)
+{
+    if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
+}
+
 // How the line is cut: part p of `used` takes the steps [total p / used, total (p + 1) / used).
 struct Line {
     long long begin;  // this CTA's first step
@@ -102,7 +111,7 @@ struct Line {
     int steps;  // this CTA's; 0: none
 
     // The part that takes step x.
-    __device__ __forceinline__ int part_of(long long x) const { return (int)(((x + 1) * used - 1) / total); }
+    __device__ __forceinline__ int part_of(long long x) const { return (int)line_div((x + 1) * used - 1, total); }
 };
 
 // Finds a CTA's piece of a line made of n_reqs stretches, the r-th cost(r) steps long; every thread of
@@ -116,6 +125,7 @@ __device__ __forceinline__ Line find_piece(int n_reqs, int part, int parts, int 
     const int per = (n_reqs + Threads - 1) / Threads;
     const int r0 = min(tid * per, n_reqs), r1 = min(r0 + per, n_reqs);
     long long mine = 0;
+#pragma unroll 1
     for (int r = r0; r < r1; r++) mine += cost(r);
     long long upto = mine;  // inclusive scan
 #pragma unroll
@@ -126,20 +136,22 @@ __device__ __forceinline__ Line find_piece(int n_reqs, int part, int parts, int 
     if (lane == 31) scratch[warp] = upto;
     __syncthreads();
     long long before = 0, total = 0;
+#pragma unroll 1
     for (int w = 0; w < kWarps; w++) {
         if (w < warp) before += scratch[w];
         total += scratch[w];
     }
     upto += before;
     // pieces of at least `least` steps; none is empty but the last ones
-    Line line{0, total, min((long long)parts, (total + least - 1) / least), 0};
+    Line line{0, total, min((long long)parts, least == 1 ? total : line_div(total + least - 1, least)), 0};
     if (part < line.used) {
-        line.begin = total * part / line.used;
-        line.steps = (int)(total * (part + 1) / line.used - line.begin);
+        line.begin = line_div(total * part, line.used);
+        line.steps = (int)(line_div(total * (part + 1), line.used) - line.begin);
         if (line.begin >= upto - mine && line.begin < upto) {
             long long rest = line.begin - (upto - mine);
+#pragma unroll 1
             for (int r = r0; r < r1; r++) {
-                const long long all = cost(r);
+                const long long all = r1 - r0 == 1 ? mine : cost(r);
                 if (rest < all) {
                     found(r, rest);
                     break;
@@ -163,8 +175,9 @@ __device__ __forceinline__ Line find_place(const Batch &b, int part, int parts, 
             const long long h = head_cost(b, q);
             Place p;
             p.req = r;
-            p.head = (int)(rest / h);
+            p.head = (int)line_div(rest, h);
             rest -= p.head * h;
+#pragma unroll 1
             for (p.unit = 0;; p.unit++) {
                 const int n = unit_cost(make_unit(b, q, p.unit));
                 if (rest < n) break;

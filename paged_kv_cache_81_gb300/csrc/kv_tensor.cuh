@@ -242,12 +242,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)  // lo in the low 
     return r;
 }
 
-// Scores of 32 keys, the first of them key `at` of its tile: those outside [a, z) become -inf.
-__device__ __forceinline__ void hide32(uint32_t (&x)[32], int at, int a, int z)
+// Scores of 32 keys: those outside [a, z) become -inf.
+__device__ __forceinline__ void hide32(uint32_t (&x)[32], int a, int z)
 {
+    const uint32_t seen = (a >= 32 ? 0u : 0xffffffffu << max(a, 0)) & (z <= 0 ? 0u : 0xffffffffu >> (32 - min(z, 32)));
 #pragma unroll
     for (int i = 0; i < 32; i++)
-        if (at + i < a || at + i >= z) x[i] = 0xff800000u;
+        if (!(seen >> i & 1)) x[i] = 0xff800000u;
 }
 
 __device__ __forceinline__ float max32(const uint32_t (&x)[32], float top)
