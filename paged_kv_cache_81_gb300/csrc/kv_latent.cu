@@ -8,8 +8,8 @@
 //   TMEM           O 256 columns, S twice 64, Q's first four panels 128 (A operand from TMEM)
 //   shared memory  Q's other five panels 80 KB; two tiles of 64 keys, 72 KB each: the four panels that
 //                  are this CTA's values, and the five that the scores alone use and free earlier
-//   warp 0 loads, warp 1 issues the products, warps 4-7 hold a row a thread (maximum, exponentials, P
-//   over S, lazy rescaling as in kv_attention.cu).  S of the next tile is formed before O += P V of
+//   warps 0 and 2 load the two kinds of panels, warp 3 loads Q, warp 1 issues the products, warps 4-7 hold
+//   a row a thread (maximum, exponentials, P over S, lazy rescaling as in kv_attention.cu).  S of the next tile is formed before O += P V of
 //   this one, so the tensor core works while the exponentials run.
 #include "kv_attention.cuh"
 
@@ -38,6 +38,7 @@ struct Params {
     int32_t num_blocks;
     FastDiv block;
     int32_t piece_rows;
+    int32_t q_rows;  // rows one TMA brings of q
     const char *q;
     int64_t q_token, q_head;
     Output o;
@@ -46,7 +47,7 @@ struct Params {
 };
 
 struct Aux {
-    uint64_t v_full[2], v_empty[2], x_full[2], x_empty[2], s_full[2], p_ready[2], o_done[2], q_full, join;
+    uint64_t v_full[2], v_empty[2], x_full[2], x_empty[2], s_full[2], p_ready[2], o_done[2], q_full, q_empty, join;
     long long scan[8];
     Place place;
     uint32_t tmem;
@@ -55,8 +56,42 @@ struct Aux {
 };
 static_assert(sizeof(Aux) <= 1024, "bookkeeping");
 
+// Panels of one tile of rows into their slot: a TMA per (run of slots inside a page, panel), spread over the
+// lanes; column(h) is the first element of panel h.  The first page a lane needs is looked up before
+// `ready` waits for the slot.
+template <int Panels, typename Column, typename Ready>
+__device__ __forceinline__ bool load_tile(const Params &p, const Walk &w, int kb, uint32_t to, uint32_t bar, const CUtensorMap *map, const Column &column,
+                                          const Ready &ready)
+{
+    const int lane = threadIdx.x & 31, pr = p.piece_rows;
+    const int p0 = max(0, w.u.lo - kb) / pr, p1 = (min(w.u.hi - kb, kKeys) + pr - 1) / pr;
+    const int32_t *row = p.table + (int64_t)w.at.req * p.table_stride;
+    int page = 0, slot = 0;
+    const auto find = [&](int i) {
+        const uint32_t key = (uint32_t)(kb + i * pr), col = fdiv(key, p.block);
+        slot = (int)(key - col * p.block.d);
+        page = __ldg(row + col);
+        if (page < 0 || page >= p.num_blocks) {
+            set_error(p.b.err, KV_DERR_TABLE);
+            page = p.num_blocks;  // outside the map: reads zeros
+        }
+    };
+    if (p0 + lane < p1) find(p0 + lane);
+    if (!ready()) return false;
+    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)((p1 - p0) * pr) * Panels * 128);
+    __syncwarp();
+    for (int i = p0 + lane; i < p1; i += 32) {
+        if (i >= p0 + 32) find(i);
+#pragma unroll
+        for (int h = 0; h < Panels; h++) tma_load_4d(to + h * kPanel + i * pr * 128, map, bar, column(h), 0, slot, page);
+    }
+    __syncwarp();
+    return true;
+}
+
 template <bool Bf16>
-__global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_constant__ CUtensorMap map, const Params p)
+__global__ void __launch_bounds__(kThreads, 1)
+latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap q_map, const Params p)
 {
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t base = smem_addr(smem);
@@ -79,7 +114,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
             // product two tiles before has completed (its scores' successor is out) but the last may not have
             mbar_init(smem_addr(&aux.o_done[i]), 1);
         }
-        mbar_init(smem_addr(&aux.q_full), 4);
+        mbar_init(smem_addr(&aux.q_full), 5);  // four warps of the softmax group, and the TMA
+        mbar_init(smem_addr(&aux.q_empty), 1);
         mbar_init(smem_addr(&aux.join), 4);
         mbar_init_fence();
         tma_prefetch_map(&map);
@@ -95,54 +131,49 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
     if (!w.start(b, aux.place, line)) {
         // nothing to do: on to the common exit
     } else if (warp == 0) {
-        // ---- loads: the five other panels, then the four of this CTA's values ----
-        const int pr = p.piece_rows;
+        // ---- the five panels that only the scores use ----
         int it = 0;
         bool ok = true;
         do {
-            if (w.u.tiles == 0) continue;
-            const int32_t *row = p.table + (int64_t)w.at.req * p.table_stride;
-            const int kt0 = w.u.tile0 + w.at.off;
-            for (int t = 0; t < w.n; t++, it++) {
-                const int kb = (kt0 + t) * kKeys;
-                const int p0 = max(0, w.u.lo - kb) / pr, p1 = (min(w.u.hi - kb, kKeys) + pr - 1) / pr;
+            for (int t = 0; ok && t < w.n && w.u.tiles; t++, it++) {
                 const int s = it & 1;
-                const uint32_t xbar = smem_addr(&aux.x_full[s]), vbar = smem_addr(&aux.v_full[s]);
-                int page = 0, slot = 0;
-                const auto find = [&](int i) {
-                    const uint32_t key = (uint32_t)(kb + i * pr), col = fdiv(key, p.block);
-                    slot = (int)(key - col * p.block.d);
-                    page = __ldg(row + col);
-                    if (page < 0 || page >= p.num_blocks) {
-                        set_error(b.err, KV_DERR_TABLE);
-                        page = p.num_blocks;  // outside the map: reads zeros
-                    }
-                };
-                if (p0 + lane < p1) find(p0 + lane);
-                const int page0 = page, slot0 = slot;
-                if (it >= 2 && !wait.warp(smem_addr(&aux.x_empty[s]), ((it >> 1) - 1) & 1)) { ok = false; break; }
-                if (lane == 0) mbar_arrive_expect_tx(xbar, (uint32_t)((p1 - p0) * pr) * 5 * 128);
-                __syncwarp();
-                for (int i = p0 + lane; i < p1; i += 32) {
-                    if (i >= p0 + 32) find(i);
-#pragma unroll
-                    for (int h = 0; h < 5; h++) {
-                        const int panel = h == 4 ? 8 : h + 4 - 4 * half;  // the other half's values, then the rotary part
-                        tma_load_4d(base + kOffX + (s * 5 + h) * kPanel + i * pr * 128, &map, xbar, panel * 64, 0, slot, page);
-                    }
-                }
-                page = page0, slot = slot0;
-                if (it >= 2 && !wait.warp(smem_addr(&aux.v_empty[s]), ((it >> 1) - 1) & 1)) { ok = false; break; }
-                if (lane == 0) mbar_arrive_expect_tx(vbar, (uint32_t)((p1 - p0) * pr) * 4 * 128);
-                __syncwarp();
-                for (int i = p0 + lane; i < p1; i += 32) {
-                    if (i >= p0 + 32) find(i);
-#pragma unroll
-                    for (int h = 0; h < 4; h++)
-                        tma_load_4d(base + kOffV + (s * 4 + h) * kPanel + i * pr * 128, &map, vbar, (h + 4 * half) * 64, 0, slot, page);
-                }
+                ok = load_tile<5>(p, w, (w.u.tile0 + w.at.off + t) * kKeys, base + kOffX + s * 5 * kPanel, smem_addr(&aux.x_full[s]), &map,
+                                  [&](int h) { return (h == 4 ? 8 : h + 4 - 4 * half) * 64; },  // the other half's values, the rotary part
+                                  [&] { return it < 2 || wait.warp(smem_addr(&aux.x_empty[s]), ((it >> 1) - 1) & 1); });
             }
         } while (ok && w.next(b));
+    } else if (warp == 2) {
+        // ---- the four panels that are this CTA's values too ----
+        int it = 0;
+        bool ok = true;
+        do {
+            for (int t = 0; ok && t < w.n && w.u.tiles; t++, it++) {
+                const int s = it & 1;
+                ok = load_tile<4>(p, w, (w.u.tile0 + w.at.off + t) * kKeys, base + kOffV + s * 4 * kPanel, smem_addr(&aux.v_full[s]), &map,
+                                  [&](int h) { return (h + 4 * half) * 64; },
+                                  [&] { return it < 2 || wait.warp(smem_addr(&aux.v_empty[s]), ((it >> 1) - 1) & 1); });
+            }
+        } while (ok && w.next(b));
+    } else if (warp == 3) {
+        // ---- the five panels of Q that go with them ----
+        int units = 0;
+        const int group = (int)b.group.d;
+        do {
+            if (w.u.tiles == 0) continue;
+            if (units && !wait.warp(smem_addr(&aux.q_empty), (units - 1) & 1)) break;
+            units++;
+            const int boxes = (w.u.rows + p.q_rows - 1) / p.q_rows;
+            if (lane == 0) mbar_arrive_expect_tx(smem_addr(&aux.q_full), (uint32_t)(boxes * p.q_rows) * 5 * 128);
+            __syncwarp();
+            for (int i = lane; i < boxes; i += 32) {
+                const int row = w.u.row0 + i * p.q_rows, tok = (int)fdiv((uint32_t)row, b.group), head = row - tok * group;
+#pragma unroll
+                for (int h = 0; h < 5; h++)
+                    tma_load_3d(base + h * kQPanel + i * p.q_rows * 128, &q_map, smem_addr(&aux.q_full), (h == 4 ? 8 : h + 4 - 4 * half) * 64, head,
+                                w.q.q0 + tok);
+            }
+            __syncwarp();
+        } while (w.next(b));
     } else if (warp == 1) {
         // ---- matrix products ----
         constexpr uint32_t qk_desc = mma_desc(Bf16, 128, kKeys, false), pv_desc = mma_desc(Bf16, 128, kHalf, true);
@@ -167,6 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                 for (int kk = 0; kk < 20; kk++)
                     mma_ss(d, qd + (((kk / 4) * kQPanel + (kk % 4) * 32) >> 4), xs + (((kk / 4) * kPanel + (kk % 4) * 32) >> 4), qk_desc, kk > 0, elected);
                 tc_commit(smem_addr(&aux.x_empty[s]), elected);
+                if (i + 1 == w.n) tc_commit(smem_addr(&aux.q_empty), elected);
                 if (!wait.warp(smem_addr(&aux.v_full[s]), (n >> 1) & 1)) return false;
 #pragma unroll
                 for (int kk = 0; kk < 16; kk++)
@@ -212,34 +244,22 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                 continue;
             }
             const bool warp_live = __any_sync(0xffffffffu, live);
-            // Q: the last tile's scores are out, so the tensor core has done with the previous one
+            // Q's four panels in tensor memory: the last unit's accumulator was complete, so its scores were too
             {
-                const int q_row0 = w.u.row0;
-#pragma unroll 4
-                for (int i = t; i < 128 * 40; i += 128) {
-                    const int rr = i / 40, cc = i % 40, ur = q_row0 + rr;
-                    if (rr < w.u.rows) {
-                        const int tt = (int)fdiv((uint32_t)ur, b.group), hh = ur - tt * (int)b.group.d;
-                        const int panel = cc / 8 == 4 ? 8 : cc / 8 + 4 - 4 * half;
-                        const uint4 v = *reinterpret_cast<const uint4 *>(p.q + (int64_t)(w.q.q0 + tt) * p.q_token + (int64_t)hh * p.q_head + panel * 128 + (cc & 7) * 16);
-                        st_smem16(base + (cc / 8) * kQPanel + panel_off(rr, cc & 7), v);
-                    }
-                }
                 if (warp_live) {
                     const char *from = p.q + out_row * p.q_token + (int64_t)head * p.q_head + half * kHalf * 2;
+                    uint4 v[kQT][8];  // all of it at once: one trip to memory
+#pragma unroll
+                    for (int i = 0; i < 8 * kQT; i++) v[i / 8][i % 8] = *reinterpret_cast<const uint4 *>(from + i * 16);
 #pragma unroll
                     for (int q = 0; q < kQT; q++) {
-                        uint32_t v[32];
+                        uint32_t x[32];
 #pragma unroll
-                        for (int i = 0; i < 8; i++) {
-                            const uint4 x = *reinterpret_cast<const uint4 *>(from + q * 128 + i * 16);
-                            v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
-                        }
-                        tmem_st32(tmem + kTmQ + q * 32 + mine, v);
+                        for (int i = 0; i < 8; i++) x[4 * i] = v[q][i].x, x[4 * i + 1] = v[q][i].y, x[4 * i + 2] = v[q][i].z, x[4 * i + 3] = v[q][i].w;
+                        tmem_st32(tmem + kTmQ + q * 32 + mine, x);
                     }
                     tc_wait_st();
                 }
-                fence_async_smem();
                 tc_fence_before();
                 warp_arrive(smem_addr(&aux.q_full));
             }
@@ -389,8 +409,19 @@ extern "C" int kv_latent_attention(const kv_attn_desc *d, const kv_attn_batch *b
     if ((st = check_rows(out, out_token_stride, out_head_stride)) != KV_OK) return st;
     if (workspace == nullptr) return KV_ERR_INVALID_ARG;
     if (!aligned16(workspace) || ((uintptr_t)lse & 3u)) return KV_ERR_ALIGN;
+    // A unit is whole tokens of up to 128 heads each, or a divisor of a token's heads; a TMA of q brings all
+    // heads of as many tokens as a request has on average (a divisor of a unit's), or a unit.
+    int box_heads = d->n_heads, box_tokens = 1;
+    if (d->n_heads > kRows) {
+        for (box_heads = kRows; d->n_heads % box_heads; box_heads--) {}
+    } else {
+        const int tokens = kRows / d->n_heads;
+        for (; box_tokens < tokens; box_tokens++)
+            if (tokens % box_tokens == 0 && (int64_t)box_tokens * batch->n_reqs >= batch->n_tokens) break;
+    }
+    const int unit_rows = d->n_heads > kRows ? box_heads : kRows / d->n_heads * d->n_heads;
     Params p = {};
-    if ((st = fill_batch(&p.b, batch, d->n_heads, 1, cache->block_size, kRows, kKeys, d->causal, d->window)) != KV_OK) return st;
+    if ((st = fill_batch(&p.b, batch, d->n_heads, 1, cache->block_size, unit_rows, kKeys, d->causal, d->window)) != KV_OK) return st;
     const DeviceInfo *dev = current_device();
     if (dev == nullptr) return KV_ERR_CUDA;
     if (workspace_bytes < attention_workspace(dev->num_sms)) return KV_ERR_RANGE;
@@ -407,8 +438,10 @@ extern "C" int kv_latent_attention(const kv_attn_desc *d, const kv_attn_batch *b
     p.o = Output{(char *)out, out_token_stride, out_head_stride, lse, d->n_heads, kDV, d->scale, d->scale * kLog2e};
     p.counters = (int *)workspace;
     p.ws = (float *)((char *)workspace + kCounterBytes);
-    CUtensorMap map;
+    CUtensorMap map, q_map;
+    p.q_rows = box_heads * box_tokens;
+    if ((st = make_q_map(&q_map, q, q_token_stride, q_head_stride, kD, d->n_heads, batch->n_tokens, box_heads, box_tokens)) != KV_OK) return st;
     if ((st = make_cache_map(&map, cache, tensor, 0, 1, kD, p.piece_rows)) != KV_OK) return st;
     return cuda_status(launch(d->dtype == KV_BF16 ? latent_kernel<true> : latent_kernel<false>, dim3(dev->num_sms / 2 * 2), dim3(kThreads), kBytes,
-                              (cudaStream_t)stream, map, p));
+                              (cudaStream_t)stream, map, q_map, p));
 }
