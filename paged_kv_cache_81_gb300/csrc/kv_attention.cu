@@ -284,12 +284,12 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                 tc_fence_after();
                 if (warp_live) {
                     // the maximum over all 128 scores.  A tile that some row sees in part (the first and last of a
-                    // request, the diagonal) goes through a short loop, all others through straight code that
-                    // keeps the upper 64 scores in registers and reads the lower 64 again: a call of one or two
-                    // tiles a CTA is bound by fetching instructions
+                    // request, the diagonal) goes through a short loop (a call of one or two tiles a CTA is bound by
+                    // fetching instructions), all others through straight code that reads 32 scores while it works
+                    // on 32: more of them in registers at once would spill
                     const int from = lo - kb, to_key = hi - kb;
                     const bool hide = __any_sync(0xffffffffu, from > 0 || to_key < kTile);
-                    uint32_t x0[32], x1[32], x2[32], x3[32];
+                    uint32_t x0[32], x1[32];
                     float top;
                     if (hide) {
                         top = -INFINITY;
@@ -302,13 +302,17 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                         }
                     } else {
                         tmem_ld32(s_at, x0);
+                        tc_wait_ld();
                         tmem_ld32(s_at + 32, x1);
+                        top = max32(x0, -INFINITY);
                         tc_wait_ld();
-                        tmem_ld32(s_at + 64, x2);
-                        tmem_ld32(s_at + 96, x3);
-                        top = max32(x1, max32(x0, -INFINITY));
+                        tmem_ld32(s_at + 64, x0);
+                        top = max32(x1, top);
                         tc_wait_ld();
-                        top = max32(x3, max32(x2, top));
+                        tmem_ld32(s_at + 96, x1);
+                        top = max32(x0, top);
+                        tc_wait_ld();
+                        top = max32(x1, top);
                     }
                     const bool grow = top > m + slack;  // -inf + slack: the first finite score
                     if (__any_sync(0xffffffffu, grow)) {
@@ -345,18 +349,20 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                             tmem_st16(s_at + 64 + q * 16, pk);
                         }
                     } else {
-                        weights32<Bf16>(x2, p.o.c, mc, sum, pk);
-                        tmem_ld32(s_at, x0);
-                        tmem_st16(s_at + 96, pk);
-                        weights32<Bf16>(x3, p.o.c, mc, sum, pk);
+                        tmem_ld32(s_at + 64, x0);  // the last 32 are still in x1
+                        weights32<Bf16>(x1, p.o.c, mc, sum, pk);
+                        tmem_st16(s_at + 112, pk);
                         tc_wait_ld();
                         tmem_ld32(s_at + 32, x1);
-                        tmem_st16(s_at + 112, pk);
                         weights32<Bf16>(x0, p.o.c, mc, sum, pk);
+                        tmem_st16(s_at + 96, pk);
                         tc_wait_ld();
-                        tmem_st16(s_at + 64, pk);
+                        tmem_ld32(s_at, x0);
                         weights32<Bf16>(x1, p.o.c, mc, sum, pk);
                         tmem_st16(s_at + 80, pk);
+                        tc_wait_ld();
+                        weights32<Bf16>(x0, p.o.c, mc, sum, pk);
+                        tmem_st16(s_at + 64, pk);
                     }
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tc_wait_st();
@@ -428,9 +434,7 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                         if (whole) {
                             store_row32<Bf16>(to, f, inv, q * 32, p.o.dv);
                         } else {
-                            float4 *d = reinterpret_cast<float4 *>(part + row * DV + q * 32);
-#pragma unroll
-                            for (int i = 0; i < 8; i++) d[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                            store_fragment32(part, kRows, row, q, f);
                         }
                     }
                 }

@@ -64,71 +64,69 @@ struct Output {
     float scale, c;
 };
 
-// Joins rows [row0, row0 + rows) of a cut unit from `count` fragments, `stride` floats a slot: accumulators
-// [.., DV], then maxima and sums `stat` apart.  128 threads; a row's fragments are read in the order of
-// their keys, so the result does not depend on which CTA came last.  Row r is (first + r) / group of the
-// request's tokens from q0 on, head head0 + the rest.  Not inlined: its registers would crowd the loop
-// over the key tiles.
+// Joins rows [row0, row0 + rows) of a cut unit from `count` fragments, `stride` floats a slot.  A fragment
+// holds its accumulators four columns at a time, [DV / 4][stat rows][4], so that writing (a thread a row)
+// and reading (a thread a row and some columns) are both coalesced, then the rows' maxima and sums.  128
+// threads; a row's fragments are added in the order of their keys, so the result does not depend on which
+// CTA came last.  Row r is (first + r) / group of the request's tokens from q0 on, head head0 + the
+// rest.  Not inlined: its registers would crowd the loop over the key tiles.
 template <int DV, bool Bf16>
 __device__ __noinline__ void join_rows(const Output p, const float *ws, int c0, int count, int halves, int half, int stride, int row0, int rows, int stat,
                                        int first, int q0, int head0, const FastDiv group)
 {
-    const int out_col = half * DV;
-    const bool with_lse = half == 0;
-    constexpr int kLanes = DV / 8, kRowsPerPass = 128 / kLanes, kBatch = 4;
-    const int t = threadIdx.x & 127, col = (t % kLanes) * 8;
-    for (int r0 = row0 + t / kLanes; r0 < row0 + rows; r0 += kRowsPerPass * kBatch) {
-        // four rows at a time: the loads, not the arithmetic, take the time
-        float o[kBatch][8], m[kBatch], l[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; k++) {
-            m[k] = -INFINITY, l[k] = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 8; j++) o[k][j] = 0.0f;
-        }
+    constexpr int kBatch = 8;  // column quads in flight for each fragment: the loads take the time
+    int shift = 4;             // rows rounded up to a power of two; the other threads share out the columns
+    while ((1 << shift) < rows) shift++;
+    const int t = threadIdx.x & 127, row = row0 + (t & ((1 << shift) - 1)), parts = 128 >> shift, quads = DV / 4 / parts;
+    const int quad0 = (t >> shift) * quads;
+    if (row >= row0 + rows) return;
+    const auto fragment = [&](int i) { return ws + (2 * ((c0 + i) * halves + half) + (i == 0)) * (int64_t)stride; };
+    float top = -INFINITY;
+#pragma unroll 4
+    for (int i = 0; i < count; i++) top = fmaxf(top, __ldcg(fragment(i) + stat * DV + row));
+    const float z = top == -INFINITY ? 0.0f : top;
+    const int tok = (int)fdiv((uint32_t)(first + row), group), head = head0 + first + row - tok * (int)group.d;
+    const int64_t token = (int64_t)q0 + tok;
+    char *to = p.out + token * p.out_token + (int64_t)head * p.out_head;
 #pragma unroll 1
+    for (int q = quad0; q < quad0 + quads; q += kBatch) {
+        float4 o[kBatch];
+        float l = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kBatch; k++) o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
         for (int i = 0; i < count; i++) {
-            const float *part = ws + (2 * ((c0 + i) * halves + half) + (i == 0)) * (int64_t)stride;
-            float pm[kBatch], pl[kBatch];
-            float4 v[kBatch][2];
+            const float *part = fragment(i);
+            const float pm = __ldcg(part + stat * DV + row), pl = __ldcg(part + stat * (DV + 1) + row);
+            float4 v[kBatch];
 #pragma unroll
-            for (int k = 0; k < kBatch; k++) {
-                const int row = min(r0 + k * kRowsPerPass, row0 + rows - 1);
-                pm[k] = __ldcg(part + stat * DV + row);
-                pl[k] = __ldcg(part + stat * (DV + 1) + row);
-                v[k][0] = __ldcg(reinterpret_cast<const float4 *>(part + row * DV + col));
-                v[k][1] = __ldcg(reinterpret_cast<const float4 *>(part + row * DV + col + 4));
-            }
+            for (int k = 0; k < kBatch; k++)
+                if (k < quads) v[k] = __ldcg(reinterpret_cast<const float4 *>(part) + (q + k) * stat + row);
+            const float a = exp2_fast((pm - z) * p.c);
+            l += pl * a;
 #pragma unroll
-            for (int k = 0; k < kBatch; k++) {
-                const float top = fmaxf(m[k], pm[k]), z = top == -INFINITY ? 0.0f : top;
-                const float a = exp2_fast((m[k] - z) * p.c), b = exp2_fast((pm[k] - z) * p.c);
-                m[k] = top;
-                l[k] = l[k] * a + pl[k] * b;
-                o[k][0] = o[k][0] * a + v[k][0].x * b, o[k][1] = o[k][1] * a + v[k][0].y * b;
-                o[k][2] = o[k][2] * a + v[k][0].z * b, o[k][3] = o[k][3] * a + v[k][0].w * b;
-                o[k][4] = o[k][4] * a + v[k][1].x * b, o[k][5] = o[k][5] * a + v[k][1].y * b;
-                o[k][6] = o[k][6] * a + v[k][1].z * b, o[k][7] = o[k][7] * a + v[k][1].w * b;
-            }
+            for (int k = 0; k < kBatch; k++)
+                if (k < quads) o[k].x += v[k].x * a, o[k].y += v[k].y * a, o[k].z += v[k].z * a, o[k].w += v[k].w * a;
         }
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
-        for (int k = 0; k < kBatch; k++) {
-            const int row = r0 + k * kRowsPerPass;
-            if (row >= row0 + rows) break;
-            const int tok = (int)fdiv((uint32_t)(first + row), group), head = head0 + first + row - tok * (int)group.d;
-            const int64_t token = (int64_t)q0 + tok;
-            const float inv = l[k] > 0.0f ? 1.0f / l[k] : 0.0f;
-            if (out_col + col < p.dv) {
-                uint4 v;
-                v.x = pack2<Bf16>(o[k][0] * inv, o[k][1] * inv);
-                v.y = pack2<Bf16>(o[k][2] * inv, o[k][3] * inv);
-                v.z = pack2<Bf16>(o[k][4] * inv, o[k][5] * inv);
-                v.w = pack2<Bf16>(o[k][6] * inv, o[k][7] * inv);
-                *reinterpret_cast<uint4 *>(p.out + token * p.out_token + (int64_t)head * p.out_head + (out_col + col) * 2) = v;
+        for (int k = 0; k < kBatch; k++)
+            if (k < quads && half * DV + (q + k) * 4 < p.dv) {
+                uint2 v;
+                v.x = pack2<Bf16>(o[k].x * inv, o[k].y * inv);
+                v.y = pack2<Bf16>(o[k].z * inv, o[k].w * inv);
+                *reinterpret_cast<uint2 *>(to + (half * DV + (q + k) * 4) * 2) = v;
             }
-            if (with_lse && col == 0 && p.lse) p.lse[token * p.heads + head] = l[k] > 0.0f ? fmaf(m[k], p.scale, logf(l[k])) : -INFINITY;
-        }
+        if (half == 0 && q == 0 && p.lse) p.lse[token * p.heads + head] = l > 0.0f ? fmaf(top, p.scale, logf(l)) : -INFINITY;
     }
+}
+
+// 32 accumulator columns of a row into its fragment, as join_rows reads them.
+__device__ __forceinline__ void store_fragment32(float *part, int rows, int row, int q, const float (&f)[32])
+{
+    float4 *d = reinterpret_cast<float4 *>(part) + q * 8 * rows + row;
+#pragma unroll
+    for (int i = 0; i < 8; i++) __stcg(d + i * rows, make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]));
 }
 
 // 32 accumulator columns of a row to the output, scaled.

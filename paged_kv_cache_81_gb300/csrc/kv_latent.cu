@@ -11,6 +11,8 @@
 //   warps 0 and 2 load the two kinds of panels, warp 3 loads Q, warp 1 issues the products, warps 4-7 hold
 //   a row a thread (maximum, exponentials, P over S, lazy rescaling as in kv_attention.cu).  S of the next tile is formed before O += P V of
 //   this one, so the tensor core works while the exponentials run.
+#include <type_traits>
+
 #include "kv_attention.cuh"
 
 namespace pkv {
@@ -47,7 +49,7 @@ struct Params {
 };
 
 struct Aux {
-    uint64_t v_full[2], v_empty[2], x_full[2], x_empty[2], s_full[2], p_ready[2], o_done[2], q_full, q_empty, join;
+    uint64_t v_full[2], v_empty[2], x_full[2], x_empty[2], s_full[2], p_ready[2], o_done[2], q_staged, q_moved, q_full, q_empty, join;
     long long scan[8];
     Place place;
     uint32_t tmem;
@@ -114,7 +116,9 @@ latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ C
             // product two tiles before has completed (its scores' successor is out) but the last may not have
             mbar_init(smem_addr(&aux.o_done[i]), 1);
         }
-        mbar_init(smem_addr(&aux.q_full), 5);  // four warps of the softmax group, and the TMA
+        mbar_init(smem_addr(&aux.q_full), 1);
+        mbar_init(smem_addr(&aux.q_staged), 1);
+        mbar_init(smem_addr(&aux.q_moved), 4);
         mbar_init(smem_addr(&aux.q_empty), 1);
         mbar_init(smem_addr(&aux.join), 4);
         mbar_init_fence();
@@ -155,24 +159,28 @@ latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ C
             }
         } while (ok && w.next(b));
     } else if (warp == 3) {
-        // ---- the five panels of Q that go with them ----
+        // ---- Q: its four panels for tensor memory by way of the place of the other five, then those ----
         int units = 0;
         const int group = (int)b.group.d;
         do {
             if (w.u.tiles == 0) continue;
             if (units && !wait.warp(smem_addr(&aux.q_empty), (units - 1) & 1)) break;
             units++;
-            const int boxes = (w.u.rows + p.q_rows - 1) / p.q_rows;
-            if (lane == 0) mbar_arrive_expect_tx(smem_addr(&aux.q_full), (uint32_t)(boxes * p.q_rows) * 5 * 128);
-            __syncwarp();
-            for (int i = lane; i < boxes; i += 32) {
-                const int row = w.u.row0 + i * p.q_rows, tok = (int)fdiv((uint32_t)row, b.group), head = row - tok * group;
+            const auto load = [&](auto count, uint32_t bar, auto column) {
+                const int boxes = (w.u.rows + p.q_rows - 1) / p.q_rows;
+                if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * p.q_rows) * count() * 128);
+                __syncwarp();
+                for (int i = lane; i < boxes; i += 32) {
+                    const int row = w.u.row0 + i * p.q_rows, tok = (int)fdiv((uint32_t)row, b.group), head = row - tok * group;
 #pragma unroll
-                for (int h = 0; h < 5; h++)
-                    tma_load_3d(base + h * kQPanel + i * p.q_rows * 128, &q_map, smem_addr(&aux.q_full), (h == 4 ? 8 : h + 4 - 4 * half) * 64, head,
-                                w.q.q0 + tok);
-            }
-            __syncwarp();
+                    for (int h = 0; h < count(); h++)
+                        tma_load_3d(base + h * kQPanel + i * p.q_rows * 128, &q_map, bar, column(h), head, w.q.q0 + tok);
+                }
+                __syncwarp();
+            };
+            load(std::integral_constant<int, kQT>(), smem_addr(&aux.q_staged), [&](int h) { return (h + 4 * half) * 64; });
+            if (!wait.warp(smem_addr(&aux.q_moved), (units - 1) & 1)) break;
+            load(std::integral_constant<int, 5>(), smem_addr(&aux.q_full), [&](int h) { return (h == 4 ? 8 : h + 4 - 4 * half) * 64; });
         } while (w.next(b));
     } else if (warp == 1) {
         // ---- matrix products ----
@@ -184,7 +192,9 @@ latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ C
         bool ok = true;
         do {
             if (w.u.tiles == 0) continue;
-            ok = wait.warp(smem_addr(&aux.q_full), units++ & 1);
+            // the TMA for q_full was issued after q_moved, so this covers both; the wait for q_moved orders tensor memory
+            ok = wait.warp(smem_addr(&aux.q_moved), units & 1) && wait.warp(smem_addr(&aux.q_full), units & 1);
+            units++;
             if (!ok) break;
             tc_fence_after();
             // Q's panels stand in the order of the key panels as this CTA holds them: the five others
@@ -228,7 +238,7 @@ latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ C
         const uint32_t mine = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t o_at = tmem + kTmO + mine;
         const float slack = 8.0f / p.o.c;
-        int it = 0, cuts = 0;
+        int it = 0, cuts = 0, units = 0;
         bool ok = true;
         do {
             const bool live = t < w.u.rows;
@@ -244,25 +254,25 @@ latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ C
                 continue;
             }
             const bool warp_live = __any_sync(0xffffffffu, live);
-            // Q's four panels in tensor memory: the last unit's accumulator was complete, so its scores were too
-            {
-                if (warp_live) {
-                    const char *from = p.q + out_row * p.q_token + (int64_t)head * p.q_head + half * kHalf * 2;
-                    uint4 v[kQT][8];  // all of it at once: one trip to memory
+            // Q's four panels into tensor memory (the last unit's accumulator was complete, so its scores were too)
+            if (!wait.warp(smem_addr(&aux.q_staged), units & 1)) { ok = false; break; }
+            units++;
+            if (warp_live) {
+#pragma unroll 1
+                for (int q = 0; q < kQT; q++) {
+                    uint32_t x[32];
 #pragma unroll
-                    for (int i = 0; i < 8 * kQT; i++) v[i / 8][i % 8] = *reinterpret_cast<const uint4 *>(from + i * 16);
-#pragma unroll
-                    for (int q = 0; q < kQT; q++) {
-                        uint32_t x[32];
-#pragma unroll
-                        for (int i = 0; i < 8; i++) x[4 * i] = v[q][i].x, x[4 * i + 1] = v[q][i].y, x[4 * i + 2] = v[q][i].z, x[4 * i + 3] = v[q][i].w;
-                        tmem_st32(tmem + kTmQ + q * 32 + mine, x);
+                    for (int i = 0; i < 8; i++) {
+                        const uint4 v = ld_smem16(base + q * kQPanel + panel_off(t, i));
+                        x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
                     }
-                    tc_wait_st();
+                    tmem_st32(tmem + kTmQ + q * 32 + mine, x);
                 }
-                tc_fence_before();
-                warp_arrive(smem_addr(&aux.q_full));
+                tc_wait_st();
             }
+            tc_fence_before();
+            fence_async_smem();  // the loads before the TMA that overwrites what they read
+            warp_arrive(smem_addr(&aux.q_moved));
             int lo, hi;
             sees(b, w.q, tok, lo, hi);
             float m = -INFINITY, l = 0.0f;
@@ -345,9 +355,7 @@ latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ C
                         if (whole) {
                             store_row32<Bf16>(to, f, inv, q * 32, kHalf);
                         } else {
-                            float4 *d = reinterpret_cast<float4 *>(frag + t * kHalf + q * 32);
-#pragma unroll
-                            for (int i = 0; i < 8; i++) d[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                            store_fragment32(frag, kRows, t, q, f);
                         }
                     }
                 }

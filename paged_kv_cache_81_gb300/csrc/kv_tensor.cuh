@@ -277,6 +277,13 @@ __device__ __forceinline__ void weights32(const uint32_t (&x)[32], float c, floa
 // Byte offset of 16-byte chunk c (0 .. 7) of row r in a panel.
 __device__ __forceinline__ uint32_t panel_off(uint32_t r, uint32_t c) { return r * 128u + ((c ^ (r & 7u)) << 4); }
 
+__device__ __forceinline__ uint4 ld_smem16(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ void st_smem16(uint32_t a, const uint4 &v)
 {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
