@@ -430,13 +430,10 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
 #pragma unroll
                         for (int i = 0; i < 32; i++) f[i] = 0.0f;
                     }
-                    if (live) {
-                        if (whole) {
-                            store_row32<Bf16>(to, f, inv, q * 32, p.o.dv);
-                        } else {
-                            store_fragment32(part, kRows, row, q, f);
-                        }
-                    }
+                    if (whole)
+                        store_rows32<Bf16>(live ? to : nullptr, f, inv, q * 32, p.o.dv);
+                    else if (live)
+                        store_fragment32(part, kRows, row, q, f);
                 }
                 if (live) {
                     if (whole) {

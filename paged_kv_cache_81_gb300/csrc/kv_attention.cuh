@@ -129,20 +129,36 @@ __device__ __forceinline__ void store_fragment32(float *part, int rows, int row,
     for (int i = 0; i < 8; i++) __stcg(d + i * rows, make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]));
 }
 
-// 32 accumulator columns of a row to the output, scaled.
+// 32 accumulator columns of every lane's row to global memory, scaled and rounded.  A thread holds a whole
+// row, and 16-byte stores a row apart would each take a cache line to themselves: four lanes first exchange
+// their 16-byte pieces, so that a store instruction writes 64 consecutive bytes of eight rows.  Called by
+// whole warps; `to` is the lane's row, nullptr where there is nothing to write; columns from `end` on do not exist.
 template <bool Bf16>
-__device__ __forceinline__ void store_row32(char *to, const float (&o)[32], float inv, int col, int dv)
+__device__ __forceinline__ void store_rows32(char *to, const float (&o)[32], float inv, int col, int end)
 {
+    const int lane = threadIdx.x & 31, a = lane & 3;
+    uint32_t v[4][4];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        if (col + 8 * i < dv) {
-            uint4 v;
-            v.x = pack2<Bf16>(o[8 * i] * inv, o[8 * i + 1] * inv);
-            v.y = pack2<Bf16>(o[8 * i + 2] * inv, o[8 * i + 3] * inv);
-            v.z = pack2<Bf16>(o[8 * i + 4] * inv, o[8 * i + 5] * inv);
-            v.w = pack2<Bf16>(o[8 * i + 6] * inv, o[8 * i + 7] * inv);
-            *reinterpret_cast<uint4 *>(to + (col + 8 * i) * 2) = v;
-        }
+    for (int i = 0; i < 16; i++) v[i / 4][i % 4] = pack2<Bf16>(o[2 * i] * inv, o[2 * i + 1] * inv);
+#pragma unroll
+    for (int s = 1; s <= 2; s *= 2)  // piece j of lane a's row <-> piece a of lane j's row
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            if (!(j & s))
+#pragma unroll
+                for (int w = 0; w < 4; w++) {
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, a & s ? v[j][w] : v[j | s][w], s);
+                    if (a & s)
+                        v[j][w] = got;
+                    else
+                        v[j | s][w] = got;
+                }
+    const unsigned long long mine = (unsigned long long)to;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        char *row = (char *)__shfl_sync(0xffffffffu, mine, (lane & 28) | j);
+        if (row != nullptr && col + 8 * a < end)
+            *reinterpret_cast<uint4 *>(row + (col + 8 * a) * 2) = make_uint4(v[j][0], v[j][1], v[j][2], v[j][3]);
     }
 }
 

@@ -14,7 +14,7 @@ namespace pkv {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
 constexpr int kTile = 128;
 constexpr int kRank = 512, kRope = 64, kNope = 128, kV = 128, kN = kNope + kV;
 constexpr uint32_t kAPanel = kTile * 128, kBPanel = kN * 128;
@@ -38,7 +38,7 @@ struct Params {
 
 struct Aux {
     uint64_t a_full, a_empty, b_full[kStages], b_empty[kStages], d_full[2], d_empty[2];
-    long long scan[8];
+    long long scan[12];
     int32_t req, tile, head;
     uint32_t tmem;
     int gave_up;
@@ -93,7 +93,7 @@ expand_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__
         mbar_init(smem_addr(&aux.a_full), 1);
         mbar_init(smem_addr(&aux.a_empty), 1);
         for (int i = 0; i < kStages; i++) mbar_init(smem_addr(&aux.b_full[i]), 1), mbar_init(smem_addr(&aux.b_empty[i]), 1);
-        for (int i = 0; i < 2; i++) mbar_init(smem_addr(&aux.d_full[i]), 1), mbar_init(smem_addr(&aux.d_empty[i]), 4);
+        for (int i = 0; i < 2; i++) mbar_init(smem_addr(&aux.d_full[i]), 1), mbar_init(smem_addr(&aux.d_empty[i]), 8);
         mbar_init_fence();
         tma_prefetch_map(&a_map);
         tma_prefetch_map(&w_map);
@@ -177,15 +177,16 @@ expand_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__
             }
         } while (ok && w.next(p));
     } else if (warp >= 4) {
-        const int t = tid & 127;
+        const int g = (warp - 4) >> 2, t = tid & 127;  // group 0 writes the keys, group 1 the values
         const uint32_t mine = (uint32_t)((warp & 3) * 32) << 16;
+        const int row_bytes = (g ? kV : kNope + kRope) * 2;
         int heads = 0;
         bool ok = true;
         do {
             const int tok = w.tile * kTile + t;
             bool live = tok < w.len;
-            char *k = nullptr, *v = nullptr;
-            uint4 rope[kRope / 8];
+            char *to = nullptr;
+            uint4 rope[kRope / 16];
             if (live) {
                 const uint32_t col = fdiv((uint32_t)tok, p.out_block);
                 const int page = __ldg(p.out_table + (int64_t)w.req * p.out_stride + col), slot = tok - (int)(col * p.out_block.d);
@@ -193,42 +194,45 @@ expand_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__
                     set_error(p.err, KV_DERR_TABLE);
                     live = false;  // nowhere to write
                 } else {
-                    k = p.k + page * p.k_block + slot * p.k_token;
-                    v = p.v + page * p.v_block + slot * p.v_token;
+                    to = g ? p.v + page * p.v_block + slot * p.v_token : p.k + page * p.k_block + slot * p.k_token;
                 }
-                const uint32_t scol = fdiv((uint32_t)tok, p.block);
-                const int spage = __ldg(p.table + (int64_t)w.req * p.table_stride + scol), sslot = tok - (int)(scol * p.block.d);
-                const bool good = spage >= 0 && spage < p.num_blocks;
+            }
+            // the rotary parts: eight lanes a row (16 bytes each), four rows at a time, half of the rows a group
+            char *rope_to[kRope / 16];
 #pragma unroll
-                for (int i = 0; i < kRope / 8; i++)
-                    rope[i] = good ? *reinterpret_cast<const uint4 *>(p.rows + spage * p.block_stride + sslot * p.token_stride + kRank * 2 + i * 16)
-                                   : make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < kRope / 16; i++) {
+                const int row = (warp & 3) * 32 + g * 16 + i * 4 + (lane >> 3), rt = w.tile * kTile + row;
+                rope_to[i] = nullptr;
+                if (rt < w.len) {
+                    const uint32_t col = fdiv((uint32_t)rt, p.out_block), scol = fdiv((uint32_t)rt, p.block);
+                    const int page = __ldg(p.out_table + (int64_t)w.req * p.out_stride + col), slot = rt - (int)(col * p.out_block.d);
+                    const int spage = __ldg(p.table + (int64_t)w.req * p.table_stride + scol), sslot = rt - (int)(scol * p.block.d);
+                    if (page >= 0 && page < p.out_blocks) rope_to[i] = p.k + page * p.k_block + slot * p.k_token + kNope * 2 + (lane & 7) * 16;
+                    rope[i] = spage >= 0 && spage < p.num_blocks
+                                  ? *reinterpret_cast<const uint4 *>(p.rows + spage * p.block_stride + sslot * p.token_stride + kRank * 2 + (lane & 7) * 16)
+                                  : make_uint4(0, 0, 0, 0);
+                }
             }
             for (int h = 0; h < w.n; h++, heads++) {
                 const int d = heads & 1, head = w.head + h;
                 if (!wait.warp(smem_addr(&aux.d_full[d]), (heads >> 1) & 1)) { ok = false; break; }
                 tc_fence_after();
 #pragma unroll 1
-                for (int q = 0; q < kN / 32; q++) {
+                for (int q = 0; q < kNope / 32; q++) {
                     uint32_t x[32];
-                    tmem_ld32(tmem + d * kN + q * 32 + mine, x);
+                    tmem_ld32(tmem + d * kN + g * kNope + q * 32 + mine, x);
                     tc_wait_ld();
                     float f[32];
 #pragma unroll
                     for (int i = 0; i < 32; i++) f[i] = __uint_as_float(x[i]);
-                    if (live) {
-                        if (q < 4)
-                            store_row32<Bf16>(k + head * (kNope + kRope) * 2, f, 1.0f, q * 32, kNope);
-                        else
-                            store_row32<Bf16>(v + head * kV * 2, f, 1.0f, q * 32 - kNope, kV);
-                    }
+                    // a warp group takes the keys, the other the values
+                    store_rows32<Bf16>(live ? to + head * row_bytes : nullptr, f, 1.0f, q * 32, kNope);
                 }
                 tc_fence_before();
                 warp_arrive(smem_addr(&aux.d_empty[d]));
-                if (live) {
 #pragma unroll
-                    for (int i = 0; i < kRope / 8; i++) *reinterpret_cast<uint4 *>(k + (head * (kNope + kRope) + kNope + i * 8) * 2) = rope[i];
-                }
+                for (int i = 0; i < kRope / 16; i++)
+                    if (rope_to[i] != nullptr) *reinterpret_cast<uint4 *>(rope_to[i] + head * (kNope + kRope) * 2) = rope[i];
             }
         } while (ok && w.next(p));
     }

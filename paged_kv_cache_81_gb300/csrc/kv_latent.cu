@@ -351,13 +351,10 @@ latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ C
                     float f[32];
 #pragma unroll
                     for (int i = 0; i < 32; i++) f[i] = l == 0.0f ? 0.0f : __uint_as_float(o[i]);
-                    if (live) {
-                        if (whole) {
-                            store_row32<Bf16>(to, f, inv, q * 32, kHalf);
-                        } else {
-                            store_fragment32(frag, kRows, t, q, f);
-                        }
-                    }
+                    if (whole)
+                        store_rows32<Bf16>(live ? to : nullptr, f, inv, q * 32, kHalf);
+                    else if (live)
+                        store_fragment32(frag, kRows, t, q, f);
                 }
                 if (live) {
                     if (whole) {

@@ -9,7 +9,8 @@
 // (token, head of the group) rows; a CTA takes an equal piece of it, and a key tile that was cut is summed
 // from its pieces' partial sums, in their order, by whichever CTA finishes the last of them.
 //   warp 0 loads (K once a head, Q a step), warp 1 issues the products, warps 4-7 and 8-11 take the even
-//   and the odd steps; warps 2 and 3 carry over what lies past the requests' lengths.
+//   and the odd steps; warp 3 stages the rows' normalisers, warp 2 carries over what lies past the requests'
+//   lengths.
 #include "kv_attention.cuh"
 
 namespace pkv {
@@ -28,7 +29,7 @@ template <int DK>
 struct Shape {
     static constexpr uint32_t kOperand = 128 * DK * 2;
     static constexpr int kNK = DK == 192 ? 2 : 3, kNQ = kNK;
-    static constexpr uint32_t kOffQ = kNK * kOperand, kOffAux = kOffQ + kNQ * kOperand, kBytes = kOffAux + 3072;
+    static constexpr uint32_t kOffQ = kNK * kOperand, kOffAux = kOffQ + kNQ * kOperand, kBytes = kOffAux + 4096;
 };
 
 struct Params {
@@ -51,16 +52,16 @@ struct Params {
 };
 
 struct Aux {
-    uint64_t k_full[3], k_empty[3], q_full[3], q_empty[3], s_full[2], s_empty[2], l_ready[2], sum_ready, sum_free, join;
+    uint64_t k_full[3], k_empty[3], q_full[3], q_empty[3], s_full[2], s_empty[2], l_full[4], l_empty[4], sum_ready, sum_free, join;
     long long scan[12];
     Place place;
-    alignas(16) float neg[2][128];  // read four at a time: -lse log2 e of a step's rows
+    alignas(16) float neg[4][128];  // read four at a time: -lse log2 e of a step's rows
     float odd[128];     // the odd steps' sums
     uint32_t tmem;
     int answer;
     int gave_up;
 };
-static_assert(sizeof(Aux) <= 3072, "bookkeeping");
+static_assert(sizeof(Aux) <= 4096, "bookkeeping");
 
 // The steps of one key tile: a key head's query rows, in steps of step_tokens tokens.
 struct KeyTile {
@@ -162,8 +163,8 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
         for (int i = 0; i < 2; i++) {
             mbar_init(smem_addr(&aux.s_full[i]), 1);
             mbar_init(smem_addr(&aux.s_empty[i]), 4);
-            mbar_init(smem_addr(&aux.l_ready[i]), 4);
         }
+        for (int i = 0; i < 4; i++) mbar_init(smem_addr(&aux.l_full[i]), 1), mbar_init(smem_addr(&aux.l_empty[i]), 4);
         mbar_init(smem_addr(&aux.sum_ready), 4);
         mbar_init(smem_addr(&aux.sum_free), 4);
         mbar_init(smem_addr(&aux.join), 4);
@@ -201,9 +202,9 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, aux.tmem, 0);
     Walk2 w;
-    if (warp == 2 || warp == 3) {
+    if (warp == 2) {
         // what lies past every request's length is carried over
-        const int me = blockIdx.x * 64 + (tid & 63), all = gridDim.x * 64;
+        const int me = blockIdx.x * 32 + lane, all = gridDim.x * 32;
         for (int r = 0; r < b.n_reqs; r++) {
             const int len = min(max(__ldg(b.kv_lens + r), 0), b.max_tokens);
             for (int j = len + me; j < p.width; j += all)
@@ -253,6 +254,30 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
                 __syncwarp();
             }
         } while (ok && w.next(p));
+    } else if (warp == 3) {
+        // ---- the rows' normalisers, four steps ahead ----
+        int it = 0;
+        bool ok = true;
+        do {
+            if (w.k.per_head == 0) continue;
+            const int tok_first = w.q.q0 + w.k.t0, ntok = w.k.t1 - w.k.t0;
+            int head = w.at.off / w.k.per_head, qi = w.at.off - head * w.k.per_head;
+            for (int i = 0; ok && i < w.n; i++, it++) {
+                const int tok0 = qi * p.step_tokens, cols = min(p.step_tokens, ntok - tok0) * group, s = it & 3;
+                float v[4];
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const int c = j * 32 + lane, tt = (int)fdiv((uint32_t)c, b.group);
+                    v[j] = c < cols ? -p.lse[(int64_t)(tok_first + tok0 + tt) * p.heads + head * group + c - tt * group] * kLog2e : -INFINITY;
+                    if (v[j] == INFINITY) v[j] = -INFINITY;  // a row that saw nothing weighs nothing
+                }
+                if (it >= 4 && !(ok = wait.warp(smem_addr(&aux.l_empty[s]), ((it >> 2) - 1) & 1))) break;
+#pragma unroll
+                for (int j = 0; j < 4; j++) aux.neg[s][j * 32 + lane] = v[j];
+                warp_arrive(smem_addr(&aux.l_full[s]));
+                if (++qi == w.k.per_head) qi = 0, head++;
+            }
+        } while (ok && w.next(p));
     } else if (warp == 1) {
         const uint32_t desc = mma_desc(Bf16, 128, (uint32_t)((p.step_tokens * group + 15) / 16 * 16), false);
         const uint32_t elected = elect_one();
@@ -293,46 +318,48 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
             const int key = w.at.unit * kTile + t;
             float sum = 0.0f;
             if (w.k.per_head) {
-                const int kt0 = w.q.q0 + w.k.t0, ntok = w.k.t1 - w.k.t0, base_pos = w.q.len - w.q.q_len + w.k.t0;
+                const int ntok = w.k.t1 - w.k.t0, base_pos = w.q.len - w.q.q_len + w.k.t0;
                 // tokens (counted from t0) that see this key: [va, vb)
                 const int va = b.causal ? max(0, key - base_pos) : 0, vb = key >= w.q.len ? 0 : b.window ? min(ntok, max(0, key + b.window - base_pos)) : ntok;
                 for (int i = 0; i < w.n; i++, it++) {
                     if ((it & 1) != g) continue;
-                    const int step = w.at.off + i, head = step / w.k.per_head, tok0 = (step - head * w.k.per_head) * p.step_tokens;
+                    const int step = w.at.off + i, tok0 = step % w.k.per_head * p.step_tokens;
                     const int cols = min(p.step_tokens, ntok - tok0) * group;
-                    float v = -INFINITY;
-                    if (t < cols) {
-                        const int tt = (int)fdiv((uint32_t)t, b.group);
-                        v = -p.lse[(int64_t)(kt0 + tok0 + tt) * p.heads + head * group + t - tt * group] * kLog2e;
-                        if (v == INFINITY) v = -INFINITY;  // a row that saw nothing weighs nothing
-                    }
-                    // these scores are out, so the whole group has done with the previous step's row of `neg`
-                    if (!wait.warp(smem_addr(&aux.s_full[g]), mine & 1)) { ok = false; break; }
-                    aux.neg[g][t] = v;
-                    warp_arrive(smem_addr(&aux.l_ready[g]));
-                    if (!wait.warp(smem_addr(&aux.l_ready[g]), mine & 1)) { ok = false; break; }
+                    if (!wait.warp(smem_addr(&aux.l_full[it & 3]), (it >> 2) & 1) || !wait.warp(smem_addr(&aux.s_full[g]), mine & 1)) { ok = false; break; }
                     tc_fence_after();
                     const int c0 = (va - tok0) * group, c1 = min(cols, (vb - tok0) * group);
-                    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 1
-                    for (int q = 0; q < cols; q += 32) {
-                        uint32_t x[32];
-                        tmem_ld32(s_at + q, x);
-                        tc_wait_ld();
-                        const float4 *neg = reinterpret_cast<const float4 *>(&aux.neg[g][q]);
+                    float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                    const auto add = [&](uint32_t(&x)[32], int q) {
+                        const float4 *neg = reinterpret_cast<const float4 *>(&aux.neg[it & 3][q]);
                         if (__any_sync(0xffffffffu, c0 > q || c1 < q + 32)) hide32(x, c0 - q, c1 - q);
+                        const float2 cc = make_float2(p.c, p.c);
 #pragma unroll
                         for (int j = 0; j < 8; j++) {
-                            const float4 e = neg[j];
-                            part[0] += exp2_fast(fmaf(__uint_as_float(x[4 * j]), p.c, e.x));
-                            part[1] += exp2_fast(fmaf(__uint_as_float(x[4 * j + 1]), p.c, e.y));
-                            part[2] += exp2_fast(fmaf(__uint_as_float(x[4 * j + 2]), p.c, e.z));
-                            part[3] += exp2_fast(fmaf(__uint_as_float(x[4 * j + 3]), p.c, e.w));
+                            const float4 n = neg[j];
+                            float2 e = fma2(make_float2(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1])), cc, make_float2(n.x, n.y));
+                            float2 f = fma2(make_float2(__uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3])), cc, make_float2(n.z, n.w));
+                            e.x = exp2_fast(e.x), e.y = exp2_fast(e.y), f.x = exp2_fast(f.x), f.y = exp2_fast(f.y);
+                            part[0] = add2(part[0], e);
+                            part[1] = add2(part[1], f);
                         }
+                    };
+                    // 32 columns are read while 32 are added
+                    uint32_t x0[32], x1[32];
+                    tmem_ld32(s_at, x0);
+                    tc_wait_ld();
+#pragma unroll 1
+                    for (int q = 0; q < cols; q += 64) {
+                        tmem_ld32(s_at + q + 32, x1);
+                        add(x0, q);
+                        tc_wait_ld();
+                        if (q + 64 < cols) tmem_ld32(s_at + q + 64, x0);
+                        if (q + 32 < cols) add(x1, q + 32);
+                        tc_wait_ld();
                     }
-                    sum += (part[0] + part[1]) + (part[2] + part[3]);
+                    sum += (part[0].x + part[0].y) + (part[1].x + part[1].y);
                     tc_fence_before();
                     warp_arrive(smem_addr(&aux.s_empty[g]));
+                    if (lane == 0) mbar_arrive(smem_addr(&aux.l_empty[it & 3]));
                     mine++;
                 }
                 if (!ok) break;
