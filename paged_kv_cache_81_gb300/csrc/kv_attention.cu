@@ -531,6 +531,13 @@ int check_plane(const kv_cache_desc *c, int tensor, int plane, int heads, int di
     return KV_OK;
 }
 
+int box_tokens(int most, const kv_attn_batch *t)
+{
+    int n = 1;
+    while (n < most && (most % n || (int64_t)n * t->n_reqs < t->n_tokens)) n++;
+    return n;
+}
+
 int make_q_map(CUtensorMap *map, const void *q, int64_t token_stride, int64_t head_stride, int head_dim, int heads, int64_t tokens, int group,
                int box_tokens)
 {
@@ -621,11 +628,7 @@ int kv_attention(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_cac
     p.o = Output{(char *)out, out_token_stride, out_head_stride, lse, d->n_heads, d->head_dim_v, d->scale, d->scale * kLog2e};
     p.counters = (int *)workspace;
     p.ws = (float *)((char *)workspace + kCounterBytes);
-    // a box of q: the smallest divisor of a softmax group's tokens that holds a request's on average (a
-    // divisor, so that the last box of a half ends with it)
-    const int per_half = 128 / group;
-    for (p.q_box = 1; p.q_box < per_half; p.q_box++)
-        if (per_half % p.q_box == 0 && (int64_t)p.q_box * batch->n_reqs >= batch->n_tokens) break;
+    p.q_box = box_tokens(128 / group, batch);
     CUtensorMap qm, km, vm;
     if ((st = make_q_map(&qm, q, q_token_stride, q_head_stride, d->head_dim, d->n_heads, batch->n_tokens, group, p.q_box)) != KV_OK) return st;
     if ((st = make_cache_map(&km, k, k_tensor, k_plane, d->n_kv_heads, d->head_dim, p.piece_rows)) != KV_OK) return st;

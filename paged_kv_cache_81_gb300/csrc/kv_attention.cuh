@@ -19,6 +19,10 @@ int check_batch(const kv_attn_batch *t);
 int fill_batch(Batch *b, const kv_attn_batch *t, int heads, int kv_heads, int block_size, int unit_rows, int tile, int causal, int window);
 int check_plane(const kv_cache_desc *c, int tensor, int plane, int heads, int dim);
 int check_rows(const void *p, int64_t token_stride, int64_t head_stride);
+// Tokens of a TMA of q: the smallest divisor of `most` (a group's tokens in 128 rows) that holds a request's
+// new tokens on average, so that decoding brings no other request's rows and a chunk takes few boxes; a
+// divisor, so that the last box of 128 rows ends with them.
+int box_tokens(int most, const kv_attn_batch *t);
 // A map of q [tokens, heads, head_dim]; a load brings 64 elements of `group` heads of box_tokens tokens.
 int make_q_map(CUtensorMap *map, const void *q, int64_t token_stride, int64_t head_stride, int head_dim, int heads, int64_t tokens, int group,
                int box_tokens);

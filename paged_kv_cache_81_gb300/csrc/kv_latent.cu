@@ -420,9 +420,7 @@ extern "C" int kv_latent_attention(const kv_attn_desc *d, const kv_attn_batch *b
     if (d->n_heads > kRows) {
         for (box_heads = kRows; d->n_heads % box_heads; box_heads--) {}
     } else {
-        const int tokens = kRows / d->n_heads;
-        for (; box_tokens < tokens; box_tokens++)
-            if (tokens % box_tokens == 0 && (int64_t)box_tokens * batch->n_reqs >= batch->n_tokens) break;
+        box_tokens = pkv::box_tokens(kRows / d->n_heads, batch);
     }
     const int unit_rows = d->n_heads > kRows ? box_heads : kRows / d->n_heads * d->n_heads;
     Params p = {};

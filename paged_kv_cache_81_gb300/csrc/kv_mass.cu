@@ -8,7 +8,8 @@
 // The line (as in kv_plan.cuh) runs over requests, tiles of 128 keys, key heads and tiles of up to 128
 // (token, head of the group) rows; a CTA takes an equal piece of it, and a key tile that was cut is summed
 // from its pieces' partial sums, in their order, by whichever CTA finishes the last of them.
-//   warp 0 loads (K once a head, Q a step), warp 1 issues the products, warps 4-7 and 8-11 take the even
+//   warp 0 loads (K once a head, Q a step), warp 1 issues the products into four accumulators (all of
+//   tensor memory: the exponentials take longer than the products), warps 4-7 and 8-11 take the even
 //   and the odd steps; warp 3 stages the rows' normalisers, warp 2 carries over what lies past the requests'
 //   lengths.
 #include "kv_attention.cuh"
@@ -40,6 +41,7 @@ struct Params {
     FastDiv block;
     int32_t piece_rows, dk, heads;
     int32_t step_tokens;  // tokens of one step: 128 / group
+    int32_t q_box;        // tokens one TMA brings of q, a divisor of step_tokens
     float c;
     const float *lse;
     const float *prev;
@@ -52,7 +54,7 @@ struct Params {
 };
 
 struct Aux {
-    uint64_t k_full[3], k_empty[3], q_full[3], q_empty[3], s_full[2], s_empty[2], l_full[4], l_empty[4], sum_ready, sum_free, join;
+    uint64_t k_full[3], k_empty[3], q_full[3], q_empty[3], s_full[4], s_empty[4], l_full[4], sum_ready, sum_free, join;
     long long scan[12];
     Place place;
     alignas(16) float neg[4][128];  // read four at a time: -lse log2 e of a step's rows
@@ -160,11 +162,11 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
             mbar_init(smem_addr(&aux.q_full[i]), 1);
             mbar_init(smem_addr(&aux.q_empty[i]), 1);
         }
-        for (int i = 0; i < 2; i++) {
+        for (int i = 0; i < 4; i++) {
             mbar_init(smem_addr(&aux.s_full[i]), 1);
             mbar_init(smem_addr(&aux.s_empty[i]), 4);
+            mbar_init(smem_addr(&aux.l_full[i]), 1);
         }
-        for (int i = 0; i < 4; i++) mbar_init(smem_addr(&aux.l_full[i]), 1), mbar_init(smem_addr(&aux.l_empty[i]), 4);
         mbar_init(smem_addr(&aux.sum_ready), 4);
         mbar_init(smem_addr(&aux.sum_free), 4);
         mbar_init(smem_addr(&aux.join), 4);
@@ -172,7 +174,7 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
         tma_prefetch_map(&k_map);
         tma_prefetch_map(&q_map);
     }
-    if (warp == 2) tmem_alloc(smem_addr(&aux.tmem), 256);
+    if (warp == 2) tmem_alloc(smem_addr(&aux.tmem), 512);
     grid_dep_entry();
     const Line line = find_piece<kThreads>(
         b.n_reqs, blockIdx.x, gridDim.x, kLeast, aux.scan,
@@ -220,38 +222,48 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
             if (w.k.per_head == 0) continue;
             const int kb = w.at.unit * kTile, p0 = max(0, w.k.lo - kb) / pr, p1 = (min(w.q.len - kb, kTile) + pr - 1) / pr;
             const int32_t *row = p.table + (int64_t)w.at.req * p.table_stride;
+            int page = 0, slot = 0;
+            const auto find = [&](int j) {
+                const uint32_t key = (uint32_t)(kb + j * pr), col = fdiv(key, p.block);
+                slot = (int)(key - col * p.block.d);
+                page = __ldg(row + col);
+                if (page < 0 || page >= p.num_blocks) {
+                    set_error(b.err, KV_DERR_TABLE);
+                    page = p.num_blocks;  // outside the map: reads zeros
+                }
+            };
+            if (p0 + lane < p1) find(p0 + lane);  // this lane's first page, the same for every head
+            const int page0 = page, slot0 = slot;
+            int head = w.at.off / w.k.per_head, qi = w.at.off - head * w.k.per_head;
             for (int i = 0; ok && i < w.n; i++, it++) {
-                const int step = w.at.off + i, head = step / w.k.per_head, qi = step - head * w.k.per_head;
                 if (i == 0 || qi == 0) {
                     const int s = kt % S::kNK;
                     const uint32_t bar = smem_addr(&aux.k_full[s]);
                     if (kt >= S::kNK && !wait.warp(smem_addr(&aux.k_empty[s]), ((kt / S::kNK) - 1) & 1)) { ok = false; break; }
                     if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)((p1 - p0) * pr) * DK * 2);
                     __syncwarp();
+                    page = page0, slot = slot0;
                     for (int j = p0 + lane; j < p1; j += 32) {
-                        const uint32_t key = (uint32_t)(kb + j * pr), col = fdiv(key, p.block);
-                        int page = __ldg(row + col);
-                        if (page < 0 || page >= p.num_blocks) {
-                            set_error(b.err, KV_DERR_TABLE);
-                            page = p.num_blocks;  // outside the map: reads zeros
-                        }
+                        if (j >= p0 + 32) find(j);
 #pragma unroll
                         for (int h = 0; h < DK / 64; h++)
-                            tma_load_4d(base + s * S::kOperand + h * kPanel + j * pr * 128, &k_map, bar, h * 64, head, (int)(key - col * p.block.d), page);
+                            tma_load_4d(base + s * S::kOperand + h * kPanel + j * pr * 128, &k_map, bar, h * 64, head, slot, page);
                     }
                     kt++;
                 }
-                const int s = it % S::kNQ;
+                const int s = it % S::kNQ, tok0 = qi * p.step_tokens, toks = min(p.step_tokens, w.k.t1 - w.k.t0 - tok0);
                 if (it >= S::kNQ && !wait.warp(smem_addr(&aux.q_empty[s]), ((it / S::kNQ) - 1) & 1)) { ok = false; break; }
-                if (lane == 0) {
-                    const uint32_t bar = smem_addr(&aux.q_full[s]);
-                    mbar_arrive_expect_tx(bar, (uint32_t)(p.step_tokens * group) * DK * 2);
+                const uint32_t bar = smem_addr(&aux.q_full[s]);
+                const int boxes = (toks + p.q_box - 1) / p.q_box;
+                if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * p.q_box * group) * DK * 2);
+                __syncwarp();
+                for (int j = lane; j < boxes; j += 32)
 #pragma unroll
                     for (int h = 0; h < DK / 64; h++)
-                        tma_load_3d(base + S::kOffQ + s * S::kOperand + h * kPanel, &q_map, bar, h * 64, head * group,
-                                    w.q.q0 + w.k.t0 + qi * p.step_tokens);
-                }
+                        tma_load_3d(base + S::kOffQ + s * S::kOperand + h * kPanel + j * p.q_box * group * 128, &q_map, bar, h * 64, head * group,
+                                    w.q.q0 + w.k.t0 + tok0 + j * p.q_box);
                 __syncwarp();
+                if (++qi == w.k.per_head) qi = 0, head++;
             }
         } while (ok && w.next(p));
     } else if (warp == 3) {
@@ -271,7 +283,7 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
                     v[j] = c < cols ? -p.lse[(int64_t)(tok_first + tok0 + tt) * p.heads + head * group + c - tt * group] * kLog2e : -INFINITY;
                     if (v[j] == INFINITY) v[j] = -INFINITY;  // a row that saw nothing weighs nothing
                 }
-                if (it >= 4 && !(ok = wait.warp(smem_addr(&aux.l_empty[s]), ((it >> 2) - 1) & 1))) break;
+                if (it >= 4 && !(ok = wait.warp(smem_addr(&aux.s_empty[s]), ((it >> 2) - 1) & 1))) break;
 #pragma unroll
                 for (int j = 0; j < 4; j++) aux.neg[s][j * 32 + lane] = v[j];
                 warp_arrive(smem_addr(&aux.l_full[s]));
@@ -279,7 +291,6 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
             }
         } while (ok && w.next(p));
     } else if (warp == 1) {
-        const uint32_t desc = mma_desc(Bf16, 128, (uint32_t)((p.step_tokens * group + 15) / 16 * 16), false);
         const uint32_t elected = elect_one();
         const uint64_t kd = smem_desc(base, 16, 1024), qd = smem_desc(base + S::kOffQ, 16, 1024);
         int kt = -1, it = 0;
@@ -288,31 +299,33 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
             if (w.k.per_head == 0) continue;
             int qi = w.at.off % w.k.per_head;
             for (int i = 0; ok && i < w.n; i++, it++) {
-                const int g = it & 1, s = it % S::kNQ;
+                const int s = it % S::kNQ;
+                const int rows = min(p.step_tokens, w.k.t1 - w.k.t0 - qi * p.step_tokens) * group;
+                const uint32_t desc = mma_desc(Bf16, 128, (uint32_t)(rows + 15) & ~15u, false);
                 if (i == 0 || qi == 0) {
                     kt++;
                     ok = wait.warp(smem_addr(&aux.k_full[kt % S::kNK]), (kt / S::kNK) & 1);
                 }
                 ok = ok && wait.warp(smem_addr(&aux.q_full[s]), (it / S::kNQ) & 1) &&
-                     (it < 2 || wait.warp(smem_addr(&aux.s_empty[g]), ((it >> 1) - 1) & 1));
+                     (it < 4 || wait.warp(smem_addr(&aux.s_empty[it & 3]), ((it >> 2) - 1) & 1));
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t ka = kd + (kt % S::kNK) * (S::kOperand >> 4), qa = qd + s * (S::kOperand >> 4);
 #pragma unroll
                 for (int kk = 0; kk < DK / 16; kk++) {
                     const uint32_t o = ((kk / 4) * kPanel + (kk % 4) * 32) >> 4;
-                    mma_ss(tmem + g * 128, ka + o, qa + o, desc, kk > 0, elected);
+                    mma_ss(tmem + (it & 3) * 128, ka + o, qa + o, desc, kk > 0, elected);
                 }
                 tc_commit(smem_addr(&aux.q_empty[s]), elected);
                 if (++qi == w.k.per_head) qi = 0;
                 if (i + 1 == w.n || qi == 0) tc_commit(smem_addr(&aux.k_empty[kt % S::kNK]), elected);
-                tc_commit(smem_addr(&aux.s_full[g]), elected);  // last: the groups wait for it before the CTA ends
+                tc_commit(smem_addr(&aux.s_full[it & 3]), elected);  // last: the groups wait for it before the CTA ends
             }
         } while (ok && w.next(p));
     } else if (warp >= 4) {
         const int g = (warp - 4) >> 2, t = tid & 127;
-        const uint32_t s_at = tmem + g * 128 + ((uint32_t)((warp & 3) * 32) << 16);
-        int it = 0, mine = 0, tiles = 0, cuts = 0;
+        const uint32_t mine = (uint32_t)((warp & 3) * 32) << 16;
+        int it = 0, tiles = 0, cuts = 0;
         bool ok = true;
         do {
             const int key = w.at.unit * kTile + t;
@@ -321,11 +334,14 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
                 const int ntok = w.k.t1 - w.k.t0, base_pos = w.q.len - w.q.q_len + w.k.t0;
                 // tokens (counted from t0) that see this key: [va, vb)
                 const int va = b.causal ? max(0, key - base_pos) : 0, vb = key >= w.q.len ? 0 : b.window ? min(ntok, max(0, key + b.window - base_pos)) : ntok;
+                int qi = w.at.off % w.k.per_head - 1;
                 for (int i = 0; i < w.n; i++, it++) {
+                    if (++qi == w.k.per_head) qi = 0;
                     if ((it & 1) != g) continue;
-                    const int step = w.at.off + i, tok0 = step % w.k.per_head * p.step_tokens;
+                    const int tok0 = qi * p.step_tokens;
+                    const uint32_t s_at = tmem + (it & 3) * 128 + mine;
                     const int cols = min(p.step_tokens, ntok - tok0) * group;
-                    if (!wait.warp(smem_addr(&aux.l_full[it & 3]), (it >> 2) & 1) || !wait.warp(smem_addr(&aux.s_full[g]), mine & 1)) { ok = false; break; }
+                    if (!wait.warp(smem_addr(&aux.l_full[it & 3]), (it >> 2) & 1) || !wait.warp(smem_addr(&aux.s_full[it & 3]), (it >> 2) & 1)) { ok = false; break; }
                     tc_fence_after();
                     const int c0 = (va - tok0) * group, c1 = min(cols, (vb - tok0) * group);
                     float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
@@ -358,9 +374,7 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
                     }
                     sum += (part[0].x + part[0].y) + (part[1].x + part[1].y);
                     tc_fence_before();
-                    warp_arrive(smem_addr(&aux.s_empty[g]));
-                    if (lane == 0) mbar_arrive(smem_addr(&aux.l_empty[it & 3]));
-                    mine++;
+                    warp_arrive(smem_addr(&aux.s_empty[it & 3]));
                 }
                 if (!ok) break;
             }
@@ -400,7 +414,7 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
         const unsigned long long t0 = now_ns();
         while (now_ns() - t0 < 10000000ull) {}
     }
-    if (warp == 2) tmem_free(tmem, 256);
+    if (warp == 2) tmem_free(tmem, 512);
 }
 
 template <int DK, bool Bf16>
@@ -488,7 +502,7 @@ int kv_attention_mass(const kv_attn_desc *d, const kv_attn_batch *batch, const k
     p.heads = d->n_heads;
     const int group = d->n_heads / d->n_kv_heads;
     p.step_tokens = 128 / group;
-    if (batch->n_tokens > 0 && p.step_tokens > batch->n_tokens) p.step_tokens = (int32_t)batch->n_tokens;
+    p.q_box = box_tokens(p.step_tokens, batch);
     p.c = d->scale * kLog2e;
     p.lse = lse;
     p.prev = prev;
@@ -501,7 +515,7 @@ int kv_attention_mass(const kv_attn_desc *d, const kv_attn_batch *batch, const k
     CUtensorMap km, qm;
     if ((st = make_cache_map(&km, k, k_tensor, k_plane, d->n_kv_heads, d->head_dim, p.piece_rows)) != KV_OK) return st;
     if (batch->n_tokens > 0) {
-        if ((st = make_q_map(&qm, q, q_token_stride, q_head_stride, d->head_dim, d->n_heads, batch->n_tokens, group, p.step_tokens)) != KV_OK)
+        if ((st = make_q_map(&qm, q, q_token_stride, q_head_stride, d->head_dim, d->n_heads, batch->n_tokens, group, p.q_box)) != KV_OK)
             return st;
     } else {
         qm = km;  // never used: no request has new tokens
