@@ -8,10 +8,10 @@
 // The line (as in kv_plan.cuh) runs over requests, tiles of 128 keys, key heads and tiles of up to 128
 // (token, head of the group) rows; a CTA takes an equal piece of it, and a key tile that was cut is summed
 // from its pieces' partial sums, in their order, by whichever CTA finishes the last of them.
-//   warp 0 loads (K once a head, Q a step), warp 1 issues the products into four accumulators (all of
-//   tensor memory: the exponentials take longer than the products), warps 4-7 and 8-11 take the even
-//   and the odd steps; warp 3 stages the rows' normalisers, warp 2 carries over what lies past the requests'
-//   lengths.
+//   warps 0 and 2 load K once a head, warp 3 Q and warps 12 and 13 its rows' normalisers a step, warp 1
+//   issues the products into four accumulators (all of tensor memory: the exponentials take longer than
+//   the products), warps 4-7 and 8-11 take the even and the odd steps.  Warp 2 first carries over what
+//   lies past the lengths.
 #include "kv_attention.cuh"
 
 namespace pkv {
@@ -22,15 +22,15 @@ namespace {
 #define KL 2
 #endif
 constexpr int kLeast = KL;  // steps of a piece, at least
-constexpr int kThreads = 384;
+constexpr int kThreads = 448;
 constexpr int kTile = 128;
 constexpr uint32_t kPanel = 128 * 128;
 
 template <int DK>
 struct Shape {
     static constexpr uint32_t kOperand = 128 * DK * 2;
-    static constexpr int kNK = DK == 192 ? 2 : 3, kNQ = kNK;
-    static constexpr uint32_t kOffQ = kNK * kOperand, kOffAux = kOffQ + kNQ * kOperand, kBytes = kOffAux + 4096;
+    static constexpr int kNK = DK == 64 ? 8 : DK == 128 ? 4 : 2, kNQ = DK == 64 ? 4 : DK == 128 ? 3 : 2;  // what 227 KB holds
+    static constexpr uint32_t kOffQ = kNK * kOperand, kOffAux = kOffQ + kNQ * kOperand, kBytes = kOffAux + 3072;
 };
 
 struct Params {
@@ -54,8 +54,8 @@ struct Params {
 };
 
 struct Aux {
-    uint64_t k_full[3], k_empty[3], q_full[3], q_empty[3], s_full[4], s_empty[4], l_full[4], sum_ready, sum_free, join;
-    long long scan[12];
+    uint64_t k_full[8], k_empty[8], q_full[4], q_empty[4], s_full[4], s_empty[4], l_full[4], sum_ready, sum_free, join;
+    long long scan[14];
     Place place;
     alignas(16) float neg[4][128];  // read four at a time: -lse log2 e of a step's rows
     float odd[128];     // the odd steps' sums
@@ -63,7 +63,7 @@ struct Aux {
     int answer;
     int gave_up;
 };
-static_assert(sizeof(Aux) <= 4096, "bookkeeping");
+static_assert(sizeof(Aux) <= 3072, "bookkeeping");
 
 // The steps of one key tile: a key head's query rows, in steps of step_tokens tokens.
 struct KeyTile {
@@ -156,12 +156,8 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
 
     if (tid == 0) {
         aux.gave_up = 0;
-        for (int i = 0; i < 3; i++) {
-            mbar_init(smem_addr(&aux.k_full[i]), 1);
-            mbar_init(smem_addr(&aux.k_empty[i]), 1);
-            mbar_init(smem_addr(&aux.q_full[i]), 1);
-            mbar_init(smem_addr(&aux.q_empty[i]), 1);
-        }
+        for (int i = 0; i < S::kNK; i++) mbar_init(smem_addr(&aux.k_full[i]), 2), mbar_init(smem_addr(&aux.k_empty[i]), 1);
+        for (int i = 0; i < S::kNQ; i++) mbar_init(smem_addr(&aux.q_full[i]), 1), mbar_init(smem_addr(&aux.q_empty[i]), 1);
         for (int i = 0; i < 4; i++) {
             mbar_init(smem_addr(&aux.s_full[i]), 1);
             mbar_init(smem_addr(&aux.s_empty[i]), 4);
@@ -203,7 +199,6 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, aux.tmem, 0);
-    Walk2 w;
     if (warp == 2) {
         // what lies past every request's length is carried over
         const int me = blockIdx.x * 32 + lane, all = gridDim.x * 32;
@@ -212,11 +207,15 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
             for (int j = len + me; j < p.width; j += all)
                 p.score[(int64_t)r * p.score_stride + j] = p.prev ? p.prev[(int64_t)r * p.prev_stride + j] : 0.0f;
         }
-    } else if (!w.start(p, aux.place, line)) {
+    }
+    Walk2 w;
+    if (!w.start(p, aux.place, line)) {
         // nothing to do: on to the common exit
-    } else if (warp == 0) {
-        const int pr = p.piece_rows;
-        int kt = 0, it = 0;
+    } else if (warp == 0 || warp == 2) {
+        // ---- keys: the two warps take every other page piece (one warp issues a TMA in about 140 cycles, which
+        // for pages of 16 slots held the whole kernel to 60% of the memory's rate) ----
+        const int pr = p.piece_rows, mine = warp >> 1;
+        int kt = 0;
         bool ok = true;
         do {
             if (w.k.per_head == 0) continue;
@@ -232,27 +231,37 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
                     page = p.num_blocks;  // outside the map: reads zeros
                 }
             };
-            if (p0 + lane < p1) find(p0 + lane);  // this lane's first page, the same for every head
+            const int first = p0 + mine + 2 * lane, count = (p1 - p0 - mine + 1) / 2;
+            if (first < p1) find(first);  // this lane's first page, the same for every head
             const int page0 = page, slot0 = slot;
-            int head = w.at.off / w.k.per_head, qi = w.at.off - head * w.k.per_head;
-            for (int i = 0; ok && i < w.n; i++, it++) {
-                if (i == 0 || qi == 0) {
-                    const int s = kt % S::kNK;
-                    const uint32_t bar = smem_addr(&aux.k_full[s]);
-                    if (kt >= S::kNK && !wait.warp(smem_addr(&aux.k_empty[s]), ((kt / S::kNK) - 1) & 1)) { ok = false; break; }
-                    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)((p1 - p0) * pr) * DK * 2);
-                    __syncwarp();
-                    page = page0, slot = slot0;
-                    for (int j = p0 + lane; j < p1; j += 32) {
-                        if (j >= p0 + 32) find(j);
+            const int head0 = w.at.off / w.k.per_head, head1 = (w.at.off + w.n - 1) / w.k.per_head;
+            for (int head = head0; head <= head1; head++, kt++) {
+                const int s = kt % S::kNK;
+                const uint32_t bar = smem_addr(&aux.k_full[s]);
+                if (kt >= S::kNK && !wait.warp(smem_addr(&aux.k_empty[s]), ((kt / S::kNK) - 1) & 1)) { ok = false; break; }
+                if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(count * pr) * DK * 2);
+                __syncwarp();
+                page = page0, slot = slot0;
+                for (int j = first; j < p1; j += 64) {
+                    if (j >= p0 + 64) find(j);
 #pragma unroll
-                        for (int h = 0; h < DK / 64; h++)
-                            tma_load_4d(base + s * S::kOperand + h * kPanel + j * pr * 128, &k_map, bar, h * 64, head, slot, page);
-                    }
-                    kt++;
+                    for (int h = 0; h < DK / 64; h++)
+                        tma_load_4d(base + s * S::kOperand + h * kPanel + j * pr * 128, &k_map, bar, h * 64, head, slot, page);
                 }
-                const int s = it % S::kNQ, tok0 = qi * p.step_tokens, toks = min(p.step_tokens, w.k.t1 - w.k.t0 - tok0);
-                if (it >= S::kNQ && !wait.warp(smem_addr(&aux.q_empty[s]), ((it / S::kNQ) - 1) & 1)) { ok = false; break; }
+                __syncwarp();
+            }
+        } while (ok && w.next(p));
+    } else if (warp == 3) {
+        // ---- queries ----
+        int it = 0;
+        bool ok = true;
+        do {
+            if (w.k.per_head == 0) continue;
+            const int tok_first = w.q.q0 + w.k.t0, ntok = w.k.t1 - w.k.t0;
+            int head = w.at.off / w.k.per_head, qi = w.at.off - head * w.k.per_head;
+            for (int i = 0; i < w.n; i++, it++) {
+                const int tok0 = qi * p.step_tokens, toks = min(p.step_tokens, ntok - tok0), s = it % S::kNQ;
+                if (it >= S::kNQ && !(ok = wait.warp(smem_addr(&aux.q_empty[s]), ((it / S::kNQ) - 1) & 1))) break;
                 const uint32_t bar = smem_addr(&aux.q_full[s]);
                 const int boxes = (toks + p.q_box - 1) / p.q_box;
                 if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * p.q_box * group) * DK * 2);
@@ -261,32 +270,35 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
 #pragma unroll
                     for (int h = 0; h < DK / 64; h++)
                         tma_load_3d(base + S::kOffQ + s * S::kOperand + h * kPanel + j * p.q_box * group * 128, &q_map, bar, h * 64, head * group,
-                                    w.q.q0 + w.k.t0 + tok0 + j * p.q_box);
+                                    tok_first + tok0 + j * p.q_box);
                 __syncwarp();
                 if (++qi == w.k.per_head) qi = 0, head++;
             }
         } while (ok && w.next(p));
-    } else if (warp == 3) {
-        // ---- the rows' normalisers, four steps ahead ----
+    } else if (warp >= 12) {
+        // ---- the normalisers of a step's rows, a warp for the even steps and one for the odd: a trip to memory
+        // takes longer than a step ----
         int it = 0;
         bool ok = true;
         do {
             if (w.k.per_head == 0) continue;
             const int tok_first = w.q.q0 + w.k.t0, ntok = w.k.t1 - w.k.t0;
             int head = w.at.off / w.k.per_head, qi = w.at.off - head * w.k.per_head;
-            for (int i = 0; ok && i < w.n; i++, it++) {
-                const int tok0 = qi * p.step_tokens, cols = min(p.step_tokens, ntok - tok0) * group, s = it & 3;
-                float v[4];
+            for (int i = 0; i < w.n; i++, it++) {
+                if ((it & 1) == warp - 12) {
+                    const int tok0 = qi * p.step_tokens, cols = min(p.step_tokens, ntok - tok0) * group, s = it & 3;
+                    float v[4];
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const int c = j * 32 + lane, tt = (int)fdiv((uint32_t)c, b.group);
-                    v[j] = c < cols ? -p.lse[(int64_t)(tok_first + tok0 + tt) * p.heads + head * group + c - tt * group] * kLog2e : -INFINITY;
-                    if (v[j] == INFINITY) v[j] = -INFINITY;  // a row that saw nothing weighs nothing
+                    for (int j = 0; j < 4; j++) {
+                        const int c = j * 32 + lane, tt = (int)fdiv((uint32_t)c, b.group);
+                        v[j] = c < cols ? -p.lse[(int64_t)(tok_first + tok0 + tt) * p.heads + head * group + c - tt * group] * kLog2e : -INFINITY;
+                        if (v[j] == INFINITY) v[j] = -INFINITY;  // a row that saw nothing weighs nothing
+                    }
+                    if (it >= 4 && !(ok = wait.warp(smem_addr(&aux.s_empty[s]), ((it >> 2) - 1) & 1))) break;
+#pragma unroll
+                    for (int j = 0; j < 4; j++) aux.neg[s][j * 32 + lane] = v[j];
+                    warp_arrive(smem_addr(&aux.l_full[s]));
                 }
-                if (it >= 4 && !(ok = wait.warp(smem_addr(&aux.s_empty[s]), ((it >> 2) - 1) & 1))) break;
-#pragma unroll
-                for (int j = 0; j < 4; j++) aux.neg[s][j * 32 + lane] = v[j];
-                warp_arrive(smem_addr(&aux.l_full[s]));
                 if (++qi == w.k.per_head) qi = 0, head++;
             }
         } while (ok && w.next(p));
