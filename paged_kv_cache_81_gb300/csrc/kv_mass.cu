@@ -357,9 +357,8 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
                     tc_fence_after();
                     const int c0 = (va - tok0) * group, c1 = min(cols, (vb - tok0) * group);
                     float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                    const auto add = [&](uint32_t(&x)[32], int q) {
+                    const auto add = [&](const uint32_t(&x)[32], int q) {
                         const float4 *neg = reinterpret_cast<const float4 *>(&aux.neg[it & 3][q]);
-                        if (__any_sync(0xffffffffu, c0 > q || c1 < q + 32)) hide32(x, c0 - q, c1 - q);
                         const float2 cc = make_float2(p.c, p.c);
 #pragma unroll
                         for (int j = 0; j < 8; j++) {
@@ -371,18 +370,28 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
                             part[1] = add2(part[1], f);
                         }
                     };
-                    // 32 columns are read while 32 are added
                     uint32_t x0[32], x1[32];
-                    tmem_ld32(s_at, x0);
-                    tc_wait_ld();
+                    if (__any_sync(0xffffffffu, c0 > 0 || c1 < 128)) {  // some key is not seen by some row, or rows are missing
 #pragma unroll 1
-                    for (int q = 0; q < cols; q += 64) {
-                        tmem_ld32(s_at + q + 32, x1);
-                        add(x0, q);
+                        for (int q = 0; q < cols; q += 32) {
+                            tmem_ld32(s_at + q, x0);
+                            tc_wait_ld();
+                            hide32(x0, c0 - q, c1 - q);
+                            add(x0, q);
+                        }
+                    } else {  // 32 columns are read while 32 are added
+                        tmem_ld32(s_at, x0);
                         tc_wait_ld();
-                        if (q + 64 < cols) tmem_ld32(s_at + q + 64, x0);
-                        if (q + 32 < cols) add(x1, q + 32);
+                        tmem_ld32(s_at + 32, x1);
+                        add(x0, 0);
                         tc_wait_ld();
+                        tmem_ld32(s_at + 64, x0);
+                        add(x1, 32);
+                        tc_wait_ld();
+                        tmem_ld32(s_at + 96, x1);
+                        add(x0, 64);
+                        tc_wait_ld();
+                        add(x1, 96);
                     }
                     sum += (part[0].x + part[0].y) + (part[1].x + part[1].y);
                     tc_fence_before();
