@@ -8,6 +8,7 @@ CPU: when the library is missing, the first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from contextlib import nullcontext as _no_context
@@ -509,10 +510,14 @@ def kv_attention_workspace(device="cuda") -> torch.Tensor:
 _workspaces = {}  # (bytes function, device, stream handle) -> the workspace of calls without one on that stream
 
 
-def _own_workspace(nbytes, dev: int, handle: int) -> torch.Tensor:
-    """The workspace of calls that bring none: one a stream, whose calls are in order.  A call that is being captured
-    gets one of its own, in the graph's memory and zeroed by the graph, as replays are not in that order."""
-    if torch.cuda.is_current_stream_capturing():
+def _workspace(nbytes, dev: int, handle: int, given: Optional[torch.Tensor]) -> torch.Tensor:
+    """The workspace of a call.  Calls that bring none share one a stream, whose calls are in order.  A call that is being
+    captured gets one of its own, in the graph's memory and zeroed by the graph, as replays are not in that order."""
+    if given is not None:
+        if given.get_device() != dev or not given.is_contiguous():
+            raise ValueError(f"the workspace must be a contiguous tensor on cuda:{dev}")
+        return given
+    if torch._C._cuda_isCurrentStreamCapturing():
         return torch.zeros(nbytes(), dtype=torch.uint8, device=f"cuda:{dev}")
     key = (nbytes, dev, handle)
     ws = _workspaces.get(key)
@@ -522,14 +527,11 @@ def _own_workspace(nbytes, dev: int, handle: int) -> torch.Tensor:
     return ws
 
 
-def _begin(t: torch.Tensor, stream):
-    """(device index, raw stream handle) of a call whose first tensor is `t`."""
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError("libpagedkv takes CUDA tensors")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on cuda:{dev}, which is not the current device")
-    return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+def _begin(dev: int, stream) -> int:
+    """The raw stream handle of a call whose tensors are on device `dev`."""
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError("libpagedkv takes CUDA tensors" if dev < 0 else f"the tensors are on cuda:{dev}, which is not the current device")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _on(dev: int, *tensors):
@@ -538,57 +540,71 @@ def _on(dev: int, *tensors):
             raise ValueError(f"every tensor must be on cuda:{dev}")
 
 
-def _outputs_on(stream):
-    """Outputs made here belong to the stream that writes them."""
-    return _no_context() if stream is None else torch.cuda.stream(stream)
+def _empty(like: torch.Tensor, shape, dtype: torch.dtype, stream) -> torch.Tensor:
+    """An output, which belongs to the stream that writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _table(dev: int, t: torch.Tensor, n: int, name: str):
+    """(pointer, pages of a row, row stride) of a block table of n requests."""
+    if t.dtype is not torch.int32 or t.dim() != 2 or t.shape[0] != n or t.get_device() != dev:
+        raise ValueError(f"{name} must be an int32 [n_reqs, max_blocks] tensor on cuda:{dev}, with the batch's requests")
+    row, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{name} must be row-major")
+    return t.data_ptr(), t.shape[1], row
+
+
+def _i32_on(dev: int, t: torch.Tensor, n: int, name: str) -> int:
+    if t.dtype is not torch.int32 or t.get_device() != dev or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor on cuda:{dev}")
+    return t.data_ptr()
 
 
 def _attn_batch(dev: int, block_table: torch.Tensor, q_offsets: torch.Tensor, kv_lens: torch.Tensor, n_tokens: int) -> KvAttnBatch:
-    _i32(q_offsets, "q_offsets"), _i32(kv_lens, "kv_lens"), _table(block_table, "block_table")
-    _on(dev, block_table, q_offsets, kv_lens)
-    n = kv_lens.shape[0]
-    rows, cols = block_table.shape
-    if rows != n or q_offsets.shape[0] != n + 1:
-        raise ValueError("block_table, q_offsets and kv_lens are of different numbers of requests")
-    return KvAttnBatch(block_table.data_ptr(), n, cols, block_table.stride(0), q_offsets.data_ptr(), kv_lens.data_ptr(), n_tokens)
+    n = kv_lens.numel()
+    table, pages, row = _table(dev, block_table, n, "block_table")
+    return KvAttnBatch(table, n, pages, row, _i32_on(dev, q_offsets, n + 1, "q_offsets"), _i32_on(dev, kv_lens, n, "kv_lens"), n_tokens)
 
 
-def _table(t: torch.Tensor, name: str) -> torch.Tensor:
-    if t.dtype != torch.int32 or t.dim() != 2 or t.stride(1) != 1:
-        raise ValueError(f"{name} must be a row-major int32 [n_reqs, max_blocks] CUDA tensor")
-    return t
-
-
-def _rows3(t: torch.Tensor, name: str) -> int:
-    """The KV_BF16 / KV_F16 code of [tokens, heads, dim] rows."""
+def _rows3(t: torch.Tensor, name: str):
+    """(KV_BF16 or KV_F16, byte strides of tokens and heads) of [tokens, heads, dim] rows."""
     code = _DTYPES.get(t.dtype)
-    if code is None or t.dim() != 3 or t.stride(2) != 1:
-        raise ValueError(f"{name} must be a bf16 or fp16 CUDA tensor [tokens, heads, dim] with contiguous rows")
-    return code
+    if code is None or t.dim() != 3:
+        raise ValueError(f"{name} must be a bf16 or fp16 CUDA tensor [tokens, heads, dim]")
+    token, head, one = t.stride()
+    if one != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return code, token * 2, head * 2
 
 
 def _like_cache(dev: int, cache: PagedCache, dtype: torch.dtype, name: str) -> KvCacheDesc:
     t = cache.tensors[0]
-    if t.dtype != dtype:
-        raise ValueError(f"{name} holds {t.dtype}, not {dtype}")
-    _on(dev, t)
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must hold {dtype} on cuda:{dev}")
     return cache.desc()
 
 
 def _attn_outputs(dev: int, q: torch.Tensor, dv: int, out: Optional[torch.Tensor], lse: Optional[torch.Tensor], stream):
     T, H, _ = q.shape
     if out is None:
-        with _outputs_on(stream):
-            out = q.new_empty((T, H, dv))
-    elif _rows3(out, "out") < 0 or out.shape != (T, H, dv) or out.dtype != q.dtype:
-        raise ValueError("out must be [tokens, heads, value dim] of q's type")
+        out = _empty(q, (T, H, dv), q.dtype, stream)
+    elif out.shape != (T, H, dv) or out.dtype is not q.dtype or out.get_device() != dev:
+        raise ValueError("out must be [tokens, heads, value dim] of q's type, on its device")
     if lse is None:
-        with _outputs_on(stream):
-            lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    elif lse.shape != (T, H) or lse.dtype != torch.float32 or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous float32 [tokens, heads] tensor")
-    _on(dev, out, lse)
+        lse = _empty(q, (T, H), torch.float32, stream)
+    elif lse.shape != (T, H) or lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.get_device() != dev:
+        raise ValueError("lse must be a contiguous float32 [tokens, heads] tensor on q's device")
     return out, lse
+
+
+@functools.lru_cache(maxsize=256)
+def _attn_desc(*fields) -> KvAttnDesc:
+    """Descriptions repeat from layer to layer; the library only reads them."""
+    return KvAttnDesc(*fields)
 
 
 def kv_attention(q: torch.Tensor, cache: PagedCache, block_table: torch.Tensor, q_offsets: torch.Tensor,
@@ -599,15 +615,18 @@ def kv_attention(q: torch.Tensor, cache: PagedCache, block_table: torch.Tensor, 
 
     Keys are tensor `k_tensor` of `cache` (plane 0).  Values are tensor `v_tensor` of `v_cache`, or, without a
     `v_cache`, plane 1 of the same tensor (two-plane caches) or tensor `v_tensor` of `cache`."""
-    code = _rows3(q, "q")
-    dev, handle = _begin(q, stream)
+    code, q_token, q_head = _rows3(q, "q")
+    dev = q.get_device()
+    handle = _begin(dev, stream)
     k_desc = _like_cache(dev, cache, q.dtype, "cache")
-    values = cache if v_cache is None else v_cache
-    v_desc = k_desc if v_cache is None else _like_cache(dev, v_cache, q.dtype, "v_cache")
-    if v_tensor is None:
-        if v_cache is None and cache.n_planes == 1:
-            raise ValueError("a one-plane cache holds the values in another tensor: give v_tensor or v_cache")
-        v_tensor = k_tensor if v_cache is None else 0
+    if v_cache is None:
+        values, v_desc = cache, k_desc
+        if v_tensor is None:
+            if cache.n_planes == 1:
+                raise ValueError("a one-plane cache holds the values in another tensor: give v_tensor or v_cache")
+            v_tensor = k_tensor
+    else:
+        values, v_desc, v_tensor = v_cache, _like_cache(dev, v_cache, q.dtype, "v_cache"), v_tensor or 0
     T, H, dk = q.shape
     kv_heads, left = divmod(cache.row_bytes, dk * 2) if dk else (0, 0)
     if left or not kv_heads or values.row_bytes % (kv_heads * 2):
@@ -615,13 +634,11 @@ def kv_attention(q: torch.Tensor, cache: PagedCache, block_table: torch.Tensor, 
     dv = values.row_bytes // (kv_heads * 2)
     batch = _attn_batch(dev, block_table, q_offsets, kv_lens, T)
     out, lse = _attn_outputs(dev, q, dv, out, lse, stream)
-    if workspace is None:
-        workspace = _own_workspace(kv_attention_workspace_bytes, dev, handle)
-    _on(dev, workspace)
-    desc = KvAttnDesc(code, H, kv_heads, dk, dv, causal, window, scale)
-    _check("kv_attention", load().kv_attention(
-        desc, batch, k_desc, k_tensor, 0, v_desc, v_tensor, values.n_planes - 1, q.data_ptr(), q.stride(0) * 2, q.stride(1) * 2,
-        out.data_ptr(), out.stride(0) * 2, out.stride(1) * 2, lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, handle))
+    _, o_token, o_head = _rows3(out, "out")
+    workspace = _workspace(kv_attention_workspace_bytes, dev, handle, workspace)
+    _check("kv_attention", (_lib or load()).kv_attention(
+        _attn_desc(code, H, kv_heads, dk, dv, causal, window, scale), batch, k_desc, k_tensor, 0, v_desc, v_tensor, values.n_planes - 1,
+        q.data_ptr(), q_token, q_head, out.data_ptr(), o_token, o_head, lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, handle))
     return out, lse
 
 
@@ -631,19 +648,18 @@ def kv_latent_attention(q: torch.Tensor, cache: PagedCache, block_table: torch.T
                         workspace: Optional[torch.Tensor] = None, stream=None):
     """Attention of new tokens q [tokens, heads, 576] over a latent cache (the absorbed form); returns
     (out [tokens, heads, 512], lse float32 [tokens, heads])."""
-    code = _rows3(q, "q")
-    dev, handle = _begin(q, stream)
+    code, q_token, q_head = _rows3(q, "q")
+    dev = q.get_device()
+    handle = _begin(dev, stream)
     c_desc = _like_cache(dev, cache, q.dtype, "cache")
     T, H, dk = q.shape
     batch = _attn_batch(dev, block_table, q_offsets, kv_lens, T)
     out, lse = _attn_outputs(dev, q, LATENT_RANK, out, lse, stream)
-    if workspace is None:
-        workspace = _own_workspace(kv_attention_workspace_bytes, dev, handle)
-    _on(dev, workspace)
-    desc = KvAttnDesc(code, H, 1, dk, LATENT_RANK, causal, window, scale)
-    _check("kv_latent_attention", load().kv_latent_attention(
-        desc, batch, c_desc, tensor, q.data_ptr(), q.stride(0) * 2, q.stride(1) * 2, out.data_ptr(), out.stride(0) * 2,
-        out.stride(1) * 2, lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, handle))
+    _, o_token, o_head = _rows3(out, "out")
+    workspace = _workspace(kv_attention_workspace_bytes, dev, handle, workspace)
+    _check("kv_latent_attention", (_lib or load()).kv_latent_attention(
+        _attn_desc(code, H, 1, dk, LATENT_RANK, causal, window, scale), batch, c_desc, tensor, q.data_ptr(), q_token, q_head,
+        out.data_ptr(), o_token, o_head, lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, handle))
     return out, lse
 
 
@@ -655,22 +671,26 @@ def kv_latent_expand(cache: PagedCache, block_table: torch.Tensor, kv_lens: torc
     code = _DTYPES.get(weight.dtype)
     if code is None or weight.dim() != 3 or tuple(weight.shape[1:]) != (256, LATENT_RANK) or not weight.is_contiguous():
         raise ValueError("weight must be a contiguous bf16 or fp16 [heads, 256, 512] CUDA tensor")
-    dev, handle = _begin(weight, stream)
-    _table(block_table, "block_table"), _table(out_table, "out_table"), _i32(kv_lens, "kv_lens")
-    _on(dev, block_table, out_table, kv_lens)
-    descs = [_like_cache(dev, c, weight.dtype, name) for c, name in ((cache, "cache"), (k_out, "k_out"), (v_out, "v_out"))]
-    n = kv_lens.shape[0]
-    if block_table.shape[0] != n or out_table.shape[0] != n:
-        raise ValueError("block_table, out_table and kv_lens are of different numbers of requests")
-    _check("kv_latent_expand", load().kv_latent_expand(
-        code, weight.shape[0], descs[0], tensor, block_table.data_ptr(), n, block_table.shape[1], block_table.stride(0),
-        kv_lens.data_ptr(), weight.data_ptr(), descs[1], k_tensor, descs[2], v_tensor, out_table.data_ptr(), out_table.shape[1],
-        out_table.stride(0), handle))
+    dev = weight.get_device()
+    handle = _begin(dev, stream)
+    n = kv_lens.numel()
+    table, pages, row = _table(dev, block_table, n, "block_table")
+    out, out_pages, out_row = _table(dev, out_table, n, "out_table")
+    dtype = weight.dtype
+    _check("kv_latent_expand", (_lib or load()).kv_latent_expand(
+        code, weight.shape[0], _like_cache(dev, cache, dtype, "cache"), tensor, table, n, pages, row, _i32_on(dev, kv_lens, n, "kv_lens"),
+        weight.data_ptr(), _like_cache(dev, k_out, dtype, "k_out"), k_tensor, _like_cache(dev, v_out, dtype, "v_out"), v_tensor, out,
+        out_pages, out_row, handle))
 
 
-def _score_rows(t: torch.Tensor, n: int, width: int, name: str):
-    if t.dtype != torch.float32 or t.dim() != 2 or t.shape[0] != n or t.shape[1] < width or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be a row-major float32 [n_reqs, {width} or more] CUDA tensor")
+def _score_rows(dev: int, t: torch.Tensor, n: int, width: int, name: str):
+    """(pointer, row stride) of scores."""
+    if t.dtype is not torch.float32 or t.dim() != 2 or t.shape[0] != n or t.shape[1] < width or t.get_device() != dev:
+        raise ValueError(f"{name} must be a float32 [n_reqs, {width} or more] tensor on cuda:{dev}")
+    row, one = t.stride()
+    if one != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name} must be row-major")
+    return t.data_ptr(), row
 
 
 def kv_attention_mass(q: torch.Tensor, cache: PagedCache, block_table: torch.Tensor, q_offsets: torch.Tensor,
@@ -679,34 +699,28 @@ def kv_attention_mass(q: torch.Tensor, cache: PagedCache, block_table: torch.Ten
                       width: Optional[int] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The attention weight every cached token receives from q, added to prev (float32 [n_reqs, width], or None);
     returns score [n_reqs, width].  width: prev's or score's columns, else a table row's slots."""
-    code = _rows3(q, "q")
-    dev, handle = _begin(q, stream)
+    code, q_token, q_head = _rows3(q, "q")
+    dev = q.get_device()
+    handle = _begin(dev, stream)
     k_desc = _like_cache(dev, cache, q.dtype, "cache")
     T, H, dk = q.shape
     kv_heads, left = divmod(cache.row_bytes, dk * 2) if dk else (0, 0)
     if left or not kv_heads:
         raise ValueError("the cache's rows are not whole heads of q's width")
     batch = _attn_batch(dev, block_table, q_offsets, kv_lens, T)
-    if lse.shape != (T, H) or lse.dtype != torch.float32 or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous float32 [tokens, heads] tensor")
-    n = kv_lens.shape[0]
+    if lse.shape != (T, H) or lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.get_device() != dev:
+        raise ValueError("lse must be a contiguous float32 [tokens, heads] tensor on q's device")
+    n = batch.n_reqs
     if width is None:
         width = prev.shape[1] if prev is not None else score.shape[1] if score is not None else batch.max_blocks_per_req * cache.block_size
     if score is None:
-        with _outputs_on(stream):
-            score = torch.empty((n, width), dtype=torch.float32, device=q.device)
-    else:
-        _score_rows(score, n, width, "score")
-    if prev is not None:
-        _score_rows(prev, n, width, "prev")
-    if workspace is None:
-        workspace = _own_workspace(kv_attention_mass_workspace_bytes, dev, handle)
-    _on(dev, lse, score, prev, workspace)
-    desc = KvAttnDesc(code, H, kv_heads, dk, dk, causal, window, scale)
-    _check("kv_attention_mass", load().kv_attention_mass(
-        desc, batch, k_desc, k_tensor, 0, q.data_ptr(), q.stride(0) * 2, q.stride(1) * 2, lse.data_ptr(),
-        prev.data_ptr() if prev is not None else None, prev.stride(0) if prev is not None else 0, score.data_ptr(), score.stride(0),
-        width, workspace.data_ptr(), workspace.nbytes, handle))
+        score = _empty(q, (n, width), torch.float32, stream)
+    to, to_row = _score_rows(dev, score, n, width, "score")
+    before, before_row = (None, 0) if prev is None else _score_rows(dev, prev, n, width, "prev")
+    workspace = _workspace(kv_attention_mass_workspace_bytes, dev, handle, workspace)
+    _check("kv_attention_mass", (_lib or load()).kv_attention_mass(
+        _attn_desc(code, H, kv_heads, dk, dk, causal, window, scale), batch, k_desc, k_tensor, 0, q.data_ptr(), q_token, q_head,
+        lse.data_ptr(), before, before_row, to, to_row, width, workspace.data_ptr(), workspace.nbytes, handle))
     return score
 
 
@@ -716,33 +730,27 @@ def kv_evict(cache: PagedCache, block_table: torch.Tensor, kv_lens: torch.Tensor
     """Trims every request to `budget` tokens: the first `sinks`, the last `recent` and the highest scores between, in
     their order; rows of every tensor and plane are gathered to out_table's pages (None: in place).  Returns
     (new_lens int32 [n_reqs], kept int32 [n_reqs, budget], out_score float32 [n_reqs, budget])."""
-    dev, handle = _begin(kv_lens, stream)
-    _table(block_table, "block_table"), _i32(kv_lens, "kv_lens")
-    if out_table is None:
-        out_table = block_table
-    _table(out_table, "out_table")
-    n = kv_lens.shape[0]
-    if block_table.shape[0] != n or out_table.shape[0] != n:
-        raise ValueError("block_table, out_table and kv_lens are of different numbers of requests")
+    dev = kv_lens.get_device()
+    handle = _begin(dev, stream)
+    n = kv_lens.numel()
+    table, pages, row = _table(dev, block_table, n, "block_table")
+    out, out_pages, out_row = (table, pages, row) if out_table is None else _table(dev, out_table, n, "out_table")
     if budget < 0:
         raise ValueError("budget must not be negative")
-    _score_rows(score, n, 0, "score")
-    with _outputs_on(stream):
-        if new_lens is None:
-            new_lens = torch.empty(n, dtype=torch.int32, device=kv_lens.device)
-        if kept is None:
-            kept = torch.empty((n, budget), dtype=torch.int32, device=kv_lens.device)
-        if out_score is None:
-            out_score = torch.empty((n, budget), dtype=torch.float32, device=kv_lens.device)
-    _i32(new_lens, "new_lens")
-    if new_lens.shape[0] != n or kept.dtype != torch.int32 or kept.shape != (n, budget) or (budget > 1 and kept.stride(1) != 1):
-        raise ValueError("new_lens must be int32 [n_reqs] and kept a row-major int32 [n_reqs, budget]")
-    _score_rows(out_score, n, budget, "out_score")
-    _on(dev, block_table, out_table, kv_lens, score, new_lens, kept, out_score, cache.tensors[0])
-    _check("kv_evict", load().kv_evict(
-        cache.desc(), block_table.data_ptr(), n, block_table.shape[1], block_table.stride(0), kv_lens.data_ptr(), score.data_ptr(),
-        score.stride(0), score.shape[1], budget, sinks, recent, out_table.data_ptr(), out_table.shape[1], out_table.stride(0),
-        new_lens.data_ptr(), kept.data_ptr(), kept.stride(0), out_score.data_ptr(), out_score.stride(0), handle))
+    if new_lens is None:
+        new_lens = _empty(kv_lens, (n,), torch.int32, stream)
+    if kept is None:
+        kept = _empty(kv_lens, (n, budget), torch.int32, stream)
+    elif kept.dtype is not torch.int32 or kept.shape != (n, budget) or kept.get_device() != dev or (budget > 1 and kept.stride(1) != 1):
+        raise ValueError("kept must be a row-major int32 [n_reqs, budget] tensor on the requests' device")
+    if out_score is None:
+        out_score = _empty(kv_lens, (n, budget), torch.float32, stream)
+    from_score, from_row = _score_rows(dev, score, n, 0, "score")
+    to_score, to_row = _score_rows(dev, out_score, n, budget, "out_score")
+    _on(dev, *cache.tensors[:1])
+    _check("kv_evict", (_lib or load()).kv_evict(
+        cache.desc(), table, n, pages, row, _i32_on(dev, kv_lens, n, "kv_lens"), from_score, from_row, score.shape[1], budget, sinks, recent,
+        out, out_pages, out_row, _i32_on(dev, new_lens, n, "new_lens"), kept.data_ptr(), kept.stride(0), to_score, to_row, handle))
     return new_lens, kept, out_score
 
 
