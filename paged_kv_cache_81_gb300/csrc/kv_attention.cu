@@ -31,7 +31,7 @@ namespace {
 constexpr int kLeast = KL;  // steps of a piece, at least
 constexpr int kThreads = 384;
 constexpr int kRows = 256;  // rows of a unit, at most: 2 * floor(128 / group) tokens of a group
-constexpr int kTile = 128;  // keys of a tile
+constexpr int kTileShift = 7, kTile = 1 << kTileShift;  // keys of a tile
 constexpr uint32_t kPanel = 128 * 128;  // bytes of a 64-element panel of 128 rows
 
 template <int DK, int DV>
@@ -60,7 +60,7 @@ struct Params {
 struct Aux {
     uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
     uint64_t s_full[2], p_ready[2], o_done[2], q_full, q_empty, merge_ready, merge_free, join[2];
-    long long scan[33];
+    int scan[12];
     Place place;
     float m[128], l[128];  // the odd tiles' group, for the join
     uint32_t tmem;
@@ -452,7 +452,7 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                 const Cut cut(line, w.pos - w.at.off, unit_cost(w.u));
                 if (last_of(p.counters + 2 * cut.c0 + g, cut.count, smem_addr(&aux.join[g]), cuts, &aux.answer[g], wait, ok)) {
                     const int row0 = both ? g * half : 0;
-                    join_rows<DV, Bf16>(p.o, p.ws, cut.c0, cut.count, 1, 0, kRows * (DV + 2), row0, min(half, w.u.rows - row0), kRows, w.u.row0, w.q.q0,
+                    join_rows<DV, Bf16, 4, 4>(p.o, p.ws, cut.c0, cut.count, 1, 0, kRows * (DV + 2), row0, min(half, w.u.rows - row0), kRows, w.u.row0, w.q.q0,
                                         w.at.head * (int)b.group.d, b.group);
                 }
                 if (!ok) break;
@@ -500,7 +500,7 @@ int check_batch(const kv_attn_batch *t)
 }
 
 // Fills the batch a kernel works on; lengths are held in 32 bits.
-int fill_batch(Batch *b, const kv_attn_batch *t, int heads, int kv_heads, int block_size, int unit_rows, int tile, int causal, int window)
+int fill_batch(Batch *b, const kv_attn_batch *t, int heads, int kv_heads, int block_size, int unit_rows, int tile_shift, int causal, int window)
 {
     const int64_t max_tokens = (int64_t)t->max_blocks_per_req * block_size;
     if (max_tokens > (1ll << 30) || t->n_tokens * (int64_t)heads > (1ll << 30)) return KV_ERR_UNSUPPORTED;
@@ -511,10 +511,14 @@ int fill_batch(Batch *b, const kv_attn_batch *t, int heads, int kv_heads, int bl
     b->max_tokens = (int32_t)max_tokens;
     b->kv_heads = kv_heads;
     b->unit_rows = unit_rows;
-    b->tile = tile;
+    b->tile_shift = tile_shift;
     b->causal = causal ? 1 : 0;
     b->window = window;
     b->group = make_fastdiv((uint32_t)(heads / kv_heads));
+    b->unit = make_fastdiv((uint32_t)unit_rows);
+    // the line's steps are counted in 32 bits
+    const int64_t units = t->n_tokens * heads / unit_rows + (int64_t)t->n_reqs * kv_heads;
+    if (units * ((max_tokens >> tile_shift) + 1) >= (1ll << 31)) return KV_ERR_UNSUPPORTED;
     b->err = nullptr;
     return KV_OK;
 }
@@ -614,7 +618,7 @@ int kv_attention(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_cac
     if (workspace == nullptr) return KV_ERR_INVALID_ARG;
     if (!aligned16(workspace) || ((uintptr_t)lse & 3u)) return KV_ERR_ALIGN;
     Params p = {};
-    if ((st = fill_batch(&p.b, batch, d->n_heads, d->n_kv_heads, k->block_size, 2 * (128 / group) * group, kTile, d->causal, d->window)) != KV_OK) return st;
+    if ((st = fill_batch(&p.b, batch, d->n_heads, d->n_kv_heads, k->block_size, 2 * (128 / group) * group, kTileShift, d->causal, d->window)) != KV_OK) return st;
     const DeviceInfo *dev = current_device();
     if (dev == nullptr) return KV_ERR_CUDA;
     if (workspace_bytes < attention_workspace(dev->num_sms)) return KV_ERR_RANGE;

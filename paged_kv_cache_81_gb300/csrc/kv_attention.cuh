@@ -16,7 +16,7 @@ constexpr int64_t kCounterBytes = 16384;  // arrival counts of cut units, zero b
 inline int64_t attention_workspace(int num_sms) { return kCounterBytes + (int64_t)num_sms * 2 * 256 * (128 + 2) * 4; }
 
 int check_batch(const kv_attn_batch *t);
-int fill_batch(Batch *b, const kv_attn_batch *t, int heads, int kv_heads, int block_size, int unit_rows, int tile, int causal, int window);
+int fill_batch(Batch *b, const kv_attn_batch *t, int heads, int kv_heads, int block_size, int unit_rows, int tile_shift, int causal, int window);
 int check_plane(const kv_cache_desc *c, int tensor, int plane, int heads, int dim);
 int check_rows(const void *p, int64_t token_stride, int64_t head_stride);
 // Tokens of a TMA of q: the smallest divisor of `most` (a group's tokens in 128 rows) that holds a request's
@@ -34,7 +34,7 @@ int piece_rows(int block_size, int tile);
 // and the others in slot 2 c (a CTA has at most one fragment that begins its unit and one that does not).
 struct Cut {
     int c0, count;
-    __device__ __forceinline__ Cut(const Line &line, long long begin, int cost)
+    __device__ __forceinline__ Cut(const Line &line, int begin, int cost)
         : c0(line.part_of(begin)), count(line.part_of(begin + cost - 1) - c0 + 1)
     {
     }
@@ -74,11 +74,12 @@ struct Output {
 // threads; a row's fragments are added in the order of their keys, so the result does not depend on which
 // CTA came last.  Row r is (first + r) / group of the request's tokens from q0 on, head head0 + the
 // rest.  Not inlined: its registers would crowd the loop over the key tiles.
-template <int DV, bool Bf16>
+template <int DV, bool Bf16, int Batch, int Ahead>
 __device__ __noinline__ void join_rows(const Output p, const float *ws, int c0, int count, int halves, int half, int stride, int row0, int rows, int stat,
                                        int first, int q0, int head0, const FastDiv group)
 {
-    constexpr int kBatch = 8;  // column quads in flight for each fragment: the loads take the time
+    // `Batch` column quads of `Ahead` fragments in flight: the loads take the time
+    constexpr int kBatch = Batch;
     int shift = 4;             // rows rounded up to a power of two; the other threads share out the columns
     while ((1 << shift) < rows) shift++;
     const int t = threadIdx.x & 127, row = row0 + (t & ((1 << shift) - 1)), parts = 128 >> shift, quads = DV / 4 / parts;
@@ -98,7 +99,7 @@ __device__ __noinline__ void join_rows(const Output p, const float *ws, int c0, 
         float l = 0.0f;
 #pragma unroll
         for (int k = 0; k < kBatch; k++) o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 2
+#pragma unroll Ahead
         for (int i = 0; i < count; i++) {
             const float *part = fragment(i);
             const float pm = __ldcg(part + stat * DV + row), pl = __ldcg(part + stat * (DV + 1) + row);

@@ -38,7 +38,7 @@ struct Params {
 
 struct Aux {
     uint64_t a_full, a_empty, b_full[kStages], b_empty[kStages], d_full[2], d_empty[2];
-    long long scan[12];
+    int scan[12];
     int32_t req, tile, head;
     uint32_t tmem;
     int gave_up;
@@ -102,11 +102,11 @@ expand_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__
     grid_dep_entry();
     const Line line = find_piece<kThreads>(
         p.n_reqs, blockIdx.x, gridDim.x, 1, aux.scan,
-        [&](int r) { return (long long)((request_len(p, r, blockIdx.x == 0) + kTile - 1) / kTile) * p.heads; },
-        [&](int r, long long rest) {
+        [&](int r) { return (request_len(p, r, blockIdx.x == 0) + kTile - 1) / kTile * p.heads; },
+        [&](int r, int rest) {
             aux.req = r;
-            aux.tile = (int)line_div(rest, p.heads);
-            aux.head = (int)(rest - (long long)aux.tile * p.heads);
+            aux.tile = (int)((uint32_t)rest / (uint32_t)p.heads);
+            aux.head = rest - aux.tile * p.heads;
         });
     tc_fence_before();
     __syncthreads();
@@ -278,7 +278,7 @@ extern "C" int kv_latent_expand(int32_t dtype, int32_t n_heads, const kv_cache_d
     if (n_reqs > 1 && (bt_row_stride < max_blocks_per_req || out_row_stride < out_blocks_per_req)) return KV_ERR_INVALID_ARG;
     if (!aligned16(weight)) return KV_ERR_ALIGN;
     const int64_t max_tokens = (int64_t)max_blocks_per_req * cache->block_size, out_tokens = (int64_t)out_blocks_per_req * k_out->block_size;
-    if (max_tokens > (1ll << 30) || out_tokens > (1ll << 30)) return KV_ERR_UNSUPPORTED;
+    if (max_tokens > (1ll << 30) || out_tokens > (1ll << 30) || n_reqs * (max_tokens / kTile + 1) * n_heads >= (1ll << 31)) return KV_ERR_UNSUPPORTED;
     const DeviceInfo *dev = current_device();
     if (dev == nullptr) return KV_ERR_CUDA;
     if ((st = prepare_attention(*dev)) != KV_OK) return st;

@@ -25,7 +25,7 @@ namespace {
 constexpr int kLeast = KL;  // steps of a piece, at least
 constexpr int kThreads = 256;
 constexpr int kRows = 128;
-constexpr int kKeys = 64;      // keys of a tile
+constexpr int kKeyShift = 6, kKeys = 1 << kKeyShift;  // keys of a tile
 constexpr int kD = 576, kDV = 512, kHalf = 256;
 constexpr int kQT = 4;         // panels of Q in tensor memory
 constexpr uint32_t kQPanel = 128 * 128, kPanel = kKeys * 128;
@@ -50,7 +50,7 @@ struct Params {
 
 struct Aux {
     uint64_t v_full[2], v_empty[2], x_full[2], x_empty[2], s_full[2], p_ready[2], o_done[2], q_staged, q_moved, q_full, q_empty, join;
-    long long scan[8];
+    int scan[8];
     Place place;
     uint32_t tmem;
     int answer;
@@ -368,7 +368,7 @@ latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ C
             if (!whole) {
                 const Cut cut(line, w.pos - w.at.off, unit_cost(w.u));
                 if (last_of(p.counters + 2 * cut.c0 + half, cut.count, smem_addr(&aux.join), cuts, &aux.answer, wait, ok))
-                    join_rows<kHalf, Bf16>(p.o, p.ws, cut.c0, cut.count, 2, half, kRows * (kHalf + 2), 0, w.u.rows, kRows, w.u.row0, w.q.q0, 0, b.group);
+                    join_rows<kHalf, Bf16, 8, 3>(p.o, p.ws, cut.c0, cut.count, 2, half, kRows * (kHalf + 2), 0, w.u.rows, kRows, w.u.row0, w.q.q0, 0, b.group);
                 if (!ok) break;
             }
         } while (w.next(b));
@@ -424,7 +424,7 @@ extern "C" int kv_latent_attention(const kv_attn_desc *d, const kv_attn_batch *b
     }
     const int unit_rows = d->n_heads > kRows ? box_heads : kRows / d->n_heads * d->n_heads;
     Params p = {};
-    if ((st = fill_batch(&p.b, batch, d->n_heads, 1, cache->block_size, unit_rows, kKeys, d->causal, d->window)) != KV_OK) return st;
+    if ((st = fill_batch(&p.b, batch, d->n_heads, 1, cache->block_size, unit_rows, kKeyShift, d->causal, d->window)) != KV_OK) return st;
     const DeviceInfo *dev = current_device();
     if (dev == nullptr) return KV_ERR_CUDA;
     if (workspace_bytes < attention_workspace(dev->num_sms)) return KV_ERR_RANGE;

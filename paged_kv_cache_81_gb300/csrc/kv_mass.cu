@@ -23,7 +23,7 @@ namespace {
 #endif
 constexpr int kLeast = KL;  // steps of a piece, at least
 constexpr int kThreads = 448;
-constexpr int kTile = 128;
+constexpr int kTileShift = 7, kTile = 1 << kTileShift;
 constexpr uint32_t kPanel = 128 * 128;
 
 template <int DK>
@@ -41,6 +41,7 @@ struct Params {
     FastDiv block;
     int32_t piece_rows, dk, heads;
     int32_t step_tokens;  // tokens of one step: 128 / group
+    FastDiv step;
     int32_t q_box;        // tokens one TMA brings of q, a divisor of step_tokens
     float c;
     const float *lse;
@@ -55,7 +56,7 @@ struct Params {
 
 struct Aux {
     uint64_t k_full[8], k_empty[8], q_full[4], q_empty[4], s_full[4], s_empty[4], l_full[4], sum_ready, sum_free, join;
-    long long scan[14];
+    int scan[14];
     Place place;
     alignas(16) float neg[4][128];  // read four at a time: -lse log2 e of a step's rows
     float odd[128];     // the odd steps' sums
@@ -80,7 +81,7 @@ __device__ __forceinline__ KeyTile key_tile(const Params &p, const Request &q, i
     KeyTile k;
     k.t0 = b.causal ? max(0, kb - base) : 0;
     k.t1 = b.window ? min(q.q_len, max(0, end - 1 + b.window - base)) : q.q_len;
-    k.per_head = k.t1 > k.t0 ? (k.t1 - k.t0 + p.step_tokens - 1) / p.step_tokens : 0;
+    k.per_head = k.t1 > k.t0 ? (int)fdiv((uint32_t)(k.t1 - k.t0 + p.step_tokens - 1), p.step) : 0;
     k.steps = max(1, k.per_head * b.kv_heads);
     k.lo = b.window ? max(0, base - b.window + 1) : 0;
     return k;
@@ -97,11 +98,12 @@ __device__ __forceinline__ int even_tiles(const Params &p, const Request &q)
     return base < 0 ? 0 : min(tiles, base / kTile + 1);
 }
 
-__device__ __forceinline__ long long request_cost(const Params &p, int r)
+__device__ __forceinline__ int request_cost(const Params &p, int r)
 {
     const Request q = load_request(p.b, r);
     int t = even_tiles(p, q);
-    long long n = t > 0 ? (long long)t * key_tile(p, q, 0).steps : 0;
+    int n = t > 0 ? t * key_tile(p, q, 0).steps : 0;
+#pragma unroll 1
     for (; t * kTile < q.len; t++) n += key_tile(p, q, t).steps;
     return n;
 }
@@ -110,7 +112,7 @@ __device__ __forceinline__ long long request_cost(const Params &p, int r)
 struct Walk2 {
     Place at;
     int left, n;
-    long long pos;  // the fragment's first step on the line
+    int pos;  // the fragment's first step on the line
     Request q;
     KeyTile k;
     __device__ __forceinline__ bool start(const Params &p, const Place &pl, const Line &line)
@@ -178,21 +180,22 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
             if (blockIdx.x == 0) load_request(b, r, true);
             return request_cost(p, r);
         },
-        [&](int r, long long rest) {
+        [&](int r, int rest) {
             const Request q = load_request(b, r);
             Place pl{r, 0, 0, 0};
             const int even = even_tiles(p, q);
             if (even > 0) {
                 const int n = key_tile(p, q, 0).steps;
-                pl.unit = (int)min((long long)even, rest / n);
-                rest -= (long long)pl.unit * n;
+                pl.unit = min(even, (int)((uint32_t)rest / (uint32_t)n));
+                rest -= pl.unit * n;
             }
+#pragma unroll 1
             for (;; pl.unit++) {
                 const int n = key_tile(p, q, pl.unit).steps;
                 if (rest < n) break;
                 rest -= n;
             }
-            pl.off = (int)rest;
+            pl.off = rest;
             aux.place = pl;
         });
     tc_fence_before();
@@ -508,7 +511,7 @@ int kv_attention_mass(const kv_attn_desc *d, const kv_attn_batch *batch, const k
     if (batch->n_reqs > 1 && (score_stride < width || (prev != nullptr && prev_stride < width))) return KV_ERR_INVALID_ARG;
     if (!aligned16(workspace) || ((uintptr_t)lse & 3u) || ((uintptr_t)prev & 3u) || ((uintptr_t)score & 3u)) return KV_ERR_ALIGN;
     Params p = {};
-    if ((st = fill_batch(&p.b, batch, d->n_heads, d->n_kv_heads, k->block_size, 128, kTile, d->causal, d->window)) != KV_OK) return st;
+    if ((st = fill_batch(&p.b, batch, d->n_heads, d->n_kv_heads, k->block_size, 128, kTileShift, d->causal, d->window)) != KV_OK) return st;
     const DeviceInfo *dev = current_device();
     if (dev == nullptr) return KV_ERR_CUDA;
     if (workspace_bytes < mass_workspace(dev->num_sms)) return KV_ERR_RANGE;
@@ -523,6 +526,7 @@ int kv_attention_mass(const kv_attn_desc *d, const kv_attn_batch *batch, const k
     p.heads = d->n_heads;
     const int group = d->n_heads / d->n_kv_heads;
     p.step_tokens = 128 / group;
+    p.step = make_fastdiv((uint32_t)p.step_tokens);
     p.q_box = box_tokens(p.step_tokens, batch);
     p.c = d->scale * kLog2e;
     p.lse = lse;
