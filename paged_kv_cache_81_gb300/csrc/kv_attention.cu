@@ -25,10 +25,7 @@ namespace pkv {
 
 namespace {
 
-#ifndef KL
-#define KL 1
-#endif
-constexpr int kLeast = KL;  // steps of a piece, at least
+constexpr int kLeast = 4;  // tiles of a piece of a unit, at least (a join costs as much as three or four more tiles: 3 to 5 us)
 constexpr int kThreads = 384;
 constexpr int kRows = 256;  // rows of a unit, at most: 2 * floor(128 / group) tokens of a group
 constexpr int kTileShift = 7, kTile = 1 << kTileShift;  // keys of a tile
@@ -38,7 +35,7 @@ template <int DK, int DV>
 struct Shape {
     static constexpr uint32_t kQ = 128 * DK * 2, kK = 128 * DK * 2, kV = 128 * DV * 2;
     static constexpr int kNK = DK == 64 ? 5 : DK == 128 ? 3 : 2;  // ring depths: what 227 KB holds
-    static constexpr int kNV = DK == 64 ? 5 : DK == 128 ? 2 : 1;
+    static constexpr int kNV = DK == 64 ? 5 : DK == 128 ? 2 : 1;  // (192: four single panels of K and two tiles of V ran 7% slower)
     static constexpr uint32_t kOffK = 2 * kQ, kOffV = kOffK + kNK * kK, kOffAux = kOffV + kNV * kV;
     static constexpr uint32_t kBytes = kOffAux + 2048;
 };
@@ -60,7 +57,7 @@ struct Params {
 struct Aux {
     uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
     uint64_t s_full[2], p_ready[2], o_done[2], q_full, q_empty, merge_ready, merge_free, join[2];
-    int scan[12];
+    int scan[48];
     Place place;
     float m[128], l[128];  // the odd tiles' group, for the join
     uint32_t tmem;

@@ -35,8 +35,14 @@ int piece_rows(int block_size, int tile);
 struct Cut {
     int c0, count;
     __device__ __forceinline__ Cut(const Line &line, int begin, int cost)
-        : c0(line.part_of(begin)), count(line.part_of(begin + cost - 1) - c0 + 1)
     {
+        if (line.nth >= 0) {
+            c0 = line.part - line.nth;
+            count = ceil_div(cost, line.each);
+        } else {
+            c0 = line.part_of(begin);
+            count = line.part_of(begin + cost - 1) - c0 + 1;
+        }
     }
     __device__ __forceinline__ int slot(int i) const { return 2 * (c0 + i) + (i == 0); }
 };

@@ -2,10 +2,11 @@
 //
 //   K[j, h] = [ W[h, 0:128] c_j ; rope_j ]     V[j, h] = W[h, 128:256] c_j       (c_j: 512 values, rope_j: 64)
 //
-// One product of 128 tokens by 256 columns (a head's keys and values) over 512.  A CTA keeps its token
-// tile's latents in shared memory (128 KB, gathered by TMA page by page) and streams the heads' weights
-// past them in panels of 64; two accumulators of 256 columns fill tensor memory, so the next head is
-// multiplied while this one is rounded and written.  The line (kv_plan.cuh) runs over requests, token
+// One product of 128 tokens by 128 columns (a head's keys, or its values) over 512.  A CTA keeps its token
+// tile's latents in tensor memory (256 columns; they come by TMA, page by page, through shared memory) and
+// streams the heads' weights past them in panels of 64 by 128: shared memory then moves 64 bytes a cycle in and
+// 64 out, its rate, where both operands from there were a quarter over it.  Two accumulators of 128 columns,
+// one for keys and one for values, each rounded and written by a warp group while the other is formed.  The line (kv_plan.cuh) runs over requests, token
 // tiles and heads, in equal pieces a CTA, so few tokens spread their heads over the GPU.  The rotary part
 // is copied beside the product.
 #include "kv_attention.cuh"
@@ -17,8 +18,9 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kTile = 128;
 constexpr int kRank = 512, kRope = 64, kNope = 128, kV = 128, kN = kNope + kV;
-constexpr uint32_t kAPanel = kTile * 128, kBPanel = kN * 128;
-constexpr int kStages = 3;
+constexpr uint32_t kAPanel = kTile * 128, kBPanel = kNope * 128;
+constexpr int kStages = 6;
+constexpr uint32_t kTmA = 256;  // accumulators: columns 0 and 128
 constexpr uint32_t kOffB = 8 * kAPanel, kOffAux = kOffB + kStages * kBPanel, kBytes = kOffAux + 1024;
 
 struct Params {
@@ -37,9 +39,9 @@ struct Params {
 };
 
 struct Aux {
-    uint64_t a_full, a_empty, b_full[kStages], b_empty[kStages], d_full[2], d_empty[2];
-    int scan[12];
-    int32_t req, tile, head;
+    uint64_t a_full, a_moved, b_full[kStages], b_empty[kStages], d_full[2], d_empty[2];
+    int scan[48];
+    Place place;
     uint32_t tmem;
     int gave_up;
 };
@@ -52,12 +54,37 @@ __device__ __forceinline__ int request_len(const Params &p, int r, bool report)
     return len;
 }
 
+// The line: a unit is a token tile, its steps are the heads.
+struct ExpandWork {
+    const Params &p;
+    bool report;
+    __device__ __forceinline__ int units(int r) const { return (request_len(p, r, false) + kTile - 1) / kTile; }
+    __device__ __forceinline__ void measure(int r, int &steps, int &n) const
+    {
+        const int tiles = (request_len(p, r, report) + kTile - 1) / kTile;
+        n += tiles;
+        steps += tiles * p.heads;
+    }
+    __device__ __forceinline__ int pieces(int r, int each) const { return units(r) * ceil_div(p.heads, each); }
+    __device__ __forceinline__ Place own(int r, int k, int each) const
+    {
+        const int n = ceil_div(p.heads, each);
+        Place pl;
+        pl.req = r, pl.head = 0;
+        pl.unit = (int)((uint32_t)k / (uint32_t)n);
+        pl.nth = k - pl.unit * n;
+        pl.off = pl.nth * each;
+        pl.steps = min(each, p.heads - pl.off);
+        return pl;
+    }
+};
+
 // Fragments of a piece: heads [head, head + n) of one token tile.
 struct Walk {
     int req, tile, head, left, len, n;
     __device__ __forceinline__ bool start(const Params &p, const Aux &a, int steps)
     {
-        req = a.req, tile = a.tile, head = a.head, left = steps;
+        req = a.place.req, tile = a.place.unit, head = a.place.off, left = steps;
         if (left <= 0) return false;
         len = request_len(p, req, false);
         n = min(left, p.heads - head);
@@ -91,23 +118,16 @@ expand_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__
     if (tid == 0) {
         aux.gave_up = 0;
         mbar_init(smem_addr(&aux.a_full), 1);
-        mbar_init(smem_addr(&aux.a_empty), 1);
+        mbar_init(smem_addr(&aux.a_moved), 8);
         for (int i = 0; i < kStages; i++) mbar_init(smem_addr(&aux.b_full[i]), 1), mbar_init(smem_addr(&aux.b_empty[i]), 1);
-        for (int i = 0; i < 2; i++) mbar_init(smem_addr(&aux.d_full[i]), 1), mbar_init(smem_addr(&aux.d_empty[i]), 8);
+        for (int i = 0; i < 2; i++) mbar_init(smem_addr(&aux.d_full[i]), 1), mbar_init(smem_addr(&aux.d_empty[i]), 4);
         mbar_init_fence();
         tma_prefetch_map(&a_map);
         tma_prefetch_map(&w_map);
     }
     if (warp == 2) tmem_alloc(smem_addr(&aux.tmem), 512);
     grid_dep_entry();
-    const Line line = find_piece<kThreads>(
-        p.n_reqs, blockIdx.x, gridDim.x, 1, aux.scan,
-        [&](int r) { return (request_len(p, r, blockIdx.x == 0) + kTile - 1) / kTile * p.heads; },
-        [&](int r, int rest) {
-            aux.req = r;
-            aux.tile = (int)((uint32_t)rest / (uint32_t)p.heads);
-            aux.head = rest - aux.tile * p.heads;
-        });
+    const Line line = find_piece<kThreads>(p.n_reqs, blockIdx.x, gridDim.x, 1, aux.scan, &aux.place, ExpandWork{p, blockIdx.x == 0});
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -124,7 +144,7 @@ expand_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__
             const int kb = w.tile * kTile, p1 = (min(w.len - kb, kTile) + pr - 1) / pr;
             const int32_t *row = p.table + (int64_t)w.req * p.table_stride;
             const uint32_t abar = smem_addr(&aux.a_full);
-            if (frag && !wait.warp(smem_addr(&aux.a_empty), (frag - 1) & 1)) break;
+            if (frag && !wait.warp(smem_addr(&aux.a_moved), (frag - 1) & 1)) break;
             if (lane == 0) mbar_arrive_expect_tx(abar, (uint32_t)(p1 * pr) * kRank * 2);
             __syncwarp();
             for (int j = lane; j < p1; j += 32) {
@@ -139,48 +159,47 @@ expand_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__
                     tma_load_4d(base + h * kAPanel + j * pr * 128, &a_map, abar, h * 64, 0, (int)(key - col * p.block.d), page);
             }
             frag++;
-            for (int h = 0; ok && h < w.n; h++)
+            for (int h = 0; ok && h < 2 * w.n; h++)
                 for (int kk = 0; kk < 8; kk++, it++) {
                     const int s = it % kStages;
                     if (it >= kStages && !wait.warp(smem_addr(&aux.b_empty[s]), ((it / kStages) - 1) & 1)) { ok = false; break; }
                     if (lane == 0) {
                         mbar_arrive_expect_tx(smem_addr(&aux.b_full[s]), kBPanel);
-                        tma_load_3d(base + kOffB + s * kBPanel, &w_map, smem_addr(&aux.b_full[s]), kk * 64, 0, w.head + h);
+                        tma_load_3d(base + kOffB + s * kBPanel, &w_map, smem_addr(&aux.b_full[s]), kk * 64, (h & 1) * kNope, w.head + (h >> 1));
                     }
                     __syncwarp();
                 }
         } while (ok && w.next(p));
     } else if (warp == 1) {
-        constexpr uint32_t desc = mma_desc(Bf16, 128, kN, false);
+        constexpr uint32_t desc = mma_desc(Bf16, 128, kNope, false);
         const uint32_t elected = elect_one();
-        const uint64_t ad = smem_desc(base, 16, 1024), bd = smem_desc(base + kOffB, 16, 1024);
+        const uint64_t bd = smem_desc(base + kOffB, 16, 1024);
         int frag = 0, it = 0, heads = 0;
         bool ok = true;
         do {
-            ok = wait.warp(smem_addr(&aux.a_full), frag++ & 1);
-            for (int h = 0; ok && h < w.n; h++, heads++) {
-                const int d = heads & 1;
-                ok = heads < 2 || wait.warp(smem_addr(&aux.d_empty[d]), ((heads >> 1) - 1) & 1);
-                for (int kk = 0; ok && kk < 8; kk++, it++) {
-                    const int s = it % kStages;
-                    ok = wait.warp(smem_addr(&aux.b_full[s]), (it / kStages) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t aa = ad + kk * (kAPanel >> 4), bb = bd + s * (kBPanel >> 4);
+            ok = wait.warp(smem_addr(&aux.a_moved), frag++ & 1);
+            tc_fence_after();
+            for (int h = 0; ok && h < w.n; h++, heads++)
+                for (int d = 0; ok && d < 2; d++) {
+                    ok = heads < 1 || wait.warp(smem_addr(&aux.d_empty[d]), (heads - 1) & 1);
+                    for (int kk = 0; ok && kk < 8; kk++, it++) {
+                        const int s = it % kStages;
+                        ok = wait.warp(smem_addr(&aux.b_full[s]), (it / kStages) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t bb = bd + s * (kBPanel >> 4);
 #pragma unroll
-                    for (int j = 0; j < 4; j++) mma_ss(tmem + d * kN, aa + j * 2, bb + j * 2, desc, kk > 0 || j > 0, elected);
-                    tc_commit(smem_addr(&aux.b_empty[s]), elected);
+                        for (int j = 0; j < 4; j++) mma_ts(tmem + d * kNope, tmem + kTmA + kk * 32 + j * 8, bb + j * 2, desc, kk > 0 || j > 0, elected);
+                        tc_commit(smem_addr(&aux.b_empty[s]), elected);
+                    }
+                    if (ok) tc_commit(smem_addr(&aux.d_full[d]), elected);  // last: the writing warps wait for it before the CTA ends
                 }
-                if (!ok) break;
-                if (h + 1 == w.n) tc_commit(smem_addr(&aux.a_empty), elected);
-                tc_commit(smem_addr(&aux.d_full[d]), elected);  // last: the writing warps wait for it before the CTA ends
-            }
         } while (ok && w.next(p));
     } else if (warp >= 4) {
         const int g = (warp - 4) >> 2, t = tid & 127;  // group 0 writes the keys, group 1 the values
         const uint32_t mine = (uint32_t)((warp & 3) * 32) << 16;
         const int row_bytes = (g ? kV : kNope + kRope) * 2;
-        int heads = 0;
+        int heads = 0, frag = 0;
         bool ok = true;
         do {
             const int tok = w.tile * kTile + t;
@@ -213,14 +232,32 @@ expand_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__
                                   : make_uint4(0, 0, 0, 0);
                 }
             }
+            // the tile's latents into tensor memory, half of the panels a group.  Both groups have waited for their
+            // last products of the tile before, and the other group's came no later than one product more
+            if (frag && !wait.warp(smem_addr(&aux.d_full[1]), (heads - 1) & 1)) break;
+            if (!wait.warp(smem_addr(&aux.a_full), frag++ & 1)) break;
+#pragma unroll 1
+            for (int q = 4 * g; q < 4 * g + 4; q++) {
+                uint32_t x[32];
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const uint4 v = ld_smem16(base + q * kAPanel + panel_off(t, i));
+                    x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+                }
+                tmem_st32(tmem + kTmA + q * 32 + mine, x);
+            }
+            tc_wait_st();
+            tc_fence_before();
+            fence_async_smem();  // the loads before the TMA that overwrites what they read
+            warp_arrive(smem_addr(&aux.a_moved));
             for (int h = 0; h < w.n; h++, heads++) {
-                const int d = heads & 1, head = w.head + h;
-                if (!wait.warp(smem_addr(&aux.d_full[d]), (heads >> 1) & 1)) { ok = false; break; }
+                const int head = w.head + h;
+                if (!wait.warp(smem_addr(&aux.d_full[g]), heads & 1)) { ok = false; break; }
                 tc_fence_after();
 #pragma unroll 1
                 for (int q = 0; q < kNope / 32; q++) {
                     uint32_t x[32];
-                    tmem_ld32(tmem + d * kN + g * kNope + q * 32 + mine, x);
+                    tmem_ld32(tmem + g * kNope + q * 32 + mine, x);
                     tc_wait_ld();
                     float f[32];
 #pragma unroll
@@ -229,7 +266,7 @@ expand_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__
                     store_rows32<Bf16>(live ? to + head * row_bytes : nullptr, f, 1.0f, q * 32, kNope);
                 }
                 tc_fence_before();
-                warp_arrive(smem_addr(&aux.d_empty[d]));
+                warp_arrive(smem_addr(&aux.d_empty[g]));
 #pragma unroll
                 for (int i = 0; i < kRope / 16; i++)
                     if (rope_to[i] != nullptr) *reinterpret_cast<uint4 *>(rope_to[i] + head * (kNope + kRope) * 2) = rope[i];
@@ -310,7 +347,7 @@ extern "C" int kv_latent_expand(int32_t dtype, int32_t n_heads, const kv_cache_d
     CUtensorMap am, wm;
     if ((st = make_cache_map(&am, cache, tensor, 0, 1, kRank + kRope, p.piece_rows)) != KV_OK) return st;
     const uint64_t dims[3] = {kRank, kN, (uint64_t)n_heads}, strides[2] = {kRank * 2, kRank * 2 * kN};
-    const uint32_t box[3] = {64, kN, 1};
+    const uint32_t box[3] = {64, kNope, 1};
     if ((st = make_map(&wm, (uint64_t)weight, 3, dims, strides, box)) != KV_OK) return st;
     return cuda_status(launch(dtype == KV_BF16 ? expand_kernel<true> : expand_kernel<false>, dim3(dev->num_sms), dim3(kThreads), kBytes,
                               (cudaStream_t)stream, am, wm, p));

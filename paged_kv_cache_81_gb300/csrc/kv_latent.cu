@@ -19,10 +19,7 @@ namespace pkv {
 
 namespace {
 
-#ifndef KL
-#define KL 2
-#endif
-constexpr int kLeast = KL;  // steps of a piece, at least
+constexpr int kLeast = 2;  // steps of a piece of a unit, at least (of 64 keys)
 constexpr int kThreads = 256;
 constexpr int kRows = 128;
 constexpr int kKeyShift = 6, kKeys = 1 << kKeyShift;  // keys of a tile
@@ -50,7 +47,7 @@ struct Params {
 
 struct Aux {
     uint64_t v_full[2], v_empty[2], x_full[2], x_empty[2], s_full[2], p_ready[2], o_done[2], q_staged, q_moved, q_full, q_empty, join;
-    int scan[8];
+    int scan[32];
     Place place;
     uint32_t tmem;
     int answer;

@@ -18,10 +18,7 @@ namespace pkv {
 
 namespace {
 
-#ifndef KL
-#define KL 2
-#endif
-constexpr int kLeast = KL;  // steps of a piece, at least
+constexpr int kLeast = 2;  // steps of a piece of a unit, at least
 constexpr int kThreads = 448;
 constexpr int kTileShift = 7, kTile = 1 << kTileShift;
 constexpr uint32_t kPanel = 128 * 128;
@@ -56,7 +53,6 @@ struct Params {
 
 struct Aux {
     uint64_t k_full[8], k_empty[8], q_full[4], q_empty[4], s_full[4], s_empty[4], l_full[4], sum_ready, sum_free, join;
-    int scan[14];
     Place place;
     alignas(16) float neg[4][128];  // read four at a time: -lse log2 e of a step's rows
     float odd[128];     // the odd steps' sums
@@ -98,15 +94,50 @@ __device__ __forceinline__ int even_tiles(const Params &p, const Request &q)
     return base < 0 ? 0 : min(tiles, base / kTile + 1);
 }
 
-__device__ __forceinline__ int request_cost(const Params &p, int r)
-{
-    const Request q = load_request(p.b, r);
-    int t = even_tiles(p, q);
-    int n = t > 0 ? t * key_tile(p, q, 0).steps : 0;
+// The line: a unit is a key tile.
+struct MassWork {
+    const Params &p;
+    bool report;
+    // sum over the request's key tiles of their pieces of `each` steps
+    __device__ __forceinline__ int count(const Request &q, int each) const
+    {
+        int t = even_tiles(p, q), n = t > 0 ? t * ceil_div(key_tile(p, q, 0).steps, each) : 0;
 #pragma unroll 1
-    for (; t * kTile < q.len; t++) n += key_tile(p, q, t).steps;
-    return n;
-}
+        for (; t * kTile < q.len; t++) n += ceil_div(key_tile(p, q, t).steps, each);
+        return n;
+    }
+    __device__ __forceinline__ void measure(int r, int &steps, int &units) const
+    {
+        const Request q = load_request(p.b, r, report);
+        steps += count(q, 1);
+        units += (q.len + kTile - 1) / kTile;
+    }
+    __device__ __forceinline__ int pieces(int r, int each) const { return count(load_request(p.b, r), each); }
+    __device__ __forceinline__ Place own(int r, int k, int each) const
+    {
+        const Request q = load_request(p.b, r);
+        Place pl;
+        pl.req = r, pl.head = 0, pl.unit = 0;
+        const int even = even_tiles(p, q);
+        if (even > 0) {
+            const int n = ceil_div(key_tile(p, q, 0).steps, each);
+            pl.unit = min(even, (int)((uint32_t)k / (uint32_t)n));
+            k -= pl.unit * n;
+        }
+        int steps = 0;
+#pragma unroll 1
+        for (;; pl.unit++) {
+            steps = key_tile(p, q, pl.unit).steps;
+            const int n = ceil_div(steps, each);
+            if (k < n) break;
+            k -= n;
+        }
+        pl.nth = k;
+        pl.off = k * each;
+        pl.steps = min(each, steps - pl.off);
+        return pl;
+    }
+};
 
 // Walks a piece key tile by key tile.  place.unit: the key tile; place.off: the step inside it.
 struct Walk2 {
@@ -174,30 +205,7 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
     }
     if (warp == 2) tmem_alloc(smem_addr(&aux.tmem), 512);
     grid_dep_entry();
-    const Line line = find_piece<kThreads>(
-        b.n_reqs, blockIdx.x, gridDim.x, kLeast, aux.scan,
-        [&](int r) {
-            if (blockIdx.x == 0) load_request(b, r, true);
-            return request_cost(p, r);
-        },
-        [&](int r, int rest) {
-            const Request q = load_request(b, r);
-            Place pl{r, 0, 0, 0};
-            const int even = even_tiles(p, q);
-            if (even > 0) {
-                const int n = key_tile(p, q, 0).steps;
-                pl.unit = min(even, (int)((uint32_t)rest / (uint32_t)n));
-                rest -= pl.unit * n;
-            }
-#pragma unroll 1
-            for (;; pl.unit++) {
-                const int n = key_tile(p, q, pl.unit).steps;
-                if (rest < n) break;
-                rest -= n;
-            }
-            pl.off = rest;
-            aux.place = pl;
-        });
+    const Line line = find_piece<kThreads>(b.n_reqs, blockIdx.x, gridDim.x, kLeast, reinterpret_cast<int *>(aux.neg), &aux.place, MassWork{p, blockIdx.x == 0});
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

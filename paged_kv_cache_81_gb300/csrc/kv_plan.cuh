@@ -5,7 +5,8 @@
 // 2^tile_shift keys between the first key that its first token sees and the last that its last token sees.
 // Laid end to end (request, key head, unit), all units' tiles form one line; CTA c of `parts` takes
 // the c-th equal piece of it.  A piece may begin and end inside a unit: those two fragments go to the
-// workspace, and whichever CTA finishes the unit's last one joins them.  So the split follows the
+// workspace, and whichever CTA finishes the unit's last one joins them.  Where there are few units the
+// pieces are cut unit by unit instead, so that none holds parts of two.  The split follows the
 // lengths, not the launch: one grid serves a captured graph whatever the lengths become, and long
 // contexts and few rows fill the GPU as well as many short requests do.
 //
@@ -94,95 +95,156 @@ __device__ __forceinline__ int head_cost(const Batch &b, const Request &q)
     return n;
 }
 
-// A place on the line: tile `off` of unit (request, head, j).
+// Where a CTA's piece begins: step `off` of unit (request, head, unit).  nth: which of its unit's pieces this
+// is, or -1 where the line is cut into equal pieces; steps: its length where it is not.
 struct Place {
-    int32_t req, head, unit, off;
+    int32_t req, head, unit, off, nth, steps;
 };
 
-// How the line of `total` steps is cut into parts: the first `more` of them take `each` + 1 steps, the
-// others `each`.
+// How the line is cut.  nth < 0: the first `more` parts take `each` + 1 steps, the others `each`.
+// Otherwise every unit on its own into pieces of `each` steps.
 struct Line {
     int32_t begin, steps;  // of this CTA's part; 0 steps: none
     int32_t each, more;
+    int32_t part, nth;
 
-    __device__ __forceinline__ int part_of(int x) const  // the part that takes step x
+    __device__ __forceinline__ int part_of(int x) const  // the part that takes step x of equal pieces
     {
         const int longer = more * (each + 1);
         return x < longer ? (int)((uint32_t)x / (uint32_t)(each + 1)) : more + (int)((uint32_t)(x - longer) / (uint32_t)each);
     }
 };
 
-// Finds a CTA's piece of a line made of n_reqs stretches, the r-th cost(r) steps long (less than 2^31 in
-// all); every thread of the block calls it.  Pieces are of at least `least` steps.  scratch: one word a
-// warp.  Calls found(request, step inside its stretch) in the one thread that holds the beginning.
-template <int Threads, typename Cost, typename Found>
-__device__ __forceinline__ Line find_piece(int n_reqs, int part, int parts, int least, int *scratch, const Cost &cost, const Found &found)
+__device__ __forceinline__ int ceil_div(int a, int b) { return (int)((uint32_t)(a + b - 1) / (uint32_t)b); }
+
+// Inclusive scan of `mine` over the block, and the sums of it and of `other`.  scratch: two words a warp.
+template <int Threads>
+__device__ __forceinline__ int block_scan(int mine, int other, int *scratch, int &total, int &other_total)
 {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (n_reqs + Threads - 1) / Threads;
-    const int r0 = min(tid * per, n_reqs), r1 = min(r0 + per, n_reqs);
-    int mine = 0;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int upto = mine;
 #pragma unroll 1
-    for (int r = r0; r < r1; r++) mine += cost(r);
-    int upto = mine;  // inclusive scan
-#pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const int o = __shfl_up_sync(0xffffffffu, upto, d);
+        other += __shfl_xor_sync(0xffffffffu, other, d);
         if (lane >= d) upto += o;
     }
-    if (lane == 31) scratch[warp] = upto;
+    if (lane == 31) scratch[2 * warp] = upto, scratch[2 * warp + 1] = other;
     __syncthreads();
-    int total = 0;
+    total = other_total = 0;
 #pragma unroll 1
     for (int w = 0; w < Threads / 32; w++) {
         if (w == warp) upto += total;
-        total += scratch[w];
+        total += scratch[2 * w];
+        other_total += scratch[2 * w + 1];
     }
-    // no part is empty but the last ones
-    const int used = max(1, min(parts, least == 1 ? total : (total + least - 1) / least));
+    return upto;
+}
+
+// Finds a CTA's piece; every thread of the block calls it.  The line is made of n_reqs stretches, and `work`
+// says of one:
+//   measure(r, steps, units)   adds its length (less than 2^31 in all) and its units
+//   pieces(r, each)            its pieces when every unit is cut by itself into pieces of `each` steps
+//   own(r, k, each)            the k-th of them (each = 1: step k)
+// scratch: four words a warp.  Pieces of units are of at least `least` steps.
+//
+// Units are cut by themselves when that makes the longest piece at most four steps longer: a piece that
+// straddles two units pays twice for what a unit costs beside its tiles (queries, outputs, a join: 4 to 5
+// us).  Eight latent requests of 200 to 2000 tokens, 16 heads: 23 us in equal pieces, 19 us so.
+template <int Threads, typename Work>
+__device__ __forceinline__ Line find_piece(int n_reqs, int part, int parts, int least, int *scratch, Place *place, const Work &work)
+{
+    const int per = n_reqs <= Threads ? 1 : ceil_div(n_reqs, Threads);
+    const int r0 = min((int)threadIdx.x * per, n_reqs), r1 = min(r0 + per, n_reqs);
+    int mine = 0, units = 0, total, unit_total;
+#pragma unroll 1
+    for (int r = r0; r < r1; r++) work.measure(r, mine, units);
+    int at = block_scan<Threads>(mine, units, scratch, total, unit_total);
+    const int used = max(1, min(parts, total));
     Line line;
+    line.part = part;
+    line.nth = -1;
     line.each = (int)((uint32_t)total / (uint32_t)used);
     line.more = total - line.each * used;
     line.begin = part * line.each + min(part, line.more);
     line.steps = part < used ? line.each + (part < line.more) : 0;
-    if (line.steps > 0 && line.begin >= upto - mine && line.begin < upto) {
-        int rest = line.begin - (upto - mine);
+    int target = line.begin, cut = 1;
+    const int own = unit_total < parts ? max(least, ceil_div(total, parts - unit_total)) : 1 << 30;
+    const bool by_unit = own <= max(least, line.each + 4);
+    if (by_unit) {  // the same search over pieces instead of steps
+        line.each = cut = own;
+        target = part;
+        mine = 0;
+#pragma unroll 1
+        for (int r = r0; r < r1; r++) mine += work.pieces(r, own);
+        at = block_scan<Threads>(mine, 0, scratch + 2 * (Threads / 32), total, unit_total);
+    }
+    if (target < total && target >= at - mine && target < at) {
+        int rest = target - (at - mine);
 #pragma unroll 1
         for (int r = r0; r < r1; r++) {
-            const int all = r1 - r0 == 1 ? mine : cost(r);
-            if (rest < all) {
-                found(r, rest);
+            const int n = r1 - r0 == 1 ? mine : work.pieces(r, cut);
+            if (rest < n) {
+                *place = work.own(r, rest, cut);
                 break;
             }
-            rest -= all;
+            rest -= n;
         }
     }
     __syncthreads();
+    if (by_unit) {
+        line.steps = part < total ? place->steps : 0;
+        line.nth = place->nth;
+    }
     return line;
 }
 
-// This CTA's piece of an attention batch's line.
+// An attention batch's line.
+struct AttentionWork {
+    const Batch &b;
+    bool report;
+    __device__ __forceinline__ void measure(int r, int &steps, int &units) const
+    {
+        const Request q = load_request(b, r, report);
+        steps += head_cost(b, q) * b.kv_heads;
+        units += q.units * b.kv_heads;
+    }
+    __device__ __forceinline__ int head_pieces(const Request &q, int each) const
+    {
+        int n = 0;
+#pragma unroll 1
+        for (int j = 0; j < q.units; j++) n += ceil_div(unit_cost(make_unit(b, q, j)), each);
+        return n;
+    }
+    __device__ __forceinline__ int pieces(int r, int each) const { return head_pieces(load_request(b, r), each) * b.kv_heads; }
+    __device__ __forceinline__ Place own(int r, int k, int each) const
+    {
+        const Request q = load_request(b, r);
+        const int h = head_pieces(q, each);
+        Place p;
+        p.req = r;
+        p.head = (int)((uint32_t)k / (uint32_t)h);
+        k -= p.head * h;
+        int cost = 0;
+#pragma unroll 1
+        for (p.unit = 0;; p.unit++) {
+            cost = unit_cost(make_unit(b, q, p.unit));
+            const int n = ceil_div(cost, each);
+            if (k < n) break;
+            k -= n;
+        }
+        p.nth = k;
+        p.off = k * each;
+        p.steps = min(each, cost - p.off);
+        return p;
+    }
+};
+
+// This CTA's piece of it.
 template <int Threads>
 __device__ __forceinline__ Line find_place(const Batch &b, int part, int parts, int least, int *scratch, Place *place, bool report)
 {
-    return find_piece<Threads>(
-        b.n_reqs, part, parts, least, scratch, [&](int r) { return head_cost(b, load_request(b, r, report)) * b.kv_heads; },
-        [&](int r, int rest) {
-            const Request q = load_request(b, r);
-            const int h = head_cost(b, q);
-            Place p;
-            p.req = r;
-            p.head = (int)((uint32_t)rest / (uint32_t)h);
-            rest -= p.head * h;
-#pragma unroll 1
-            for (p.unit = 0;; p.unit++) {
-                const int n = unit_cost(make_unit(b, q, p.unit));
-                if (rest < n) break;
-                rest -= n;
-            }
-            p.off = rest;
-            *place = p;
-        });
+    return find_piece<Threads>(b.n_reqs, part, parts, least, scratch, place, AttentionWork{b, report});
 }
 
 // Walks a piece unit by unit.
