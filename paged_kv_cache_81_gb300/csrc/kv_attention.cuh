@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cmath>
+#include <type_traits>
 
 #include "kv_plan.cuh"
 #include "kv_tensor.cuh"
@@ -80,56 +81,63 @@ struct Output {
 // threads; a row's fragments are added in the order of their keys, so the result does not depend on which
 // CTA came last.  Row r is (first + r) / group of the request's tokens from q0 on, head head0 + the
 // rest.  Not inlined: its registers would crowd the loop over the key tiles.
-template <int DV, bool Bf16, int Batch, int Ahead>
+template <int DV, bool Bf16>
 __device__ __noinline__ void join_rows(const Output p, const float *ws, int c0, int count, int halves, int half, int stride, int row0, int rows, int stat,
                                        int first, int q0, int head0, const FastDiv group)
 {
-    // `Batch` column quads of `Ahead` fragments in flight: the loads take the time
-    constexpr int kBatch = Batch;
-    int shift = 4;             // rows rounded up to a power of two; the other threads share out the columns
+    // rows rounded up to a power of two; the other threads share out the columns (at least one quad each)
+    int shift = DV == 64 ? 3 : DV == 128 ? 2 : 1;
     while ((1 << shift) < rows) shift++;
     const int t = threadIdx.x & 127, row = row0 + (t & ((1 << shift) - 1)), parts = 128 >> shift, quads = DV / 4 / parts;
     const int quad0 = (t >> shift) * quads;
     if (row >= row0 + rows) return;
     const auto fragment = [&](int i) { return ws + (2 * ((c0 + i) * halves + half) + (i == 0)) * (int64_t)stride; };
     float top = -INFINITY;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = 0; i < count; i++) top = fmaxf(top, __ldcg(fragment(i) + stat * DV + row));
     const float z = top == -INFINITY ? 0.0f : top;
     const int tok = (int)fdiv((uint32_t)(first + row), group), head = head0 + first + row - tok * (int)group.d;
     const int64_t token = (int64_t)q0 + tok;
     char *to = p.out + token * p.out_token + (int64_t)head * p.out_head;
+    // `Batch` column quads of `Ahead` fragments in flight: the loads take the time
+    const auto columns = [&](auto batch, auto ahead) {
+        constexpr int kBatch = batch(), kAhead = ahead();
 #pragma unroll 1
-    for (int q = quad0; q < quad0 + quads; q += kBatch) {
-        float4 o[kBatch];
-        float l = 0.0f;
+        for (int q = quad0; q < quad0 + quads; q += kBatch) {
+            float4 o[kBatch];
+            float l = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kBatch; k++) o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll Ahead
-        for (int i = 0; i < count; i++) {
-            const float *part = fragment(i);
-            const float pm = __ldcg(part + stat * DV + row), pl = __ldcg(part + stat * (DV + 1) + row);
-            float4 v[kBatch];
+            for (int k = 0; k < kBatch; k++) o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll kAhead
+            for (int i = 0; i < count; i++) {
+                const float *part = fragment(i);
+                const float pm = __ldcg(part + stat * DV + row), pl = __ldcg(part + stat * (DV + 1) + row);
+                float4 v[kBatch];
 #pragma unroll
-            for (int k = 0; k < kBatch; k++)
-                if (k < quads) v[k] = __ldcg(reinterpret_cast<const float4 *>(part) + (q + k) * stat + row);
-            const float a = exp2_fast((pm - z) * p.c);
-            l += pl * a;
+                for (int k = 0; k < kBatch; k++)
+                    if (k < quads) v[k] = __ldcg(reinterpret_cast<const float4 *>(part) + (q + k) * stat + row);
+                const float a = exp2_fast((pm - z) * p.c);
+                l += pl * a;
 #pragma unroll
-            for (int k = 0; k < kBatch; k++)
-                if (k < quads) o[k].x += v[k].x * a, o[k].y += v[k].y * a, o[k].z += v[k].z * a, o[k].w += v[k].w * a;
-        }
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll
-        for (int k = 0; k < kBatch; k++)
-            if (k < quads && half * DV + (q + k) * 4 < p.dv) {
-                uint2 v;
-                v.x = pack2<Bf16>(o[k].x * inv, o[k].y * inv);
-                v.y = pack2<Bf16>(o[k].z * inv, o[k].w * inv);
-                *reinterpret_cast<uint2 *>(to + (half * DV + (q + k) * 4) * 2) = v;
+                for (int k = 0; k < kBatch; k++)
+                    if (k < quads) o[k].x += v[k].x * a, o[k].y += v[k].y * a, o[k].z += v[k].z * a, o[k].w += v[k].w * a;
             }
-        if (half == 0 && q == 0 && p.lse) p.lse[token * p.heads + head] = l > 0.0f ? fmaf(top, p.scale, logf(l)) : -INFINITY;
-    }
+            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll
+            for (int k = 0; k < kBatch; k++)
+                if (k < quads && half * DV + (q + k) * 4 < p.dv) {
+                    uint2 v;
+                    v.x = pack2<Bf16>(o[k].x * inv, o[k].y * inv);
+                    v.y = pack2<Bf16>(o[k].z * inv, o[k].w * inv);
+                    *reinterpret_cast<uint2 *>(to + (half * DV + (q + k) * 4) * 2) = v;
+                }
+            if (half == 0 && q == 0 && p.lse) p.lse[token * p.heads + head] = l > 0.0f ? fmaf(top, p.scale, logf(l)) : -INFINITY;
+        }
+    };
+    if (quads <= 4)
+        columns(std::integral_constant<int, 4>(), std::integral_constant<int, 6>());
+    else
+        columns(std::integral_constant<int, 8>(), std::integral_constant<int, 3>());
 }
 
 // 32 accumulator columns of a row into its fragment, as join_rows reads them.

@@ -11,8 +11,6 @@
 //   warps 0 and 2 load the two kinds of panels, warp 3 loads Q, warp 1 issues the products, warps 4-7 hold
 //   a row a thread (maximum, exponentials, P over S, lazy rescaling as in kv_attention.cu).  S of the next tile is formed before O += P V of
 //   this one, so the tensor core works while the exponentials run.
-#include <type_traits>
-
 #include "kv_attention.cuh"
 
 namespace pkv {
@@ -365,7 +363,7 @@ latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ C
             if (!whole) {
                 const Cut cut(line, w.pos - w.at.off, unit_cost(w.u));
                 if (last_of(p.counters + 2 * cut.c0 + half, cut.count, smem_addr(&aux.join), cuts, &aux.answer, wait, ok))
-                    join_rows<kHalf, Bf16, 8, 3>(p.o, p.ws, cut.c0, cut.count, 2, half, kRows * (kHalf + 2), 0, w.u.rows, kRows, w.u.row0, w.q.q0, 0, b.group);
+                    join_rows<kHalf, Bf16>(p.o, p.ws, cut.c0, cut.count, 2, half, kRows * (kHalf + 2), 0, w.u.rows, kRows, w.u.row0, w.q.q0, 0, b.group);
                 if (!ok) break;
             }
         } while (w.next(b));
