@@ -588,8 +588,12 @@ def _like_cache(dev: int, cache: PagedCache, dtype: torch.dtype, name: str) -> K
     return cache.desc()
 
 
-def _attn_outputs(dev: int, q: torch.Tensor, dv: int, out: Optional[torch.Tensor], lse: Optional[torch.Tensor], stream):
-    T, H, _ = q.shape
+def _attn_outputs(dev: int, q: torch.Tensor, T: int, H: int, dv: int, out: Optional[torch.Tensor], lse: Optional[torch.Tensor], stream):
+    """(out, its token and head strides in bytes, lse)."""
+    if out is None and lse is None and stream is None:
+        device = q.device
+        return (torch.empty((T, H, dv), dtype=q.dtype, device=device), H * dv * 2, dv * 2,
+                torch.empty((T, H), dtype=torch.float32, device=device))
     if out is None:
         out = _empty(q, (T, H, dv), q.dtype, stream)
     elif out.shape != (T, H, dv) or out.dtype is not q.dtype or out.get_device() != dev:
@@ -598,7 +602,8 @@ def _attn_outputs(dev: int, q: torch.Tensor, dv: int, out: Optional[torch.Tensor
         lse = _empty(q, (T, H), torch.float32, stream)
     elif lse.shape != (T, H) or lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.get_device() != dev:
         raise ValueError("lse must be a contiguous float32 [tokens, heads] tensor on q's device")
-    return out, lse
+    _, token, head = _rows3(out, "out")
+    return out, token, head, lse
 
 
 @functools.lru_cache(maxsize=256)
@@ -633,8 +638,7 @@ def kv_attention(q: torch.Tensor, cache: PagedCache, block_table: torch.Tensor, 
         raise ValueError("the cache's rows are not whole heads of q's width")
     dv = values.row_bytes // (kv_heads * 2)
     batch = _attn_batch(dev, block_table, q_offsets, kv_lens, T)
-    out, lse = _attn_outputs(dev, q, dv, out, lse, stream)
-    _, o_token, o_head = _rows3(out, "out")
+    out, o_token, o_head, lse = _attn_outputs(dev, q, T, H, dv, out, lse, stream)
     workspace = _workspace(kv_attention_workspace_bytes, dev, handle, workspace)
     _check("kv_attention", (_lib or load()).kv_attention(
         _attn_desc(code, H, kv_heads, dk, dv, causal, window, scale), batch, k_desc, k_tensor, 0, v_desc, v_tensor, values.n_planes - 1,
@@ -654,8 +658,7 @@ def kv_latent_attention(q: torch.Tensor, cache: PagedCache, block_table: torch.T
     c_desc = _like_cache(dev, cache, q.dtype, "cache")
     T, H, dk = q.shape
     batch = _attn_batch(dev, block_table, q_offsets, kv_lens, T)
-    out, lse = _attn_outputs(dev, q, LATENT_RANK, out, lse, stream)
-    _, o_token, o_head = _rows3(out, "out")
+    out, o_token, o_head, lse = _attn_outputs(dev, q, T, H, LATENT_RANK, out, lse, stream)
     workspace = _workspace(kv_attention_workspace_bytes, dev, handle, workspace)
     _check("kv_latent_attention", (_lib or load()).kv_latent_attention(
         _attn_desc(code, H, 1, dk, LATENT_RANK, causal, window, scale), batch, c_desc, tensor, q.data_ptr(), q_token, q_head,
