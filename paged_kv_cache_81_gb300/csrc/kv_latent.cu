@@ -197,6 +197,7 @@ latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ C
             const auto qk = [&](int i) {
                 const int n = it + i, s = n & 1;
                 const uint32_t d = tmem + kTmS + s * kKeys;
+                const bool v_here = Waiter::over(smem_addr(&aux.v_full[s]), (n >> 1) & 1);
                 if (!wait.warp(smem_addr(&aux.x_full[s]), (n >> 1) & 1)) return false;
                 const uint64_t xs = xd + s * (5 * kPanel >> 4), ks = kd + s * (4 * kPanel >> 4);
 #pragma unroll
@@ -204,7 +205,7 @@ latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ C
                     mma_ss(d, qd + (((kk / 4) * kQPanel + (kk % 4) * 32) >> 4), xs + (((kk / 4) * kPanel + (kk % 4) * 32) >> 4), qk_desc, kk > 0, elected);
                 tc_commit(smem_addr(&aux.x_empty[s]), elected);
                 if (i + 1 == w.n) tc_commit(smem_addr(&aux.q_empty), elected);
-                if (!wait.warp(smem_addr(&aux.v_full[s]), (n >> 1) & 1)) return false;
+                if (!__all_sync(0xffffffffu, v_here) && !wait.warp(smem_addr(&aux.v_full[s]), (n >> 1) & 1)) return false;
 #pragma unroll
                 for (int kk = 0; kk < 16; kk++)
                     mma_ts(d, tmem + kTmQ + kk * 8, ks + (((kk / 4) * kPanel + (kk % 4) * 32) >> 4), qk_desc, true, elected);

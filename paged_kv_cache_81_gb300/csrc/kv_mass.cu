@@ -325,12 +325,11 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
                 const int s = it % S::kNQ;
                 const int rows = min(p.step_tokens, w.k.t1 - w.k.t0 - qi * p.step_tokens) * group;
                 const uint32_t desc = mma_desc(Bf16, 128, (uint32_t)(rows + 15) & ~15u, false);
-                if (i == 0 || qi == 0) {
-                    kt++;
-                    ok = wait.warp(smem_addr(&aux.k_full[kt % S::kNK]), (kt / S::kNK) & 1);
-                }
-                ok = ok && wait.warp(smem_addr(&aux.q_full[s]), (it / S::kNQ) & 1) &&
-                     (it < 4 || wait.warp(smem_addr(&aux.s_empty[it & 3]), ((it >> 2) - 1) & 1));
+                if (i == 0 || qi == 0) kt++;  // another head's K
+                const uint32_t k_bar = smem_addr(&aux.k_full[kt % S::kNK]), q_bar = smem_addr(&aux.q_full[s]);
+                const uint32_t k_parity = (kt / S::kNK) & 1, q_parity = (it / S::kNQ) & 1;
+                ok = it < 4 ? wait.warp(k_bar, k_parity, q_bar, q_parity)
+                            : wait.warp(k_bar, k_parity, q_bar, q_parity, smem_addr(&aux.s_empty[it & 3]), ((it >> 2) - 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t ka = kd + (kt % S::kNK) * (S::kOperand >> 4), qa = qd + s * (S::kOperand >> 4);

@@ -49,6 +49,31 @@ struct Waiter {
     {
         return __all_sync(0xffffffffu, one(bar, parity));
     }
+    // Whether the phase is over, without waiting.
+    static __device__ __forceinline__ bool over(uint32_t bar, uint32_t parity)
+    {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        return ok != 0;
+    }
+    // Two and three waits at once: asked one after another, each costs the issuing warp about 100 cycles in
+    // which it feeds the tensor core nothing, ready or not.
+    __device__ __forceinline__ bool warp(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1) const
+    {
+        const bool a = over(bar0, parity0), b = over(bar1, parity1);
+        return __all_sync(0xffffffffu, a && b) || (warp(bar0, parity0) && warp(bar1, parity1));
+    }
+    __device__ __forceinline__ bool warp(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1, uint32_t bar2, uint32_t parity2) const
+    {
+        const bool a = over(bar0, parity0), b = over(bar1, parity1), c = over(bar2, parity2);
+        return __all_sync(0xffffffffu, a && b && c) || (warp(bar0, parity0) && warp(bar1, parity1) && warp(bar2, parity2));
+    }
 };
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar)
