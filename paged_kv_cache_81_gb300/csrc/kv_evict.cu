@@ -18,7 +18,7 @@ namespace pkv {
 
 namespace {
 
-constexpr int kSelectThreads = 1024, kPer = 4;
+constexpr int kSelectThreads = 1024, kPer = 8;  // scores that a thread has in flight
 constexpr int kMoveThreads = 256, kUnroll = 8, kMoveRows = 256;  // a chunk: up to 2048 vectors of up to 256 rows
 
 struct Select {
@@ -40,6 +40,17 @@ __device__ __forceinline__ uint32_t order_key(float x)
     if (!(x == x)) return 0;
     uint32_t u = __float_as_uint(x + 0.0f);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// Inclusive scan over a warp's lanes.
+__device__ __forceinline__ uint32_t warp_scan(uint32_t x)
+{
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xffffffffu, x, d);
+        if ((threadIdx.x & 31) >= d) x += o;
+    }
+    return x;
 }
 
 __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Select p)
@@ -73,21 +84,32 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Sele
 #pragma unroll
         for (int pass = 0; pass < 3; pass++) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
+            const uint32_t zero_bin = (0x80000000u >> shift) & (bins - 1);
             for (int i = tid; i < bins; i += kSelectThreads) hist[i] = 0;
             __syncthreads();
-            for (int j0 = a; j0 < z; j0 += kSelectThreads) {
-                const int j = j0 + tid;
-                uint32_t bin = 0xffffffffu;
-                if (j < z) {
-                    const uint32_t k = order_key(score[j]);
-                    if ((k & mask) == prefix) bin = (k >> shift) & (bins - 1);
+            for (int j0 = a; j0 < z; j0 += kSelectThreads * kPer) {
+                float s[kPer];
+#pragma unroll
+                for (int i = 0; i < kPer; i++) {
+                    const int j = j0 + i * kSelectThreads + tid;
+                    s[i] = j < z ? score[j] : 0.0f;
                 }
-                // a warp whose tokens all fall into one bin (zeros do) adds once
-                const uint32_t first = __shfl_sync(0xffffffffu, bin, 0);
-                if (__all_sync(0xffffffffu, bin == first)) {
-                    if (lane == 0 && first != 0xffffffffu) atomicAdd(&hist[first], 32);
-                } else if (bin != 0xffffffffu) {
-                    atomicAdd(&hist[bin], 1);
+#pragma unroll
+                for (int i = 0; i < kPer; i++) {
+                    if (j0 + i * kSelectThreads >= z) break;
+                    uint32_t bin = 0xffffffffu;
+                    if (j0 + i * kSelectThreads + tid < z) {
+                        const uint32_t k = order_key(s[i]);
+                        if ((k & mask) == prefix) bin = (k >> shift) & (bins - 1);
+                    }
+                    // zeros (most weights of a long request) are added once a warp: their additions to one word
+                    // would go one by one
+                    const uint32_t zeros = __ballot_sync(0xffffffffu, bin == zero_bin);
+                    if (bin == zero_bin) {
+                        if (lane == __ffs(zeros) - 1) atomicAdd(&hist[bin], __popc(zeros));
+                    } else if (bin != 0xffffffffu) {
+                        atomicAdd(&hist[bin], 1);
+                    }
                 }
             }
             __syncthreads();
@@ -95,16 +117,11 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Sele
             const int each = bins / kSelectThreads;
             uint32_t c[2] = {0, 0}, mine = 0;
             for (int i = 0; i < each; i++) mine += c[i] = hist[bins - 1 - (tid * each + i)];
-            uint32_t upto = mine;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const uint32_t o = __shfl_up_sync(0xffffffffu, upto, d);
-                if (lane >= d) upto += o;
-            }
+            const uint32_t upto = warp_scan(mine);
             if (lane == 31) sums[warp] = upto;
             __syncthreads();
-            for (int w = 0; w < warp; w++) upto += sums[w];
-            uint32_t before = upto - mine;
+            const uint32_t warps = warp_scan(sums[lane]), earlier = __shfl_sync(0xffffffffu, warps, (warp - 1) & 31);
+            uint32_t before = upto - mine + (warp ? earlier : 0);
             for (int i = 0; i < each; i++) {
                 if (before < want && before + c[i] >= want) {
                     picked[0] = (uint32_t)(bins - 1 - (tid * each + i));
@@ -128,9 +145,12 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Sele
 #pragma unroll
         for (int i = 0; i < kPer; i++) {
             const int j = j0 + tid * kPer + i;
-            s[i] = 0.0f;
+            s[i] = j < len ? score[j] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; i++) {
+            const int j = j0 + tid * kPer + i;
             if (j < len) {
-                s[i] = score[j];
                 const uint32_t k = order_key(s[i]);
                 if (j < a || j >= z || (some && k > prefix)) {
                     flags |= 1u << (2 * i);
@@ -141,20 +161,12 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Sele
                 }
             }
         }
-        uint32_t upto = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const uint32_t o = __shfl_up_sync(0xffffffffu, upto, d);
-            if (lane >= d) upto += o;
-        }
+        const uint32_t upto = warp_scan(mine);
         if (lane == 31) sums[warp] = upto;
         __syncthreads();  // also: every score of these tokens has been read before any is written
-        uint32_t all = 0;
-        for (int w = 0; w < 32; w++) {
-            if (w == warp) upto += all;
-            all += sums[w];
-        }
-        uint32_t sure = sure0 + ((upto - mine) & 0xffff), ties = ties0 + ((upto - mine) >> 16);
+        const uint32_t warps = warp_scan(sums[lane]), all = __shfl_sync(0xffffffffu, warps, 31);
+        const uint32_t earlier = __shfl_sync(0xffffffffu, warps, (warp - 1) & 31), at0 = upto - mine + (warp ? earlier : 0);
+        uint32_t sure = sure0 + (at0 & 0xffff), ties = ties0 + (at0 >> 16);
 #pragma unroll
         for (int i = 0; i < kPer; i++) {
             const uint32_t f = (flags >> (2 * i)) & 3;
