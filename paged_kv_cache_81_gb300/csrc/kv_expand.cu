@@ -3,7 +3,7 @@
 //   K[j, h] = [ W[h, 0:128] c_j ; rope_j ]     V[j, h] = W[h, 128:256] c_j       (c_j: 512 values, rope_j: 64)
 //
 // One product of 128 tokens by 128 columns (a head's keys, or its values) over 512.  A CTA keeps its token
-// tile's latents in tensor memory (256 columns; they come by TMA, page by page, through shared memory) and
+// tile's latents in tensor memory (256 columns; they come by TMA, page by page, through 64 KB of shared memory) and
 // streams the heads' weights past them in panels of 64 by 128: shared memory then moves 64 bytes a cycle in and
 // 64 out, its rate, where both operands from there were a quarter over it.  Two accumulators of 128 columns,
 // one for keys and one for values, each rounded and written by a warp group while the other is formed.  The line (kv_plan.cuh) runs over requests, token
@@ -19,9 +19,9 @@ constexpr int kThreads = 384;
 constexpr int kTile = 128;
 constexpr int kRank = 512, kRope = 64, kNope = 128, kV = 128, kN = kNope + kV;
 constexpr uint32_t kAPanel = kTile * 128, kBPanel = kNope * 128;
-constexpr int kStages = 6;
+constexpr int kStages = 10, kAPart = 4;  // panels of latents that stand in shared memory at a time
 constexpr uint32_t kTmA = 256;  // accumulators: columns 0 and 128
-constexpr uint32_t kOffB = 8 * kAPanel, kOffAux = kOffB + kStages * kBPanel, kBytes = kOffAux + 1024;
+constexpr uint32_t kOffB = kAPart * kAPanel, kOffAux = kOffB + kStages * kBPanel, kBytes = kOffAux + 1024;
 
 struct Params {
     const int32_t *kv_lens;
@@ -39,7 +39,7 @@ struct Params {
 };
 
 struct Aux {
-    uint64_t a_full, a_moved, b_full[kStages], b_empty[kStages], d_full[2], d_empty[2];
+    uint64_t a_full, a_moved[2], b_full[kStages], b_empty[kStages], d_full[2], d_empty[2];
     int scan[48];
     Place place;
     uint32_t tmem;
@@ -118,7 +118,7 @@ expand_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__
     if (tid == 0) {
         aux.gave_up = 0;
         mbar_init(smem_addr(&aux.a_full), 1);
-        mbar_init(smem_addr(&aux.a_moved), 8);
+        for (int i = 0; i < 2; i++) mbar_init(smem_addr(&aux.a_moved[i]), 8);  // the halves of a tile
         for (int i = 0; i < kStages; i++) mbar_init(smem_addr(&aux.b_full[i]), 1), mbar_init(smem_addr(&aux.b_empty[i]), 1);
         for (int i = 0; i < 2; i++) mbar_init(smem_addr(&aux.d_full[i]), 1), mbar_init(smem_addr(&aux.d_empty[i]), 4);
         mbar_init_fence();
@@ -136,33 +136,42 @@ expand_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__
     Walk w;
     if (!w.start(p, aux, line.steps)) {
         // nothing to do: on to the common exit
-    } else if (warp == 0) {
+    } else if (warp == 2) {
+        // ---- latents: half of a token tile's panels at a time, each as soon as the one before has been moved on ----
         const int pr = p.piece_rows;
-        int frag = 0, it = 0;
+        int round = 0;
         bool ok = true;
         do {
             const int kb = w.tile * kTile, p1 = (min(w.len - kb, kTile) + pr - 1) / pr;
             const int32_t *row = p.table + (int64_t)w.req * p.table_stride;
             const uint32_t abar = smem_addr(&aux.a_full);
-            if (frag && !wait.warp(smem_addr(&aux.a_moved), (frag - 1) & 1)) break;
-            if (lane == 0) mbar_arrive_expect_tx(abar, (uint32_t)(p1 * pr) * kRank * 2);
-            __syncwarp();
-            for (int j = lane; j < p1; j += 32) {
-                const uint32_t key = (uint32_t)(kb + j * pr), col = fdiv(key, p.block);
-                int page = __ldg(row + col);
-                if (page < 0 || page >= p.num_blocks) {
-                    set_error(p.err, KV_DERR_TABLE);
-                    page = p.num_blocks;  // outside the map: reads zeros
-                }
+            for (int part = 0; part < 8; part += kAPart, round++) {
+                if (round && !(ok = wait.warp(smem_addr(&aux.a_moved[(round - 1) & 1]), ((round - 1) >> 1) & 1))) break;
+                if (lane == 0) mbar_arrive_expect_tx(abar, (uint32_t)(p1 * pr) * kAPart * 128);
+                __syncwarp();
+                for (int j = lane; j < p1; j += 32) {
+                    const uint32_t key = (uint32_t)(kb + j * pr), col = fdiv(key, p.block);
+                    int page = __ldg(row + col);
+                    if (page < 0 || page >= p.num_blocks) {
+                        set_error(p.err, KV_DERR_TABLE);
+                        page = p.num_blocks;  // outside the map: reads zeros
+                    }
 #pragma unroll
-                for (int h = 0; h < 8; h++)
-                    tma_load_4d(base + h * kAPanel + j * pr * 128, &a_map, abar, h * 64, 0, (int)(key - col * p.block.d), page);
+                    for (int h = 0; h < kAPart; h++)
+                        tma_load_4d(base + h * kAPanel + j * pr * 128, &a_map, abar, (part + h) * 64, 0, (int)(key - col * p.block.d), page);
+                }
+                __syncwarp();
             }
-            frag++;
+        } while (ok && w.next(p));
+    } else if (warp == 0) {
+        // ---- weights ----
+        int it = 0;
+        bool ok = true;
+        do {
             for (int h = 0; ok && h < 2 * w.n; h++)
                 for (int kk = 0; kk < 8; kk++, it++) {
                     const int s = it % kStages;
-                    if (it >= kStages && !wait.warp(smem_addr(&aux.b_empty[s]), ((it / kStages) - 1) & 1)) { ok = false; break; }
+                    if (it >= kStages && !(ok = wait.warp(smem_addr(&aux.b_empty[s]), ((it / kStages) - 1) & 1))) break;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(smem_addr(&aux.b_full[s]), kBPanel);
                         tma_load_3d(base + kOffB + s * kBPanel, &w_map, smem_addr(&aux.b_full[s]), kk * 64, (h & 1) * kNope, w.head + (h >> 1));
@@ -174,10 +183,11 @@ expand_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__
         constexpr uint32_t desc = mma_desc(Bf16, 128, kNope, false);
         const uint32_t elected = elect_one();
         const uint64_t bd = smem_desc(base + kOffB, 16, 1024);
-        int frag = 0, it = 0, heads = 0;
+        int it = 0, heads = 0, frag = 0;
         bool ok = true;
         do {
-            ok = wait.warp(smem_addr(&aux.a_moved), frag++ & 1);
+            ok = wait.warp(smem_addr(&aux.a_moved[0]), frag & 1) && wait.warp(smem_addr(&aux.a_moved[1]), frag & 1);
+            frag++;
             tc_fence_after();
             for (int h = 0; ok && h < w.n; h++, heads++)
                 for (int d = 0; ok && d < 2; d++) {
@@ -199,7 +209,8 @@ expand_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__
         const int g = (warp - 4) >> 2, t = tid & 127;  // group 0 writes the keys, group 1 the values
         const uint32_t mine = (uint32_t)((warp & 3) * 32) << 16;
         const int row_bytes = (g ? kV : kNope + kRope) * 2;
-        int heads = 0, frag = 0;
+        int heads = 0;
+        bool frag = false;  // a tile before this one
         bool ok = true;
         do {
             const int tok = w.tile * kTile + t;
@@ -235,21 +246,25 @@ expand_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__
             // the tile's latents into tensor memory, half of the panels a group.  Both groups have waited for their
             // last products of the tile before, and the other group's came no later than one product more
             if (frag && !wait.warp(smem_addr(&aux.d_full[1]), (heads - 1) & 1)) break;
-            if (!wait.warp(smem_addr(&aux.a_full), frag++ & 1)) break;
+            frag = true;
+            for (int part = 0; part < 8; part += kAPart) {
+                if (!(ok = wait.warp(smem_addr(&aux.a_full), (part / kAPart) & 1))) break;
 #pragma unroll 1
-            for (int q = 4 * g; q < 4 * g + 4; q++) {
-                uint32_t x[32];
+                for (int i = g; i < kAPart; i += 2) {
+                    uint32_t x[32];
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const uint4 v = ld_smem16(base + q * kAPanel + panel_off(t, i));
-                    x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+                    for (int j = 0; j < 8; j++) {
+                        const uint4 v = ld_smem16(base + i * kAPanel + panel_off(t, j));
+                        x[4 * j] = v.x, x[4 * j + 1] = v.y, x[4 * j + 2] = v.z, x[4 * j + 3] = v.w;
+                    }
+                    tmem_st32(tmem + kTmA + (part + i) * 32 + mine, x);
                 }
-                tmem_st32(tmem + kTmA + q * 32 + mine, x);
+                tc_wait_st();
+                tc_fence_before();
+                fence_async_smem();  // the loads before the TMA that overwrites what they read
+                warp_arrive(smem_addr(&aux.a_moved[part / kAPart]));
             }
-            tc_wait_st();
-            tc_fence_before();
-            fence_async_smem();  // the loads before the TMA that overwrites what they read
-            warp_arrive(smem_addr(&aux.a_moved));
+            if (!ok) break;
             for (int h = 0; h < w.n; h++, heads++) {
                 const int head = w.head + h;
                 if (!wait.warp(smem_addr(&aux.d_full[g]), heads & 1)) { ok = false; break; }
