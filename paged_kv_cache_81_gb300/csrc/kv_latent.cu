@@ -236,24 +236,10 @@ latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ C
         const float slack = 8.0f / p.o.c;
         int it = 0, cuts = 0, units = 0;
         bool ok = true;
-        do {
-            const bool live = t < w.u.rows;
-            const int r = w.u.row0 + min(t, w.u.rows - 1);
-            const int tok = (int)fdiv((uint32_t)r, b.group), head = r - tok * (int)b.group.d;
-            const int64_t out_row = (int64_t)(w.q.q0 + tok);
-            char *to = p.o.out + out_row * p.o.out_token + (int64_t)head * p.o.out_head + half * kHalf * 2;
-            if (w.u.tiles == 0) {
-                if (live) {
-                    for (int col = 0; col < kHalf; col += 8) *reinterpret_cast<uint4 *>(to + col * 2) = make_uint4(0, 0, 0, 0);
-                    if (p.o.lse && half == 0) p.o.lse[out_row * p.o.heads + head] = -INFINITY;
-                }
-                continue;
-            }
-            const bool warp_live = __any_sync(0xffffffffu, live);
-            // Q's four panels into tensor memory (the last unit's accumulator was complete, so its scores were too)
-            if (!wait.warp(smem_addr(&aux.q_staged), units & 1)) { ok = false; break; }
-            units++;
-            if (warp_live) {
+        // A unit's four panels of Q into tensor memory, once the scores of the unit before are out.
+        const auto move_q = [&](const Unit &u) {
+            if (!wait.warp(smem_addr(&aux.q_staged), units++ & 1)) return false;
+            if (__any_sync(0xffffffffu, t < u.rows)) {
 #pragma unroll 1
                 for (int q = 0; q < kQT; q++) {
                     uint32_t x[32];
@@ -269,6 +255,24 @@ latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ C
             tc_fence_before();
             fence_async_smem();  // the loads before the TMA that overwrites what they read
             warp_arrive(smem_addr(&aux.q_moved));
+            return true;
+        };
+        bool moved = false;  // the unit's Q is on its way already
+        do {
+            const bool live = t < w.u.rows;
+            const int r = w.u.row0 + min(t, w.u.rows - 1);
+            const int tok = (int)fdiv((uint32_t)r, b.group), head = r - tok * (int)b.group.d;
+            const int64_t out_row = (int64_t)(w.q.q0 + tok);
+            char *to = p.o.out + out_row * p.o.out_token + (int64_t)head * p.o.out_head + half * kHalf * 2;
+            if (w.u.tiles == 0) {
+                if (live) {
+                    for (int col = 0; col < kHalf; col += 8) *reinterpret_cast<uint4 *>(to + col * 2) = make_uint4(0, 0, 0, 0);
+                    if (p.o.lse && half == 0) p.o.lse[out_row * p.o.heads + head] = -INFINITY;
+                }
+                continue;
+            }
+            const bool warp_live = __any_sync(0xffffffffu, live);
+            if (!moved && !(ok = move_q(w.u))) break;
             int lo, hi;
             sees(b, w.q, tok, lo, hi);
             float m = -INFINITY, l = 0.0f;
@@ -333,6 +337,13 @@ latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ C
             }
             if (!ok) break;
             it += w.n;
+            // the next unit's Q now, so that its first scores are formed while this one's rows are written
+            {
+                Walk nx = w;
+                moved = false;
+                while (!moved && nx.next(b)) moved = nx.u.tiles > 0;
+                if (moved && !(ok = move_q(nx.u))) break;
+            }
             if (!wait.warp(smem_addr(&aux.o_done[(it - 1) & 1]), ((it - 1) >> 1) & 1)) { ok = false; break; }
             tc_fence_after();
             const bool whole = w.whole();
