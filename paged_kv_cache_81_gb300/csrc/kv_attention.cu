@@ -66,6 +66,10 @@ struct Aux {
 };
 static_assert(sizeof(Aux) <= 2048, "bookkeeping");
 
+// Which runs of 32 keys of the tile that begins at key kb some row of the unit sees: [from, to).
+__device__ __forceinline__ int seen_from(const Unit &u, int kb) { return max(0, u.lo - kb) >> 5; }
+__device__ __forceinline__ int seen_to(const Unit &u, int kb) { return (min(u.hi - kb, kTile) + 31) >> 5; }
+
 // One tile of K or V rows into its slot: a TMA per (run of slots inside a page, panel), spread over the
 // lanes.  The first page a lane needs is looked up before `ready` waits for the slot.
 template <int Panels, typename Ready>
@@ -223,10 +227,11 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                 ok = wait.warp(smem_addr(&aux.p_ready[s]), steps[s]++ & 1) &&
                      ((both && s) || wait.warp(smem_addr(&aux.v_full[slot]), (vt / S::kNV) & 1));
                 if (!ok) break;
-                // rows of V that no query sees must not reach the product: they may hold anything
-                const int kb = (w.u.tile0 + w.at.off + vt - it) * kTile;
+                // the tile's runs of 32 keys that some query sees; in them, rows of V that none sees must not reach the
+                // product: they may hold anything
+                const int kb = (w.u.tile0 + w.at.off + vt - it) * kTile, q0 = seen_from(w.u, kb), q1 = seen_to(w.u, kb);
                 if (!(both && s) && (kb < w.u.lo || kb + kTile > w.u.hi)) {
-                    for (int r = lane >> 3; r < kTile; r += 4)
+                    for (int r = 32 * q0 + (lane >> 3); r < 32 * q1; r += 4)
                         if (kb + r < w.u.lo || kb + r >= w.u.hi)
 #pragma unroll
                             for (int h = 0; h < DV / 64; h++)
@@ -238,7 +243,8 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                 const uint64_t va = vd + slot * (S::kV >> 4);
 #pragma unroll
                 for (int kk = 0; kk < 8; kk++)
-                    mma_ts(tmem + 256 + s * 128, tmem + s * 128 + 64 + kk * 8, va + kk * (2048 >> 4), pv_desc, i >= 2 || kk > 0, elected);
+                    mma_ts(tmem + 256 + s * 128, tmem + s * 128 + 64 + kk * 8, va + kk * (2048 >> 4), pv_desc, i >= 2 || kk > 2 * q0,
+                           elected && kk >= 2 * q0 && kk < 2 * q1);
                 if (!both || s == 1) tc_commit(smem_addr(&aux.v_empty[slot]), elected);
                 tc_commit(smem_addr(&aux.o_done[s]), elected);  // last: the groups wait for it before the CTA ends
                 if (i + 2 < n) ok = qk(i + 2);
@@ -258,20 +264,25 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
             const bool both = w.u.rows > half;
             const int row = (both ? g * half : 0) + t;         // row of the unit
             const bool live = t < half && row < w.u.rows;
-            const int r = w.u.row0 + min(row, w.u.rows - 1);   // row of the request; spare rows repeat the last
-            const int tok = (int)fdiv((uint32_t)r, b.group), head = w.at.head * (int)b.group.d + r - tok * (int)b.group.d;
-            const int64_t out_row = (int64_t)(w.q.q0 + tok);
-            char *to = p.o.out + out_row * p.o.out_token + (int64_t)head * p.o.out_head;
+            // where the row's output and its lse go (asked for after the key tiles: held over them it would spill)
+            const auto place = [&](float *&lse) {
+                const int r = w.u.row0 + row, tok = (int)fdiv((uint32_t)r, b.group), head = w.at.head * (int)b.group.d + r - tok * (int)b.group.d;
+                const int64_t token = w.q.q0 + tok;
+                lse = p.o.lse ? p.o.lse + token * p.o.heads + head : nullptr;
+                return p.o.out + token * p.o.out_token + (int64_t)head * p.o.out_head;
+            };
             if (w.u.tiles == 0) {  // nothing is seen
                 if (live && (both || g == 0)) {
+                    float *lse;
+                    char *to = place(lse);
                     for (int col = 0; col < p.o.dv; col += 8) *reinterpret_cast<uint4 *>(to + col * 2) = make_uint4(0, 0, 0, 0);
-                    if (p.o.lse) p.o.lse[out_row * p.o.heads + head] = -INFINITY;
+                    if (lse) *lse = -INFINITY;
                 }
                 continue;
             }
-            // key tiles
+            // key tiles; spare rows see what the last one does
             int lo, hi;
-            sees(b, w.q, tok, lo, hi);
+            sees(b, w.q, (int)fdiv((uint32_t)(w.u.row0 + min(row, w.u.rows - 1)), b.group), lo, hi);
             const bool warp_live = __any_sync(0xffffffffu, live);
             float m = -INFINITY, l = 0.0f;
             const int first = both ? 0 : g, step = both ? 1 : 2, kt0 = w.u.tile0 + w.at.off;
@@ -291,7 +302,7 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                     if (hide) {
                         top = -INFINITY;
 #pragma unroll 1
-                        for (int q = 0; q < 4; q++) {
+                        for (int q = seen_from(w.u, kb); q < seen_to(w.u, kb); q++) {
                             tmem_ld32(s_at + q * 32, x0);
                             tc_wait_ld();
                             hide32(x0, from - q * 32, to_key - q * 32);
@@ -338,7 +349,7 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                     // going down no score is overwritten before it has been read
                     if (hide) {
 #pragma unroll 1
-                        for (int q = 3; q >= 0; q--) {
+                        for (int q = seen_to(w.u, kb) - 1; q >= seen_from(w.u, kb); q--) {
                             tmem_ld32(s_at + q * 32, x0);
                             tc_wait_ld();
                             hide32(x0, from - q * 32, to_key - q * 32);
@@ -405,7 +416,8 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
             const bool whole = w.whole();
             const float inv = l > 0.0f ? 1.0f / l : 0.0f;
             const int slot = 2 * blockIdx.x + (w.at.off == 0 ? 1 : 0);
-            float *part = p.ws + (int64_t)slot * (kRows * (DV + 2));
+            float *part = p.ws + (int64_t)slot * (kRows * (DV + 2)), *lse = nullptr;
+            char *to = live ? place(lse) : nullptr;
             if (warp_live) {
 #pragma unroll 1
                 for (int q = 0; q < DV / 32; q++) {
@@ -428,13 +440,13 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                         for (int i = 0; i < 32; i++) f[i] = 0.0f;
                     }
                     if (whole)
-                        store_rows32<Bf16>(live ? to : nullptr, f, inv, q * 32, p.o.dv);
+                        store_rows32<Bf16>(to, f, inv, q * 32, p.o.dv);
                     else if (live)
                         store_fragment32(part, kRows, row, q, f);
                 }
                 if (live) {
                     if (whole) {
-                        if (p.o.lse) p.o.lse[out_row * p.o.heads + head] = l > 0.0f ? fmaf(m, p.o.scale, logf(l)) : -INFINITY;
+                        if (lse) *lse = l > 0.0f ? fmaf(m, p.o.scale, logf(l)) : -INFINITY;
                     } else {
                         part[kRows * DV + row] = m;
                         part[kRows * DV + kRows + row] = l;

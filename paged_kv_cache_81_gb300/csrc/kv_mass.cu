@@ -10,8 +10,8 @@
 // from its pieces' partial sums, in their order, by whichever CTA finishes the last of them.
 //   warps 0 and 2 load K once a head, warp 3 Q and warps 12 and 13 its rows' normalisers a step, warp 1
 //   issues the products into four accumulators (all of tensor memory: the exponentials take longer than
-//   the products), warps 4-7 and 8-11 take the even and the odd steps.  Warp 2 first carries over what
-//   lies past the lengths.
+//   the products), warps 4-7 and 8-11 take the even and the odd steps.  Warp 2 ends with what lies past
+//   the requests' lengths.
 #include "kv_attention.cuh"
 
 namespace pkv {
@@ -210,15 +210,6 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, aux.tmem, 0);
-    if (warp == 2) {
-        // what lies past every request's length is carried over
-        const int me = blockIdx.x * 32 + lane, all = gridDim.x * 32;
-        for (int r = 0; r < b.n_reqs; r++) {
-            const int len = min(max(__ldg(b.kv_lens + r), 0), b.max_tokens);
-            for (int j = len + me; j < p.width; j += all)
-                p.score[(int64_t)r * p.score_stride + j] = p.prev ? p.prev[(int64_t)r * p.prev_stride + j] : 0.0f;
-        }
-    }
     Walk2 w;
     if (!w.start(p, aux.place, line)) {
         // nothing to do: on to the common exit
@@ -436,6 +427,23 @@ mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
             tiles++;
         } while (w.next(p));
         (void)ok;
+    }
+    if (warp == 2) {
+        // what lies past every request's length is carried over, a piece of up to 1024 columns at a time
+        const int each = (p.width + 1023) >> 10;
+#pragma unroll 1
+        for (int i = blockIdx.x; i < b.n_reqs * each; i += gridDim.x) {
+            const int r = i / each, j0 = (i - r * each) << 10, len = min(max(__ldg(b.kv_lens + r), 0), b.max_tokens);
+            const int end = min(j0 + 1024, p.width);
+            for (int j = max(j0, len) + lane; j < end; j += 256) {
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; k++) v[k] = p.prev && j + 32 * k < end ? p.prev[(int64_t)r * p.prev_stride + j + 32 * k] : 0.0f;
+#pragma unroll
+                for (int k = 0; k < 8; k++)
+                    if (j + 32 * k < end) p.score[(int64_t)r * p.score_stride + j + 32 * k] = v[k];
+            }
+        }
     }
     // common exit
     __syncwarp();
