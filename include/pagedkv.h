@@ -418,10 +418,11 @@ typedef struct {
 } kv_attn_batch;
 
 /*
- * Softmax attention.  Query head h uses key head h / (n_heads / n_kv_heads).  causal: a token sees keys
+ * Softmax attention.  Query head h uses key head h / (n_heads / n_kv_heads), at most 128 query heads a key head
+ * (KV_ERR_UNSUPPORTED; kv_latent_attention takes any number).  causal: a token sees keys
  * at positions <= its own; otherwise all kv_lens[r].  window > 0 (causal only): of these only the last
- * `window`, and pages wholly before them are never read, so their table entries may be stale.  scale > 0
- * multiplies the products.
+ * `window`, and pages wholly before them are never read, so their table entries may be stale.  scale, in
+ * [1e-30, 1e30], multiplies the products.
  */
 typedef struct {
     int32_t dtype; /* KV_BF16 or KV_F16: of q, the cache and out */
@@ -455,7 +456,10 @@ KV_API int kv_attention_workspace_bytes(int64_t *bytes_out);
  *    [0, max_blocks_per_req * block_size] is clamped, and a table entry outside the cache reads as a
  *    page of zeros: both set KV_DERR_TABLE.
  *  - out must not overlap q, the cache or the workspace.
- * Limits: n_tokens * n_heads and max_blocks_per_req * block_size <= 2^30 (KV_ERR_UNSUPPORTED).
+ * Limits (KV_ERR_UNSUPPORTED): n_tokens * n_heads and max_blocks_per_req * block_size <= 2^30, and the
+ * capacity's work, (n_tokens * n_heads / 256 + n_reqs * n_kv_heads) units of rows times max_blocks_per_req *
+ * block_size / 128 tiles of keys, below 2^31.  Pages of fewer than 16 slots cost more: one TMA brings a run of slots
+ * inside a page, and a long decode batch runs at 97% of the memory's rate with pages of 16 slots, at 78% with 8.
  * The result does not depend on timing: the same call gives the same bits.
  */
 KV_API int kv_attention(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_cache_desc *k, int32_t k_tensor,

@@ -610,7 +610,7 @@ int kv_attention(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_cac
                  int64_t workspace_bytes, kv_stream_t stream)
 {
     if (d == nullptr || d->n_heads <= 0 || d->n_kv_heads <= 0 || d->n_heads % d->n_kv_heads != 0 || d->head_dim <= 0 ||
-        d->head_dim_v <= 0 || d->window < 0 || !(d->scale > 0.0f) || !std::isfinite(d->scale) ||
+        d->head_dim_v <= 0 || d->window < 0 || !good_scale(d->scale) ||
         (d->dtype != KV_BF16 && d->dtype != KV_F16))
         return KV_ERR_INVALID_ARG;
     int st = check_batch(batch);

@@ -17,6 +17,9 @@ constexpr int64_t kCounterBytes = 16384;  // arrival counts of cut units, zero b
 inline int64_t attention_workspace(int num_sms) { return kCounterBytes + (int64_t)num_sms * 2 * 256 * (128 + 2) * 4; }
 
 int check_batch(const kv_attn_batch *t);
+// A factor of the products that the kernels take: 8 / (scale log2 e), by which the maximum may grow before an
+// accumulator is rescaled, and its reciprocal stay finite.
+inline bool good_scale(float scale) { return scale >= 1e-30f && scale <= 1e30f; }
 int fill_batch(Batch *b, const kv_attn_batch *t, int heads, int kv_heads, int block_size, int unit_rows, int tile_shift, int causal, int window);
 int check_plane(const kv_cache_desc *c, int tensor, int plane, int heads, int dim);
 int check_rows(const void *p, int64_t token_stride, int64_t head_stride);

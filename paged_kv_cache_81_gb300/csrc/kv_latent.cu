@@ -409,7 +409,7 @@ extern "C" int kv_latent_attention(const kv_attn_desc *d, const kv_attn_batch *b
                                    const void *q, int64_t q_token_stride, int64_t q_head_stride, void *out, int64_t out_token_stride,
                                    int64_t out_head_stride, float *lse, void *workspace, int64_t workspace_bytes, kv_stream_t stream)
 {
-    if (d == nullptr || d->n_heads <= 0 || d->n_kv_heads != 1 || d->window < 0 || !(d->scale > 0.0f) || !std::isfinite(d->scale) ||
+    if (d == nullptr || d->n_heads <= 0 || d->n_kv_heads != 1 || d->window < 0 || !good_scale(d->scale) ||
         (d->dtype != KV_BF16 && d->dtype != KV_F16))
         return KV_ERR_INVALID_ARG;
     int st = check_batch(batch);

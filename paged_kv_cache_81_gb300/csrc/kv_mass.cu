@@ -510,7 +510,7 @@ int kv_attention_mass(const kv_attn_desc *d, const kv_attn_batch *batch, const k
                       kv_stream_t stream)
 {
     if (d == nullptr || d->n_heads <= 0 || d->n_kv_heads <= 0 || d->n_heads % d->n_kv_heads != 0 || d->head_dim <= 0 || d->window < 0 ||
-        !(d->scale > 0.0f) || !std::isfinite(d->scale) || (d->dtype != KV_BF16 && d->dtype != KV_F16) || width < 0)
+        !good_scale(d->scale) || (d->dtype != KV_BF16 && d->dtype != KV_F16) || width < 0)
         return KV_ERR_INVALID_ARG;
     int st = check_batch(batch);
     if (st != KV_OK) return st;
@@ -525,8 +525,9 @@ int kv_attention_mass(const kv_attn_desc *d, const kv_attn_batch *batch, const k
     if (score == nullptr || workspace == nullptr || score_stride < 0 || prev_stride < 0) return KV_ERR_INVALID_ARG;
     if (batch->n_reqs > 1 && (score_stride < width || (prev != nullptr && prev_stride < width))) return KV_ERR_INVALID_ARG;
     if (!aligned16(workspace) || ((uintptr_t)lse & 3u) || ((uintptr_t)prev & 3u) || ((uintptr_t)score & 3u)) return KV_ERR_ALIGN;
+    const int group = d->n_heads / d->n_kv_heads;
     Params p = {};
-    if ((st = fill_batch(&p.b, batch, d->n_heads, d->n_kv_heads, k->block_size, 128, kTileShift, d->causal, d->window)) != KV_OK) return st;
+    if ((st = fill_batch(&p.b, batch, d->n_heads, d->n_kv_heads, k->block_size, 128 / group * group, kTileShift, d->causal, d->window)) != KV_OK) return st;
     const DeviceInfo *dev = current_device();
     if (dev == nullptr) return KV_ERR_CUDA;
     if (workspace_bytes < mass_workspace(dev->num_sms)) return KV_ERR_RANGE;
@@ -539,7 +540,6 @@ int kv_attention_mass(const kv_attn_desc *d, const kv_attn_batch *batch, const k
     p.piece_rows = piece_rows(k->block_size, kTile);
     p.dk = d->head_dim;
     p.heads = d->n_heads;
-    const int group = d->n_heads / d->n_kv_heads;
     p.step_tokens = 128 / group;
     p.step = make_fastdiv((uint32_t)p.step_tokens);
     p.q_box = box_tokens(p.step_tokens, batch);

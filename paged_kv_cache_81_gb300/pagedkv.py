@@ -510,21 +510,21 @@ def kv_attention_workspace(device="cuda") -> torch.Tensor:
 _workspaces = {}  # (bytes function, device, stream handle) -> the workspace of calls without one on that stream
 
 
-def _workspace(nbytes, dev: int, handle: int, given: Optional[torch.Tensor]) -> torch.Tensor:
+def _workspace(nbytes, dev: int, handle: int, given: Optional[torch.Tensor], stream) -> torch.Tensor:
     """The workspace of a call.  Calls that bring none share one a stream, whose calls are in order.  A call that is being
     captured gets one of its own, in the graph's memory and zeroed by the graph, as replays are not in that order."""
     if given is not None:
         if given.get_device() != dev or not given.is_contiguous():
             raise ValueError(f"the workspace must be a contiguous tensor on cuda:{dev}")
         return given
-    if torch._C._cuda_isCurrentStreamCapturing():
-        return torch.zeros(nbytes(), dtype=torch.uint8, device=f"cuda:{dev}")
-    key = (nbytes, dev, handle)
-    ws = _workspaces.get(key)
-    if ws is None:
-        with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev)) if handle else _no_context():
+    with _no_context() if stream is None else torch.cuda.stream(stream):
+        if torch.cuda.is_current_stream_capturing():
+            return torch.zeros(nbytes(), dtype=torch.uint8, device=f"cuda:{dev}")
+        key = (nbytes, dev, handle)
+        ws = _workspaces.get(key)
+        if ws is None:
             ws = _workspaces[key] = torch.zeros(nbytes(), dtype=torch.uint8, device=f"cuda:{dev}")
-    return ws
+        return ws
 
 
 def _begin(dev: int, stream) -> int:
@@ -639,9 +639,9 @@ def kv_attention(q: torch.Tensor, cache: PagedCache, block_table: torch.Tensor, 
     dv = values.row_bytes // (kv_heads * 2)
     batch = _attn_batch(dev, block_table, q_offsets, kv_lens, T)
     out, o_token, o_head, lse = _attn_outputs(dev, q, T, H, dv, out, lse, stream)
-    workspace = _workspace(kv_attention_workspace_bytes, dev, handle, workspace)
+    workspace = _workspace(kv_attention_workspace_bytes, dev, handle, workspace, stream)
     _check("kv_attention", (_lib or load()).kv_attention(
-        _attn_desc(code, H, kv_heads, dk, dv, causal, window, scale), batch, k_desc, k_tensor, 0, v_desc, v_tensor, values.n_planes - 1,
+        _attn_desc(code, H, kv_heads, dk, dv, causal, window, float(scale)), batch, k_desc, k_tensor, 0, v_desc, v_tensor, values.n_planes - 1,
         q.data_ptr(), q_token, q_head, out.data_ptr(), o_token, o_head, lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, handle))
     return out, lse
 
@@ -659,9 +659,9 @@ def kv_latent_attention(q: torch.Tensor, cache: PagedCache, block_table: torch.T
     T, H, dk = q.shape
     batch = _attn_batch(dev, block_table, q_offsets, kv_lens, T)
     out, o_token, o_head, lse = _attn_outputs(dev, q, T, H, LATENT_RANK, out, lse, stream)
-    workspace = _workspace(kv_attention_workspace_bytes, dev, handle, workspace)
+    workspace = _workspace(kv_attention_workspace_bytes, dev, handle, workspace, stream)
     _check("kv_latent_attention", (_lib or load()).kv_latent_attention(
-        _attn_desc(code, H, 1, dk, LATENT_RANK, causal, window, scale), batch, c_desc, tensor, q.data_ptr(), q_token, q_head,
+        _attn_desc(code, H, 1, dk, LATENT_RANK, causal, window, float(scale)), batch, c_desc, tensor, q.data_ptr(), q_token, q_head,
         out.data_ptr(), o_token, o_head, lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, handle))
     return out, lse
 
@@ -720,9 +720,9 @@ def kv_attention_mass(q: torch.Tensor, cache: PagedCache, block_table: torch.Ten
         score = _empty(q, (n, width), torch.float32, stream)
     to, to_row = _score_rows(dev, score, n, width, "score")
     before, before_row = (None, 0) if prev is None else _score_rows(dev, prev, n, width, "prev")
-    workspace = _workspace(kv_attention_mass_workspace_bytes, dev, handle, workspace)
+    workspace = _workspace(kv_attention_mass_workspace_bytes, dev, handle, workspace, stream)
     _check("kv_attention_mass", (_lib or load()).kv_attention_mass(
-        _attn_desc(code, H, kv_heads, dk, dk, causal, window, scale), batch, k_desc, k_tensor, 0, q.data_ptr(), q_token, q_head,
+        _attn_desc(code, H, kv_heads, dk, dk, causal, window, float(scale)), batch, k_desc, k_tensor, 0, q.data_ptr(), q_token, q_head,
         lse.data_ptr(), before, before_row, to, to_row, width, workspace.data_ptr(), workspace.nbytes, handle))
     return score
 

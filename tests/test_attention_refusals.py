@@ -47,7 +47,7 @@ def test_attention_arguments(lib):
     assert attention(lib, b=none) == OK  # no requests: nothing is looked at
     assert attention(lib, b=batch(tokens=0), q=None) == OK
     for bad in (desc(dtype=2), desc(heads=0), desc(heads=7), desc(kv_heads=0), desc(dk=0), desc(dv=-8), desc(window=-1), desc(scale=0.0),
-                desc(scale=-1.0), desc(scale=float("nan")), desc(scale=float("inf"))):
+                desc(scale=-1.0), desc(scale=float("nan")), desc(scale=float("inf")), desc(scale=1e-35), desc(scale=1e35)):
         assert attention(lib, d=bad) == ARG
     assert attention(lib, d=desc(dk=100)) == ALIGN  # heads of 200 bytes
     assert attention(lib, d=desc(dk=200)) == UNSUPPORTED and attention(lib, d=desc(dv=136)) == UNSUPPORTED

@@ -262,3 +262,23 @@ def test_large_pool_offsets_past_32_bits():
     o, l, to, tl = reference(q, [kr], [vr], [2], 0.1)
     close(out, o, to, "out")
     close(lse, l, tl, "lse")
+
+
+def test_capture_of_a_named_stream():
+    """A call that names the capturing stream: its outputs and workspace are the graph's, not the stream's."""
+    b = Batch([1, 2], [900, 300], 8, 2, 64, seed=3)
+    s = torch.cuda.Stream()
+    want = [x.clone() for x in b.run(0.1)]
+    b.run(0.1, stream=s)  # the stream has a workspace of its own by now
+    torch.cuda.synchronize()
+    kept = len(K._workspaces)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        got = b.run(0.1, stream=s)
+    for _ in range(2):
+        for x in got:
+            x.zero_()
+        g.replay()
+    torch.cuda.synchronize()
+    assert len(K._workspaces) == kept
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
