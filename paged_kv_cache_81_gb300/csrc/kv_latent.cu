@@ -1,5 +1,7 @@
 // kv_latent_attention: attention over one shared latent row a token (the absorbed form).
 //
+// This kernel takes units of up to 128 query rows (kv_latent_few.cu: 64).
+//
 // Keys are whole rows of 576 elements, values their first 512.  The accumulator of 128 query rows by 512
 // values would fill tensor memory by itself, so two CTAs share a part of the batch's line
 // (kv_plan.cuh): each forms the products S = Q K^T over all 576 elements and accumulates 256 of the 512
@@ -11,7 +13,7 @@
 //   warps 0 and 2 load the two kinds of panels, warp 3 loads Q, warp 1 issues the products, warps 4-7 hold
 //   a row a thread (maximum, exponentials, P over S, lazy rescaling as in kv_attention.cu).  S of the next tile is formed before O += P V of
 //   this one, so the tensor core works while the exponentials run.
-#include "kv_attention.cuh"
+#include "kv_latent.cuh"
 
 namespace pkv {
 
@@ -21,27 +23,12 @@ constexpr int kLeast = 2;  // steps of a piece of a unit, at least (of 64 keys)
 constexpr int kThreads = 256;
 constexpr int kRows = 128;
 constexpr int kKeyShift = 6, kKeys = 1 << kKeyShift;  // keys of a tile
-constexpr int kD = 576, kDV = 512, kHalf = 256;
+constexpr int kHalf = kLatentRank / 2;
 constexpr int kQT = 4;         // panels of Q in tensor memory
 constexpr uint32_t kQPanel = 128 * 128, kPanel = kKeys * 128;
 constexpr uint32_t kOffV = 5 * kQPanel, kOffX = kOffV + 2 * 4 * kPanel, kOffAux = kOffX + 2 * 5 * kPanel;
 constexpr uint32_t kBytes = kOffAux + 1024;
 constexpr uint32_t kTmO = 0, kTmS = 256, kTmQ = 384;
-
-struct Params {
-    Batch b;
-    const int32_t *table;
-    int64_t table_stride;
-    int32_t num_blocks;
-    FastDiv block;
-    int32_t piece_rows;
-    int32_t q_rows;  // rows one TMA brings of q
-    const char *q;
-    int64_t q_token, q_head;
-    Output o;
-    float *ws;
-    int *counters;
-};
 
 struct Aux {
     uint64_t v_full[2], v_empty[2], x_full[2], x_empty[2], s_full[2], p_ready[2], o_done[2], q_staged, q_moved, q_full, q_empty, join;
@@ -53,42 +40,9 @@ struct Aux {
 };
 static_assert(sizeof(Aux) <= 1024, "bookkeeping");
 
-// Panels of one tile of rows into their slot: a TMA per (run of slots inside a page, panel), spread over the
-// lanes; column(h) is the first element of panel h.  The first page a lane needs is looked up before
-// `ready` waits for the slot.
-template <int Panels, typename Column, typename Ready>
-__device__ __forceinline__ bool load_tile(const Params &p, const Walk &w, int kb, uint32_t to, uint32_t bar, const CUtensorMap *map, const Column &column,
-                                          const Ready &ready)
-{
-    const int lane = threadIdx.x & 31, pr = p.piece_rows;
-    const int p0 = max(0, w.u.lo - kb) / pr, p1 = (min(w.u.hi - kb, kKeys) + pr - 1) / pr;
-    const int32_t *row = p.table + (int64_t)w.at.req * p.table_stride;
-    int page = 0, slot = 0;
-    const auto find = [&](int i) {
-        const uint32_t key = (uint32_t)(kb + i * pr), col = fdiv(key, p.block);
-        slot = (int)(key - col * p.block.d);
-        page = __ldg(row + col);
-        if (page < 0 || page >= p.num_blocks) {
-            set_error(p.b.err, KV_DERR_TABLE);
-            page = p.num_blocks;  // outside the map: reads zeros
-        }
-    };
-    if (p0 + lane < p1) find(p0 + lane);
-    if (!ready()) return false;
-    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)((p1 - p0) * pr) * Panels * 128);
-    __syncwarp();
-    for (int i = p0 + lane; i < p1; i += 32) {
-        if (i >= p0 + 32) find(i);
-#pragma unroll
-        for (int h = 0; h < Panels; h++) tma_load_4d(to + h * kPanel + i * pr * 128, map, bar, column(h), 0, slot, page);
-    }
-    __syncwarp();
-    return true;
-}
-
 template <bool Bf16>
 __global__ void __launch_bounds__(kThreads, 1)
-latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap q_map, const Params p)
+latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap q_map, const LatentParams p)
 {
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t base = smem_addr(smem);
@@ -136,7 +90,7 @@ latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ C
         do {
             for (int t = 0; ok && t < w.n && w.u.tiles; t++, it++) {
                 const int s = it & 1;
-                ok = load_tile<5>(p, w, (w.u.tile0 + w.at.off + t) * kKeys, base + kOffX + s * 5 * kPanel, smem_addr(&aux.x_full[s]), &map,
+                ok = load_latent_tile<kKeys, 5>(p, w, (w.u.tile0 + w.at.off + t) * kKeys, base + kOffX + s * 5 * kPanel, smem_addr(&aux.x_full[s]), &map,
                                   [&](int h) { return (h == 4 ? 8 : h + 4 - 4 * half) * 64; },  // the other half's values, the rotary part
                                   [&] { return it < 2 || wait.warp(smem_addr(&aux.x_empty[s]), ((it >> 1) - 1) & 1); });
             }
@@ -148,7 +102,7 @@ latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ C
         do {
             for (int t = 0; ok && t < w.n && w.u.tiles; t++, it++) {
                 const int s = it & 1;
-                ok = load_tile<4>(p, w, (w.u.tile0 + w.at.off + t) * kKeys, base + kOffV + s * 4 * kPanel, smem_addr(&aux.v_full[s]), &map,
+                ok = load_latent_tile<kKeys, 4>(p, w, (w.u.tile0 + w.at.off + t) * kKeys, base + kOffV + s * 4 * kPanel, smem_addr(&aux.v_full[s]), &map,
                                   [&](int h) { return (h + 4 * half) * 64; },
                                   [&] { return it < 2 || wait.warp(smem_addr(&aux.v_empty[s]), ((it >> 1) - 1) & 1); });
             }
@@ -398,6 +352,7 @@ int preload_latent_kernels()
 {
     int st = cuda_status(cudaFuncSetAttribute(latent_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes));
     if (st == KV_OK) st = cuda_status(cudaFuncSetAttribute(latent_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes));
+    if (st == KV_OK) st = preload_latent_few_kernels();
     return st != KV_OK ? st : load_kernels(latent_kernel<false>, latent_kernel<true>);
 }
 
@@ -414,26 +369,35 @@ extern "C" int kv_latent_attention(const kv_attn_desc *d, const kv_attn_batch *b
         return KV_ERR_INVALID_ARG;
     int st = check_batch(batch);
     if (st != KV_OK) return st;
-    if (d->head_dim != kD || d->head_dim_v != kDV || (d->window && !d->causal)) return KV_ERR_UNSUPPORTED;
-    if ((st = check_plane(cache, tensor, 0, 1, kD)) != KV_OK) return st;
+    if (d->head_dim != kLatentDim || d->head_dim_v != kLatentRank || (d->window && !d->causal)) return KV_ERR_UNSUPPORTED;
+    if ((st = check_plane(cache, tensor, 0, 1, kLatentDim)) != KV_OK) return st;
     if (batch->n_reqs == 0 || batch->n_tokens == 0) return KV_OK;
     if ((st = check_rows(q, q_token_stride, q_head_stride)) != KV_OK) return st;
     if ((st = check_rows(out, out_token_stride, out_head_stride)) != KV_OK) return st;
     if (workspace == nullptr) return KV_ERR_INVALID_ARG;
     if (!aligned16(workspace) || ((uintptr_t)lse & 3u)) return KV_ERR_ALIGN;
-    // A unit is whole tokens of up to 128 heads each, or a divisor of a token's heads; a TMA of q brings all
-    // heads of as many tokens as a request has on average (a divisor of a unit's), or a unit.
-    int box_heads = d->n_heads, box_tokens = 1;
-    if (d->n_heads > kRows) {
-        for (box_heads = kRows; d->n_heads % box_heads; box_heads--) {}
-    } else {
-        box_tokens = pkv::box_tokens(kRows / d->n_heads, batch);
-    }
-    const int unit_rows = d->n_heads > kRows ? box_heads : kRows / d->n_heads * d->n_heads;
-    Params p = {};
-    if ((st = fill_batch(&p.b, batch, d->n_heads, 1, cache->block_size, unit_rows, kKeyShift, d->causal, d->window)) != KV_OK) return st;
     const DeviceInfo *dev = current_device();
     if (dev == nullptr) return KV_ERR_CUDA;
+    // Many requests of few rows (tokens times heads, on average) take the kernel that holds 64 rows and all values
+    // a CTA, others the one of 128 rows with a CTA for each half of the values.  One token of 16 heads after 2500
+    // and 10000 tokens at most: 25.6 and 61.9 us here against 26.8 and 53.0 there with 19 requests, 75.0 and
+    // 235.6 against 57.2 and 164.9 with 100; of 64 heads 40.1 and 93.7 against 49.1 and 89.1 with 32 requests,
+    // 65.1 and 190.0 against 64.8 and 146.2 with 76.  With few requests the join of a unit's pieces, by one CTA
+    // there, decides: four requests of 64 rows after 8000 tokens 38 here, 90 there.
+    const int64_t few_rows = batch->n_reqs < kLatentFewRows ? batch->n_reqs : kLatentFewRows;
+    const bool few = batch->n_tokens * d->n_heads <= few_rows * batch->n_reqs && (int64_t)batch->n_reqs * 8 >= dev->num_sms;
+    // A unit is whole tokens of up to that many heads each, or a divisor of a token's heads; a TMA of q brings all
+    // heads of as many tokens as a request has on average (a divisor of a unit's), or a unit.
+    const int rows = few ? kLatentFewRows : kRows, key_shift = few ? kLatentFewKeyShift : kKeyShift;
+    int box_heads = d->n_heads, box_tokens = 1;
+    if (d->n_heads > rows) {
+        for (box_heads = rows; d->n_heads % box_heads; box_heads--) {}
+    } else {
+        box_tokens = pkv::box_tokens(rows / d->n_heads, batch);
+    }
+    const int unit_rows = d->n_heads > rows ? box_heads : rows / d->n_heads * d->n_heads;
+    LatentParams p = {};
+    if ((st = fill_batch(&p.b, batch, d->n_heads, 1, cache->block_size, unit_rows, key_shift, d->causal, d->window)) != KV_OK) return st;
     if (workspace_bytes < attention_workspace(dev->num_sms)) return KV_ERR_RANGE;
     if ((st = prepare_attention(*dev)) != KV_OK) return st;
     p.b.err = dev->err_word;
@@ -441,17 +405,15 @@ extern "C" int kv_latent_attention(const kv_attn_desc *d, const kv_attn_batch *b
     p.table_stride = batch->bt_row_stride;
     p.num_blocks = (int32_t)cache->num_blocks;
     p.block = make_fastdiv((uint32_t)cache->block_size);
-    p.piece_rows = piece_rows(cache->block_size, kKeys);
-    p.q = (const char *)q;
-    p.q_token = q_token_stride;
-    p.q_head = q_head_stride;
-    p.o = Output{(char *)out, out_token_stride, out_head_stride, lse, d->n_heads, kDV, d->scale, d->scale * kLog2e};
+    p.piece_rows = piece_rows(cache->block_size, 1 << key_shift);
+    p.o = Output{(char *)out, out_token_stride, out_head_stride, lse, d->n_heads, kLatentRank, d->scale, d->scale * kLog2e};
     p.counters = (int *)workspace;
     p.ws = (float *)((char *)workspace + kCounterBytes);
     CUtensorMap map, q_map;
     p.q_rows = box_heads * box_tokens;
-    if ((st = make_q_map(&q_map, q, q_token_stride, q_head_stride, kD, d->n_heads, batch->n_tokens, box_heads, box_tokens)) != KV_OK) return st;
-    if ((st = make_cache_map(&map, cache, tensor, 0, 1, kD, p.piece_rows)) != KV_OK) return st;
+    if ((st = make_q_map(&q_map, q, q_token_stride, q_head_stride, kLatentDim, d->n_heads, batch->n_tokens, box_heads, box_tokens)) != KV_OK) return st;
+    if ((st = make_cache_map(&map, cache, tensor, 0, 1, kLatentDim, p.piece_rows)) != KV_OK) return st;
+    if (few) return run_latent_few(d->dtype == KV_BF16, map, q_map, p, dev->num_sms, (cudaStream_t)stream);
     return cuda_status(launch(d->dtype == KV_BF16 ? latent_kernel<true> : latent_kernel<false>, dim3(dev->num_sms / 2 * 2), dim3(kThreads), kBytes,
                               (cudaStream_t)stream, map, q_map, p));
 }

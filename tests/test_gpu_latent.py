@@ -195,3 +195,57 @@ def test_expanded_and_absorbed_forms_agree():
         assert bool(((o2[r] - want).abs() <= tol2).all())
         assert bool(((lse[r].cpu() - torch.logsumexp(s, -1)).abs() <= d[:, 0] + 1e-4).all())
         assert bool(((lse2[r].cpu() - torch.logsumexp(s, -1)).abs() <= 2.0 ** -8 * 4 * size.amax(-1) + 1e-4).all())
+
+
+# Many requests of few rows take a kernel of their own: up to 64 rows a request on average, and no more rows than requests.
+SHORT = [1, 31, 32, 33, 63, 64, 65, 95, 97, 128, 500, 3, 2, 129, 40, 0, 1300, 10, 20, 160]
+
+
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 1), (True, 32), (True, 50)])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_many_requests(causal, window, dtype):
+    q_lens = [(1, 1, 2, 0, 5, 1)[i % 6] for i in range(60)]
+    check(Latent(q_lens, SHORT * 3, 16, dtype=dtype, seed=window), causal, window)
+
+
+@pytest.mark.parametrize("heads,reqs", [(1, 20), (7, 20), (16, 24), (33, 40), (64, 64), (48, 80), (5, 300)])
+def test_many_requests_heads(heads, reqs):
+    check(Latent([1] * reqs, [(SHORT[i % 20] + i) % 900 for i in range(reqs)], heads, seed=heads))
+
+
+@pytest.mark.parametrize("block", [1, 3, 8, 16, 17, 24, 32, 256])
+def test_many_requests_pages(block):
+    check(Latent([1, 2] * 10, SHORT, 4, block=block, seed=block))
+
+
+@pytest.mark.parametrize("reqs,heads", [(20, 16), (70, 64)])
+def test_many_requests_split_contexts(reqs, heads):
+    b = Latent([1] * reqs, [2500 - 30 * i for i in range(reqs)], heads, seed=reqs)
+    ws = K.kv_attention_workspace()
+    want = [x.clone() for x in check(b, workspace=ws)]
+    for _ in range(10):
+        assert all(torch.equal(x, y) for x, y in zip(want, b.run(workspace=ws)))
+    assert int(ws[:16384].sum()) == 0
+    # a long unit before short ones and one request of all the rows: units of more than one unit a request
+    check(Latent([40] + [1] * 39, [4000] + [5] * 39, 16, seed=1))
+
+
+def test_many_requests_padding_and_bad_pages():
+    b = Latent([1, 2, 0, 1] * 6, [70, 200, 10, 33] * 6, 12, seed=4)
+    b.q = torch.cat([b.q, torch.full((9, 12, 576), NAN, dtype=BF, device="cuda")])
+    out, lse = torch.full((33, 12, 512), 2.0, dtype=BF, device="cuda"), torch.full((33, 12), 4.0, device="cuda")
+    K.kv_get_last_error(clear=True)
+    b.run(out=out, lse=lse)
+    assert K.kv_get_last_error(clear=True) == 0
+    o, l, to, tl = reference(b.q_cpu[:24], b.k_rows, b.v_rows, b.q_lens, SCALE)
+    close(out[:24], o, to, "out")
+    close(lse[:24], l, tl, "lse")
+    assert (out[24:] == 2).all() and (lse[24:] == 4).all()
+
+    b.table[1, 2] = b.pages  # tokens 128-191 of request 1
+    b.k_rows[1][128:192] = 0
+    b.run(out=out, lse=lse)
+    assert K.kv_get_last_error(clear=True) != 0
+    o, l, to, tl = reference(b.q_cpu[:24], b.k_rows, b.v_rows, b.q_lens, SCALE)
+    close(out[:24], o, to, "out")
+    close(lse[:24], l, tl, "lse")
