@@ -459,11 +459,9 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
             }
             if (!whole) {
                 const Cut cut(line, w.pos - w.at.off, unit_cost(w.u));
-                if (last_of(p.counters + 2 * cut.c0 + g, cut.count, smem_addr(&aux.join[g]), cuts, &aux.answer[g], wait, ok)) {
-                    const int row0 = both ? g * half : 0;
-                    join_rows<DV, Bf16>(p.o, p.ws, cut.c0, cut.count, 1, 0, kRows * (DV + 2), row0, min(half, w.u.rows - row0), kRows, w.u.row0, w.q.q0,
-                                        w.at.head * (int)b.group.d, b.group);
-                }
+                const int row0 = both ? g * half : 0;
+                join_unit<DV, Bf16>(p.o, p.ws, cut, p.counters + 2 * cut.c0 + g, 2, 1, 0, 1, kRows * (DV + 2), row0, min(half, w.u.rows - row0), kRows,
+                                    w.u.row0, w.q.q0, w.at.head * (int)b.group.d, b.group, smem_addr(&aux.join[g]), cuts, &aux.answer[g], wait, ok);
                 if (!ok) break;
             }
         } while (w.next(b));

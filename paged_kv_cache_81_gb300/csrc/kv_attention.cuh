@@ -34,10 +34,11 @@ int make_q_map(CUtensorMap *map, const void *q, int64_t token_stride, int64_t he
 // piece never leaves its page.
 int piece_rows(int block_size, int tile);
 
-// A unit that was cut: parts c0 .. c1 hold a fragment each, the first in slot 2 c0 + 1 of the workspace
-// and the others in slot 2 c (a CTA has at most one fragment that begins its unit and one that does not).
+// A unit that was cut: parts c0 .. c0 + count - 1 hold a fragment each, the first in slot 2 c0 + 1 of the workspace
+// and the others in slot 2 c (a part has at most one fragment that begins its unit and one that does not).
+// Slot 2 c + 1 and the counter of an inner part belong to this unit too.
 struct Cut {
-    int c0, count;
+    int c0, count, nth;  // nth: this part's
     __device__ __forceinline__ Cut(const Line &line, int begin, int cost)
     {
         if (line.nth >= 0) {
@@ -47,8 +48,16 @@ struct Cut {
             c0 = line.part_of(begin);
             count = line.part_of(begin + cost - 1) - c0 + 1;
         }
+        nth = line.part - c0;
     }
     __device__ __forceinline__ int slot(int i) const { return 2 * (c0 + i) + (i == 0); }
+};
+
+// Fragments that one group of threads adds up, for one half of the columns: `count` of them, `pitch` floats apart, the
+// first `head` further on; sum: where a sum goes.
+struct Pieces {
+    float *at, *sum;
+    int count, pitch, head;
 };
 
 // Called by the 128 threads of a group once they have written a fragment: true in the group that wrote
@@ -78,15 +87,16 @@ struct Output {
     float scale, c;
 };
 
-// Joins rows [row0, row0 + rows) of a cut unit from `count` fragments, `stride` floats a slot.  A fragment
+// Joins rows [row0, row0 + rows) of a cut unit from fragments of `stride` floats, or (at.sum) adds fragments up to a
+// new one, in an inner part's odd slot.  A fragment
 // holds its accumulators four columns at a time, [DV / 4][stat rows][4], so that writing (a thread a row)
 // and reading (a thread a row and some columns) are both coalesced, then the rows' maxima and sums.  128
 // threads; a row's fragments are added in the order of their keys, so the result does not depend on which
 // CTA came last.  Row r is (first + r) / group of the request's tokens from q0 on, head head0 + the
 // rest.  Not inlined: its registers would crowd the loop over the key tiles.
 template <int DV, bool Bf16>
-__device__ __noinline__ void join_rows(const Output p, const float *ws, int c0, int count, int halves, int half, int stride, int row0, int rows, int stat,
-                                       int first, int q0, int head0, const FastDiv group)
+__device__ __noinline__ void join_rows(const Output p, const Pieces at, int half, int row0, int rows, int stat, int first, int q0, int head0,
+                                       const FastDiv group)
 {
     // rows rounded up to a power of two; the other threads share out the columns (at least one quad each)
     int shift = DV == 64 ? 3 : DV == 128 ? 2 : 1;
@@ -94,7 +104,8 @@ __device__ __noinline__ void join_rows(const Output p, const float *ws, int c0, 
     const int t = threadIdx.x & 127, row = row0 + (t & ((1 << shift) - 1)), parts = 128 >> shift, quads = DV / 4 / parts;
     const int quad0 = (t >> shift) * quads;
     if (row >= row0 + rows) return;
-    const auto fragment = [&](int i) { return ws + (2 * ((c0 + i) * halves + half) + (i == 0)) * (int64_t)stride; };
+    const int count = at.count;
+    const auto fragment = [&](int i) { return at.at + (i * at.pitch + (i == 0 ? at.head : 0)); };
     float top = -INFINITY;
 #pragma unroll 8
     for (int i = 0; i < count; i++) top = fmaxf(top, __ldcg(fragment(i) + stat * DV + row));
@@ -111,19 +122,43 @@ __device__ __noinline__ void join_rows(const Output p, const float *ws, int c0, 
             float l = 0.0f;
 #pragma unroll
             for (int k = 0; k < kBatch; k++) o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll kAhead
-            for (int i = 0; i < count; i++) {
-                const float *part = fragment(i);
-                const float pm = __ldcg(part + stat * DV + row), pl = __ldcg(part + stat * (DV + 1) + row);
-                float4 v[kBatch];
+#pragma unroll 1
+            for (int i0 = 0; i0 < count; i0 += kAhead) {
+                float4 v[kAhead][kBatch];
+                float pm[kAhead], pl[kAhead];
+#pragma unroll
+                for (int j = 0; j < kAhead; j++) {
+                    const float *part = fragment(i0 + j);
+                    pm[j] = -INFINITY;
+                    pl[j] = 0.0f;
+                    if (i0 + j < count) {
+                        pm[j] = __ldcg(part + stat * DV + row);
+                        pl[j] = __ldcg(part + stat * (DV + 1) + row);
+                    }
+#pragma unroll
+                    for (int k = 0; k < kBatch; k++) {
+                        v[j][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (k < quads && i0 + j < count) v[j][k] = __ldcg(reinterpret_cast<const float4 *>(part) + (q + k) * stat + row);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kAhead; j++) {
+                    const float a = exp2_fast((pm[j] - z) * p.c);
+                    l += pl[j] * a;
+#pragma unroll
+                    for (int k = 0; k < kBatch; k++)
+                        o[k].x += v[j][k].x * a, o[k].y += v[j][k].y * a, o[k].z += v[j][k].z * a, o[k].w += v[j][k].w * a;
+                }
+            }
+            if (at.sum) {
 #pragma unroll
                 for (int k = 0; k < kBatch; k++)
-                    if (k < quads) v[k] = __ldcg(reinterpret_cast<const float4 *>(part) + (q + k) * stat + row);
-                const float a = exp2_fast((pm - z) * p.c);
-                l += pl * a;
-#pragma unroll
-                for (int k = 0; k < kBatch; k++)
-                    if (k < quads) o[k].x += v[k].x * a, o[k].y += v[k].y * a, o[k].z += v[k].z * a, o[k].w += v[k].w * a;
+                    if (k < quads) __stcg(reinterpret_cast<float4 *>(at.sum) + (q + k) * stat + row, o[k]);
+                if (q == 0) {
+                    at.sum[stat * DV + row] = top;
+                    at.sum[stat * (DV + 1) + row] = l;
+                }
+                continue;
             }
             const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
@@ -139,8 +174,42 @@ __device__ __noinline__ void join_rows(const Output p, const float *ws, int c0, 
     };
     if (quads <= 4)
         columns(std::integral_constant<int, 4>(), std::integral_constant<int, 6>());
-    else
+    else if (DV == 256)
         columns(std::integral_constant<int, 8>(), std::integral_constant<int, 3>());
+    else
+        columns(std::integral_constant<int, 4>(), std::integral_constant<int, 4>());
+}
+
+// Called by the 128 threads of a group once they have written their fragment: rows [row0, row0 + rows) of
+// halves [half0, half1) of the unit are joined by the group that wrote the last one.  Of many pieces the last of
+// every kSum (3 to 10 at the unit's end) adds those up first, into the odd slot of the second of them: a group has
+// some 40 KB of loads in flight, so a fragment takes it 0.3 (8 rows of 128) to 0.9 us (64 rows of 256).  One
+// request of 16000 tokens, 8 heads over one key head: 30 us with one join of all pieces, 20 us so; of 60000 tokens,
+// 128 heads: 164 and 55 us; latent, 32000 tokens, 64 heads: 81 and 40 us; 16 pieces of 128 rows 44 and 39 us.
+// counter: the first part's; those of the parts are `apart`.
+constexpr int kSum = 8;
+
+template <int DV, bool Bf16>
+__device__ __forceinline__ void join_unit(const Output &p, float *ws, const Cut &cut, int *counter, int apart, int halves, int half0, int half1,
+                                          int stride, int row0, int rows, int stat, int first, int q0, int head0, const FastDiv &group, uint32_t bar,
+                                          int &phase, volatile int *answer, const Waiter &wait, bool &ok)
+{
+    const bool many = cut.count > kSum + kSum / 2;
+    const int sums = (cut.count - 3) / kSum + 1, mine = min(cut.nth / kSum, sums - 1);
+    bool sum = many;
+    for (;; sum = false) {
+        const int from = sum ? mine * kSum : 0, n = sum ? (mine + 1 < sums ? kSum : cut.count - from) : many ? sums : cut.count;
+        if (!last_of(counter + (sum ? (1 + mine) * apart : 0), n, bar, phase, answer, wait, ok)) return;
+        const bool sums_of = many && !sum;
+#pragma unroll 1
+        for (int h = half0; h < half1; h++) {
+            const auto slot = [&](int piece, int odd) { return ws + (2 * ((cut.c0 + piece) * halves + h) + odd) * stride; };
+            const Pieces at{sums_of ? slot(1, 1) : slot(from, 0), sum ? slot(from + 1, 1) : nullptr, n, (sums_of ? kSum : 1) * 2 * halves * stride,
+                            from == 0 && !sums_of ? stride : 0};
+            join_rows<DV, Bf16>(p, at, h, row0, rows, stat, first, q0, head0, group);
+        }
+        if (!sum) return;
+    }
 }
 
 // 32 accumulator columns of a row into its fragment, as join_rows reads them.

@@ -328,8 +328,8 @@ latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ C
             }
             if (!whole) {
                 const Cut cut(line, w.pos - w.at.off, unit_cost(w.u));
-                if (last_of(p.counters + 2 * cut.c0 + half, cut.count, smem_addr(&aux.join), cuts, &aux.answer, wait, ok))
-                    join_rows<kHalf, Bf16>(p.o, p.ws, cut.c0, cut.count, 2, half, kRows * (kHalf + 2), 0, w.u.rows, kRows, w.u.row0, w.q.q0, 0, b.group);
+                join_unit<kHalf, Bf16>(p.o, p.ws, cut, p.counters + 2 * cut.c0 + half, 2, 2, half, half + 1, kRows * (kHalf + 2), 0, w.u.rows, kRows,
+                                       w.u.row0, w.q.q0, 0, b.group, smem_addr(&aux.join), cuts, &aux.answer, wait, ok);
                 if (!ok) break;
             }
         } while (w.next(b));

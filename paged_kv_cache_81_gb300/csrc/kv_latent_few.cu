@@ -270,10 +270,8 @@ latent_few_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant
             }
             if (!whole) {
                 const Cut cut(line, w.pos - w.at.off, unit_cost(w.u));
-                if (last_of(p.counters + cut.c0, cut.count, smem_addr(&aux.join), cuts, &aux.answer, wait, ok))
-#pragma unroll 1
-                    for (int h = 0; h < 2; h++)
-                        join_rows<kHalf, Bf16>(p.o, p.ws, cut.c0, cut.count, 2, h, kRows * (kHalf + 2), 0, w.u.rows, kRows, w.u.row0, w.q.q0, 0, b.group);
+                join_unit<kHalf, Bf16>(p.o, p.ws, cut, p.counters + cut.c0, 1, 2, 0, 2, kRows * (kHalf + 2), 0, w.u.rows, kRows, w.u.row0, w.q.q0, 0,
+                                       b.group, smem_addr(&aux.join), cuts, &aux.answer, wait, ok);
                 if (!ok) break;
             }
         } while (w.next(b));

@@ -59,6 +59,21 @@ def test_long_contexts_are_split(reqs, kv):
     check(Batch([150] + [1] * (reqs - 1), [kv] * reqs, 4, 1, 192, 128, seed=kv))
 
 
+@pytest.mark.parametrize("q_len,heads,kv_heads,kv,dim", [(1, 128, 1, 9000, 128), (4, 32, 1, 33333, 128), (16, 16, 2, 8200, 128), (1, 100, 1, 6700, 64),
+                                                         (7, 9, 1, 25000, 64)])
+def test_many_pieces_of_many_rows(q_len, heads, kv_heads, kv, dim):
+    """Units of more than a dozen pieces are joined in two stages, in the same order every time."""
+    b = Batch([q_len], [kv], heads, kv_heads, dim, block=64, seed=kv)
+    ws = K.kv_attention_workspace()
+    want = [x.clone() for x in check(b, workspace=ws)]
+    for _ in range(20):
+        got = b.run(dim ** -0.5, workspace=ws)
+        assert all(torch.equal(x, y) for x, y in zip(want, got))
+    assert int(ws[:16384].sum()) == 0
+    # one long request before short ones: equal pieces, of which some hold the ends of two units
+    check(Batch([q_len] + [1] * 30, [kv] + [300] * 30, heads, kv_heads, dim, block=64, seed=kv))
+
+
 def test_many_short_requests():
     lens = [1 + 37 * i % 300 for i in range(700)]
     check(Batch([1] * 700, lens, 4, 2, 64, block=8, seed=1))
