@@ -525,7 +525,7 @@ KV_API int kv_attention_mass(const kv_attn_desc *d, const kv_attn_batch *batch, 
  *  - out_table == block_table (the same pointer): in place; the pages past new_lens[r] are then free.  The
  *    pages of a request must then belong to it alone.  Otherwise the pages out_table lists must not be
  *    among those block_table lists; shared prefix pages stay as they are.
- *  - out_score may be score itself (row strides equal).
+ *  - new_lens may be kv_lens itself, and out_score score itself (row strides equal).
  *  - kv_lens outside [0, min(max_blocks_per_req * block_size, width)] are clamped, an out_table too short for
  *    the kept tokens truncates their rows, a table entry outside the cache skips its rows: each sets
  *    KV_DERR_TABLE.

@@ -300,3 +300,16 @@ def test_a_requests_life():
         close(out, o, to, "out")
         close(lse, l, tl, "lse")
     assert K.kv_get_last_error(clear=True) == 0
+
+
+def test_lengths_in_place():
+    """A trimmed request's new length may be written over its old one."""
+    s = scores(40, 3000, 8).cuda()
+    cache = K.PagedCache.from_tensors([torch.zeros(40 * 47, 64, 8, dtype=BF, device="cuda")], "separate")
+    table = torch.arange(40 * 47, dtype=torch.int32, device="cuda").view(40, 47)
+    old = [3000 - 70 * i for i in range(40)]
+    lens = torch.tensor(old, dtype=torch.int32, device="cuda")
+    new, kept, _ = K.kv_evict(cache, table, lens, s, 700, sinks=2, recent=9, new_lens=lens)
+    assert new is lens and lens.tolist() == [min(n, 700) for n in old]
+    for r, n in enumerate(old):
+        assert kept[r].tolist() == keep_reference(s[r].tolist(), n, 700, 2, 9) + [-1] * (700 - min(n, 700))
