@@ -473,7 +473,8 @@ KV_API int kv_attention(const kv_attn_desc *d, const kv_attn_batch *batch, const
  *     out[t, h] = sum_j p_j row[j][0:512],  p = softmax over the j that t sees of scale * q[t, h] . row[j]
  * This is the absorbed form: q holds the up-projection of the keys already, and out is multiplied by that
  * of the values afterwards.  d->n_kv_heads is 1, head_dim 576 and head_dim_v 512 (KV_ERR_UNSUPPORTED
- * otherwise).  Everything else as for kv_attention.
+ * otherwise).  Everything else as for kv_attention; the capacity's work is counted in units of 128 rows (whole
+ * tokens; of more than 128 heads the largest divisor of their number up to 128) and tiles of 64 keys.
  */
 KV_API int kv_latent_attention(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_cache_desc *cache, int32_t tensor,
                                const void *q, int64_t q_token_stride, int64_t q_head_stride, void *out,

@@ -11,8 +11,11 @@
 //   shared memory  Q's other five panels 80 KB; two tiles of 64 keys, 72 KB each: the four panels that
 //                  are this CTA's values, and the five that the scores alone use and free earlier
 //   warps 0 and 2 load the two kinds of panels, warp 3 loads Q, warp 1 issues the products, warps 4-7 hold
-//   a row a thread (maximum, exponentials, P over S, lazy rescaling as in kv_attention.cu).  S of the next tile is formed before O += P V of
-//   this one, so the tensor core works while the exponentials run.
+//   a row a thread (maximum, exponentials, P over S, lazy rescaling as in kv_attention.cu).  S of the next
+//   tile is formed before O += P V of this one, so the tensor core works while the exponentials run.
+// A tile of 64 keys takes about 2050 cycles of shared memory's rate for the products' operands, which is what
+// bounds it: 64 requests of 4096 to 12288 tokens, 128 heads, take 187 us, half of the rate at which memory
+// could bring the rows (each is read once, by both CTAs of a pair, the second time from the L2).
 #include "kv_latent.cuh"
 
 namespace pkv {
@@ -384,8 +387,10 @@ extern "C" int kv_latent_attention(const kv_attn_desc *d, const kv_attn_batch *b
     // 235.6 against 57.2 and 164.9 with 100; of 64 heads 40.1 and 93.7 against 49.1 and 89.1 with 32 requests,
     // 65.1 and 190.0 against 64.8 and 146.2 with 76.  With few requests the join of a unit's pieces, by one CTA
     // there, decides: four requests of 64 rows after 8000 tokens 38 here, 90 there.
-    const int64_t few_rows = batch->n_reqs < kLatentFewRows ? batch->n_reqs : kLatentFewRows;
-    const bool few = batch->n_tokens * d->n_heads <= few_rows * batch->n_reqs && (int64_t)batch->n_reqs * 8 >= dev->num_sms;
+    // (Its tiles are half as long: the last condition keeps a batch of any capacity that the other takes.)
+    const int64_t reqs = batch->n_reqs, few_rows = reqs < kLatentFewRows ? reqs : kLatentFewRows;
+    const bool few = d->n_heads <= kLatentFewRows && batch->n_tokens <= few_rows * reqs / d->n_heads && reqs * 8 >= dev->num_sms &&
+                     reqs * ((int64_t)batch->max_blocks_per_req * cache->block_size >> kLatentFewKeyShift) < (1ll << 29);
     // A unit is whole tokens of up to that many heads each, or a divisor of a token's heads; a TMA of q brings all
     // heads of as many tokens as a request has on average (a divisor of a unit's), or a unit.
     const int rows = few ? kLatentFewRows : kRows, key_shift = few ? kLatentFewKeyShift : kKeyShift;

@@ -18,7 +18,7 @@ namespace pkv {
 
 namespace {
 
-constexpr int kLeast = 4;  // tiles of a piece of a unit, at least
+constexpr int kLeast = 4;  // tiles of a piece of a unit, at least (as many keys as in kv_latent.cu)
 constexpr int kThreads = 256;
 constexpr int kRows = kLatentFewRows, kKeys = 1 << kLatentFewKeyShift, kHalf = kLatentRank / 2;
 constexpr int kStages = 4;

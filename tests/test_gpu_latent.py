@@ -249,3 +249,16 @@ def test_many_requests_padding_and_bad_pages():
     o, l, to, tl = reference(b.q_cpu[:24], b.k_rows, b.v_rows, b.q_lens, SCALE)
     close(out[:24], o, to, "out")
     close(lse[:24], l, tl, "lse")
+
+
+def test_many_requests_with_more_heads_than_rows():
+    check(Latent([1, 0, 0] * 10, SHORT + SHORT[:10], 67, seed=3))
+
+
+def test_capacity_is_the_same_for_many_requests():
+    """A table that could hold more tokens than short tiles can count still works."""
+    b = Latent([1] * 64, [40 + i for i in range(64)], 8, block=1024, seed=3)
+    table = torch.full((64, 1 << 20), -1, dtype=torch.int32, device="cuda")  # 2^30 tokens a request
+    table[:, : b.table.shape[1]] = b.table
+    b.table = table
+    check(b)
