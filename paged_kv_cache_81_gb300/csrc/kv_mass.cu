@@ -25,13 +25,13 @@ namespace {
 constexpr int kLeast = 2;  // steps of a piece of a unit, at least
 constexpr int kThreads = 448;
 constexpr int kTileShift = 7, kTile = 1 << kTileShift;
-constexpr uint32_t kPanel = 128 * 128;
+constexpr uint32_t kPanel = 128 * 128, kAuxBytes = 3 << 10;
 
 template <int DK>
 struct Shape {
     static constexpr uint32_t kOperand = 128 * DK * 2;
     static constexpr int kNK = DK == 64 ? 8 : DK == 128 ? 4 : 2, kNQ = DK == 64 ? 4 : DK == 128 ? 3 : 2;  // what 227 KB holds
-    static constexpr uint32_t kOffQ = kNK * kOperand, kOffAux = kOffQ + kNQ * kOperand, kBytes = kOffAux + 3072;
+    static constexpr uint32_t kOffQ = kNK * kOperand, kOffAux = kOffQ + kNQ * kOperand, kBytes = kOffAux + kAuxBytes;
 };
 
 struct Params {
@@ -64,7 +64,7 @@ struct Aux {
     int answer;
     int gave_up;
 };
-static_assert(sizeof(Aux) <= 3072, "bookkeeping");
+static_assert(sizeof(Aux) <= kAuxBytes, "bookkeeping");
 
 // The steps of one key tile: a key head's query rows, in steps of step_tokens tokens.
 struct KeyTile {

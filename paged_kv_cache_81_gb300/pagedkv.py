@@ -606,9 +606,17 @@ def _attn_outputs(dev: int, q: torch.Tensor, T: int, H: int, dv: int, out: Optio
     return out, token, head, lse
 
 
+def _int32(**values):
+    """ctypes would cut a number off to 32 bits without a word."""
+    for name, x in values.items():
+        if not -2 ** 31 <= x < 2 ** 31:
+            raise ValueError(f"{name} must be a 32-bit number")
+
+
 @functools.lru_cache(maxsize=256)
 def _attn_desc(*fields) -> KvAttnDesc:
     """Descriptions repeat from layer to layer; the library only reads them."""
+    _int32(window=fields[6])
     return KvAttnDesc(*fields)
 
 
@@ -733,6 +741,7 @@ def kv_evict(cache: PagedCache, block_table: torch.Tensor, kv_lens: torch.Tensor
     """Trims every request to `budget` tokens: the first `sinks`, the last `recent` and the highest scores between, in
     their order; rows of every tensor and plane are gathered to out_table's pages (None: in place).  Returns
     (new_lens int32 [n_reqs], kept int32 [n_reqs, budget], out_score float32 [n_reqs, budget])."""
+    _int32(budget=budget, sinks=sinks, recent=recent)
     dev = kv_lens.get_device()
     handle = _begin(dev, stream)
     n = kv_lens.numel()

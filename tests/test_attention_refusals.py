@@ -125,3 +125,15 @@ def test_binding_refuses_what_is_not_on_the_gpu():
         K.kv_attention(q.float(), None, None, None, None, 0.1)
     with pytest.raises(ValueError):
         K.kv_latent_attention(q[0], None, None, None, None, 0.1)
+
+
+def test_binding_refuses_numbers_past_32_bits():
+    """They would reach the library cut off: a window of 2^32 + 5 as one of 5."""
+    assert K._attn_desc(K.KV_BF16, 8, 2, 128, 128, True, 2 ** 31 - 1, 0.1).window == 2 ** 31 - 1
+    for window in (2 ** 31, 2 ** 32 + 5, -2 ** 32):
+        with pytest.raises(ValueError):
+            K._attn_desc(K.KV_BF16, 8, 2, 128, 128, True, window, 0.1)
+    lens = torch.zeros(1, dtype=torch.int32)
+    for kw in (dict(budget=2 ** 32 + 4), dict(budget=8, sinks=2 ** 32), dict(budget=8, recent=-2 ** 32)):
+        with pytest.raises(ValueError, match="32-bit"):
+            K.kv_evict(None, None, lens, None, **kw)
