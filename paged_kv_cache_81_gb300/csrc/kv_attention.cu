@@ -525,7 +525,7 @@ int fill_batch(Batch *b, const kv_attn_batch *t, int heads, int kv_heads, int bl
     b->unit_rows = unit_rows;
     b->tile_shift = tile_shift;
     b->causal = causal ? 1 : 0;
-    b->window = window;
+    b->window = window < max_tokens ? window : 0;  // a longer one hides nothing, and would overflow beside a position
     b->group = make_fastdiv((uint32_t)(heads / kv_heads));
     b->unit = make_fastdiv((uint32_t)unit_rows);
     // the line's steps are counted in 32 bits

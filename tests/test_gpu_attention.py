@@ -297,3 +297,13 @@ def test_capture_of_a_named_stream():
     torch.cuda.synchronize()
     assert len(K._workspaces) == kept
     assert all(torch.equal(x, y) for x, y in zip(want, got))
+
+
+@pytest.mark.parametrize("window", [2 ** 30, 2 ** 31 - 1])
+def test_windows_longer_than_any_context(window):
+    b = Batch([1, 3, 200, 9], [700, 129, 300, 4], 6, 2, 128, seed=1)
+    want = check(b)
+    got = b.run(128 ** -0.5, True, window)
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+    args = (b.q, b.cache, b.table, b.offsets, b.lens, want[1], 128 ** -0.5)
+    assert torch.equal(K.kv_attention_mass(*args), K.kv_attention_mass(*args, window=window))
