@@ -506,9 +506,10 @@ KV_API int kv_latent_expand(int32_t dtype, int32_t n_heads, const kv_cache_desc 
  * with lse as kv_attention wrote it ([n_tokens, n_heads]; a row of -inf adds nothing).  prev (NULL: zeros)
  * and score are float [n_reqs, width] with row strides in elements; they may be the same buffer.  Adding layer
  * by layer and step by step gives the accumulated weights that kv_evict ranks by.  d->head_dim_v is
- * ignored; at most 128 query heads a key head.  The sum of a token is formed in a fixed order, so the same call
- * gives the same bits.  workspace: kv_attention_mass_workspace_bytes(), 16-byte aligned, zeroed once
- * by the caller as for kv_attention (whose workspace serves too); calls sharing it must be ordered.  Lengths and tables as for kv_attention.
+ * ignored; at most 128 query heads a key head, width <= 2^30.  The sum of a token is formed in a fixed order, so the
+ * same call gives the same bits.  workspace: kv_attention_mass_workspace_bytes(), 16-byte aligned, zeroed once
+ * by the caller as for kv_attention (whose workspace serves too); calls sharing it must be ordered.  Lengths and
+ * tables as for kv_attention.
  */
 KV_API int kv_attention_mass_workspace_bytes(int64_t *bytes_out);
 KV_API int kv_attention_mass(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_cache_desc *k, int32_t k_tensor,
@@ -530,7 +531,7 @@ KV_API int kv_attention_mass(const kv_attn_desc *d, const kv_attn_batch *batch, 
  *  - kv_lens outside [0, min(max_blocks_per_req * block_size, width)] are clamped, an out_table too short for
  *    the kept tokens truncates their rows, a table entry outside the cache skips its rows: each sets
  *    KV_DERR_TABLE.
- * sinks + recent <= budget (KV_ERR_INVALID_ARG).  Limits: n_reqs <= 65535, 2^30 tokens a table row.
+ * sinks + recent <= budget (KV_ERR_INVALID_ARG).  Limits: n_reqs <= 65535, budget and the tokens a table row <= 2^30.
  */
 KV_API int kv_evict(const kv_cache_desc *cache, const int32_t *block_table, int32_t n_reqs, int32_t max_blocks_per_req,
                     int64_t bt_row_stride, const int32_t *kv_lens, const float *score, int64_t score_stride, int32_t width,

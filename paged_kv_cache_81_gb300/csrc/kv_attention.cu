@@ -530,7 +530,7 @@ int fill_batch(Batch *b, const kv_attn_batch *t, int heads, int kv_heads, int bl
     b->unit = make_fastdiv((uint32_t)unit_rows);
     // the line's steps are counted in 32 bits
     const int64_t units = t->n_tokens * heads / unit_rows + (int64_t)t->n_reqs * kv_heads;
-    if (units * ((max_tokens >> tile_shift) + 1) >= (1ll << 31)) return KV_ERR_UNSUPPORTED;
+    if (units > ((1ll << 31) - 1) / ((max_tokens >> tile_shift) + 1)) return KV_ERR_UNSUPPORTED;
     b->err = nullptr;
     return KV_OK;
 }

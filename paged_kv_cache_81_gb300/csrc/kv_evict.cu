@@ -294,7 +294,8 @@ extern "C" int kv_evict(const kv_cache_desc *cache, const int32_t *block_table, 
         return KV_ERR_INVALID_ARG;
     if (((uintptr_t)score & 3u) || ((uintptr_t)out_score & 3u)) return KV_ERR_ALIGN;
     const int64_t max_tokens = (int64_t)max_blocks_per_req * cache->block_size, out_tokens = (int64_t)out_blocks_per_req * cache->block_size;
-    if (max_tokens > (1ll << 30) || out_tokens > (1ll << 30) || cache->num_blocks >= (1ll << 31) || n_reqs > 65535) return KV_ERR_UNSUPPORTED;
+    if (max_tokens > (1ll << 30) || out_tokens > (1ll << 30) || cache->num_blocks >= (1ll << 31) || n_reqs > 65535 || budget > (1 << 30))
+        return KV_ERR_UNSUPPORTED;
     const DeviceInfo *dev = current_device();
     if (dev == nullptr) return KV_ERR_CUDA;
     cudaStream_t s = (cudaStream_t)stream;

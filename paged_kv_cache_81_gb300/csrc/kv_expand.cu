@@ -333,7 +333,8 @@ extern "C" int kv_latent_expand(int32_t dtype, int32_t n_heads, const kv_cache_d
     if (n_reqs > 1 && (bt_row_stride < max_blocks_per_req || out_row_stride < out_blocks_per_req)) return KV_ERR_INVALID_ARG;
     if (!aligned16(weight)) return KV_ERR_ALIGN;
     const int64_t max_tokens = (int64_t)max_blocks_per_req * cache->block_size, out_tokens = (int64_t)out_blocks_per_req * k_out->block_size;
-    if (max_tokens > (1ll << 30) || out_tokens > (1ll << 30) || n_reqs * (max_tokens / kTile + 1) * n_heads >= (1ll << 31)) return KV_ERR_UNSUPPORTED;
+    if (max_tokens > (1ll << 30) || out_tokens > (1ll << 30) || (int64_t)n_reqs * n_heads > ((1ll << 31) - 1) / (max_tokens / kTile + 1))
+        return KV_ERR_UNSUPPORTED;
     const DeviceInfo *dev = current_device();
     if (dev == nullptr) return KV_ERR_CUDA;
     if ((st = prepare_attention(*dev)) != KV_OK) return st;

@@ -519,7 +519,7 @@ int kv_attention_mass(const kv_attn_desc *d, const kv_attn_batch *batch, const k
     int st = check_batch(batch);
     if (st != KV_OK) return st;
     if (d->head_dim % 8) return KV_ERR_ALIGN;
-    if (d->head_dim > 192 || d->n_heads / d->n_kv_heads > 128 || (d->window && !d->causal)) return KV_ERR_UNSUPPORTED;
+    if (d->head_dim > 192 || d->n_heads / d->n_kv_heads > 128 || (d->window && !d->causal) || width > (1 << 30)) return KV_ERR_UNSUPPORTED;
     if ((st = check_plane(k, k_tensor, k_plane, d->n_kv_heads, d->head_dim)) != KV_OK) return st;
     if (batch->n_reqs == 0 || width == 0) return KV_OK;
     if (batch->n_tokens > 0) {

@@ -137,3 +137,16 @@ def test_binding_refuses_numbers_past_32_bits():
     for kw in (dict(budget=2 ** 32 + 4), dict(budget=8, sinks=2 ** 32), dict(budget=8, recent=-2 ** 32)):
         with pytest.raises(ValueError, match="32-bit"):
             K.kv_evict(None, None, lens, None, **kw)
+
+
+def test_lengths_past_what_is_counted(lib):
+    """Columns are counted in 32 bits, in steps of a thousand."""
+    big = (1 << 30) + 1
+    assert lib.kv_attention_mass(desc(), batch(), cache(), 0, 0, 0x50000, 2048, 256, 0x7000, None, 0, 0x9000, big, big, 0x80000, 1 << 40, None) == UNSUPPORTED
+    assert lib.kv_evict(cache(), 0x2000, 2, 8, 8, 0x4000, 0x9000, 300, 300, big, 4, 20, 0x3000, 8, 8, 0x5000, 0x6000, big, 0x7000, big, None) == UNSUPPORTED
+    # a product of requests, heads and tiles that would pass 64 bits
+    wide, n = 1 << 22, (1 << 31) - 1
+    assert lib.kv_latent_expand(K.KV_BF16, wide, cache(row=1152), 0, 0x2000, n, 1 << 20, 1 << 20, 0x4000, 0x90000, cache(row=wide * 384), 0,
+                                cache(row=wide * 256), 0, 0x3000, 1 << 20, 1 << 20, None) == UNSUPPORTED
+    rows = cache(row=wide * 256)
+    assert attention(lib, d=desc(heads=wide, kv_heads=wide), b=batch(n_reqs=n, pages=1 << 20), k=rows) == UNSUPPORTED
