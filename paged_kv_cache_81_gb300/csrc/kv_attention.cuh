@@ -10,7 +10,7 @@
 namespace pkv {
 
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr int64_t kCounterBytes = 16384;  // arrival counts of cut units, zero between calls
+constexpr int64_t kCounterBytes = KV_ATTENTION_ZEROED_BYTES;  // arrival counts of cut units, zero between calls
 
 // Two fragments a CTA: of 256 rows x (128 values + maximum + sum) for kv_attention, of 128 rows x (256
 // values + maximum + sum) for each CTA of kv_latent_attention.

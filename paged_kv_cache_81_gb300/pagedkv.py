@@ -25,6 +25,7 @@ KV_DERR_TABLE, KV_DERR_SLOT, KV_DERR_BLOCK, KV_DERR_LIST = 0x01, 0x02, 0x04, 0x0
 KV_DERR_CAPACITY, KV_DERR_STAGE, KV_DERR_DST_TABLE, KV_DERR_TIMEOUT = 0x10, 0x20, 0x40, 0x80
 
 KV_BF16, KV_F16 = 0, 1
+KV_ATTENTION_ZEROED_BYTES = 16384
 _DTYPES = {torch.bfloat16: KV_BF16, torch.float16: KV_F16}
 
 RUN_WORDS = 6  # a kv_xfer_run is 24 bytes: six int32 words (the last two hold the int64 stage_block)
@@ -519,7 +520,9 @@ def _workspace(nbytes, dev: int, handle: int, given: Optional[torch.Tensor], str
         return given
     with _no_context() if stream is None else torch.cuda.stream(stream):
         if torch.cuda.is_current_stream_capturing():
-            return torch.zeros(nbytes(), dtype=torch.uint8, device=f"cuda:{dev}")
+            ws = torch.empty(nbytes(), dtype=torch.uint8, device=f"cuda:{dev}")
+            ws[:KV_ATTENTION_ZEROED_BYTES].zero_()
+            return ws
         key = (nbytes, dev, handle)
         ws = _workspaces.get(key)
         if ws is None:
