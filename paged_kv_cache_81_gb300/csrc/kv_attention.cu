@@ -18,10 +18,11 @@
 // key tiles of the same rows and are joined through TMEM, so both ways keep two tiles in flight between
 // the tensor core and the exponentials.
 //
-// Decoding is bound by memory: 64 requests of 4096 to 12288 tokens, 32 heads over 8 of 128, take 330 us, 97% of
-// the copy rate.  Chunks are bound by shared memory, which moves 128 bytes a cycle: a step of 256 rows by 128 keys
-// reads operands for 1024 of its cycles, and its exponentials take 512 beside them (four chunks of 2048 to 4096 tokens
-// over 4096 to 8192: 694 us, 1.28 PFLOP/s, two thirds of the tensor cores' measured rate).
+// Decoding is bound by memory: 64 requests of 4096 to 12288 tokens, 32 heads over 8 of 128, take 322 to
+// 331 us, 97% of the copy rate or more.  Chunks are bound by shared memory, which moves 128 bytes a cycle: a
+// step of 256 rows by 128 keys reads operands for 1024 of its cycles, and its exponentials take 512 beside them
+// (four chunks of 2048 to 4096 tokens over 4096 to 8192: 689 us, 1.29 PFLOP/s, two thirds of the tensor cores'
+// measured rate).
 #include <cmath>
 
 #include "kv_attention.cuh"
