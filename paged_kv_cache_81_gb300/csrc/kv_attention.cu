@@ -21,7 +21,7 @@
 // Decoding is bound by memory: 64 requests of 4096 to 12288 tokens, 32 heads over 8 of 128, take 322 to
 // 331 us, 97% of the copy rate or more.  Chunks are bound by shared memory, which moves 128 bytes a cycle: a
 // step of 256 rows by 128 keys reads operands for 1024 of its cycles, and its exponentials take 512 beside them
-// (four chunks of 2048 to 4096 tokens over 4096 to 8192: 689 us, 1.29 PFLOP/s, two thirds of the tensor cores'
+// (four chunks of 2048 to 4096 tokens over 4096 to 8192: 681 to 694 us, 1.3 PFLOP/s, two thirds of the tensor cores'
 // measured rate).
 #include <cmath>
 

@@ -46,7 +46,16 @@ struct Cut {
             count = ceil_div(cost, line.each);
         } else {
             c0 = line.part_of(begin);
-            count = line.part_of(begin + cost - 1) - c0 + 1;
+            int c1 = line.part_of(begin + cost - 1);
+            if (line.snap && c0 < c1) {  // as Walk moves the ends of its pieces
+                const int x = line.begin_of(c0 + 1) - begin;
+                if (x <= line.snap && x <= cost - x) c0++;
+            }
+            if (line.snap && c0 < c1) {
+                const int y = begin + cost - line.begin_of(c1);
+                if (y <= line.snap && y < cost - y) c1--;
+            }
+            count = c1 - c0 + 1;
         }
         nth = line.part - c0;
     }

@@ -59,6 +59,7 @@ __device__ __forceinline__ int request_len(const Params &p, int r, bool report)
 
 // The line: a unit is a token tile, its steps are the heads.
 struct ExpandWork {
+    static constexpr int kSnap = 0;
     const Params &p;
     bool report;
     __device__ __forceinline__ int units(int r) const { return (request_len(p, r, false) + kTile - 1) / kTile; }

@@ -100,6 +100,7 @@ __device__ __forceinline__ int even_tiles(const Params &p, const Request &q)
 
 // The line: a unit is a key tile.
 struct MassWork {
+    static constexpr int kSnap = 0;
     const Params &p;
     bool report;
     // sum over the request's key tiles of their pieces of `each` steps

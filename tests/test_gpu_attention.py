@@ -307,3 +307,13 @@ def test_windows_longer_than_any_context(window):
     assert all(torch.equal(x, y) for x, y in zip(want, got))
     args = (b.q, b.cache, b.table, b.offsets, b.lens, want[1], 128 ** -0.5)
     assert torch.equal(K.kv_attention_mass(*args), K.kv_attention_mass(*args, window=window))
+
+
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 150)])
+def test_many_short_units(causal, window):
+    """Pieces of many units: their ends move to the units' edges."""
+    q = [300 + 7 * i for i in range(48)]
+    b = Batch(q, [n + 13 * i for i, n in enumerate(q)], 12, 12, 64, seed=window, dtype=FP)
+    want = check(b, causal=causal, window=window)
+    for _ in range(5):
+        assert all(torch.equal(x, y) for x, y in zip(want, b.run(64 ** -0.5, causal, window)))

@@ -262,3 +262,12 @@ def test_capacity_is_the_same_for_many_requests():
     table[:, : b.table.shape[1]] = b.table
     b.table = table
     check(b)
+
+
+@pytest.mark.parametrize("heads,reqs", [(16, 300), (100, 150)])
+def test_many_short_contexts(heads, reqs):
+    """Pieces of many units: their ends move to the units' edges."""
+    b = Latent([1] * reqs, [(37 * i) % 1000 + 1 for i in range(reqs)], heads, seed=heads)
+    want = check(b)
+    for _ in range(5):
+        assert all(torch.equal(x, y) for x, y in zip(want, b.run()))
