@@ -382,11 +382,12 @@ extern "C" int kv_latent_attention(const kv_attn_desc *d, const kv_attn_batch *b
     const DeviceInfo *dev = current_device();
     if (dev == nullptr) return KV_ERR_CUDA;
     // Many requests of few rows (tokens times heads, on average) take the kernel that holds 64 rows and all values
-    // a CTA, others the one of 128 rows with a CTA for each half of the values.  One token of 16 heads after 2500
-    // and 10000 tokens at most: 25.6 and 61.9 us here against 26.8 and 53.0 there with 19 requests, 75.0 and
-    // 235.6 against 57.2 and 164.9 with 100; of 64 heads 40.1 and 93.7 against 49.1 and 89.1 with 32 requests,
-    // 65.1 and 190.0 against 64.8 and 146.2 with 76.  With few requests the join of a unit's pieces, by one CTA
-    // there, decides: four requests of 64 rows after 8000 tokens 38 here, 90 there.
+    // a CTA, others the one of 128 rows with a CTA for each half of the values.  In us, one token of 16 heads after at
+    // most 375, 2500 and 10000 tokens: 14.8, 19.6, 34.2 here against 16.3, 25.2, 33.8 there with 8 requests; 16.0,
+    // 26.1, 60.7 against 16.7, 26.7, 53.1 with 19; 27.8, 73.6, 234.9 against 23.6, 57.3, 165.4 with 100.  Of 64 heads
+    // 19.6, 41.5, 95.0 against 25.8, 49.3, 90.1 with 32 requests; 29.6, 63.9, 189.4 against 39.8, 66.7, 146.2 with
+    // 76; 31.9, 80.0, 242.6 against 33.6, 72.0, 180.8 with 100.  With few requests the join of a unit's pieces, by one
+    // CTA there, decides.
     // (Its tiles are half as long: the last condition keeps a batch of any capacity that the other takes.)
     const int64_t reqs = batch->n_reqs, few_rows = reqs < kLatentFewRows ? reqs : kLatentFewRows;
     const bool few = d->n_heads <= kLatentFewRows && batch->n_tokens <= few_rows * reqs / d->n_heads && reqs * 8 >= dev->num_sms &&
