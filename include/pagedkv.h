@@ -529,8 +529,10 @@ KV_API int kv_attention_mass(const kv_attn_desc *d, const kv_attn_batch *batch, 
  *  - out_table == block_table (the same pointer): in place; the pages past new_lens[r] are then free.  The
  *    pages of a request must then belong to it alone.  Otherwise the pages out_table lists must not be
  *    among those block_table lists; shared prefix pages stay as they are.
- *  - new_lens may be kv_lens itself, and out_score score itself (row strides equal).
- *  - kv_lens outside [0, min(max_blocks_per_req * block_size, width)] are clamped, an out_table too short for
+ *  - score has `width` columns; tokens at and past them (written since the scores were taken) count as 0.
+ *  - new_lens may be kv_lens itself, and out_score score itself (row strides equal).  Only budget columns of
+ *    out_score are written: a caller that adds the next weights to the same buffer clears the others first.
+ *  - kv_lens outside [0, max_blocks_per_req * block_size] are clamped, an out_table too short for
  *    the kept tokens truncates their rows, a table entry outside the cache skips its rows: each sets
  *    KV_DERR_TABLE.
  * sinks + recent <= budget (KV_ERR_INVALID_ARG).  Limits: n_reqs <= 65535, budget and the tokens a table row <= 2^30.

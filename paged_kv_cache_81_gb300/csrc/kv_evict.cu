@@ -64,16 +64,17 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Sele
     const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int given = p.kv_lens[r];
     __syncthreads();  // new_lens may be kv_lens
-    const int len = min(max(given, 0), min(p.max_tokens, p.width)), fit = min(p.budget, p.out_tokens);
+    const int len = min(max(given, 0), p.max_tokens), fit = min(p.budget, p.out_tokens);
     if (tid == 0 && (given != len || fit < min(len, p.budget))) set_error(p.err, KV_DERR_TABLE);
     const int total = min(len, p.budget);
-    const float *score = p.score + (int64_t)r * p.score_stride;
+    const float *scores = p.score + (int64_t)r * p.score_stride;
+    const auto score = [&](int j) { return j < p.width ? scores[j] : 0.0f; };  // newer tokens than the scores know weigh nothing yet
     int32_t *kept = p.kept + (int64_t)r * p.kept_stride;
     float *out = p.out_score ? p.out_score + (int64_t)r * p.out_score_stride : nullptr;
     if (tid == 0) p.new_lens[r] = total;
     if (len <= p.budget) {
         for (int i = tid; i < p.budget; i += kSelectThreads) {
-            const float s = i < len ? score[i] : 0.0f;
+            const float s = i < len ? score(i) : 0.0f;
             kept[i] = i < len ? i : -1;
             if (out) out[i] = s;
         }
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Sele
 #pragma unroll
                 for (int i = 0; i < kPer; i++) {
                     const int j = j0 + i * kSelectThreads + tid;
-                    s[i] = j < z ? score[j] : 0.0f;
+                    s[i] = j < z ? score(j) : 0.0f;
                 }
 #pragma unroll
                 for (int i = 0; i < kPer; i++) {
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Sele
 #pragma unroll
         for (int i = 0; i < kPer; i++) {
             const int j = j0 + tid * kPer + i;
-            s[i] = j < len ? score[j] : 0.0f;
+            s[i] = j < len ? score(j) : 0.0f;
         }
 #pragma unroll
         for (int i = 0; i < kPer; i++) {

@@ -743,7 +743,10 @@ def kv_evict(cache: PagedCache, block_table: torch.Tensor, kv_lens: torch.Tensor
              kept: Optional[torch.Tensor] = None, out_score: Optional[torch.Tensor] = None, stream=None):
     """Trims every request to `budget` tokens: the first `sinks`, the last `recent` and the highest scores between, in
     their order; rows of every tensor and plane are gathered to out_table's pages (None: in place).  Returns
-    (new_lens int32 [n_reqs], kept int32 [n_reqs, budget], out_score float32 [n_reqs, budget])."""
+    (new_lens int32 [n_reqs], kept int32 [n_reqs, budget], out_score float32 [n_reqs, budget]).
+
+    Tokens past score's columns count as 0.  Of out_score only `budget` columns are written: to go on adding weights,
+    keep a score of a table row's slots, clear it and copy out_score to its first columns."""
     _int32(budget=budget, sinks=sinks, recent=recent)
     dev = kv_lens.get_device()
     handle = _begin(dev, stream)

@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import math
+from types import SimpleNamespace
 
 import numpy as np
 import pytest
@@ -313,3 +314,109 @@ def test_lengths_in_place():
     assert new is lens and lens.tolist() == [min(n, 700) for n in old]
     for r, n in enumerate(old):
         assert kept[r].tolist() == keep_reference(s[r].tolist(), n, 700, 2, 9) + [-1] * (700 - min(n, 700))
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("width,budget,sinks,recent", [(100, 64, 4, 20), (100, 160, 0, 0), (0, 64, 4, 20), (280, 64, 0, 64), (299, 30, 0, 1), (300, 30, 0, 1)])
+def test_scores_narrower_than_the_cache(width, budget, sinks, recent, in_place):
+    """Tokens that came after the scores were taken count as 0; none is dropped for it, the last ones least of all."""
+    lens = [300, 90, 100, 101, 400]
+    s = torch.zeros(5, 400)
+    s[:, :width] = scores(5, 400, 2)[:, :width]
+    g = torch.Generator().manual_seed(width)
+    block, row = 16, 16
+    need = [-(-n // block) for n in lens]
+    table = torch.full((5, max(need)), -1, dtype=torch.int32)
+    ids = torch.randperm(sum(need) + 5 * 10, generator=g).to(torch.int32)
+    for r, n in enumerate(need):
+        table[r, :n] = ids[sum(need[:r]):sum(need[:r]) + n]
+    out_table = table if in_place else ids[sum(need):].view(5, 10).contiguous()
+    host = torch.randint(-2 ** 15, 2 ** 15, (len(ids), block, row), generator=g, dtype=torch.int16)
+    dev = host.cuda().view(BF)
+    K.kv_get_last_error(clear=True)
+    new, kept, out = K.kv_evict(K.PagedCache.from_tensors([dev], "separate"), table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                s[:, :width].contiguous().cuda(), budget, sinks=sinks, recent=recent, out_table=None if in_place else out_table.cuda())
+    assert K.kv_get_last_error(clear=True) == 0
+    got = dev.view(torch.int16).cpu()
+    for r, n in enumerate(lens):
+        keep = keep_reference(s[r].tolist(), n, budget, sinks, recent)
+        assert int(new[r]) == len(keep) == min(n, budget)
+        assert kept[r].tolist() == keep + [-1] * (budget - len(keep))
+        assert out[r].tolist() == s[r][keep].tolist() + [0.0] * (budget - len(keep))
+        j, i = torch.tensor(keep), torch.arange(len(keep))
+        assert torch.equal(got[out_table[r].long()[i // block], i % block], host[table[r].long()[j // block], j % block])
+
+
+def test_narrow_scores_in_place_of_longer_lists():
+    """out_score may be the score's buffer when the budget is larger than the columns that hold scores."""
+    buf = torch.full((2, 300), 7.0, device="cuda")
+    buf[:, :50] = scores(2, 50, 4).cuda()
+    want = buf.cpu()
+    cache = K.PagedCache.from_tensors([torch.zeros(2 * 30, 16, 8, dtype=BF, device="cuda")], "separate")
+    table = torch.arange(60, dtype=torch.int32, device="cuda").view(2, 30)
+    _, kept, _ = K.kv_evict(cache, table, torch.tensor([400, 70], dtype=torch.int32, device="cuda"), buf[:, :50], 100, sinks=2, recent=60,
+                            out_score=buf)
+    for r, n in enumerate((400, 70)):
+        s = torch.zeros(n)
+        s[:50] = want[r, :50]
+        keep = keep_reference(s.tolist(), n, 100, 2, 60)
+        assert kept[r, :len(keep)].tolist() == keep
+        assert buf[r, :100].tolist() == s[keep].tolist() + [0.0] * (100 - len(keep))
+    assert torch.equal(buf[:, 100:].cpu(), want[:, 100:])
+
+
+@pytest.mark.parametrize("narrow", [False, True])
+def test_trimming_again_and_again(narrow):
+    """Decode steps and trims in turn: the newest tokens always stay, and a new token's weight starts at nothing.
+    narrow: the trimmed scores are handed on as they are, and tokens past their columns count as 0."""
+    heads, kv_heads, d, block, budget, sinks, recent, scale, slots = 4, 2, 64, 16, 48, 4, 16, 64 ** -0.5, 96
+    g = torch.Generator().manual_seed(3)
+    lens = [70, 40, 48]
+    table = torch.randperm(18, generator=g).to(torch.int32).view(3, 6).cuda()
+    pool = torch.zeros(18, 2, block, kv_heads, d, dtype=BF, device="cuda")
+    cache = K.PagedCache.from_tensors([pool], "blocks_first")
+    k_rows, v_rows = ([torch.zeros(0, kv_heads, d, dtype=BF) for _ in lens] for _ in range(2))
+    score = torch.zeros(3, slots, device="cuda")
+    held, names, count = [0, 0, 0], [[], [], []], [0, 0, 0]  # names: each held token's number in its request's life
+    K.kv_get_last_error(clear=True)
+    for step in range(12):
+        new = lens if step == 0 else [1, 1, 1]
+        req = torch.cat([torch.full((n,), r) for r, n in enumerate(new)]).to(torch.int32).cuda()
+        pos = torch.cat([torch.arange(h, h + n) for h, n in zip(held, new)]).to(torch.int32).cuda()
+        k_new, v_new = ([torch.randn(n, kv_heads, d, generator=g).to(BF) for n in new] for _ in range(2))
+        K.kv_write_tokens(cache, [torch.cat(k_new).cuda(), torch.cat(v_new).cuda()], table, req, pos)
+        k_rows, v_rows = ([torch.cat(x) for x in zip(rows, fresh)] for rows, fresh in ((k_rows, k_new), (v_rows, v_new)))
+        for r, n in enumerate(new):
+            names[r] += range(count[r], count[r] + n)
+            count[r] += n
+            assert torch.all(score[r, held[r]:] == 0)  # of tokens that were trimmed nothing is left for the new ones
+        held = [h + n for h, n in zip(held, new)]
+        kv = torch.tensor(held, dtype=torch.int32, device="cuda")
+        offsets = torch.tensor([0] + list(np.cumsum(new)), dtype=torch.int32, device="cuda")
+        q = torch.randn(sum(new), heads, d, generator=g).to(BF)
+        out, lse = K.kv_attention(q.cuda(), cache, table, offsets, kv, scale)
+        o, l, to, tl = reference(q, k_rows, v_rows, new, scale)
+        close(out, o, to, "out")
+        close(lse, l, tl, "lse")
+        b = SimpleNamespace(q_cpu=q, q_lens=new, kv_lens=held, k_rows=k_rows, heads=heads, kv_heads=kv_heads, dk=d)
+        want, tol = mass_reference(b, lse, scale, True, 0, score.shape[1], score)
+        score = K.kv_attention_mass(q.cuda(), cache, table, offsets, kv, lse, scale, prev=score)
+        close(score, want, tol, "mass")
+        if step % 2 == 0 or narrow:
+            known = [(score[r].tolist() + [0.0] * held[r])[:held[r]] for r in range(3)]
+            keeps = [keep_reference(known[r], held[r], budget, sinks, recent) for r in range(3)]
+            kv, kept, heavy = K.kv_evict(cache, table, kv, score, budget, sinks=sinks, recent=recent)
+            held = [min(h, budget) for h in held]
+            assert kv.tolist() == held
+            for r, keep in enumerate(keeps):
+                assert kept[r, :held[r]].tolist() == keep, (step, r)
+                names[r] = [names[r][j] for j in keep]
+                k_rows[r], v_rows[r] = k_rows[r][keep], v_rows[r][keep]
+            if narrow:
+                score = heavy
+            else:
+                score.zero_()[:, :budget] = heavy
+        for r in range(3):
+            tail = min(recent, count[r])
+            assert names[r][-tail:] == list(range(count[r] - tail, count[r])), (step, r)
+    assert K.kv_get_last_error(clear=True) == 0
