@@ -437,8 +437,8 @@ typedef struct {
 
 /* Device workspace bytes that one kv_attention or kv_latent_attention call needs on the current device,
  * whatever its sizes.  The caller zeroes the workspace once (its first KV_ATTENTION_ZEROED_BYTES are enough);
- * every call leaves its counters zero again (after KV_DERR_TIMEOUT, zero it anew).  Calls sharing a workspace must
- * be ordered. */
+ * every call leaves its counters zero again, but one that sets KV_DERR_TIMEOUT: the workspaces of calls since the word
+ * was last clear are then zeroed anew before they are used.  Calls sharing a workspace must be ordered. */
 enum { KV_ATTENTION_ZEROED_BYTES = 16384 };
 KV_API int kv_attention_workspace_bytes(int64_t *bytes_out);
 

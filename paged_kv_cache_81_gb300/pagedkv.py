@@ -476,8 +476,12 @@ def kv_wait_signal(signal: torch.Tensor, expected: int, timeout_us: int, status:
 
 
 def kv_get_last_error(clear: bool = True, stream=None) -> int:
+    """The sticky error word (KV_DERR_* bits).  Where it reports KV_DERR_TIMEOUT, the workspaces that the attention
+    calls without one keep on this device are given up: a call that broke off leaves its counters in them."""
     out = ctypes.c_int32(0)
     _check("kv_get_last_error", load().kv_get_last_error(ctypes.byref(out), 1 if clear else 0, _stream(stream)))
+    if out.value & KV_DERR_TIMEOUT:
+        kv_reset_workspaces()
     return out.value
 
 
@@ -509,6 +513,15 @@ def kv_attention_workspace(device="cuda") -> torch.Tensor:
 
 
 _workspaces = {}  # (bytes function, device, stream handle) -> the workspace of calls without one on that stream
+
+
+def kv_reset_workspaces(device: Optional[int] = None):
+    """Gives up the workspaces that calls without one keep, one a stream, on a device (default: the current one).  The
+    next such call makes a zeroed one.  Done by kv_get_last_error after a timeout; also frees those of streams that are no longer used."""
+    dev = torch.cuda.current_device() if device is None else device
+    for key in list(_workspaces):
+        if key[1] == dev:
+            _workspaces.pop(key, None)
 
 
 def _workspace(nbytes, dev: int, handle: int, given: Optional[torch.Tensor], stream) -> torch.Tensor:
