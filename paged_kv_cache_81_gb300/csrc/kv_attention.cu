@@ -50,7 +50,8 @@ struct Params {
     Batch b;
     const int32_t *table;
     int64_t table_stride;
-    int32_t num_blocks;
+    int32_t num_blocks;  // pages that both caches have
+    int32_t no_page;     // a page that neither has: its loads bring zeros
     FastDiv block;       // slots of a page
     int32_t piece_rows;  // slots one TMA brings: gcd(block, 128), so it never leaves a page
     int32_t q_box;       // tokens one TMA brings of q
@@ -91,7 +92,7 @@ __device__ __forceinline__ bool load_tile(const Params &p, const CUtensorMap *ma
         page = __ldg(row + col);
         if (page < 0 || page >= p.num_blocks) {
             set_error(p.b.err, KV_DERR_TABLE);
-            page = p.num_blocks;  // outside the map: reads zeros
+            page = p.no_page;
         }
     };
     if (p0 + lane < p1) find(p0 + lane);
@@ -640,6 +641,7 @@ int kv_attention(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_cac
     p.table = batch->block_table;
     p.table_stride = batch->bt_row_stride;
     p.num_blocks = (int32_t)(k->num_blocks < v->num_blocks ? k->num_blocks : v->num_blocks);
+    p.no_page = (int32_t)(k->num_blocks < v->num_blocks ? v->num_blocks : k->num_blocks);
     p.block = make_fastdiv((uint32_t)k->block_size);
     p.piece_rows = piece_rows(k->block_size, kTile);
     p.o = Output{(char *)out, out_token_stride, out_head_stride, lse, d->n_heads, d->head_dim_v, d->scale, d->scale * kLog2e};

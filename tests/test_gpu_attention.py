@@ -317,3 +317,29 @@ def test_many_short_units(causal, window):
     want = check(b, causal=causal, window=window)
     for _ in range(5):
         assert all(torch.equal(x, y) for x, y in zip(want, b.run(64 ** -0.5, causal, window)))
+
+
+@pytest.mark.parametrize("more_keys", [True, False])
+@pytest.mark.parametrize("dtype,dv", [(BF, 64), (FP, 128)])
+def test_pools_of_different_sizes(more_keys, dtype, dv):
+    """A page that only one of the two pools has is outside the cache: zeros from both, whatever that page holds."""
+    b = Batch([1, 3], [100, 50], 4, 2, 64, dv, block=16, dtype=dtype, seed=6)
+    large = 0 if more_keys else 1
+    pools = [b.tensors[0], b.tensors[1]]
+    more = torch.full((9, *pools[large].shape[1:]), NAN, dtype=dtype, device="cuda")
+    pools[large] = torch.cat([pools[large], more])
+    b.tensors = pools
+    b.cache, b.v_cache = (K.PagedCache.from_tensors([x], "separate") for x in pools)
+    check(b)  # the pages that both have
+    b.table[0, 2] = b.pages  # the first that one lacks, the last that the other has, and one that neither has
+    b.table[0, 4] = b.pages + 8
+    b.table[1, 0] = b.pages + 9
+    for r, page in ((0, 2), (0, 4), (1, 0)):
+        b.k_rows[r][page * 16:(page + 1) * 16] = 0
+        b.v_rows[r][page * 16:(page + 1) * 16] = 0
+    K.kv_get_last_error(clear=True)
+    out, lse = b.run(0.125)
+    assert K.kv_get_last_error(clear=True) == K.KV_DERR_TABLE
+    o, l, to, tl = reference(b.q_cpu, b.k_rows, b.v_rows, b.q_lens, 0.125)
+    close(out, o, to, "out")
+    close(lse, l, tl, "lse")
