@@ -247,9 +247,11 @@ expand_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__
                                   : make_uint4(0, 0, 0, 0);
                 }
             }
-            // the tile's latents into tensor memory, half of the panels a group.  Both groups have waited for their
-            // last products of the tile before, and the other group's came no later than one product more
+            // the tile's latents into tensor memory, half of the panels a group, once the last product of the tile before,
+            // which reads the ones that they replace, has ended (both groups have seen the last but one end, so the
+            // barrier is in this phase or past it)
             if (frag && !wait.warp(smem_addr(&aux.d_full[1]), (heads - 1) & 1)) break;
+            tc_fence_after();
             frag = true;
             for (int part = 0; part < 8; part += kAPart) {
                 if (!(ok = wait.warp(smem_addr(&aux.a_full), (part / kAPart) & 1))) break;

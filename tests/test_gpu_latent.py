@@ -271,3 +271,38 @@ def test_many_short_contexts(heads, reqs):
     want = check(b)
     for _ in range(5):
         assert all(torch.equal(x, y) for x, y in zip(want, b.run()))
+
+
+@pytest.mark.parametrize("heads", [1, 3])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_expand_tile_after_tile(heads, dtype):
+    """Few heads and many token tiles: a CTA replaces its latents in tensor memory after every few products."""
+    lens, block = [60000, 33333], 64
+    g = torch.Generator(device="cuda").manual_seed(heads)
+    need = [-(-n // block) for n in lens]
+    ids = torch.randperm(sum(need), generator=g, device="cuda").to(torch.int32)
+    table = torch.full((2, need[0]), -1, dtype=torch.int32, device="cuda")
+    table[0], table[1, : need[1]] = ids[: need[0]], ids[need[0]:]
+    pool = torch.randn(sum(need), block, 576, generator=g, device="cuda").to(dtype)
+    w = (torch.randn(heads, 256, 512, generator=g, device="cuda") / 16).to(dtype)
+    k, v = (torch.zeros(sum(need), block, heads, d, dtype=dtype, device="cuda") for d in (192, 128))
+    latent, k_cache, v_cache = K.PagedCache.from_tensors([pool], "mla"), *(K.PagedCache.from_tensors([x], "separate") for x in (k, v))
+    kv_lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    first = None
+    for _ in range(8):
+        k.fill_(9), v.fill_(9)
+        K.kv_latent_expand(latent, table, kv_lens, w, k_cache, v_cache, table)
+        if first is None:
+            first = k.clone(), v.clone()
+        assert torch.equal(k, first[0]) and torch.equal(v, first[1])
+    for r, n in enumerate(lens):
+        at = torch.arange(n, device="cuda")
+        page, slot = table[r].long()[at // block], at % block
+        rows = pool[page, slot].double()
+        for h in range(heads):
+            want = rows[:, :512] @ w[h].double().t()
+            # rounded once; sums of 512 terms and the order of 32 bits as in expand_reference
+            tol = U[dtype] * want.abs() * 1.01 + 528 * 2.0 ** -24 * (rows[:, :512].abs() @ w[h].double().abs().t()) + 2.0 ** -25
+            got = torch.cat([k[page, slot, h, :128], v[page, slot, h]], 1).double()
+            assert bool(((got - want).abs() <= tol).all())
+            assert torch.equal(k[page, slot, h, 128:].double(), rows[:, 512:])
