@@ -454,7 +454,8 @@ KV_API int kv_attention_workspace_bytes(int64_t *bytes_out);
  * held in 32 bits; the weights p are rounded to the element type before they multiply the values.
  * Slots at and past kv_lens[r], and before every window, are not used whatever they hold; the
  * tokens a request does hold must be finite.
- *  - q_offsets that decrease or leave [0, n_tokens] are clamped and set KV_DERR_LIST; a kv_len outside
+ *  - q_offsets that decrease or leave [0, n_tokens] are clamped and set KV_DERR_LIST (requests that then overlap
+ *    are not to be relied on, and nothing is computed where their work passes 2^31 steps); a kv_len outside
  *    [0, max_blocks_per_req * block_size] is clamped, and a table entry outside the cache reads as a
  *    page of zeros: both set KV_DERR_TABLE.
  *  - out must not overlap q, the cache or the workspace.

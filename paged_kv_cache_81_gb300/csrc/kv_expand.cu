@@ -67,7 +67,7 @@ struct ExpandWork {
     {
         const int tiles = (request_len(p, r, report) + kTile - 1) / kTile;
         n += tiles;
-        steps += tiles * p.heads;
+        steps = add_steps(steps, tiles * p.heads);
     }
     __device__ __forceinline__ int pieces(int r, int each) const { return units(r) * ceil_div(p.heads, each); }
     __device__ __forceinline__ Place own(int r, int k, int each) const

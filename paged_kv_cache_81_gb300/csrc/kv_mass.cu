@@ -114,7 +114,7 @@ struct MassWork {
     __device__ __forceinline__ void measure(int r, int &steps, int &units) const
     {
         const Request q = load_request(p.b, r, report);
-        steps += count(q, 1);
+        steps = add_steps(steps, count(q, 1));
         units += (q.len + kTile - 1) / kTile;
     }
     __device__ __forceinline__ int pieces(int r, int each) const { return count(load_request(p.b, r), each); }

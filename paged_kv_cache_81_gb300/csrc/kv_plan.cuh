@@ -120,6 +120,11 @@ struct Line {
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (int)((uint32_t)(a + b - 1) / (uint32_t)b); }
 
+// A sum of steps, which stays at kTooLong once it gets there.  The hosts refuse batches whose steps would not fit 32 bits;
+// offsets that decrease name requests that overlap, and many of those may add up to more.
+constexpr int kTooLong = 0x7fffffff;
+__device__ __forceinline__ int add_steps(int a, int b) { return (int)min((uint32_t)a + (uint32_t)b, (uint32_t)kTooLong); }
+
 // Inclusive scan of `mine` over the block, and the sums of it and of `other`.  scratch: two words a warp.
 template <int Threads>
 __device__ __forceinline__ int block_scan(int mine, int other, int *scratch, int &total, int &other_total)
@@ -130,15 +135,15 @@ __device__ __forceinline__ int block_scan(int mine, int other, int *scratch, int
     for (int d = 1; d < 32; d <<= 1) {
         const int o = __shfl_up_sync(0xffffffffu, upto, d);
         other += __shfl_xor_sync(0xffffffffu, other, d);
-        if (lane >= d) upto += o;
+        if (lane >= d) upto = add_steps(upto, o);
     }
     if (lane == 31) scratch[2 * warp] = upto, scratch[2 * warp + 1] = other;
     __syncthreads();
     total = other_total = 0;
 #pragma unroll 1
     for (int w = 0; w < Threads / 32; w++) {
-        if (w == warp) upto += total;
-        total += scratch[2 * w];
+        if (w == warp) upto = add_steps(upto, total);
+        total = add_steps(total, scratch[2 * w]);
         other_total += scratch[2 * w + 1];
     }
     return upto;
@@ -146,10 +151,10 @@ __device__ __forceinline__ int block_scan(int mine, int other, int *scratch, int
 
 // Finds a CTA's piece; every thread of the block calls it.  The line is made of n_reqs stretches, and `work`
 // says of one:
-//   measure(r, steps, units)   adds its length (less than 2^31 in all) and its units
+//   measure(r, steps, units)   adds its length (add_steps; less than 2^31) and its units
 //   pieces(r, each)            its pieces when every unit is cut by itself into pieces of `each` steps
 //   own(r, k, each)            the k-th of them (each = 1: step k)
-// scratch: four words a warp.  Pieces of units are of at least `least` steps.
+// scratch: four words a warp.  Pieces of units are of at least `least` steps.  A line that is too long has no pieces.
 //
 // The ends of equal pieces move to the edge of a unit where that is within Work::kSnap steps (a cut costs both of its
 // sides three or four), if pieces are long against that and units short enough for most ends to find an edge:
@@ -168,8 +173,9 @@ __device__ __forceinline__ Line find_piece(int n_reqs, int part, int parts, int 
 #pragma unroll 1
     for (int r = r0; r < r1; r++) work.measure(r, mine, units);
     int at = block_scan<Threads>(mine, units, scratch, total, unit_total);
+    Line line = {};
+    if (total == kTooLong) return line;
     const int used = max(1, min(parts, total));
-    Line line;
     line.part = part;
     line.nth = -1;
     line.snap = total / 32 <= unit_total && total >= 16 * used ? Work::kSnap : 0;
@@ -217,7 +223,7 @@ struct AttentionWork {
     __device__ __forceinline__ void measure(int r, int &steps, int &units) const
     {
         const Request q = load_request(b, r, report);
-        steps += head_cost(b, q) * b.kv_heads;
+        steps = add_steps(steps, head_cost(b, q) * b.kv_heads);
         units += q.units * b.kv_heads;
     }
     __device__ __forceinline__ int head_pieces(const Request &q, int each) const

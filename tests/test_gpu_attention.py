@@ -343,3 +343,37 @@ def test_pools_of_different_sizes(more_keys, dtype, dv):
     o, l, to, tl = reference(b.q_cpu, b.k_rows, b.v_rows, b.q_lens, 0.125)
     close(out, o, to, "out")
     close(lse, l, tl, "lse")
+
+
+@pytest.mark.parametrize("op,n_reqs", [("attention", 8400), ("attention", 16400), ("mass", 4200), ("mass", 8200), ("latent", 16500), ("latent", 33000)])
+def test_offsets_that_name_the_same_tokens_again_and_again(op, n_reqs):
+    """Every other request takes the whole batch: their steps pass 2^31, and 2^32, although the batch is within the limits.
+    It is reported, nothing is computed, and the next call is right."""
+    tokens, heads, kv_heads, dk, dv, block = (8192, 16, 1, 576, 512, 64) if op == "latent" else (32768, 32, 8, 64, 64, 16)
+    pool = torch.zeros(4, block, kv_heads * dk, dtype=BF, device="cuda")
+    cache = K.PagedCache.from_tensors([pool], "separate")
+    q = torch.zeros(tokens, heads, dk, dtype=BF, device="cuda")
+    table = torch.zeros(n_reqs, tokens // block, dtype=torch.int32, device="cuda")
+    offsets = torch.zeros(n_reqs + 1, dtype=torch.int32, device="cuda")
+    offsets[1::2] = tokens
+    lens = torch.full((n_reqs,), tokens, dtype=torch.int32, device="cuda")
+    lse = torch.full((tokens, heads), 5.0, device="cuda")
+    # steps of one such request: rows of 64 (latent), 256 or, for the mass, tokens in steps of 32, against tiles of 32 or 128 keys
+    if op == "latent":
+        each = sum((4 * u + 3) // 32 + 1 for u in range(tokens // 4))
+    elif op == "mass":
+        each = sum((tokens - 128 * t + 31) // 32 * kv_heads for t in range(tokens // 128))
+    else:
+        each = sum((64 * u + 63) // 128 + 1 for u in range(tokens // 64)) * kv_heads
+    assert each * (n_reqs // 2) >= 2 ** 31
+    K.kv_get_last_error(clear=True)
+    if op == "mass":
+        out = torch.full((n_reqs, 40), 3.0, device="cuda")
+        K.kv_attention_mass(q, cache, table, offsets, lens, lse, 0.1, score=out)
+    else:
+        out = torch.full((tokens, heads, dv), 3.0, dtype=BF, device="cuda")
+        call = K.kv_latent_attention if op == "latent" else K.kv_attention
+        call(q, cache, table, offsets, lens, 0.1, out=out, lse=lse, **({} if op == "latent" else dict(v_cache=cache)))
+    assert K.kv_get_last_error(clear=True) == K.KV_DERR_LIST
+    assert bool((out == 3).all()) and bool((lse == 5).all())
+    check(Batch([1, 60], [300, 200], 8, 2, 64, seed=1))
