@@ -173,9 +173,9 @@ __device__ __forceinline__ Line find_piece(int n_reqs, int part, int parts, int 
 #pragma unroll 1
     for (int r = r0; r < r1; r++) work.measure(r, mine, units);
     int at = block_scan<Threads>(mine, units, scratch, total, unit_total);
-    Line line = {};
-    if (total == kTooLong) return line;
+    if (total == kTooLong) total = 0, unit_total = 1 << 30;
     const int used = max(1, min(parts, total));
+    Line line;
     line.part = part;
     line.nth = -1;
     line.snap = total / 32 <= unit_total && total >= 16 * used ? Work::kSnap : 0;
