@@ -329,7 +329,7 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                         tc_wait_ld();
                         top = max32(x1, top);
                     }
-                    const bool grow = top > m + slack;  // -inf + slack: the first finite score
+                    const bool grow = top > __fadd_rd(m, slack);  // -inf + slack: the first finite score
                     if (__any_sync(0xffffffffu, grow)) {
                         const float to_m = grow ? top : m;
                         const float alpha = grow ? exp2_fast((m - to_m) * p.o.c) : 1.0f;
@@ -349,7 +349,7 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                             }
                         }
                     }
-                    const float mc = m == -INFINITY ? 0.0f : m * p.o.c;
+                    const float mc = weight_offset<Bf16>(m, p.o.c);
                     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                     uint32_t pk[16];
                     // P takes the columns of the upper 64 scores: 32 keys' weights stand in 16 columns from 64 on, so
@@ -453,7 +453,7 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                 }
                 if (live) {
                     if (whole) {
-                        if (lse) *lse = l > 0.0f ? fmaf(m, p.o.scale, logf(l)) : -INFINITY;
+                        if (lse) *lse = l > 0.0f ? fmaf(m, p.o.scale, weight_log<Bf16>(l)) : -INFINITY;
                     } else {
                         part[kRows * DV + row] = m;
                         part[kRows * DV + kRows + row] = l;

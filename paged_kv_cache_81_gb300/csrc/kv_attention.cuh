@@ -178,7 +178,7 @@ __device__ __noinline__ void join_rows(const Output p, const Pieces at, int half
                     v.y = pack2<Bf16>(o[k].z * inv, o[k].w * inv);
                     *reinterpret_cast<uint2 *>(to + (half * DV + (q + k) * 4) * 2) = v;
                 }
-            if (half == 0 && q == 0 && p.lse) p.lse[token * p.heads + head] = l > 0.0f ? fmaf(top, p.scale, logf(l)) : -INFINITY;
+            if (half == 0 && q == 0 && p.lse) p.lse[token * p.heads + head] = l > 0.0f ? fmaf(top, p.scale, weight_log<Bf16>(l)) : -INFINITY;
         }
     };
     // what the registers beside the tile loop hold; two fragments (a long unit's usual cut) in four trips a row instead

@@ -249,7 +249,7 @@ latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ C
                         hide32(x[1], lo - kb - 32, hi - kb - 32);
                     }
                     const float top = max32(x[1], max32(x[0], -INFINITY));
-                    const bool grow = top > m + slack;
+                    const bool grow = top > __fadd_rd(m, slack);
                     if (__any_sync(0xffffffffu, grow)) {
                         const float to_m = grow ? top : m;
                         const float alpha = grow ? exp2_fast((m - to_m) * p.o.c) : 1.0f;
@@ -269,7 +269,7 @@ latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ C
                             }
                         }
                     }
-                    const float mc = m == -INFINITY ? 0.0f : m * p.o.c;
+                    const float mc = weight_offset<Bf16>(m, p.o.c);
                     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                     uint32_t pk[16];
                     weights32<Bf16>(x[0], p.o.c, mc, sum, pk);
@@ -322,7 +322,7 @@ latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ C
                 }
                 if (live) {
                     if (whole) {
-                        if (p.o.lse && half == 0) p.o.lse[out_row * p.o.heads + head] = l > 0.0f ? fmaf(m, p.o.scale, logf(l)) : -INFINITY;
+                        if (p.o.lse && half == 0) p.o.lse[out_row * p.o.heads + head] = l > 0.0f ? fmaf(m, p.o.scale, weight_log<Bf16>(l)) : -INFINITY;
                     } else {
                         frag[kRows * kHalf + t] = m;
                         frag[kRows * (kHalf + 1) + t] = l;

@@ -189,7 +189,7 @@ latent_few_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant
                     if (__any_sync(0xffffffffu, kb < lo || kb + kKeys > hi)) hide32(v, lo - kb, hi - kb);
                     // the upper lanes hold no scores; they follow the row's maximum for their half of O
                     const float top = __shfl_sync(0xffffffffu, max32(v, -INFINITY), lane & 15);
-                    const bool grow = top > m + slack;
+                    const bool grow = top > __fadd_rd(m, slack);
                     any = __any_sync(0xffffffffu, grow);
                     if (any) {
                         const float to_m = grow ? top : m;
@@ -197,7 +197,7 @@ latent_few_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant
                         l *= alpha;
                         m = to_m;
                     }
-                    const float mc = m == -INFINITY ? 0.0f : m * p.o.c;
+                    const float mc = weight_offset<Bf16>(m, p.o.c);
                     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                     weights32<Bf16>(v, p.o.c, mc, sum, pk);
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
@@ -261,7 +261,7 @@ latent_few_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant
                 }
                 if (live) {
                     if (whole) {
-                        if (p.o.lse && half == 0) p.o.lse[out_row * p.o.heads + head] = l > 0.0f ? fmaf(m, p.o.scale, logf(l)) : -INFINITY;
+                        if (p.o.lse && half == 0) p.o.lse[out_row * p.o.heads + head] = l > 0.0f ? fmaf(m, p.o.scale, weight_log<Bf16>(l)) : -INFINITY;
                     } else {
                         frag[kRows * kHalf + row] = m;
                         frag[kRows * (kHalf + 1) + row] = l;

@@ -284,6 +284,22 @@ __device__ __forceinline__ float max32(const uint32_t (&x)[32], float top)
     return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
 }
 
+// The weights P = 2^(c (s - m)) become 16-bit numbers for the second product, whose operands have one type; a second
+// product for what the rounding leaves would double its time.  m is the row's reference: its largest score, or one
+// that it exceeds by less than 2^8.  bf16 holds such weights however small.  fp16 has nothing below 2^-25, while the
+// sum of the weights counts them all: behind one heavy key, 8191 light ones of 2^-26 (together 1.2e-4 of the sum) came
+// out as 0.  So fp16 weights are held 2^7 times as large, up to 2^15 of 2^16, and what is lost is below 2^-32 each.  The rounding
+// goes up, so that no weight passes that bound for what the product of large scores rounds off.
+template <bool Bf16>
+__device__ __forceinline__ float weight_offset(float m, float c)
+{
+    return m == -INFINITY ? 0.0f : Bf16 ? m * c : __fmaf_ru(m, c, -7.0f);
+}
+
+// The logarithm of a sum of such weights.
+template <bool Bf16>
+__device__ __forceinline__ float weight_log(float l) { return logf(Bf16 ? l : l * 0x1p-7f); }
+
 // Weights 2^(c s - mc) of 32 scores, added to two partial sums and rounded to pairs of the element type.
 template <bool Bf16>
 __device__ __forceinline__ void weights32(const uint32_t (&x)[32], float c, float mc, float2 (&sum)[2], uint32_t (&pk)[16])

@@ -1,6 +1,8 @@
 """kv_attention on the GPU against 64-bit references: shapes, masks, page layouts, strides, streams, graphs."""
 from __future__ import annotations
 
+import math
+
 import pytest
 import torch
 
@@ -377,3 +379,39 @@ def test_offsets_that_name_the_same_tokens_again_and_again(op, n_reqs):
     assert K.kv_get_last_error(clear=True) == K.KV_DERR_LIST
     assert bool((out == 3).all()) and bool((lse == 5).all())
     check(Batch([1, 60], [300, 200], 8, 2, 64, seed=1))
+
+
+@pytest.mark.parametrize("op", ["attention", "latent", "latent of many heads"])
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("score", [10.0, 18.0, 21.0])
+def test_many_light_weights_behind_a_heavy_one(op, dtype, score):
+    """One key takes nearly all; the 8191 others, of weight e^-score each, hold all the value there is.  Their sum has to be
+    in the output as it is in the sum of the weights, though each of them is below what an fp16 number can hold."""
+    n, reqs, block = 8192, 160, 64
+    heads, dk, dv = {"attention": (1, 64, 64), "latent": (1, 576, 512), "latent of many heads": (128, 576, 512)}[op]
+    at = 0 if op == "attention" else 512  # the rotary part is no value
+    q = torch.zeros(reqs, heads, dk, dtype=dtype, device="cuda")
+    q[:, :, at] = 1
+    keys = torch.zeros(n // block, block, dk, dtype=dtype, device="cuda")
+    if op == "attention":
+        values = torch.ones(n // block, block, dv, dtype=dtype, device="cuda")
+        values[0, 0] = 0
+    else:
+        keys[:, :, :512] = 1
+        keys[0, 0] = 0
+    keys[0, 0, at] = score
+    table = torch.arange(n // block, dtype=torch.int32, device="cuda").repeat(reqs, 1)
+    lens, offsets = torch.full((reqs,), n, dtype=torch.int32, device="cuda"), torch.arange(reqs + 1, dtype=torch.int32, device="cuda")
+    cache = K.PagedCache.from_tensors([keys], "separate")
+    if op == "attention":
+        out, lse = K.kv_attention(q, cache, table, offsets, lens, 1.0, v_cache=K.PagedCache.from_tensors([values], "separate"))
+    else:
+        out, lse = K.kv_latent_attention(q, cache, table, offsets, lens, 1.0)
+    light = (n - 1) * math.exp(-score)
+    want = light / (1 + light)
+    # every weight is alike, so their roundings add up: half a step of the type (bf16), or half of fp16's smallest step, 2^-25, of
+    # weights held 2^7 times as large; then the output's rounding, and 32-bit sums and exponentials
+    u = 2.0 ** -8 if dtype is BF else 2.0 ** -11
+    tol = 2 * u * want * 1.01 + (n * 2.0 ** -32 if dtype is FP else 0.0) + 2.0 ** -17 * want
+    assert float((out.double() - want).abs().max()) <= tol
+    assert float((lse.double() - (score + math.log1p(light))).abs().max()) <= 2.0 ** -21 * (score + 1)
