@@ -571,7 +571,10 @@ def _table(dev: int, t: torch.Tensor, n: int, name: str):
     row, one = t.stride()
     if one != 1:
         raise ValueError(f"{name} must be row-major")
-    return t.data_ptr(), t.shape[1], row
+    pages = t.shape[1]
+    if pages >= 2 ** 31:
+        raise ValueError(f"{name}'s columns must be a 32-bit number")
+    return t.data_ptr(), pages, row
 
 
 def _i32_on(dev: int, t: torch.Tensor, n: int, name: str) -> int:
@@ -629,6 +632,13 @@ def _int32(**values):
             raise ValueError(f"{name} must be a 32-bit number")
 
 
+def _tensor_numbers(*numbers):
+    """Short of _int32's names: these are checked at every call."""
+    for x in numbers:
+        if not -2 ** 31 <= x < 2 ** 31:
+            raise ValueError("a tensor's number must be a 32-bit number")
+
+
 @functools.lru_cache(maxsize=256)
 def _attn_desc(*fields) -> KvAttnDesc:
     """Descriptions repeat from layer to layer; the library only reads them."""
@@ -644,6 +654,7 @@ def kv_attention(q: torch.Tensor, cache: PagedCache, block_table: torch.Tensor, 
 
     Keys are tensor `k_tensor` of `cache` (plane 0).  Values are tensor `v_tensor` of `v_cache`, or, without a
     `v_cache`, plane 1 of the same tensor (two-plane caches) or tensor `v_tensor` of `cache`."""
+    _tensor_numbers(k_tensor, v_tensor or 0)
     code, q_token, q_head = _rows3(q, "q")
     dev = q.get_device()
     handle = _begin(dev, stream)
@@ -676,6 +687,7 @@ def kv_latent_attention(q: torch.Tensor, cache: PagedCache, block_table: torch.T
                         workspace: Optional[torch.Tensor] = None, stream=None):
     """Attention of new tokens q [tokens, heads, 576] over a latent cache (the absorbed form); returns
     (out [tokens, heads, 512], lse float32 [tokens, heads])."""
+    _tensor_numbers(tensor)
     code, q_token, q_head = _rows3(q, "q")
     dev = q.get_device()
     handle = _begin(dev, stream)
@@ -695,6 +707,7 @@ def kv_latent_expand(cache: PagedCache, block_table: torch.Tensor, kv_lens: torc
                      v_tensor: int = 0, stream=None):
     """The latent rows of every request multiplied out by weight [heads, 256, 512] into per-head keys (192) and
     values (128) of the caches k_out and v_out, at the same tokens of out_table."""
+    _tensor_numbers(tensor, k_tensor, v_tensor)
     code = _DTYPES.get(weight.dtype)
     if code is None or weight.dim() != 3 or tuple(weight.shape[1:]) != (256, LATENT_RANK) or not weight.is_contiguous():
         raise ValueError("weight must be a contiguous bf16 or fp16 [heads, 256, 512] CUDA tensor")
@@ -717,6 +730,8 @@ def _score_rows(dev: int, t: torch.Tensor, n: int, width: int, name: str):
     row, one = t.stride()
     if one != 1 and t.shape[1] > 1:
         raise ValueError(f"{name} must be row-major")
+    if t.shape[1] >= 2 ** 31:
+        raise ValueError(f"{name}'s columns must be a 32-bit number")
     return t.data_ptr(), row
 
 
@@ -726,6 +741,7 @@ def kv_attention_mass(q: torch.Tensor, cache: PagedCache, block_table: torch.Ten
                       width: Optional[int] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The attention weight every cached token receives from q, added to prev (float32 [n_reqs, width], or None);
     returns score [n_reqs, width].  width: prev's or score's columns, else a table row's slots."""
+    _tensor_numbers(k_tensor)
     code, q_token, q_head = _rows3(q, "q")
     dev = q.get_device()
     handle = _begin(dev, stream)

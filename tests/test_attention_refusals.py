@@ -150,3 +150,27 @@ def test_lengths_past_what_is_counted(lib):
                                 cache(row=wide * 256), 0, 0x3000, 1 << 20, 1 << 20, None) == UNSUPPORTED
     rows = cache(row=wide * 256)
     assert attention(lib, d=desc(heads=wide, kv_heads=wide), b=batch(n_reqs=n, pages=1 << 20), k=rows) == UNSUPPORTED
+
+
+def test_binding_refuses_tensor_numbers_past_32_bits():
+    """Tensor 2^32 of a cache would be taken for its first."""
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    for number in (2 ** 31, 2 ** 32, -2 ** 32 + 1):
+        for call in (lambda: K.kv_attention(q, None, None, None, None, 0.1, k_tensor=number),
+                     lambda: K.kv_attention(q, None, None, None, None, 0.1, v_tensor=number),
+                     lambda: K.kv_latent_attention(q, None, None, None, None, 0.1, tensor=number),
+                     lambda: K.kv_latent_expand(None, None, None, q, None, None, None, tensor=number),
+                     lambda: K.kv_latent_expand(None, None, None, q, None, None, None, k_tensor=number),
+                     lambda: K.kv_latent_expand(None, None, None, q, None, None, None, v_tensor=number),
+                     lambda: K.kv_attention_mass(q, None, None, None, None, None, 0.1, k_tensor=number)):
+            with pytest.raises(ValueError, match="32-bit"):
+                call()
+
+
+def test_binding_refuses_columns_past_32_bits():
+    table, score = (torch.empty(1, 2 ** 32 + 5, dtype=t, device="meta") for t in (torch.int32, torch.float32))
+    with pytest.raises(ValueError, match="32-bit"):
+        K._table(-1, table, 1, "block_table")
+    with pytest.raises(ValueError, match="32-bit"):
+        K._score_rows(-1, score, 1, 0, "score")
+    assert K._score_rows(-1, score[:, :7], 1, 5, "score")[1] == 2 ** 32 + 5
