@@ -517,7 +517,7 @@ int check_batch(const kv_attn_batch *t)
 int fill_batch(Batch *b, const kv_attn_batch *t, int heads, int kv_heads, int block_size, int unit_rows, int tile_shift, int causal, int window)
 {
     const int64_t max_tokens = (int64_t)t->max_blocks_per_req * block_size;
-    if (max_tokens > (1ll << 30) || t->n_tokens * (int64_t)heads > (1ll << 30)) return KV_ERR_UNSUPPORTED;
+    if (max_tokens > (1ll << 30) || t->n_tokens > (1ll << 30) / heads) return KV_ERR_UNSUPPORTED;
     b->q_offsets = t->q_offsets;
     b->kv_lens = t->kv_lens;
     b->n_reqs = t->n_reqs;

@@ -174,3 +174,11 @@ def test_binding_refuses_columns_past_32_bits():
     with pytest.raises(ValueError, match="32-bit"):
         K._score_rows(-1, score, 1, 0, "score")
     assert K._score_rows(-1, score[:, :7], 1, 5, "score")[1] == 2 ** 32 + 5
+
+
+def test_token_counts_whose_product_with_the_heads_passes_64_bits(lib):
+    """2^60 tokens of 16 heads would be taken for none."""
+    for tokens in (1 << 60, (1 << 61) + 1, (1 << 63) - 1):
+        assert attention(lib, d=desc(heads=16, kv_heads=2), b=batch(tokens=tokens)) == UNSUPPORTED
+        assert lib.kv_attention_mass(desc(heads=16), batch(tokens=tokens), cache(), 0, 0, 0x50000, 2048, 256, 0x7000, None, 0, 0x9000, 100, 100, 0x80000,
+                                     1 << 40, None) == UNSUPPORTED
