@@ -120,12 +120,13 @@ struct Line {
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (int)((uint32_t)(a + b - 1) / (uint32_t)b); }
 
-// A sum of steps, which stays at kTooLong once it gets there.  The hosts refuse batches whose steps would not fit 32 bits;
-// offsets that decrease name requests that overlap, and many of those may add up to more.
+// A thread's or warp's sum of steps, which stays at kTooLong once it gets there.  The hosts refuse batches whose steps
+// would not fit 32 bits; offsets that decrease name requests that overlap, and many of those may add up to more.
 constexpr int kTooLong = 0x7fffffff;
 __device__ __forceinline__ int add_steps(int a, int b) { return (int)min((uint32_t)a + (uint32_t)b, (uint32_t)kTooLong); }
 
-// Inclusive scan of `mine` over the block, and the sums of it and of `other`.  scratch: two words a warp.
+// Inclusive scan of `mine` over the block, and the sums of it and of `other`.  Where `mine` adds up to kTooLong or more, its sum
+// is kTooLong or that of `other` negative.  scratch: two words a warp.
 template <int Threads>
 __device__ __forceinline__ int block_scan(int mine, int other, int *scratch, int &total, int &other_total)
 {
@@ -140,12 +141,15 @@ __device__ __forceinline__ int block_scan(int mine, int other, int *scratch, int
     if (lane == 31) scratch[2 * warp] = upto, scratch[2 * warp + 1] = other;
     __syncthreads();
     total = other_total = 0;
+    int past = 0;
 #pragma unroll 1
     for (int w = 0; w < Threads / 32; w++) {
-        if (w == warp) upto = add_steps(upto, total);
-        total = add_steps(total, scratch[2 * w]);
+        if (w == warp) upto = (int)((uint32_t)upto + (uint32_t)total);
+        total = (int)((uint32_t)total + (uint32_t)scratch[2 * w]);
+        past |= total;
         other_total += scratch[2 * w + 1];
     }
+    other_total |= past & (int)0x80000000;
     return upto;
 }
 
@@ -173,7 +177,7 @@ __device__ __forceinline__ Line find_piece(int n_reqs, int part, int parts, int 
 #pragma unroll 1
     for (int r = r0; r < r1; r++) work.measure(r, mine, units);
     int at = block_scan<Threads>(mine, units, scratch, total, unit_total);
-    if (total == kTooLong) total = 0, unit_total = 1 << 30;
+    if (total == kTooLong || unit_total < 0) total = 0, unit_total = 1 << 30;
     const int used = max(1, min(parts, total));
     Line line;
     line.part = part;
