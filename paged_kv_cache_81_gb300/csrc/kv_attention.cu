@@ -329,7 +329,7 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                         tc_wait_ld();
                         top = max32(x1, top);
                     }
-                    const bool grow = top > __fadd_rd(m, slack);  // -inf + slack: the first finite score
+                    const bool grow = top > (Bf16 ? m + slack : __fadd_rd(m, slack));  // -inf + slack: the first finite score
                     if (__any_sync(0xffffffffu, grow)) {
                         const float to_m = grow ? top : m;
                         const float alpha = grow ? exp2_fast((m - to_m) * p.o.c) : 1.0f;

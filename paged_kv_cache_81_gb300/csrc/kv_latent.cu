@@ -249,7 +249,7 @@ latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ C
                         hide32(x[1], lo - kb - 32, hi - kb - 32);
                     }
                     const float top = max32(x[1], max32(x[0], -INFINITY));
-                    const bool grow = top > __fadd_rd(m, slack);
+                    const bool grow = top > (Bf16 ? m + slack : __fadd_rd(m, slack));
                     if (__any_sync(0xffffffffu, grow)) {
                         const float to_m = grow ? top : m;
                         const float alpha = grow ? exp2_fast((m - to_m) * p.o.c) : 1.0f;

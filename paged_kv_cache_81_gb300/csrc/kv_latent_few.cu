@@ -189,7 +189,7 @@ latent_few_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant
                     if (__any_sync(0xffffffffu, kb < lo || kb + kKeys > hi)) hide32(v, lo - kb, hi - kb);
                     // the upper lanes hold no scores; they follow the row's maximum for their half of O
                     const float top = __shfl_sync(0xffffffffu, max32(v, -INFINITY), lane & 15);
-                    const bool grow = top > __fadd_rd(m, slack);
+                    const bool grow = top > (Bf16 ? m + slack : __fadd_rd(m, slack));
                     any = __any_sync(0xffffffffu, grow);
                     if (any) {
                         const float to_m = grow ? top : m;
