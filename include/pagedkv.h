@@ -404,8 +404,8 @@ enum { KV_BF16 = 0, KV_F16 = 1 };
  * holds kv_lens[r] tokens, the new ones last: new token i of request r stands at position
  * kv_lens[r] - q_len + i, and token j of the cache is slot j % block_size of page
  * block_table[r * bt_row_stride + j / block_size].  The lengths are read on the device, so a captured
- * graph follows them.  n_tokens is the capacity of q in tokens; rows at and past q_offsets[n_reqs] are
- * not read and their outputs not written.  A request may have no new tokens, or no cached ones.
+ * graph follows them.  n_tokens is the capacity of q in tokens; rows at and past q_offsets[n_reqs] may be read (tokens
+ * come several at a time) and may hold anything, and their outputs are not written.  A request may have no new tokens, or no cached ones.
  */
 typedef struct {
     const int32_t *block_table; /* [n_reqs, max_blocks_per_req], row stride bt_row_stride (elements) */
@@ -451,7 +451,8 @@ KV_API int kv_attention_workspace_bytes(int64_t *bytes_out);
  * block sizes are equal).  q: [n_tokens, n_heads, head_dim] and out: [n_tokens, n_heads, head_dim_v] with
  * byte strides of tokens and heads.  lse (float [n_tokens, n_heads], may be NULL): the natural logarithm
  * of the sum of the exponentials.  A row that sees nothing gets out 0 and lse -inf.  Products and sums are
- * held in 32 bits; the weights p are rounded to the element type before they multiply the values.
+ * held in 32 bits; the weights p are rounded to the element type before they multiply the values (fp16: what is
+ * below 2^-32 of a row's largest is lost).  scale q . K should stay below 2^24 in size, where its steps are of one.
  * Slots at and past kv_lens[r], and before every window, are not used whatever they hold; the
  * tokens a request does hold must be finite.
  *  - q_offsets that decrease or leave [0, n_tokens] are clamped and set KV_DERR_LIST (requests that then overlap
@@ -529,7 +530,7 @@ KV_API int kv_attention_mass(const kv_attn_desc *d, const kv_attn_batch *batch, 
  * new_lens[r]; out_score (may be NULL) float [n_reqs, budget], the kept tokens' scores, 0 past them.
  *  - out_table == block_table (the same pointer): in place; the pages past new_lens[r] are then free.  The
  *    pages of a request must then belong to it alone.  Otherwise the pages out_table lists must not be
- *    among those block_table lists; shared prefix pages stay as they are.
+ *    among those block_table lists, nor listed twice; shared prefix pages stay as they are.
  *  - score has `width` columns; tokens at and past them (written since the scores were taken) count as 0.
  *  - new_lens may be kv_lens itself, and out_score score itself (row strides equal).  Only budget columns of
  *    out_score are written: a caller that adds the next weights to the same buffer clears the others first.

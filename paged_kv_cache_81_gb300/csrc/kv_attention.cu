@@ -19,10 +19,12 @@
 // the tensor core and the exponentials.
 //
 // Decoding is bound by memory: 64 requests of 4096 to 12288 tokens, 32 heads over 8 of 128, take 322 to
-// 331 us, 97% of the copy rate or more.  Chunks are bound by shared memory, which moves 128 bytes a cycle: a
-// step of 256 rows by 128 keys reads operands for 1024 of its cycles, and its exponentials take 512 beside them
-// (four chunks of 2048 to 4096 tokens over 4096 to 8192: 681 to 694 us, 1.3 PFLOP/s, two thirds of the tensor cores'
-// measured rate).
+// 331 us, 97% of the copy rate or more.  Chunks (four of 2048 to 4096 tokens over 4096 to 8192: 670 to 705 us, 1.3
+// PFLOP/s, two thirds of the tensor cores' measured rate) fill no unit of the SM.  A step of 256 rows by 128 keys takes
+// about 3600 cycles, and needs 2048 of the tensor core, 1536 of shared memory for its operands and 512 of the
+// exponentials.  What bounds it is the order within a group: scores, their maximum, all 128 weights of every row, the value
+// product, and only then the next scores; two groups do not hide each other's waits.  With keys of 192 a step takes
+// about 5900 cycles, 2560 of them tensor work: there one stage of values and two of keys is all that fits.
 #include <cmath>
 
 #include "kv_attention.cuh"

@@ -10,8 +10,8 @@
 // of (above, equal) counts.  evict_move_kernel, bound by memory: a CTA walks a stretch of the list for a
 // (request, tensor, plane) in chunks of 32 KB, all loads of a chunk before its stores.  In place, slot i
 // receives a row of slot >= i, so chunks in order never overwrite a row that is still to be read.  16 requests
-// of 4000 to 16000 tokens trimmed to 2048 in 32 tensors of 8 x 128 take 673 us, 94% of the copy rate; four short
-// ones in two tensors 9.9 us, most of it the two launches' latencies.
+// of 4000 to 16000 tokens trimmed to 2048 in 32 tensors of 8 x 128 take 673 us, 94% of the copy rate (851 in
+// place, where one CTA walks a whole list); four short ones in two tensors 9.9 us, most of it the two launches' latencies.
 #include <algorithm>
 
 #include "kv_attention.cuh"

@@ -13,9 +13,11 @@
 //   warps 0 and 2 load the two kinds of panels, warp 3 loads Q, warp 1 issues the products, warps 4-7 hold
 //   a row a thread (maximum, exponentials, P over S, lazy rescaling as in kv_attention.cu).  S of the next
 //   tile is formed before O += P V of this one, so the tensor core works while the exponentials run.
-// A tile of 64 keys takes about 2050 cycles of shared memory's rate for the products' operands, which is what
-// bounds it: 64 requests of 4096 to 12288 tokens, 128 heads, take 187 us, half of the rate at which memory
-// could bring the rows (each is read once, by both CTAs of a pair, the second time from the L2).
+// 64 requests of 4096 to 12288 tokens, 128 heads, take 183 to 188 us, half of the rate at which memory could bring the rows
+// (each is read once, by both CTAs of a pair, the second time from the L2).  A tile of 64 keys takes about 3300 cycles, and
+// needs 1664 of the tensor core and about 2050 of shared memory for the products' operands and the loads.  What bounds it
+// is a trip to memory a tile: two tiles stand at a time, and a tile's value panels are free only behind its value
+// product, while the scores of the next but one wait for them.
 #include "kv_latent.cuh"
 
 namespace pkv {
@@ -387,7 +389,8 @@ extern "C" int kv_latent_attention(const kv_attn_desc *d, const kv_attn_batch *b
     // 26.1, 60.7 against 16.7, 26.7, 53.1 with 19; 27.8, 73.6, 234.9 against 23.6, 57.3, 165.4 with 100.  Of 64 heads
     // 19.6, 41.5, 95.0 against 25.8, 49.3, 90.1 with 32 requests; 29.6, 63.9, 189.4 against 39.8, 66.7, 146.2 with
     // 76; 31.9, 80.0, 242.6 against 33.6, 72.0, 180.8 with 100.  With few requests the join of a unit's pieces, by one
-    // CTA there, decides.
+    // CTA there, decides.  The host knows neither the lengths nor which of them a captured graph will meet: with 64 heads the
+    // rule costs short contexts up to 10 us and brings long ones up to 62.
     // (Its tiles are half as long: the last condition keeps a batch of any capacity that the other takes.)
     const int64_t reqs = batch->n_reqs, few_rows = reqs < kLatentFewRows ? reqs : kLatentFewRows;
     const bool few = d->n_heads <= kLatentFewRows && batch->n_tokens <= few_rows * reqs / d->n_heads && reqs * 8 >= dev->num_sms &&

@@ -13,9 +13,9 @@
 //   the products), warps 4-7 and 8-11 take the even and the odd steps.  Warp 2 ends with what lies past
 //   the requests' lengths.
 // A decode step is bound by memory once there is enough of it: 128 requests of 6000 to 8000 tokens, 32 heads over 8,
-// take 296 us, 92% of the copy rate (16 of 2000 to 6000: 34 us, 61%).  Chunks are bound by a step's 512 cycles of
+// take 293 us, 93% of the copy rate (16 of 2000 to 6000: 32 us, 65%).  Chunks are bound by a step's 512 cycles of
 // exponentials and 768 of shared memory (operands and the normalisers that every thread reads): four of 512 to 1024
-// tokens over 4000 to 8000 take 136 us.
+// tokens over 4000 to 8000 take 134 us.
 #include "kv_attention.cuh"
 
 namespace pkv {

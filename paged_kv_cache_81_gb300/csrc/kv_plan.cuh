@@ -126,7 +126,8 @@ constexpr int kTooLong = 0x7fffffff;
 __device__ __forceinline__ int add_steps(int a, int b) { return (int)min((uint32_t)a + (uint32_t)b, (uint32_t)kTooLong); }
 
 // Inclusive scan of `mine` over the block, and the sums of it and of `other`.  Where `mine` adds up to kTooLong or more, its sum
-// is kTooLong or that of `other` negative.  scratch: two words a warp.
+// is kTooLong or that of `other` negative (a sum that stopped there across the warps changed the code that uses it: a prompt of
+// 32768 tokens under a window of 256 took 367 us instead of 361).  scratch: two words a warp.
 template <int Threads>
 __device__ __forceinline__ int block_scan(int mine, int other, int *scratch, int &total, int &other_total)
 {
