@@ -11,8 +11,8 @@
 //   warp 1        issues every tcgen05.mma: S = Q K^T and O += P V, accumulators in TMEM
 //   warps 4-7, 8-11   two softmax groups, a thread per row: S from TMEM, maximum, exponentials, P back to
 //                 TMEM (over S) as the A operand of the second product, O rescaled only when the
-//                 maximum has grown by more than 2^8 (P stays below 2^8, far inside 16-bit range, so
-//                 most tiles touch O not at all)
+//                 maximum has grown by more than 2^8 (P stays below 2^8, in fp16 2^7 times that, inside
+//                 16-bit range, so most tiles touch O not at all)
 // TMEM: S0, S1 (128 columns each) and O0, O1 (128 columns each).  With more than 128 rows the two groups
 // own 128 rows each and share every K and V tile; with fewer (decoding) they take the even and the odd
 // key tiles of the same rows and are joined through TMEM, so both ways keep two tiles in flight between
