@@ -546,6 +546,114 @@ KV_API int kv_evict(const kv_cache_desc *cache, const int32_t *block_table, int3
                     int64_t out_score_stride, kv_stream_t stream);
 
 /*
+ * Rotary positions.  Pair i of a head, elements (rot_offset + i, rot_offset + i + rot_dim / 2) or, interleaved,
+ * (rot_offset + 2 i, rot_offset + 2 i + 1), becomes
+ *     (a, b) -> magnitude * (a cos t - b sin t, a sin t + b cos t),   t = 2 pi * position * turns[i] / 2^64,
+ * the other elements stay.  Frequencies are fractions of a turn a position, 2^64 to the turn, so whole turns drop out of the
+ * integer product and the angle of any 32-bit position (negative ones too) is exact before its cosine is taken.
+ * rot_dim: a multiple of 16 (interleaved: of 8), at most 512 (0: nothing rotates); rot_offset: a multiple of 8.
+ */
+typedef struct {
+    const uint64_t *turns; /* device [rot_dim / 2], 8-byte aligned */
+    int32_t rot_dim;
+    int32_t rot_offset;
+    int32_t interleaved;
+    float magnitude;
+} kv_rope;
+
+/*
+ * How kv_rope_frequencies scales the frequencies w_i = base^(-2 i / rot_dim) (radians a position) for contexts `factor` times
+ * as long as original_length:
+ *   KV_ROPE_LINEAR  w_i / factor (positions interpolated)
+ *   KV_ROPE_BASE    base times factor^(rot_dim / (rot_dim - 2)): the slowest pair slows down by factor, the fastest not
+ *   KV_ROPE_BANDS   pairs that turn `fast` times or more over original_length stay, those that turn `slow` times or fewer
+ *                   are divided by factor, between them both are mixed in proportion to the turns
+ *   KV_ROPE_YARN    the same with the mix in proportion to the pair's number, between the (whole) numbers at which a pair
+ *                   turns `fast` and `slow` times, and magnitude 0.1 ln(factor) + 1 (Peng et al. 2023, "YaRN")
+ */
+enum { KV_ROPE_PLAIN = 0, KV_ROPE_LINEAR = 1, KV_ROPE_BASE = 2, KV_ROPE_BANDS = 3, KV_ROPE_YARN = 4 };
+typedef struct {
+    int32_t kind;
+    double factor;
+    double original_length; /* BANDS, YARN: tokens */
+    double fast, slow;      /* BANDS, YARN: turns, fast > slow > 0 */
+} kv_rope_scaling;
+
+/* The frequencies as kv_rope takes them, into HOST memory (rot_dim / 2 numbers), and the magnitude (may be NULL).
+ * scaling may be NULL (KV_ROPE_PLAIN).  rot_dim even, base > 1. */
+KV_API int kv_rope_frequencies(int32_t rot_dim, double base, const kv_rope_scaling *scaling, uint64_t *turns_out, float *magnitude_out);
+
+/*
+ * kv_rotate: rows x [n_tokens, n_heads, head_dim] of `dtype` rotated by token_pos (device int32 [n_tokens]) into out, whose
+ * elements that do not rotate are x's.  inverse: by the negative angle, which with the same magnitude is the transposed
+ * map: the gradient of x from that of out.  Products and sums in 32 bits, one rounding.  head_dim a multiple of 8;
+ * byte strides and addresses multiples of 16; out may be x itself (same strides), else they must not overlap.
+ */
+KV_API int kv_rotate(int32_t dtype, int32_t n_heads, int32_t head_dim, const void *x, int64_t token_stride, int64_t head_stride, void *out,
+                     int64_t out_token_stride, int64_t out_head_stride, int64_t n_tokens, const int32_t *token_pos, const kv_rope *rope,
+                     int32_t inverse, kv_stream_t stream);
+
+/*
+ * One layer's new tokens for the rotating writes.  q [n_tokens, n_heads, head_dim] (n_heads 0: none) goes rotated to q_out, which
+ * may be q itself; k [n_tokens, n_kv_heads, head_dim] goes rotated, v [n_tokens, n_kv_heads, head_dim_v] (head_dim_v 0: none, as
+ * for latent rows) as it is to the cache.  Byte strides and addresses are multiples of 16, so the three may be parts of one
+ * projection's rows.  Token i belongs to position token_pos[i] of request token_req[i], whose slot the block table gives as for
+ * kv_slot_mapping; it is rotated by rope_pos[i] (NULL: token_pos[i]; they differ once kv_evict has moved tokens).
+ */
+typedef struct {
+    int32_t dtype; /* KV_BF16 or KV_F16 */
+    int32_t n_heads;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int32_t head_dim_v;
+    const void *q;
+    int64_t q_token_stride, q_head_stride;
+    void *q_out;
+    int64_t q_out_token_stride, q_out_head_stride;
+    const void *k;
+    int64_t k_token_stride, k_head_stride;
+    const void *v;
+    int64_t v_token_stride, v_head_stride;
+    const int32_t *token_req, *token_pos, *rope_pos; /* device [n_tokens] */
+    int64_t n_tokens;
+    const int32_t *block_table; /* device [n_reqs, max_blocks_per_req], row stride bt_row_stride (elements) */
+    int32_t n_reqs;
+    int32_t max_blocks_per_req;
+    int64_t bt_row_stride;
+} kv_new_tokens;
+
+/*
+ * kv_rotate_write [S "batch tensor 组装", "Paged kv cache"]: kv_rotate of the queries and keys and kv_write_tokens of the keys and
+ * values, in one launch: keys to plane k_plane of tensor k_tensor of *k (rows of n_kv_heads * head_dim elements), values likewise
+ * of *v (may be the same descriptor; ignored when head_dim_v is 0).  rope NULL: nothing rotates.  An invalid token (as for
+ * kv_write_tokens) sets KV_DERR_TABLE, a page outside either cache KV_DERR_SLOT: neither its key nor its value is written; its query is
+ * rotated all the same.  Two tokens with one slot race.  Limit: n_tokens < 2^31.
+ */
+KV_API int kv_rotate_write(const kv_new_tokens *tokens, const kv_rope *rope, const kv_cache_desc *k, int32_t k_tensor, int32_t k_plane,
+                           const kv_cache_desc *v, int32_t v_tensor, int32_t v_plane, kv_stream_t stream);
+
+/*
+ * A 4-bit cache holds a token's heads in groups of 16 elements with a scale each: element = code * scale * tensor scale, codes
+ * e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and, with the highest bit, their negatives), scales e4m3.  A row is n_heads * head_dim / 2
+ * bytes of codes (element 2 i of the row in the low half of byte i), then n_heads * head_dim / 16 bytes of scales, filled up to a multiple
+ * of 16: kv_q4_row_bytes.  To every call that moves rows (pack, unpack, evict, write) such a row is a row like any other; heads
+ * are sliced in two parts, codes and scales.  head_dim: a multiple of 32, at most 128.
+ */
+KV_API int kv_q4_row_bytes(int32_t heads, int32_t head_dim, int32_t *bytes_out);
+
+/*
+ * kv_rotate_write_q4: kv_rotate_write into a 4-bit cache.  A group's elements x, rounded to the element type after the rotation, become
+ *     y = x * (1 / tensor scale),   scale = max|y| / 6 rounded to e4m3 (at most 448, at least 2^-9),   code = y / scale rounded,
+ * both to nearest, ties to even, in 32 bits; what exceeds 6 * scale becomes +-6.  The keys' rotation is exact to the
+ * rounding (2^-37 before it), so codes follow from the values alone.  k_scale, v_scale: the tensors' scales, in [1e-30, 1e30].
+ * k_held, v_held (NULL, or contiguous [n_tokens, n_kv_heads, dim], 16-byte aligned): the values the cache now stands for, in the
+ * element type.  Elements must be finite.  n_kv_heads * head_dim <= 16384 and values are required (KV_ERR_UNSUPPORTED).
+ */
+KV_API int kv_rotate_write_q4(const kv_new_tokens *tokens, const kv_rope *rope, const kv_cache_desc *k, int32_t k_tensor, int32_t k_plane,
+                              const kv_cache_desc *v, int32_t v_tensor, int32_t v_plane, float k_scale, float v_scale, void *k_held, void *v_held,
+                              kv_stream_t stream);
+
+/*
  * kv_get_last_error: copies the current device's sticky error word (KV_DERR_* bits) to
  * *host_out after the work queued on `stream` so far, clears it when clear != 0, and
  * SYNCHRONISES `stream`.  Work on other streams is not waited for.

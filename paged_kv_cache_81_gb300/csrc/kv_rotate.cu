@@ -1,0 +1,570 @@
+// kv_rotate, kv_rotate_write, kv_rotate_write_q4: heads rotated by their tokens' positions, and the new tokens' keys and values
+// appended to the pages with the rotation (and the rounding to 4 bits) on the way.
+//
+// A pair (a, b) of a head becomes m (a cos t - b sin t, a sin t + b cos t), t = position * frequency.  Frequencies are 64-bit
+// fractions of a turn, so position * frequency is an integer product whose overflow drops whole turns: the angle of position
+// 2^31 is as good as that of position 1 (in 32-bit floating point t is off by 0.06 at a million).
+//
+// 4-bit codes must not depend on how the angle was rounded: a border between two codes is 2^-5 of a value wide in steps of
+// bf16, so one in 2^20 elements would come out otherwise than from exact angles.  Cosines and sines are therefore held in two
+// floats (what is left is below 2^-37), the products keep what their rounding leaves (Dekker; Knuth's sum), and the result is rounded
+// once to 32 bits and once to the element type, as a 16-bit cache would hold it, before it is rounded to 4 bits.
+//
+// One CTA a token: its cosines and sines are formed once, into shared memory, and serve every head.
+#include <cmath>
+
+#include "kv_attention.cuh"
+#include "kv_q4.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxRot = 512;             // rotated elements of a head
+constexpr int kMaxQ4Keys = 16384;        // elements of a token's keys that pass through shared memory
+
+// ---------------------------------------------------------------------------
+// Cosine and sine of 256 angles a turn in two floats each, from their Taylor series in 64 bits at compile time.
+// ---------------------------------------------------------------------------
+constexpr double kPi = 3.14159265358979323846;
+
+constexpr double series(double x, bool sine)  // |x| <= pi / 4
+{
+    double term = sine ? x : 1.0, sum = 0.0;
+    for (int n = sine ? 1 : 0; n < 26; n += 2) {
+        sum += term;
+        term *= -x * x / ((n + 1) * (n + 2));
+    }
+    return sum;
+}
+
+constexpr double turn256(int i, bool sine)
+{
+    // quarter turns and a remainder of at most an eighth of a turn
+    const int q = ((i + 32) >> 6) & 3, r = ((i + 32) & 63) - 32;
+    const double x = r * (kPi / 128), c = series(x, false), s = series(x, true);
+    const double co = q == 0 ? c : q == 1 ? -s : q == 2 ? -c : s, si = q == 0 ? s : q == 1 ? c : q == 2 ? -s : -c;
+    return sine ? si : co;
+}
+
+struct Turns {
+    float v[256][4];  // cosine, sine, what their rounding leaves
+    constexpr Turns() : v()
+    {
+        for (int i = 0; i < 256; i++) {
+            const double c = turn256(i, false), s = turn256(i, true);
+            v[i][0] = (float)c;
+            v[i][1] = (float)s;
+            v[i][2] = (float)(c - (double)(float)c);
+            v[i][3] = (float)(s - (double)(float)s);
+        }
+    }
+};
+
+__device__ const __align__(16) Turns g_turns = Turns();
+
+struct Angle {
+    float c, s, cl, sl;  // cosine, sine; what their rounding leaves
+};
+
+// x + y and what its rounding leaves (Knuth).
+__device__ __forceinline__ float sum2(float x, float y, float &left)
+{
+    const float s = __fadd_rn(x, y), t = __fadd_rn(s, -x);
+    left = __fadd_rn(__fadd_rn(x, -__fadd_rn(s, -t)), __fadd_rn(y, -t));
+    return s;
+}
+
+// m cos, m sin of `u` 2^-64 turns: the nearest of 256 table angles and a rest of at most pi / 256, whose sine and cosine
+// take two terms more than themselves.
+__device__ __forceinline__ Angle angle_of(uint64_t u, float m)
+{
+    const uint64_t r = u + (1ull << 55);
+    const int64_t d = (int64_t)(r & ((1ull << 56) - 1)) - (1ll << 55);
+    const float4 t = __ldg(reinterpret_cast<const float4 *>(g_turns.v[r >> 56]));
+    // the rest in radians: the upper 24 bits of d are exact in 32-bit floating point
+    constexpr double kHi = 2 * kPi / 4294967296.0;
+    constexpr float k1 = (float)kHi, k1l = (float)(kHi - (double)k1), k2 = (float)(kHi / 4294967296.0);
+    const float a = (float)(int32_t)(d >> 32), b = (float)(uint32_t)d;
+    float x = __fmul_rn(a, k1), xl = fmaf(a, k1l, fmaf(a, k1, -x));
+    xl = fmaf(b, k2, xl);
+    const float x0 = x;
+    x = __fadd_rn(x0, xl);
+    xl = __fadd_rn(xl, -__fadd_rn(x, -x0));
+    const float x2 = __fmul_rn(x, x);
+    const float sl = fmaf(__fmul_rn(x, x2), fmaf(x2, 1.0f / 120, -1.0f / 6), xl);            // sine: x + sl
+    const float ch = -0.5f * x2;                                                             // cosine: 1 + ch + cl
+    const float cl = fmaf(__fmul_rn(x2, x2), 1.0f / 24, fmaf(-x, xl, -0.5f * fmaf(x, x, -x2)));
+    Angle o;
+    // cosine t.x (1 + ch) - t.y x and sine t.y (1 + ch) + t.x x, the large products with what their rounding leaves
+    float e, p = __fmul_rn(t.y, x), pe = fmaf(t.y, x, -p), s = sum2(t.x, -p, e);
+    float lo = fmaf(t.x, ch, fmaf(t.x, cl, fmaf(-t.y, sl, fmaf(-t.w, x, fmaf(t.z, ch, t.z + (e - pe))))));
+    o.c = __fadd_rn(s, lo);
+    o.cl = __fadd_rn(lo, -__fadd_rn(o.c, -s));
+    p = __fmul_rn(t.x, x), pe = fmaf(t.x, x, -p), s = sum2(t.y, p, e);
+    lo = fmaf(t.y, ch, fmaf(t.y, cl, fmaf(t.x, sl, fmaf(t.z, x, fmaf(t.w, ch, t.w + (e + pe))))));
+    o.s = __fadd_rn(s, lo);
+    o.sl = __fadd_rn(lo, -__fadd_rn(o.s, -s));
+    if (m != 1.0f) {
+        const float c = __fmul_rn(o.c, m), si = __fmul_rn(o.s, m);
+        o.cl = fmaf(o.cl, m, fmaf(o.c, m, -c));
+        o.sl = fmaf(o.sl, m, fmaf(o.s, m, -si));
+        o.c = c, o.s = si;
+    }
+    return o;
+}
+
+// a c - b s of two-float c and s, rounded once.
+__device__ __forceinline__ float turned(float a, float b, float c, float s, float cl, float sl)
+{
+    const float p = __fmul_rn(a, c), q = __fmul_rn(b, s);
+    float e;
+    const float d = sum2(p, -q, e);
+    return __fadd_rn(d, e + ((fmaf(a, c, -p) - fmaf(b, s, -q)) + fmaf(a, cl, -b * sl)));
+}
+
+// One set of heads: [tokens, heads, dim] rows with byte strides.
+struct Rows {
+    const char *in;
+    char *out;
+    int64_t in_token, in_head, out_token, out_head;
+};
+
+// A plane of the cache that takes new rows.
+struct Plane {
+    char *base;
+    int64_t block_stride, token_stride;
+    int32_t num_blocks;
+};
+
+struct Params {
+    Rows q, k, v;  // k.out, v.out: the held values of a 4-bit write, may be null
+    Plane kp, vp;
+    const int32_t *token_req, *token_pos, *rope_pos;
+    const int32_t *table;
+    int64_t table_stride;
+    const uint64_t *turns;
+    int32_t n_reqs, max_blocks;
+    int32_t heads, kv_heads, dk, dv;
+    int32_t half, offset;  // pairs of a head, its first rotated element
+    float magnitude;
+    int32_t inverse;
+    FastDiv block;
+    FastDiv turn_items;   // items that rotate of a head: 8 pairs each
+    FastDiv plain_items;  // 16-byte pieces of a head that do not
+    FastDiv v_items;
+    FastDiv k_groups, v_groups;  // groups of 16 of a head
+    float k_scale, v_scale, k_inv, v_inv;
+    int *err;
+};
+
+template <bool Bf16>
+__device__ __forceinline__ float2 unpack2(uint32_t v)
+{
+    if (Bf16) return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+    float2 f;
+    asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(f.x), "=f"(f.y) : "r"(v));
+    return f;
+}
+
+// A group of 16 elements to 4 bits: its codes, its scale, and (held) the values they stand for.
+template <bool Bf16>
+__device__ __forceinline__ void quantise(const uint4 (&in)[2], float inv, float scale, char *codes, char *unit, char *held)
+{
+    const uint32_t w[8] = {in[0].x, in[0].y, in[0].z, in[0].w, in[1].x, in[1].y, in[1].z, in[1].w};
+    float y[16], most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const float2 f = unpack2<Bf16>(w[i]);
+        y[2 * i] = __fmul_rn(f.x, inv), y[2 * i + 1] = __fmul_rn(f.y, inv);
+        most = fmaxf(most, fmaxf(fabsf(y[2 * i]), fabsf(y[2 * i + 1])));
+    }
+    const uint32_t b = q4_scale_of(most);
+    const uint32_t ss = e4m3x2_to_f16(b * 0x101u);
+    const float s = unpack2<false>(ss).x;
+    if (most > 6.0f * s * 2) {  // far outside: the largest code, also for infinities
+#pragma unroll
+        for (int i = 0; i < 16; i++) y[i] = fminf(fmaxf(y[i], -12.0f * s), 12.0f * s);
+    }
+    // y / s: a quotient that is exact where it can be decides the ties.  One step on the product with the reciprocal gives the
+    // rounded quotient (Markstein 1990); with these signs it keeps that of a zero.
+    const float r = __frcp_rn(s);
+    uint32_t c[2];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        float z[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const float z0 = __fmul_rn(y[8 * h + i], r);
+            z[i] = fmaf(fmaf(z0, s, -y[8 * h + i]), -r, z0);
+        }
+        c[h] = f32_to_q4(z);
+    }
+    if (codes != nullptr) {
+        *reinterpret_cast<uint2 *>(codes) = make_uint2(c[0], c[1]);
+        *unit = (char)b;
+    }
+    if (held != nullptr) {
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            uint32_t v[4], o[4];
+            q4_to_f16(c[h], v);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float2 f = unpack2<false>(mul_f16x2(v[i], ss));
+                o[i] = pack2<Bf16>(__fmul_rn(f.x, scale), __fmul_rn(f.y, scale));
+            }
+            reinterpret_cast<uint4 *>(held)[h] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+}
+
+template <bool Bf16, bool Interleaved, bool Q4>
+__global__ void __launch_bounds__(kThreads) rotate_kernel(const Params p)
+{
+    __shared__ __align__(16) Angle angles[kMaxRot / 2];
+    __shared__ int place[2];  // page and slot of the token, page -1: it has none
+    extern __shared__ __align__(16) char keys[];
+    const int tid = threadIdx.x;
+    const int64_t tok = blockIdx.x;
+    grid_dep_entry();
+    const int32_t pos = __ldg(p.rope_pos + tok);
+    for (int i = tid; i < p.half; i += kThreads) {
+        Angle a = angle_of((uint64_t)(int64_t)pos * __ldg(p.turns + i), p.magnitude);
+        if (p.inverse) a.s = -a.s, a.sl = -a.sl;
+        angles[i] = a;
+    }
+    if (tid == kThreads - 1 && p.kv_heads) {
+        const int32_t req = __ldg(p.token_req + tok), at = __ldg(p.token_pos + tok);
+        int page = -1, slot = 0;
+        if (req >= 0 && req < p.n_reqs && at >= 0) {
+            const uint32_t col = fdiv((uint32_t)at, p.block);
+            if (col < (uint32_t)p.max_blocks) {
+                page = __ldg(p.table + (int64_t)req * p.table_stride + col);
+                slot = (int)((uint32_t)at - col * p.block.d);
+            }
+        }
+        if (page < 0)
+            set_error(p.err, KV_DERR_TABLE), page = -1;
+        else if (page >= p.kp.num_blocks || (p.dv && page >= p.vp.num_blocks))
+            set_error(p.err, KV_DERR_SLOT), page = -1;
+        place[0] = page, place[1] = slot;
+    }
+    __syncthreads();
+    const int page = p.kv_heads ? place[0] : -1;
+    char *const k_row = p.kp.base + (int64_t)page * p.kp.block_stride + (int64_t)place[1] * p.kp.token_stride;
+    char *const v_row = p.vp.base + (int64_t)page * p.vp.block_stride + (int64_t)place[1] * p.vp.token_stride;
+    // where head h of the queries and, after them, the keys is read and written; false where it is not written
+    const auto head_of = [&](int h, const char *&from, char *&to) {
+        if (h < p.heads) {
+            from = p.q.in + tok * p.q.in_token + h * p.q.in_head;
+            to = p.q.out + tok * p.q.out_token + h * p.q.out_head;
+            return true;
+        }
+        h -= p.heads;
+        from = p.k.in + tok * p.k.in_token + h * p.k.in_head;
+        to = (Q4 ? keys : k_row) + (int64_t)h * p.dk * 2;
+        return Q4 || page >= 0;
+    };
+    const int all = p.heads + p.kv_heads;
+    for (int i = tid; i < all * (int)p.turn_items.d && p.half; i += kThreads) {
+        const int h = (int)fdiv((uint32_t)i, p.turn_items), n = i - h * (int)p.turn_items.d;
+        const char *from;
+        char *to;
+        if (!head_of(h, from, to)) continue;
+        const Angle *a = angles + n * (Interleaved ? 4 : 8);
+        const int at0 = (p.offset + n * 8) * 2, at1 = at0 + (Interleaved ? 0 : p.half * 2);
+        const uint4 x = *reinterpret_cast<const uint4 *>(from + at0), y = Interleaved ? x : *reinterpret_cast<const uint4 *>(from + at1);
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+        const bool exact = Q4 && h >= p.heads;
+        const auto turn = [&](float u, float v, const Angle &g, float &nu, float &nv) {
+            if (exact) {
+                nu = turned(u, v, g.c, g.s, g.cl, g.sl);
+                nv = turned(u, -v, g.s, g.c, g.sl, g.cl);
+            } else {
+                nu = fmaf(u, g.c, -v * g.s);
+                nv = fmaf(u, g.s, v * g.c);
+            }
+        };
+        uint32_t ox[4], oy[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const float2 u = unpack2<Bf16>(xs[j]), v = unpack2<Bf16>(ys[j]);
+            if (Interleaved) {
+                float n0, n1;
+                turn(u.x, u.y, a[j], n0, n1);
+                ox[j] = pack2<Bf16>(n0, n1);
+            } else {
+                float a0, a1, b0, b1;
+                turn(u.x, v.x, a[2 * j], a0, b0);
+                turn(u.y, v.y, a[2 * j + 1], a1, b1);
+                ox[j] = pack2<Bf16>(a0, a1);
+                oy[j] = pack2<Bf16>(b0, b1);
+            }
+        }
+        *reinterpret_cast<uint4 *>(to + at0) = make_uint4(ox[0], ox[1], ox[2], ox[3]);
+        if (!Interleaved) *reinterpret_cast<uint4 *>(to + at1) = make_uint4(oy[0], oy[1], oy[2], oy[3]);
+    }
+    for (int i = tid; i < all * (int)p.plain_items.d && p.half * 2 < p.dk; i += kThreads) {
+        const int h = (int)fdiv((uint32_t)i, p.plain_items);
+        int at = (i - h * (int)p.plain_items.d) * 8;
+        if (at >= p.offset) at += p.half * 2;
+        const char *from;
+        char *to;
+        if (!head_of(h, from, to) || from == to) continue;
+        *reinterpret_cast<uint4 *>(to + at * 2) = *reinterpret_cast<const uint4 *>(from + at * 2);
+    }
+    if (!Q4) {
+        if (page < 0) return;
+        for (int i = tid; i < p.kv_heads * (int)p.v_items.d && p.dv; i += kThreads) {
+            const int h = (int)fdiv((uint32_t)i, p.v_items), at = (i - h * (int)p.v_items.d) * 8;
+            *reinterpret_cast<uint4 *>(v_row + ((int64_t)h * p.dv + at) * 2) =
+                *reinterpret_cast<const uint4 *>(p.v.in + tok * p.v.in_token + h * p.v.in_head + at * 2);
+        }
+        return;
+    }
+    __syncthreads();
+    const int k_count = p.kv_heads * (int)p.k_groups.d, v_count = p.kv_heads * (int)p.v_groups.d;
+    for (int i = tid; i < k_count + v_count; i += kThreads) {
+        const bool key = i < k_count;
+        const int g = key ? i : i - k_count, dim = key ? p.dk : p.dv;
+        const int h = (int)fdiv((uint32_t)g, key ? p.k_groups : p.v_groups), at = g * 16 - h * dim;
+        const Rows &rows = key ? p.k : p.v;
+        const char *from = key ? keys + g * 32 : p.v.in + tok * p.v.in_token + h * p.v.in_head + at * 2;
+        const uint4 x[2] = {reinterpret_cast<const uint4 *>(from)[0], reinterpret_cast<const uint4 *>(from)[1]};
+        char *row = page < 0 ? nullptr : key ? k_row : v_row;
+        quantise<Bf16>(x, key ? p.k_inv : p.v_inv, key ? p.k_scale : p.v_scale, row ? row + g * 8 : nullptr,
+                       row ? row + p.kv_heads * dim / 2 + g : nullptr, rows.out ? rows.out + tok * rows.out_token + (int64_t)g * 32 : nullptr);
+    }
+}
+
+template <bool Bf16, bool Interleaved>
+int pick_rotate(bool q4, const Params &p, int64_t n_tokens, cudaStream_t s)
+{
+    const size_t keys = q4 ? (size_t)p.kv_heads * p.dk * 2 : 0;
+    const DeviceInfo *dev = current_device();
+    if (dev == nullptr) return KV_ERR_CUDA;
+    const bool pdl = n_tokens <= 2ll * dev->num_sms * (2048 / kThreads);  // two waves (kv_common.cuh, launch_as)
+    const auto kernel = q4 ? rotate_kernel<Bf16, Interleaved, true> : rotate_kernel<Bf16, Interleaved, false>;
+    return cuda_status(launch_as(pdl, kernel, dim3((unsigned)n_tokens), dim3(kThreads), keys, s, p));
+}
+
+int launch_rotate(int dtype, bool interleaved, bool q4, const Params &p, int64_t n_tokens, cudaStream_t s)
+{
+    if (dtype == KV_BF16) return interleaved ? pick_rotate<true, true>(q4, p, n_tokens, s) : pick_rotate<true, false>(q4, p, n_tokens, s);
+    return interleaved ? pick_rotate<false, true>(q4, p, n_tokens, s) : pick_rotate<false, false>(q4, p, n_tokens, s);
+}
+
+// The rotation's part of the parameters, for heads of `dim` elements.
+int fill_rope(Params *p, const kv_rope *r, int dim)
+{
+    p->magnitude = 1.0f;
+    p->turn_items = make_fastdiv(1);
+    p->plain_items = make_fastdiv((uint32_t)(dim / 8));
+    if (r == nullptr || r->rot_dim == 0) return KV_OK;
+    if (r->rot_dim < 0 || r->rot_offset < 0 || r->turns == nullptr || !std::isfinite(r->magnitude)) return KV_ERR_INVALID_ARG;
+    if (r->rot_dim > dim || r->rot_offset > dim - r->rot_dim) return KV_ERR_RANGE;
+    if (r->rot_dim % (r->interleaved ? 8 : 16) || r->rot_offset % 8 || ((uintptr_t)r->turns & 7u)) return KV_ERR_ALIGN;
+    if (r->rot_dim > kMaxRot) return KV_ERR_UNSUPPORTED;
+    p->turns = r->turns;
+    p->half = r->rot_dim / 2;
+    p->offset = r->rot_offset;
+    p->magnitude = r->magnitude;
+    p->turn_items = make_fastdiv((uint32_t)(r->rot_dim / (r->interleaved ? 8 : 16)));
+    if (r->rot_dim < dim) p->plain_items = make_fastdiv((uint32_t)((dim - r->rot_dim) / 8));
+    return KV_OK;
+}
+
+int check_heads(int dtype, int heads, int dim)
+{
+    if (dtype != KV_BF16 && dtype != KV_F16) return KV_ERR_INVALID_ARG;
+    if (heads < 0 || dim <= 0) return KV_ERR_INVALID_ARG;
+    if (dim % 8) return KV_ERR_ALIGN;
+    if (dim > (1 << 16) || heads > (1 << 14)) return KV_ERR_UNSUPPORTED;
+    return KV_OK;
+}
+
+// What both writes check and fill in.
+int fill_write(Params *p, const kv_new_tokens *t, const kv_rope *rope, const kv_cache_desc *k, int k_tensor, int k_plane,
+               const kv_cache_desc *v, int v_tensor, int v_plane, bool q4)
+{
+    if (t == nullptr || t->n_tokens < 0 || t->n_reqs < 0 || t->max_blocks_per_req < 0 || t->bt_row_stride < 0 || t->n_kv_heads <= 0 ||
+        t->head_dim_v < 0)
+        return KV_ERR_INVALID_ARG;
+    int st;
+    if ((st = check_heads(t->dtype, t->n_heads, t->head_dim)) != KV_OK) return st;
+    if ((st = check_heads(t->dtype, t->n_kv_heads, t->head_dim_v ? t->head_dim_v : 8)) != KV_OK) return st;
+    if (t->n_reqs > 1 && t->bt_row_stride < t->max_blocks_per_req) return KV_ERR_INVALID_ARG;
+    if ((st = fill_rope(p, rope, t->head_dim)) != KV_OK) return st;
+    const auto check = q4 ? check_q4_plane : check_plane;
+    if ((st = check(k, k_tensor, k_plane, t->n_kv_heads, t->head_dim)) != KV_OK) return st;
+    if (t->head_dim_v) {
+        if ((st = check(v, v_tensor, v_plane, t->n_kv_heads, t->head_dim_v)) != KV_OK) return st;
+        if (k->block_size != v->block_size) return KV_ERR_INVALID_ARG;
+    }
+    if (t->n_tokens == 0) return KV_OK;
+    if (t->n_tokens >= (1ll << 31)) return KV_ERR_UNSUPPORTED;
+    if (t->token_req == nullptr || t->token_pos == nullptr || (t->block_table == nullptr && t->n_reqs > 0 && t->max_blocks_per_req > 0))
+        return KV_ERR_INVALID_ARG;
+    const DeviceInfo *dev = current_device();
+    if (t->n_heads) {
+        if ((st = check_rows(t->q, t->q_token_stride, t->q_head_stride)) != KV_OK) return st;
+        if ((st = check_rows(t->q_out, t->q_out_token_stride, t->q_out_head_stride)) != KV_OK) return st;
+        p->q = Rows{(const char *)t->q, (char *)t->q_out, t->q_token_stride, t->q_head_stride, t->q_out_token_stride, t->q_out_head_stride};
+    }
+    if ((st = check_rows(t->k, t->k_token_stride, t->k_head_stride)) != KV_OK) return st;
+    p->k = Rows{(const char *)t->k, nullptr, t->k_token_stride, t->k_head_stride, 0, 0};
+    p->kp = Plane{(char *)k->base[k_tensor] + (k_plane ? k->plane_stride : 0), k->block_stride, k->token_stride, (int32_t)k->num_blocks};
+    p->v_items = p->v_groups = make_fastdiv(1);
+    if (t->head_dim_v) {
+        if ((st = check_rows(t->v, t->v_token_stride, t->v_head_stride)) != KV_OK) return st;
+        p->v = Rows{(const char *)t->v, nullptr, t->v_token_stride, t->v_head_stride, 0, 0};
+        p->vp = Plane{(char *)v->base[v_tensor] + (v_plane ? v->plane_stride : 0), v->block_stride, v->token_stride, (int32_t)v->num_blocks};
+        p->v_items = make_fastdiv((uint32_t)(t->head_dim_v / 8));
+        p->v_groups = make_fastdiv((uint32_t)(t->head_dim_v >= 16 ? t->head_dim_v / 16 : 1));
+    }
+    p->k_groups = make_fastdiv((uint32_t)(t->head_dim >= 16 ? t->head_dim / 16 : 1));
+    p->token_req = t->token_req;
+    p->token_pos = t->token_pos;
+    p->rope_pos = t->rope_pos ? t->rope_pos : t->token_pos;
+    p->table = t->block_table;
+    p->table_stride = t->bt_row_stride;
+    p->n_reqs = t->n_reqs;
+    p->max_blocks = t->max_blocks_per_req;
+    p->heads = t->n_heads;
+    p->kv_heads = t->n_kv_heads;
+    p->dk = t->head_dim;
+    p->dv = t->head_dim_v;
+    p->block = make_fastdiv((uint32_t)k->block_size);
+    if (dev == nullptr) return KV_ERR_CUDA;
+    p->err = dev->err_word;
+    return KV_OK;
+}
+
+}  // namespace
+
+int check_q4_plane(const kv_cache_desc *c, int tensor, int plane, int heads, int dim)
+{
+    const int st = check_cache(c);
+    if (st != KV_OK) return st;
+    if (tensor < 0 || tensor >= c->n_tensors || plane < 0 || plane >= c->n_planes) return KV_ERR_INVALID_ARG;
+    if (dim % 32) return KV_ERR_ALIGN;
+    if (dim > kQ4MaxDim) return KV_ERR_UNSUPPORTED;
+    if (q4_row_bytes(heads, dim) != c->row_bytes || c->num_blocks == 0) return KV_ERR_INVALID_ARG;
+    if (c->num_blocks >= (1ll << 31) || c->token_stride >= (1ll << 40) || c->block_stride >= (1ll << 40)) return KV_ERR_UNSUPPORTED;
+    return KV_OK;
+}
+
+int preload_rotate_kernels()
+{
+    return load_kernels(rotate_kernel<false, false, false>, rotate_kernel<false, false, true>, rotate_kernel<false, true, false>,
+                        rotate_kernel<false, true, true>, rotate_kernel<true, false, false>, rotate_kernel<true, false, true>,
+                        rotate_kernel<true, true, false>, rotate_kernel<true, true, true>);
+}
+
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" {
+
+int kv_rope_frequencies(int32_t rot_dim, double base, const kv_rope_scaling *scaling, uint64_t *turns_out, float *magnitude_out)
+{
+    const int kind = scaling ? scaling->kind : KV_ROPE_PLAIN;
+    if (turns_out == nullptr || rot_dim <= 0 || rot_dim % 2 || !(base > 1.0) || !std::isfinite(base) || kind < KV_ROPE_PLAIN || kind > KV_ROPE_YARN)
+        return KV_ERR_INVALID_ARG;
+    const double f = kind == KV_ROPE_PLAIN ? 1.0 : scaling->factor, length = scaling ? scaling->original_length : 0.0;
+    if (!(f > 0.0) || !std::isfinite(f)) return KV_ERR_INVALID_ARG;
+    const bool banded = kind == KV_ROPE_BANDS || kind == KV_ROPE_YARN;
+    if (banded && (!(length > 0.0) || !std::isfinite(length) || !(scaling->slow > 0.0) || !(scaling->fast > scaling->slow) || !std::isfinite(scaling->fast)))
+        return KV_ERR_INVALID_ARG;
+    constexpr double kTurn = 6.283185307179586476925;
+    const double d = rot_dim;
+    if (kind == KV_ROPE_BASE) {
+        if (rot_dim <= 2) return KV_ERR_INVALID_ARG;
+        base *= std::pow(f, d / (d - 2.0));
+    }
+    double low = 0.0, high = 0.0;
+    if (kind == KV_ROPE_YARN) {  // pairs that turn `fast` and `slow` times over the original length
+        low = std::fmax(std::floor(d * std::log(length / (scaling->fast * kTurn)) / (2.0 * std::log(base))), 0.0);
+        high = std::fmin(std::ceil(d * std::log(length / (scaling->slow * kTurn)) / (2.0 * std::log(base))), d - 1.0);
+    }
+    for (int i = 0; i < rot_dim / 2; i++) {
+        double w = std::pow(base, -2.0 * i / d), mix = 1.0;  // mix: how much of the frequency stays as it is
+        if (kind == KV_ROPE_LINEAR) mix = 0.0;
+        if (kind == KV_ROPE_BANDS) mix = (length * w / kTurn - scaling->slow) / (scaling->fast - scaling->slow);
+        if (kind == KV_ROPE_YARN) mix = 1.0 - (i - low) / std::fmax(high - low, 1e-3);
+        mix = std::fmin(std::fmax(mix, 0.0), 1.0);
+        if (kind != KV_ROPE_BASE) w = w * mix + w / f * (1.0 - mix);
+        // of a turn: below 2^64, as w is at most 1 (or 1 / f)
+        const double t = std::nearbyint(std::ldexp(std::fmod(w / kTurn, 1.0), 64));
+        turns_out[i] = t >= 18446744073709551616.0 ? 0 : (uint64_t)t;
+    }
+    if (magnitude_out) *magnitude_out = (float)(kind == KV_ROPE_YARN && f > 1.0 ? 0.1 * std::log(f) + 1.0 : 1.0);
+    return KV_OK;
+}
+
+int kv_rotate(int32_t dtype, int32_t n_heads, int32_t head_dim, const void *x, int64_t token_stride, int64_t head_stride, void *out,
+              int64_t out_token_stride, int64_t out_head_stride, int64_t n_tokens, const int32_t *token_pos, const kv_rope *rope, int32_t inverse,
+              kv_stream_t stream)
+{
+    Params p = {};
+    int st = check_heads(dtype, n_heads, head_dim);
+    if (st != KV_OK) return st;
+    if (n_tokens < 0 || rope == nullptr) return KV_ERR_INVALID_ARG;
+    if ((st = fill_rope(&p, rope, head_dim)) != KV_OK) return st;
+    if (n_tokens >= (1ll << 31)) return KV_ERR_UNSUPPORTED;
+    if (n_tokens == 0 || n_heads == 0) return KV_OK;
+    if (token_pos == nullptr) return KV_ERR_INVALID_ARG;
+    if ((st = check_rows(x, token_stride, head_stride)) != KV_OK) return st;
+    if ((st = check_rows(out, out_token_stride, out_head_stride)) != KV_OK) return st;
+    p.q = Rows{(const char *)x, (char *)out, token_stride, head_stride, out_token_stride, out_head_stride};
+    p.rope_pos = token_pos;
+    p.heads = n_heads;
+    p.dk = head_dim;
+    p.inverse = inverse != 0;
+    return launch_rotate(dtype, rope->interleaved != 0, false, p, n_tokens, (cudaStream_t)stream);
+}
+
+int kv_q4_row_bytes(int32_t heads, int32_t head_dim, int32_t *bytes_out)
+{
+    if (bytes_out == nullptr || heads <= 0 || head_dim <= 0) return KV_ERR_INVALID_ARG;
+    if (head_dim % 32) return KV_ERR_ALIGN;
+    if (head_dim > kQ4MaxDim || heads > (1 << 14)) return KV_ERR_UNSUPPORTED;
+    *bytes_out = (int32_t)q4_row_bytes(heads, head_dim);
+    return KV_OK;
+}
+
+int kv_rotate_write(const kv_new_tokens *tokens, const kv_rope *rope, const kv_cache_desc *k, int32_t k_tensor, int32_t k_plane,
+                    const kv_cache_desc *v, int32_t v_tensor, int32_t v_plane, kv_stream_t stream)
+{
+    Params p = {};
+    const int st = fill_write(&p, tokens, rope, k, k_tensor, k_plane, v, v_tensor, v_plane, false);
+    if (st != KV_OK || tokens->n_tokens == 0) return st;
+    return launch_rotate(tokens->dtype, rope && rope->interleaved, false, p, tokens->n_tokens, (cudaStream_t)stream);
+}
+
+int kv_rotate_write_q4(const kv_new_tokens *tokens, const kv_rope *rope, const kv_cache_desc *k, int32_t k_tensor, int32_t k_plane,
+                       const kv_cache_desc *v, int32_t v_tensor, int32_t v_plane, float k_scale, float v_scale, void *k_held, void *v_held,
+                       kv_stream_t stream)
+{
+    Params p = {};
+    if (tokens != nullptr && tokens->head_dim_v == 0) return KV_ERR_UNSUPPORTED;
+    if (!good_scale(k_scale) || !good_scale(v_scale)) return KV_ERR_INVALID_ARG;
+    if (tokens != nullptr && (int64_t)tokens->n_kv_heads * tokens->head_dim > kMaxQ4Keys) return KV_ERR_UNSUPPORTED;
+    if (!aligned16(k_held) || !aligned16(v_held)) return KV_ERR_ALIGN;
+    const int st = fill_write(&p, tokens, rope, k, k_tensor, k_plane, v, v_tensor, v_plane, true);
+    if (st != KV_OK || tokens->n_tokens == 0) return st;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.k_inv = (float)(1.0 / k_scale);
+    p.v_inv = (float)(1.0 / v_scale);
+    p.k.out = (char *)k_held;
+    p.v.out = (char *)v_held;
+    p.k.out_token = (int64_t)tokens->n_kv_heads * tokens->head_dim * 2;
+    p.v.out_token = (int64_t)tokens->n_kv_heads * tokens->head_dim_v * 2;
+    return launch_rotate(tokens->dtype, rope && rope->interleaved, true, p, tokens->n_tokens, (cudaStream_t)stream);
+}
+
+}  // extern "C"

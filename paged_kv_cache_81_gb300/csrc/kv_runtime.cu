@@ -79,7 +79,7 @@ int preload_all_kernels(const DeviceInfo &dev)
     std::lock_guard<std::mutex> lock(mu);
     if (done[dev.device]) return KV_OK;
     for (int (*load)() : {preload_write_kernels, preload_xfer_kernels, preload_copy_kernels, preload_bulk_kernels,
-                          preload_clip_kernels, preload_hash_kernels, preload_signal_kernels}) {
+                          preload_clip_kernels, preload_hash_kernels, preload_signal_kernels, preload_rotate_kernels}) {
         const int st = load();
         if (st != KV_OK) return st;
     }

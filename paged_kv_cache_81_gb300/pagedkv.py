@@ -34,7 +34,8 @@ EXPORTS = ("kv_version", "kv_status_string", "kv_last_cuda_error", "kv_slot_mapp
            "kv_get_last_error", "kv_build_xfer_list_static", "kv_unpack_blocks_signal", "kv_wait_signal",
            "kv_clip_block_lists", "kv_block_hashes", "kv_block_hashes_workspace_bytes", "kv_write_tokens",
            "kv_attention", "kv_attention_workspace_bytes", "kv_latent_attention", "kv_latent_expand", "kv_attention_mass",
-           "kv_attention_mass_workspace_bytes", "kv_evict")
+           "kv_attention_mass_workspace_bytes", "kv_evict", "kv_rope_frequencies", "kv_rotate", "kv_rotate_write",
+           "kv_q4_row_bytes", "kv_rotate_write_q4")
 
 
 class KvError(RuntimeError):
@@ -92,6 +93,56 @@ class KvAttnDesc(ctypes.Structure):
     ]
 
 
+class KvRope(ctypes.Structure):
+    _fields_ = [
+        ("turns", ctypes.c_void_p),
+        ("rot_dim", ctypes.c_int32),
+        ("rot_offset", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("magnitude", ctypes.c_float),
+    ]
+
+
+class KvRopeScaling(ctypes.Structure):
+    _fields_ = [
+        ("kind", ctypes.c_int32),
+        ("factor", ctypes.c_double),
+        ("original_length", ctypes.c_double),
+        ("fast", ctypes.c_double),
+        ("slow", ctypes.c_double),
+    ]
+
+
+class KvNewTokens(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32),
+        ("n_heads", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("head_dim_v", ctypes.c_int32),
+        ("q", ctypes.c_void_p),
+        ("q_token_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64),
+        ("q_out", ctypes.c_void_p),
+        ("q_out_token_stride", ctypes.c_int64),
+        ("q_out_head_stride", ctypes.c_int64),
+        ("k", ctypes.c_void_p),
+        ("k_token_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("v", ctypes.c_void_p),
+        ("v_token_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64),
+        ("token_req", ctypes.c_void_p),
+        ("token_pos", ctypes.c_void_p),
+        ("rope_pos", ctypes.c_void_p),
+        ("n_tokens", ctypes.c_int64),
+        ("block_table", ctypes.c_void_p),
+        ("n_reqs", ctypes.c_int32),
+        ("max_blocks_per_req", ctypes.c_int32),
+        ("bt_row_stride", ctypes.c_int64),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -109,6 +160,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         D = ctypes.POINTER(KvCacheDesc)
         S = ctypes.POINTER(KvStageDesc)
         A, B = ctypes.POINTER(KvAttnDesc), ctypes.POINTER(KvAttnBatch)
+        R, N = ctypes.POINTER(KvRope), ctypes.POINTER(KvNewTokens)
+        f32 = ctypes.c_float
         sig = {
             "kv_version": ([], ctypes.c_char_p),
             "kv_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -136,6 +189,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             "kv_evict": ([D, P, i32, i32, i64, P, P, i64, i32, i32, i32, i32, P, i32, i64, P, P, i64, P, i64, P],
                          ctypes.c_int),
             "kv_write_tokens": ([D, P, i64, P, i32, i32, i64, P, P, i64, P, P], ctypes.c_int),
+            "kv_rope_frequencies": ([i32, ctypes.c_double, ctypes.POINTER(KvRopeScaling), P, ctypes.POINTER(f32)], ctypes.c_int),
+            "kv_rotate": ([i32, i32, i32, P, i64, i64, P, i64, i64, i64, P, R, i32, P], ctypes.c_int),
+            "kv_rotate_write": ([N, R, D, i32, i32, D, i32, i32, P], ctypes.c_int),
+            "kv_q4_row_bytes": ([i32, i32, ctypes.POINTER(i32)], ctypes.c_int),
+            "kv_rotate_write_q4": ([N, R, D, i32, i32, D, i32, i32, f32, f32, P, P, P], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             f = getattr(lib, name)
@@ -799,6 +857,158 @@ def kv_evict(cache: PagedCache, block_table: torch.Tensor, kv_lens: torch.Tensor
         cache.desc(), table, n, pages, row, _i32_on(dev, kv_lens, n, "kv_lens"), from_score, from_row, score.shape[1], budget, sinks, recent,
         out, out_pages, out_row, _i32_on(dev, new_lens, n, "new_lens"), kept.data_ptr(), kept.stride(0), to_score, to_row, handle))
     return new_lens, kept, out_score
+
+
+# ---------------------------------------------------------------------------
+# rotary positions, and the writes that apply them
+# ---------------------------------------------------------------------------
+_ROPE_KINDS = {"none": 0, "linear": 1, "base": 2, "bands": 3, "yarn": 4}
+
+
+def kv_rope_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
+                        original_length: float = 8192.0, fast: Optional[float] = None, slow: float = 1.0):
+    """(frequencies as 64-bit fractions of a turn, int64 [rot_dim / 2] on the CPU; magnitude), see kv_rope_scaling.
+
+    scaling: "none", "linear", "base", "bands" or "yarn"; fast: turns over original_length from which a pair stays as it
+    is (default 4 for "bands", 32 for "yarn")."""
+    if scaling not in _ROPE_KINDS:
+        raise ValueError(f"scaling must be one of {', '.join(_ROPE_KINDS)}")
+    _int32(rot_dim=rot_dim)
+    turns = torch.empty(max(rot_dim, 0) // 2, dtype=torch.int64)
+    magnitude = ctypes.c_float(0)
+    how = KvRopeScaling(_ROPE_KINDS[scaling], factor, original_length, fast if fast is not None else 32.0 if scaling == "yarn" else 4.0, slow)
+    _check("kv_rope_frequencies", load().kv_rope_frequencies(rot_dim, base, ctypes.byref(how), turns.data_ptr(), ctypes.byref(magnitude)))
+    return turns, magnitude.value
+
+
+class Rope:
+    """What rotates of a head (kv_rope): the frequencies on the GPU, the part of the head, the order of its pairs."""
+
+    def __init__(self, turns: torch.Tensor, *, offset: int = 0, interleaved: bool = False, magnitude: float = 1.0):
+        if turns.dtype is not torch.int64 or turns.dim() != 1 or not turns.is_contiguous() or not turns.is_cuda:
+            raise ValueError("turns must be a contiguous int64 CUDA tensor, one frequency a pair")
+        _int32(rot_dim=2 * turns.numel(), offset=offset)
+        self.turns, self.device = turns, turns.get_device()
+        self.desc = KvRope(turns.data_ptr(), 2 * turns.numel(), offset, 1 if interleaved else 0, magnitude)
+
+    @classmethod
+    def make(cls, rot_dim: int, base: float = 10000.0, *, offset: int = 0, interleaved: bool = False, device="cuda", **scaling) -> "Rope":
+        """The rotation of rot_dim elements; scaling: the keywords of kv_rope_frequencies."""
+        turns, magnitude = kv_rope_frequencies(rot_dim, base, **scaling)
+        return cls(turns.to(device), offset=offset, interleaved=interleaved, magnitude=magnitude)
+
+
+def _rope_on(dev: int, rope: Optional[Rope]) -> Optional[KvRope]:
+    if rope is None:
+        return None
+    if rope.device != dev:
+        raise ValueError(f"the rotation's frequencies must be on cuda:{dev}")
+    return rope.desc
+
+
+def _rotated_rows(dev: int, x: torch.Tensor, out: Optional[torch.Tensor], name: str, stream):
+    """(type code, strides of x, out, strides of out)."""
+    code, token, head = _rows3(x, name)
+    if out is None:
+        out = _empty(x, x.shape, x.dtype, stream)
+    elif out.shape != x.shape or out.dtype is not x.dtype or out.get_device() != dev:
+        raise ValueError(f"the output of {name} must have its shape and type, on its device")
+    _, to_token, to_head = _rows3(out, f"the output of {name}")
+    return code, token, head, out, to_token, to_head
+
+
+def kv_rotate(x: torch.Tensor, token_pos: torch.Tensor, rope: Rope, *, inverse: bool = False, out: Optional[torch.Tensor] = None,
+              stream=None) -> torch.Tensor:
+    """Heads x [tokens, heads, dim] rotated by their tokens' positions (int32 [tokens]); out may be x itself.  inverse: the
+    transposed map, which takes the output's gradient to x's."""
+    dev = x.get_device()
+    handle = _begin(dev, stream)
+    code, token, head, out, to_token, to_head = _rotated_rows(dev, x, out, "x", stream)
+    T, H, d = x.shape
+    _check("kv_rotate", (_lib or load()).kv_rotate(code, H, d, x.data_ptr(), token, head, out.data_ptr(), to_token, to_head, T,
+                                                   _i32_on(dev, token_pos, T, "token_pos"), _rope_on(dev, rope), 1 if inverse else 0, handle))
+    return out
+
+
+def _new_tokens(q, k, v, block_table, token_req, token_pos, rope_pos, q_out, stream):
+    """(kv_new_tokens, device, stream handle, q_out)."""
+    code, k_token, k_head = _rows3(k, "k")
+    dev = k.get_device()
+    handle = _begin(dev, stream)
+    T, G, dk = k.shape
+    d = KvNewTokens(dtype=code, n_kv_heads=G, head_dim=dk, k=k.data_ptr(), k_token_stride=k_token, k_head_stride=k_head, n_tokens=T)
+    if q is not None:
+        if q.dim() != 3 or q.dtype is not k.dtype or q.shape[0] != T or q.shape[2] != dk or q.get_device() != dev:
+            raise ValueError("q must have k's tokens, width, type and device")
+        _, d.q_token_stride, d.q_head_stride, q_out, d.q_out_token_stride, d.q_out_head_stride = _rotated_rows(dev, q, q_out, "q", stream)
+        d.n_heads, d.q, d.q_out = q.shape[1], q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if v is not None:
+        if v.dim() != 3 or v.dtype is not k.dtype or v.shape[:2] != k.shape[:2] or v.get_device() != dev:
+            raise ValueError("v must have k's tokens, heads, type and device")
+        _, d.v_token_stride, d.v_head_stride = _rows3(v, "v")
+        d.v, d.head_dim_v = v.data_ptr(), v.shape[2]
+    d.token_req, d.token_pos = _i32_on(dev, token_req, T, "token_req"), _i32_on(dev, token_pos, T, "token_pos")
+    if rope_pos is not None:
+        d.rope_pos = _i32_on(dev, rope_pos, T, "rope_pos")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be an int32 [n_reqs, max_blocks] tensor")
+    d.n_reqs = block_table.shape[0]
+    d.block_table, d.max_blocks_per_req, d.bt_row_stride = _table(dev, block_table, d.n_reqs, "block_table")
+    return d, dev, handle, q_out
+
+
+def _key_and_value_planes(dev: int, cache: PagedCache, v_cache: Optional[PagedCache], k_tensor: int, v_tensor: Optional[int], dtype, values: bool = True):
+    """(descriptions of the keys' and values' caches, the values' tensor, their plane), as kv_attention finds them."""
+    k_desc = _like_cache(dev, cache, dtype, "cache")
+    if v_cache is not None:
+        return k_desc, _like_cache(dev, v_cache, dtype, "v_cache"), v_tensor or 0, v_cache.n_planes - 1
+    if v_tensor is None:
+        if cache.n_planes == 1 and values:
+            raise ValueError("a one-plane cache holds the values in another tensor: give v_tensor or v_cache")
+        v_tensor = k_tensor
+    return k_desc, k_desc, v_tensor, cache.n_planes - 1
+
+
+def kv_rotate_write(q: Optional[torch.Tensor], k: torch.Tensor, v: Optional[torch.Tensor], cache: PagedCache, block_table: torch.Tensor,
+                    token_req: torch.Tensor, token_pos: torch.Tensor, rope: Optional[Rope], *, v_cache: Optional[PagedCache] = None,
+                    k_tensor: int = 0, v_tensor: Optional[int] = None, rope_pos: Optional[torch.Tensor] = None,
+                    q_out: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """One layer's new tokens: keys k [tokens, key heads, dim] rotated and values v as they are written to the pages that the
+    block table gives, queries q [tokens, heads, dim] rotated into q_out (may be q), which is returned.  v None: rows
+    without values (latent ones).  Keys and values are placed as kv_attention finds them.  rope_pos: positions to rotate by, where
+    they are not token_pos."""
+    _tensor_numbers(k_tensor, v_tensor or 0)
+    d, dev, handle, q_out = _new_tokens(q, k, v, block_table, token_req, token_pos, rope_pos, q_out, stream)
+    k_desc, v_desc, v_tensor, v_plane = _key_and_value_planes(dev, cache, v_cache, k_tensor, v_tensor, k.dtype, v is not None)
+    _check("kv_rotate_write", (_lib or load()).kv_rotate_write(d, _rope_on(dev, rope), k_desc, k_tensor, 0, v_desc, v_tensor, v_plane, handle))
+    return q_out
+
+
+def kv_q4_row_bytes(heads: int, head_dim: int) -> int:
+    """Bytes of a 4-bit cache's row; such a cache is a PagedCache of uint8 tensors [.., block, row bytes]."""
+    _int32(heads=heads, head_dim=head_dim)
+    out = ctypes.c_int32(0)
+    _check("kv_q4_row_bytes", load().kv_q4_row_bytes(heads, head_dim, ctypes.byref(out)))
+    return out.value
+
+
+def kv_rotate_write_q4(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, cache: PagedCache, block_table: torch.Tensor,
+                       token_req: torch.Tensor, token_pos: torch.Tensor, rope: Optional[Rope], *, v_cache: Optional[PagedCache] = None,
+                       k_tensor: int = 0, v_tensor: Optional[int] = None, rope_pos: Optional[torch.Tensor] = None, k_scale: float = 1.0,
+                       v_scale: float = 1.0, q_out: Optional[torch.Tensor] = None, held: bool = False, stream=None):
+    """kv_rotate_write into a 4-bit cache; k_scale and v_scale are the tensors' scales.  Returns
+    q_out, or (q_out, keys, values) with what the cache now stands for when `held`."""
+    _tensor_numbers(k_tensor, v_tensor or 0)
+    d, dev, handle, q_out = _new_tokens(q, k, v, block_table, token_req, token_pos, rope_pos, q_out, stream)
+    k_desc, v_desc, v_tensor, v_plane = _key_and_value_planes(dev, cache, v_cache, k_tensor, v_tensor, torch.uint8)
+    k_held = _empty(k, k.shape, k.dtype, stream) if held else None
+    v_held = _empty(k, v.shape, v.dtype, stream) if held else None
+    _check("kv_rotate_write_q4", (_lib or load()).kv_rotate_write_q4(
+        d, _rope_on(dev, rope), k_desc, k_tensor, 0, v_desc, v_tensor, v_plane, k_scale, v_scale, k_held.data_ptr() if held else None,
+        v_held.data_ptr() if held else None, handle))
+    return (q_out, k_held, v_held) if held else q_out
 
 
 def default_max_run_blocks(stage_block_bytes: int, target_bytes: int = 16 * 1024) -> int:
