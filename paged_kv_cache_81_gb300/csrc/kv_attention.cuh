@@ -273,5 +273,6 @@ int preload_latent_kernels();     // kv_latent.cu
 int preload_expand_kernels();     // kv_expand.cu
 int preload_mass_kernels();       // kv_mass.cu
 int preload_evict_kernels();      // kv_evict.cu
+int preload_q4_kernels();         // kv_attention_q4.cu
 
 }  // namespace pkv

@@ -1,0 +1,68 @@
+// kv_attention_q4: attention over a 4-bit cache, its checks and the choice of its kernel.
+#include <cmath>
+
+#include "kv_attention_q4.cuh"
+
+namespace pkv {
+
+int preload_q4_kernels() { return preload_q4_few_kernels(); }
+
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" {
+
+int kv_attention_q4(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_cache_desc *k, int32_t k_tensor, int32_t k_plane,
+                    const kv_cache_desc *v, int32_t v_tensor, int32_t v_plane, float k_scale, float v_scale, const void *q, int64_t q_token_stride,
+                    int64_t q_head_stride, void *out, int64_t out_token_stride, int64_t out_head_stride, float *lse, void *workspace,
+                    int64_t workspace_bytes, kv_stream_t stream)
+{
+    if (d == nullptr || d->n_heads <= 0 || d->n_kv_heads <= 0 || d->n_heads % d->n_kv_heads != 0 || d->head_dim <= 0 || d->head_dim_v <= 0 ||
+        d->window < 0 || !good_scale(d->scale) || !good_scale(k_scale) || !good_scale(v_scale) || !good_scale(d->scale * k_scale) ||
+        (d->dtype != KV_BF16 && d->dtype != KV_F16))
+        return KV_ERR_INVALID_ARG;
+    int st = check_batch(batch);
+    if (st != KV_OK) return st;
+    const int group = d->n_heads / d->n_kv_heads;
+    if (d->head_dim % 32 || d->head_dim_v % 32) return KV_ERR_ALIGN;
+    if (group > 128 || (d->window && !d->causal)) return KV_ERR_UNSUPPORTED;
+    if ((st = check_q4_plane(k, k_tensor, k_plane, d->n_kv_heads, d->head_dim)) != KV_OK) return st;
+    if ((st = check_q4_plane(v, v_tensor, v_plane, d->n_kv_heads, d->head_dim_v)) != KV_OK) return st;
+    if (k->block_size != v->block_size) return KV_ERR_INVALID_ARG;
+    if (batch->n_reqs == 0 || batch->n_tokens == 0) return KV_OK;
+    if ((st = check_rows(q, q_token_stride, q_head_stride)) != KV_OK) return st;
+    if ((st = check_rows(out, out_token_stride, out_head_stride)) != KV_OK) return st;
+    if (workspace == nullptr) return KV_ERR_INVALID_ARG;
+    if (!aligned16(workspace) || ((uintptr_t)lse & 3u)) return KV_ERR_ALIGN;
+    const int rows = batch->n_tokens * group <= 8ll * batch->n_reqs ? 8 : 16;
+    Q4Params p = {};
+    if ((st = fill_batch(&p.b, batch, d->n_heads, d->n_kv_heads, k->block_size, group > rows ? rows : rows / group * group, 5, d->causal, d->window)) != KV_OK)
+        return st;
+    const DeviceInfo *dev = current_device();
+    if (dev == nullptr) return KV_ERR_CUDA;
+    if (workspace_bytes < attention_workspace(dev->num_sms)) return KV_ERR_RANGE;
+    if ((st = prepare_attention(*dev)) != KV_OK) return st;
+    p.b.err = dev->err_word;
+    const auto plane = [](const kv_cache_desc *c, int tensor, int which, int dim) {
+        return Q4Plane{(const char *)c->base[tensor] + (which ? c->plane_stride : 0), c->block_stride, c->token_stride, c->row_bytes, dim};
+    };
+    p.k = plane(k, k_tensor, k_plane, d->head_dim);
+    p.v = plane(v, v_tensor, v_plane, d->head_dim_v);
+    p.table = batch->block_table;
+    p.table_stride = batch->bt_row_stride;
+    p.num_blocks = (int32_t)(k->num_blocks < v->num_blocks ? k->num_blocks : v->num_blocks);
+    p.block = make_fastdiv((uint32_t)k->block_size);
+    p.q = (const char *)q;
+    p.q_token = q_token_stride;
+    p.q_head = q_head_stride;
+    p.heads_all = d->n_kv_heads;
+    const float scale = d->scale * k_scale;
+    p.o = Output{(char *)out, out_token_stride, out_head_stride, lse, d->n_heads, d->head_dim_v, scale, scale * kLog2e};
+    p.v_scale = v_scale;
+    p.counters = (int *)workspace;
+    p.ws = (float *)((char *)workspace + kCounterBytes);
+    return run_q4_few(d->dtype == KV_BF16, p, batch, rows, *dev, (cudaStream_t)stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,36 @@
+// What the two kernels of kv_attention_q4 share.
+#pragma once
+
+#include "kv_attention.cuh"
+#include "kv_q4.cuh"
+
+namespace pkv {
+
+// A plane of 4-bit rows.
+struct Q4Plane {
+    const char *base;
+    int64_t block_stride, token_stride;
+    int32_t row_bytes, dim;
+};
+
+struct Q4Params {
+    Batch b;
+    Q4Plane k, v;
+    const int32_t *table;
+    int64_t table_stride;
+    int32_t num_blocks;  // pages that both planes have
+    FastDiv block;       // slots of a page
+    const char *q;
+    int64_t q_token, q_head;
+    int32_t heads_all;   // key heads of a row
+    Output o;            // o.scale: of the products, with the keys' tensor scale
+    float v_scale;
+    float *ws;
+    int *counters;
+};
+
+int run_q4_few(bool bf16, const Q4Params &p, const kv_attn_batch *batch, int rows, const DeviceInfo &dev, cudaStream_t s);
+int preload_q4_few_kernels();  // kv_attention_q4_few.cu
+int preload_q4_kernels();      // kv_attention_q4.cu
+
+}  // namespace pkv

@@ -1,0 +1,639 @@
+// kv_attention_q4 for few rows: decoding, with at most 16 query rows (tokens x heads of a key head's group) a unit.
+//
+// The same one-pass softmax as kv_attention.cu.  What bounds it is memory, at 4.5 bits an element, so the work a
+// byte is 3.5 times that of a 16-bit cache: an SM gets 41 elements a cycle, and can issue about three instructions for
+// each.  So a code is touched once: it goes from shared memory to the registers of the warp that multiplies it, where
+// one conversion and one product with its scale make two fp16 values of it, exact (six significant bits), in the place that a
+// warp-wide product's operand wants (mma.sync with 8 query rows as its N: keys are the rows of S^T = K Q^T, and O^T = V^T P^T;
+// the dimensions' order within a thread's part is free in the first product, the keys' order in the second).  A
+// tcgen05 product would want them written to shared memory, twice the bytes of the cache's 16-bit rows a cycle
+// (82 in and 82 out of 128), or both operands in 4 bits, which queries and weights are not.
+//
+// Queries are brought to [1, 2) by a power of two a row and held in fp16, weights are fp16 (kv_tensor.cuh, weight_offset);
+// sums are in 32 bits.
+//
+// One persistent CTA per SM; a unit is one request's rows of up to eight key heads.
+//   warp 0        brings rows of keys and of values, one bulk copy a token (its heads lie together), into a ring of tiles
+//   other warps   each one key head and every n-th 16 keys of a tile: scores, weights, values, with a running maximum and sum of
+//                 its own, joined through shared memory at the unit's end
+// Rows lie 32 or 96 bytes off a multiple of 128 apart and the 16 keys of a step are taken in an order (kOrder) in which neither the
+// keys' 16-byte nor the values' 8-byte reads meet in a bank.
+#include "kv_attention_q4.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kLeast = 2;     // tiles of a piece of a unit, at least
+constexpr int kMaxHeads = 8;  // key heads of a unit
+constexpr int kMaxSlots = 4;
+constexpr uint32_t kOrder = 0x57463120u;  // key of row r of 8: hexadecimal digit r
+
+template <int D, int NT>
+struct Few {
+    static constexpr int kWarps = NT == 1 ? 16 : 8;  // that compute
+    static constexpr int kThreads = 32 * (kWarps + 1);
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kSteps = NT == 1 ? 2 : 4;   // groups of 16 keys that a warp takes of a tile
+    static constexpr int kPitch = D + 4;             // floats of a row in the join
+    static constexpr uint32_t kJoin = (uint32_t)kWarps * kRows * kPitch * 4;
+};
+static_assert(kMaxHeads * Few<128, 2>::kRows <= 256, "a fragment fits its place in the workspace");
+
+struct FewParams : Q4Params {
+    int32_t unit_heads;        // key heads of a unit
+    int32_t split;             // warps of a key head
+    int32_t tile;              // keys
+    int32_t k_pitch, v_pitch;  // bytes of a row in shared memory
+    int32_t slots;             // tiles of each ring
+};
+
+struct Aux {
+    uint64_t k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots], sync;
+    uint32_t k_valid[kMaxSlots][16], v_valid[kMaxSlots][16];  // bit a key of the tile: it is there
+    int scan[4 * 17];
+    Place place;
+    float m[16][16], l[16][16];  // of a warp's rows
+    int answer;
+    int gave_up;
+};
+
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The 8 x 8 matrix of 16-bit elements that the warp holds, a row in four lanes, transposed.
+__device__ __forceinline__ uint32_t transposed8(uint32_t v)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s)
+{
+    uint32_t v;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(v) : "r"(a), "r"(b), "r"(s));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t ld_smem4(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 ld_smem8(uint32_t a)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_smem2(uint32_t a)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_smem1(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// Where a unit's heads lie in a row, and in a row of shared memory: codes, then (from `rest` on) scales.
+struct Part {
+    uint32_t codes, code_bytes;    // in the row
+    uint32_t scales, scale_bytes;  // 16-byte pieces that hold them
+    uint32_t rest;                 // where the first scale stands in them
+    __device__ __forceinline__ Part(const Q4Plane &p, int all, int heads, int h0)
+    {
+        codes = (uint32_t)h0 * p.dim / 2;
+        code_bytes = (uint32_t)heads * p.dim / 2;
+        const uint32_t s = (uint32_t)all * p.dim / 2 + (uint32_t)h0 * p.dim / 16;
+        scales = s & ~15u;
+        rest = s - scales;
+        scale_bytes = ((s + (uint32_t)heads * p.dim / 16 + 15) & ~15u) - scales;
+    }
+};
+
+// One tile's rows, each token by its own bulk copy, and which of them are there.  `ready` waits for the slot.
+template <typename Ready>
+__device__ __forceinline__ bool load_rows(const FewParams &p, const Q4Plane &plane, const Part &part, const int32_t *row, int kb, int lo, int hi,
+                                          uint32_t to, uint32_t pitch, uint32_t bar, volatile uint32_t *valid, bool report, const Ready &ready)
+{
+    const int lane = threadIdx.x & 31;
+    const bool together = part.scales == part.codes + part.code_bytes;
+    const uint32_t bytes = part.code_bytes + part.scale_bytes;
+    const char *from = nullptr;
+    const auto find = [&](int j) {
+        from = nullptr;
+        const int key = kb + j;
+        if (key < lo || key >= hi) return;
+        const uint32_t col = fdiv((uint32_t)key, p.block);
+        const int page = __ldg(row + col);
+        if (page >= 0 && page < p.num_blocks)
+            from = plane.base + (int64_t)page * plane.block_stride + (int64_t)((uint32_t)key - col * p.block.d) * plane.token_stride;
+        else if (report)
+            set_error(p.b.err, KV_DERR_TABLE);
+    };
+    find(lane);
+    if (!ready()) return false;
+    for (int j = lane; j < p.tile; j += 32) {
+        if (j >= 32) find(j);
+        const uint32_t there = __ballot_sync(0xffffffffu, from != nullptr);
+        if (lane == 0) {
+            valid[j >> 5] = there;
+            mbar_expect(bar, (uint32_t)__popc(there) * bytes);
+        }
+        __syncwarp();
+        if (from != nullptr) {
+            const uint32_t at = to + (uint32_t)j * pitch;
+            if (together) {
+                bulk_load(at, from + part.codes, bytes, bar);
+            } else {
+                bulk_load(at, from + part.codes, part.code_bytes, bar);
+                bulk_load(at + part.code_bytes, from + part.scales, part.scale_bytes, bar);
+            }
+        }
+    }
+    warp_arrive(bar);
+    return true;
+}
+
+template <int D, int NT, bool Bf16>
+__global__ void __launch_bounds__(Few<D, NT>::kThreads, 1) attention_q4_few_kernel(const __grid_constant__ FewParams p)
+{
+    using F = Few<D, NT>;
+    extern __shared__ __align__(128) unsigned char smem[];
+    Aux &aux = *reinterpret_cast<Aux *>(smem);
+    float *const joins = reinterpret_cast<float *>(smem + ((sizeof(Aux) + 127) & ~127u));
+    const uint32_t ring = smem_addr(joins) + ((F::kJoin + 127) & ~127u);
+    const uint32_t k_bytes = (uint32_t)p.tile * p.k_pitch, v_bytes = (uint32_t)p.tile * p.v_pitch, v_ring = ring + p.slots * k_bytes;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const Batch &b = p.b;
+    const Waiter wait{&aux.gave_up, b.err};
+    const int users = p.unit_heads * p.split;  // warps that compute
+
+    if (tid == 0) {
+        aux.gave_up = 0;
+        for (int i = 0; i < p.slots; i++) {
+            mbar_init(smem_addr(&aux.k_full[i]), 1);
+            mbar_init(smem_addr(&aux.v_full[i]), 1);
+            mbar_init(smem_addr(&aux.k_empty[i]), users);
+            mbar_init(smem_addr(&aux.v_empty[i]), users);
+        }
+        mbar_init(smem_addr(&aux.sync), users);
+        mbar_init_fence();
+    }
+    grid_dep_entry();
+    const Line line = find_place<F::kThreads>(b, blockIdx.x, gridDim.x, kLeast, aux.scan, &aux.place, blockIdx.x == 0);
+    __syncthreads();
+    Walk w;
+    if (!w.start(b, aux.place, line)) {
+        // nothing to do: on to the common exit
+    } else if (warp == 0) {
+        // ---- rows of keys and values ----
+        int it = 0;
+        bool ok = true;
+        do {
+            if (w.u.tiles == 0) continue;
+            const int32_t *row = p.table + (int64_t)w.at.req * p.table_stride;
+            const Part kp(p.k, p.heads_all, p.unit_heads, w.at.head * p.unit_heads), vp(p.v, p.heads_all, p.unit_heads, w.at.head * p.unit_heads);
+            for (int t = 0; ok && t < w.n; t++, it++) {
+                const int s = it % p.slots, kb = (w.u.tile0 + w.at.off + t) << b.tile_shift;
+                const uint32_t phase = (uint32_t)(it / p.slots - 1) & 1;
+                ok = load_rows(p, p.k, kp, row, kb, w.u.lo, w.u.hi, ring + s * k_bytes, p.k_pitch, smem_addr(&aux.k_full[s]), aux.k_valid[s], true,
+                               [&] { return it < p.slots || wait.warp(smem_addr(&aux.k_empty[s]), phase); }) &&
+                     load_rows(p, p.v, vp, row, kb, w.u.lo, w.u.hi, v_ring + s * v_bytes, p.v_pitch, smem_addr(&aux.v_full[s]), aux.v_valid[s], false,
+                               [&] { return it < p.slots || wait.warp(smem_addr(&aux.v_empty[s]), phase); });
+            }
+        } while (ok && w.next(b));
+    } else if (warp <= users) {
+        const int me = warp - 1, h = me / p.split, part = me - h * p.split;
+        const int n = lane >> 2, t = lane & 3;
+        const uint32_t rk = (kOrder >> (4 * n)) & 7;                                            // keys of score rows n, n + 8
+        const uint32_t ra = (kOrder >> (8 * t)) & 7, rb = (kOrder >> (8 * t + 4)) & 7;          // keys of product columns 2 t, 2 t + 1
+        const bool k_has0 = t * (D / 4) < p.k.dim, k_has1 = t * (D / 4) + 16 < p.k.dim, v_has = n * (D / 8) < p.v.dim;
+        int it = 0, syncs = 0;
+        bool ok = true;
+        const auto sync_all = [&] {
+            warp_arrive(smem_addr(&aux.sync));
+            ok = wait.warp(smem_addr(&aux.sync), syncs++ & 1);
+            return ok;
+        };
+        do {
+            const int rows = w.u.rows, head0 = w.at.head * p.unit_heads;
+            // row r of a key head: its token and query head
+            const auto token_of = [&](int r, int &head_in) {
+                const int x = w.u.row0 + r, tok = (int)fdiv((uint32_t)x, b.group);
+                head_in = x - tok * (int)b.group.d;
+                return (int64_t)w.q.q0 + tok;
+            };
+            if (w.u.tiles == 0) {  // nothing is seen
+                for (int i = me * 32 + lane; i < p.unit_heads * rows; i += users * 32) {
+                    int g;
+                    const int hh = i / rows;
+                    const int64_t token = token_of(i - hh * rows, g);
+                    const int head = (head0 + hh) * (int)b.group.d + g;
+                    char *to = p.o.out + token * p.o.out_token + (int64_t)head * p.o.out_head;
+                    for (int col = 0; col < p.o.dv; col += 8) *reinterpret_cast<uint4 *>(to + col * 2) = make_uint4(0, 0, 0, 0);
+                    if (p.o.lse) p.o.lse[token * p.o.heads + head] = -INFINITY;
+                }
+                continue;
+            }
+            // ---- queries: row n (and n + 8) of the unit, this thread's quarter of the dimensions ----
+            uint32_t qf[NT][D / 16][2];
+            float c[NT][2];  // of the columns 2 t, 2 t + 1: log2 of a weight a unit of the products
+            int lo[NT][2], hi[NT][2];
+#pragma unroll
+            for (int x = 0; x < NT; x++) {
+                const int r = 8 * x + n;
+                uint4 raw[D / 32];
+#pragma unroll
+                for (int i = 0; i < D / 32; i++) raw[i] = make_uint4(0, 0, 0, 0);
+                if (r < rows) {
+                    int g;
+                    const int64_t token = token_of(r, g);
+                    const char *from = p.q + token * p.q_token + (int64_t)((head0 + h) * (int)b.group.d + g) * p.q_head;
+#pragma unroll
+                    for (int i = 0; i < D / 32; i++)
+                        if (t * (D / 4) + 8 * i < p.k.dim) raw[i] = __ldg(reinterpret_cast<const uint4 *>(from) + t * (D / 32) + i);
+                }
+                float to = 1.0f, back = 1.0f;
+                if (Bf16) {
+                    float most = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < D / 32; i++) {
+                        const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+                        for (int j = 0; j < 4; j++)
+                            most = fmaxf(most, fmaxf(fabsf(__uint_as_float(v[j] << 16)), fabsf(__uint_as_float(v[j] & 0xffff0000u))));
+                    }
+                    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+                    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+                    const uint32_t e = min(max(__float_as_uint(most) >> 23, 1u), 253u);
+                    to = __uint_as_float((254u - e) << 23);
+                    back = __uint_as_float(e << 23);
+                }
+#pragma unroll
+                for (int i = 0; i < D / 32; i++) {
+                    const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        qf[x][2 * i + (j >> 1)][j & 1] =
+                            Bf16 ? pack2<false>(__uint_as_float(v[j] << 16) * to, __uint_as_float(v[j] & 0xffff0000u) * to) : v[j];
+                }
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    // a normal number: a hidden score, -inf, stays that in the product with it
+                    c[x][i] = fminf(fmaxf(p.o.c * __shfl_sync(0xffffffffu, back, (2 * t + i) * 4), 0x1p-126f), 0x1p127f);
+                    sees(b, w.q, (int)fdiv((uint32_t)(w.u.row0 + min(8 * x + 2 * t + i, rows - 1)), b.group), lo[x][i], hi[x][i]);
+                }
+            }
+            float o[D / 16][NT][4];
+            float m[NT][2], l[NT][2];
+#pragma unroll
+            for (int x = 0; x < NT; x++) {
+#pragma unroll
+                for (int i = 0; i < D / 16; i++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++) o[i][x][j] = 0.0f;
+                m[x][0] = m[x][1] = -INFINITY;
+                l[x][0] = l[x][1] = 0.0f;
+            }
+            const Part kp(p.k, p.heads_all, p.unit_heads, head0), vp(p.v, p.heads_all, p.unit_heads, head0);
+            const uint32_t k_code = h * p.k.dim / 2 + t * (D / 8), k_unit = kp.code_bytes + kp.rest + h * p.k.dim / 16 + (D == 128 ? 2 * t : t);
+            const uint32_t v_code = h * p.v.dim / 2 + n * (D / 16), v_unit = vp.code_bytes + vp.rest + h * p.v.dim / 16 + (D == 128 ? n : n / 2);
+            for (int tile = 0; tile < w.n; tile++, it++) {
+                const int s = it % p.slots, kb = (w.u.tile0 + w.at.off + tile) << b.tile_shift;
+                const uint32_t phase = (uint32_t)(it / p.slots) & 1;
+                if (!wait.warp(smem_addr(&aux.k_full[s]), phase)) { ok = false; break; }
+                // ---- scores: S^T of 16 keys by 8 rows a step ----
+                float sc[F::kSteps][NT][4];
+#pragma unroll
+                for (int step = 0; step < F::kSteps; step++) {
+#pragma unroll
+                    for (int x = 0; x < NT; x++)
+#pragma unroll
+                        for (int j = 0; j < 4; j++) sc[step][x][j] = 0.0f;
+                    const int g = part + step * p.split;  // of the tile's groups of 16 keys
+                    const uint32_t there = aux.k_valid[s][g >> 1] >> (16 * (g & 1));
+                    const uint32_t r0 = ring + s * k_bytes + (uint32_t)(16 * g + rk) * p.k_pitch, r1 = r0 + 8u * p.k_pitch;
+                    const bool is0 = there >> rk & 1, is1 = there >> (rk + 8) & 1;
+                    uint32_t w0[D / 32], w1[D / 32], u0, u1;
+                    if (D == 128) {
+                        const uint4 a = ld_smem16(r0 + k_code), d = ld_smem16(r1 + k_code);
+                        w0[0] = a.x, w0[1] = a.y, w0[D / 32 - 2] = a.z, w0[D / 32 - 1] = a.w;
+                        w1[0] = d.x, w1[1] = d.y, w1[D / 32 - 2] = d.z, w1[D / 32 - 1] = d.w;
+                        u0 = ld_smem2(r0 + k_unit), u1 = ld_smem2(r1 + k_unit);
+                        if (!k_has1) u0 &= 0xff, u1 &= 0xff;
+                    } else {
+                        const uint2 a = ld_smem8(r0 + k_code), d = ld_smem8(r1 + k_code);
+                        w0[0] = a.x, w0[1] = a.y, w1[0] = d.x, w1[1] = d.y;
+                        u0 = ld_smem1(r0 + k_unit), u1 = ld_smem1(r1 + k_unit);
+                    }
+                    // what is not there counts as zeros
+                    u0 = e4m3x2_to_f16(is0 && k_has0 ? u0 : 0), u1 = e4m3x2_to_f16(is1 && k_has0 ? u1 : 0);
+#pragma unroll
+                    for (int i = 0; i < D / 32; i++) {
+                        const uint32_t z0 = prmt(u0, u0, i < 2 ? 0x1010 : 0x3232), z1 = prmt(u1, u1, i < 2 ? 0x1010 : 0x3232);
+                        uint32_t a[4], d[4];
+                        q4_to_f16(w0[i], a);
+                        q4_to_f16(w1[i], d);
+#pragma unroll
+                        for (int j = 0; j < 4; j++) a[j] = mul_f16x2(a[j], z0), d[j] = mul_f16x2(d[j], z1);
+#pragma unroll
+                        for (int j = 0; j < 2; j++)
+#pragma unroll
+                            for (int x = 0; x < NT; x++) mma16816(sc[step][x], a[2 * j], d[2 * j], a[2 * j + 1], d[2 * j + 1], qf[x][2 * i + j][0], qf[x][2 * i + j][1]);
+                    }
+                }
+                warp_arrive(smem_addr(&aux.k_empty[s]));
+                // ---- weights ----
+                bool hide = false;
+#pragma unroll
+                for (int x = 0; x < NT; x++)
+#pragma unroll
+                    for (int i = 0; i < 2; i++) hide |= lo[x][i] > kb || hi[x][i] < kb + p.tile;
+                if (__any_sync(0xffffffffu, hide)) {
+#pragma unroll
+                    for (int step = 0; step < F::kSteps; step++) {
+                        const int key = kb + 16 * (part + step * p.split) + (int)rk;
+#pragma unroll
+                        for (int x = 0; x < NT; x++)
+#pragma unroll
+                            for (int j = 0; j < 4; j++) {
+                                const int k = key + 8 * (j >> 1);
+                                if (k < lo[x][j & 1] || k >= hi[x][j & 1]) sc[step][x][j] = -INFINITY;
+                            }
+                    }
+                }
+                bool grow = false;
+                float top[NT][2];
+#pragma unroll
+                for (int x = 0; x < NT; x++)
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        float v = -INFINITY;
+#pragma unroll
+                        for (int step = 0; step < F::kSteps; step++) v = fmaxf(v, fmaxf(sc[step][x][i], sc[step][x][i + 2]));
+                        top[x][i] = v * c[x][i];
+                        grow |= top[x][i] > m[x][i] + 8.0f;
+                    }
+                if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                    for (int x = 0; x < NT; x++)
+#pragma unroll
+                        for (int i = 0; i < 2; i++) {
+                            float v = top[x][i];
+#pragma unroll
+                            for (int d = 4; d < 32; d *= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+                            const float now = fmaxf(m[x][i], v);
+                            const float a = now == -INFINITY ? 1.0f : exp2_fast(m[x][i] - now);
+                            m[x][i] = now;
+                            l[x][i] *= a;
+#pragma unroll
+                            for (int k = 0; k < D / 16; k++) o[k][x][i] *= a, o[k][x][i + 2] *= a;
+                        }
+                }
+                uint32_t pf[F::kSteps][NT][2];
+#pragma unroll
+                for (int x = 0; x < NT; x++) {
+                    const float off0 = m[x][0] == -INFINITY ? 0.0f : m[x][0] - 7.0f, off1 = m[x][1] == -INFINITY ? 0.0f : m[x][1] - 7.0f;
+#pragma unroll
+                    for (int step = 0; step < F::kSteps; step++) {
+                        float e[4];
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            e[j] = exp2_fast(fmaf(sc[step][x][j], c[x][j & 1], j & 1 ? -off1 : -off0));
+                            l[x][j & 1] += e[j];
+                        }
+                        pf[step][x][0] = transposed8(pack2<false>(e[0], e[1]));
+                        pf[step][x][1] = transposed8(pack2<false>(e[2], e[3]));
+                    }
+                }
+                // ---- values: O^T of 16 dimensions by 8 rows a product ----
+                if (!wait.warp(smem_addr(&aux.v_full[s]), phase)) { ok = false; break; }
+#pragma unroll
+                for (int step = 0; step < F::kSteps; step++) {
+                    const int g = part + step * p.split;
+                    const uint32_t there = aux.v_valid[s][g >> 1] >> (16 * (g & 1));
+                    const uint32_t at = v_ring + s * v_bytes + (uint32_t)(16 * g) * p.v_pitch;
+                    const uint32_t key[4] = {ra, rb, ra + 8, rb + 8};
+                    uint32_t cw[4][D / 64], unit[4];
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const uint32_t row = at + key[j] * p.v_pitch;
+                        if (D == 128) {
+                            const uint2 x = ld_smem8(row + v_code);
+                            cw[j][0] = x.x, cw[j][D / 64 - 1] = x.y;
+                        } else {
+                            cw[j][0] = ld_smem4(row + v_code);
+                        }
+                        unit[j] = ld_smem1(row + v_unit);
+                        if (!(there >> key[j] & 1) || !v_has) unit[j] = 0;
+                    }
+                    const uint32_t z0 = e4m3x2_to_f16(unit[0] | unit[1] << 8), z1 = e4m3x2_to_f16(unit[2] | unit[3] << 8);
+#pragma unroll
+                    for (int i = 0; i < D / 64; i++) {
+                        // two keys' codes side by side: the even dimensions' and the odd ones'
+                        uint32_t a0[4], a1[4], a2[4], a3[4];
+                        q4_to_f16((cw[0][i] & 0x0f0f0f0fu) | (cw[1][i] & 0x0f0f0f0fu) << 4, a0);
+                        q4_to_f16((cw[0][i] >> 4 & 0x0f0f0f0fu) | (cw[1][i] & 0xf0f0f0f0u), a1);
+                        q4_to_f16((cw[2][i] & 0x0f0f0f0fu) | (cw[3][i] & 0x0f0f0f0fu) << 4, a2);
+                        q4_to_f16((cw[2][i] >> 4 & 0x0f0f0f0fu) | (cw[3][i] & 0xf0f0f0f0u), a3);
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            a0[j] = mul_f16x2(a0[j], z0), a1[j] = mul_f16x2(a1[j], z0), a2[j] = mul_f16x2(a2[j], z1), a3[j] = mul_f16x2(a3[j], z1);
+#pragma unroll
+                            for (int x = 0; x < NT; x++) mma16816(o[4 * i + j][x], a0[j], a1[j], a2[j], a3[j], pf[step][x][0], pf[step][x][1]);
+                        }
+                    }
+                }
+                warp_arrive(smem_addr(&aux.v_empty[s]));
+            }
+            if (!ok) break;
+            // ---- the warps of a head join ----
+#pragma unroll
+            for (int x = 0; x < NT; x++)
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    float v = l[x][i];
+#pragma unroll
+                    for (int d = 4; d < 32; d *= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
+                    const int r = 8 * x + 2 * t + i;
+                    if (n == 0) aux.m[me][r] = m[x][i], aux.l[me][r] = v;
+                    float4 *to = reinterpret_cast<float4 *>(joins + (me * F::kRows + r) * F::kPitch + n * (D / 8));
+#pragma unroll
+                    for (int k = 0; k < D / 32; k++) to[k] = make_float4(o[2 * k][x][i], o[2 * k][x][i + 2], o[2 * k + 1][x][i], o[2 * k + 1][x][i + 2]);
+                }
+            if (!sync_all()) break;
+            const bool whole = w.whole();
+            const auto row_out = [&](int hh, int r, int64_t &lse_at) {
+                int g;
+                const int64_t token = token_of(r, g);
+                const int head = (head0 + hh) * (int)b.group.d + g;
+                lse_at = token * p.o.heads + head;
+                return p.o.out + token * p.o.out_token + (int64_t)head * p.o.out_head;
+            };
+            // (O, m, l) of a row as the caller wants it: to the output, or to a fragment [head, row][D], m, l
+            const auto finish = [&](int hh, int r, int quad, float4 v, float top, float sum, float *frag) {
+                if (frag != nullptr) {
+                    const int at = hh * F::kRows + r;
+                    __stcg(reinterpret_cast<float4 *>(frag + at * D) + quad, v);
+                    if (quad == 0) {
+                        __stcg(frag + p.unit_heads * F::kRows * D + 2 * at, top);
+                        __stcg(frag + p.unit_heads * F::kRows * D + 2 * at + 1, sum);
+                    }
+                    return;
+                }
+                int64_t lse_at;
+                char *to = row_out(hh, r, lse_at);
+                const float inv = sum > 0.0f ? p.v_scale / sum : 0.0f;
+                if (quad * 4 < p.o.dv) {
+                    uint2 z;
+                    z.x = pack2<Bf16>(v.x * inv, v.y * inv);
+                    z.y = pack2<Bf16>(v.z * inv, v.w * inv);
+                    *reinterpret_cast<uint2 *>(to + quad * 8) = z;
+                }
+                if (quad == 0 && p.o.lse) p.o.lse[lse_at] = sum > 0.0f ? fmaf(top, 0.69314718055994530942f, weight_log<false>(sum)) : -INFINITY;
+            };
+            float *const mine = p.ws + (int64_t)(2 * blockIdx.x + (w.at.off == 0 ? 1 : 0)) * (256 * 130);
+            for (int i = me * 32 + lane; i < p.unit_heads * rows * (D / 4); i += users * 32) {
+                const int quad = i % (D / 4), hr = i / (D / 4), hh = hr / rows, r = hr - hh * rows;
+                float top = -INFINITY, sum = 0.0f;
+                for (int k = 0; k < p.split; k++) top = fmaxf(top, aux.m[hh * p.split + k][r]);
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int k = 0; k < p.split; k++) {
+                    const int at = hh * p.split + k;
+                    const float a = top == -INFINITY ? 0.0f : exp2_fast(aux.m[at][r] - top);
+                    const float4 x = *reinterpret_cast<const float4 *>(joins + (at * F::kRows + r) * F::kPitch + 4 * quad);
+                    sum += aux.l[at][r] * a;
+                    v.x += x.x * a, v.y += x.y * a, v.z += x.z * a, v.w += x.w * a;
+                }
+                finish(hh, r, quad, v, top, sum, whole ? nullptr : mine);
+            }
+            if (!whole) {
+                // ---- the CTA that finishes a cut unit's last piece joins them, in the order of the keys ----
+                const Cut cut(line, w.pos - w.at.off, unit_cost(w.u));
+                __threadfence();
+                if (!sync_all()) break;
+                if (me == 0 && lane == 0) {
+                    int *counter = p.counters + 2 * cut.c0;
+                    const bool last = atomicAdd(counter, 1) == cut.count - 1;
+                    if (last) atomicExch(counter, 0);  // as the next call wants it
+                    __threadfence();
+                    *(volatile int *)&aux.answer = last;
+                }
+                if (!sync_all()) break;
+                if (*(volatile int *)&aux.answer) {
+                    for (int i = me * 32 + lane; i < p.unit_heads * rows * (D / 4); i += users * 32) {
+                        const int quad = i % (D / 4), hr = i / (D / 4), hh = hr / rows, r = hr - hh * rows, at = hh * F::kRows + r;
+                        const int stat = p.unit_heads * F::kRows * D + 2 * at;
+                        float top = -INFINITY, sum = 0.0f;
+                        const auto fragment = [&](int k) { return p.ws + (int64_t)cut.slot(k) * (256 * 130); };
+                        for (int k = 0; k < cut.count; k++) top = fmaxf(top, __ldcg(fragment(k) + stat));
+                        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        for (int k = 0; k < cut.count; k++) {
+                            const float a = top == -INFINITY ? 0.0f : exp2_fast(__ldcg(fragment(k) + stat) - top);
+                            const float4 x = __ldcg(reinterpret_cast<const float4 *>(fragment(k) + at * D) + quad);
+                            sum += __ldcg(fragment(k) + stat + 1) * a;
+                            v.x += x.x * a, v.y += x.y * a, v.z += x.z * a, v.w += x.w * a;
+                        }
+                        finish(hh, r, quad, v, top, sum, nullptr);
+                    }
+                }
+            }
+            if (!sync_all()) break;  // the next unit writes to the join's place
+        } while (w.next(b));
+    }
+    // common exit
+    __syncwarp();
+    __syncthreads();
+    if (aux.gave_up) {  // let copies in flight land before the shared memory is given back
+        const unsigned long long t0 = now_ns();
+        while (now_ns() - t0 < 10000000ull) {}
+    }
+}
+
+template <int D, int NT, bool Bf16>
+int launch_few(FewParams &p, const DeviceInfo *dev, cudaStream_t s)
+{
+    using F = Few<D, NT>;
+    const auto kernel = attention_q4_few_kernel<D, NT, Bf16>;
+    constexpr uint32_t kFixed = ((sizeof(Aux) + 127) & ~127u) + ((F::kJoin + 127) & ~127u), kAll = 227 * 1024;
+    if (dev == nullptr) return cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAll));
+    const int all = p.heads_all;
+    int heads = all < kMaxHeads ? all : kMaxHeads;
+    while (all % heads) heads--;
+    int split = 1;
+    while (2 * split * heads <= F::kWarps) split *= 2;
+    p.unit_heads = heads;
+    p.split = split;
+    p.tile = 16 * split * F::kSteps;
+    // rows 32 or 96 bytes off a multiple of 128 apart
+    const auto pitch = [&](int dim) {
+        const int scales = heads * dim / 16 + (heads < all ? 14 : 0), bytes = heads * dim / 2 + (scales + 15) / 16 * 16;
+        return (bytes + 31) / 64 * 64 + 32;
+    };
+    p.k_pitch = pitch(p.k.dim);
+    p.v_pitch = pitch(p.v.dim);
+    const uint32_t pair = (uint32_t)p.tile * (p.k_pitch + p.v_pitch);
+    p.slots = (int)((kAll - kFixed - 64) / pair);
+    if (p.slots > kMaxSlots) p.slots = kMaxSlots;
+    if (p.slots < 1) return KV_ERR_UNSUPPORTED;
+    p.b.kv_heads = all / heads;
+    p.b.tile_shift = 0;
+    while ((1 << p.b.tile_shift) < p.tile) p.b.tile_shift++;
+    const uint32_t bytes = kFixed + 64 + p.slots * pair;
+    return cuda_status(launch(kernel, dim3(dev->num_sms), dim3(F::kThreads), bytes, s, p));
+}
+
+template <int D>
+int pick_few(int rows, bool bf16, FewParams &p, const DeviceInfo *dev, cudaStream_t s)
+{
+    if (rows <= 8) return bf16 ? launch_few<D, 1, true>(p, dev, s) : launch_few<D, 1, false>(p, dev, s);
+    return bf16 ? launch_few<D, 2, true>(p, dev, s) : launch_few<D, 2, false>(p, dev, s);
+}
+
+}  // namespace
+
+// rows: of a unit, 8 or 16.
+int run_q4_few(bool bf16, const Q4Params &q, const kv_attn_batch *batch, int rows, const DeviceInfo &dev, cudaStream_t s)
+{
+    FewParams p = {};
+    static_cast<Q4Params &>(p) = q;
+    return p.k.dim <= 64 && p.v.dim <= 64 ? pick_few<64>(rows, bf16, p, &dev, s) : pick_few<128>(rows, bf16, p, &dev, s);
+}
+
+int preload_q4_few_kernels()
+{
+    FewParams p = {};
+    for (int rows : {8, 16})
+        for (bool bf : {false, true}) {
+            int st = pick_few<64>(rows, bf, p, nullptr, nullptr);
+            if (st == KV_OK) st = pick_few<128>(rows, bf, p, nullptr, nullptr);
+            if (st != KV_OK) return st;
+        }
+    return load_kernels(attention_q4_few_kernel<64, 1, false>, attention_q4_few_kernel<64, 1, true>, attention_q4_few_kernel<64, 2, false>,
+                        attention_q4_few_kernel<64, 2, true>, attention_q4_few_kernel<128, 1, false>, attention_q4_few_kernel<128, 1, true>,
+                        attention_q4_few_kernel<128, 2, false>, attention_q4_few_kernel<128, 2, true>);
+}
+
+}  // namespace pkv

@@ -96,7 +96,7 @@ int prepare_attention(const DeviceInfo &dev)
     std::lock_guard<std::mutex> lock(mu);
     if (done[dev.device]) return KV_OK;
     for (int (*load)() : {preload_attention_kernels, preload_latent_kernels, preload_expand_kernels, preload_mass_kernels,
-                          preload_evict_kernels}) {
+                          preload_evict_kernels, preload_q4_kernels}) {
         const int st = load();
         if (st != KV_OK) return st;
     }

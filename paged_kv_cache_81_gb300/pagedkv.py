@@ -35,7 +35,7 @@ EXPORTS = ("kv_version", "kv_status_string", "kv_last_cuda_error", "kv_slot_mapp
            "kv_clip_block_lists", "kv_block_hashes", "kv_block_hashes_workspace_bytes", "kv_write_tokens",
            "kv_attention", "kv_attention_workspace_bytes", "kv_latent_attention", "kv_latent_expand", "kv_attention_mass",
            "kv_attention_mass_workspace_bytes", "kv_evict", "kv_rope_frequencies", "kv_rotate", "kv_rotate_write",
-           "kv_q4_row_bytes", "kv_rotate_write_q4")
+           "kv_q4_row_bytes", "kv_rotate_write_q4", "kv_attention_q4")
 
 
 class KvError(RuntimeError):
@@ -194,6 +194,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             "kv_rotate_write": ([N, R, D, i32, i32, D, i32, i32, P], ctypes.c_int),
             "kv_q4_row_bytes": ([i32, i32, ctypes.POINTER(i32)], ctypes.c_int),
             "kv_rotate_write_q4": ([N, R, D, i32, i32, D, i32, i32, f32, f32, P, P, P], ctypes.c_int),
+            "kv_attention_q4": ([A, B, D, i32, i32, D, i32, i32, f32, f32, P, i64, i64, P, i64, i64, P, P, i64, P], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             f = getattr(lib, name)
@@ -998,7 +999,7 @@ def kv_rotate_write_q4(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tens
                        token_req: torch.Tensor, token_pos: torch.Tensor, rope: Optional[Rope], *, v_cache: Optional[PagedCache] = None,
                        k_tensor: int = 0, v_tensor: Optional[int] = None, rope_pos: Optional[torch.Tensor] = None, k_scale: float = 1.0,
                        v_scale: float = 1.0, q_out: Optional[torch.Tensor] = None, held: bool = False, stream=None):
-    """kv_rotate_write into a 4-bit cache; k_scale and v_scale are the tensors' scales.  Returns
+    """kv_rotate_write into a 4-bit cache; k_scale and v_scale are the tensors' scales, which kv_attention_q4 takes too.  Returns
     q_out, or (q_out, keys, values) with what the cache now stands for when `held`."""
     _tensor_numbers(k_tensor, v_tensor or 0)
     d, dev, handle, q_out = _new_tokens(q, k, v, block_table, token_req, token_pos, rope_pos, q_out, stream)
@@ -1009,6 +1010,31 @@ def kv_rotate_write_q4(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tens
         d, _rope_on(dev, rope), k_desc, k_tensor, 0, v_desc, v_tensor, v_plane, k_scale, v_scale, k_held.data_ptr() if held else None,
         v_held.data_ptr() if held else None, handle))
     return (q_out, k_held, v_held) if held else q_out
+
+
+def kv_attention_q4(q: torch.Tensor, cache: PagedCache, block_table: torch.Tensor, q_offsets: torch.Tensor, kv_lens: torch.Tensor,
+                    scale: float, *, kv_heads: int, head_dim_v: Optional[int] = None, v_cache: Optional[PagedCache] = None, k_tensor: int = 0,
+                    v_tensor: Optional[int] = None, k_scale: float = 1.0, v_scale: float = 1.0, causal: bool = True, window: int = 0,
+                    out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """kv_attention over a 4-bit cache that kv_rotate_write_q4 filled; returns (out, lse float32 [tokens, heads]).  kv_heads and
+    head_dim_v (default: q's width) say what a row holds; k_scale and v_scale are the tensors' scales."""
+    _tensor_numbers(k_tensor, v_tensor or 0)
+    code, q_token, q_head = _rows3(q, "q")
+    dev = q.get_device()
+    handle = _begin(dev, stream)
+    k_desc, v_desc, v_tensor, v_plane = _key_and_value_planes(dev, cache, v_cache, k_tensor, v_tensor, torch.uint8)
+    T, H, dk = q.shape
+    dv = dk if head_dim_v is None else head_dim_v
+    _int32(kv_heads=kv_heads, head_dim_v=dv)
+    if dv < 0:
+        raise ValueError("head_dim_v must not be negative")
+    batch = _attn_batch(dev, block_table, q_offsets, kv_lens, T)
+    out, o_token, o_head, lse = _attn_outputs(dev, q, T, H, dv, out, lse, stream)
+    workspace = _workspace(kv_attention_workspace_bytes, dev, handle, workspace, stream)
+    _check("kv_attention_q4", (_lib or load()).kv_attention_q4(
+        _attn_desc(code, H, kv_heads, dk, dv, causal, window, float(scale)), batch, k_desc, k_tensor, 0, v_desc, v_tensor, v_plane, k_scale, v_scale,
+        q.data_ptr(), q_token, q_head, out.data_ptr(), o_token, o_head, lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, handle))
+    return out, lse
 
 
 def default_max_run_blocks(stage_block_bytes: int, target_bytes: int = 16 * 1024) -> int:

@@ -81,7 +81,7 @@ def packed(code, b):
     rows = torch.zeros(t, K.kv_q4_row_bytes(h, d), dtype=torch.uint8)
     flat = code.reshape(t, h * d)
     rows[:, :h * d // 2] = (flat[:, 0::2] | flat[:, 1::2] << 4).to(torch.uint8)
-    rows[:, h * d // 2:h * d // 2 + h * d // 16] = b.reshape(t, -1).to(torch.uint8)
+    rows[:, h * d // 2:h * d // 2 + h * d // 16] = b.reshape(t, h * d // 16).to(torch.uint8)
     return rows
 
 
