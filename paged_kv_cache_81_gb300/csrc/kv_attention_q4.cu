@@ -45,13 +45,14 @@ int kv_attention_q4(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_
     if ((st = prepare_attention(*dev)) != KV_OK) return st;
     p.b.err = dev->err_word;
     const auto plane = [](const kv_cache_desc *c, int tensor, int which, int dim) {
-        return Q4Plane{(const char *)c->base[tensor] + (which ? c->plane_stride : 0), c->block_stride, c->token_stride, c->row_bytes, dim};
+        return Q4Plane{c->base[tensor] + (which ? (uint64_t)c->plane_stride : 0), c, dim};
     };
     p.k = plane(k, k_tensor, k_plane, d->head_dim);
     p.v = plane(v, v_tensor, v_plane, d->head_dim_v);
     p.table = batch->block_table;
     p.table_stride = batch->bt_row_stride;
     p.num_blocks = (int32_t)(k->num_blocks < v->num_blocks ? k->num_blocks : v->num_blocks);
+    p.no_page = (int32_t)(k->num_blocks < v->num_blocks ? v->num_blocks : k->num_blocks);
     p.block = make_fastdiv((uint32_t)k->block_size);
     p.q = (const char *)q;
     p.q_token = q_token_stride;

@@ -8,9 +8,9 @@ namespace pkv {
 
 // A plane of 4-bit rows.
 struct Q4Plane {
-    const char *base;
-    int64_t block_stride, token_stride;
-    int32_t row_bytes, dim;
+    uint64_t base;
+    const kv_cache_desc *desc;  // host
+    int32_t dim;
 };
 
 struct Q4Params {
@@ -19,6 +19,7 @@ struct Q4Params {
     const int32_t *table;
     int64_t table_stride;
     int32_t num_blocks;  // pages that both planes have
+    int32_t no_page;     // a page that neither has: its loads bring zeros
     FastDiv block;       // slots of a page
     const char *q;
     int64_t q_token, q_head;

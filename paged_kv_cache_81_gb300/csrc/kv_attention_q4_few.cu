@@ -13,7 +13,7 @@
 // sums are in 32 bits.
 //
 // One persistent CTA per SM; a unit is one request's rows of up to eight key heads.
-//   warp 0        brings rows of keys and of values, one bulk copy a token (its heads lie together), into a ring of tiles
+//   warp 0        brings rows of keys and of values by tiled TMA, one for each run of slots inside a page, into a ring of tiles
 //   other warps   each one key head and every n-th 16 keys of a tile: scores, weights, values, with a running maximum and sum of
 //                 its own, joined through shared memory at the unit's end
 // Rows lie 32 or 96 bytes off a multiple of 128 apart and the 16 keys of a step are taken in an order (kOrder) in which neither the
@@ -40,34 +40,32 @@ struct Few {
 };
 static_assert(kMaxHeads * Few<128, 2>::kRows <= 256, "a fragment fits its place in the workspace");
 
+// Where a unit's heads of a tile lie in shared memory: rows of codes and of scales, `codes` and `scales` bytes apart.  All heads of
+// a row come together, the scales behind the codes; some of them in two loads, the scales behind all codes of the tile.
+struct Place4 {
+    int32_t codes, scales;
+    int32_t first;  // of the first row's scales
+    int32_t bytes;  // of a tile
+    int32_t apart;  // two loads
+};
+
 struct FewParams : Q4Params {
     int32_t unit_heads;        // key heads of a unit
     int32_t split;             // warps of a key head
     int32_t tile;              // keys
-    int32_t k_pitch, v_pitch;  // bytes of a row in shared memory
     int32_t slots;             // tiles of each ring
+    int32_t piece_rows;        // slots that one TMA brings: they never leave a page
+    Place4 kl, vl;
 };
 
 struct Aux {
     uint64_t k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots], sync;
-    uint32_t k_valid[kMaxSlots][16], v_valid[kMaxSlots][16];  // bit a key of the tile: it is there
     int scan[4 * 17];
     Place place;
     float m[16][16], l[16][16];  // of a warp's rows
     int answer;
     int gave_up;
 };
-
-__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes)
-{
-    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-}
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
@@ -116,75 +114,50 @@ __device__ __forceinline__ uint32_t ld_smem1(uint32_t a)
     return v;
 }
 
-// Where a unit's heads lie in a row, and in a row of shared memory: codes, then (from `rest` on) scales.
-struct Part {
-    uint32_t codes, code_bytes;    // in the row
-    uint32_t scales, scale_bytes;  // 16-byte pieces that hold them
-    uint32_t rest;                 // where the first scale stands in them
-    __device__ __forceinline__ Part(const Q4Plane &p, int all, int heads, int h0)
-    {
-        codes = (uint32_t)h0 * p.dim / 2;
-        code_bytes = (uint32_t)heads * p.dim / 2;
-        const uint32_t s = (uint32_t)all * p.dim / 2 + (uint32_t)h0 * p.dim / 16;
-        scales = s & ~15u;
-        rest = s - scales;
-        scale_bytes = ((s + (uint32_t)heads * p.dim / 16 + 15) & ~15u) - scales;
-    }
-};
-
-// One tile's rows, each token by its own bulk copy, and which of them are there.  `ready` waits for the slot.
+// One tile of rows of keys or values: a TMA (two where heads are apart) for each run of slots inside a page, spread over the lanes.
+// h0: the unit's first head; `ready` waits for the slot.
 template <typename Ready>
-__device__ __forceinline__ bool load_rows(const FewParams &p, const Q4Plane &plane, const Part &part, const int32_t *row, int kb, int lo, int hi,
-                                          uint32_t to, uint32_t pitch, uint32_t bar, volatile uint32_t *valid, bool report, const Ready &ready)
+__device__ __forceinline__ bool load_rows(const FewParams &p, const CUtensorMap *map, const CUtensorMap *scale_map, const Q4Plane &plane,
+                                          const Place4 &place, const int32_t *row, int kb, int lo, int hi, int h0, uint32_t to, uint32_t bar,
+                                          const Ready &ready)
 {
-    const int lane = threadIdx.x & 31;
-    const bool together = part.scales == part.codes + part.code_bytes;
-    const uint32_t bytes = part.code_bytes + part.scale_bytes;
-    const char *from = nullptr;
-    const auto find = [&](int j) {
-        from = nullptr;
-        const int key = kb + j;
-        if (key < lo || key >= hi) return;
-        const uint32_t col = fdiv((uint32_t)key, p.block);
-        const int page = __ldg(row + col);
-        if (page >= 0 && page < p.num_blocks)
-            from = plane.base + (int64_t)page * plane.block_stride + (int64_t)((uint32_t)key - col * p.block.d) * plane.token_stride;
-        else if (report)
+    const int lane = threadIdx.x & 31, pr = p.piece_rows;
+    const int p0 = max(0, lo - kb) / pr, p1 = (min(hi - kb, p.tile) + pr - 1) / pr;
+    int page = 0, slot = 0;
+    const auto find = [&](int i) {
+        const uint32_t key = (uint32_t)(kb + i * pr), col = fdiv(key, p.block);
+        slot = (int)(key - col * p.block.d);
+        page = __ldg(row + col);
+        if (page < 0 || page >= p.num_blocks) {
             set_error(p.b.err, KV_DERR_TABLE);
+            page = p.no_page;
+        }
     };
-    find(lane);
+    if (p0 + lane < p1) find(p0 + lane);
     if (!ready()) return false;
-    for (int j = lane; j < p.tile; j += 32) {
-        if (j >= 32) find(j);
-        const uint32_t there = __ballot_sync(0xffffffffu, from != nullptr);
-        if (lane == 0) {
-            valid[j >> 5] = there;
-            mbar_expect(bar, (uint32_t)__popc(there) * bytes);
-        }
-        __syncwarp();
-        if (from != nullptr) {
-            const uint32_t at = to + (uint32_t)j * pitch;
-            if (together) {
-                bulk_load(at, from + part.codes, bytes, bar);
-            } else {
-                bulk_load(at, from + part.codes, part.code_bytes, bar);
-                bulk_load(at + part.code_bytes, from + part.scales, part.scale_bytes, bar);
-            }
-        }
+    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)((p1 - p0) * pr) * (place.codes + (place.apart ? place.scales : 0)));
+    __syncwarp();
+    for (int i = p0 + lane; i < p1; i += 32) {
+        if (i >= p0 + 32) find(i);
+        tma_load_3d(to + i * pr * place.codes, map, bar, h0 * plane.dim / 8, slot, page);
+        if (place.apart)
+            tma_load_3d(to + place.first + i * pr * place.scales, scale_map, bar, ((p.heads_all * plane.dim / 2 + h0 * plane.dim / 16) & ~15) / 4, slot, page);
     }
-    warp_arrive(bar);
+    __syncwarp();
     return true;
 }
 
 template <int D, int NT, bool Bf16>
-__global__ void __launch_bounds__(Few<D, NT>::kThreads, 1) attention_q4_few_kernel(const __grid_constant__ FewParams p)
+__global__ void __launch_bounds__(Few<D, NT>::kThreads, 1)
+attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap ks_map,
+                        const __grid_constant__ CUtensorMap vs_map, const __grid_constant__ FewParams p)
 {
     using F = Few<D, NT>;
     extern __shared__ __align__(128) unsigned char smem[];
     Aux &aux = *reinterpret_cast<Aux *>(smem);
     float *const joins = reinterpret_cast<float *>(smem + ((sizeof(Aux) + 127) & ~127u));
     const uint32_t ring = smem_addr(joins) + ((F::kJoin + 127) & ~127u);
-    const uint32_t k_bytes = (uint32_t)p.tile * p.k_pitch, v_bytes = (uint32_t)p.tile * p.v_pitch, v_ring = ring + p.slots * k_bytes;
+    const uint32_t v_ring = ring + p.slots * p.kl.bytes;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const Batch &b = p.b;
     const Waiter wait{&aux.gave_up, b.err};
@@ -200,6 +173,8 @@ __global__ void __launch_bounds__(Few<D, NT>::kThreads, 1) attention_q4_few_kern
         }
         mbar_init(smem_addr(&aux.sync), users);
         mbar_init_fence();
+        tma_prefetch_map(&k_map);
+        tma_prefetch_map(&v_map);
     }
     grid_dep_entry();
     const Line line = find_place<F::kThreads>(b, blockIdx.x, gridDim.x, kLeast, aux.scan, &aux.place, blockIdx.x == 0);
@@ -214,13 +189,13 @@ __global__ void __launch_bounds__(Few<D, NT>::kThreads, 1) attention_q4_few_kern
         do {
             if (w.u.tiles == 0) continue;
             const int32_t *row = p.table + (int64_t)w.at.req * p.table_stride;
-            const Part kp(p.k, p.heads_all, p.unit_heads, w.at.head * p.unit_heads), vp(p.v, p.heads_all, p.unit_heads, w.at.head * p.unit_heads);
+            const int h0 = w.at.head * p.unit_heads;
             for (int t = 0; ok && t < w.n; t++, it++) {
                 const int s = it % p.slots, kb = (w.u.tile0 + w.at.off + t) << b.tile_shift;
                 const uint32_t phase = (uint32_t)(it / p.slots - 1) & 1;
-                ok = load_rows(p, p.k, kp, row, kb, w.u.lo, w.u.hi, ring + s * k_bytes, p.k_pitch, smem_addr(&aux.k_full[s]), aux.k_valid[s], true,
+                ok = load_rows(p, &k_map, &ks_map, p.k, p.kl, row, kb, w.u.lo, w.u.hi, h0, ring + s * p.kl.bytes, smem_addr(&aux.k_full[s]),
                                [&] { return it < p.slots || wait.warp(smem_addr(&aux.k_empty[s]), phase); }) &&
-                     load_rows(p, p.v, vp, row, kb, w.u.lo, w.u.hi, v_ring + s * v_bytes, p.v_pitch, smem_addr(&aux.v_full[s]), aux.v_valid[s], false,
+                     load_rows(p, &v_map, &vs_map, p.v, p.vl, row, kb, w.u.lo, w.u.hi, h0, v_ring + s * p.vl.bytes, smem_addr(&aux.v_full[s]),
                                [&] { return it < p.slots || wait.warp(smem_addr(&aux.v_empty[s]), phase); });
             }
         } while (ok && w.next(b));
@@ -317,9 +292,11 @@ __global__ void __launch_bounds__(Few<D, NT>::kThreads, 1) attention_q4_few_kern
                 m[x][0] = m[x][1] = -INFINITY;
                 l[x][0] = l[x][1] = 0.0f;
             }
-            const Part kp(p.k, p.heads_all, p.unit_heads, head0), vp(p.v, p.heads_all, p.unit_heads, head0);
-            const uint32_t k_code = h * p.k.dim / 2 + t * (D / 8), k_unit = kp.code_bytes + kp.rest + h * p.k.dim / 16 + (D == 128 ? 2 * t : t);
-            const uint32_t v_code = h * p.v.dim / 2 + n * (D / 16), v_unit = vp.code_bytes + vp.rest + h * p.v.dim / 16 + (D == 128 ? n : n / 2);
+            const uint32_t seen = (uint32_t)(w.u.hi - w.u.lo);
+            // where this thread's codes and scales lie in a row; scales of heads that come apart begin off a 16-byte boundary
+            const auto rest = [&](int dim) { return (p.heads_all * dim / 2 + head0 * dim / 16) & 15; };
+            const uint32_t k_code = h * p.k.dim / 2 + t * (D / 8), k_unit = p.kl.first + rest(p.k.dim) + h * p.k.dim / 16 + (D == 128 ? 2 * t : t);
+            const uint32_t v_code = h * p.v.dim / 2 + n * (D / 16), v_unit = p.vl.first + rest(p.v.dim) + h * p.v.dim / 16 + (D == 128 ? n : n / 2);
             for (int tile = 0; tile < w.n; tile++, it++) {
                 const int s = it % p.slots, kb = (w.u.tile0 + w.at.off + tile) << b.tile_shift;
                 const uint32_t phase = (uint32_t)(it / p.slots) & 1;
@@ -333,22 +310,23 @@ __global__ void __launch_bounds__(Few<D, NT>::kThreads, 1) attention_q4_few_kern
 #pragma unroll
                         for (int j = 0; j < 4; j++) sc[step][x][j] = 0.0f;
                     const int g = part + step * p.split;  // of the tile's groups of 16 keys
-                    const uint32_t there = aux.k_valid[s][g >> 1] >> (16 * (g & 1));
-                    const uint32_t r0 = ring + s * k_bytes + (uint32_t)(16 * g + rk) * p.k_pitch, r1 = r0 + 8u * p.k_pitch;
-                    const bool is0 = there >> rk & 1, is1 = there >> (rk + 8) & 1;
+                    const uint32_t at = ring + s * p.kl.bytes, j0 = 16 * g + rk, j1 = j0 + 8;
+                    const uint32_t r0 = at + j0 * p.kl.codes + k_code, r1 = at + j1 * p.kl.codes + k_code;
+                    const uint32_t y0 = at + j0 * p.kl.scales + k_unit, y1 = at + j1 * p.kl.scales + k_unit;
+                    const bool is0 = (uint32_t)(kb + (int)j0 - w.u.lo) < seen, is1 = (uint32_t)(kb + (int)j1 - w.u.lo) < seen;
                     uint32_t w0[D / 32], w1[D / 32], u0, u1;
                     if (D == 128) {
-                        const uint4 a = ld_smem16(r0 + k_code), d = ld_smem16(r1 + k_code);
+                        const uint4 a = ld_smem16(r0), d = ld_smem16(r1);
                         w0[0] = a.x, w0[1] = a.y, w0[D / 32 - 2] = a.z, w0[D / 32 - 1] = a.w;
                         w1[0] = d.x, w1[1] = d.y, w1[D / 32 - 2] = d.z, w1[D / 32 - 1] = d.w;
-                        u0 = ld_smem2(r0 + k_unit), u1 = ld_smem2(r1 + k_unit);
+                        u0 = ld_smem2(y0), u1 = ld_smem2(y1);
                         if (!k_has1) u0 &= 0xff, u1 &= 0xff;
                     } else {
-                        const uint2 a = ld_smem8(r0 + k_code), d = ld_smem8(r1 + k_code);
+                        const uint2 a = ld_smem8(r0), d = ld_smem8(r1);
                         w0[0] = a.x, w0[1] = a.y, w1[0] = d.x, w1[1] = d.y;
-                        u0 = ld_smem1(r0 + k_unit), u1 = ld_smem1(r1 + k_unit);
+                        u0 = ld_smem1(y0), u1 = ld_smem1(y1);
                     }
-                    // what is not there counts as zeros
+                    // what no row sees counts as zeros: it may hold anything
                     u0 = e4m3x2_to_f16(is0 && k_has0 ? u0 : 0), u1 = e4m3x2_to_f16(is1 && k_has0 ? u1 : 0);
 #pragma unroll
                     for (int i = 0; i < D / 32; i++) {
@@ -433,21 +411,20 @@ __global__ void __launch_bounds__(Few<D, NT>::kThreads, 1) attention_q4_few_kern
 #pragma unroll
                 for (int step = 0; step < F::kSteps; step++) {
                     const int g = part + step * p.split;
-                    const uint32_t there = aux.v_valid[s][g >> 1] >> (16 * (g & 1));
-                    const uint32_t at = v_ring + s * v_bytes + (uint32_t)(16 * g) * p.v_pitch;
-                    const uint32_t key[4] = {ra, rb, ra + 8, rb + 8};
+                    const uint32_t at = v_ring + s * p.vl.bytes, g16 = 16 * g;
+                    const uint32_t key[4] = {g16 + ra, g16 + rb, g16 + ra + 8, g16 + rb + 8};
                     uint32_t cw[4][D / 64], unit[4];
 #pragma unroll
                     for (int j = 0; j < 4; j++) {
-                        const uint32_t row = at + key[j] * p.v_pitch;
+                        const uint32_t row = at + key[j] * p.vl.codes + v_code;
                         if (D == 128) {
-                            const uint2 x = ld_smem8(row + v_code);
+                            const uint2 x = ld_smem8(row);
                             cw[j][0] = x.x, cw[j][D / 64 - 1] = x.y;
                         } else {
-                            cw[j][0] = ld_smem4(row + v_code);
+                            cw[j][0] = ld_smem4(row);
                         }
-                        unit[j] = ld_smem1(row + v_unit);
-                        if (!(there >> key[j] & 1) || !v_has) unit[j] = 0;
+                        unit[j] = ld_smem1(at + key[j] * p.vl.scales + v_unit);
+                        if ((uint32_t)(kb + (int)key[j] - w.u.lo) >= seen || !v_has) unit[j] = 0;
                     }
                     const uint32_t z0 = e4m3x2_to_f16(unit[0] | unit[1] << 8), z1 = e4m3x2_to_f16(unit[2] | unit[3] << 8);
 #pragma unroll
@@ -587,22 +564,47 @@ int launch_few(FewParams &p, const DeviceInfo *dev, cudaStream_t s)
     p.unit_heads = heads;
     p.split = split;
     p.tile = 16 * split * F::kSteps;
-    // rows 32 or 96 bytes off a multiple of 128 apart
-    const auto pitch = [&](int dim) {
-        const int scales = heads * dim / 16 + (heads < all ? 14 : 0), bytes = heads * dim / 2 + (scales + 15) / 16 * 16;
-        return (bytes + 31) / 64 * 64 + 32;
+    p.piece_rows = piece_rows(p.k.desc->block_size, p.tile < 256 ? p.tile : 256);
+    // A run of rows ends on a multiple of 128 bytes, where a TMA may begin; its rows lie 32 or 96 bytes off one where that allows it.
+    const auto pitch = [&](int bytes) {
+        const int step = p.piece_rows >= 4 ? 64 : 128 / p.piece_rows, off = p.piece_rows >= 4 ? 32 : 0;
+        return (bytes - off + step - 1) / step * step + off;
     };
-    p.k_pitch = pitch(p.k.dim);
-    p.v_pitch = pitch(p.v.dim);
-    const uint32_t pair = (uint32_t)p.tile * (p.k_pitch + p.v_pitch);
-    p.slots = (int)((kAll - kFixed - 64) / pair);
+    const auto place = [&](int dim) {
+        Place4 l = {};
+        const int codes = heads * dim / 2;
+        l.apart = heads < all;
+        if (l.apart) {
+            l.codes = pitch(codes);
+            l.scales = pitch((heads * dim / 16 + 14 + 15) / 16 * 16);
+            l.first = p.tile * l.codes;
+            l.bytes = p.tile * (l.codes + l.scales);
+        } else {
+            l.codes = l.scales = pitch((int)q4_row_bytes(heads, dim));
+            l.first = codes;
+            l.bytes = p.tile * l.codes;
+        }
+        return l;
+    };
+    p.kl = place(p.k.dim);
+    p.vl = place(p.v.dim);
+    const uint32_t pair = (uint32_t)(p.kl.bytes + p.vl.bytes);
+    p.slots = (int)((kAll - kFixed - 128) / pair);
     if (p.slots > kMaxSlots) p.slots = kMaxSlots;
     if (p.slots < 1) return KV_ERR_UNSUPPORTED;
+    CUtensorMap map[4];
+    int st;
+    if ((st = make_row_map(&map[0], p.k.base, p.k.desc, p.kl.codes, p.piece_rows)) != KV_OK) return st;
+    if ((st = make_row_map(&map[1], p.v.base, p.v.desc, p.vl.codes, p.piece_rows)) != KV_OK) return st;
+    map[2] = map[0], map[3] = map[1];
+    if (heads < all && ((st = make_row_map(&map[2], p.k.base, p.k.desc, p.kl.scales, p.piece_rows)) != KV_OK ||
+                        (st = make_row_map(&map[3], p.v.base, p.v.desc, p.vl.scales, p.piece_rows)) != KV_OK))
+        return st;
     p.b.kv_heads = all / heads;
     p.b.tile_shift = 0;
     while ((1 << p.b.tile_shift) < p.tile) p.b.tile_shift++;
-    const uint32_t bytes = kFixed + 64 + p.slots * pair;
-    return cuda_status(launch(kernel, dim3(dev->num_sms), dim3(F::kThreads), bytes, s, p));
+    const uint32_t bytes = kFixed + 128 + p.slots * pair;
+    return cuda_status(launch(kernel, dim3(dev->num_sms), dim3(F::kThreads), bytes, s, map[0], map[1], map[2], map[3], p));
 }
 
 template <int D>
