@@ -15,7 +15,8 @@
 // One persistent CTA per SM; a unit is one request's rows of up to eight key heads.
 //   warp 0        brings rows of keys and of values by tiled TMA, one for each run of slots inside a page, into rings of tiles
 //   other warps   each one key head and every n-th 16 keys of a tile: scores, weights, values, with a running maximum and sum of
-//                 its own, joined through shared memory at the unit's end
+//                 its own; at the unit's end the first warp of a head joins the others' through shared memory, and through
+//                 the workspace where a unit is cut, while they go on with the next
 // Rows lie 32 or 96 bytes off a multiple of 128 apart and the 16 keys of a step are taken in an order (kOrder) in which neither the
 // keys' 16-byte nor the values' 8-byte reads meet in a bank.
 #include "kv_attention_q4.cuh"
@@ -26,21 +27,19 @@ namespace {
 
 constexpr int kLeast = 2;     // tiles of a piece of a unit, at least
 constexpr int kMaxHeads = 8;  // key heads of a unit
-constexpr int kMaxSlots = 4;
+constexpr int kMaxSlots = 8;
+constexpr int kMany = 12;     // pieces of a unit from which on they are joined in two stages
 constexpr uint32_t kOrder = 0x57463120u;  // key of row r of 8: hexadecimal digit r
 
 template <int D, int NT>
 struct Few {
     static constexpr int kWarps = NT == 1 ? 16 : 8;  // that compute
     static constexpr int kThreads = 32 * (kWarps + 1);
-    static constexpr int kRows = 8 * NT;
     static constexpr int kSteps = NT == 1 ? 2 : 4;   // groups of 16 keys that a warp takes of a tile
-    static constexpr int kPitch = D + 4;             // floats of a row in the join
-    static constexpr uint32_t kJoin = (uint32_t)kWarps * kRows * kPitch * 4;
+    static constexpr uint32_t kQ = NT * (D / 32) * 512;  // bytes of a warp's queries
     // bytes between a tile's rows of H heads of D, 32 off a multiple of 64
     static constexpr uint32_t pitch(int h) { return (uint32_t)((h * D * 9 + 255) / 256 * 16 - 32 + 63) / 64 * 64 + 32; }
 };
-static_assert(kMaxHeads * Few<128, 2>::kRows <= 256, "a fragment fits its place in the workspace");
 
 // Where a unit's heads of a tile lie in shared memory: rows of codes and of scales, `codes` and `scales` bytes apart.  All heads of
 // a row come together, the scales behind the codes; some of them in two loads, the scales behind all codes of the tile.
@@ -62,12 +61,11 @@ struct FewParams : Q4Params {
 };
 
 struct Aux {
-    uint64_t k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots], sync;
+    uint64_t k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots];
+    uint64_t join_full[kMaxHeads], join_free[kMaxHeads];  // a head's other warps have left their sums; its first has read them
     int scan[4 * 17];
     Place place;
     Walk walk[17];  // of each warp: held in registers it would crowd the loop over the tiles
-    float m[16][16], l[16][16];  // of a warp's rows
-    int answer;
     int gave_up;
 };
 
@@ -128,77 +126,127 @@ __device__ __forceinline__ bool next_of(Walk &shared, const Batch &b)
     return more;
 }
 
-// One tile of rows of keys or values: a TMA (two where heads are apart) for each run of slots inside a page, spread over the lanes.
-// h0: the unit's first head; `ready` waits for the slot.
-template <typename Ready>
-__device__ __forceinline__ bool load_rows(const FewParams &p, const CUtensorMap *map, const CUtensorMap *scale_map, int dim, const Place4 &place,
-                                          const int32_t *row, int kb, int lo, int hi, int h0, uint32_t to, uint32_t bar, const Ready &ready)
-{
-    const int lane = threadIdx.x & 31, pr = p.piece_rows;
-    const int p0 = max(0, lo - kb) / pr, p1 = (min(hi - kb, p.tile) + pr - 1) / pr;
-    int page = 0, slot = 0;
-    const auto find = [&](int i) {
-        const uint32_t key = (uint32_t)(kb + i * pr), col = fdiv(key, p.block);
+// A tile as the loading warp sees it: the runs of slots inside a page that it takes, one a lane (and every 32nd after it), and the
+// page of the lane's first one, asked for a tile ahead: a trip to the block table takes as long as half a tile's work.
+struct Tile {
+    const int32_t *row;
+    int kb, h0, p0, p1;
+    int page, slot;
+
+    __device__ __forceinline__ void look(const FewParams &p, int i)
+    {
+        const uint32_t key = (uint32_t)(kb + i * p.piece_rows), col = fdiv(key, p.block);
         slot = (int)(key - col * p.block.d);
         page = __ldg(row + col);
-        if (page < 0 || page >= p.num_blocks) {
-            set_error(p.b.err, KV_DERR_TABLE);
-            page = p.no_page;
-        }
-    };
-    if (p0 + lane < p1) find(p0 + lane);
-    if (!ready()) return false;
-    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)((p1 - p0) * pr) * (place.codes + (place.apart ? place.scales : 0)));
-    __syncwarp();
-    for (int i = p0 + lane; i < p1; i += 32) {
-        if (i >= p0 + 32) find(i);
-        tma_load_3d(to + i * pr * place.codes, map, bar, h0 * dim / 8, slot, page);
-        if (place.apart)
-            tma_load_3d(to + place.first + i * pr * place.scales, scale_map, bar, ((p.heads_all * dim / 2 + h0 * dim / 16) & ~15) / 4, slot, page);
     }
-    __syncwarp();
-    return true;
-}
-
-// Pieces (O [head, row][D], then a maximum and a sum a row) of rows that some part holds, for join_pieces.
-struct Q4Pieces {
-    const float *first;  // the first piece
-    int64_t second;      // floats from it to the second one
-    int64_t apart;       // between the others
-    int count;
-    __device__ __forceinline__ const float *operator()(int i) const { return first + (i == 0 ? 0 : second + (i - 1) * apart); }
+    __device__ __forceinline__ void start(const FewParams &p, const Walk &w, int t, int tile_keys, int heads)
+    {
+        row = p.table + (int64_t)w.at.req * p.table_stride;
+        kb = (w.u.tile0 + w.at.off + t) * tile_keys;
+        h0 = w.at.head * heads;
+        p0 = max(0, w.u.lo - kb) / p.piece_rows;
+        p1 = (min(w.u.hi - kb, tile_keys) + p.piece_rows - 1) / p.piece_rows;
+        const int i = p0 + (threadIdx.x & 31);
+        if (i < p1) look(p, i);
+    }
+    // Its rows of keys or values: a TMA (two where heads are apart) a run.
+    __device__ __forceinline__ void load(const FewParams &p, const CUtensorMap *map, const CUtensorMap *scale_map, int dim, const Place4 &place, uint32_t to,
+                                         uint32_t bar)
+    {
+        const int lane = threadIdx.x & 31, pr = p.piece_rows;
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)((p1 - p0) * pr) * (place.codes + (place.apart ? place.scales : 0)));
+        __syncwarp();
+        for (int i = p0 + lane; i < p1; i += 32) {
+            if (p1 - p0 > 32) look(p, i);
+            int from = page;
+            if (from < 0 || from >= p.num_blocks) {
+                set_error(p.b.err, KV_DERR_TABLE);
+                from = p.no_page;
+            }
+            tma_load_3d(to + i * pr * place.codes, map, bar, h0 * dim / 8, slot, from);
+            if (place.apart)
+                tma_load_3d(to + place.first + i * pr * place.scales, scale_map, bar, ((p.heads_all * dim / 2 + h0 * dim / 16) & ~15) / 4, slot, from);
+        }
+        __syncwarp();
+    }
 };
 
-// Four columns of a row of all pieces, in their order: eight pieces' loads in flight.
-template <int D>
-__device__ __forceinline__ float4 join_pieces(const Q4Pieces &at, int row, int quad, int stats, float &top, float &sum)
-{
-    top = -INFINITY, sum = 0.0f;
-#pragma unroll 8
-    for (int i = 0; i < at.count; i++) top = fmaxf(top, __ldcg(at(i) + stats + 2 * row));
-    const float z = top == -INFINITY ? 0.0f : top;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 1
-    for (int i0 = 0; i0 < at.count; i0 += 8) {
-        float4 x[8];
-        float2 ml[8];
+// One warp's sums over some keys, as its threads hold them: O in 16-byte pieces, then a maximum and a sum a column, all 32 lanes'
+// side by side.  A warp that joins a head's sums holds them alike.
+template <int D, int NT>
+struct Sums {
+    static constexpr int kPieces = NT * 2 * (D / 32);  // of 512 bytes
+    static constexpr int kFloats = kPieces * 128 + NT * 2 * 64;
+    float o[D / 16][NT][4];
+    float m[NT][2], l[NT][2];
+
+    // f(16 bytes of O, where they go), f(maximum and sum, where they go): the columns of rows below `rows`
+    template <typename F4, typename F2>
+    __device__ __forceinline__ void store(float *at, int rows, const F4 &f4, const F2 &f2) const
+    {
+        const int lane = threadIdx.x & 31, t = lane & 3;
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f), ml[i] = make_float2(-INFINITY, 0.0f);
-            if (i0 + i < at.count) {
-                x[i] = __ldcg(reinterpret_cast<const float4 *>(at(i0 + i) + row * D) + quad);
-                ml[i] = __ldcg(reinterpret_cast<const float2 *>(at(i0 + i) + stats + 2 * row));
-            }
-        }
+        for (int x = 0; x < NT; x++)
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const float a = exp2_fast(ml[i].x - z);
-            sum += ml[i].y * a;
-            v.x += x[i].x * a, v.y += x[i].y * a, v.z += x[i].z * a, v.w += x[i].w * a;
-        }
+            for (int i = 0; i < 2; i++)
+                if (8 * x + 2 * t + i < rows) {
+#pragma unroll
+                    for (int k = 0; k < D / 32; k++)
+                        f4(reinterpret_cast<float4 *>(at) + ((x * 2 + i) * (D / 32) + k) * 32 + lane,
+                           make_float4(o[2 * k][x][i], o[2 * k][x][i + 2], o[2 * k + 1][x][i], o[2 * k + 1][x][i + 2]));
+                    f2(reinterpret_cast<float2 *>(at + kPieces * 128) + (x * 2 + i) * 32 + lane, make_float2(m[x][i], l[x][i]));
+                }
     }
-    return v;
-}
+    __device__ __forceinline__ void store_shared(float *at, int rows) const
+    {
+        store(at, rows, [](float4 *p, float4 v) { *p = v; }, [](float2 *p, float2 v) { *p = v; });
+    }
+    __device__ __forceinline__ void store_global(float *at, int rows) const
+    {
+        store(at, rows, [](float4 *p, float4 v) { __stcg(p, v); }, [](float2 *p, float2 v) { __stcg(p, v); });
+    }
+    // This and `count` more, in their order: at(i) is the i-th.  Own: without this, which is overwritten.
+    template <bool Own, typename At>
+    __device__ __forceinline__ void join(const At &at, int count, int rows)
+    {
+        const int lane = threadIdx.x & 31, t = lane & 3;
+#pragma unroll
+        for (int x = 0; x < NT; x++)
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                const int col = x * 2 + i;
+                const bool live = 8 * x + 2 * t + i < rows;
+                const auto stats = [&](int k) { return Own ? reinterpret_cast<const float2 *>(at(k) + kPieces * 128)[col * 32 + lane]
+                                                           : __ldcg(reinterpret_cast<const float2 *>(at(k) + kPieces * 128) + col * 32 + lane); };
+                float top = Own ? m[x][i] : -INFINITY;
+#pragma unroll 4
+                for (int k = 0; k < count; k++) top = fmaxf(top, live ? stats(k).x : -INFINITY);
+                const float z = top == -INFINITY ? 0.0f : top, a = Own ? exp2_fast(m[x][i] - z) : 0.0f;
+                m[x][i] = top;
+                l[x][i] = Own ? l[x][i] * a : 0.0f;
+#pragma unroll
+                for (int k = 0; k < D / 16; k++) o[k][x][i] = Own ? o[k][x][i] * a : 0.0f, o[k][x][i + 2] = Own ? o[k][x][i + 2] * a : 0.0f;
+                if (!live) continue;
+#pragma unroll 2
+                for (int k = 0; k < count; k++) {
+                    const float2 ml = stats(k);
+                    const float4 *from = reinterpret_cast<const float4 *>(at(k)) + col * (D / 32) * 32 + lane;
+                    float4 v[D / 32];
+#pragma unroll
+                    for (int j = 0; j < D / 32; j++) v[j] = Own ? from[j * 32] : __ldcg(from + j * 32);
+                    const float f = exp2_fast(ml.x - z);
+                    l[x][i] += ml.y * f;
+#pragma unroll
+                    for (int j = 0; j < D / 32; j++) {
+                        o[2 * j][x][i] += v[j].x * f, o[2 * j][x][i + 2] += v[j].y * f;
+                        o[2 * j + 1][x][i] += v[j].z * f, o[2 * j + 1][x][i + 2] += v[j].w * f;
+                    }
+                }
+            }
+    }
+};
+
+static_assert(kMaxHeads * Sums<128, 2>::kFloats <= 256 * 130, "a piece fits its place in the workspace");
 
 // H: the unit's heads where they are all of a row's and fill the widths D, and pages have runs of four slots or more (rows then lie
 // a constant distance apart), else 0.
@@ -210,12 +258,6 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     using F = Few<D, NT>;
     extern __shared__ __align__(128) unsigned char smem[];
     Aux &aux = *reinterpret_cast<Aux *>(smem);
-    float *const joins = reinterpret_cast<float *>(smem + ((sizeof(Aux) + 127) & ~127u));
-    const uint32_t ring = smem_addr(joins) + ((F::kJoin + 127) & ~127u);
-    const uint32_t v_ring = ring + (uint32_t)p.slots * p.kl.bytes;
-    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const Batch &b = p.b;
-    const Waiter wait{&aux.gave_up, b.err};
     const bool bf16 = p.bf16;
     const int heads = H ? H : p.unit_heads, split = H ? F::kWarps / H : p.split, users = heads * split;  // warps that compute: users
     const int dk = H ? D : p.k.dim, dv = H ? D : p.v.dim, tile_keys = 16 * split * F::kSteps;
@@ -223,6 +265,13 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     const uint32_t k_row = H ? kPitch : p.kl.codes, y_row = H ? kPitch : p.kl.scales, v_row = H ? kPitch : p.vl.codes, x_row = H ? kPitch : p.vl.scales;
     const uint32_t k_tile = H ? kPitch * tile_keys : p.kl.bytes, v_tile = H ? kPitch * tile_keys : p.vl.bytes;
 
+    unsigned char *const queries = smem + ((sizeof(Aux) + 127) & ~127u);
+    float *const joins = reinterpret_cast<float *>(queries + F::kWarps * F::kQ);
+    const uint32_t ring = smem_addr(joins) + (uint32_t)(users - heads) * Sums<D, NT>::kFloats * 4;
+    const uint32_t v_ring = ring + (uint32_t)p.slots * p.kl.bytes;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const Batch &b = p.b;
+    const Waiter wait{&aux.gave_up, b.err};
     if (tid == 0) {
         aux.gave_up = 0;
         for (int i = 0; i < p.slots; i++) {
@@ -231,7 +280,10 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
             mbar_init(smem_addr(&aux.k_empty[i]), users);
             mbar_init(smem_addr(&aux.v_empty[i]), users);
         }
-        mbar_init(smem_addr(&aux.sync), users);
+        for (int i = 0; i < heads; i++) {
+            mbar_init(smem_addr(&aux.join_full[i]), max(split - 1, 1));
+            mbar_init(smem_addr(&aux.join_free[i]), 1);
+        }
         mbar_init_fence();
         tma_prefetch_map(&k_map);
         tma_prefetch_map(&v_map);
@@ -248,23 +300,29 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
         // nothing to do: on to the common exit
     } else if (warp == 0) {
         // ---- rows of keys and values ----
-        int it = 0;
-        bool ok = true;
-        do {
-            const int32_t *row = p.table + (int64_t)w.at.req * p.table_stride;
-            const int h0 = w.at.head * heads;
-            for (int t = 0; ok && t < w.n && w.u.tiles > 0; t++, it++) {
-                const int s = it % p.slots, kb = (w.u.tile0 + w.at.off + t) << b.tile_shift;
-                const uint32_t phase = (uint32_t)(it / p.slots - 1) & 1;
-                ok = load_rows(p, &k_map, &ks_map, p.k.dim, p.kl, row, kb, w.u.lo, w.u.hi, h0, ring + s * p.kl.bytes, smem_addr(&aux.k_full[s]),
-                               [&] { return it < p.slots || wait.warp(smem_addr(&aux.k_empty[s]), phase); }) &&
-                     load_rows(p, &v_map, &vs_map, p.v.dim, p.vl, row, kb, w.u.lo, w.u.hi, h0, v_ring + s * p.vl.bytes, smem_addr(&aux.v_full[s]),
-                               [&] { return it < p.slots || wait.warp(smem_addr(&aux.v_empty[s]), phase); });
+        int it = 0, s = 0, at = 0;
+        uint32_t phase = 1;
+        Tile tile, next;
+        // the tile after the one that `to` was called for last
+        const auto ahead = [&](Tile &to) {
+            while (at >= first.n || first.u.tiles == 0) {
+                at = 0;
+                if (!first.next(b)) return false;
             }
-            __syncwarp();
-            if (ok) ok = next_of(w, b);
-            __syncwarp();
-        } while (ok);
+            to.start(p, first, at++, tile_keys, heads);
+            return true;
+        };
+        bool more = ahead(next);
+        while (more) {
+            tile = next;
+            more = ahead(next);
+            if (it >= p.slots && !wait.warp(smem_addr(&aux.k_empty[s]), phase)) break;
+            tile.load(p, &k_map, &ks_map, p.k.dim, p.kl, ring + s * k_tile, smem_addr(&aux.k_full[s]));
+            if (it >= p.slots && !wait.warp(smem_addr(&aux.v_empty[s]), phase)) break;
+            tile.load(p, &v_map, &vs_map, p.v.dim, p.vl, v_ring + s * v_tile, smem_addr(&aux.v_full[s]));
+            it++;
+            if (++s == p.slots) s = 0, phase ^= 1;
+        }
     } else if (warp <= users) {
         const int me = warp - 1, h = me / split, part = me - h * split;
         bool ok = true;
@@ -275,12 +333,12 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
         // this thread's scales in a word of them; dimensions that heads do not have count as zeros
         const uint32_t k_mask = t * (D / 4) >= dk ? 0u : D == 128 && t * (D / 4) + 16 < dk ? 0xffffu : 0xffu;
         const uint32_t v_mask = n * (D / 8) < dv ? 0xffu : 0u;
-        int it = 0, syncs = 0;
-        const auto sync_all = [&] {
-            warp_arrive(smem_addr(&aux.sync));
-            ok = wait.warp(smem_addr(&aux.sync), syncs++ & 1);
-            return ok;
-        };
+        int s = 0, joined = 0;
+        uint32_t phase = 0;
+        Sums<D, NT> sums;
+        auto &o = sums.o;
+        auto &m = sums.m;
+        auto &l = sums.l;
         const auto next_unit = [&] {
             __syncwarp();
             const bool more = next_of(w, b);
@@ -308,7 +366,8 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
                 continue;
             }
             // ---- queries: row n (and n + 8) of the unit, this thread's quarter of the dimensions ----
-            uint32_t qf[NT][D / 16][2];
+            // as the products take it, 16 bytes a thread for two of them
+            const uint32_t q_at = smem_addr(queries) + me * F::kQ + lane * 16;
             float c[NT][2];  // of the columns 2 t, 2 t + 1: log2 of a weight a unit of the products
 #pragma unroll
             for (int x = 0; x < NT; x++) {
@@ -343,17 +402,15 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
 #pragma unroll
                 for (int i = 0; i < D / 32; i++) {
                     const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                    uint32_t f[4];
 #pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        qf[x][2 * i + (j >> 1)][j & 1] =
-                            bf16 ? pack2<false>(__uint_as_float(v[j] << 16) * to, __uint_as_float(v[j] & 0xffff0000u) * to) : v[j];
+                    for (int j = 0; j < 4; j++) f[j] = bf16 ? pack2<false>(__uint_as_float(v[j] << 16) * to, __uint_as_float(v[j] & 0xffff0000u) * to) : v[j];
+                    st_smem16(q_at + (x * (D / 32) + i) * 512, make_uint4(f[0], f[1], f[2], f[3]));
                 }
 #pragma unroll
                 for (int i = 0; i < 2; i++)  // a normal number: a hidden score, -inf, stays that in the product with it
                     c[x][i] = fminf(fmaxf(p.o.c * __shfl_sync(0xffffffffu, back, (2 * t + i) * 4), 0x1p-126f), 0x1p127f);
             }
-            float o[D / 16][NT][4];
-            float m[NT][2], l[NT][2];
 #pragma unroll
             for (int x = 0; x < NT; x++) {
 #pragma unroll
@@ -375,13 +432,14 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
             sees(b, w.q, (int)fdiv((uint32_t)(w.u.row0 + rows - 1), b.group), clean_lo, other);
             sees(b, w.q, (int)fdiv((uint32_t)w.u.row0, b.group), other, clean_hi);
             // One tile; Hide: some row does not see all of it.
-            const auto work = [&](auto hide, int kb, int s, uint32_t phase) {
+            const auto work = [&](auto hide, int kb) {
                 constexpr bool kHide = decltype(hide)::value;
                 const auto unseen = [&](int key) { return key < seen_lo || key >= seen_hi; };
                 if (!wait.warp(smem_addr(&aux.k_full[s]), phase)) return false;
                 // ---- scores: S^T of 16 keys by 8 rows a step ----
                 const uint32_t kp = k_at + s * k_tile, yp = y_at + s * k_tile;
                 float sc[F::kSteps][NT][4];
+                uint32_t w0[F::kSteps][D / 32], w1[F::kSteps][D / 32], u0[F::kSteps], u1[F::kSteps];
 #pragma unroll
                 for (int step = 0; step < F::kSteps; step++) {
 #pragma unroll
@@ -390,36 +448,42 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
                         for (int j = 0; j < 4; j++) sc[step][x][j] = 0.0f;
                     const uint32_t r0 = kp + step * 16 * split * k_row, r1 = r0 + 8 * k_row;
                     const uint32_t y0 = yp + step * 16 * split * y_row, y1 = y0 + 8 * y_row;
-                    uint32_t w0[D / 32], w1[D / 32], u0, u1;
                     if (D == 128) {
                         const uint4 a = ld_smem16(r0), d = ld_smem16(r1);
-                        w0[0] = a.x, w0[1] = a.y, w0[D / 32 - 2] = a.z, w0[D / 32 - 1] = a.w;
-                        w1[0] = d.x, w1[1] = d.y, w1[D / 32 - 2] = d.z, w1[D / 32 - 1] = d.w;
-                        u0 = ld_smem2(y0), u1 = ld_smem2(y1);
+                        w0[step][0] = a.x, w0[step][1] = a.y, w0[step][D / 32 - 2] = a.z, w0[step][D / 32 - 1] = a.w;
+                        w1[step][0] = d.x, w1[step][1] = d.y, w1[step][D / 32 - 2] = d.z, w1[step][D / 32 - 1] = d.w;
+                        u0[step] = ld_smem2(y0), u1[step] = ld_smem2(y1);
                     } else {
                         const uint2 a = ld_smem8(r0), d = ld_smem8(r1);
-                        w0[0] = a.x, w0[1] = a.y, w1[0] = d.x, w1[1] = d.y;
-                        u0 = ld_smem1(y0), u1 = ld_smem1(y1);
+                        w0[step][0] = a.x, w0[step][1] = a.y, w1[step][0] = d.x, w1[step][1] = d.y;
+                        u0[step] = ld_smem1(y0), u1[step] = ld_smem1(y1);
                     }
-                    if (!H) u0 &= k_mask, u1 &= k_mask;
+                    if (!H) u0[step] &= k_mask, u1[step] &= k_mask;
                     if (kHide) {  // what no row sees counts as zeros: it may hold anything
                         const int key = kb + (int)(g0 + 16 * split * step + rk);
-                        if (unseen(key)) u0 = 0;
-                        if (unseen(key + 8)) u1 = 0;
+                        if (unseen(key)) u0[step] = 0;
+                        if (unseen(key + 8)) u1[step] = 0;
                     }
-                    u0 = e4m3x2_to_f16(u0), u1 = e4m3x2_to_f16(u1);
+                    u0[step] = e4m3x2_to_f16(u0[step]), u1[step] = e4m3x2_to_f16(u1[step]);
+                }
 #pragma unroll
-                    for (int i = 0; i < D / 32; i++) {
-                        const uint32_t z0 = prmt(u0, u0, i < 2 ? 0x1010 : 0x3232), z1 = prmt(u1, u1, i < 2 ? 0x1010 : 0x3232);
+                for (int i = 0; i < D / 32; i++) {
+                    uint4 q[NT];
+#pragma unroll
+                    for (int x = 0; x < NT; x++) q[x] = ld_smem16(q_at + (x * (D / 32) + i) * 512);
+#pragma unroll
+                    for (int step = 0; step < F::kSteps; step++) {
+                        const uint32_t z0 = prmt(u0[step], u0[step], i < 2 ? 0x1010 : 0x3232), z1 = prmt(u1[step], u1[step], i < 2 ? 0x1010 : 0x3232);
                         uint32_t a[4], d[4];
-                        q4_to_f16(w0[i], a);
-                        q4_to_f16(w1[i], d);
+                        q4_to_f16(w0[step][i], a);
+                        q4_to_f16(w1[step][i], d);
 #pragma unroll
                         for (int j = 0; j < 4; j++) a[j] = mul_f16x2(a[j], z0), d[j] = mul_f16x2(d[j], z1);
 #pragma unroll
-                        for (int j = 0; j < 2; j++)
-#pragma unroll
-                            for (int x = 0; x < NT; x++) mma16816(sc[step][x], a[2 * j], d[2 * j], a[2 * j + 1], d[2 * j + 1], qf[x][2 * i + j][0], qf[x][2 * i + j][1]);
+                        for (int x = 0; x < NT; x++) {
+                            mma16816(sc[step][x], a[0], d[0], a[1], d[1], q[x].x, q[x].y);
+                            mma16816(sc[step][x], a[2], d[2], a[3], d[3], q[x].z, q[x].w);
+                        }
                     }
                 }
                 warp_arrive(smem_addr(&aux.k_empty[s]));
@@ -523,112 +587,89 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
                 warp_arrive(smem_addr(&aux.v_empty[s]));
                 return true;
             };
-            for (int tile = 0; ok && tile < tiles; tile++, it++) {
-                const int s = it % p.slots, kb = key0 + tile * tile_keys;
-                const uint32_t phase = (uint32_t)(it / p.slots) & 1;
+            for (int tile = 0; ok && tile < tiles; tile++) {
+                const int kb = key0 + tile * tile_keys;
                 if (kb < clean_lo || kb + tile_keys > clean_hi)
-                    ok = work(std::true_type(), kb, s, phase);
+                    ok = work(std::true_type(), kb);
                 else
-                    ok = work(std::false_type(), kb, s, phase);
+                    ok = work(std::false_type(), kb);
+                if (++s == p.slots) s = 0, phase ^= 1;
             }
             if (!ok) break;
-            // ---- the warps of a head join ----
+#pragma unroll
+            for (int x = 0; x < NT; x++)
+#pragma unroll
+                for (int i = 0; i < 2; i++)
+#pragma unroll
+                    for (int d = 4; d < 32; d *= 2) l[x][i] += __shfl_xor_sync(0xffffffffu, l[x][i], d);
+            // ---- the warps of a head join: the others leave their sums, and go on ----
+            const auto left = [&](int k) { return joins + (h * (split - 1) + k) * Sums<D, NT>::kFloats; };
+            if (part > 0) {
+                if (joined++ && !wait.warp(smem_addr(&aux.join_free[h]), (joined - 2) & 1)) break;
+                sums.store_shared(left(part - 1), rows);
+                warp_arrive(smem_addr(&aux.join_full[h]));
+                continue;
+            }
+            if (split > 1) {
+                if (!wait.warp(smem_addr(&aux.join_full[h]), joined++ & 1)) break;
+                sums.template join<true>(left, split - 1, rows);
+                warp_arrive(smem_addr(&aux.join_free[h]));
+            }
+            if (!w.whole()) {
+                // ---- the warp that finishes a cut unit's last piece of its head joins them, in the order of the keys; of many pieces
+                // the last of every `each` (so that both stages have as many) adds those up first, into the odd slot of the second ----
+                const Cut cut(line, w.pos - w.at.off, unit_cost(w.u));
+                const auto slot = [&](int piece, int odd) {
+                    return p.ws + (int64_t)(2 * (cut.c0 + piece) + odd) * (256 * 130) + h * Sums<D, NT>::kFloats;
+                };
+                sums.store_global(slot(cut.nth, cut.nth == 0), rows);
+                int each = 3;
+                while (each * each < cut.count) each++;
+                const bool many = cut.count > kMany;
+                const int groups = cut.count / each, group = min(cut.nth / each, groups - 1);
+                bool last = true;
+                for (bool sum = many; last; sum = false) {
+                    const int from = sum ? group * each : 0;
+                    const int count = sum ? (group + 1 < groups ? each : cut.count - from) : many ? groups : cut.count;
+                    __threadfence();
+                    __syncwarp();
+                    int *const counter = p.counters + kMaxHeads * (cut.c0 + (sum ? 1 + group : 0)) + h;
+                    int before = 0;
+                    if (lane == 0) before = atomicAdd(counter, 1);
+                    last = __shfl_sync(0xffffffffu, before, 0) == count - 1;
+                    if (!last) break;
+                    if (lane == 0) atomicExch(counter, 0);  // as the next call wants it
+                    __threadfence();
+                    const bool of_sums = many && !sum;
+                    sums.template join<false>([&](int k) { return of_sums ? slot(k * each + 1, 1) : slot(from + k, from + k == 0); }, count, rows);
+                    if (!sum) break;
+                    sums.store_global(slot(from + 1, 1), rows);
+                }
+                if (!last) continue;
+            }
 #pragma unroll
             for (int x = 0; x < NT; x++)
 #pragma unroll
                 for (int i = 0; i < 2; i++) {
-                    float v = l[x][i];
-#pragma unroll
-                    for (int d = 4; d < 32; d *= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
                     const int r = 8 * x + 2 * t + i;
-                    if (n == 0) aux.m[me][r] = m[x][i], aux.l[me][r] = v;
-                    float4 *to = reinterpret_cast<float4 *>(joins + (me * F::kRows + r) * F::kPitch + n * (D / 8));
+                    if (r >= rows) continue;
+                    int g;
+                    const int64_t token = token_of(r, g);
+                    const int head = (head0 + h) * (int)b.group.d + g;
+                    const float inv = l[x][i] > 0.0f ? p.v_scale / l[x][i] : 0.0f;
+                    char *to = p.o.out + token * p.o.out_token + (int64_t)head * p.o.out_head + n * (D / 8) * 2;
+                    uint32_t z[D / 16];
 #pragma unroll
-                    for (int k = 0; k < D / 32; k++) to[k] = make_float4(o[2 * k][x][i], o[2 * k][x][i + 2], o[2 * k + 1][x][i], o[2 * k + 1][x][i + 2]);
-                }
-            if (!sync_all()) break;
-            const bool whole = w.whole();
-            const auto row_out = [&](int hh, int r, int64_t &lse_at) {
-                int g;
-                const int64_t token = token_of(r, g);
-                const int head = (head0 + hh) * (int)b.group.d + g;
-                lse_at = token * p.o.heads + head;
-                return p.o.out + token * p.o.out_token + (int64_t)head * p.o.out_head;
-            };
-            // (O, m, l) of a row as the caller wants it: to the output, or to a fragment [head, row][D], m, l
-            const auto finish = [&](int hh, int r, int quad, float4 v, float top, float sum, float *frag) {
-                if (frag != nullptr) {
-                    const int at = hh * F::kRows + r;
-                    __stcg(reinterpret_cast<float4 *>(frag + at * D) + quad, v);
-                    if (quad == 0) {
-                        __stcg(frag + heads * F::kRows * D + 2 * at, top);
-                        __stcg(frag + heads * F::kRows * D + 2 * at + 1, sum);
+                    for (int k = 0; k < D / 16; k++) {
+                        const float u = o[k][x][i] * inv, v = o[k][x][i + 2] * inv;
+                        z[k] = bf16 ? pack2<true>(u, v) : pack2<false>(u, v);
                     }
-                    return;
+                    if (n * (D / 8) < dv)
+#pragma unroll
+                        for (int k = 0; k < D / 64; k++) reinterpret_cast<uint4 *>(to)[k] = make_uint4(z[4 * k], z[4 * k + 1], z[4 * k + 2], z[4 * k + 3]);
+                    if (n == 0 && p.o.lse)
+                        p.o.lse[token * p.o.heads + head] = l[x][i] > 0.0f ? fmaf(m[x][i], 0.69314718055994530942f, weight_log<false>(l[x][i])) : -INFINITY;
                 }
-                int64_t lse_at;
-                char *to = row_out(hh, r, lse_at);
-                const float inv = sum > 0.0f ? p.v_scale / sum : 0.0f;
-                if (quad * 4 < p.o.dv) {
-                    uint2 z;
-                    z.x = bf16 ? pack2<true>(v.x * inv, v.y * inv) : pack2<false>(v.x * inv, v.y * inv);
-                    z.y = bf16 ? pack2<true>(v.z * inv, v.w * inv) : pack2<false>(v.z * inv, v.w * inv);
-                    *reinterpret_cast<uint2 *>(to + quad * 8) = z;
-                }
-                if (quad == 0 && p.o.lse) p.o.lse[lse_at] = sum > 0.0f ? fmaf(top, 0.69314718055994530942f, weight_log<false>(sum)) : -INFINITY;
-            };
-            float *const mine = p.ws + (int64_t)(2 * blockIdx.x + (w.at.off == 0 ? 1 : 0)) * (256 * 130);
-            for (int i = me * 32 + lane; i < heads * rows * (D / 4); i += users * 32) {
-                const int quad = i % (D / 4), hr = i / (D / 4), hh = hr / rows, r = hr - hh * rows;
-                float top = -INFINITY, sum = 0.0f;
-                for (int k = 0; k < split; k++) top = fmaxf(top, aux.m[hh * split + k][r]);
-                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                for (int k = 0; k < split; k++) {
-                    const int at = hh * split + k;
-                    const float a = top == -INFINITY ? 0.0f : exp2_fast(aux.m[at][r] - top);
-                    const float4 x = *reinterpret_cast<const float4 *>(joins + (at * F::kRows + r) * F::kPitch + 4 * quad);
-                    sum += aux.l[at][r] * a;
-                    v.x += x.x * a, v.y += x.y * a, v.z += x.z * a, v.w += x.w * a;
-                }
-                finish(hh, r, quad, v, top, sum, whole ? nullptr : mine);
-            }
-            if (!whole) {
-                // ---- the CTA that finishes a cut unit's last piece joins them, in the order of the keys; of many pieces the last of
-                // every kSum (3 to 10 at the unit's end) adds those up first, as in kv_attention.cuh ----
-                const Cut cut(line, w.pos - w.at.off, unit_cost(w.u));
-                const bool many = cut.count > kSum + kSum / 2;
-                const int sums = (cut.count - 3) / kSum + 1, mine_of = min(cut.nth / kSum, sums - 1);
-                const auto slot = [&](int piece, int odd) { return p.ws + (int64_t)(2 * (cut.c0 + piece) + odd) * (256 * 130); };
-                for (bool sum = many;; sum = false) {
-                    const int from = sum ? mine_of * kSum : 0, count = sum ? (mine_of + 1 < sums ? kSum : cut.count - from) : many ? sums : cut.count;
-                    __threadfence();
-                    if (!sync_all()) break;
-                    if (me == 0 && lane == 0) {
-                        int *counter = p.counters + 2 * (cut.c0 + (sum ? 1 + mine_of : 0));
-                        const bool last = atomicAdd(counter, 1) == count - 1;
-                        if (last) atomicExch(counter, 0);  // as the next call wants it
-                        __threadfence();
-                        *(volatile int *)&aux.answer = last;
-                    }
-                    if (!sync_all()) break;
-                    if (!*(volatile int *)&aux.answer) break;
-                    const bool of_sums = many && !sum;
-                    Q4Pieces at;  // pieces lie in even slots but the unit's first, sums in the odd slot of their second piece
-                    at.count = count;
-                    at.first = of_sums ? slot(1, 1) : slot(from, from == 0);
-                    at.apart = (int64_t)(of_sums ? kSum : 1) * 2 * (256 * 130);
-                    at.second = of_sums ? at.apart : slot(from + 1, 0) - at.first;
-                    for (int i = me * 32 + lane; i < heads * rows * (D / 4); i += users * 32) {
-                        const int quad = i % (D / 4), hr = i / (D / 4), hh = hr / rows, r = hr - hh * rows;
-                        float top, total;
-                        const float4 v = join_pieces<D>(at, hh * F::kRows + r, quad, heads * F::kRows * D, top, total);
-                        finish(hh, r, quad, v, top, total, sum ? slot(from + 1, 1) : nullptr);
-                    }
-                    if (!sum) break;
-                }
-                if (!ok) break;
-            }
-            if (!sync_all()) break;  // the next unit writes to the join's place
         } while (next_unit());
     }
     // common exit
@@ -656,7 +697,7 @@ template <int D, int NT>
 int launch_few(FewParams &p, const DeviceInfo *dev, cudaStream_t s)
 {
     using F = Few<D, NT>;
-    constexpr uint32_t kFixed = ((sizeof(Aux) + 127) & ~127u) + ((F::kJoin + 127) & ~127u), kAll = 227 * 1024;
+    constexpr uint32_t kFixed = ((sizeof(Aux) + 127) & ~127u) + F::kWarps * F::kQ, kAll = 227 * 1024;
     CUtensorMap map[4];
     if (dev == nullptr) {
         const int st = launch_kernel<D, NT, 0>(map, p, dev, kAll, s);
@@ -694,10 +735,10 @@ int launch_few(FewParams &p, const DeviceInfo *dev, cudaStream_t s)
     };
     p.kl = place(p.k.dim);
     p.vl = place(p.v.dim);
-    const uint32_t pair = (uint32_t)(p.kl.bytes + p.vl.bytes);
-    p.slots = (int)((kAll - kFixed - 128) / pair);
+    const uint32_t pair = (uint32_t)(p.kl.bytes + p.vl.bytes), join = (uint32_t)heads * (split - 1) * Sums<D, NT>::kFloats * 4;
+    p.slots = (int)((kAll - kFixed - join - 128) / pair);
     if (p.slots > kMaxSlots) p.slots = kMaxSlots;
-    if (p.slots < 1) return KV_ERR_UNSUPPORTED;
+    if (p.slots < 1 || dev->num_sms * kMaxHeads * 4 > kCounterBytes) return KV_ERR_UNSUPPORTED;
     int st;
     if ((st = make_row_map(&map[0], p.k.base, p.k.desc, p.kl.codes, p.piece_rows)) != KV_OK) return st;
     if ((st = make_row_map(&map[1], p.v.base, p.v.desc, p.vl.codes, p.piece_rows)) != KV_OK) return st;
@@ -708,7 +749,7 @@ int launch_few(FewParams &p, const DeviceInfo *dev, cudaStream_t s)
     p.b.kv_heads = all / heads;
     p.b.tile_shift = 0;
     while ((1 << p.b.tile_shift) < p.tile) p.b.tile_shift++;
-    const uint32_t bytes = kFixed + 128 + p.slots * pair;
+    const uint32_t bytes = kFixed + join + 128 + p.slots * pair;
     const bool plain = heads == 8 && all == 8 && p.k.dim == D && p.v.dim == D && p.piece_rows >= 4;
     return plain ? launch_kernel<D, NT, 8>(map, p, dev, bytes, s) : launch_kernel<D, NT, 0>(map, p, dev, bytes, s);
 }
