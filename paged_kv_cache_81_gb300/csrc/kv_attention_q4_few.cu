@@ -15,8 +15,8 @@
 // One persistent CTA per SM; a unit is one request's rows of up to eight key heads.
 //   warp 0        brings rows of keys and of values by tiled TMA, one for each run of slots inside a page, into rings of tiles
 //   other warps   each one key head and every n-th 16 keys of a tile: scores, weights, values, with a running maximum and sum of
-//                 its own; at the unit's end the first warp of a head joins the others' through shared memory, and through
-//                 the workspace where a unit is cut, while they go on with the next
+//                 its own; at the unit's end the first warp of a head joins the others' through shared memory, while they go
+//                 on with the next unit; pieces of cut units are joined through the workspace at the CTA's end
 // Rows lie 32 or 96 bytes off a multiple of 128 apart and the 16 keys of a step are taken in an order (kOrder) in which neither the
 // keys' 16-byte nor the values' 8-byte reads meet in a bank.
 #include "kv_attention_q4.cuh"
@@ -60,9 +60,45 @@ struct FewParams : Q4Params {
     Place4 kl, vl;
 };
 
+// A unit's rows.
+struct HeadRows {
+    int row0, rows;  // of the request
+    int64_t q0;      // its first token
+};
+
+// Counts a piece whose writes come before this; true for the last of `count`, which sees what the others wrote.
+__device__ __forceinline__ bool count_in(int *counter, int count)
+{
+    int before;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+    if (before != count - 1) return false;
+    atomicExch(counter, 0);  // as the next call wants it
+    return true;
+}
+
+// A cut unit of which this CTA has a piece (at most one that ends in its part of the line, and one that begins there).
+struct CutUnit {
+    int c0, count, nth;  // Cut
+    int head0;           // the first key head
+    HeadRows rows;
+    int stored;          // heads whose pieces are in the workspace
+    int last;            // every part's are: this CTA joins them
+};
+
+// Pieces of a group, so that both stages have as many.
+__device__ __forceinline__ int group_of(int count)
+{
+    int n = 3;
+#pragma unroll 1
+    while (n * n < count) n++;
+    return n;
+}
+
 struct Aux {
     uint64_t k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots];
     uint64_t join_full[kMaxHeads], join_free[kMaxHeads];  // a head's other warps have left their sums; its first has read them
+    uint64_t sync;
+    CutUnit cut[2];  // that end in its part, that begin there
     int scan[4 * 17];
     Place place;
     Walk walk[17];  // of each warp: held in registers it would crowd the loop over the tiles
@@ -171,82 +207,137 @@ struct Tile {
     }
 };
 
-// One warp's sums over some keys, as its threads hold them: O in 16-byte pieces, then a maximum and a sum a column, all 32 lanes'
-// side by side.  A warp that joins a head's sums holds them alike.
+// One warp's sums over some keys, as its threads hold them.  A piece of them in memory: O [row][D], then a maximum and a sum a row.
 template <int D, int NT>
 struct Sums {
-    static constexpr int kPieces = NT * 2 * (D / 32);  // of 512 bytes
-    static constexpr int kFloats = kPieces * 128 + NT * 2 * 64;
+    static constexpr int kPitch = D + 4;                    // floats of a row in shared memory
+    static constexpr int kShared = 8 * NT * (kPitch + 2);   // of a piece there
+    static constexpr int kFloats = 8 * NT * (D + 2);        // of a piece in the workspace
     float o[D / 16][NT][4];
     float m[NT][2], l[NT][2];
 
-    // f(16 bytes of O, where they go), f(maximum and sum, where they go): the columns of rows below `rows`
-    template <typename F4, typename F2>
-    __device__ __forceinline__ void store(float *at, int rows, const F4 &f4, const F2 &f2) const
+    // The columns of rows below `rows` to a place in shared or global memory.
+    template <bool Shared>
+    __device__ __forceinline__ void store(float *at, int rows) const
     {
-        const int lane = threadIdx.x & 31, t = lane & 3;
-#pragma unroll
-        for (int x = 0; x < NT; x++)
-#pragma unroll
-            for (int i = 0; i < 2; i++)
-                if (8 * x + 2 * t + i < rows) {
-#pragma unroll
-                    for (int k = 0; k < D / 32; k++)
-                        f4(reinterpret_cast<float4 *>(at) + ((x * 2 + i) * (D / 32) + k) * 32 + lane,
-                           make_float4(o[2 * k][x][i], o[2 * k][x][i + 2], o[2 * k + 1][x][i], o[2 * k + 1][x][i + 2]));
-                    f2(reinterpret_cast<float2 *>(at + kPieces * 128) + (x * 2 + i) * 32 + lane, make_float2(m[x][i], l[x][i]));
-                }
-    }
-    __device__ __forceinline__ void store_shared(float *at, int rows) const
-    {
-        store(at, rows, [](float4 *p, float4 v) { *p = v; }, [](float2 *p, float2 v) { *p = v; });
-    }
-    __device__ __forceinline__ void store_global(float *at, int rows) const
-    {
-        store(at, rows, [](float4 *p, float4 v) { __stcg(p, v); }, [](float2 *p, float2 v) { __stcg(p, v); });
-    }
-    // This and `count` more, in their order: at(i) is the i-th.  Own: without this, which is overwritten.
-    template <bool Own, typename At>
-    __device__ __forceinline__ void join(const At &at, int count, int rows)
-    {
-        const int lane = threadIdx.x & 31, t = lane & 3;
+        const int lane = threadIdx.x & 31, n = lane >> 2, t = lane & 3;
 #pragma unroll
         for (int x = 0; x < NT; x++)
 #pragma unroll
             for (int i = 0; i < 2; i++) {
-                const int col = x * 2 + i;
-                const bool live = 8 * x + 2 * t + i < rows;
-                const auto stats = [&](int k) { return Own ? reinterpret_cast<const float2 *>(at(k) + kPieces * 128)[col * 32 + lane]
-                                                           : __ldcg(reinterpret_cast<const float2 *>(at(k) + kPieces * 128) + col * 32 + lane); };
-                float top = Own ? m[x][i] : -INFINITY;
-#pragma unroll 4
-                for (int k = 0; k < count; k++) top = fmaxf(top, live ? stats(k).x : -INFINITY);
-                const float z = top == -INFINITY ? 0.0f : top, a = Own ? exp2_fast(m[x][i] - z) : 0.0f;
-                m[x][i] = top;
-                l[x][i] = Own ? l[x][i] * a : 0.0f;
+                const int r = 8 * x + 2 * t + i;
+                if (r >= rows) continue;
+                float4 *const to = reinterpret_cast<float4 *>(at + r * (Shared ? kPitch : D) + n * (D / 8));
 #pragma unroll
-                for (int k = 0; k < D / 16; k++) o[k][x][i] = Own ? o[k][x][i] * a : 0.0f, o[k][x][i + 2] = Own ? o[k][x][i + 2] * a : 0.0f;
-                if (!live) continue;
-#pragma unroll 2
-                for (int k = 0; k < count; k++) {
-                    const float2 ml = stats(k);
-                    const float4 *from = reinterpret_cast<const float4 *>(at(k)) + col * (D / 32) * 32 + lane;
-                    float4 v[D / 32];
-#pragma unroll
-                    for (int j = 0; j < D / 32; j++) v[j] = Own ? from[j * 32] : __ldcg(from + j * 32);
-                    const float f = exp2_fast(ml.x - z);
-                    l[x][i] += ml.y * f;
-#pragma unroll
-                    for (int j = 0; j < D / 32; j++) {
-                        o[2 * j][x][i] += v[j].x * f, o[2 * j][x][i + 2] += v[j].y * f;
-                        o[2 * j + 1][x][i] += v[j].z * f, o[2 * j + 1][x][i + 2] += v[j].w * f;
-                    }
+                for (int k = 0; k < D / 32; k++) {
+                    const float4 v = make_float4(o[2 * k][x][i], o[2 * k][x][i + 2], o[2 * k + 1][x][i], o[2 * k + 1][x][i + 2]);
+                    if (Shared)
+                        to[k] = v;
+                    else
+                        __stcg(to + k, v);
+                }
+                if (n == 0) {
+                    float2 *const stat = reinterpret_cast<float2 *>(at + 8 * NT * (Shared ? kPitch : D)) + r;
+                    if (Shared)
+                        *stat = make_float2(m[x][i], l[x][i]);
+                    else
+                        __stcg(stat, make_float2(m[x][i], l[x][i]));
                 }
             }
     }
+    // `count` more from shared memory, in their order: at(k) is the k-th.
+    template <typename At>
+    __device__ __forceinline__ void join(const At &at, int count, int rows)
+    {
+        const int lane = threadIdx.x & 31, n = lane >> 2, t = lane & 3;
+#pragma unroll 1
+        for (int k = 0; k < count; k++) {
+            const float *const from = at(k);
+#pragma unroll
+            for (int x = 0; x < NT; x++)
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    const int r = 8 * x + 2 * t + i;
+                    if (r >= rows) continue;
+                    const float2 ml = reinterpret_cast<const float2 *>(from + 8 * NT * kPitch)[r];
+                    const float top = fmaxf(m[x][i], ml.x), z = top == -INFINITY ? 0.0f : top;
+                    const float a = exp2_fast(m[x][i] - z), f = exp2_fast(ml.x - z);
+                    m[x][i] = top;
+                    l[x][i] = l[x][i] * a + ml.y * f;
+#pragma unroll
+                    for (int j = 0; j < D / 32; j++) {
+                        const float4 v = reinterpret_cast<const float4 *>(from + r * kPitch + n * (D / 8))[j];
+                        o[2 * j][x][i] = o[2 * j][x][i] * a + v.x * f, o[2 * j][x][i + 2] = o[2 * j][x][i + 2] * a + v.y * f;
+                        o[2 * j + 1][x][i] = o[2 * j + 1][x][i] * a + v.z * f, o[2 * j + 1][x][i + 2] = o[2 * j + 1][x][i + 2] * a + v.w * f;
+                    }
+                }
+        }
+    }
 };
-
 static_assert(kMaxHeads * Sums<128, 2>::kFloats <= 256 * 130, "a piece fits its place in the workspace");
+
+// Row r of a unit: where its output begins, and its lse.
+__device__ __forceinline__ char *row_out(const FewParams &p, const HeadRows &u, int head0, int r, float *&lse)
+{
+    const int x = u.row0 + r, tok = (int)fdiv((uint32_t)x, p.b.group), head = head0 + x - tok * (int)p.b.group.d;
+    const int64_t token = u.q0 + tok;
+    lse = p.o.lse ? p.o.lse + token * p.o.heads + head : nullptr;
+    return p.o.out + token * p.o.out_token + (int64_t)head * p.o.out_head;
+}
+__device__ __forceinline__ float lse_of(float m, float l) { return l > 0.0f ? fmaf(m, 0.69314718055994530942f, weight_log<false>(l)) : -INFINITY; }
+__device__ __forceinline__ uint32_t pack_out(const FewParams &p, float a, float b) { return p.bf16 ? pack2<true>(a, b) : pack2<false>(a, b); }
+
+// Joins `count` pieces of one head of a cut unit in the workspace, in their order, by `threads` threads of which this is number `thread`.
+// each 0: pieces from, from + 1, ..; else the sums of groups of `each`.  sum: to a new piece, the odd one of piece from + 1, else to the
+// output.  A thread takes four values of a row at a time, of four pieces a trip to memory.
+template <int D, int NT>
+__device__ __forceinline__ void join_pieces(const FewParams &p, const CutUnit &unit, int h, int from, int each, int count, bool sum, int thread, int threads)
+{
+    const HeadRows u = unit.rows;
+    float *const ws = p.ws + (int64_t)(2 * unit.c0) * (256 * 130) + h * Sums<D, NT>::kFloats;
+    constexpr int kStats = 8 * NT * D;
+#pragma unroll 1
+    for (int i = thread; i < u.rows * (D / 4); i += threads) {
+        const int r = i / (D / 4), quad = i % (D / 4);
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float top = -INFINITY, l = 0.0f;
+#pragma unroll 1
+        for (int k0 = 0; k0 < count; k0 += 4) {
+            float4 w[4];
+            float2 s[4];
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                // pieces lie in even slots but the unit's first, sums in the odd slot of their second piece
+                const int piece = each ? (k0 + k) * each + 1 : from + k0 + k;
+                const float *const at = ws + (2 * piece + (each || piece == 0)) * (256 * 130);
+                w[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f), s[k] = make_float2(-INFINITY, 0.0f);
+                if (k0 + k < count) {
+                    w[k] = __ldcg(reinterpret_cast<const float4 *>(at + r * D) + quad);
+                    s[k] = __ldcg(reinterpret_cast<const float2 *>(at + kStats) + r);
+                }
+            }
+            const float now = fmaxf(fmaxf(fmaxf(s[0].x, s[1].x), fmaxf(s[2].x, s[3].x)), top), z = now == -INFINITY ? 0.0f : now, a = exp2_fast(top - z);
+            top = now;
+            l *= a, o.x *= a, o.y *= a, o.z *= a, o.w *= a;
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const float f = exp2_fast(s[k].x - z);
+                l += s[k].y * f, o.x += w[k].x * f, o.y += w[k].y * f, o.z += w[k].z * f, o.w += w[k].w * f;
+            }
+        }
+        if (sum) {
+            float *const to = ws + (2 * (from + 1) + 1) * (256 * 130);
+            __stcg(reinterpret_cast<float4 *>(to + r * D) + quad, o);
+            if (quad == 0) __stcg(reinterpret_cast<float2 *>(to + kStats) + r, make_float2(top, l));
+        } else {
+            float *lse;
+            char *const to = row_out(p, u, (unit.head0 + h) * (int)p.b.group.d, r, lse);
+            const float inv = l > 0.0f ? p.v_scale / l : 0.0f;
+            if (quad * 4 < p.o.dv) reinterpret_cast<uint2 *>(to)[quad] = make_uint2(pack_out(p, o.x * inv, o.y * inv), pack_out(p, o.z * inv, o.w * inv));
+            if (quad == 0 && lse) *lse = lse_of(top, l);
+        }
+    }
+}
 
 // H: the unit's heads where they are all of a row's and fill the widths D, and pages have runs of four slots or more (rows then lie
 // a constant distance apart), else 0.
@@ -267,13 +358,15 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
 
     unsigned char *const queries = smem + ((sizeof(Aux) + 127) & ~127u);
     float *const joins = reinterpret_cast<float *>(queries + F::kWarps * F::kQ);
-    const uint32_t ring = smem_addr(joins) + (uint32_t)(users - heads) * Sums<D, NT>::kFloats * 4;
+    const uint32_t ring = smem_addr(joins) + (((uint32_t)(users - heads) * Sums<D, NT>::kShared * 4 + 127) & ~127u);
     const uint32_t v_ring = ring + (uint32_t)p.slots * p.kl.bytes;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const Batch &b = p.b;
     const Waiter wait{&aux.gave_up, b.err};
     if (tid == 0) {
         aux.gave_up = 0;
+        aux.cut[0].last = aux.cut[1].last = aux.cut[0].stored = aux.cut[1].stored = aux.cut[0].rows.rows = 0;
+        mbar_init(smem_addr(&aux.sync), users);
         for (int i = 0; i < p.slots; i++) {
             mbar_init(smem_addr(&aux.k_full[i]), 1);
             mbar_init(smem_addr(&aux.v_full[i]), 1);
@@ -603,49 +696,38 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
 #pragma unroll
                     for (int d = 4; d < 32; d *= 2) l[x][i] += __shfl_xor_sync(0xffffffffu, l[x][i], d);
             // ---- the warps of a head join: the others leave their sums, and go on ----
-            const auto left = [&](int k) { return joins + (h * (split - 1) + k) * Sums<D, NT>::kFloats; };
+            const auto left = [&](int k) { return joins + (h * (split - 1) + k) * Sums<D, NT>::kShared; };
             if (part > 0) {
                 if (joined++ && !wait.warp(smem_addr(&aux.join_free[h]), (joined - 2) & 1)) break;
-                sums.store_shared(left(part - 1), rows);
+                sums.template store<true>(left(part - 1), rows);
                 warp_arrive(smem_addr(&aux.join_full[h]));
                 continue;
             }
             if (split > 1) {
                 if (!wait.warp(smem_addr(&aux.join_full[h]), joined++ & 1)) break;
-                sums.template join<true>(left, split - 1, rows);
+                sums.join(left, split - 1, rows);
                 warp_arrive(smem_addr(&aux.join_free[h]));
             }
             if (!w.whole()) {
-                // ---- the warp that finishes a cut unit's last piece of its head joins them, in the order of the keys; of many pieces
-                // the last of every `each` (so that both stages have as many) adds those up first, into the odd slot of the second ----
+                // the last of the CTA's heads to be in the workspace counts the piece; who counts the last one joins them all in the end
                 const Cut cut(line, w.pos - w.at.off, unit_cost(w.u));
-                const auto slot = [&](int piece, int odd) {
-                    return p.ws + (int64_t)(2 * (cut.c0 + piece) + odd) * (256 * 130) + h * Sums<D, NT>::kFloats;
-                };
-                sums.store_global(slot(cut.nth, cut.nth == 0), rows);
-                int each = 3;
-                while (each * each < cut.count) each++;
-                const bool many = cut.count > kMany;
-                const int groups = cut.count / each, group = min(cut.nth / each, groups - 1);
-                bool last = true;
-                for (bool sum = many; last; sum = false) {
-                    const int from = sum ? group * each : 0;
-                    const int count = sum ? (group + 1 < groups ? each : cut.count - from) : many ? groups : cut.count;
-                    __threadfence();
-                    __syncwarp();
-                    int *const counter = p.counters + kMaxHeads * (cut.c0 + (sum ? 1 + group : 0)) + h;
-                    int before = 0;
-                    if (lane == 0) before = atomicAdd(counter, 1);
-                    last = __shfl_sync(0xffffffffu, before, 0) == count - 1;
-                    if (!last) break;
-                    if (lane == 0) atomicExch(counter, 0);  // as the next call wants it
-                    __threadfence();
-                    const bool of_sums = many && !sum;
-                    sums.template join<false>([&](int k) { return of_sums ? slot(k * each + 1, 1) : slot(from + k, from + k == 0); }, count, rows);
-                    if (!sum) break;
-                    sums.store_global(slot(from + 1, 1), rows);
+                sums.template store<false>(p.ws + (int64_t)cut.slot(cut.nth) * (256 * 130) + h * Sums<D, NT>::kFloats, rows);
+                CutUnit &mine = aux.cut[cut.nth == 0];
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) {
+                    if (h == 0) {
+                        mine.c0 = cut.c0, mine.count = cut.count, mine.nth = cut.nth, mine.head0 = head0;
+                        mine.rows = HeadRows{w.u.row0, rows, w.q.q0};
+                    }
+                    if (atomicAdd(&mine.stored, 1) == heads - 1) {
+                        __threadfence();
+                        const int each = group_of(cut.count), groups = cut.count > kMany ? cut.count / each : 1, group = min(cut.nth / each, groups - 1);
+                        const int count = groups == 1 ? cut.count : group + 1 < groups ? each : cut.count - group * each;
+                        mine.last = count_in(p.counters + 2 * (cut.c0 + (groups > 1 ? 1 + group : 0)), count);
+                    }
                 }
-                if (!last) continue;
+                continue;
             }
 #pragma unroll
             for (int x = 0; x < NT; x++)
@@ -653,24 +735,45 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
                 for (int i = 0; i < 2; i++) {
                     const int r = 8 * x + 2 * t + i;
                     if (r >= rows) continue;
-                    int g;
-                    const int64_t token = token_of(r, g);
-                    const int head = (head0 + h) * (int)b.group.d + g;
+                    float *lse;
+                    char *const to = row_out(p, HeadRows{w.u.row0, rows, w.q.q0}, (head0 + h) * (int)b.group.d, r, lse);
                     const float inv = l[x][i] > 0.0f ? p.v_scale / l[x][i] : 0.0f;
-                    char *to = p.o.out + token * p.o.out_token + (int64_t)head * p.o.out_head + n * (D / 8) * 2;
                     uint32_t z[D / 16];
 #pragma unroll
-                    for (int k = 0; k < D / 16; k++) {
-                        const float u = o[k][x][i] * inv, v = o[k][x][i + 2] * inv;
-                        z[k] = bf16 ? pack2<true>(u, v) : pack2<false>(u, v);
-                    }
-                    if (n * (D / 8) < dv)
+                    for (int k = 0; k < D / 16; k++) z[k] = pack_out(p, o[k][x][i] * inv, o[k][x][i + 2] * inv);
 #pragma unroll
-                        for (int k = 0; k < D / 64; k++) reinterpret_cast<uint4 *>(to)[k] = make_uint4(z[4 * k], z[4 * k + 1], z[4 * k + 2], z[4 * k + 3]);
-                    if (n == 0 && p.o.lse)
-                        p.o.lse[token * p.o.heads + head] = l[x][i] > 0.0f ? fmaf(m[x][i], 0.69314718055994530942f, weight_log<false>(l[x][i])) : -INFINITY;
+                    for (int k = 0; k < D / 64; k++)
+                        if (n * (D / 8) < dv) reinterpret_cast<uint4 *>(to)[n * (D / 64) + k] = make_uint4(z[4 * k], z[4 * k + 1], z[4 * k + 2], z[4 * k + 3]);
+                    if (n == 0 && lse) *lse = lse_of(m[x][i], l[x][i]);
                 }
         } while (next_unit());
+        // ---- cut units: the CTA that brought the last piece joins them, in the order of the keys; of many pieces the last of every
+        // group adds those up first.  Done when the CTA has nothing else to do, by all its warps ----
+        int syncs = 0;
+        const auto sync_all = [&] {
+            warp_arrive(smem_addr(&aux.sync));
+            return wait.warp(smem_addr(&aux.sync), syncs++ & 1);
+        };
+        if (ok && sync_all()) {
+#pragma unroll 1
+            for (int f = 0; f < 2; f++) {
+                const CutUnit &c = aux.cut[f];
+                if (!c.last) continue;
+                const int each = group_of(c.count), groups = c.count > kMany ? c.count / each : 1, group = min(c.nth / each, groups - 1);
+                bool sum = groups > 1;
+#pragma unroll 1
+                for (;; sum = false) {
+                    const bool of_sums = groups > 1 && !sum;
+                    const int from = sum ? group * each : 0, count = groups == 1 ? c.count : of_sums ? groups : group + 1 < groups ? each : c.count - from;
+                    join_pieces<D, NT>(p, c, h, from, of_sums ? each : 0, count, sum, part * 32 + lane, split * 32);
+                    if (!sum) break;
+                    __threadfence();
+                    if (!sync_all()) break;
+                    if (me == 0 && lane == 0) aux.cut[f].last = count_in(p.counters + 2 * c.c0, groups);
+                    if (!sync_all() || !c.last) break;
+                }
+            }
+        }
     }
     // common exit
     __syncwarp();
@@ -735,7 +838,7 @@ int launch_few(FewParams &p, const DeviceInfo *dev, cudaStream_t s)
     };
     p.kl = place(p.k.dim);
     p.vl = place(p.v.dim);
-    const uint32_t pair = (uint32_t)(p.kl.bytes + p.vl.bytes), join = (uint32_t)heads * (split - 1) * Sums<D, NT>::kFloats * 4;
+    const uint32_t pair = (uint32_t)(p.kl.bytes + p.vl.bytes), join = ((uint32_t)heads * (split - 1) * Sums<D, NT>::kShared * 4 + 127) & ~127u;
     p.slots = (int)((kAll - kFixed - join - 128) / pair);
     if (p.slots > kMaxSlots) p.slots = kMaxSlots;
     if (p.slots < 1 || dev->num_sms * kMaxHeads * 4 > kCounterBytes) return KV_ERR_UNSUPPORTED;
