@@ -296,45 +296,65 @@ __device__ __forceinline__ void join_pieces(const FewParams &p, const CutUnit &u
     const HeadRows u = unit.rows;
     float *const ws = p.ws + (int64_t)(2 * unit.c0) * (256 * 130) + h * Sums<D, NT>::kFloats;
     constexpr int kStats = 8 * NT * D;
+    constexpr int kWide = NT == 1 ? 2 : 4;  // values of so many rows at a time
 #pragma unroll 1
-    for (int i = thread; i < u.rows * (D / 4); i += threads) {
-        const int r = i / (D / 4), quad = i % (D / 4);
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        float top = -INFINITY, l = 0.0f;
+    for (int i0 = thread; i0 < u.rows * (D / 4); i0 += kWide * threads) {
+        int r[kWide], quad[kWide];
+        float4 o[kWide];
+        float top[kWide], l[kWide];
+#pragma unroll
+        for (int j = 0; j < kWide; j++) {
+            const int i = min(i0 + j * threads, u.rows * (D / 4) - 1);  // the last one again past the end
+            r[j] = i / (D / 4), quad[j] = i % (D / 4);
+            o[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            top[j] = -INFINITY, l[j] = 0.0f;
+        }
 #pragma unroll 1
         for (int k0 = 0; k0 < count; k0 += 4) {
-            float4 w[4];
-            float2 s[4];
+            float4 w[kWide][4];
+            float2 s[kWide][4];
 #pragma unroll
             for (int k = 0; k < 4; k++) {
                 // pieces lie in even slots but the unit's first, sums in the odd slot of their second piece
                 const int piece = each ? (k0 + k) * each + 1 : from + k0 + k;
                 const float *const at = ws + (2 * piece + (each || piece == 0)) * (256 * 130);
-                w[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f), s[k] = make_float2(-INFINITY, 0.0f);
-                if (k0 + k < count) {
-                    w[k] = __ldcg(reinterpret_cast<const float4 *>(at + r * D) + quad);
-                    s[k] = __ldcg(reinterpret_cast<const float2 *>(at + kStats) + r);
+#pragma unroll
+                for (int j = 0; j < kWide; j++) {
+                    w[j][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f), s[j][k] = make_float2(-INFINITY, 0.0f);
+                    if (k0 + k < count) {
+                        w[j][k] = __ldcg(reinterpret_cast<const float4 *>(at + r[j] * D) + quad[j]);
+                        s[j][k] = __ldcg(reinterpret_cast<const float2 *>(at + kStats) + r[j]);
+                    }
                 }
             }
-            const float now = fmaxf(fmaxf(fmaxf(s[0].x, s[1].x), fmaxf(s[2].x, s[3].x)), top), z = now == -INFINITY ? 0.0f : now, a = exp2_fast(top - z);
-            top = now;
-            l *= a, o.x *= a, o.y *= a, o.z *= a, o.w *= a;
 #pragma unroll
-            for (int k = 0; k < 4; k++) {
-                const float f = exp2_fast(s[k].x - z);
-                l += s[k].y * f, o.x += w[k].x * f, o.y += w[k].y * f, o.z += w[k].z * f, o.w += w[k].w * f;
+            for (int j = 0; j < kWide; j++) {
+                const float now = fmaxf(fmaxf(fmaxf(s[j][0].x, s[j][1].x), fmaxf(s[j][2].x, s[j][3].x)), top[j]), z = now == -INFINITY ? 0.0f : now;
+                const float a = exp2_fast(top[j] - z);
+                top[j] = now;
+                l[j] *= a, o[j].x *= a, o[j].y *= a, o[j].z *= a, o[j].w *= a;
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    const float f = exp2_fast(s[j][k].x - z);
+                    l[j] += s[j][k].y * f, o[j].x += w[j][k].x * f, o[j].y += w[j][k].y * f, o[j].z += w[j][k].z * f, o[j].w += w[j][k].w * f;
+                }
             }
         }
-        if (sum) {
-            float *const to = ws + (2 * (from + 1) + 1) * (256 * 130);
-            __stcg(reinterpret_cast<float4 *>(to + r * D) + quad, o);
-            if (quad == 0) __stcg(reinterpret_cast<float2 *>(to + kStats) + r, make_float2(top, l));
-        } else {
-            float *lse;
-            char *const to = row_out(p, u, (unit.head0 + h) * (int)p.b.group.d, r, lse);
-            const float inv = l > 0.0f ? p.v_scale / l : 0.0f;
-            if (quad * 4 < p.o.dv) reinterpret_cast<uint2 *>(to)[quad] = make_uint2(pack_out(p, o.x * inv, o.y * inv), pack_out(p, o.z * inv, o.w * inv));
-            if (quad == 0 && lse) *lse = lse_of(top, l);
+#pragma unroll
+        for (int j = 0; j < kWide; j++) {
+            if (j > 0 && i0 + j * threads >= u.rows * (D / 4)) break;
+            if (sum) {
+                float *const to = ws + (2 * (from + 1) + 1) * (256 * 130);
+                __stcg(reinterpret_cast<float4 *>(to + r[j] * D) + quad[j], o[j]);
+                if (quad[j] == 0) __stcg(reinterpret_cast<float2 *>(to + kStats) + r[j], make_float2(top[j], l[j]));
+            } else {
+                float *lse;
+                char *const to = row_out(p, u, (unit.head0 + h) * (int)p.b.group.d, r[j], lse);
+                const float inv = l[j] > 0.0f ? p.v_scale / l[j] : 0.0f;
+                if (quad[j] * 4 < p.o.dv)
+                    reinterpret_cast<uint2 *>(to)[quad[j]] = make_uint2(pack_out(p, o[j].x * inv, o[j].y * inv), pack_out(p, o[j].z * inv, o[j].w * inv));
+                if (quad[j] == 0 && lse) *lse = lse_of(top[j], l[j]);
+            }
         }
     }
 }
