@@ -5,7 +5,11 @@
 
 namespace pkv {
 
-int preload_q4_kernels() { return preload_q4_few_kernels(); }
+int preload_q4_kernels()
+{
+    const int st = preload_q4_few64_kernels();
+    return st != KV_OK ? st : preload_q4_few128_kernels();
+}
 
 }  // namespace pkv
 
@@ -63,7 +67,8 @@ int kv_attention_q4(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_
     p.v_scale = v_scale;
     p.counters = (int *)workspace;
     p.ws = (float *)((char *)workspace + kCounterBytes);
-    return run_q4_few(d->dtype == KV_BF16, p, batch, rows, *dev, (cudaStream_t)stream);
+    const auto few = d->head_dim <= 64 && d->head_dim_v <= 64 ? run_q4_few64 : run_q4_few128;
+    return few(d->dtype == KV_BF16, p, rows, *dev, (cudaStream_t)stream);
 }
 
 }  // extern "C"

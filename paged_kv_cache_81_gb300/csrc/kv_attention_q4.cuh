@@ -30,8 +30,11 @@ struct Q4Params {
     int *counters;
 };
 
-int run_q4_few(bool bf16, const Q4Params &p, const kv_attn_batch *batch, int rows, const DeviceInfo &dev, cudaStream_t s);
-int preload_q4_few_kernels();  // kv_attention_q4_few.cu
+// Units of `rows` rows, 8 or 16, of heads of at most 64 and of 128 elements (kv_attention_q4_few64.cu, kv_attention_q4_few128.cu).
+int run_q4_few64(bool bf16, const Q4Params &p, int rows, const DeviceInfo &dev, cudaStream_t s);
+int run_q4_few128(bool bf16, const Q4Params &p, int rows, const DeviceInfo &dev, cudaStream_t s);
+int preload_q4_few64_kernels();
+int preload_q4_few128_kernels();
 int preload_q4_kernels();      // kv_attention_q4.cu
 
 }  // namespace pkv

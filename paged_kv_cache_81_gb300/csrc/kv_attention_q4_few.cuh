@@ -13,12 +13,14 @@
 // sums are in 32 bits.
 //
 // One persistent CTA per SM; a unit is one request's rows of up to eight key heads.
-//   warp 0        brings rows of keys and of values by tiled TMA, one for each run of slots inside a page, into rings of tiles
+//   warps 0, 1    bring rows of keys and of values by TMA, one for each run of slots inside a page, into rings of tiles
 //   other warps   each one key head and every n-th 16 keys of a tile: scores, weights, values, with a running maximum and sum of
 //                 its own; at the unit's end the first warp of a head joins the others' through shared memory, while they go
 //                 on with the next unit; pieces of cut units are joined through the workspace at the CTA's end
-// Rows lie 32 or 96 bytes off a multiple of 128 apart and the 16 keys of a step are taken in an order (kOrder) in which neither the
-// keys' 16-byte nor the values' 8-byte reads meet in a bank.
+// The 16 keys of a step are taken in an order (order_of) in which the keys' 16-byte reads do not meet in a bank, and the values'
+// 8-byte reads at most in pairs.
+#pragma once
+
 #include "kv_attention_q4.cuh"
 
 namespace pkv {
@@ -26,19 +28,21 @@ namespace pkv {
 namespace {
 
 constexpr int kLeast = 2;     // tiles of a piece of a unit, at least
-constexpr int kMaxHeads = 8;  // key heads of a unit
+constexpr int kMaxHeads = 16;  // key heads of a unit
 constexpr int kMaxSlots = 8;
 constexpr int kMany = 12;     // pieces of a unit from which on they are joined in two stages
-constexpr uint32_t kOrder = 0x57463120u;  // key of row r of 8: hexadecimal digit r
+// The key of row r of 8 (hexadecimal digit r) by how far rows lie apart: in pairs that are 64 bytes off one another, modulo 128.
+constexpr uint32_t order_of(uint32_t pitch)
+{
+    return pitch % 128 == 64 ? 0x76543210u : 2 * pitch % 128 == 64 ? 0x57463120u : 0x73516240u;
+}
 
 template <int D, int NT>
 struct Few {
     static constexpr int kWarps = NT == 1 ? 16 : 8;  // that compute
-    static constexpr int kThreads = 32 * (kWarps + 1);
+    static constexpr int kThreads = 32 * (kWarps + 2);
     static constexpr int kSteps = NT == 1 ? 2 : 4;   // groups of 16 keys that a warp takes of a tile
     static constexpr uint32_t kQ = NT * (D / 32) * 512;  // bytes of a warp's queries
-    // bytes between a tile's rows of H heads of D, 32 off a multiple of 64
-    static constexpr uint32_t pitch(int h) { return (uint32_t)((h * D * 9 + 255) / 256 * 16 - 32 + 63) / 64 * 64 + 32; }
 };
 
 // Where a unit's heads of a tile lie in shared memory: rows of codes and of scales, `codes` and `scales` bytes apart.  All heads of
@@ -48,10 +52,15 @@ struct Place4 {
     int32_t first;  // of the first row's scales
     int32_t bytes;  // of a tile
     int32_t apart;  // two loads
+    // rows follow one another in the page too: a run is one untiled copy (a tiled one takes 8 cycles a row, and more a load)
+    int32_t dense;
+    uint64_t base;
+    int64_t block_stride;
 };
 
 struct FewParams : Q4Params {
     int32_t bf16;
+    uint32_t order;
     int32_t unit_heads;        // key heads of a unit
     int32_t split;             // warps of a key head
     int32_t tile;              // keys
@@ -99,11 +108,17 @@ struct Aux {
     uint64_t join_full[kMaxHeads], join_free[kMaxHeads];  // a head's other warps have left their sums; its first has read them
     uint64_t sync;
     CutUnit cut[2];  // that end in its part, that begin there
-    int scan[4 * 17];
+    int scan[4 * 18];
     Place place;
-    Walk walk[17];  // of each warp: held in registers it would crowd the loop over the tiles
+    Walk walk[18];  // of each warp: held in registers it would crowd the loop over the tiles
     int gave_up;
 };
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, uint64_t src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
@@ -187,7 +202,7 @@ struct Tile {
     }
     // Its rows of keys or values: a TMA (two where heads are apart) a run.
     __device__ __forceinline__ void load(const FewParams &p, const CUtensorMap *map, const CUtensorMap *scale_map, int dim, const Place4 &place, uint32_t to,
-                                         uint32_t bar)
+                                         uint32_t bar, bool report)
     {
         const int lane = threadIdx.x & 31, pr = p.piece_rows;
         if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)((p1 - p0) * pr) * (place.codes + (place.apart ? place.scales : 0)));
@@ -196,8 +211,11 @@ struct Tile {
             if (p1 - p0 > 32) look(p, i);
             int from = page;
             if (from < 0 || from >= p.num_blocks) {
-                set_error(p.b.err, KV_DERR_TABLE);
+                if (report) set_error(p.b.err, KV_DERR_TABLE);
                 from = p.no_page;
+            } else if (place.dense) {
+                bulk_load(to + i * pr * place.codes, place.base + (uint64_t)from * place.block_stride + (uint32_t)(slot * place.codes), pr * place.codes, bar);
+                continue;
             }
             tma_load_3d(to + i * pr * place.codes, map, bar, h0 * dim / 8, slot, from);
             if (place.apart)
@@ -274,7 +292,7 @@ struct Sums {
         }
     }
 };
-static_assert(kMaxHeads * Sums<128, 2>::kFloats <= 256 * 130, "a piece fits its place in the workspace");
+static_assert(16 * Sums<128, 1>::kFloats <= 256 * 130 && 8 * Sums<128, 2>::kFloats <= 256 * 130, "a piece fits its place in the workspace");
 
 // Row r of a unit: where its output begins, and its lse.
 __device__ __forceinline__ char *row_out(const FewParams &p, const HeadRows &u, int head0, int r, float *&lse)
@@ -359,8 +377,8 @@ __device__ __forceinline__ void join_pieces(const FewParams &p, const CutUnit &u
     }
 }
 
-// H: the unit's heads where they are all of a row's and fill the widths D, and pages have runs of four slots or more (rows then lie
-// a constant distance apart), else 0.
+// H: the unit's heads where they are all of a row's, fill the widths D, and rows follow one another (they then lie a constant
+// distance apart), else 0.
 template <int D, int NT, int H>
 __global__ void __launch_bounds__(Few<D, NT>::kThreads, 1)
 attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap ks_map,
@@ -372,7 +390,7 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     const bool bf16 = p.bf16;
     const int heads = H ? H : p.unit_heads, split = H ? F::kWarps / H : p.split, users = heads * split;  // warps that compute: users
     const int dk = H ? D : p.k.dim, dv = H ? D : p.v.dim, tile_keys = 16 * split * F::kSteps;
-    constexpr uint32_t kPitch = Few<D, NT>::pitch(H);
+    constexpr uint32_t kPitch = (H * D * 9 + 255) / 256 * 16;
     const uint32_t k_row = H ? kPitch : p.kl.codes, y_row = H ? kPitch : p.kl.scales, v_row = H ? kPitch : p.vl.codes, x_row = H ? kPitch : p.vl.scales;
     const uint32_t k_tile = H ? kPitch * tile_keys : p.kl.bytes, v_tile = H ? kPitch * tile_keys : p.vl.bytes;
 
@@ -411,37 +429,39 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     __syncwarp();
     if (!any) {
         // nothing to do: on to the common exit
-    } else if (warp == 0) {
-        // ---- rows of keys and values ----
+    } else if (warp < 2) {
+        // ---- rows of keys, rows of values ----
+        const CUtensorMap *const map = warp ? &v_map : &k_map, *const scale_map = warp ? &vs_map : &ks_map;
+        const Place4 &place = warp ? p.vl : p.kl;
+        const uint32_t to = warp ? v_ring : ring, bytes = warp ? v_tile : k_tile;
+        const uint64_t *const full = warp ? aux.v_full : aux.k_full, *const empty = warp ? aux.v_empty : aux.k_empty;
         int it = 0, s = 0, at = 0;
         uint32_t phase = 1;
         Tile tile, next;
-        // the tile after the one that `to` was called for last
-        const auto ahead = [&](Tile &to) {
+        // the tile after the one that it was called for last
+        const auto ahead = [&](Tile &t) {
             while (at >= first.n || first.u.tiles == 0) {
                 at = 0;
                 if (!first.next(b)) return false;
             }
-            to.start(p, first, at++, tile_keys, heads);
+            t.start(p, first, at++, tile_keys, heads);
             return true;
         };
         bool more = ahead(next);
         while (more) {
             tile = next;
             more = ahead(next);
-            if (it >= p.slots && !wait.warp(smem_addr(&aux.k_empty[s]), phase)) break;
-            tile.load(p, &k_map, &ks_map, p.k.dim, p.kl, ring + s * k_tile, smem_addr(&aux.k_full[s]));
-            if (it >= p.slots && !wait.warp(smem_addr(&aux.v_empty[s]), phase)) break;
-            tile.load(p, &v_map, &vs_map, p.v.dim, p.vl, v_ring + s * v_tile, smem_addr(&aux.v_full[s]));
-            it++;
+            if (it++ >= p.slots && !wait.warp(smem_addr(&empty[s]), phase)) break;
+            tile.load(p, map, scale_map, warp ? dv : dk, place, to + s * bytes, smem_addr(&full[s]), warp == 0);
             if (++s == p.slots) s = 0, phase ^= 1;
         }
-    } else if (warp <= users) {
-        const int me = warp - 1, h = me / split, part = me - h * split;
+    } else if (warp < users + 2) {
+        const int me = warp - 2, h = me / split, part = me - h * split;
         bool ok = true;
         const int n = lane >> 2, t = lane & 3;
-        const uint32_t rk = (kOrder >> (4 * n)) & 7;                                            // keys of score rows n, n + 8
-        const uint32_t ra = (kOrder >> (8 * t)) & 7, rb = (kOrder >> (8 * t + 4)) & 7;          // keys of product columns 2 t, 2 t + 1
+        const uint32_t order = H ? order_of(kPitch) : p.order;
+        const uint32_t rk = (order >> (4 * n)) & 7;                                    // keys of score rows n, n + 8
+        const uint32_t ra = (order >> (8 * t)) & 7, rb = (order >> (8 * t + 4)) & 7;  // keys of product columns 2 t, 2 t + 1
         const uint32_t g0 = 16u * part;
         // this thread's scales in a word of them; dimensions that heads do not have count as zeros
         const uint32_t k_mask = t * (D / 4) >= dk ? 0u : D == 128 && t * (D / 4) + 16 < dk ? 0xffffu : 0xffu;
@@ -815,6 +835,19 @@ int launch_kernel(const CUtensorMap *map, const FewParams &p, const DeviceInfo *
     return cuda_status(launch(kernel, dim3(dev->num_sms), dim3(Few<D, NT>::kThreads), bytes, s, map[0], map[1], map[2], map[3], p));
 }
 
+// Rows whose heads all come together, a power of two of them.
+template <int D, int NT>
+int launch_full(int heads, const CUtensorMap *map, const FewParams &p, const DeviceInfo *dev, uint32_t bytes, cudaStream_t s)
+{
+    switch (heads) {
+    case 1: return launch_kernel<D, NT, 1>(map, p, dev, bytes, s);
+    case 2: return launch_kernel<D, NT, 2>(map, p, dev, bytes, s);
+    case 4: return launch_kernel<D, NT, 4>(map, p, dev, bytes, s);
+    case 8: return launch_kernel<D, NT, 8>(map, p, dev, bytes, s);
+    default: return launch_kernel<D, NT, NT == 1 ? 16 : 8>(map, p, dev, bytes, s);
+    }
+}
+
 // dev: null to prepare the kernels.
 template <int D, int NT>
 int launch_few(FewParams &p, const DeviceInfo *dev, cudaStream_t s)
@@ -823,11 +856,12 @@ int launch_few(FewParams &p, const DeviceInfo *dev, cudaStream_t s)
     constexpr uint32_t kFixed = ((sizeof(Aux) + 127) & ~127u) + F::kWarps * F::kQ, kAll = 227 * 1024;
     CUtensorMap map[4];
     if (dev == nullptr) {
-        const int st = launch_kernel<D, NT, 0>(map, p, dev, kAll, s);
-        return st != KV_OK ? st : launch_kernel<D, NT, 8>(map, p, dev, kAll, s);
+        int st = launch_kernel<D, NT, 0>(map, p, dev, kAll, s);
+        for (int h = 1; st == KV_OK && h <= F::kWarps; h *= 2) st = launch_full<D, NT>(h, map, p, dev, kAll, s);
+        return st;
     }
     const int all = p.heads_all;
-    int heads = all < kMaxHeads ? all : kMaxHeads;
+    int heads = all < F::kWarps ? all : F::kWarps;
     while (all % heads) heads--;
     int split = 1;
     while (2 * split * heads <= F::kWarps) split *= 2;
@@ -840,24 +874,28 @@ int launch_few(FewParams &p, const DeviceInfo *dev, cudaStream_t s)
         const int step = p.piece_rows >= 4 ? 64 : 128 / p.piece_rows, off = p.piece_rows >= 4 ? 32 : 0;
         return (bytes - off + step - 1) / step * step + off;
     };
-    const auto place = [&](int dim) {
+    const auto place = [&](const Q4Plane &plane) {
         Place4 l = {};
-        const int codes = heads * dim / 2;
+        const int codes = heads * plane.dim / 2, row = plane.desc->row_bytes;
         l.apart = heads < all;
+        l.dense = !l.apart && plane.desc->token_stride == row && row * p.piece_rows % 128 == 0;
+        l.base = plane.base;
+        l.block_stride = plane.desc->block_stride;
         if (l.apart) {
             l.codes = pitch(codes);
-            l.scales = pitch((heads * dim / 16 + 14 + 15) / 16 * 16);
+            l.scales = pitch((heads * plane.dim / 16 + 14 + 15) / 16 * 16);
             l.first = p.tile * l.codes;
             l.bytes = p.tile * (l.codes + l.scales);
         } else {
-            l.codes = l.scales = pitch((int)q4_row_bytes(heads, dim));
+            l.codes = l.scales = l.dense ? row : pitch(row);
             l.first = codes;
             l.bytes = p.tile * l.codes;
         }
         return l;
     };
-    p.kl = place(p.k.dim);
-    p.vl = place(p.v.dim);
+    p.kl = place(p.k);
+    p.vl = place(p.v);
+    p.order = order_of(p.kl.codes);
     const uint32_t pair = (uint32_t)(p.kl.bytes + p.vl.bytes), join = ((uint32_t)heads * (split - 1) * Sums<D, NT>::kShared * 4 + 127) & ~127u;
     p.slots = (int)((kAll - kFixed - join - 128) / pair);
     if (p.slots > kMaxSlots) p.slots = kMaxSlots;
@@ -873,30 +911,10 @@ int launch_few(FewParams &p, const DeviceInfo *dev, cudaStream_t s)
     p.b.tile_shift = 0;
     while ((1 << p.b.tile_shift) < p.tile) p.b.tile_shift++;
     const uint32_t bytes = kFixed + join + 128 + p.slots * pair;
-    const bool plain = heads == 8 && all == 8 && p.k.dim == D && p.v.dim == D && p.piece_rows >= 4;
-    return plain ? launch_kernel<D, NT, 8>(map, p, dev, bytes, s) : launch_kernel<D, NT, 0>(map, p, dev, bytes, s);
+    const bool full = p.kl.dense && p.vl.dense && p.k.dim == D && p.v.dim == D && (heads & (heads - 1)) == 0;
+    return full ? launch_full<D, NT>(heads, map, p, dev, bytes, s) : launch_kernel<D, NT, 0>(map, p, dev, bytes, s);
 }
 
 }  // namespace
-
-// rows: of a unit, 8 or 16.
-int run_q4_few(bool bf16, const Q4Params &q, const kv_attn_batch *batch, int rows, const DeviceInfo &dev, cudaStream_t s)
-{
-    FewParams p = {};
-    static_cast<Q4Params &>(p) = q;
-    p.bf16 = bf16;
-    if (p.k.dim <= 64 && p.v.dim <= 64) return rows <= 8 ? launch_few<64, 1>(p, &dev, s) : launch_few<64, 2>(p, &dev, s);
-    return rows <= 8 ? launch_few<128, 1>(p, &dev, s) : launch_few<128, 2>(p, &dev, s);
-}
-
-int preload_q4_few_kernels()
-{
-    FewParams p = {};
-    for (int (*prepare)(FewParams &, const DeviceInfo *, cudaStream_t) : {launch_few<64, 1>, launch_few<64, 2>, launch_few<128, 1>, launch_few<128, 2>}) {
-        const int st = prepare(p, nullptr, nullptr);
-        if (st != KV_OK) return st;
-    }
-    return KV_OK;
-}
 
 }  // namespace pkv

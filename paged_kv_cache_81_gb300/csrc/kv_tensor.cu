@@ -51,10 +51,11 @@ int make_row_map(CUtensorMap *map, uint64_t base, const kv_cache_desc *c, int by
 {
     const EncodeFn fn = encoder();
     if (fn == nullptr) return KV_ERR_CUDA;
-    const cuuint64_t dims[3] = {(cuuint64_t)c->row_bytes / 4, (cuuint64_t)c->block_size, (cuuint64_t)c->num_blocks};
+    const int word = bytes > 1024 ? 8 : 4;  // a box has at most 256
+    const cuuint64_t dims[3] = {(cuuint64_t)(c->row_bytes / word), (cuuint64_t)c->block_size, (cuuint64_t)c->num_blocks};
     const cuuint64_t strides[2] = {(cuuint64_t)c->token_stride, (cuuint64_t)c->block_stride};
-    const cuuint32_t box[3] = {(cuuint32_t)bytes / 4, (cuuint32_t)rows, 1}, one[3] = {1, 1, 1};
-    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, (void *)base, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    const cuuint32_t box[3] = {(cuuint32_t)(bytes / word), (cuuint32_t)rows, 1}, one[3] = {1, 1, 1};
+    const CUresult r = fn(map, word == 8 ? CU_TENSOR_MAP_DATA_TYPE_UINT64 : CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, (void *)base, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                           CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? KV_OK : KV_ERR_UNSUPPORTED;
 }

@@ -341,8 +341,8 @@ int make_map(CUtensorMap *map, uint64_t base, int rank, const uint64_t *dims, co
 // brings 64 elements of one head of `rows` consecutive slots of a block.
 int make_cache_map(CUtensorMap *map, const kv_cache_desc *c, int tensor, int plane, int heads, int head_dim, int rows);
 
-// A map of a plane's rows as opaque 32-bit words, (word of a row, slot, block), without a swizzle; a load brings `bytes` of
-// each of `rows` consecutive slots of a block, densely, with zeros for what lies past a row's end.
+// A map of a plane's rows as opaque 32-bit words (64-bit ones for boxes of more than 1024 bytes), (word of a row, slot, block), without a
+// swizzle; a load brings `bytes` of each of `rows` consecutive slots of a block, densely, with zeros for what lies past a row's end.
 int make_row_map(CUtensorMap *map, uint64_t base, const kv_cache_desc *c, int bytes, int rows);
 
 }  // namespace pkv
