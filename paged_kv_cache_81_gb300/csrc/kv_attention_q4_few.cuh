@@ -13,10 +13,10 @@
 // sums are in 32 bits.
 //
 // One persistent CTA per SM; a unit is one request's rows of up to eight key heads.
-//   warps 0, 1    bring rows of keys and of values by TMA, one for each run of slots inside a page, into rings of tiles
-//   other warps   each one key head and every n-th 16 keys of a tile: scores, weights, values, with a running maximum and sum of
-//                 its own; at the unit's end the first warp of a head joins the others' through shared memory, while they go
-//                 on with the next unit; pieces of cut units are joined through the workspace at the CTA's end
+//   warps 0, 1 (to 3)  bring rows of keys and of values by TMA, one for each run of slots inside a page, into rings of tiles
+//   other warps        each one key head and every n-th 16 keys of a tile: scores, weights, values, with a running maximum and sum of
+//                      its own; at the unit's end the warps of a head join through shared memory, while those that are done go on
+//                      with the next unit; pieces of cut units are joined through the workspace at the CTA's end
 // The 16 keys of a step are taken in an order (order_of) in which the keys' 16-byte reads do not meet in a bank, and the values'
 // 8-byte reads at most in pairs.
 #pragma once
@@ -37,11 +37,16 @@ constexpr uint32_t order_of(uint32_t pitch)
     return pitch % 128 == 64 ? 0x76543210u : 2 * pitch % 128 == 64 ? 0x57463120u : 0x73516240u;
 }
 
-template <int D, int NT>
+// H: see attention_q4_few_kernel.
+template <int D, int NT, int H>
 struct Few {
     static constexpr int kWarps = NT == 1 ? 16 : 8;  // that compute
-    static constexpr int kThreads = 32 * (kWarps + 2);
-    static constexpr int kSteps = NT == 1 ? 2 : 4;   // groups of 16 keys that a warp takes of a tile
+    // Warps that load.  Rows of one or two heads come in short runs, and two warps do not issue them fast enough (152 requests of 20480
+    // tokens, two heads: 167 us, with four 151); where they do, two more cost a call 2 us.
+    static constexpr int kLoaders = H == 1 || H == 2 ? 4 : 2;
+    static constexpr int kThreads = 32 * (kWarps + kLoaders);
+    // Groups of 16 keys that a warp takes of a tile; of one head's rows half as many leave room for more than one tile.
+    static constexpr int kSteps = (NT == 1 ? 2 : 4) / (H == 1 ? 2 : 1);
     static constexpr uint32_t kQ = NT * (D / 32) * 512;  // bytes of a warp's queries
 };
 
@@ -103,14 +108,21 @@ __device__ __forceinline__ int group_of(int count)
     return n;
 }
 
+// Whether all heads of a row come together and rows follow one another, in runs that end on a multiple of 128 bytes.
+inline bool dense_rows(const FewParams &p, const Q4Plane &plane)
+{
+    const kv_cache_desc &d = *plane.desc;
+    return p.unit_heads == p.heads_all && d.token_stride == d.row_bytes && (int64_t)d.row_bytes * p.piece_rows % 128 == 0;
+}
+
 struct Aux {
     uint64_t k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots];
-    uint64_t join_full[kMaxHeads], join_free[kMaxHeads];  // a head's other warps have left their sums; its first has read them
+    uint64_t join_first[8], join_full[8], join_free[8];  // a place of the join: filled in the first round, in a later one; free
     uint64_t sync;
     CutUnit cut[2];  // that end in its part, that begin there
-    int scan[4 * 18];
+    int scan[4 * 20];
     Place place;
-    Walk walk[18];  // of each warp: held in registers it would crowd the loop over the tiles
+    Walk walk[20];  // of each warp: held in registers it would crowd the loop over the tiles
     int gave_up;
 };
 
@@ -177,11 +189,12 @@ __device__ __forceinline__ bool next_of(Walk &shared, const Batch &b)
     return more;
 }
 
-// A tile as the loading warp sees it: the runs of slots inside a page that it takes, one a lane (and every 32nd after it), and the
-// page of the lane's first one, asked for a tile ahead: a trip to the block table takes as long as half a tile's work.
+// A tile as a loading warp sees it, one of Warps that share it: every Warps-th run of slots inside a page, one a lane (and every 32nd
+// after it), and the page of the lane's first one, asked for a tile ahead: a trip to the block table takes as long as half a tile's work.
+template <int Warps>
 struct Tile {
     const int32_t *row;
-    int kb, h0, p0, p1;
+    int kb, h0, p0, p1;  // this warp's runs: p0, p0 + Warps, .. below p1
     int page, slot;
 
     __device__ __forceinline__ void look(const FewParams &p, int i)
@@ -190,25 +203,26 @@ struct Tile {
         slot = (int)(key - col * p.block.d);
         page = __ldg(row + col);
     }
-    __device__ __forceinline__ void start(const FewParams &p, const Walk &w, int t, int tile_keys, int heads)
+    __device__ __forceinline__ void start(const FewParams &p, const Walk &w, int t, int tile_keys, int heads, int which)
     {
         row = p.table + (int64_t)w.at.req * p.table_stride;
         kb = (w.u.tile0 + w.at.off + t) * tile_keys;
         h0 = w.at.head * heads;
-        p0 = max(0, w.u.lo - kb) / p.piece_rows;
+        p0 = max(0, w.u.lo - kb) / p.piece_rows + which;
         p1 = (min(w.u.hi - kb, tile_keys) + p.piece_rows - 1) / p.piece_rows;
-        const int i = p0 + (threadIdx.x & 31);
+        const int i = p0 + Warps * (threadIdx.x & 31);
         if (i < p1) look(p, i);
     }
     // Its rows of keys or values: a TMA (two where heads are apart) a run.
     __device__ __forceinline__ void load(const FewParams &p, const CUtensorMap *map, const CUtensorMap *scale_map, int dim, const Place4 &place, uint32_t to,
                                          uint32_t bar, bool report)
     {
-        const int lane = threadIdx.x & 31, pr = p.piece_rows;
-        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)((p1 - p0) * pr) * (place.codes + (place.apart ? place.scales : 0)));
+        const int lane = threadIdx.x & 31, pr = p.piece_rows, runs = max(p1 - p0 + Warps - 1, 0) / Warps;
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(runs * pr) * (place.codes + (place.apart ? place.scales : 0)));
         __syncwarp();
-        for (int i = p0 + lane; i < p1; i += 32) {
-            if (p1 - p0 > 32) look(p, i);
+        for (int j = lane; j < runs; j += 32) {
+            const int i = p0 + Warps * j;
+            if (j >= 32) look(p, i);
             int from = page;
             if (from < 0 || from >= p.num_blocks) {
                 if (report) set_error(p.b.err, KV_DERR_TABLE);
@@ -263,33 +277,28 @@ struct Sums {
                 }
             }
     }
-    // `count` more from shared memory, in their order: at(k) is the k-th.
-    template <typename At>
-    __device__ __forceinline__ void join(const At &at, int count, int rows)
+    // Others from shared memory are added.
+    __device__ __forceinline__ void join(const float *from, int rows)
     {
         const int lane = threadIdx.x & 31, n = lane >> 2, t = lane & 3;
-#pragma unroll 1
-        for (int k = 0; k < count; k++) {
-            const float *const from = at(k);
 #pragma unroll
-            for (int x = 0; x < NT; x++)
+        for (int x = 0; x < NT; x++)
 #pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    const int r = 8 * x + 2 * t + i;
-                    if (r >= rows) continue;
-                    const float2 ml = reinterpret_cast<const float2 *>(from + 8 * NT * kPitch)[r];
-                    const float top = fmaxf(m[x][i], ml.x), z = top == -INFINITY ? 0.0f : top;
-                    const float a = exp2_fast(m[x][i] - z), f = exp2_fast(ml.x - z);
-                    m[x][i] = top;
-                    l[x][i] = l[x][i] * a + ml.y * f;
+            for (int i = 0; i < 2; i++) {
+                const int r = 8 * x + 2 * t + i;
+                if (r >= rows) continue;
+                const float2 ml = reinterpret_cast<const float2 *>(from + 8 * NT * kPitch)[r];
+                const float top = fmaxf(m[x][i], ml.x), z = top == -INFINITY ? 0.0f : top;
+                const float a = exp2_fast(m[x][i] - z), f = exp2_fast(ml.x - z);
+                m[x][i] = top;
+                l[x][i] = l[x][i] * a + ml.y * f;
 #pragma unroll
-                    for (int j = 0; j < D / 32; j++) {
-                        const float4 v = reinterpret_cast<const float4 *>(from + r * kPitch + n * (D / 8))[j];
-                        o[2 * j][x][i] = o[2 * j][x][i] * a + v.x * f, o[2 * j][x][i + 2] = o[2 * j][x][i + 2] * a + v.y * f;
-                        o[2 * j + 1][x][i] = o[2 * j + 1][x][i] * a + v.z * f, o[2 * j + 1][x][i + 2] = o[2 * j + 1][x][i + 2] * a + v.w * f;
-                    }
+                for (int j = 0; j < D / 32; j++) {
+                    const float4 v = reinterpret_cast<const float4 *>(from + r * kPitch + n * (D / 8))[j];
+                    o[2 * j][x][i] = o[2 * j][x][i] * a + v.x * f, o[2 * j][x][i + 2] = o[2 * j][x][i + 2] * a + v.y * f;
+                    o[2 * j + 1][x][i] = o[2 * j + 1][x][i] * a + v.z * f, o[2 * j + 1][x][i + 2] = o[2 * j + 1][x][i + 2] * a + v.w * f;
                 }
-        }
+            }
     }
 };
 static_assert(16 * Sums<128, 1>::kFloats <= 256 * 130 && 8 * Sums<128, 2>::kFloats <= 256 * 130, "a piece fits its place in the workspace");
@@ -380,11 +389,11 @@ __device__ __forceinline__ void join_pieces(const FewParams &p, const CutUnit &u
 // H: the unit's heads where they are all of a row's, fill the widths D, and rows follow one another (they then lie a constant
 // distance apart), else 0.
 template <int D, int NT, int H>
-__global__ void __launch_bounds__(Few<D, NT>::kThreads, 1)
+__global__ void __launch_bounds__(Few<D, NT, H>::kThreads, 1)
 attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap ks_map,
                         const __grid_constant__ CUtensorMap vs_map, const __grid_constant__ FewParams p)
 {
-    using F = Few<D, NT>;
+    using F = Few<D, NT, H>;
     extern __shared__ __align__(128) unsigned char smem[];
     Aux &aux = *reinterpret_cast<Aux *>(smem);
     const bool bf16 = p.bf16;
@@ -396,7 +405,7 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
 
     unsigned char *const queries = smem + ((sizeof(Aux) + 127) & ~127u);
     float *const joins = reinterpret_cast<float *>(queries + F::kWarps * F::kQ);
-    const uint32_t ring = smem_addr(joins) + (((uint32_t)(users - heads) * Sums<D, NT>::kShared * 4 + 127) & ~127u);
+    const uint32_t ring = smem_addr(joins) + (((uint32_t)(users / 2) * Sums<D, NT>::kShared * 4 + 127) & ~127u);
     const uint32_t v_ring = ring + (uint32_t)p.slots * p.kl.bytes;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const Batch &b = p.b;
@@ -406,13 +415,14 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
         aux.cut[0].last = aux.cut[1].last = aux.cut[0].stored = aux.cut[1].stored = aux.cut[0].rows.rows = 0;
         mbar_init(smem_addr(&aux.sync), users);
         for (int i = 0; i < p.slots; i++) {
-            mbar_init(smem_addr(&aux.k_full[i]), 1);
-            mbar_init(smem_addr(&aux.v_full[i]), 1);
+            mbar_init(smem_addr(&aux.k_full[i]), F::kLoaders / 2);
+            mbar_init(smem_addr(&aux.v_full[i]), F::kLoaders / 2);
             mbar_init(smem_addr(&aux.k_empty[i]), users);
             mbar_init(smem_addr(&aux.v_empty[i]), users);
         }
-        for (int i = 0; i < heads; i++) {
-            mbar_init(smem_addr(&aux.join_full[i]), max(split - 1, 1));
+        for (int i = 0; i < 8; i++) {
+            mbar_init(smem_addr(&aux.join_first[i]), 1);
+            mbar_init(smem_addr(&aux.join_full[i]), 1);
             mbar_init(smem_addr(&aux.join_free[i]), 1);
         }
         mbar_init_fence();
@@ -429,22 +439,23 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     __syncwarp();
     if (!any) {
         // nothing to do: on to the common exit
-    } else if (warp < 2) {
+    } else if (warp < F::kLoaders) {
         // ---- rows of keys, rows of values ----
-        const CUtensorMap *const map = warp ? &v_map : &k_map, *const scale_map = warp ? &vs_map : &ks_map;
-        const Place4 &place = warp ? p.vl : p.kl;
-        const uint32_t to = warp ? v_ring : ring, bytes = warp ? v_tile : k_tile;
-        const uint64_t *const full = warp ? aux.v_full : aux.k_full, *const empty = warp ? aux.v_empty : aux.k_empty;
+        const bool v = warp & 1;
+        const CUtensorMap *const map = v ? &v_map : &k_map, *const scale_map = v ? &vs_map : &ks_map;
+        const Place4 &place = v ? p.vl : p.kl;
+        const uint32_t to = v ? v_ring : ring, bytes = v ? v_tile : k_tile;
+        const uint64_t *const full = v ? aux.v_full : aux.k_full, *const empty = v ? aux.v_empty : aux.k_empty;
         int it = 0, s = 0, at = 0;
         uint32_t phase = 1;
-        Tile tile, next;
+        Tile<F::kLoaders / 2> tile, next;
         // the tile after the one that it was called for last
-        const auto ahead = [&](Tile &t) {
+        const auto ahead = [&](Tile<F::kLoaders / 2> &t) {
             while (at >= first.n || first.u.tiles == 0) {
                 at = 0;
                 if (!first.next(b)) return false;
             }
-            t.start(p, first, at++, tile_keys, heads);
+            t.start(p, first, at++, tile_keys, heads, warp >> 1);
             return true;
         };
         bool more = ahead(next);
@@ -452,11 +463,11 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
             tile = next;
             more = ahead(next);
             if (it++ >= p.slots && !wait.warp(smem_addr(&empty[s]), phase)) break;
-            tile.load(p, map, scale_map, warp ? dv : dk, place, to + s * bytes, smem_addr(&full[s]), warp == 0);
+            tile.load(p, map, scale_map, v ? dv : dk, place, to + s * bytes, smem_addr(&full[s]), !v);
             if (++s == p.slots) s = 0, phase ^= 1;
         }
-    } else if (warp < users + 2) {
-        const int me = warp - 2, h = me / split, part = me - h * split;
+    } else if (warp < users + F::kLoaders) {
+        const int me = warp - F::kLoaders, h = me / split, part = me - h * split;
         bool ok = true;
         const int n = lane >> 2, t = lane & 3;
         const uint32_t order = H ? order_of(kPitch) : p.order;
@@ -735,19 +746,31 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
                 for (int i = 0; i < 2; i++)
 #pragma unroll
                     for (int d = 4; d < 32; d *= 2) l[x][i] += __shfl_xor_sync(0xffffffffu, l[x][i], d);
-            // ---- the warps of a head join: the others leave their sums, and go on ----
-            const auto left = [&](int k) { return joins + (h * (split - 1) + k) * Sums<D, NT>::kShared; };
-            if (part > 0) {
-                if (joined++ && !wait.warp(smem_addr(&aux.join_free[h]), (joined - 2) & 1)) break;
-                sums.template store<true>(left(part - 1), rows);
-                warp_arrive(smem_addr(&aux.join_full[h]));
-                continue;
+            // ---- the warps of a head join, the upper half of them to the lower one and so on; who has left its sums goes on.  Of the
+            // head's split / 2 places warp j reads place j in the first round, and leaves its own sums there in a later one ----
+            bool gone = false;
+#pragma unroll 1
+            for (int half = split / 2; half > 0 && !gone; half /= 2) {
+                const bool first_round = half == split / 2;
+                gone = part >= half;
+                const int j = first_round ? part & (half - 1) : gone ? part : part + half, place = h * (split / 2) + j;
+                float *const at = joins + place * Sums<D, NT>::kShared;
+                const uint32_t full = smem_addr(first_round ? &aux.join_first[place] : &aux.join_full[place]);
+                if (gone) {
+                    if (first_round && joined && !wait.warp(smem_addr(&aux.join_free[place]), (joined - 1) & 1)) ok = false;
+                    if (!ok) break;
+                    sums.template store<true>(at, rows);
+                    warp_arrive(full);
+                } else {
+                    if (!wait.warp(full, joined & 1)) ok = false;
+                    if (!ok) break;
+                    sums.join(at, rows);
+                    if (!first_round || part == 0) warp_arrive(smem_addr(&aux.join_free[place]));
+                }
             }
-            if (split > 1) {
-                if (!wait.warp(smem_addr(&aux.join_full[h]), joined++ & 1)) break;
-                sums.join(left, split - 1, rows);
-                warp_arrive(smem_addr(&aux.join_free[h]));
-            }
+            joined++;
+            if (!ok) break;
+            if (gone) continue;
             if (!w.whole()) {
                 // the last of the CTA's heads to be in the workspace counts the piece; who counts the last one joins them all in the end
                 const Cut cut(line, w.pos - w.at.off, unit_cost(w.u));
@@ -824,50 +847,19 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     }
 }
 
+// dev: null to prepare the kernel.
 template <int D, int NT, int H>
-int launch_kernel(const CUtensorMap *map, const FewParams &p, const DeviceInfo *dev, uint32_t bytes, cudaStream_t s)
+int launch_kernel(FewParams p, const DeviceInfo *dev, cudaStream_t s)
 {
+    using F = Few<D, NT, H>;
     const auto kernel = attention_q4_few_kernel<D, NT, H>;
+    constexpr uint32_t kFixed = ((sizeof(Aux) + 127) & ~127u) + F::kWarps * F::kQ, kAll = 227 * 1024;
     if (dev == nullptr) {
-        const int st = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
+        const int st = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAll));
         return st != KV_OK ? st : load_kernels(kernel);
     }
-    return cuda_status(launch(kernel, dim3(dev->num_sms), dim3(Few<D, NT>::kThreads), bytes, s, map[0], map[1], map[2], map[3], p));
-}
-
-// Rows whose heads all come together, a power of two of them.
-template <int D, int NT>
-int launch_full(int heads, const CUtensorMap *map, const FewParams &p, const DeviceInfo *dev, uint32_t bytes, cudaStream_t s)
-{
-    switch (heads) {
-    case 1: return launch_kernel<D, NT, 1>(map, p, dev, bytes, s);
-    case 2: return launch_kernel<D, NT, 2>(map, p, dev, bytes, s);
-    case 4: return launch_kernel<D, NT, 4>(map, p, dev, bytes, s);
-    case 8: return launch_kernel<D, NT, 8>(map, p, dev, bytes, s);
-    default: return launch_kernel<D, NT, NT == 1 ? 16 : 8>(map, p, dev, bytes, s);
-    }
-}
-
-// dev: null to prepare the kernels.
-template <int D, int NT>
-int launch_few(FewParams &p, const DeviceInfo *dev, cudaStream_t s)
-{
-    using F = Few<D, NT>;
-    constexpr uint32_t kFixed = ((sizeof(Aux) + 127) & ~127u) + F::kWarps * F::kQ, kAll = 227 * 1024;
-    CUtensorMap map[4];
-    if (dev == nullptr) {
-        int st = launch_kernel<D, NT, 0>(map, p, dev, kAll, s);
-        for (int h = 1; st == KV_OK && h <= F::kWarps; h *= 2) st = launch_full<D, NT>(h, map, p, dev, kAll, s);
-        return st;
-    }
-    const int all = p.heads_all;
-    int heads = all < F::kWarps ? all : F::kWarps;
-    while (all % heads) heads--;
-    int split = 1;
-    while (2 * split * heads <= F::kWarps) split *= 2;
-    p.unit_heads = heads;
-    p.split = split;
-    p.tile = 16 * split * F::kSteps;
+    const int all = p.heads_all, heads = p.unit_heads;
+    p.tile = 16 * p.split * F::kSteps;
     p.piece_rows = piece_rows(p.k.desc->block_size, p.tile < 256 ? p.tile : 256);
     // A run of rows ends on a multiple of 128 bytes, where a TMA may begin; its rows lie 32 or 96 bytes off one where that allows it.
     const auto pitch = [&](int bytes) {
@@ -878,7 +870,7 @@ int launch_few(FewParams &p, const DeviceInfo *dev, cudaStream_t s)
         Place4 l = {};
         const int codes = heads * plane.dim / 2, row = plane.desc->row_bytes;
         l.apart = heads < all;
-        l.dense = !l.apart && plane.desc->token_stride == row && row * p.piece_rows % 128 == 0;
+        l.dense = dense_rows(p, plane);
         l.base = plane.base;
         l.block_stride = plane.desc->block_stride;
         if (l.apart) {
@@ -896,10 +888,11 @@ int launch_few(FewParams &p, const DeviceInfo *dev, cudaStream_t s)
     p.kl = place(p.k);
     p.vl = place(p.v);
     p.order = order_of(p.kl.codes);
-    const uint32_t pair = (uint32_t)(p.kl.bytes + p.vl.bytes), join = ((uint32_t)heads * (split - 1) * Sums<D, NT>::kShared * 4 + 127) & ~127u;
+    const uint32_t pair = (uint32_t)(p.kl.bytes + p.vl.bytes), join = ((uint32_t)(heads * p.split / 2) * Sums<D, NT>::kShared * 4 + 127) & ~127u;
     p.slots = (int)((kAll - kFixed - join - 128) / pair);
     if (p.slots > kMaxSlots) p.slots = kMaxSlots;
-    if (p.slots < 1 || dev->num_sms * kMaxHeads * 4 > kCounterBytes) return KV_ERR_UNSUPPORTED;
+    if (p.slots < 1 || dev->num_sms * 2 * 4 > kCounterBytes) return KV_ERR_UNSUPPORTED;
+    CUtensorMap map[4];
     int st;
     if ((st = make_row_map(&map[0], p.k.base, p.k.desc, p.kl.codes, p.piece_rows)) != KV_OK) return st;
     if ((st = make_row_map(&map[1], p.v.base, p.v.desc, p.vl.codes, p.piece_rows)) != KV_OK) return st;
@@ -911,8 +904,33 @@ int launch_few(FewParams &p, const DeviceInfo *dev, cudaStream_t s)
     p.b.tile_shift = 0;
     while ((1 << p.b.tile_shift) < p.tile) p.b.tile_shift++;
     const uint32_t bytes = kFixed + join + 128 + p.slots * pair;
-    const bool full = p.kl.dense && p.vl.dense && p.k.dim == D && p.v.dim == D && (heads & (heads - 1)) == 0;
-    return full ? launch_full<D, NT>(heads, map, p, dev, bytes, s) : launch_kernel<D, NT, 0>(map, p, dev, bytes, s);
+    return cuda_status(launch(kernel, dim3(dev->num_sms), dim3(F::kThreads), bytes, s, map[0], map[1], map[2], map[3], p));
+}
+
+// dev: null to prepare the kernels.
+template <int D, int NT>
+int launch_few(FewParams &p, const DeviceInfo *dev, cudaStream_t s)
+{
+    constexpr int kWarps = Few<D, NT, 0>::kWarps;
+    int (*const full[])(FewParams, const DeviceInfo *, cudaStream_t) = {launch_kernel<D, NT, 1>, launch_kernel<D, NT, 2>, launch_kernel<D, NT, 4>,
+                                                                       launch_kernel<D, NT, 8>, launch_kernel<D, NT, kWarps>};
+    if (dev == nullptr) {
+        int st = launch_kernel<D, NT, 0>(p, dev, s);
+        for (int i = 0; st == KV_OK && i < 5; i++) st = full[i](p, dev, s);
+        return st;
+    }
+    const int all = p.heads_all;
+    int heads = all < kWarps ? all : kWarps;
+    while (all % heads) heads--;
+    p.unit_heads = heads;
+    p.split = 1;
+    while (2 * p.split * heads <= kWarps) p.split *= 2;
+    int at = 0;
+    while (1 << at < heads) at++;
+    // runs of rows as long as the shortest tile allows, in every page
+    p.piece_rows = piece_rows(p.k.desc->block_size, 16 * p.split);
+    return 1 << at == heads && p.k.dim == D && p.v.dim == D && dense_rows(p, p.k) && dense_rows(p, p.v) ? full[at](p, dev, s)
+                                                                                                        : launch_kernel<D, NT, 0>(p, dev, s);
 }
 
 }  // namespace
