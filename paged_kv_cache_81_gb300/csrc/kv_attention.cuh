@@ -94,6 +94,7 @@ struct Output {
     float *lse;
     int32_t heads, dv;
     float scale, c;
+    float values = 1.0f;  // what outputs are multiplied by at the end
 };
 
 // Joins rows [row0, row0 + rows) of a cut unit from fragments of `stride` floats, or (at.sum) adds fragments up to a
@@ -169,7 +170,7 @@ __device__ __noinline__ void join_rows(const Output p, const Pieces at, int half
                 }
                 continue;
             }
-            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+            const float inv = (l > 0.0f ? 1.0f / l : 0.0f) * p.values;
 #pragma unroll
             for (int k = 0; k < kBatch; k++)
                 if (k < quads && half * DV + (q + k) * 4 < p.dv) {

@@ -7,8 +7,9 @@ namespace pkv {
 
 int preload_q4_kernels()
 {
-    const int st = preload_q4_few64_kernels();
-    return st != KV_OK ? st : preload_q4_few128_kernels();
+    int st = preload_q4_few64_kernels();
+    if (st == KV_OK) st = preload_q4_few128_kernels();
+    return st != KV_OK ? st : preload_q4_many_kernels();
 }
 
 }  // namespace pkv
@@ -39,9 +40,12 @@ int kv_attention_q4(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_
     if ((st = check_rows(out, out_token_stride, out_head_stride)) != KV_OK) return st;
     if (workspace == nullptr) return KV_ERR_INVALID_ARG;
     if (!aligned16(workspace) || ((uintptr_t)lse & 3u)) return KV_ERR_ALIGN;
+    // by the rows that a request has on average
+    const bool many = batch->n_tokens * group > 16ll * batch->n_reqs;
     const int rows = batch->n_tokens * group <= 8ll * batch->n_reqs ? 8 : 16;
     Q4Params p = {};
-    if ((st = fill_batch(&p.b, batch, d->n_heads, d->n_kv_heads, k->block_size, group > rows ? rows : rows / group * group, 5, d->causal, d->window)) != KV_OK)
+    if ((st = fill_batch(&p.b, batch, d->n_heads, d->n_kv_heads, k->block_size, many ? q4_unit_rows(group) : group > rows ? rows : rows / group * group,
+                         many ? q4_tile_shift() : 5, d->causal, d->window)) != KV_OK)
         return st;
     const DeviceInfo *dev = current_device();
     if (dev == nullptr) return KV_ERR_CUDA;
@@ -67,6 +71,7 @@ int kv_attention_q4(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_
     p.v_scale = v_scale;
     p.counters = (int *)workspace;
     p.ws = (float *)((char *)workspace + kCounterBytes);
+    if (many) return run_q4_many(d->dtype == KV_BF16, p, batch, *dev, (cudaStream_t)stream);
     const auto few = d->head_dim <= 64 && d->head_dim_v <= 64 ? run_q4_few64 : run_q4_few128;
     return few(d->dtype == KV_BF16, p, rows, *dev, (cudaStream_t)stream);
 }

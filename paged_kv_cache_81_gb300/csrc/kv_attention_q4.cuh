@@ -35,6 +35,11 @@ int run_q4_few64(bool bf16, const Q4Params &p, int rows, const DeviceInfo &dev, 
 int run_q4_few128(bool bf16, const Q4Params &p, int rows, const DeviceInfo &dev, cudaStream_t s);
 int preload_q4_few64_kernels();
 int preload_q4_few128_kernels();
+// Units of whole tokens of up to 256 rows, key tiles of 2^q4_tile_shift() (kv_attention_q4_many.cu).
+int q4_unit_rows(int group);
+int q4_tile_shift();
+int run_q4_many(bool bf16, const Q4Params &p, const kv_attn_batch *batch, const DeviceInfo &dev, cudaStream_t s);
+int preload_q4_many_kernels();
 int preload_q4_kernels();      // kv_attention_q4.cu
 
 }  // namespace pkv
