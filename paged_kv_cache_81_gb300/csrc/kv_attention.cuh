@@ -105,7 +105,7 @@ struct Output {
 // CTA came last.  Row r is (first + r) / group of the request's tokens from q0 on, head head0 + the
 // rest.  Not inlined: its registers would crowd the loop over the key tiles.
 template <int DV, bool Bf16>
-__device__ __noinline__ void join_rows(const Output p, const Pieces at, int half, int row0, int rows, int stat, int first, int q0, int head0,
+__device__ PKV_APART void join_rows(const Output p, const Pieces at, int half, int row0, int rows, int stat, int first, int q0, int head0,
                                        const FastDiv group)
 {
     // rows rounded up to a power of two; the other threads share out the columns (at least one quad each)

@@ -11,18 +11,20 @@ namespace pkv {
 namespace {
 
 constexpr int kLeast = 4;  // tiles of a piece of a unit, at least (a join costs as much as three or four more tiles: 3 to 5 us)
-constexpr int kThreads = 384;
+constexpr int kThreads = 384, kRowsThreads = 512;
 constexpr int kRows = 256;  // rows of a unit, at most: 2 * floor(128 / group) tokens of a group
 constexpr int kTileShift = 7, kTile = 1 << kTileShift;  // keys of a tile
 constexpr uint32_t kPanel = 128 * 128;  // bytes of a 64-element panel of 128 rows
 
-template <int DK, int DV>
+// Staged: with room for packed rows.
+template <int DK, int DV, bool Staged = false>
 struct Shape {
     static constexpr uint32_t kQ = 128 * DK * 2, kK = 128 * DK * 2, kV = 128 * DV * 2;
-    static constexpr int kNK = DK == 64 ? 5 : DK == 128 ? 3 : 2;  // ring depths: what 227 KB holds
-    static constexpr int kNV = DK == 64 ? 5 : DK == 128 ? 2 : 1;  // (192: four single panels of K and two tiles of V ran 7% slower)
+    static constexpr int kNK = Staged ? 2 : DK == 64 ? 5 : DK == 128 ? 3 : 2;  // ring depths: what 227 KB holds
+    static constexpr int kNV = Staged ? 2 : DK == 64 ? 5 : DK == 128 ? 2 : 1;  // (192: four single panels of K and two tiles of V ran 7% slower)
     static constexpr uint32_t kOffK = 2 * kQ, kOffV = kOffK + kNK * kK, kOffAux = kOffV + kNV * kV;
     static constexpr uint32_t kBytes = kOffAux + 2048;
+    static constexpr uint32_t kOffStage = kBytes, kStage = 227 * 1024 - kOffStage;  // where Staged
 };
 
 struct AttentionParams {
@@ -39,10 +41,12 @@ struct AttentionParams {
     int *counters;
 };
 
-// Keys and values that are rows of another kind are put into the tiles by three warps.
+// Keys and values of another kind than 16-bit rows: their packed rows come by TMA into a stage of `stages` slots, keys and values in
+// turn, and four warps more make tiles of them.
 template <typename Rows>
 struct RowsParams : AttentionParams {
     Rows k, v;
+    int32_t stages;
 };
 struct NoRows {};
 template <typename Rows>
@@ -50,9 +54,9 @@ using KernelParams = std::conditional_t<std::is_same_v<Rows, NoRows>, AttentionP
 
 // Bookkeeping at the end of shared memory.
 struct Aux {
-    uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
+    uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5], stage_full[4], stage_empty[4];
     uint64_t s_full[2], p_ready[2], o_done[2], q_full, q_empty, merge_ready, merge_free, join[2];
-    int scan[48];
+    int scan[64];
     Place place;
     float m[128], l[128];  // the odd tiles' group, for the join
     uint32_t tmem;
@@ -115,16 +119,17 @@ __device__ __forceinline__ void load_queries(const AttentionParams &p, const CUt
     __syncwarp();
 }
 
-// Rows: NoRows where K and V come by TMA.  Otherwise rows of another kind: warps 0, 2 and 3 put them into the tiles, and warp 1 loads Q,
-// as soon as the weights of the unit before show that its last scores are out.
+// Rows: NoRows where tiles of K and V come by TMA.  Otherwise rows of another kind: warps 0 and 2 load them packed (k_scale_map, v_scale_map
+// are for them alone), and warps 12 to 15 make the tiles.  Those 512 threads have 128 registers each; the softmax groups take
+// 168, the others give theirs away, and as no function can be called then, PKV_APART has to be inline.
 template <int DK, int DV, bool Bf16, typename Rows>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(std::is_same_v<Rows, NoRows> ? kThreads : kRowsThreads, 1)
 attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
-                 const __grid_constant__ CUtensorMap v_map, const KernelParams<Rows> p)
+                 const __grid_constant__ CUtensorMap v_map, const __grid_constant__ KernelParams<Rows> p)
 {
     constexpr bool kRowsKind = !std::is_same_v<Rows, NoRows>;
-    constexpr int kFull = kRowsKind ? 3 : 1;  // arrivals that fill a tile
-    using S = Shape<DK, DV>;
+    constexpr int kFull = kRowsKind ? 4 : 1;  // arrivals that fill a tile
+    using S = Shape<DK, DV, kRowsKind>;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t base = smem_addr(smem);
     Aux &aux = *reinterpret_cast<Aux *>(smem + S::kOffAux);
@@ -142,20 +147,20 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
             mbar_init(smem_addr(&aux.o_done[i]), 1);
             mbar_init(smem_addr(&aux.join[i]), 4);
         }
+        if (kRowsKind)
+            for (int i = 0; i < 4; i++) mbar_init(smem_addr(&aux.stage_full[i]), 1), mbar_init(smem_addr(&aux.stage_empty[i]), 4);
         mbar_init(smem_addr(&aux.q_full), 1);
         mbar_init(smem_addr(&aux.q_empty), 1);
         mbar_init(smem_addr(&aux.merge_ready), 4);
         mbar_init(smem_addr(&aux.merge_free), 4);
         mbar_init_fence();
         tma_prefetch_map(&q_map);
-        if (!kRowsKind) {
-            tma_prefetch_map(&k_map);
-            tma_prefetch_map(&v_map);
-        }
+        tma_prefetch_map(&k_map);
+        tma_prefetch_map(&v_map);
     }
     if (warp == 3) tmem_alloc(smem_addr(&aux.tmem), 512);
     grid_dep_entry();
-    const Line line = find_place<kThreads>(b, blockIdx.x, gridDim.x, kLeast, aux.scan, &aux.place, blockIdx.x == 0);
+    const Line line = find_place<kRowsKind ? kRowsThreads : kThreads>(b, blockIdx.x, gridDim.x, kLeast, aux.scan, &aux.place, blockIdx.x == 0);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -165,145 +170,8 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
     const bool any = w.start(b, aux.place, line);
     if (!any) {
         // nothing to do: on to the common exit
-    } else if (!kRowsKind && warp == 0) {
-        // ---- keys ----
-        int it = 0;
-        bool ok = true;
-        do {
-            if (w.u.tiles == 0) continue;
-            const int32_t *row = p.table + (int64_t)w.at.req * p.table_stride;
-            for (int t = 0; ok && t < w.n; t++, it++) {
-                const int s = it % S::kNK;
-                ok = load_tile<DK / 64>(p, &k_map, row, (w.u.tile0 + w.at.off + t) * kTile, w.u.lo, w.u.hi, w.at.head, base + S::kOffK + s * S::kK,
-                                        smem_addr(&aux.k_full[s]), [&] { return it < S::kNK || wait.warp(smem_addr(&aux.k_empty[s]), ((it / S::kNK) - 1) & 1); });
-            }
-        } while (ok && w.next(b));
-    } else if (!kRowsKind && warp == 2) {
-        // ---- values ----
-        int it = 0;
-        bool ok = true;
-        do {
-            if (w.u.tiles == 0) continue;
-            const int32_t *row = p.table + (int64_t)w.at.req * p.table_stride;
-            for (int t = 0; ok && t < w.n; t++, it++) {
-                const int s = it % S::kNV;
-                ok = load_tile<DV / 64>(p, &v_map, row, (w.u.tile0 + w.at.off + t) * kTile, w.u.lo, w.u.hi, w.at.head, base + S::kOffV + s * S::kV,
-                                        smem_addr(&aux.v_full[s]), [&] { return it < S::kNV || wait.warp(smem_addr(&aux.v_empty[s]), ((it / S::kNV) - 1) & 1); });
-            }
-        } while (ok && w.next(b));
-    } else if (!kRowsKind && warp == 3) {
-        // ---- queries: as soon as the last scores of the unit before are out ----
-        int units = 0;
-        bool ok = true;
-        do {
-            if (w.u.tiles == 0) continue;
-            if (units && !wait.warp(smem_addr(&aux.q_empty), (units - 1) & 1)) break;
-            units++;
-            load_queries<DK>(p, &q_map, w, half, base, smem_addr(&aux.q_full));
-        } while (ok && w.next(b));
-    } else if (warp == 1) {
-        // ---- matrix products ----
-        constexpr uint32_t qk_desc = mma_desc(Bf16, 128, 128, false), pv_desc = mma_desc(Bf16, 128, DV, true);
-        const uint32_t elected = elect_one();
-        const uint64_t qd = smem_desc(base, 16, 1024), kd = smem_desc(base + S::kOffK, 16, 1024), vd = smem_desc(base + S::kOffV, kPanel, 1024);
-        int it = 0, steps[2] = {0, 0}, units = 0;
-        bool ok = true;
-        const auto queries_of = [&](Walk x, bool more) {  // of the first unit from x on that sees anything
-            while (more && x.u.tiles == 0) more = x.next(b);
-            if (more) load_queries<DK>(p, &q_map, x, half, base, smem_addr(&aux.q_full));
-        };
-        if (kRowsKind) queries_of(w, true);
-        do {
-            if (w.u.tiles == 0) continue;
-            const bool both = w.u.rows > half;
-            const int n = both ? 2 * w.n : w.n;
-            ok = wait.warp(smem_addr(&aux.q_full), units++ & 1);
-            if (!ok) break;
-            tc_fence_after();
-            const auto qk = [&](int i) {
-                const int s = i & 1, kt = it + (both ? i >> 1 : i), slot = kt % S::kNK;
-                if ((!both || s == 0) && !wait.warp(smem_addr(&aux.k_full[slot]), (kt / S::kNK) & 1)) return false;
-                const uint64_t qa = qd + (both && s ? S::kQ >> 4 : 0), ka = kd + slot * (S::kK >> 4);
-#pragma unroll
-                for (int kk = 0; kk < DK / 16; kk++) {
-                    const uint32_t o = ((kk / 4) * kPanel + (kk % 4) * 32) >> 4;
-                    mma_ss(tmem + s * 128, qa + o, ka + o, qk_desc, kk > 0, elected);
-                }
-                if (!both || s == 1) tc_commit(smem_addr(&aux.k_empty[slot]), elected);
-                if (i == n - 1) tc_commit(smem_addr(&aux.q_empty), elected);
-                tc_commit(smem_addr(&aux.s_full[s]), elected);
-                return true;
-            };
-            ok = qk(0) && (n < 2 || qk(1));
-            for (int i = 0; ok && i < n; i++) {
-                const int s = i & 1, vt = it + (both ? i >> 1 : i), slot = vt % S::kNV;
-                ok = wait.warp(smem_addr(&aux.p_ready[s]), steps[s]++ & 1) &&
-                     ((both && s) || wait.warp(smem_addr(&aux.v_full[slot]), (vt / S::kNV) & 1));
-                if (!ok) break;
-                if (kRowsKind && i == n - 1) {
-                    Walk x = w;
-                    const bool more = x.next(b);
-                    queries_of(x, more);
-                }
-                // the tile's runs of 32 keys that some query sees; in them, rows of V that none sees must not reach the
-                // product: they may hold anything (rows of another kind were left out when the tile was made)
-                const int kb = (w.u.tile0 + w.at.off + vt - it) * kTile, q0 = seen_from(w.u, kb), q1 = seen_to(w.u, kb);
-                if (!kRowsKind && !(both && s) && (kb < w.u.lo || kb + kTile > w.u.hi)) {
-                    for (int r = 32 * q0 + (lane >> 3); r < 32 * q1; r += 4)
-                        if (kb + r < w.u.lo || kb + r >= w.u.hi)
-#pragma unroll
-                            for (int h = 0; h < DV / 64; h++)
-                                st_smem16(base + S::kOffV + slot * S::kV + h * kPanel + r * 128 + (lane & 7) * 16, make_uint4(0, 0, 0, 0));
-                    fence_async_smem();
-                    __syncwarp();
-                }
-                tc_fence_after();
-                const uint64_t va = vd + slot * (S::kV >> 4);
-#pragma unroll
-                for (int kk = 0; kk < 8; kk++)
-                    mma_ts(tmem + 256 + s * 128, tmem + s * 128 + 64 + kk * 8, va + kk * (2048 >> 4), pv_desc, i >= 2 || kk > 2 * q0,
-                           elected && kk >= 2 * q0 && kk < 2 * q1);
-                if (!both || s == 1) tc_commit(smem_addr(&aux.v_empty[slot]), elected);
-                tc_commit(smem_addr(&aux.o_done[s]), elected);  // last: the groups wait for it before the CTA ends
-                if (i + 2 < n) ok = qk(i + 2);
-            }
-            it += w.n;
-        } while (ok && w.next(b));
-    } else if (kRowsKind && warp < 4) {
-        // ---- rows of another kind: both planes' of the next tile are on their way while this one's are put down ----
-        if constexpr (kRowsKind) {
-            const int thread = (warp ? warp - 1 : 0) * 32 + lane;
-            int at = 0, ks = 0, vs = 0, it = 0;
-            typename Rows::template Pages<DK> pages;
-            typename Rows::template Raw<DK> k_raw, v_raw;
-            // the pages of the next tile, whose rows fetch() then asks for
-            const auto look = [&] {
-                while (at >= w.n || w.u.tiles == 0) {
-                    at = 0;
-                    if (!w.next(b)) return false;
-                }
-                pages.look(p, w, (w.u.tile0 + w.at.off + at++) * kTile, thread);
-                return true;
-            };
-            bool more = look();
-            if (more) k_raw.fetch(p.k, pages, w.at.head, thread), v_raw.fetch(p.v, pages, w.at.head, thread);
-            for (bool now = more; now; now = more, it++) {
-                more = look();
-                if (it >= S::kNK && !wait.warp(smem_addr(&aux.k_empty[ks]), ((it / S::kNK) - 1) & 1)) break;
-                k_raw.template put<Bf16>(base + S::kOffK + ks * S::kK, thread);
-                fence_async_smem();
-                warp_arrive(smem_addr(&aux.k_full[ks]));
-                if (++ks == S::kNK) ks = 0;
-                if (more) k_raw.fetch(p.k, pages, w.at.head, thread);
-                if (it >= S::kNV && !wait.warp(smem_addr(&aux.v_empty[vs]), ((it / S::kNV) - 1) & 1)) break;
-                v_raw.template put<Bf16>(base + S::kOffV + vs * S::kV, thread);
-                fence_async_smem();
-                warp_arrive(smem_addr(&aux.v_full[vs]));
-                if (++vs == S::kNV) vs = 0;
-                if (more) v_raw.fetch(p.v, pages, w.at.head, thread);
-            }
-        }
-    } else {
+    } else if (warp >= 4 && warp < 12) {
+        if (kRowsKind) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         // ---- softmax: group g, a thread per row ----
         const int g = (warp - 4) >> 2, t = tid & 127;
         const uint32_t mine = (uint32_t)((warp & 3) * 32) << 16;
@@ -518,6 +386,150 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
             }
         } while (w.next(b));
         (void)ok;
+    } else {
+        if (kRowsKind) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (!kRowsKind && warp == 0) {
+        // ---- keys ----
+        int it = 0;
+        bool ok = true;
+        do {
+            if (w.u.tiles == 0) continue;
+            const int32_t *row = p.table + (int64_t)w.at.req * p.table_stride;
+            for (int t = 0; ok && t < w.n; t++, it++) {
+                const int s = it % S::kNK;
+                ok = load_tile<DK / 64>(p, &k_map, row, (w.u.tile0 + w.at.off + t) * kTile, w.u.lo, w.u.hi, w.at.head, base + S::kOffK + s * S::kK,
+                                        smem_addr(&aux.k_full[s]), [&] { return it < S::kNK || wait.warp(smem_addr(&aux.k_empty[s]), ((it / S::kNK) - 1) & 1); });
+            }
+        } while (ok && w.next(b));
+    } else if (!kRowsKind && warp == 2) {
+        // ---- values ----
+        int it = 0;
+        bool ok = true;
+        do {
+            if (w.u.tiles == 0) continue;
+            const int32_t *row = p.table + (int64_t)w.at.req * p.table_stride;
+            for (int t = 0; ok && t < w.n; t++, it++) {
+                const int s = it % S::kNV;
+                ok = load_tile<DV / 64>(p, &v_map, row, (w.u.tile0 + w.at.off + t) * kTile, w.u.lo, w.u.hi, w.at.head, base + S::kOffV + s * S::kV,
+                                        smem_addr(&aux.v_full[s]), [&] { return it < S::kNV || wait.warp(smem_addr(&aux.v_empty[s]), ((it / S::kNV) - 1) & 1); });
+            }
+        } while (ok && w.next(b));
+    } else if (warp == 3) {
+        // ---- queries: as soon as the last scores of the unit before are out ----
+        int units = 0;
+        bool ok = true;
+        do {
+            if (w.u.tiles == 0) continue;
+            if (units && !wait.warp(smem_addr(&aux.q_empty), (units - 1) & 1)) break;
+            units++;
+            load_queries<DK>(p, &q_map, w, half, base, smem_addr(&aux.q_full));
+        } while (ok && w.next(b));
+    } else if (warp == 1) {
+        // ---- matrix products ----
+        constexpr uint32_t qk_desc = mma_desc(Bf16, 128, 128, false), pv_desc = mma_desc(Bf16, 128, DV, true);
+        const uint32_t elected = elect_one();
+        const uint64_t qd = smem_desc(base, 16, 1024), kd = smem_desc(base + S::kOffK, 16, 1024), vd = smem_desc(base + S::kOffV, kPanel, 1024);
+        int it = 0, steps[2] = {0, 0}, units = 0;
+        bool ok = true;
+        do {
+            if (w.u.tiles == 0) continue;
+            const bool both = w.u.rows > half;
+            const int n = both ? 2 * w.n : w.n;
+            ok = wait.warp(smem_addr(&aux.q_full), units++ & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const auto qk = [&](int i) {
+                const int s = i & 1, kt = it + (both ? i >> 1 : i), slot = kt % S::kNK;
+                if ((!both || s == 0) && !wait.warp(smem_addr(&aux.k_full[slot]), (kt / S::kNK) & 1)) return false;
+                const uint64_t qa = qd + (both && s ? S::kQ >> 4 : 0), ka = kd + slot * (S::kK >> 4);
+#pragma unroll
+                for (int kk = 0; kk < DK / 16; kk++) {
+                    const uint32_t o = ((kk / 4) * kPanel + (kk % 4) * 32) >> 4;
+                    mma_ss(tmem + s * 128, qa + o, ka + o, qk_desc, kk > 0, elected);
+                }
+                if (!both || s == 1) tc_commit(smem_addr(&aux.k_empty[slot]), elected);
+                if (i == n - 1) tc_commit(smem_addr(&aux.q_empty), elected);
+                tc_commit(smem_addr(&aux.s_full[s]), elected);
+                return true;
+            };
+            ok = qk(0) && (n < 2 || qk(1));
+            for (int i = 0; ok && i < n; i++) {
+                const int s = i & 1, vt = it + (both ? i >> 1 : i), slot = vt % S::kNV;
+                ok = wait.warp(smem_addr(&aux.p_ready[s]), steps[s]++ & 1) &&
+                     ((both && s) || wait.warp(smem_addr(&aux.v_full[slot]), (vt / S::kNV) & 1));
+                if (!ok) break;
+                // the tile's runs of 32 keys that some query sees; in them, rows of V that none sees must not reach the
+                // product: they may hold anything (rows of another kind were left out when the tile was made)
+                const int kb = (w.u.tile0 + w.at.off + vt - it) * kTile, q0 = seen_from(w.u, kb), q1 = seen_to(w.u, kb);
+                if (!kRowsKind && !(both && s) && (kb < w.u.lo || kb + kTile > w.u.hi)) {
+                    for (int r = 32 * q0 + (lane >> 3); r < 32 * q1; r += 4)
+                        if (kb + r < w.u.lo || kb + r >= w.u.hi)
+#pragma unroll
+                            for (int h = 0; h < DV / 64; h++)
+                                st_smem16(base + S::kOffV + slot * S::kV + h * kPanel + r * 128 + (lane & 7) * 16, make_uint4(0, 0, 0, 0));
+                    fence_async_smem();
+                    __syncwarp();
+                }
+                tc_fence_after();
+                const uint64_t va = vd + slot * (S::kV >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 8; kk++)
+                    mma_ts(tmem + 256 + s * 128, tmem + s * 128 + 64 + kk * 8, va + kk * (2048 >> 4), pv_desc, i >= 2 || kk > 2 * q0,
+                           elected && kk >= 2 * q0 && kk < 2 * q1);
+                if (!both || s == 1) tc_commit(smem_addr(&aux.v_empty[slot]), elected);
+                tc_commit(smem_addr(&aux.o_done[s]), elected);  // last: the groups wait for it before the CTA ends
+                if (i + 2 < n) ok = qk(i + 2);
+            }
+            it += w.n;
+        } while (ok && w.next(b));
+    } else if (kRowsKind && warp < 12) {
+        // ---- packed rows of keys (warp 0) and of values (warp 2) ----
+        if constexpr (kRowsKind) {
+            const bool v = warp == 2;
+            const Rows &rows = v ? p.v : p.k;
+            int slot = v ? 1 : 0, turn = 0;
+            bool ok = true;
+            do {
+                if (w.u.tiles == 0) continue;
+                const int32_t *row = p.table + (int64_t)w.at.req * p.table_stride;
+                for (int t = 0; ok && t < w.n; t++) {
+                    ok = rows.load(p, v ? &v_map : &k_map, row, (w.u.tile0 + w.at.off + t) * kTile, w.u.lo, w.u.hi, w.at.head,
+                                   base + S::kOffStage + slot * rows.stage_bytes, smem_addr(&aux.stage_full[slot]), !v,
+                                   [&] { return turn == 0 || wait.warp(smem_addr(&aux.stage_empty[slot]), (turn - 1) & 1); });
+                    if ((slot += 2) >= p.stages) slot -= p.stages, turn++;
+                }
+            } while (ok && w.next(b));
+        }
+    } else if (kRowsKind) {
+        // ---- tiles of them ----
+        if constexpr (kRowsKind) {
+            const int thread = tid - 384;
+            int slot = 0, turn = 0, it = 0;
+            bool ok = true;
+            do {
+                if (w.u.tiles == 0) continue;
+                for (int t = 0; ok && t < w.n; t++, it++) {
+                    const int kb = (w.u.tile0 + w.at.off + t) * kTile;
+#pragma unroll 1
+                    for (int v = 0; v < 2; v++) {
+                        static_assert(!kRowsKind || S::kNK == S::kNV, "one ring depth");
+                        constexpr int depth = S::kNK;
+                        const int to = it % depth;
+                        const uint32_t full = smem_addr(v ? &aux.v_full[to] : &aux.k_full[to]), empty = smem_addr(v ? &aux.v_empty[to] : &aux.k_empty[to]);
+                        const Rows &rows = v ? p.v : p.k;
+                        ok = (it < depth || wait.warp(empty, (it / depth - 1) & 1)) && wait.warp(smem_addr(&aux.stage_full[slot]), turn & 1);
+                        if (!ok) break;
+                        rows.template unpack<DK, Bf16>(base + S::kOffStage + slot * rows.stage_bytes, base + (v ? S::kOffV + to * S::kV : S::kOffK + to * S::kK),
+                                                       w.at.head, w.u.lo - kb, w.u.hi - kb, thread);
+                        fence_async_smem();
+                        warp_arrive(full);
+                        if (lane == 0) mbar_arrive(smem_addr(&aux.stage_empty[slot]));
+                        if (++slot == p.stages) slot = 0, turn++;
+                    }
+                }
+            } while (ok && w.next(b));
+        }
+    }
     }
     // common exit
     __syncwarp();

@@ -30,6 +30,19 @@ struct Q4Params {
     int *counters;
 };
 
+// Bytes that the barrier's phase waits for, without an arrival.
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// An untiled copy: addresses and size multiples of 16.
+__device__ __forceinline__ void bulk_load(uint32_t dst, uint64_t src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
 // Units of `rows` rows, 8 or 16, of heads of at most 64 and of 128 elements (kv_attention_q4_few64.cu, kv_attention_q4_few128.cu).
 int run_q4_few64(bool bf16, const Q4Params &p, int rows, const DeviceInfo &dev, cudaStream_t s);
 int run_q4_few128(bool bf16, const Q4Params &p, int rows, const DeviceInfo &dev, cudaStream_t s);

@@ -47,6 +47,18 @@ int make_map(CUtensorMap *map, uint64_t base, int rank, const uint64_t *dims, co
     return r == CUDA_SUCCESS ? KV_OK : KV_ERR_UNSUPPORTED;
 }
 
+int make_q4_code_map(CUtensorMap *map, uint64_t base, const kv_cache_desc *c, int heads, int dim, int bytes, int rows)
+{
+    const EncodeFn fn = encoder();
+    if (fn == nullptr) return KV_ERR_CUDA;
+    const cuuint64_t dims[4] = {(cuuint64_t)dim / 8, (cuuint64_t)heads, (cuuint64_t)c->block_size, (cuuint64_t)c->num_blocks};
+    const cuuint64_t strides[3] = {(cuuint64_t)dim / 2, (cuuint64_t)c->token_stride, (cuuint64_t)c->block_stride};
+    const cuuint32_t box[4] = {(cuuint32_t)bytes / 4, 1, (cuuint32_t)rows, 1}, one[4] = {1, 1, 1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, (void *)base, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? KV_OK : KV_ERR_UNSUPPORTED;
+}
+
 int make_row_map(CUtensorMap *map, uint64_t base, const kv_cache_desc *c, int bytes, int rows)
 {
     const EncodeFn fn = encoder();

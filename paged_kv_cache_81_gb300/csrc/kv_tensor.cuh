@@ -14,6 +14,11 @@
 #include "kv_async.cuh"
 #include "kv_common.cuh"
 
+// Code that is called seldom and kept out of its callers' registers.  A kernel that changes its warps' registers cannot call.
+#ifndef PKV_APART
+#define PKV_APART __noinline__
+#endif
+
 namespace pkv {
 
 // ---------------------------------------------------------------------------
@@ -31,7 +36,7 @@ struct Waiter {
         if (mbar_try_wait(bar, parity)) return true;
         return slow(bar, parity);
     }
-    __device__ __noinline__ bool slow(uint32_t bar, uint32_t parity) const
+    __device__ PKV_APART bool slow(uint32_t bar, uint32_t parity) const
     {
         const unsigned long long t0 = now_ns();
         while (!mbar_try_wait(bar, parity)) {
@@ -340,6 +345,10 @@ int make_map(CUtensorMap *map, uint64_t base, int rank, const uint64_t *dims, co
 // A map of one plane of one tensor of a paged cache as (element of a head, head, slot, block); a load
 // brings 64 elements of one head of `rows` consecutive slots of a block.
 int make_cache_map(CUtensorMap *map, const kv_cache_desc *c, int tensor, int plane, int heads, int head_dim, int rows);
+
+// A map of the codes of 4-bit rows as (32-bit word of a head's codes, head, slot, block), without a swizzle; a load brings one head's
+// codes of `rows` consecutive slots of a block, `bytes` apart, with zeros past their end.
+int make_q4_code_map(CUtensorMap *map, uint64_t base, const kv_cache_desc *c, int heads, int dim, int bytes, int rows);
 
 // A map of a plane's rows as opaque 32-bit words (64-bit ones for boxes of more than 1024 bytes), (word of a row, slot, block), without a
 // swizzle; a load brings `bytes` of each of `rows` consecutive slots of a block, densely, with zeros for what lies past a row's end.
