@@ -9,6 +9,7 @@
 
 namespace pkv {
 
+constexpr bool kOneJoin = PKV_ONE_JOIN;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int64_t kCounterBytes = KV_ATTENTION_ZEROED_BYTES;  // arrival counts of cut units, zero between calls
 
@@ -184,7 +185,9 @@ __device__ PKV_APART void join_rows(const Output p, const Pieces at, int half, i
     };
     // what the registers beside the tile loop hold; two fragments (a long unit's usual cut) in four trips a row instead
     // of eight: three prefill chunks of 500 to 2000 tokens 117 us, so 114.5
-    if (quads <= 4)
+    if (kOneJoin)  // inlined: short
+        columns(std::integral_constant<int, 4>(), std::integral_constant<int, 2>());
+    else if (quads <= 4)
         columns(std::integral_constant<int, 4>(), std::integral_constant<int, 6>());
     else if (DV == 256)
         columns(std::integral_constant<int, 8>(), std::integral_constant<int, 3>());

@@ -3,9 +3,9 @@
 // kv_attention's kernel (kv_attention.cu) with tiles of 16-bit keys and values that four warps make of packed rows, which come by
 // TMA: a head's codes and the 16 bytes that hold its scales.  A thread takes 32 elements of a row (16 bytes of codes, two scales) at a
 // time and writes them as four 16-byte pieces of the swizzled panels.  A code times its scale is exact in fp16 and in bf16, so the
-// products are those of the values that the cache stands for.  fp16: one conversion and one product a pair.  bf16: the
-// conversion gives fp16 pairs; moved three bits down, their exponents stand where bf16's do, 112 too low, and the product with the
-// scale times 2^112 mends that, exactly.
+// products are those of the values that the cache stands for.  fp16: one conversion and one product a pair; bf16 goes through two
+// 32-bit products, which keeps three units busy with it (shifting the fp16 bits into bf16's place took the integer unit 32 cycles
+// a word of codes, this 16).
 #define PKV_APART __forceinline__
 
 #include "kv_attention_kernel.cuh"
@@ -78,18 +78,6 @@ struct Q4Rows {
         return true;
     }
 
-    // Pairs of one scale as the products take them.
-    template <bool Bf16>
-    static __device__ __forceinline__ uint32_t times(uint32_t pair, uint32_t unit)
-    {
-        uint32_t v;
-        if (Bf16)
-            asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(v) : "r"((pair >> 3 & 0x0fff0fffu) | (pair & 0x80008000u)), "r"(unit));
-        else
-            v = mul_f16x2(pair, unit);
-        return v;
-    }
-
     // A staged tile into panels, by 128 threads; rows outside [lo, hi) become zeros, whatever the stage holds there.
     template <int D, bool Bf16>
     __device__ __forceinline__ void unpack(uint32_t stage, uint32_t tile, int head, int lo, int hi, int thread) const
@@ -120,23 +108,26 @@ struct Q4Rows {
         for (int j = 0; j < kTile / kRowsATurn; j++) {
             c = next_c, unit = next_unit;
             if (j + 1 < kTile / kRowsATurn) load(j + 1, next_c, next_unit);
-            uint32_t u = e4m3x2_to_f16(unit), z[2];
+            uint32_t u = e4m3x2_to_f16(unit);
             if (swap) u = u >> 16 | u << 16;
-            if (Bf16) {
-                float a, b;
-                asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(a), "=f"(b) : "r"(u));
-                a *= 0x1p112f, b *= 0x1p112f;
-                z[0] = pack2<true>(a, a), z[1] = pack2<true>(b, b);
-            } else {
-                z[0] = u << 16 | (u & 0xffffu), z[1] = u >> 16 | (u & 0xffff0000u);
-            }
+            const float2 f = f16x2_to_f32(u);
+            const uint32_t z[2] = {u << 16 | (u & 0xffffu), u >> 16 | (u & 0xffff0000u)};
             const uint32_t word[4] = {swap ? c.z : c.x, swap ? c.w : c.y, swap ? c.x : c.z, swap ? c.y : c.w};
 #pragma unroll
             for (int i = 0; i < 4; i++) {
                 uint32_t v[4];
                 q4_to_f16(word[i], v);
-                const uint32_t s = z[i >> 1];
-                st_smem16(at[i] + j * kRowsATurn * 128, make_uint4(times<Bf16>(v[0], s), times<Bf16>(v[1], s), times<Bf16>(v[2], s), times<Bf16>(v[3], s)));
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    if (Bf16) {
+                        const float s = i < 2 ? f.x : f.y;
+                        const float2 x = f16x2_to_f32(v[k]);
+                        v[k] = pack2<true>(x.x * s, x.y * s);
+                    } else {
+                        v[k] = mul_f16x2(v[k], z[i >> 1]);
+                    }
+                }
+                st_smem16(at[i] + j * kRowsATurn * 128, make_uint4(v[0], v[1], v[2], v[3]));
             }
         }
     }

@@ -17,6 +17,9 @@
 // Code that is called seldom and kept out of its callers' registers.  A kernel that changes its warps' registers cannot call.
 #ifndef PKV_APART
 #define PKV_APART __noinline__
+#define PKV_ONE_JOIN 0
+#else
+#define PKV_ONE_JOIN 1
 #endif
 
 namespace pkv {
