@@ -11,6 +11,7 @@
 // once to 32 bits and once to the element type, as a 16-bit cache would hold it, before it is rounded to 4 bits.
 //
 // One CTA a token: its cosines and sines are formed once, into shared memory, and serve every head.
+#include <algorithm>
 #include <cmath>
 
 #include "kv_attention.cuh"
@@ -20,7 +21,8 @@ namespace pkv {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;            // at most
+constexpr int kSmThreads = 1024;         // resident on an SM
 constexpr int kMaxRot = 512;             // rotated elements of a head
 constexpr int kMaxQ4Keys = 16384;        // elements of a token's keys that pass through shared memory
 
@@ -77,7 +79,17 @@ __device__ __forceinline__ float sum2(float x, float y, float &left)
 }
 
 // m cos, m sin of `u` 2^-64 turns: the nearest of 256 table angles and a rest of at most pi / 256, whose sine and cosine
-// take two terms more than themselves.
+// take two terms more than themselves.  In one float each, off by little more than their rounding:
+__device__ __forceinline__ float2 plain_angle_of(uint64_t u, float m)
+{
+    const uint64_t r = u + (1ull << 55);
+    const float4 t = __ldg(reinterpret_cast<const float4 *>(g_turns.v[r >> 56]));
+    const float x = (float)((int32_t)((uint32_t)(r >> 32) & 0xffffffu) - (1 << 23)) * (float)(2 * kPi / 4294967296.0);
+    const float x2 = x * x, s = fmaf(x * x2, -1.0f / 6, x), c = x2 * fmaf(x2, 1.0f / 24, -0.5f);
+    return make_float2(m * (t.x + fmaf(t.x, c, fmaf(-t.y, s, t.z))), m * (t.y + fmaf(t.y, c, fmaf(t.x, s, t.w))));
+}
+
+// ... and in two:
 __device__ __forceinline__ Angle angle_of(uint64_t u, float m)
 {
     const uint64_t r = u + (1ull << 55);
@@ -115,13 +127,49 @@ __device__ __forceinline__ Angle angle_of(uint64_t u, float m)
     return o;
 }
 
-// a c - b s of two-float c and s, rounded once.
-__device__ __forceinline__ float turned(float a, float b, float c, float s, float cl, float sl)
+// Two 32-bit numbers that one instruction adds or multiplies, each result rounded by itself.
+using Two = uint64_t;
+
+__device__ __forceinline__ Two two(float a, float b)
 {
-    const float p = __fmul_rn(a, c), q = __fmul_rn(b, s);
-    float e;
-    const float d = sum2(p, -q, e);
-    return __fadd_rn(d, e + ((fmaf(a, c, -p) - fmaf(b, s, -q)) + fmaf(a, cl, -b * sl)));
+    Two v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    return v;
+}
+__device__ __forceinline__ float2 one_by_one(Two v)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ Two add2(Two a, Two b)
+{
+    Two v;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b)
+{
+    Two v;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c)
+{
+    Two v;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+    return v;
+}
+__device__ __forceinline__ Two neg2(Two a) { return a ^ 0x8000000080000000ull; }
+
+// a c + b s of two-float c and s (what their rounding leaves in cl and sl), rounded once.
+__device__ __forceinline__ Two turned(Two a, Two b, Two c, Two s, Two cl, Two sl)
+{
+    const Two p = mul2(a, c), q = mul2(b, s);
+    const Two d = add2(p, q), t = add2(d, neg2(p));  // d and what its rounding leaves (Knuth)
+    const Two e = add2(add2(p, neg2(add2(d, neg2(t)))), add2(q, neg2(t)));
+    const Two pq = add2(fma2(a, c, neg2(p)), fma2(b, s, neg2(q)));
+    return add2(d, add2(e, add2(pq, fma2(a, cl, mul2(b, sl)))));
 }
 
 // One set of heads: [tokens, heads, dim] rows with byte strides.
@@ -151,10 +199,14 @@ struct Params {
     float magnitude;
     int32_t inverse;
     FastDiv block;
-    FastDiv turn_items;   // items that rotate of a head: 8 pairs each
-    FastDiv plain_items;  // 16-byte pieces of a head that do not
-    FastDiv v_items;
-    FastDiv k_groups, v_groups;  // groups of 16 of a head
+    // what a head consists of: items of 16 elements that rotate (8 pairs), items that do not, groups of 16 for 4 bits
+    int32_t n_turn, n_plain, n_v, k_groups, v_groups;
+    FastDiv by_turn, by_plain, by_v, by_k_groups, by_v_groups;
+    int64_t n_tokens;
+    int32_t step;         // tokens that are worked on at a time
+    FastDiv chunks;       // CTAs that share a token
+    int32_t chunk_heads;  // heads of each, for 4 bits
+    int32_t movers;       // threads that rotate and copy; the others round to 4 bits
     float k_scale, v_scale, k_inv, v_inv;
     int *err;
 };
@@ -173,31 +225,39 @@ template <bool Bf16>
 __device__ __forceinline__ void quantise(const uint4 (&in)[2], float inv, float scale, char *codes, char *unit, char *held)
 {
     const uint32_t w[8] = {in[0].x, in[0].y, in[0].z, in[0].w, in[1].x, in[1].y, in[1].z, in[1].w};
-    float y[16], most = 0.0f;
+    Two y[8];  // the negatives of what is rounded
+    float most = 0.0f;
+    const Two by = two(-inv, -inv);
 #pragma unroll
     for (int i = 0; i < 8; i++) {
         const float2 f = unpack2<Bf16>(w[i]);
-        y[2 * i] = __fmul_rn(f.x, inv), y[2 * i + 1] = __fmul_rn(f.y, inv);
-        most = fmaxf(most, fmaxf(fabsf(y[2 * i]), fabsf(y[2 * i + 1])));
+        y[i] = mul2(two(f.x, f.y), by);
+        const float2 g = one_by_one(y[i]);
+        most = fmaxf(most, fmaxf(fabsf(g.x), fabsf(g.y)));
     }
     const uint32_t b = q4_scale_of(most);
     const uint32_t ss = e4m3x2_to_f16(b * 0x101u);
     const float s = unpack2<false>(ss).x;
     if (most > 6.0f * s * 2) {  // far outside: the largest code, also for infinities
 #pragma unroll
-        for (int i = 0; i < 16; i++) y[i] = fminf(fmaxf(y[i], -12.0f * s), 12.0f * s);
+        for (int i = 0; i < 8; i++) {
+            const float2 f = one_by_one(y[i]);
+            y[i] = two(fminf(fmaxf(f.x, -12.0f * s), 12.0f * s), fminf(fmaxf(f.y, -12.0f * s), 12.0f * s));
+        }
     }
     // y / s: a quotient that is exact where it can be decides the ties.  One step on the product with the reciprocal gives the
     // rounded quotient (Markstein 1990); with these signs it keeps that of a zero.
-    const float r = __frcp_rn(s);
+    const float r = -__frcp_rn(s);
+    const Two rr = two(r, r), s2 = two(s, s);
     uint32_t c[2];
 #pragma unroll
     for (int h = 0; h < 2; h++) {
         float z[8];
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const float z0 = __fmul_rn(y[8 * h + i], r);
-            z[i] = fmaf(fmaf(z0, s, -y[8 * h + i]), -r, z0);
+        for (int i = 0; i < 4; i++) {
+            const Two z0 = mul2(y[4 * h + i], rr);
+            const float2 f = one_by_one(fma2(fma2(z0, s2, y[4 * h + i]), rr, z0));
+            z[2 * i] = f.x, z[2 * i + 1] = f.y;
         }
         c[h] = f32_to_q4(z);
     }
@@ -220,148 +280,288 @@ __device__ __forceinline__ void quantise(const uint4 (&in)[2], float inv, float 
     }
 }
 
+constexpr int kAngles = kMaxRot / 2;
+
+template <bool Q4>
+struct Angles {
+    float v[Q4 ? 4 : 2][kAngles];  // cosines, sines, what their rounding leaves
+};
+
 template <bool Bf16, bool Interleaved, bool Q4>
-__global__ void __launch_bounds__(kThreads) rotate_kernel(const Params p)
+__global__ void __launch_bounds__(kThreads, 2) rotate_kernel(const __grid_constant__ Params p)
 {
-    __shared__ __align__(16) Angle angles[kMaxRot / 2];
-    __shared__ int place[2];  // page and slot of the token, page -1: it has none
+    __shared__ __align__(16) Angles<Q4> angles[2];
+    __shared__ char *rows[4][2];  // a token's rows of keys and values, null: it has none
     extern __shared__ __align__(16) char keys[];
-    const int tid = threadIdx.x;
-    const int64_t tok = blockIdx.x;
-    grid_dep_entry();
-    const int32_t pos = __ldg(p.rope_pos + tok);
-    for (int i = tid; i < p.half; i += kThreads) {
-        Angle a = angle_of((uint64_t)(int64_t)pos * __ldg(p.turns + i), p.magnitude);
-        if (p.inverse) a.s = -a.s, a.sl = -a.sl;
-        angles[i] = a;
+    const int tid = threadIdx.x, threads = blockDim.x;
+    const uint32_t first = fdiv(blockIdx.x, p.chunks), chunk = blockIdx.x - first * p.chunks.d;
+    const int count = (int)(((uint32_t)p.n_tokens - first - 1) / (uint32_t)p.step) + 1;  // of tokens that this CTA works on
+    // The thread's item: two pieces of 16 bytes of a head, `d1` bytes apart, that move together.
+    const bool mover = !Q4 || tid < p.movers;
+    const int h0 = Q4 ? (int)chunk * p.chunk_heads : 0, n_heads = Q4 ? min(p.chunk_heads, p.heads + p.kv_heads - h0) : p.heads + p.kv_heads;
+    const int n_keys = Q4 ? max(min(p.kv_heads - h0, n_heads), 0) : 0;  // key heads of this CTA
+    enum { kNone, kOut, kKeyRow, kValueRow, kKeys, kKeyGroup, kValueGroup } what = kNone;
+    bool turn = false, two_pieces = true;
+    const char *src = nullptr;
+    int64_t in_step = 0, at_out = 0, out_step = 0;  // at_out: from the row, from `keys`, or an address
+    int d1 = 16, n = 0, dim = p.dk;
+    if (mover) {
+        int i = Q4 ? tid : (int)(chunk * threads) + tid, h = 0, o0 = 0;
+        const int turns = n_heads * p.n_turn, plains = n_heads * p.n_plain;
+        if (i < turns) {
+            h = (int)fdiv((uint32_t)i, p.by_turn), n = i - h * p.n_turn;
+            turn = true;
+            o0 = p.offset + n * (Interleaved ? 16 : 8);
+            if (Interleaved)
+                two_pieces = n * 8 + 4 < p.half;
+            else
+                d1 = p.half * 2;
+            what = kOut;
+        } else if ((i -= turns) < plains) {
+            h = (int)fdiv((uint32_t)i, p.by_plain);
+            o0 = (i - h * p.n_plain) * 16;
+            int o1 = o0 + 8;
+            two_pieces = o1 < p.dk - 2 * p.half;
+            if (o0 >= p.offset) o0 += 2 * p.half;
+            if (o1 >= p.offset) o1 += 2 * p.half;
+            d1 = (o1 - o0) * 2;
+            what = kOut;
+        } else if (!Q4 && (i -= plains) < p.kv_heads * p.n_v) {
+            h = (int)fdiv((uint32_t)i, p.by_v);
+            o0 = (i - h * p.n_v) * 16;
+            two_pieces = o0 + 8 < p.dv;
+            src = p.v.in + h * p.v.in_head, in_step = p.v.in_token;
+            at_out = ((int64_t)h * p.dv + o0) * 2;
+            what = kValueRow;
+        }
+        if (what == kOut) {  // keys come before queries
+            const int g = h0 + h - p.kv_heads;
+            if (g < 0) {
+                src = p.k.in + (h0 + h) * p.k.in_head, in_step = p.k.in_token;
+                at_out = ((int64_t)h * p.dk + o0) * 2;
+                what = Q4 ? kKeys : kKeyRow;
+            } else {
+                src = p.q.in + g * p.q.in_head, in_step = p.q.in_token;
+                at_out = (int64_t)(p.q.out + g * p.q.out_head + o0 * 2), out_step = p.q.out_token;
+                if (!turn && p.q.out == p.q.in && out_step == in_step && p.q.out_head == p.q.in_head) what = kNone;  // in place
+            }
+        }
+        src += o0 * 2;
+    } else {
+        const int ks = n_keys * p.k_groups;
+        int i = tid - p.movers;
+        if (i < ks) {
+            at_out = h0 * p.k_groups + i;
+            n = i;
+            out_step = p.k.out_token, what = kKeyGroup;
+        } else if ((i -= ks) < n_keys * p.v_groups) {
+            const int h = (int)fdiv((uint32_t)i, p.by_v_groups);
+            src = p.v.in + (h0 + h) * p.v.in_head + (i - h * p.v_groups) * 32, in_step = p.v.in_token;
+            at_out = h0 * p.v_groups + i;
+            dim = p.dv, out_step = p.v.out_token, what = kValueGroup;
+        }
     }
-    if (tid == kThreads - 1 && p.kv_heads) {
-        const int32_t req = __ldg(p.token_req + tok), at = __ldg(p.token_pos + tok);
-        int page = -1, slot = 0;
+    const bool loads = what != kNone && what != kKeyGroup, group = what >= kKeyGroup, placer = tid == threads - 1 && p.kv_heads;
+    uint4 x = {}, y = {}, nx = {}, ny = {};
+    const auto load = [&](uint4 &a, uint4 &b) {
+        a = *reinterpret_cast<const uint4 *>(src);
+        if (two_pieces) b = *reinterpret_cast<const uint4 *>(src + d1);
+        src += in_step;
+    };
+    const auto form_angles = [&](Angles<Q4> &to, int32_t pos) {
+        for (int i = tid; i < p.half; i += threads) {
+            // four pairs side by side, the halves of the items apart: a warp's reads of 16 bytes are then of one run
+            const int at = (((i >> 2 & 1) * p.n_turn + (i >> 3)) << 2) + (i & 3);
+            const uint64_t u = (uint64_t)(int64_t)pos * __ldg(p.turns + i);
+            if constexpr (Q4) {
+                const Angle a = angle_of(u, p.magnitude);
+                to.v[0][at] = a.c, to.v[1][at] = a.s, to.v[2][at] = a.cl, to.v[3][at] = a.sl;
+            } else {
+                const float2 a = plain_angle_of(u, p.magnitude);
+                to.v[0][at] = a.x, to.v[1][at] = p.inverse ? -a.y : a.y;
+            }
+        }
+    };
+    // a token's page in three steps, so that none waits for the one before: its request and place, its entry, its rows
+    int32_t req = -1, at = -1, slot = 0, entry = -1, pos = 0;
+    const auto read_token = [&](int64_t t) {
+        pos = __ldg(p.rope_pos + t);
+        if (placer) req = __ldg(p.token_req + t), at = __ldg(p.token_pos + t);
+    };
+    const auto read_entry = [&] {
+        entry = -1;
         if (req >= 0 && req < p.n_reqs && at >= 0) {
             const uint32_t col = fdiv((uint32_t)at, p.block);
             if (col < (uint32_t)p.max_blocks) {
-                page = __ldg(p.table + (int64_t)req * p.table_stride + col);
+                entry = __ldg(p.table + (int64_t)req * p.table_stride + col);
                 slot = (int)((uint32_t)at - col * p.block.d);
             }
         }
+    };
+    const auto set_rows = [&](int ring) {
+        int page = entry;
         if (page < 0)
-            set_error(p.err, KV_DERR_TABLE), page = -1;
+            set_error(p.err, KV_DERR_TABLE);
         else if (page >= p.kp.num_blocks || (p.dv && page >= p.vp.num_blocks))
             set_error(p.err, KV_DERR_SLOT), page = -1;
-        place[0] = page, place[1] = slot;
-    }
-    __syncthreads();
-    const int page = p.kv_heads ? place[0] : -1;
-    char *const k_row = p.kp.base + (int64_t)page * p.kp.block_stride + (int64_t)place[1] * p.kp.token_stride;
-    char *const v_row = p.vp.base + (int64_t)page * p.vp.block_stride + (int64_t)place[1] * p.vp.token_stride;
-    // where head h of the queries and, after them, the keys is read and written; false where it is not written
-    const auto head_of = [&](int h, const char *&from, char *&to) {
-        if (h < p.heads) {
-            from = p.q.in + tok * p.q.in_token + h * p.q.in_head;
-            to = p.q.out + tok * p.q.out_token + h * p.q.out_head;
-            return true;
-        }
-        h -= p.heads;
-        from = p.k.in + tok * p.k.in_token + h * p.k.in_head;
-        to = (Q4 ? keys : k_row) + (int64_t)h * p.dk * 2;
-        return Q4 || page >= 0;
+        rows[ring][0] = page < 0 ? nullptr : p.kp.base + (int64_t)page * p.kp.block_stride + (int64_t)slot * p.kp.token_stride;
+        rows[ring][1] = page < 0 ? nullptr : p.vp.base + (int64_t)page * p.vp.block_stride + (int64_t)slot * p.vp.token_stride;
     };
-    const int all = p.heads + p.kv_heads;
-    for (int i = tid; i < all * (int)p.turn_items.d && p.half; i += kThreads) {
-        const int h = (int)fdiv((uint32_t)i, p.turn_items), n = i - h * (int)p.turn_items.d;
-        const char *from;
-        char *to;
-        if (!head_of(h, from, to)) continue;
-        const Angle *a = angles + n * (Interleaved ? 4 : 8);
-        const int at0 = (p.offset + n * 8) * 2, at1 = at0 + (Interleaved ? 0 : p.half * 2);
-        const uint4 x = *reinterpret_cast<const uint4 *>(from + at0), y = Interleaved ? x : *reinterpret_cast<const uint4 *>(from + at1);
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-        const bool exact = Q4 && h >= p.heads;
-        const auto turn = [&](float u, float v, const Angle &g, float &nu, float &nv) {
-            if (exact) {
-                nu = turned(u, v, g.c, g.s, g.cl, g.sl);
-                nv = turned(u, -v, g.s, g.c, g.sl, g.cl);
-            } else {
-                nu = fmaf(u, g.c, -v * g.s);
-                nv = fmaf(u, g.s, v * g.c);
-            }
-        };
-        uint32_t ox[4], oy[4];
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const float2 u = unpack2<Bf16>(xs[j]), v = unpack2<Bf16>(ys[j]);
-            if (Interleaved) {
-                float n0, n1;
-                turn(u.x, u.y, a[j], n0, n1);
-                ox[j] = pack2<Bf16>(n0, n1);
-            } else {
-                float a0, a1, b0, b1;
-                turn(u.x, v.x, a[2 * j], a0, b0);
-                turn(u.y, v.y, a[2 * j + 1], a1, b1);
-                ox[j] = pack2<Bf16>(a0, a1);
-                oy[j] = pack2<Bf16>(b0, b1);
-            }
-        }
-        *reinterpret_cast<uint4 *>(to + at0) = make_uint4(ox[0], ox[1], ox[2], ox[3]);
-        if (!Interleaved) *reinterpret_cast<uint4 *>(to + at1) = make_uint4(oy[0], oy[1], oy[2], oy[3]);
+    grid_dep_entry();
+    int64_t tok = first;
+    read_token(tok);
+    if (loads) src += tok * in_step;
+    if (what == kOut) at_out += tok * out_step;
+    out_step *= p.step;
+    in_step *= p.step;
+    int64_t done = tok * (what == kKeyGroup ? p.k.out_token : p.v.out_token);
+    if (loads && mover) load(x, y);
+    if (placer) {
+        read_entry();
+        set_rows(0);
     }
-    for (int i = tid; i < all * (int)p.plain_items.d && p.half * 2 < p.dk; i += kThreads) {
-        const int h = (int)fdiv((uint32_t)i, p.plain_items);
-        int at = (i - h * (int)p.plain_items.d) * 8;
-        if (at >= p.offset) at += p.half * 2;
-        const char *from;
-        char *to;
-        if (!head_of(h, from, to) || from == to) continue;
-        *reinterpret_cast<uint4 *>(to + at * 2) = *reinterpret_cast<const uint4 *>(from + at * 2);
-    }
-    if (!Q4) {
-        if (page < 0) return;
-        for (int i = tid; i < p.kv_heads * (int)p.v_items.d && p.dv; i += kThreads) {
-            const int h = (int)fdiv((uint32_t)i, p.v_items), at = (i - h * (int)p.v_items.d) * 8;
-            *reinterpret_cast<uint4 *>(v_row + ((int64_t)h * p.dv + at) * 2) =
-                *reinterpret_cast<const uint4 *>(p.v.in + tok * p.v.in_token + h * p.v.in_head + at * 2);
-        }
-        return;
-    }
+    form_angles(angles[0], pos);
+    if (count > 1) read_token(tok + p.step);
     __syncthreads();
-    const int k_count = p.kv_heads * (int)p.k_groups.d, v_count = p.kv_heads * (int)p.v_groups.d;
-    for (int i = tid; i < k_count + v_count; i += kThreads) {
-        const bool key = i < k_count;
-        const int g = key ? i : i - k_count, dim = key ? p.dk : p.dv;
-        const int h = (int)fdiv((uint32_t)g, key ? p.k_groups : p.v_groups), at = g * 16 - h * dim;
-        const Rows &rows = key ? p.k : p.v;
-        const char *from = key ? keys + g * 32 : p.v.in + tok * p.v.in_token + h * p.v.in_head + at * 2;
-        const uint4 x[2] = {reinterpret_cast<const uint4 *>(from)[0], reinterpret_cast<const uint4 *>(from)[1]};
-        char *row = page < 0 ? nullptr : key ? k_row : v_row;
-        quantise<Bf16>(x, key ? p.k_inv : p.v_inv, key ? p.k_scale : p.v_scale, row ? row + g * 8 : nullptr,
-                       row ? row + p.kv_heads * dim / 2 + g : nullptr, rows.out ? rows.out + tok * rows.out_token + (int64_t)g * 32 : nullptr);
+    for (int it = 0; it < count + Q4; it++) {
+        // the next token's loads are under way while this one's heads are turned
+        const bool more = it + 1 < count;
+        if (loads && (mover ? more : it < count)) load(nx, ny);
+        if (more) {
+            const int32_t next = pos;
+            if (placer) read_entry();
+            if (it + 2 < count) {
+                tok += p.step;
+                read_token(tok + p.step);
+            }
+            form_angles(angles[(it + 1) & 1], next);
+        }
+        if (!group && what != kNone && (!Q4 || it < count)) {
+            char *to = reinterpret_cast<char *>(at_out);
+            if (what == kOut) {
+                at_out += out_step;
+            } else if (what == kKeys) {
+                to = keys + (it & 1) * (n_keys * p.dk * 2) + at_out;
+            } else {
+                char *const row = rows[it & 3][what == kValueRow];
+                to = row == nullptr ? nullptr : row + at_out;
+            }
+            if (turn) {
+                const Angles<Q4> &g = angles[it & 1];
+                const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+                uint32_t ox[4], oy[4];
+#pragma unroll
+                for (int j = 0; j < 2; j++) {
+                    const int ga = (j * p.n_turn + n) * 4;
+                    const ulonglong2 c = *reinterpret_cast<const ulonglong2 *>(&g.v[0][ga]), s = *reinterpret_cast<const ulonglong2 *>(&g.v[1][ga]);
+                    ulonglong2 cl = {}, sl = {};
+                    const bool exact = Q4 && what == kKeys;
+                    if constexpr (Q4)
+                        if (exact) cl = *reinterpret_cast<const ulonglong2 *>(&g.v[2][ga]), sl = *reinterpret_cast<const ulonglong2 *>(&g.v[3][ga]);
+#pragma unroll
+                    for (int k = 0; k < 2; k++) {
+                        // two pairs (a, b)
+                        Two a, b, na, nb;
+                        const uint32_t w0 = Interleaved ? (j ? ys : xs)[2 * k] : xs[2 * j + k], w1 = Interleaved ? (j ? ys : xs)[2 * k + 1] : ys[2 * j + k];
+                        const float2 u = unpack2<Bf16>(w0), v = unpack2<Bf16>(w1);
+                        a = Interleaved ? two(u.x, v.x) : two(u.x, u.y);
+                        b = Interleaved ? two(u.y, v.y) : two(v.x, v.y);
+                        const Two cc = k ? c.y : c.x, sn = k ? s.y : s.x;
+                        if (exact) {
+                            const Two ccl = k ? cl.y : cl.x, snl = k ? sl.y : sl.x;
+                            na = turned(a, neg2(b), cc, sn, ccl, snl);
+                            nb = turned(a, b, sn, cc, snl, ccl);
+                        } else {
+                            na = fma2(a, cc, neg2(mul2(b, sn)));
+                            nb = fma2(a, sn, mul2(b, cc));
+                        }
+                        const float2 fa = one_by_one(na), fb = one_by_one(nb);
+                        if (Interleaved) {
+                            (j ? oy : ox)[2 * k] = pack2<Bf16>(fa.x, fb.x);
+                            (j ? oy : ox)[2 * k + 1] = pack2<Bf16>(fa.y, fb.y);
+                        } else {
+                            ox[2 * j + k] = pack2<Bf16>(fa.x, fa.y);
+                            oy[2 * j + k] = pack2<Bf16>(fb.x, fb.y);
+                        }
+                    }
+                }
+                x = make_uint4(ox[0], ox[1], ox[2], ox[3]);
+                y = make_uint4(oy[0], oy[1], oy[2], oy[3]);
+            }
+            if (to != nullptr) {
+                *reinterpret_cast<uint4 *>(to) = x;
+                if (two_pieces) *reinterpret_cast<uint4 *>(to + d1) = y;
+            }
+        }
+        if constexpr (Q4) {
+            if (group && it > 0) {  // a token behind: its keys are in shared memory
+                const bool key = what == kKeyGroup;
+                uint4 in[2] = {x, y};
+                if (key) {
+                    const uint4 *from = reinterpret_cast<const uint4 *>(keys + ((it - 1) & 1) * (n_keys * p.dk * 2) + n * 32);
+                    in[0] = from[0], in[1] = from[1];
+                }
+                char *const row = rows[(it - 1) & 3][!key], *const held = key ? p.k.out : p.v.out;
+                quantise<Bf16>(in, key ? p.k_inv : p.v_inv, key ? p.k_scale : p.v_scale, row ? row + at_out * 8 : nullptr,
+                               row ? row + p.kv_heads * dim / 2 + at_out : nullptr, held ? held + done + at_out * 32 : nullptr);
+                done += out_step;
+            }
+        }
+        if (more && placer) set_rows((it + 1) & 3);
+        if (it + 1 < count + Q4) __syncthreads();
+        x = nx, y = ny;
     }
+}
+
+template <bool Bf16, bool Interleaved, bool Q4>
+int run_rotate(Params *p, cudaStream_t s)
+{
+    const DeviceInfo *dev = current_device();
+    if (dev == nullptr) return KV_ERR_CUDA;
+    const auto warps = [](int64_t n) { return (n + 31) / 32 * 32; };
+    const int all = p->heads + p->kv_heads;
+    int64_t chunks = 1, threads;
+    size_t keys = 0;
+    if (Q4) {
+        const int each = p->n_turn + p->n_plain, groups = p->k_groups + p->v_groups;
+        for (;; chunks++) {
+            p->chunk_heads = (int)((all + chunks - 1) / chunks);
+            p->movers = (int)warps((int64_t)p->chunk_heads * each);
+            threads = p->movers + warps((int64_t)std::min(p->chunk_heads, p->kv_heads) * groups);
+            if (threads <= kThreads) break;
+        }
+        chunks = (all + p->chunk_heads - 1) / p->chunk_heads;
+        keys = (size_t)std::min(p->chunk_heads, p->kv_heads) * p->dk * 4;
+    } else {
+        const int64_t items = (int64_t)all * (p->n_turn + p->n_plain) + (int64_t)p->kv_heads * p->n_v;
+        chunks = (items + kThreads - 1) / kThreads;
+        threads = warps((items + chunks - 1) / chunks);
+    }
+    const auto by = [](int n) { return make_fastdiv((uint32_t)std::max(n, 1)); };
+    p->by_turn = by(p->n_turn), p->by_plain = by(p->n_plain), p->by_v = by(p->n_v), p->by_k_groups = by(p->k_groups), p->by_v_groups = by(p->v_groups);
+    p->chunks = by((int)chunks);
+    const int64_t at_once = std::max<int64_t>((int64_t)dev->num_sms * (kSmThreads / threads) / chunks, 1);
+    p->step = (int)std::min(p->n_tokens, at_once);
+    return cuda_status(launch(rotate_kernel<Bf16, Interleaved, Q4>, dim3((unsigned)(p->step * chunks)), dim3((unsigned)threads), keys, s, *p));
 }
 
 template <bool Bf16, bool Interleaved>
-int pick_rotate(bool q4, const Params &p, int64_t n_tokens, cudaStream_t s)
+int pick_rotate(bool q4, Params *p, cudaStream_t s)
 {
-    const size_t keys = q4 ? (size_t)p.kv_heads * p.dk * 2 : 0;
-    const DeviceInfo *dev = current_device();
-    if (dev == nullptr) return KV_ERR_CUDA;
-    const bool pdl = n_tokens <= 2ll * dev->num_sms * (2048 / kThreads);  // two waves (kv_common.cuh, launch_as)
-    const auto kernel = q4 ? rotate_kernel<Bf16, Interleaved, true> : rotate_kernel<Bf16, Interleaved, false>;
-    return cuda_status(launch_as(pdl, kernel, dim3((unsigned)n_tokens), dim3(kThreads), keys, s, p));
+    return q4 ? run_rotate<Bf16, Interleaved, true>(p, s) : run_rotate<Bf16, Interleaved, false>(p, s);
 }
 
-int launch_rotate(int dtype, bool interleaved, bool q4, const Params &p, int64_t n_tokens, cudaStream_t s)
+int launch_rotate(int dtype, bool interleaved, bool q4, Params *p, cudaStream_t s)
 {
-    if (dtype == KV_BF16) return interleaved ? pick_rotate<true, true>(q4, p, n_tokens, s) : pick_rotate<true, false>(q4, p, n_tokens, s);
-    return interleaved ? pick_rotate<false, true>(q4, p, n_tokens, s) : pick_rotate<false, false>(q4, p, n_tokens, s);
+    if (dtype == KV_BF16) return interleaved ? pick_rotate<true, true>(q4, p, s) : pick_rotate<true, false>(q4, p, s);
+    return interleaved ? pick_rotate<false, true>(q4, p, s) : pick_rotate<false, false>(q4, p, s);
 }
 
 // The rotation's part of the parameters, for heads of `dim` elements.
 int fill_rope(Params *p, const kv_rope *r, int dim)
 {
     p->magnitude = 1.0f;
-    p->turn_items = make_fastdiv(1);
-    p->plain_items = make_fastdiv((uint32_t)(dim / 8));
+    p->n_plain = (dim + 15) / 16;
     if (r == nullptr || r->rot_dim == 0) return KV_OK;
     if (r->rot_dim < 0 || r->rot_offset < 0 || r->turns == nullptr || !std::isfinite(r->magnitude)) return KV_ERR_INVALID_ARG;
     if (r->rot_dim > dim || r->rot_offset > dim - r->rot_dim) return KV_ERR_RANGE;
@@ -371,8 +571,8 @@ int fill_rope(Params *p, const kv_rope *r, int dim)
     p->half = r->rot_dim / 2;
     p->offset = r->rot_offset;
     p->magnitude = r->magnitude;
-    p->turn_items = make_fastdiv((uint32_t)(r->rot_dim / (r->interleaved ? 8 : 16)));
-    if (r->rot_dim < dim) p->plain_items = make_fastdiv((uint32_t)((dim - r->rot_dim) / 8));
+    p->n_turn = (r->rot_dim + 15) / 16;
+    p->n_plain = (dim - r->rot_dim + 15) / 16;
     return KV_OK;
 }
 
@@ -416,15 +616,15 @@ int fill_write(Params *p, const kv_new_tokens *t, const kv_rope *rope, const kv_
     if ((st = check_rows(t->k, t->k_token_stride, t->k_head_stride)) != KV_OK) return st;
     p->k = Rows{(const char *)t->k, nullptr, t->k_token_stride, t->k_head_stride, 0, 0};
     p->kp = Plane{(char *)k->base[k_tensor] + (k_plane ? k->plane_stride : 0), k->block_stride, k->token_stride, (int32_t)k->num_blocks};
-    p->v_items = p->v_groups = make_fastdiv(1);
     if (t->head_dim_v) {
         if ((st = check_rows(t->v, t->v_token_stride, t->v_head_stride)) != KV_OK) return st;
         p->v = Rows{(const char *)t->v, nullptr, t->v_token_stride, t->v_head_stride, 0, 0};
         p->vp = Plane{(char *)v->base[v_tensor] + (v_plane ? v->plane_stride : 0), v->block_stride, v->token_stride, (int32_t)v->num_blocks};
-        p->v_items = make_fastdiv((uint32_t)(t->head_dim_v / 8));
-        p->v_groups = make_fastdiv((uint32_t)(t->head_dim_v >= 16 ? t->head_dim_v / 16 : 1));
+        p->n_v = (t->head_dim_v + 15) / 16;
+        p->v_groups = t->head_dim_v / 16;
     }
-    p->k_groups = make_fastdiv((uint32_t)(t->head_dim >= 16 ? t->head_dim / 16 : 1));
+    p->k_groups = t->head_dim / 16;
+    p->n_tokens = t->n_tokens;
     p->token_req = t->token_req;
     p->token_pos = t->token_pos;
     p->rope_pos = t->rope_pos ? t->rope_pos : t->token_pos;
@@ -524,7 +724,8 @@ int kv_rotate(int32_t dtype, int32_t n_heads, int32_t head_dim, const void *x, i
     p.heads = n_heads;
     p.dk = head_dim;
     p.inverse = inverse != 0;
-    return launch_rotate(dtype, rope->interleaved != 0, false, p, n_tokens, (cudaStream_t)stream);
+    p.n_tokens = n_tokens;
+    return launch_rotate(dtype, rope->interleaved != 0, false, &p, (cudaStream_t)stream);
 }
 
 int kv_q4_row_bytes(int32_t heads, int32_t head_dim, int32_t *bytes_out)
@@ -542,7 +743,7 @@ int kv_rotate_write(const kv_new_tokens *tokens, const kv_rope *rope, const kv_c
     Params p = {};
     const int st = fill_write(&p, tokens, rope, k, k_tensor, k_plane, v, v_tensor, v_plane, false);
     if (st != KV_OK || tokens->n_tokens == 0) return st;
-    return launch_rotate(tokens->dtype, rope && rope->interleaved, false, p, tokens->n_tokens, (cudaStream_t)stream);
+    return launch_rotate(tokens->dtype, rope && rope->interleaved, false, &p, (cudaStream_t)stream);
 }
 
 int kv_rotate_write_q4(const kv_new_tokens *tokens, const kv_rope *rope, const kv_cache_desc *k, int32_t k_tensor, int32_t k_plane,
@@ -564,7 +765,7 @@ int kv_rotate_write_q4(const kv_new_tokens *tokens, const kv_rope *rope, const k
     p.v.out = (char *)v_held;
     p.k.out_token = (int64_t)tokens->n_kv_heads * tokens->head_dim * 2;
     p.v.out_token = (int64_t)tokens->n_kv_heads * tokens->head_dim_v * 2;
-    return launch_rotate(tokens->dtype, rope && rope->interleaved, true, p, tokens->n_tokens, (cudaStream_t)stream);
+    return launch_rotate(tokens->dtype, rope && rope->interleaved, true, &p, (cudaStream_t)stream);
 }
 
 }  // extern "C"
