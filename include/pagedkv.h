@@ -647,7 +647,7 @@ KV_API int kv_q4_row_bytes(int32_t heads, int32_t head_dim, int32_t *bytes_out);
  * both to nearest, ties to even, in 32 bits; what exceeds 6 * scale becomes +-6.  The keys' rotation is exact to the
  * rounding (2^-37 before it), so codes follow from the values alone.  k_scale, v_scale: the tensors' scales, in [1e-30, 1e30].
  * k_held, v_held (NULL, or contiguous [n_tokens, n_kv_heads, dim], 16-byte aligned): the values the cache now stands for, in the
- * element type.  Elements must be finite.  n_kv_heads * head_dim <= 16384 and values are required (KV_ERR_UNSUPPORTED).
+ * element type.  Elements must be finite.  Values are required (KV_ERR_UNSUPPORTED).
  */
 KV_API int kv_rotate_write_q4(const kv_new_tokens *tokens, const kv_rope *rope, const kv_cache_desc *k, int32_t k_tensor, int32_t k_plane,
                               const kv_cache_desc *v, int32_t v_tensor, int32_t v_plane, float k_scale, float v_scale, void *k_held, void *v_held,

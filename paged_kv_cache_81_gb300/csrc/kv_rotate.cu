@@ -10,7 +10,17 @@
 // floats (what is left is below 2^-37), the products keep what their rounding leaves (Dekker; Knuth's sum), and the result is rounded
 // once to 32 bits and once to the element type, as a 16-bit cache would hold it, before it is rounded to 4 bits.
 //
-// One CTA a token: its cosines and sines are formed once, into shared memory, and serve every head.
+// Bound by bandwidth: every element is read and written once.  A CTA takes tokens one after another, a thread the same two pieces of
+// 16 bytes of each, so that where they come from and go to is worked out once.  While a token's heads are turned, the next one's
+// pieces are on their way into shared memory and its cosines and sines, which serve every head, are formed: one barrier a token.
+// Into 4 bits, turned keys pass to further warps through shared memory, which round groups of 16 a token behind.
+//
+// Measured (8 prompts of 1000 to 2000 tokens, 32 heads and 8 key heads of 128): 51 us in 16 bits, 6.1 TB/s of a measured 6.65; a CTA
+// that takes one token and loads after its angles 84.  8000 tokens of 20 heads of 192, 64 of them turned: 18.5 us, 6.65 TB/s.  Into 4 bits
+// 65 us (111), 5.0 TB/s, three quarters of the issue slots taken by the exact products and the rounding.  Two numbers an instruction
+// (f32x2) took 8 % off it.  Pieces are copied to shared memory rather than loaded ahead into registers: the copies of values from one
+// iteration to the next waited for them (4 bits 86).  The table of angles lies in shared memory and a warp finds the places of 32 tokens
+// at once, as loads that depend on one another took longer than the rest of an iteration (4 bits 86, 16 bits 56).
 #include <algorithm>
 #include <cmath>
 
@@ -21,10 +31,7 @@ namespace pkv {
 
 namespace {
 
-constexpr int kThreads = 512;            // at most
-constexpr int kSmThreads = 1024;         // resident on an SM
 constexpr int kMaxRot = 512;             // rotated elements of a head
-constexpr int kMaxQ4Keys = 16384;        // elements of a token's keys that pass through shared memory
 
 // ---------------------------------------------------------------------------
 // Cosine and sine of 256 angles a turn in two floats each, from their Taylor series in 64 bits at compile time.
@@ -78,23 +85,18 @@ __device__ __forceinline__ float sum2(float x, float y, float &left)
     return s;
 }
 
-// m cos, m sin of `u` 2^-64 turns: the nearest of 256 table angles and a rest of at most pi / 256, whose sine and cosine
-// take two terms more than themselves.  In one float each, off by little more than their rounding:
-__device__ __forceinline__ float2 plain_angle_of(uint64_t u, float m)
+// m cos, m sin of the sum of an angle of the table and a rest of at most pi / 256, in 2^-64 turns, whose sine and cosine take two
+// terms more than themselves.  In one float each, off by little more than their rounding:
+__device__ __forceinline__ float2 plain_angle_of(const float4 &t, int64_t rest, float m)
 {
-    const uint64_t r = u + (1ull << 55);
-    const float4 t = __ldg(reinterpret_cast<const float4 *>(g_turns.v[r >> 56]));
-    const float x = (float)((int32_t)((uint32_t)(r >> 32) & 0xffffffu) - (1 << 23)) * (float)(2 * kPi / 4294967296.0);
+    const float x = (float)(int32_t)(rest >> 32) * (float)(2 * kPi / 4294967296.0);
     const float x2 = x * x, s = fmaf(x * x2, -1.0f / 6, x), c = x2 * fmaf(x2, 1.0f / 24, -0.5f);
     return make_float2(m * (t.x + fmaf(t.x, c, fmaf(-t.y, s, t.z))), m * (t.y + fmaf(t.y, c, fmaf(t.x, s, t.w))));
 }
 
 // ... and in two:
-__device__ __forceinline__ Angle angle_of(uint64_t u, float m)
+__device__ __forceinline__ Angle angle_of(const float4 &t, int64_t d, float m)
 {
-    const uint64_t r = u + (1ull << 55);
-    const int64_t d = (int64_t)(r & ((1ull << 56) - 1)) - (1ll << 55);
-    const float4 t = __ldg(reinterpret_cast<const float4 *>(g_turns.v[r >> 56]));
     // the rest in radians: the upper 24 bits of d are exact in 32-bit floating point
     constexpr double kHi = 2 * kPi / 4294967296.0;
     constexpr float k1 = (float)kHi, k1l = (float)(kHi - (double)k1), k2 = (float)(kHi / 4294967296.0);
@@ -160,14 +162,15 @@ __device__ __forceinline__ Two fma2(Two a, Two b, Two c)
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
     return v;
 }
-__device__ __forceinline__ Two neg2(Two a) { return a ^ 0x8000000080000000ull; }
+__device__ __forceinline__ Two neg2(Two a) { return mul2(a, two(-1.0f, -1.0f)); }
+__device__ __forceinline__ Two sub2(Two a, Two b) { return fma2(b, two(-1.0f, -1.0f), a); }
 
 // a c + b s of two-float c and s (what their rounding leaves in cl and sl), rounded once.
 __device__ __forceinline__ Two turned(Two a, Two b, Two c, Two s, Two cl, Two sl)
 {
     const Two p = mul2(a, c), q = mul2(b, s);
-    const Two d = add2(p, q), t = add2(d, neg2(p));  // d and what its rounding leaves (Knuth)
-    const Two e = add2(add2(p, neg2(add2(d, neg2(t)))), add2(q, neg2(t)));
+    const Two d = add2(p, q), t = sub2(d, p);  // d and what its rounding leaves (Knuth)
+    const Two e = add2(sub2(p, sub2(d, t)), sub2(q, t));
     const Two pq = add2(fma2(a, c, neg2(p)), fma2(b, s, neg2(q)));
     return add2(d, add2(e, add2(pq, fma2(a, cl, mul2(b, sl)))));
 }
@@ -207,6 +210,7 @@ struct Params {
     FastDiv chunks;       // CTAs that share a token
     int32_t chunk_heads;  // heads of each, for 4 bits
     int32_t movers;       // threads that rotate and copy; the others round to 4 bits
+    int32_t loaders;      // threads that load: all but those that round keys
     float k_scale, v_scale, k_inv, v_inv;
     int *err;
 };
@@ -281,6 +285,21 @@ __device__ __forceinline__ void quantise(const uint4 (&in)[2], float inv, float 
 }
 
 constexpr int kAngles = kMaxRot / 2;
+constexpr int kSmBytes = 228 * 1024;  // of an SM's shared memory
+
+// 16 bytes into shared memory, by themselves.
+__device__ __forceinline__ void copy_async(uint32_t to, const char *from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+
+// Threads of a CTA at most and CTAs on an SM, which give the registers of a thread.  16 bits: 64 registers; the prompts above with 256 x 4
+// 51.0 us, 128 x 8 52.5, 192 x 5 50.9 (but 18.5, 19.0, 19.8 for 8000 tokens without a cache), 128 x 9 with 56 registers 54.5.  4 bits: a
+// token's keys and their groups best lie in one CTA; 72 registers with 448 x 2 65 us, 64 with 512 x 2 82 (they do not fit).
+template <bool Q4>
+struct Shape {
+    static constexpr int kThreads = Q4 ? 448 : 256, kCtas = Q4 ? 2 : 4;
+};
 
 template <bool Q4>
 struct Angles {
@@ -288,15 +307,20 @@ struct Angles {
 };
 
 template <bool Bf16, bool Interleaved, bool Q4>
-__global__ void __launch_bounds__(kThreads, 2) rotate_kernel(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(Shape<Q4>::kThreads, Shape<Q4>::kCtas) rotate_kernel(const __grid_constant__ Params p)
 {
     __shared__ __align__(16) Angles<Q4> angles[2];
-    __shared__ char *rows[4][2];  // a token's rows of keys and values, null: it has none
-    extern __shared__ __align__(16) char keys[];
+    __shared__ __align__(16) float4 near_angles[256];
+    // by a token's number here, modulo 64: its rows of keys and values (null: it has none), its position
+    __shared__ char *rows[64][2];
+    __shared__ int32_t positions[64];
+    extern __shared__ __align__(16) char stage[];  // every thread's pieces, then the turned keys
     const int tid = threadIdx.x, threads = blockDim.x;
     const uint32_t first = fdiv(blockIdx.x, p.chunks), chunk = blockIdx.x - first * p.chunks.d;
     const int count = (int)(((uint32_t)p.n_tokens - first - 1) / (uint32_t)p.step) + 1;  // of tokens that this CTA works on
-    // The thread's item: two pieces of 16 bytes of a head, `d1` bytes apart, that move together.
+    const int loaders = Q4 ? p.loaders : threads;
+    char *const keys = stage + 64 * loaders;
+    // The thread's item: two pieces of 16 bytes of a head, `d1` bytes apart, that move together (apart, so that a warp's are in runs).
     const bool mover = !Q4 || tid < p.movers;
     const int h0 = Q4 ? (int)chunk * p.chunk_heads : 0, n_heads = Q4 ? min(p.chunk_heads, p.heads + p.kv_heads - h0) : p.heads + p.kv_heads;
     const int n_keys = Q4 ? max(min(p.kv_heads - h0, n_heads), 0) : 0;  // key heads of this CTA
@@ -311,16 +335,14 @@ __global__ void __launch_bounds__(kThreads, 2) rotate_kernel(const __grid_consta
         if (i < turns) {
             h = (int)fdiv((uint32_t)i, p.by_turn), n = i - h * p.n_turn;
             turn = true;
-            o0 = p.offset + n * (Interleaved ? 16 : 8);
-            if (Interleaved)
-                two_pieces = n * 8 + 4 < p.half;
-            else
-                d1 = p.half * 2;
+            o0 = p.offset + n * 8;
+            d1 = Interleaved ? p.n_turn * 16 : p.half * 2;
+            two_pieces = !Interleaved || (n + p.n_turn) * 4 < p.half;
             what = kOut;
         } else if ((i -= turns) < plains) {
             h = (int)fdiv((uint32_t)i, p.by_plain);
-            o0 = (i - h * p.n_plain) * 16;
-            int o1 = o0 + 8;
+            o0 = (i - h * p.n_plain) * 8;
+            int o1 = o0 + p.n_plain * 8;
             two_pieces = o1 < p.dk - 2 * p.half;
             if (o0 >= p.offset) o0 += 2 * p.half;
             if (o1 >= p.offset) o1 += 2 * p.half;
@@ -328,8 +350,9 @@ __global__ void __launch_bounds__(kThreads, 2) rotate_kernel(const __grid_consta
             what = kOut;
         } else if (!Q4 && (i -= plains) < p.kv_heads * p.n_v) {
             h = (int)fdiv((uint32_t)i, p.by_v);
-            o0 = (i - h * p.n_v) * 16;
-            two_pieces = o0 + 8 < p.dv;
+            o0 = (i - h * p.n_v) * 8;
+            d1 = p.n_v * 16;
+            two_pieces = o0 + p.n_v * 8 < p.dv;
             src = p.v.in + h * p.v.in_head, in_step = p.v.in_token;
             at_out = ((int64_t)h * p.dv + o0) * 2;
             what = kValueRow;
@@ -361,81 +384,89 @@ __global__ void __launch_bounds__(kThreads, 2) rotate_kernel(const __grid_consta
             dim = p.dv, out_step = p.v.out_token, what = kValueGroup;
         }
     }
-    const bool loads = what != kNone && what != kKeyGroup, group = what >= kKeyGroup, placer = tid == threads - 1 && p.kv_heads;
-    uint4 x = {}, y = {}, nx = {}, ny = {};
-    const auto load = [&](uint4 &a, uint4 &b) {
-        a = *reinterpret_cast<const uint4 *>(src);
-        if (two_pieces) b = *reinterpret_cast<const uint4 *>(src + d1);
-        src += in_step;
-    };
-    const auto form_angles = [&](Angles<Q4> &to, int32_t pos) {
-        for (int i = tid; i < p.half; i += threads) {
-            // four pairs side by side, the halves of the items apart: a warp's reads of 16 bytes are then of one run
-            const int at = (((i >> 2 & 1) * p.n_turn + (i >> 3)) << 2) + (i & 3);
-            const uint64_t u = (uint64_t)(int64_t)pos * __ldg(p.turns + i);
-            if constexpr (Q4) {
-                const Angle a = angle_of(u, p.magnitude);
-                to.v[0][at] = a.c, to.v[1][at] = a.s, to.v[2][at] = a.cl, to.v[3][at] = a.sl;
-            } else {
-                const float2 a = plain_angle_of(u, p.magnitude);
-                to.v[0][at] = a.x, to.v[1][at] = p.inverse ? -a.y : a.y;
-            }
+    const bool loads = what != kNone && what != kKeyGroup, group = what >= kKeyGroup;
+    // The thread's own pairs: the first with its frequency at hand.  (4 bits: the threads that turn queries come first, as keys take longer.)
+    const int own = !mover ? p.half : !Q4 ? tid : tid - n_keys * p.n_turn + (tid < n_keys * p.n_turn ? p.movers : 0);
+    const int owners = Q4 ? p.movers : threads;
+    const auto angle = [](int32_t pos, uint64_t turn) { return (uint64_t)(int64_t)pos * turn + (1ull << 55); };  // rounded to the table's by its upper byte
+    const auto put_angle = [&](Angles<Q4> &to, int i, uint64_t u, const float4 &close) {
+        const int64_t rest = (int64_t)(u & ((1ull << 56) - 1)) - (1ll << 55);
+        // four pairs side by side; halves: a piece's first four pairs before all pieces' second four, so that a warp reads runs
+        const int at = Interleaved ? i : (((i >> 2 & 1) * p.n_turn + (i >> 3)) << 2) + (i & 3);
+        if constexpr (Q4) {
+            const Angle a = angle_of(close, rest, p.magnitude);
+            to.v[0][at] = a.c, to.v[1][at] = a.s, to.v[2][at] = a.cl, to.v[3][at] = a.sl;
+        } else {
+            const float2 a = plain_angle_of(close, rest, p.magnitude);
+            to.v[0][at] = a.x, to.v[1][at] = p.inverse ? -a.y : a.y;
         }
     };
-    // a token's page in three steps, so that none waits for the one before: its request and place, its entry, its rows
-    int32_t req = -1, at = -1, slot = 0, entry = -1, pos = 0;
-    const auto read_token = [&](int64_t t) {
-        pos = __ldg(p.rope_pos + t);
-        if (placer) req = __ldg(p.token_req + t), at = __ldg(p.token_pos + t);
-    };
-    const auto read_entry = [&] {
-        entry = -1;
-        if (req >= 0 && req < p.n_reqs && at >= 0) {
-            const uint32_t col = fdiv((uint32_t)at, p.block);
+    // the places of 32 tokens from number `at` on, by one warp: a wait for three loads in a row, one in 32 tokens
+    const auto place_tokens = [&](int at) {
+        at += tid & 31;
+        if (at >= count) return;
+        const int64_t t = first + (int64_t)at * p.step;
+        int32_t req = -1, pos = -1;
+        if (p.kv_heads) req = __ldg(p.token_req + t), pos = __ldg(p.token_pos + t);
+        positions[at & 63] = __ldg(p.rope_pos + t);
+        if (p.kv_heads == 0) return;
+        int page = -1, slot = 0;
+        if (req >= 0 && req < p.n_reqs && pos >= 0) {
+            const uint32_t col = fdiv((uint32_t)pos, p.block);
             if (col < (uint32_t)p.max_blocks) {
-                entry = __ldg(p.table + (int64_t)req * p.table_stride + col);
-                slot = (int)((uint32_t)at - col * p.block.d);
+                page = __ldg(p.table + (int64_t)req * p.table_stride + col);
+                slot = (int)((uint32_t)pos - col * p.block.d);
             }
         }
-    };
-    const auto set_rows = [&](int ring) {
-        int page = entry;
         if (page < 0)
             set_error(p.err, KV_DERR_TABLE);
         else if (page >= p.kp.num_blocks || (p.dv && page >= p.vp.num_blocks))
             set_error(p.err, KV_DERR_SLOT), page = -1;
-        rows[ring][0] = page < 0 ? nullptr : p.kp.base + (int64_t)page * p.kp.block_stride + (int64_t)slot * p.kp.token_stride;
-        rows[ring][1] = page < 0 ? nullptr : p.vp.base + (int64_t)page * p.vp.block_stride + (int64_t)slot * p.vp.token_stride;
+        rows[at & 63][0] = page < 0 ? nullptr : p.kp.base + (int64_t)page * p.kp.block_stride + (int64_t)slot * p.kp.token_stride;
+        rows[at & 63][1] = page < 0 ? nullptr : p.vp.base + (int64_t)page * p.vp.block_stride + (int64_t)slot * p.vp.token_stride;
     };
     grid_dep_entry();
-    int64_t tok = first;
-    read_token(tok);
-    if (loads) src += tok * in_step;
-    if (what == kOut) at_out += tok * out_step;
+    const uint64_t own_turn = own < p.half ? __ldg(p.turns + own) : 0;
+    src += first * in_step;
+    const char *src1 = src + d1;
+    if (what == kOut) at_out += first * out_step;
+    int64_t done = first * out_step;
     out_step *= p.step;
     in_step *= p.step;
-    int64_t done = tok * (what == kKeyGroup ? p.k.out_token : p.v.out_token);
-    if (loads && mover) load(x, y);
-    if (placer) {
-        read_entry();
-        set_rows(0);
+    const int mine = mover ? tid : what == kValueGroup ? tid - n_keys * p.k_groups : 0;  // the thread's place among those that load
+    const auto load = [&](int to) {
+        if (loads) {
+            const uint32_t at = smem_addr(stage) + ((to & 1) * 2 * loaders + mine) * 16;
+            copy_async(at, src);
+            if (two_pieces) copy_async(at + loaders * 16, src1);
+            src += in_step, src1 += in_step;
+        }
+    };
+    if (mover) load(0);
+    if (count > 1)
+        for (int i = tid; i < 256; i += threads) copy_async(smem_addr(near_angles + i), reinterpret_cast<const char *>(g_turns.v[i]));
+    if (tid >= threads - 32) place_tokens(0);
+    for (int i = own; i < p.half; i += owners) {
+        const uint64_t u = angle(__ldg(p.rope_pos + first), i == own ? own_turn : __ldg(p.turns + i));
+        put_angle(angles[0], i, u, __ldg(reinterpret_cast<const float4 *>(g_turns.v[u >> 56])));
     }
-    form_angles(angles[0], pos);
-    if (count > 1) read_token(tok + p.step);
+    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
     __syncthreads();
     for (int it = 0; it < count + Q4; it++) {
-        // the next token's loads are under way while this one's heads are turned
+        // the next token's loads are under way while this one's heads are turned (values are rounded a token behind)
         const bool more = it + 1 < count;
-        if (loads && (mover ? more : it < count)) load(nx, ny);
-        if (more) {
-            const int32_t next = pos;
-            if (placer) read_entry();
-            if (it + 2 < count) {
-                tok += p.step;
-                read_token(tok + p.step);
+        if (mover ? more : it < count) load(mover ? it + 1 : it);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if ((it & 31) == 16 && tid >= threads - 32) place_tokens(it + 16);
+        if (more)
+            for (int i = own; i < p.half; i += owners) {
+                const uint64_t u = angle(positions[(it + 1) & 63], i == own ? own_turn : __ldg(p.turns + i));
+                put_angle(angles[(it + 1) & 1], i, u, near_angles[u >> 56]);
             }
-            form_angles(angles[(it + 1) & 1], next);
-        }
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        const int slot = (mover ? it : it - 1) & 1;
+        uint4 x = *reinterpret_cast<const uint4 *>(stage + (slot * 2 * loaders + mine) * 16);
+        uint4 y = *reinterpret_cast<const uint4 *>(stage + ((slot * 2 + 1) * loaders + mine) * 16);
         if (!group && what != kNone && (!Q4 || it < count)) {
             char *to = reinterpret_cast<char *>(at_out);
             if (what == kOut) {
@@ -443,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 2) rotate_kernel(const __grid_consta
             } else if (what == kKeys) {
                 to = keys + (it & 1) * (n_keys * p.dk * 2) + at_out;
             } else {
-                char *const row = rows[it & 3][what == kValueRow];
+                char *const row = rows[it & 63][what == kValueRow];
                 to = row == nullptr ? nullptr : row + at_out;
             }
             if (turn) {
@@ -472,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 2) rotate_kernel(const __grid_consta
                             na = turned(a, neg2(b), cc, sn, ccl, snl);
                             nb = turned(a, b, sn, cc, snl, ccl);
                         } else {
-                            na = fma2(a, cc, neg2(mul2(b, sn)));
+                            na = fma2(b, neg2(sn), mul2(a, cc));
                             nb = fma2(a, sn, mul2(b, cc));
                         }
                         const float2 fa = one_by_one(na), fb = one_by_one(nb);
@@ -501,15 +532,13 @@ __global__ void __launch_bounds__(kThreads, 2) rotate_kernel(const __grid_consta
                     const uint4 *from = reinterpret_cast<const uint4 *>(keys + ((it - 1) & 1) * (n_keys * p.dk * 2) + n * 32);
                     in[0] = from[0], in[1] = from[1];
                 }
-                char *const row = rows[(it - 1) & 3][!key], *const held = key ? p.k.out : p.v.out;
+                char *const row = rows[(it - 1) & 63][!key], *const held = key ? p.k.out : p.v.out;
                 quantise<Bf16>(in, key ? p.k_inv : p.v_inv, key ? p.k_scale : p.v_scale, row ? row + at_out * 8 : nullptr,
                                row ? row + p.kv_heads * dim / 2 + at_out : nullptr, held ? held + done + at_out * 32 : nullptr);
                 done += out_step;
             }
         }
-        if (more && placer) set_rows((it + 1) & 3);
         if (it + 1 < count + Q4) __syncthreads();
-        x = nx, y = ny;
     }
 }
 
@@ -528,21 +557,24 @@ int run_rotate(Params *p, cudaStream_t s)
             p->chunk_heads = (int)((all + chunks - 1) / chunks);
             p->movers = (int)warps((int64_t)p->chunk_heads * each);
             threads = p->movers + warps((int64_t)std::min(p->chunk_heads, p->kv_heads) * groups);
-            if (threads <= kThreads) break;
+            if (threads <= Shape<Q4>::kThreads) break;
         }
         chunks = (all + p->chunk_heads - 1) / p->chunk_heads;
+        p->loaders = p->movers + std::min(p->chunk_heads, p->kv_heads) * p->v_groups;
         keys = (size_t)std::min(p->chunk_heads, p->kv_heads) * p->dk * 4;
     } else {
         const int64_t items = (int64_t)all * (p->n_turn + p->n_plain) + (int64_t)p->kv_heads * p->n_v;
-        chunks = (items + kThreads - 1) / kThreads;
+        chunks = (items + Shape<Q4>::kThreads - 1) / Shape<Q4>::kThreads;
         threads = warps((items + chunks - 1) / chunks);
     }
     const auto by = [](int n) { return make_fastdiv((uint32_t)std::max(n, 1)); };
     p->by_turn = by(p->n_turn), p->by_plain = by(p->n_plain), p->by_v = by(p->n_v), p->by_k_groups = by(p->k_groups), p->by_v_groups = by(p->v_groups);
     p->chunks = by((int)chunks);
-    const int64_t at_once = std::max<int64_t>((int64_t)dev->num_sms * (kSmThreads / threads) / chunks, 1);
+    const size_t smem = keys + 64 * (Q4 ? p->loaders : threads), fixed = 2 * sizeof(Angles<Q4>) + 256 * 16 + 64 * 20 + 1024;
+    const int64_t on_sm = std::min<int64_t>(Shape<Q4>::kThreads * Shape<Q4>::kCtas / threads, kSmBytes / (smem + fixed));
+    const int64_t at_once = std::max<int64_t>(dev->num_sms * on_sm / chunks, 1);
     p->step = (int)std::min(p->n_tokens, at_once);
-    return cuda_status(launch(rotate_kernel<Bf16, Interleaved, Q4>, dim3((unsigned)(p->step * chunks)), dim3((unsigned)threads), keys, s, *p));
+    return cuda_status(launch(rotate_kernel<Bf16, Interleaved, Q4>, dim3((unsigned)(p->step * chunks)), dim3((unsigned)threads), smem, s, *p));
 }
 
 template <bool Bf16, bool Interleaved>
@@ -753,7 +785,6 @@ int kv_rotate_write_q4(const kv_new_tokens *tokens, const kv_rope *rope, const k
     Params p = {};
     if (tokens != nullptr && tokens->head_dim_v == 0) return KV_ERR_UNSUPPORTED;
     if (!good_scale(k_scale) || !good_scale(v_scale)) return KV_ERR_INVALID_ARG;
-    if (tokens != nullptr && (int64_t)tokens->n_kv_heads * tokens->head_dim > kMaxQ4Keys) return KV_ERR_UNSUPPORTED;
     if (!aligned16(k_held) || !aligned16(v_held)) return KV_ERR_ALIGN;
     const int st = fill_write(&p, tokens, rope, k, k_tensor, k_plane, v, v_tensor, v_plane, true);
     if (st != KV_OK || tokens->n_tokens == 0) return st;
