@@ -701,7 +701,7 @@ def _tensor_numbers(*numbers):
 @functools.lru_cache(maxsize=256)
 def _attn_desc(*fields) -> KvAttnDesc:
     """Descriptions repeat from layer to layer; the library only reads them."""
-    _int32(window=fields[6])
+    _int32(n_kv_heads=fields[2], head_dim_v=fields[4], window=fields[6])
     return KvAttnDesc(*fields)
 
 
@@ -907,15 +907,15 @@ def _rope_on(dev: int, rope: Optional[Rope]) -> Optional[KvRope]:
     return rope.desc
 
 
-def _rotated_rows(dev: int, x: torch.Tensor, out: Optional[torch.Tensor], name: str, stream):
-    """(type code, strides of x, out, strides of out)."""
-    code, token, head = _rows3(x, name)
+def _rotated_out(dev: int, x: torch.Tensor, out: Optional[torch.Tensor], name: str, stream):
+    """(out, its token and head strides in bytes) for x [tokens, heads, dim] rotated."""
     if out is None:
-        out = _empty(x, x.shape, x.dtype, stream)
-    elif out.shape != x.shape or out.dtype is not x.dtype or out.get_device() != dev:
+        _, H, d = shape = x.shape
+        return _empty(x, shape, x.dtype, stream), H * d * 2, d * 2
+    if out.shape != x.shape or out.dtype is not x.dtype or out.get_device() != dev:
         raise ValueError(f"the output of {name} must have its shape and type, on its device")
-    _, to_token, to_head = _rows3(out, f"the output of {name}")
-    return code, token, head, out, to_token, to_head
+    _, token, head = _rows3(out, f"the output of {name}")
+    return out, token, head
 
 
 def kv_rotate(x: torch.Tensor, token_pos: torch.Tensor, rope: Rope, *, inverse: bool = False, out: Optional[torch.Tensor] = None,
@@ -924,7 +924,8 @@ def kv_rotate(x: torch.Tensor, token_pos: torch.Tensor, rope: Rope, *, inverse: 
     transposed map, which takes the output's gradient to x's."""
     dev = x.get_device()
     handle = _begin(dev, stream)
-    code, token, head, out, to_token, to_head = _rotated_rows(dev, x, out, "x", stream)
+    code, token, head = _rows3(x, "x")
+    out, to_token, to_head = _rotated_out(dev, x, out, "x", stream)
     T, H, d = x.shape
     _check("kv_rotate", (_lib or load()).kv_rotate(code, H, d, x.data_ptr(), token, head, out.data_ptr(), to_token, to_head, T,
                                                    _i32_on(dev, token_pos, T, "token_pos"), _rope_on(dev, rope), 1 if inverse else 0, handle))
@@ -937,26 +938,27 @@ def _new_tokens(q, k, v, block_table, token_req, token_pos, rope_pos, q_out, str
     dev = k.get_device()
     handle = _begin(dev, stream)
     T, G, dk = k.shape
-    d = KvNewTokens(dtype=code, n_kv_heads=G, head_dim=dk, k=k.data_ptr(), k_token_stride=k_token, k_head_stride=k_head, n_tokens=T)
+    H = q_at = q_token = q_head = to_at = to_token = to_head = v_at = v_token = v_head = dv = 0
     if q is not None:
         if q.dim() != 3 or q.dtype is not k.dtype or q.shape[0] != T or q.shape[2] != dk or q.get_device() != dev:
             raise ValueError("q must have k's tokens, width, type and device")
-        _, d.q_token_stride, d.q_head_stride, q_out, d.q_out_token_stride, d.q_out_head_stride = _rotated_rows(dev, q, q_out, "q", stream)
-        d.n_heads, d.q, d.q_out = q.shape[1], q.data_ptr(), q_out.data_ptr()
+        _, q_token, q_head = _rows3(q, "q")
+        q_out, to_token, to_head = _rotated_out(dev, q, q_out, "q", stream)
+        H, q_at, to_at = q.shape[1], q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
     if v is not None:
         if v.dim() != 3 or v.dtype is not k.dtype or v.shape[:2] != k.shape[:2] or v.get_device() != dev:
             raise ValueError("v must have k's tokens, heads, type and device")
-        _, d.v_token_stride, d.v_head_stride = _rows3(v, "v")
-        d.v, d.head_dim_v = v.data_ptr(), v.shape[2]
-    d.token_req, d.token_pos = _i32_on(dev, token_req, T, "token_req"), _i32_on(dev, token_pos, T, "token_pos")
-    if rope_pos is not None:
-        d.rope_pos = _i32_on(dev, rope_pos, T, "rope_pos")
+        _, v_token, v_head = _rows3(v, "v")
+        v_at, dv = v.data_ptr(), v.shape[2]
     if block_table.dim() != 2:
         raise ValueError("block_table must be an int32 [n_reqs, max_blocks] tensor")
-    d.n_reqs = block_table.shape[0]
-    d.block_table, d.max_blocks_per_req, d.bt_row_stride = _table(dev, block_table, d.n_reqs, "block_table")
+    n = block_table.shape[0]
+    table, pages, row = _table(dev, block_table, n, "block_table")
+    d = KvNewTokens(code, H, G, dk, dv, q_at, q_token, q_head, to_at, to_token, to_head, k.data_ptr(), k_token, k_head, v_at, v_token, v_head,
+                    _i32_on(dev, token_req, T, "token_req"), _i32_on(dev, token_pos, T, "token_pos"),
+                    None if rope_pos is None else _i32_on(dev, rope_pos, T, "rope_pos"), T, table, n, pages, row)
     return d, dev, handle, q_out
 
 
@@ -1025,14 +1027,14 @@ def kv_attention_q4(q: torch.Tensor, cache: PagedCache, block_table: torch.Tenso
     k_desc, v_desc, v_tensor, v_plane = _key_and_value_planes(dev, cache, v_cache, k_tensor, v_tensor, torch.uint8)
     T, H, dk = q.shape
     dv = dk if head_dim_v is None else head_dim_v
-    _int32(kv_heads=kv_heads, head_dim_v=dv)
     if dv < 0:
         raise ValueError("head_dim_v must not be negative")
+    attn = _attn_desc(code, H, kv_heads, dk, dv, causal, window, float(scale))
     batch = _attn_batch(dev, block_table, q_offsets, kv_lens, T)
     out, o_token, o_head, lse = _attn_outputs(dev, q, T, H, dv, out, lse, stream)
     workspace = _workspace(kv_attention_workspace_bytes, dev, handle, workspace, stream)
     _check("kv_attention_q4", (_lib or load()).kv_attention_q4(
-        _attn_desc(code, H, kv_heads, dk, dv, causal, window, float(scale)), batch, k_desc, k_tensor, 0, v_desc, v_tensor, v_plane, k_scale, v_scale,
+        attn, batch, k_desc, k_tensor, 0, v_desc, v_tensor, v_plane, k_scale, v_scale,
         q.data_ptr(), q_token, q_head, out.data_ptr(), o_token, o_head, lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, handle))
     return out, lse
 
