@@ -1,4 +1,4 @@
-// kv_attention_q4 for many rows: prefill chunks, and decoding of more than 16 query rows a key head.
+// kv_attention_q4 for many rows: prefill chunks, and decoding of more than 32 query rows a key head.
 //
 // kv_attention's kernel (kv_attention.cu) with tiles of 16-bit keys and values that four warps make of packed rows, which come by
 // TMA: a head's codes and the 16 bytes that hold its scales.  A thread takes 32 elements of a row (16 bytes of codes, two scales) at a

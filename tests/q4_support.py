@@ -9,7 +9,7 @@ from paged_kv_cache_81_gb300 import pagedkv as K
 from tests.attention_support import close, hidden
 from tests.rotate_support import U, VALUES, packed, plane, q4_pages
 
-MANY_ROWS = 16  # rows a request and key head, on average, up to which weights are fp16 whatever the type
+MANY_ROWS = 32  # rows a request and key head, on average, up to which weights are fp16 whatever the type
 
 
 class Q4Batch:

@@ -33,7 +33,7 @@ def test_head_widths(dk, dv, q_lens):
 
 @pytest.mark.parametrize("heads,kv_heads", [(1, 1), (3, 3), (3, 1), (14, 2), (10, 2), (16, 1), (5, 5), (6, 6), (7, 7), (32, 8), (18, 9), (10, 10), (11, 11), (12, 12),
                                             (32, 16), (64, 64), (17, 1), (40, 1), (128, 1), (200, 2)])
-@pytest.mark.parametrize("q_lens", [[1, 1, 2], [1, 5, 40]])
+@pytest.mark.parametrize("q_lens", [[1, 1, 2], [1, 5, 40], [2, 7, 120]])
 def test_head_groups(heads, kv_heads, q_lens):
     check(Q4Batch(q_lens, [300, 77, 131], heads, kv_heads, 64, seed=heads))
     if kv_heads < 20:
@@ -91,7 +91,7 @@ def test_many_short_requests():
 
 
 @pytest.mark.parametrize("spread", [1e-3, 1e-20, 30.0])
-@pytest.mark.parametrize("long", [2, 40])
+@pytest.mark.parametrize("long", [2, 40, 100])
 def test_flat_and_peaked_scores(spread, long):
     """Weights that are all alike, and ones where a single key takes it all and the maximum moves by hundreds."""
     check(Q4Batch([2, long], [900, 500], 4, 2, 128, spread=spread, seed=3))
@@ -146,7 +146,7 @@ def test_strides_of_q_and_out(long):
     check(b)
 
 
-@pytest.mark.parametrize("heads", [4, 64])
+@pytest.mark.parametrize("heads", [4, 64, 96])
 def test_rows_behind_the_last_sequence_stay(heads):
     b = Q4Batch([3, 2], [90, 20], heads, 2, 64, seed=2)
     b.q = torch.cat([b.q, torch.full((4, heads, 64), NAN, dtype=BF, device="cuda")])
@@ -162,14 +162,14 @@ def test_rows_behind_the_last_sequence_stay(heads):
 
 
 def test_pages_before_the_window_are_not_read():
-    for long in (3, 30):
+    for long in (3, 30, 80):
         b = Q4Batch([1, long], [500, 400], 4, 2, 64, block=16, seed=6)
         b.table[0, : (500 - 64) // 16] = -1
         b.table[1, : (400 - long - 64 + 1) // 16] = 1 << 30
         check(b, window=64)
 
 
-@pytest.mark.parametrize("heads", [4, 64])
+@pytest.mark.parametrize("heads", [4, 64, 96])
 def test_bad_table_entries_read_as_zeros(heads):
     b = Q4Batch([1, 1], [100, 50], heads, 2, 64, block=16, layout="blocks_first", seed=6)
     b.table[0, 2] = -7
@@ -185,7 +185,7 @@ def test_bad_table_entries_read_as_zeros(heads):
     close(lse, l, tl, "lse")
 
 
-@pytest.mark.parametrize("heads", [4, 64])
+@pytest.mark.parametrize("heads", [4, 64, 96])
 def test_pages_that_only_one_cache_has(heads):
     b = Q4Batch([1], [40], heads, 2, 64, block=16, seed=6)
     have = int(b.table_cpu[0, :3].max())
@@ -204,7 +204,7 @@ def test_pages_that_only_one_cache_has(heads):
     close(lse, l, tl, "lse")
 
 
-@pytest.mark.parametrize("heads", [4, 64])
+@pytest.mark.parametrize("heads", [4, 64, 96])
 def test_lengths_and_offsets_out_of_range_are_clamped(heads):
     b = Q4Batch([1, 1], [64, 64], heads, 2, 64, block=16, seed=6)
     want = [x.clone() for x in check(b)]
@@ -340,3 +340,31 @@ def test_a_requests_life(layout):
     assert int(new_lens[0]) == 40
     agree(step(1, total + 1, total + 3, 40), torch.cat([kept, torch.tensor([total + 1, total + 2])]), total + 1, total + 3)
     assert K.kv_get_last_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(4, 1), (8, 2), (16, 2), (32, 8), (40, 8), (9, 3)])
+@pytest.mark.parametrize("long", [2, 90])
+@pytest.mark.parametrize("block", [1, 16, 24])
+def test_padded_rows(heads, kv_heads, long, block):
+    """Rows that do not follow one another without a gap."""
+    b = Q4Batch([1, long], [400, 300], heads, kv_heads, 64, block=block, seed=heads)
+    want = [x.clone() for x in b.run(0.125)]
+    wide = [torch.full((x.shape[0], block, x.shape[2] + 48), 0x7F, dtype=torch.uint8, device="cuda") for x in b.tensors]
+    for x, y in zip(b.tensors, wide):
+        y[:, :, 16:16 + x.shape[2]] = x
+    b.cache, b.v_cache = (K.PagedCache.from_tensors([y[:, :, 16:16 + x.shape[2]]], "separate") for x, y in zip(b.tensors, wide))
+    out, lse = check(b, scale=0.125)
+    assert torch.allclose(out.float(), want[0].float(), rtol=0, atol=0.02) and torch.allclose(lse, want[1], rtol=0, atol=1e-3)
+
+
+@pytest.mark.parametrize("long", [2, 90])
+def test_pages_past_4_gib(long):
+    b = Q4Batch([1, long], [400, 300], 16, 4, 64, seed=3)
+    want = [x.clone() for x in b.run(0.125)]
+    far = (5 << 30) // (16 * b.tensors[0].shape[2])
+    wide = [torch.empty(far + b.pages, 16, x.shape[2], dtype=torch.uint8, device="cuda") for x in b.tensors]
+    for x, y in zip(b.tensors, wide):
+        y[far:] = x
+    b.cache, b.v_cache = (K.PagedCache.from_tensors([y], "separate") for y in wide)
+    b.table = torch.where(b.table < 0, b.table, b.table + far)
+    assert all(torch.equal(x, y) for x, y in zip(want, b.run(0.125)))

@@ -420,3 +420,73 @@ def test_python_refusals():
         K.kv_rotate(q, where[2][:1], rope)
     with pytest.raises(K.KvError):
         K.kv_rotate(q, where[2], K.Rope.make(128))
+
+
+# ---------------------------------------------------------------------------
+# many tokens, wide strides, far pages
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("heads,dim,tokens,interleaved", [(128, 64, 21000, False), (9, 16, 200000, True), (40, 128, 45000, False), (1, 576, 150000, True)])
+def test_many_tokens_as_few(heads, dim, tokens, interleaved):
+    """A long call, whose blocks take many tokens each, gives what short ones give."""
+    x = torch.randn(tokens, heads, dim, generator=torch.Generator("cuda").manual_seed(dim), device="cuda", dtype=BF)
+    pos = positions(heads, tokens, 1 << 30).cuda()
+    rope = K.Rope.make(16, offset=dim - 16, interleaved=interleaved)
+    out = K.kv_rotate(x, pos, rope)
+    for at in range(0, tokens, 300):
+        assert torch.equal(out[at:at + 300], K.kv_rotate(x[at:at + 300], pos[at:at + 300], rope))
+    assert torch.equal(K.kv_rotate(x, pos, rope, out=x), out)
+
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("heads,kv_heads,dk,tokens", [(16, 4, 64, 72000), (32, 8, 128, 21000), (0, 1, 32, 180000), (90, 20, 64, 11000)])
+def test_many_tokens_written_as_few(four, heads, kv_heads, dk, tokens):
+    g = torch.Generator("cuda").manual_seed(dk)
+    row = torch.randn(tokens, (heads + 2 * kv_heads) * dk, generator=g, device="cuda", dtype=FP)
+    q, k, v = (x.unflatten(1, (-1, dk)) if x.shape[1] else None for x in row.split([heads * dk, kv_heads * dk, kv_heads * dk], 1))
+    pages = tokens // 16 + 3
+    table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)[None]
+    pos = torch.randperm(tokens, generator=g, device="cuda").to(torch.int32)
+    req = torch.zeros_like(pos)
+    req[::97] = -1  # written nowhere
+    rope, at = K.Rope.make(dk), torch.randint(0, 1 << 30, (tokens,), generator=g, device="cuda", dtype=torch.int32)
+    width = K.kv_q4_row_bytes(kv_heads, dk) if four else kv_heads * dk
+    call = K.kv_rotate_write_q4 if four else K.kv_rotate_write
+    kw = dict(held=True, k_scale=0.5) if four else {}
+
+    def run(spans):
+        t = [torch.full((pages, 16, width), 7, dtype=torch.uint8 if four else FP, device="cuda") for _ in range(2)]
+        cache, v_cache = (K.PagedCache.from_tensors([x], "separate") for x in t)
+        got = [call(q[a:b] if heads else None, k[a:b], v[a:b], cache, table, req[a:b], pos[a:b], rope, v_cache=v_cache, rope_pos=at[a:b], **kw) for a, b in spans]
+        return t, got
+    few, parts = run([(a, min(a + 300, tokens)) for a in range(0, tokens, 300)])
+    many, whole = run([(0, tokens)])
+    assert all(torch.equal(a, b) for a, b in zip(few, many))
+    joined = [torch.cat(x) if x[0] is not None else None for x in zip(*parts)] if four else [torch.cat(parts) if heads else None]
+    for a, b in zip(joined, whole[0] if four else whole):
+        assert (a is None and b is None) or torch.equal(a, b)
+    K.kv_get_last_error(clear=True)
+
+
+def test_q4_many_key_heads():
+    check_q4(New([3, 20], [50, 20], 2, 136, 128, 128, seed=1))
+
+
+@pytest.mark.parametrize("four", [False, True])
+def test_write_padded_rows_and_pages_past_4_gib(four):
+    n = New([3, 20], [50, 20], 4, 2, 64, 64, seed=1)
+    t, cache, v_cache = q4_pages("separate", n.pages, 16, 2, 64, 64) if four else pages16(n, "separate")
+    call, rope = K.kv_rotate_write_q4 if four else K.kv_rotate_write, K.Rope.make(64)
+    want = call(*n.args(), cache, *n.where(), rope, v_cache=v_cache)
+    flat = [x.flatten(2) for x in t]
+    width = flat[0].shape[2]
+    pad = 16 // flat[0].element_size()
+    far = (5 << 30) // (16 * (width + pad) * flat[0].element_size())
+    wide = [torch.empty(far + n.pages, 16, width + pad, dtype=x.dtype, device="cuda") for x in flat]
+    for x in wide:
+        x[far:].fill_(0x77 if four else 7.0)
+    n.table = torch.where(n.table < 0, n.table, n.table + far)
+    caches = [K.PagedCache.from_tensors([x[:, :, :width]], "separate") for x in wide]
+    got = call(*n.args(), caches[0], *n.where(), rope, v_cache=caches[1])
+    assert torch.equal(got, want)
+    for x, y in zip(flat, wide):
+        assert torch.equal(y[far:, :, :width], x) and torch.all(y[far:, :, width:] == (0x77 if four else 7.0))

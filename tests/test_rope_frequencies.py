@@ -138,9 +138,6 @@ def test_q4_arguments(lib):
     for bad in (0.0, -1.0, float("nan"), float("inf"), 1e-35):
         assert run(ks=bad) == ARG and run(vs=bad) == ARG
     assert run(kh=0x50008) == ALIGN and run(vh=0x50004) == ALIGN
-    many = tokens(n_kv_heads=136, k_token_stride=136 * 256, v_token_stride=136 * 256)
-    big = K.kv_q4_row_bytes(136, 128)
-    assert run(many, k=cache(row=big), v=cache(row=big)) == UNSUPPORTED
 
 
 def test_struct_sizes(lib):
