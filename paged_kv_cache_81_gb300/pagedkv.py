@@ -293,7 +293,7 @@ class PagedCache:
 
     def desc(self) -> KvCacheDesc:
         """The kv_cache_desc of these tensors, built once and rebuilt only if a tensor moved."""
-        ptrs = tuple(x.data_ptr() for x in self.tensors)
+        ptrs = [x.data_ptr() for x in self.tensors]
         if getattr(self, "_desc_ptrs", None) != ptrs:
             n = len(ptrs)
             self._bases = (ctypes.c_uint64 * max(1, n))(*ptrs)
@@ -907,12 +907,12 @@ def _rope_on(dev: int, rope: Optional[Rope]) -> Optional[KvRope]:
     return rope.desc
 
 
-def _rotated_out(dev: int, x: torch.Tensor, out: Optional[torch.Tensor], name: str, stream):
+def _rotated_out(dev: int, x: torch.Tensor, shape, out: Optional[torch.Tensor], name: str, stream):
     """(out, its token and head strides in bytes) for x [tokens, heads, dim] rotated."""
     if out is None:
-        _, H, d = shape = x.shape
+        _, H, d = shape
         return _empty(x, shape, x.dtype, stream), H * d * 2, d * 2
-    if out.shape != x.shape or out.dtype is not x.dtype or out.get_device() != dev:
+    if out.shape != shape or out.dtype is not x.dtype or out.get_device() != dev:
         raise ValueError(f"the output of {name} must have its shape and type, on its device")
     _, token, head = _rows3(out, f"the output of {name}")
     return out, token, head
@@ -925,8 +925,8 @@ def kv_rotate(x: torch.Tensor, token_pos: torch.Tensor, rope: Rope, *, inverse: 
     dev = x.get_device()
     handle = _begin(dev, stream)
     code, token, head = _rows3(x, "x")
-    out, to_token, to_head = _rotated_out(dev, x, out, "x", stream)
-    T, H, d = x.shape
+    T, H, d = shape = x.shape
+    out, to_token, to_head = _rotated_out(dev, x, shape, out, "x", stream)
     _check("kv_rotate", (_lib or load()).kv_rotate(code, H, d, x.data_ptr(), token, head, out.data_ptr(), to_token, to_head, T,
                                                    _i32_on(dev, token_pos, T, "token_pos"), _rope_on(dev, rope), 1 if inverse else 0, handle))
     return out
@@ -940,18 +940,20 @@ def _new_tokens(q, k, v, block_table, token_req, token_pos, rope_pos, q_out, str
     T, G, dk = k.shape
     H = q_at = q_token = q_head = to_at = to_token = to_head = v_at = v_token = v_head = dv = 0
     if q is not None:
-        if q.dim() != 3 or q.dtype is not k.dtype or q.shape[0] != T or q.shape[2] != dk or q.get_device() != dev:
+        q_code, q_token, q_head = _rows3(q, "q")
+        tokens, H, d = shape = q.shape
+        if q_code != code or tokens != T or d != dk or q.get_device() != dev:
             raise ValueError("q must have k's tokens, width, type and device")
-        _, q_token, q_head = _rows3(q, "q")
-        q_out, to_token, to_head = _rotated_out(dev, q, q_out, "q", stream)
-        H, q_at, to_at = q.shape[1], q.data_ptr(), q_out.data_ptr()
+        q_out, to_token, to_head = _rotated_out(dev, q, shape, q_out, "q", stream)
+        q_at, to_at = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
     if v is not None:
-        if v.dim() != 3 or v.dtype is not k.dtype or v.shape[:2] != k.shape[:2] or v.get_device() != dev:
+        v_code, v_token, v_head = _rows3(v, "v")
+        tokens, heads, dv = v.shape
+        if v_code != code or tokens != T or heads != G or v.get_device() != dev:
             raise ValueError("v must have k's tokens, heads, type and device")
-        _, v_token, v_head = _rows3(v, "v")
-        v_at, dv = v.data_ptr(), v.shape[2]
+        v_at = v.data_ptr()
     if block_table.dim() != 2:
         raise ValueError("block_table must be an int32 [n_reqs, max_blocks] tensor")
     n = block_table.shape[0]
