@@ -12,7 +12,7 @@
 // Queries are brought to [1, 2) by a power of two a row and held in fp16, weights are fp16 (kv_tensor.cuh, weight_offset);
 // sums are in 32 bits.
 //
-// One persistent CTA per SM; a unit is one request's rows of up to eight key heads.
+// One persistent CTA per SM; a unit is one request's rows of as many key heads as there are warps for, or fewer (launch_few).
 //   warps 0, 1 (to 3)  bring rows of keys and of values by TMA, one for each run of slots inside a page, into rings of tiles
 //   other warps        each one key head and every n-th 16 keys of a tile: scores, weights, values, with a running maximum and sum of
 //                      its own; at the unit's end the warps of a head join through shared memory, while those that are done go on
@@ -20,6 +20,8 @@
 // The 16 keys of a step are taken in an order (order_of) in which the keys' 16-byte reads do not meet in a bank, and the values'
 // 8-byte reads at most in pairs.
 #pragma once
+
+#include <algorithm>
 
 #include "kv_attention_q4.cuh"
 
@@ -225,7 +227,7 @@ struct Tile {
                 bulk_load(to + i * pr * place.codes, place.base + (uint64_t)from * place.block_stride + (uint32_t)(slot * place.codes), pr * place.codes, bar);
                 continue;
             }
-            tma_load_3d(to + i * pr * place.codes, map, bar, h0 * dim / 8, slot, from);
+            tma_load_3d(to + i * pr * place.codes, map, bar, h0 * dim / 2 >> row_map_shift(place.codes), slot, from);
             if (place.apart)
                 tma_load_3d(to + place.first + i * pr * place.scales, scale_map, bar, ((p.heads_all * dim / 2 + h0 * dim / 16) & ~15) / 4, slot, from);
         }
@@ -916,6 +918,20 @@ int launch_few(FewParams &p, const DeviceInfo *dev, cudaStream_t s)
     const int all = p.heads_all;
     int heads = all < kWarps ? all : kWarps;
     while (all % heads) heads--;
+    // A unit of few heads lies in fewer pieces, of fewer bytes, when many CTAs share a request: joining them is bound by what one SM reads
+    // (45 GB/s).  But rows that come apart into heads cost more to load, so that this pays for short contexts only.  8 key heads of 128
+    // and a unit of 8, 4, 2 of them, one request of 120000 and of 8000: 12 rows 74, 64, 58 and 40, 28, 22 us; 8 rows 53, 49, 50 and 30, 21, 19
+    // us; eight requests of 15000: 62, 59, 58 and 46, 47, 51; 64 requests of 8000: 12 rows 152, 177, 245, 4 rows 113, 181, 244.
+    constexpr int kPieces = NT == 1 ? 40 : 10;            // of a unit, above which it gets fewer heads
+    constexpr int64_t kShort = NT == 1 ? 6144 : 10240;    // keys times heads an SM, up to which (where the two would meet for one request)
+    const int64_t seen = p.b.window ? std::min<int64_t>(p.b.max_tokens, (int64_t)p.b.window + p.b.n_tokens) : p.b.max_tokens;
+    if (p.b.n_reqs * seen * all <= kShort * dev->num_sms)
+        while ((int64_t)dev->num_sms * heads > (int64_t)kPieces * p.b.n_reqs * all) {
+            int h = heads - 1;
+            while (h > 1 && all % h) h--;
+            if (h < 2) break;
+            heads = h;
+        }
     p.unit_heads = heads;
     p.split = 1;
     while (2 * p.split * heads <= kWarps) p.split *= 2;

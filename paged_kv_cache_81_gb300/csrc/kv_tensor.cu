@@ -63,7 +63,7 @@ int make_row_map(CUtensorMap *map, uint64_t base, const kv_cache_desc *c, int by
 {
     const EncodeFn fn = encoder();
     if (fn == nullptr) return KV_ERR_CUDA;
-    const int word = bytes > 1024 ? 8 : 4;  // a box has at most 256
+    const int word = 1 << row_map_shift(bytes);
     const cuuint64_t dims[3] = {(cuuint64_t)(c->row_bytes / word), (cuuint64_t)c->block_size, (cuuint64_t)c->num_blocks};
     const cuuint64_t strides[2] = {(cuuint64_t)c->token_stride, (cuuint64_t)c->block_stride};
     const cuuint32_t box[3] = {(cuuint32_t)(bytes / word), (cuuint32_t)rows, 1}, one[3] = {1, 1, 1};

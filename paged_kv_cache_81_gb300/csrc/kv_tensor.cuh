@@ -355,6 +355,7 @@ int make_q4_code_map(CUtensorMap *map, uint64_t base, const kv_cache_desc *c, in
 
 // A map of a plane's rows as opaque 32-bit words (64-bit ones for boxes of more than 1024 bytes), (word of a row, slot, block), without a
 // swizzle; a load brings `bytes` of each of `rows` consecutive slots of a block, densely, with zeros for what lies past a row's end.
+__host__ __device__ inline int row_map_shift(int bytes) { return bytes > 1024 ? 3 : 2; }  // log2 of a word's bytes: a box has at most 256 words
 int make_row_map(CUtensorMap *map, uint64_t base, const kv_cache_desc *c, int bytes, int rows);
 
 }  // namespace pkv

@@ -84,6 +84,20 @@ def test_many_pieces_same_bits():
         check(Q4Batch([q_len] + [1] * 30, [kv] + [300] * 30, heads, kv_heads, dim, block=64, seed=kv))
 
 
+@pytest.mark.parametrize("kv_heads", [1, 2, 3, 4, 8, 16, 32])
+@pytest.mark.parametrize("group", [1, 6])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_many_requests_of_whole_rows(kv_heads, group, dim):
+    """So many requests that a block takes all heads of a row, some of them with new tokens beyond one unit, the longest cut."""
+    g = torch.Generator().manual_seed(kv_heads)
+    lens = torch.randint(1, 250, (160,), generator=g).tolist()
+    lens[7], lens[33] = 3000, 0
+    q_lens = [3 if i % 5 == 0 else 1 for i in range(160)]
+    for q, dtype in ((q_lens, BF), ([2 * n for n in q_lens], FP)):
+        check(Q4Batch(q, [max(n, m) if n else 0 for n, m in zip(lens, q)], group * kv_heads, kv_heads, dim, block=24 if group + kv_heads == 8 else 16,
+                      dtype=dtype, seed=dim))
+
+
 def test_many_short_requests():
     lens = [1 + 37 * i % 300 for i in range(700)]
     check(Q4Batch([1] * 700, lens, 4, 2, 64, block=8, seed=1))
