@@ -278,5 +278,6 @@ int preload_expand_kernels();     // kv_expand.cu
 int preload_mass_kernels();       // kv_mass.cu
 int preload_evict_kernels();      // kv_evict.cu
 int preload_q4_kernels();         // kv_attention_q4.cu
+int preload_rotate_kernels();     // kv_rotate.cu
 
 }  // namespace pkv

@@ -192,7 +192,6 @@ int preload_bulk_kernels();    // kv_bulk.cu
 int preload_clip_kernels();    // kv_clip.cu
 int preload_hash_kernels();    // kv_hash.cu
 int preload_signal_kernels();  // kv_signal.cu
-int preload_rotate_kernels();  // kv_rotate.cu
 // All of the above, once per device (kv_runtime.cu).
 int preload_all_kernels(const DeviceInfo &dev);
 
