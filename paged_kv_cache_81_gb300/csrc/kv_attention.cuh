@@ -105,7 +105,7 @@ struct Output {
 // threads; a row's fragments are added in the order of their keys, so the result does not depend on which
 // CTA came last.  Row r is (first + r) / group of the request's tokens from q0 on, head head0 + the
 // rest.  Not inlined: its registers would crowd the loop over the key tiles.
-template <int DV, bool Bf16>
+template <int DV, bool Bf16, bool BfMath = Bf16>
 __device__ PKV_APART void join_rows(const Output p, const Pieces at, int half, int row0, int rows, int stat, int first, int q0, int head0,
                                        const FastDiv group)
 {
@@ -180,7 +180,7 @@ __device__ PKV_APART void join_rows(const Output p, const Pieces at, int half, i
                     v.y = pack2<Bf16>(o[k].z * inv, o[k].w * inv);
                     *reinterpret_cast<uint2 *>(to + (half * DV + (q + k) * 4) * 2) = v;
                 }
-            if (half == 0 && q == 0 && p.lse) p.lse[token * p.heads + head] = l > 0.0f ? fmaf(top, p.scale, weight_log<Bf16>(l)) : -INFINITY;
+            if (half == 0 && q == 0 && p.lse) p.lse[token * p.heads + head] = l > 0.0f ? fmaf(top, p.scale, weight_log<BfMath>(l)) : -INFINITY;
         }
     };
     // what the registers beside the tile loop hold; two fragments (a long unit's usual cut) in four trips a row instead
@@ -206,7 +206,7 @@ __device__ PKV_APART void join_rows(const Output p, const Pieces at, int half, i
 // counter: the first part's; those of the parts are `apart`.
 constexpr int kSum = 8;
 
-template <int DV, bool Bf16>
+template <int DV, bool Bf16, bool BfMath = Bf16>
 __device__ __forceinline__ void join_unit(const Output &p, float *ws, const Cut &cut, int *counter, int apart, int halves, int half0, int half1,
                                           int stride, int row0, int rows, int stat, int first, int q0, int head0, const FastDiv &group, uint32_t bar,
                                           int &phase, volatile int *answer, const Waiter &wait, bool &ok)
@@ -223,7 +223,7 @@ __device__ __forceinline__ void join_unit(const Output &p, float *ws, const Cut 
             const auto slot = [&](int piece, int odd) { return ws + (2 * ((cut.c0 + piece) * halves + h) + odd) * stride; };
             const Pieces at{sums_of ? slot(1, 1) : slot(from, 0), sum ? slot(from + 1, 1) : nullptr, n, (sums_of ? kSum : 1) * 2 * halves * stride,
                             from == 0 && !sums_of ? stride : 0};
-            join_rows<DV, Bf16>(p, at, h, row0, rows, stat, first, q0, head0, group);
+            join_rows<DV, Bf16, BfMath>(p, at, h, row0, rows, stat, first, q0, head0, group);
         }
         if (!sum) return;
     }

@@ -23,7 +23,8 @@ struct Shape {
     static constexpr int kNK = Staged ? 2 : DK == 64 ? 5 : DK == 128 ? 3 : 2;  // ring depths: what 227 KB holds
     static constexpr int kNV = Staged ? 2 : DK == 64 ? 5 : DK == 128 ? 2 : 1;  // (192: four single panels of K and two tiles of V ran 7% slower)
     static constexpr uint32_t kOffK = 2 * kQ, kOffV = kOffK + kNK * kK, kOffAux = kOffV + kNV * kV;
-    static constexpr uint32_t kBytes = kOffAux + 2048;
+    static constexpr uint32_t kOffScales = kOffAux + 2048;  // where Staged: the queries' exponents of two units, a byte a row
+    static constexpr uint32_t kBytes = kOffScales + (Staged ? 512 : 0);
     static constexpr uint32_t kOffStage = kBytes, kStage = 227 * 1024 - kOffStage;  // where Staged
 };
 
@@ -55,7 +56,7 @@ using KernelParams = std::conditional_t<std::is_same_v<Rows, NoRows>, AttentionP
 // Bookkeeping at the end of shared memory.
 struct Aux {
     uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5], stage_full[4], stage_empty[4];
-    uint64_t s_full[2], p_ready[2], o_done[2], q_full, q_empty, merge_ready, merge_free, join[2];
+    uint64_t s_full[2], p_ready[2], o_done[2], q_full, q_ready[2], q_empty, merge_ready, merge_free, join[2];
     int scan[64];
     Place place;
     float m[128], l[128];  // the odd tiles' group, for the join
@@ -100,6 +101,28 @@ __device__ __forceinline__ bool load_tile(const AttentionParams &p, const CUtens
     return true;
 }
 
+// Row `thread` of a set of bf16 queries in shared memory to fp16, brought to [1, 2) by a power of two: returns its exponent.
+template <int DK>
+__device__ __forceinline__ uint32_t scale_row(uint32_t set, int thread)
+{
+    const auto at = [&](int c) { return set + (c >> 3) * kPanel + thread * 128 + (((c & 7) ^ (thread & 7)) << 4); };
+    uint32_t most = 0;  // magnitudes, two by two
+#pragma unroll 4
+    for (int c = 0; c < DK / 8; c++) {
+        const uint4 v = ld_smem16(at(c));
+        most = __vmaxu2(most, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+    }
+    const uint32_t e = min(max(max(most & 0xffffu, most >> 16) >> 7, 1u), 253u);
+    const float to = __uint_as_float((254u - e) << 23);
+#pragma unroll 2
+    for (int c = 0; c < DK / 8; c++) {
+        const uint4 v = ld_smem16(at(c));
+        const auto f16 = [&](uint32_t x) { return pack2<false>(__uint_as_float(x << 16) * to, __uint_as_float(x & 0xffff0000u) * to); };
+        st_smem16(at(c), make_uint4(f16(v.x), f16(v.y), f16(v.z), f16(v.w)));
+    }
+    return e;
+}
+
 // A unit's queries, `half` rows at `base` and the others at its second panel set, by one warp.
 template <int DK>
 __device__ __forceinline__ void load_queries(const AttentionParams &p, const CUtensorMap *map, const Walk &w, int half, uint32_t base, uint32_t bar)
@@ -121,7 +144,8 @@ __device__ __forceinline__ void load_queries(const AttentionParams &p, const CUt
 
 // Rows: NoRows where tiles of K and V come by TMA.  Otherwise rows of another kind: warps 0 and 2 load them packed (k_scale_map, v_scale_map
 // are for them alone), and warps 12 to 15 make the tiles.  Those 512 threads have 128 registers each; the softmax groups take
-// 168, the others give theirs away, and as no function can be called then, PKV_APART has to be inline.
+// 168, the others give theirs away, and as no function can be called then, PKV_APART has to be inline.  Tiles are fp16 ones; bf16 queries
+// are brought to fp16 by warps 12 to 15 too, with a power of two a row that the row's softmax takes into its scale.
 template <int DK, int DV, bool Bf16, typename Rows>
 __global__ void __launch_bounds__(std::is_same_v<Rows, NoRows> ? kThreads : kRowsThreads, 1)
 attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
@@ -129,6 +153,8 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
 {
     constexpr bool kRowsKind = !std::is_same_v<Rows, NoRows>;
     constexpr int kFull = kRowsKind ? 4 : 1;  // arrivals that fill a tile
+    constexpr bool kScaled = kRowsKind && Bf16;    // queries are brought to fp16, as the tiles are: 4-bit codes times their scales are exact in it
+    constexpr bool kBfMath = Bf16 && !kScaled;     // the products' type
     using S = Shape<DK, DV, kRowsKind>;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t base = smem_addr(smem);
@@ -146,6 +172,7 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
             mbar_init(smem_addr(&aux.p_ready[i]), 4);
             mbar_init(smem_addr(&aux.o_done[i]), 1);
             mbar_init(smem_addr(&aux.join[i]), 4);
+            mbar_init(smem_addr(&aux.q_ready[i]), 4);
         }
         if (kRowsKind)
             for (int i = 0; i < 4; i++) mbar_init(smem_addr(&aux.stage_full[i]), 1), mbar_init(smem_addr(&aux.stage_empty[i]), 4);
@@ -176,8 +203,8 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         const int g = (warp - 4) >> 2, t = tid & 127;
         const uint32_t mine = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_at = tmem + g * 128 + mine, o_at = tmem + 256 + g * 128 + mine;
-        const float slack = 8.0f / p.o.c;  // how far the maximum may grow before O is rescaled
-        int steps = 0, joins = 0, cuts = 0;
+        float c = p.o.c, slack = 8.0f / c;  // log2 of a weight a unit of the scores; how far the maximum may grow before O is rescaled
+        int steps = 0, joins = 0, cuts = 0, units = 0;
         bool owes_free = false;  // the even group may still be reading this (odd) group's O
         bool ok = true;
         do {
@@ -204,7 +231,14 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
             int lo, hi;
             sees(b, w.q, (int)fdiv((uint32_t)(w.u.row0 + min(row, w.u.rows - 1)), b.group), lo, hi);
             const bool warp_live = __any_sync(0xffffffffu, live);
-            float m = -INFINITY, l = 0.0f;
+            float m = -INFINITY, l = 0.0f, back = 1.0f;
+            if (kScaled) {  // the row's own unit
+                if (!wait.warp(smem_addr(&aux.q_ready[units & 1]), units >> 1 & 1)) { ok = false; break; }
+                back = __uint_as_float((uint32_t)smem[S::kOffScales + (units & 1) * 256 + (both ? g * 128 : 0) + t] << 23);
+                units++;
+                c = fminf(fmaxf(p.o.c * back, 0x1p-120f), 0x1p127f);  // so small a one weighs all alike, and leaves slack a number
+                slack = 8.0f / c;
+            }
             const int first = both ? 0 : g, step = both ? 1 : 2, kt0 = w.u.tile0 + w.at.off;
             for (int k = first; k < w.n; k += step) {
                 const int kb = (kt0 + k) * kTile;
@@ -242,10 +276,10 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                         tc_wait_ld();
                         top = max32(x1, top);
                     }
-                    const bool grow = top > (Bf16 ? m + slack : __fadd_rd(m, slack));  // -inf + slack: the first finite score
+                    const bool grow = top > (kBfMath ? m + slack : __fadd_rd(m, slack));  // -inf + slack: the first finite score
                     if (__any_sync(0xffffffffu, grow)) {
                         const float to_m = grow ? top : m;
-                        const float alpha = grow ? exp2_fast((m - to_m) * p.o.c) : 1.0f;
+                        const float alpha = grow ? exp2_fast((m - to_m) * c) : 1.0f;
                         l *= alpha;
                         m = to_m;
                         if (k > first) {
@@ -262,7 +296,7 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                             }
                         }
                     }
-                    const float mc = weight_offset<Bf16>(m, p.o.c);
+                    const float mc = weight_offset<kBfMath>(m, c);
                     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                     uint32_t pk[16];
                     // P takes the columns of the upper 64 scores: 32 keys' weights stand in 16 columns from 64 on, so
@@ -273,23 +307,23 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                             tmem_ld32(s_at + q * 32, x0);
                             tc_wait_ld();
                             hide32(x0, from - q * 32, to_key - q * 32);
-                            weights32<Bf16>(x0, p.o.c, mc, sum, pk);
+                            weights32<kBfMath>(x0, c, mc, sum, pk);
                             tmem_st16(s_at + 64 + q * 16, pk);
                         }
                     } else {
                         tmem_ld32(s_at + 64, x0);  // the last 32 are still in x1
-                        weights32<Bf16>(x1, p.o.c, mc, sum, pk);
+                        weights32<kBfMath>(x1, c, mc, sum, pk);
                         tmem_st16(s_at + 112, pk);
                         tc_wait_ld();
                         tmem_ld32(s_at + 32, x1);
-                        weights32<Bf16>(x0, p.o.c, mc, sum, pk);
+                        weights32<kBfMath>(x0, c, mc, sum, pk);
                         tmem_st16(s_at + 96, pk);
                         tc_wait_ld();
                         tmem_ld32(s_at, x0);
-                        weights32<Bf16>(x1, p.o.c, mc, sum, pk);
+                        weights32<kBfMath>(x1, c, mc, sum, pk);
                         tmem_st16(s_at + 80, pk);
                         tc_wait_ld();
-                        weights32<Bf16>(x0, p.o.c, mc, sum, pk);
+                        weights32<kBfMath>(x0, c, mc, sum, pk);
                         tmem_st16(s_at + 64, pk);
                     }
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
@@ -304,6 +338,7 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                 steps++;
             }
             if (!ok) break;
+            if (kScaled) m *= back;
             const bool had = first < w.n;
             if (had && !wait.warp(smem_addr(&aux.o_done[g]), (steps - 1) & 1)) { ok = false; break; }
             tc_fence_after();
@@ -366,7 +401,7 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                 }
                 if (live) {
                     if (whole) {
-                        if (lse) *lse = l > 0.0f ? fmaf(m, p.o.scale, weight_log<Bf16>(l)) : -INFINITY;
+                        if (lse) *lse = l > 0.0f ? fmaf(m, p.o.scale, weight_log<kBfMath>(l)) : -INFINITY;
                     } else {
                         part[kRows * DV + row] = m;
                         part[kRows * DV + kRows + row] = l;
@@ -380,7 +415,7 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
             if (!whole) {
                 const Cut cut(line, w.pos - w.at.off, unit_cost(w.u));
                 const int row0 = both ? g * half : 0;
-                join_unit<DV, Bf16>(p.o, p.ws, cut, p.counters + 2 * cut.c0 + g, 2, 1, 0, 1, kRows * (DV + 2), row0, min(half, w.u.rows - row0), kRows,
+                join_unit<DV, Bf16, kBfMath>(p.o, p.ws, cut, p.counters + 2 * cut.c0 + g, 2, 1, 0, 1, kRows * (DV + 2), row0, min(half, w.u.rows - row0), kRows,
                                     w.u.row0, w.q.q0, w.at.head * (int)b.group.d, b.group, smem_addr(&aux.join[g]), cuts, &aux.answer[g], wait, ok);
                 if (!ok) break;
             }
@@ -426,7 +461,7 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         } while (ok && w.next(b));
     } else if (warp == 1) {
         // ---- matrix products ----
-        constexpr uint32_t qk_desc = mma_desc(Bf16, 128, 128, false), pv_desc = mma_desc(Bf16, 128, DV, true);
+        constexpr uint32_t qk_desc = mma_desc(kBfMath, 128, 128, false), pv_desc = mma_desc(kBfMath, 128, DV, true);
         const uint32_t elected = elect_one();
         const uint64_t qd = smem_desc(base, 16, 1024), kd = smem_desc(base + S::kOffK, 16, 1024), vd = smem_desc(base + S::kOffV, kPanel, 1024);
         int it = 0, steps[2] = {0, 0}, units = 0;
@@ -435,7 +470,8 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
             if (w.u.tiles == 0) continue;
             const bool both = w.u.rows > half;
             const int n = both ? 2 * w.n : w.n;
-            ok = wait.warp(smem_addr(&aux.q_full), units++ & 1);
+            ok = kScaled ? wait.warp(smem_addr(&aux.q_ready[units & 1]), units >> 1 & 1) : wait.warp(smem_addr(&aux.q_full), units & 1);
+            units++;
             if (!ok) break;
             tc_fence_after();
             const auto qk = [&](int i) {
@@ -504,7 +540,7 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         // ---- tiles of them ----
         if constexpr (kRowsKind) {
             const int thread = tid - 384;
-            int slot = 0, turn = 0, it = 0;
+            int slot = 0, turn = 0, it = 0, units = 0;
             bool ok = true;
             do {
                 if (w.u.tiles == 0) continue;
@@ -519,12 +555,21 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                         const Rows &rows = v ? p.v : p.k;
                         ok = (it < depth || wait.warp(empty, (it / depth - 1) & 1)) && wait.warp(smem_addr(&aux.stage_full[slot]), turn & 1);
                         if (!ok) break;
-                        rows.template unpack<DK, Bf16>(base + S::kOffStage + slot * rows.stage_bytes, base + (v ? S::kOffV + to * S::kV : S::kOffK + to * S::kK),
+                        rows.template unpack<DK>(base + S::kOffStage + slot * rows.stage_bytes, base + (v ? S::kOffV + to * S::kV : S::kOffK + to * S::kK),
                                                        w.at.head, w.u.lo - kb, w.u.hi - kb, thread);
                         fence_async_smem();
                         warp_arrive(full);
                         if (lane == 0) mbar_arrive(smem_addr(&aux.stage_empty[slot]));
                         if (++slot == p.stages) slot = 0, turn++;
+                    }
+                    if (kScaled && t == 0 && ok) {  // behind the first tiles, which can be made before the unit's queries are there
+                        ok = wait.warp(smem_addr(&aux.q_full), units & 1);
+                        if (!ok) break;
+#pragma unroll 1
+                        for (int g = 0; g < (w.u.rows > half ? 2 : 1); g++)
+                            smem[S::kOffScales + (units & 1) * 256 + g * 128 + thread] = (unsigned char)scale_row<DK>(base + g * S::kQ, thread);
+                        fence_async_smem();
+                        warp_arrive(smem_addr(&aux.q_ready[units++ & 1]));
                     }
                 }
             } while (ok && w.next(b));

@@ -41,8 +41,8 @@ int kv_attention_q4(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_
     if (workspace == nullptr) return KV_ERR_INVALID_ARG;
     if (!aligned16(workspace) || ((uintptr_t)lse & 3u)) return KV_ERR_ALIGN;
     // By the rows (tokens times query heads of a key head) that a request has on average.  Each side measured, 16 requests of 8000 with 8 key
-    // heads of 128 in bf16, groups of 4: 8 rows in units of 8 46 us, of 16 57; 16 rows with few rows' kernel 67, many rows' 115; 20 rows 95 and 116;
-    // 32 rows 98 and 116; 48 rows 125 and 120.  (64 requests of 2000: 32 rows 96 and 134, 64 rows 169 and 137; one of 120000: 32 rows 101 and 116.)
+    // heads of 128 in bf16, groups of 4: 8 rows in units of 8 46 us, of 16 57; 16 rows with few rows' kernel 67, many rows' 104; 20 rows 95 and 106;
+    // 32 rows 98 and 106; 36 rows 124 and 111.  (64 requests of 2000: 32 rows 97 and 127, 48 rows 137 and 131; one of 120000: 32 rows 89 and 104.)
     const bool many = batch->n_tokens * group > 32ll * batch->n_reqs;
     const int rows = batch->n_tokens * group <= 8ll * batch->n_reqs ? 8 : 16;
     Q4Params p = {};

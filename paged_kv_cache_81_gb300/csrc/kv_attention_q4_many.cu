@@ -1,11 +1,14 @@
 // kv_attention_q4 for many rows: prefill chunks, and decoding of more than 32 query rows a key head.
 //
-// kv_attention's kernel (kv_attention.cu) with tiles of 16-bit keys and values that four warps make of packed rows, which come by
+// kv_attention's kernel (kv_attention.cu) with tiles of fp16 keys and values that four warps make of packed rows, which come by
 // TMA: a head's codes and the 16 bytes that hold its scales.  A thread takes 32 elements of a row (16 bytes of codes, two scales) at a
-// time and writes them as four 16-byte pieces of the swizzled panels.  A code times its scale is exact in fp16 and in bf16, so the
-// products are those of the values that the cache stands for.  fp16: one conversion and one product a pair; bf16 goes through two
-// 32-bit products, which keeps three units busy with it (shifting the fp16 bits into bf16's place took the integer unit 32 cycles
-// a word of codes, this 16).
+// time and writes them as four 16-byte pieces of the swizzled panels, one conversion and one product a pair: a code times its scale is
+// exact in fp16, so the products are those of the values that the cache stands for.  bf16 queries are brought to fp16 as well, a
+// power of two a row apart; made into bf16 instead, through 32-bit products, tiles took 870 us where they take 811 now, and weights lost three bits.
+//
+// Four chunks of 2048 to 4096 tokens over 4096 to 8192, 32 heads over 8 of 128: 811 us (fp16 789), 1.1 PFLOP/s; kv_attention over 16-bit rows
+// 670.  The warps that make tiles take issue slots and shared memory from the softmax: a step of 256 rows by 128 keys takes about 4000
+// cycles, 3600 there.  Their loop is short: straight code for all rows of a tile runs at the rate that instructions come at (870, 1041 us).
 #define PKV_APART __forceinline__
 
 #include "kv_attention_kernel.cuh"
@@ -79,7 +82,7 @@ struct Q4Rows {
     }
 
     // A staged tile into panels, by 128 threads; rows outside [lo, hi) become zeros, whatever the stage holds there.
-    template <int D, bool Bf16>
+    template <int D>
     __device__ __forceinline__ void unpack(uint32_t stage, uint32_t tile, int head, int lo, int hi, int thread) const
     {
         constexpr int kParts = D / 32, kRowsATurn = 128 / kParts;
@@ -110,7 +113,6 @@ struct Q4Rows {
             if (j + 1 < kTile / kRowsATurn) load(j + 1, next_c, next_unit);
             uint32_t u = e4m3x2_to_f16(unit);
             if (swap) u = u >> 16 | u << 16;
-            const float2 f = f16x2_to_f32(u);
             const uint32_t z[2] = {u << 16 | (u & 0xffffu), u >> 16 | (u & 0xffff0000u)};
             const uint32_t word[4] = {swap ? c.z : c.x, swap ? c.w : c.y, swap ? c.x : c.z, swap ? c.y : c.w};
 #pragma unroll
@@ -118,15 +120,7 @@ struct Q4Rows {
                 uint32_t v[4];
                 q4_to_f16(word[i], v);
 #pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    if (Bf16) {
-                        const float s = i < 2 ? f.x : f.y;
-                        const float2 x = f16x2_to_f32(v[k]);
-                        v[k] = pack2<true>(x.x * s, x.y * s);
-                    } else {
-                        v[k] = mul_f16x2(v[k], z[i >> 1]);
-                    }
-                }
+                for (int k = 0; k < 4; k++) v[k] = mul_f16x2(v[k], z[i >> 1]);
                 st_smem16(at[i] + j * kRowsATurn * 128, make_uint4(v[0], v[1], v[2], v[3]));
             }
         }

@@ -9,8 +9,6 @@ from paged_kv_cache_81_gb300 import pagedkv as K
 from tests.attention_support import close, hidden
 from tests.rotate_support import U, VALUES, packed, plane, q4_pages
 
-MANY_ROWS = 32  # rows a request and key head, on average, up to which weights are fp16 whatever the type
-
 
 class Q4Batch:
     """A ragged batch over a scattered pool of 4-bit pages.  Slots that no token uses hold scales of NaN."""
@@ -55,15 +53,14 @@ class Q4Batch:
 def reference(q, k_rows, v_rows, q_lens, scale, causal=True, window=0):
     """(out, lse, out tolerance, lse tolerance) in float64.
 
-    The rounding of the output to its type is u of its value.  Weights are rounded to 16 bits (u_w: fp16, or bf16 for many rows of that type; below 2^-25 of the
+    The rounding of the output to its type is u of its value.  Weights are rounded to fp16 (u_w; below 2^-25 of the
     largest they may be lost), the queries to 2^-25 of the row's largest; products and sums are in 32 bits, of dk terms."""
     u = U[q.dtype]
     outs, lses, tol_o, tol_l = [], [], [], []
     first = 0
     kv_heads = k_rows[0].shape[1]
     group = q.shape[1] // kv_heads
-    many = q.shape[0] * group > MANY_ROWS * len(q_lens)
-    u_w = u if many else 2.0 ** -11
+    u_w = 2.0 ** -11
     for k, v, m in zip(k_rows, v_rows, q_lens):
         x = q[first:first + m].double()
         first += m

@@ -98,6 +98,14 @@ def test_many_requests_of_whole_rows(kv_heads, group, dim):
                       dtype=dtype, seed=dim))
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_many_units_of_one_tile(dtype):
+    """Prompts whose units have a tile or two each, so that the next unit's queries come while the last one is still being written."""
+    lens = [1 + 53 * i % 150 for i in range(900)]
+    check(Q4Batch(lens, lens, 4, 1, 64, dtype=dtype, seed=2))
+    check(Q4Batch([n // 2 + 33 for n in lens[:300]], [n + 40 for n in lens[:300]], 8, 2, 128, dtype=dtype, seed=3))
+
+
 def test_many_short_requests():
     lens = [1 + 37 * i % 300 for i in range(700)]
     check(Q4Batch([1] * 700, lens, 4, 2, 64, block=8, seed=1))
@@ -113,9 +121,11 @@ def test_flat_and_peaked_scores(spread, long):
         check(Q4Batch([2, long], [900, 500], 4, 2, 64, spread=spread, dtype=FP, seed=4))
 
 
-def test_queries_of_very_different_sizes():
+@pytest.mark.parametrize("tokens", [4, 64, 200])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_queries_of_very_different_sizes(tokens, dim):
     """Rows of 2^-100 and of 2^60 beside one another, a row of zeros, and elements far below their row's largest."""
-    b = Q4Batch([4], [300], 4, 2, 64, seed=6)
+    b = Q4Batch([tokens], [300], 4, 2, dim, seed=6)
     q = b.q_cpu.float()
     q[0] *= 2.0 ** -100
     q[1] = 0
