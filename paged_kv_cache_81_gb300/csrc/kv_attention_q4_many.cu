@@ -7,8 +7,8 @@
 // power of two a row apart; made into bf16 instead, through 32-bit products, tiles took 870 us where they take 811 now, and weights lost three bits.
 //
 // Four chunks of 2048 to 4096 tokens over 4096 to 8192, 32 heads over 8 of 128: 811 us (fp16 789), 1.1 PFLOP/s; kv_attention over 16-bit rows
-// 670.  The warps that make tiles take issue slots and shared memory from the softmax: a step of 256 rows by 128 keys takes about 4000
-// cycles, 3600 there.  Their loop is short: straight code for all rows of a tile runs at the rate that instructions come at (870, 1041 us).
+// 670.  The warps that make tiles take issue slots and shared memory from the softmax, so that a step takes a fifth more than there.
+// Their loop is short: straight code for all rows of a tile runs at the rate that instructions come at (870, 1041 us).
 #define PKV_APART __forceinline__
 
 #include "kv_attention_kernel.cuh"
