@@ -9,6 +9,10 @@
 // tcgen05 product would want them written to shared memory, twice the bytes of the cache's 16-bit rows a cycle
 // (82 in and 82 out of 128), or both operands in 4 bits, which queries and weights are not.
 //
+// Measured: 64 requests of 4096 to 12288 tokens, 32 heads over 8 of 128, pages of 16: 113 us, 82% of the copy rate: about 98% between the
+// first tile and the last, 8 us before and 5 to 12 after (ends of pieces, joins); with 16 key heads 213 us, 86%.  The integer pipe is half
+// taken, by codes.  12 rows over 64 requests of 8000: 152 us, 59%: two products of 8 rows, twice the exponentials.
+//
 // Queries are brought to [1, 2) by a power of two a row and held in fp16, weights are fp16 (kv_tensor.cuh, weight_offset);
 // sums are in 32 bits.
 //
