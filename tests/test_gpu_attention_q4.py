@@ -98,6 +98,16 @@ def test_many_requests_of_whole_rows(kv_heads, group, dim):
                       dtype=dtype, seed=dim))
 
 
+@pytest.mark.parametrize("kv_heads", [1, 2, 4, 6, 8, 16, 32])
+@pytest.mark.parametrize("tokens", [1, 4, 60])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_tables_as_wide_as_long_contexts(kv_heads, tokens, dim):
+    """Few requests that may be long: whole rows of heads, in many pieces."""
+    b = Q4Batch([tokens, 1], [4000, 100], 3 * kv_heads, kv_heads, dim, seed=dim)
+    b.table = torch.cat([b.table, torch.full((2, 40000), -1, dtype=torch.int32, device="cuda")], 1)
+    check(b)
+
+
 @pytest.mark.parametrize("dtype", [BF, FP])
 def test_many_units_of_one_tile(dtype):
     """Prompts whose units have a tile or two each, so that the next unit's queries come while the last one is still being written."""
