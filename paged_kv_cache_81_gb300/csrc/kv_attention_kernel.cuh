@@ -232,14 +232,19 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
             sees(b, w.q, (int)fdiv((uint32_t)(w.u.row0 + min(row, w.u.rows - 1)), b.group), lo, hi);
             const bool warp_live = __any_sync(0xffffffffu, live);
             float m = -INFINITY, l = 0.0f, back = 1.0f;
+            const int first = both ? 0 : g, step = both ? 1 : 2, kt0 = w.u.tile0 + w.at.off;
             if (kScaled) {  // the row's own unit
-                if (!wait.warp(smem_addr(&aux.q_ready[units & 1]), units >> 1 & 1)) { ok = false; break; }
-                back = __uint_as_float((uint32_t)smem[S::kOffScales + (units & 1) * 256 + (both ? g * 128 : 0) + t] << 23);
+                // Only a group with a step in the unit waits: its weights hold the products back from the unit after, whose last one
+                // lets the queries of the one after that complete this barrier again.  The odd group of a unit of one tile holds
+                // nothing back: late (joining a cut unit), it would find the barrier a phase further on and wait for good.
+                if (first < w.n) {
+                    if (!wait.warp(smem_addr(&aux.q_ready[units & 1]), units >> 1 & 1)) { ok = false; break; }
+                    back = __uint_as_float((uint32_t)smem[S::kOffScales + (units & 1) * 256 + (both ? g * 128 : 0) + t] << 23);
+                }
                 units++;
                 c = fminf(fmaxf(p.o.c * back, 0x1p-120f), 0x1p127f);  // so small a one weighs all alike, and leaves slack a number
                 slack = 8.0f / c;
             }
-            const int first = both ? 0 : g, step = both ? 1 : 2, kt0 = w.u.tile0 + w.at.off;
             for (int k = first; k < w.n; k += step) {
                 const int kb = (kt0 + k) * kTile;
                 if (!wait.warp(smem_addr(&aux.s_full[g]), steps & 1)) { ok = false; break; }

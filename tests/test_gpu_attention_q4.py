@@ -116,6 +116,24 @@ def test_many_units_of_one_tile(dtype):
     check(Q4Batch([n // 2 + 33 for n in lens[:300]], [n + 40 for n in lens[:300]], 8, 2, 128, dtype=dtype, seed=3))
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("shorts", [1, 3, 12])
+def test_cut_units_before_short_ones(dtype, dim, shorts):
+    """Long prompts, whose units are cut and joined, with prompts of one tile and at most 128 rows behind each: the half of a
+    block that joins is late for those. The same bits every time, and no wait that runs out."""
+    q_lens, kv_lens = [], []
+    for i in range(8):
+        q_lens += [300] + [20 + (7 * i + 5 * j) % 13 for j in range(shorts)]
+        kv_lens += [2000 + 250 * i] + [33 + (31 * i + 17 * j) % 96 for j in range(shorts)]
+    b = Q4Batch(q_lens, kv_lens, 8, 2, dim, dtype=dtype, seed=shorts)
+    ws = K.kv_attention_workspace()
+    want = [x.clone() for x in check(b, workspace=ws)]
+    for _ in range(100):
+        assert all(torch.equal(x, y) for x, y in zip(want, b.run(dim ** -0.5, workspace=ws)))
+    assert K.kv_get_last_error(clear=True) == 0 and int(ws[:16384].sum()) == 0
+
+
 def test_many_short_requests():
     lens = [1 + 37 * i % 300 for i in range(700)]
     check(Q4Batch([1] * 700, lens, 4, 2, 64, block=8, seed=1))
