@@ -657,7 +657,8 @@ KV_API int kv_rotate_write_q4(const kv_new_tokens *tokens, const kv_rope *rope, 
  * kv_attention_q4: kv_attention over a 4-bit cache: K[j], V[j] = the values that the rows stand for, with the tensors' scales
  * k_scale and v_scale (in [1e-30, 1e30], scale * k_scale too).  d->dtype is that of q and out; head_dim and head_dim_v are multiples of
  * 32, at most 128.  The values are exact in the products; queries and weights are rounded to fp16 at most: a query to 2^-25 of its row's
- * largest element, a weight as kv_attention's in fp16.
+ * largest element, a weight to fp16, of which none is lost above 2^-31 of its row's largest, at any size of the scores (the products
+ * q . K before the scales have to be finite 32-bit numbers).
  * Everything else, the workspace among it, as for kv_attention.
  */
 KV_API int kv_attention_q4(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_cache_desc *k, int32_t k_tensor, int32_t k_plane,

@@ -123,6 +123,22 @@ __device__ __forceinline__ uint32_t scale_row(uint32_t set, int thread)
     return e;
 }
 
+// Weights of 32 scores as weights32 gives them in fp16, the reference m (0 for none) taken off before the product: 2^(c (s - m) + 7), right at any
+// size of s.  weights32 rounds c m - 7 by itself, upwards: weights of different references do not agree then (by 2% at 2^19), and at
+// 2^29 every one is lost.
+__device__ __forceinline__ void weights32_at_any_size(const uint32_t (&x)[32], float c, float m, float2 (&sum)[2], uint32_t (&pk)[16])
+{
+    const float2 cc = make_float2(c, c), nn = make_float2(-m, -m), seven = make_float2(7.0f, 7.0f);
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+        float2 e = fma2(add2(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), nn), cc, seven);
+        e.x = exp2_fast(e.x);
+        e.y = exp2_fast(e.y);
+        sum[i & 1] = add2(sum[i & 1], e);
+        pk[i] = pack2<false>(e.x, e.y);
+    }
+}
+
 // A unit's queries, `half` rows at `base` and the others at its second panel set, by one warp.
 template <int DK>
 __device__ __forceinline__ void load_queries(const AttentionParams &p, const CUtensorMap *map, const Walk &w, int half, uint32_t base, uint32_t bar)
@@ -302,17 +318,23 @@ attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                         }
                     }
                     const float mc = weight_offset<kBfMath>(m, c);
+                    // rows of another kind: large scores take the short loop, whose weights are right at any size.  Up to here the
+                    // rounding of c m - 7 is a sixth of a weight's.
+                    const bool short_loop = hide || (kRowsKind && __any_sync(0xffffffffu, fabsf(mc) > 0x1p10f));
                     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                     uint32_t pk[16];
                     // P takes the columns of the upper 64 scores: 32 keys' weights stand in 16 columns from 64 on, so
                     // going down no score is overwritten before it has been read
-                    if (hide) {
+                    if (short_loop) {
 #pragma unroll 1
                         for (int q = seen_to(w.u, kb) - 1; q >= seen_from(w.u, kb); q--) {
                             tmem_ld32(s_at + q * 32, x0);
                             tc_wait_ld();
                             hide32(x0, from - q * 32, to_key - q * 32);
-                            weights32<kBfMath>(x0, c, mc, sum, pk);
+                            if constexpr (kRowsKind)
+                                weights32_at_any_size(x0, c, m == -INFINITY ? 0.0f : m, sum, pk);
+                            else
+                                weights32<kBfMath>(x0, c, mc, sum, pk);
                             tmem_st16(s_at + 64 + q * 16, pk);
                         }
                     } else {

@@ -13,8 +13,10 @@
 // first tile and the last, 8 us before and 5 to 12 after (ends of pieces, joins); with 16 key heads 213 us, 86%.  The integer pipe is half
 // taken, by codes.  12 rows over 64 requests of 8000: 152 us, 59%: two products of 8 rows, twice the exponentials.
 //
-// Queries are brought to [1, 2) by a power of two a row and held in fp16, weights are fp16 (kv_tensor.cuh, weight_offset);
-// sums are in 32 bits.
+// Queries are brought to [1, 2) by a power of two a row and held in fp16, weights are fp16, 2^7 times as large (kv_tensor.cuh,
+// weight_offset); sums are in 32 bits.  The reference m of a row's weights is one of its scores, as the product left them, and is taken off
+// before the product with c: 2^(c (s - m) + 7) with s - m <= 8 / c, which stays below fp16's 2^16 whatever the size of s.  (With c s and c m rounded
+// by themselves it did not from scaled scores of 10^7 on.)
 //
 // One persistent CTA per SM; a unit is one request's rows of as many key heads as there are warps for, or fewer (launch_few).
 //   warps 0, 1 (to 3)  bring rows of keys and of values by TMA, one for each run of slots inside a page, into rings of tiles
@@ -36,6 +38,7 @@ namespace {
 constexpr int kLeast = 2;     // tiles of a piece of a unit, at least
 constexpr int kMaxHeads = 16;  // key heads of a unit
 constexpr int kMaxSlots = 8;
+constexpr float kNothing = -3e38f;  // the reference of a row that has seen no key yet: a number, so that a hidden score less it is -inf still
 constexpr int kMany = 12;     // pieces of a unit from which on they are joined in two stages
 // The key of row r of 8 (hexadecimal digit r) by how far rows lie apart: in pairs that are 64 bytes off one another, modulo 128.
 constexpr uint32_t order_of(uint32_t pitch)
@@ -129,6 +132,7 @@ struct Aux {
     int scan[4 * 20];
     Place place;
     Walk walk[20];  // of each warp: held in registers it would crowd the loop over the tiles
+    unsigned char size[16][16];  // of each computing warp's rows: the exponent of the power of two that was taken off
     int gave_up;
 };
 
@@ -277,8 +281,8 @@ struct Sums {
                 }
             }
     }
-    // Others from shared memory are added.
-    __device__ __forceinline__ void join(const float *from, int rows)
+    // Others from shared memory are added; c: log2 of a weight a unit of the maxima.
+    __device__ __forceinline__ void join(const float *from, int rows, const float (&c)[NT][2])
     {
         const int lane = threadIdx.x & 31, n = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -288,8 +292,8 @@ struct Sums {
                 const int r = 8 * x + 2 * t + i;
                 if (r >= rows) continue;
                 const float2 ml = reinterpret_cast<const float2 *>(from + 8 * NT * kPitch)[r];
-                const float top = fmaxf(m[x][i], ml.x), z = top == -INFINITY ? 0.0f : top;
-                const float a = exp2_fast(m[x][i] - z), f = exp2_fast(ml.x - z);
+                const float top = fmaxf(m[x][i], ml.x);
+                const float a = exp2_fast((m[x][i] - top) * c[x][i]), f = exp2_fast((ml.x - top) * c[x][i]);
                 m[x][i] = top;
                 l[x][i] = l[x][i] * a + ml.y * f;
 #pragma unroll
@@ -311,7 +315,7 @@ __device__ __forceinline__ char *row_out(const FewParams &p, const HeadRows &u, 
     lse = p.o.lse ? p.o.lse + token * p.o.heads + head : nullptr;
     return p.o.out + token * p.o.out_token + (int64_t)head * p.o.out_head;
 }
-__device__ __forceinline__ float lse_of(float m, float l) { return l > 0.0f ? fmaf(m, 0.69314718055994530942f, weight_log<false>(l)) : -INFINITY; }
+__device__ __forceinline__ float lse_of(const FewParams &p, float m, float l) { return l > 0.0f ? fmaf(m, p.o.scale, weight_log<false>(l)) : -INFINITY; }
 __device__ __forceinline__ uint32_t pack_out(const FewParams &p, float a, float b) { return p.bf16 ? pack2<true>(a, b) : pack2<false>(a, b); }
 
 // Joins `count` pieces of one head of a cut unit in the workspace, in their order, by `threads` threads of which this is number `thread`.
@@ -357,12 +361,12 @@ __device__ __forceinline__ void join_pieces(const FewParams &p, const CutUnit &u
 #pragma unroll
             for (int j = 0; j < kWide; j++) {
                 const float now = fmaxf(fmaxf(fmaxf(s[j][0].x, s[j][1].x), fmaxf(s[j][2].x, s[j][3].x)), top[j]), z = now == -INFINITY ? 0.0f : now;
-                const float a = exp2_fast(top[j] - z);
+                const float a = exp2_fast((top[j] - z) * p.o.c);
                 top[j] = now;
                 l[j] *= a, o[j].x *= a, o[j].y *= a, o[j].z *= a, o[j].w *= a;
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
-                    const float f = exp2_fast(s[j][k].x - z);
+                    const float f = exp2_fast((s[j][k].x - z) * p.o.c);
                     l[j] += s[j][k].y * f, o[j].x += w[j][k].x * f, o[j].y += w[j][k].y * f, o[j].z += w[j][k].z * f, o[j].w += w[j][k].w * f;
                 }
             }
@@ -380,7 +384,7 @@ __device__ __forceinline__ void join_pieces(const FewParams &p, const CutUnit &u
                 const float inv = l[j] > 0.0f ? p.v_scale / l[j] : 0.0f;
                 if (quad[j] * 4 < p.o.dv)
                     reinterpret_cast<uint2 *>(to)[quad[j]] = make_uint2(pack_out(p, o[j].x * inv, o[j].y * inv), pack_out(p, o[j].z * inv, o[j].w * inv));
-                if (quad[j] == 0 && lse) *lse = lse_of(top[j], l[j]);
+                if (quad[j] == 0 && lse) *lse = lse_of(p, top[j], l[j]);
             }
         }
     }
@@ -527,7 +531,8 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
                     for (int i = 0; i < D / 32; i++)
                         if (t * (D / 4) + 8 * i < dk) raw[i] = __ldg(reinterpret_cast<const uint4 *>(from) + t * (D / 32) + i);
                 }
-                float to = 1.0f, back = 1.0f;
+                float to = 1.0f;
+                uint32_t e = 127;
                 if (bf16) {
                     float most = 0.0f;
 #pragma unroll
@@ -539,10 +544,11 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
                     }
                     most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
                     most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-                    const uint32_t e = min(max(__float_as_uint(most) >> 23, 1u), 253u);
+                    e = min(max(__float_as_uint(most) >> 23, 1u), 253u);
                     to = __uint_as_float((254u - e) << 23);
-                    back = __uint_as_float(e << 23);
                 }
+                if (t == 0) aux.size[me][r] = (unsigned char)e;
+                const float back = __uint_as_float(e << 23);
 #pragma unroll
                 for (int i = 0; i < D / 32; i++) {
                     const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
@@ -552,8 +558,8 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
                     st_smem16(q_at + (x * (D / 32) + i) * 512, make_uint4(f[0], f[1], f[2], f[3]));
                 }
 #pragma unroll
-                for (int i = 0; i < 2; i++)  // a normal number: a hidden score, -inf, stays that in the product with it
-                    c[x][i] = fminf(fmaxf(p.o.c * __shfl_sync(0xffffffffu, back, (2 * t + i) * 4), 0x1p-126f), 0x1p127f);
+                for (int i = 0; i < 2; i++)  // so small a one weighs all alike, and a hidden score, -inf, stays that in the product with it
+                    c[x][i] = fminf(fmaxf(p.o.c * __shfl_sync(0xffffffffu, back, (2 * t + i) * 4), 0x1p-120f), 0x1p127f);
             }
 #pragma unroll
             for (int x = 0; x < NT; x++) {
@@ -561,7 +567,7 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
                 for (int i = 0; i < D / 16; i++)
 #pragma unroll
                     for (int j = 0; j < 4; j++) o[i][x][j] = 0.0f;
-                m[x][0] = m[x][1] = -INFINITY;
+                m[x][0] = m[x][1] = kNothing;
                 l[x][0] = l[x][1] = 0.0f;
             }
             // where this thread's codes and scales lie in a tile; scales of heads that come apart begin off a 16-byte boundary
@@ -657,8 +663,8 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
                         float v = -INFINITY;
 #pragma unroll
                         for (int step = 0; step < F::kSteps; step++) v = fmaxf(v, fmaxf(sc[step][x][i], sc[step][x][i + 2]));
-                        top[x][i] = v * c[x][i];
-                        grow |= top[x][i] > m[x][i] + 8.0f;
+                        top[x][i] = v;
+                        grow |= (v - m[x][i]) * c[x][i] > 8.0f;
                     }
                 if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -669,7 +675,7 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
 #pragma unroll
                             for (int d = 4; d < 32; d *= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
                             const float now = fmaxf(m[x][i], v);
-                            const float a = now == -INFINITY ? 1.0f : exp2_fast(m[x][i] - now);
+                            const float a = exp2_fast((m[x][i] - now) * c[x][i]);
                             m[x][i] = now;
                             l[x][i] *= a;
 #pragma unroll
@@ -679,14 +685,15 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
                 uint32_t pf[F::kSteps][NT][2];
 #pragma unroll
                 for (int x = 0; x < NT; x++) {
-                    const float off0 = m[x][0] == -INFINITY ? 0.0f : 7.0f - m[x][0], off1 = m[x][1] == -INFINITY ? 0.0f : 7.0f - m[x][1];
+                    const float2 off = make_float2(-m[x][0], -m[x][1]), cc = make_float2(c[x][0], c[x][1]), seven = make_float2(7.0f, 7.0f);
 #pragma unroll
                     for (int step = 0; step < F::kSteps; step++) {
                         float e[4];
 #pragma unroll
-                        for (int j = 0; j < 4; j++) {
-                            e[j] = exp2_fast(fmaf(sc[step][x][j], c[x][j & 1], j & 1 ? off1 : off0));
-                            l[x][j & 1] += e[j];
+                        for (int j = 0; j < 4; j += 2) {
+                            const float2 z = fma2(add2(make_float2(sc[step][x][j], sc[step][x][j + 1]), off), cc, seven);
+                            e[j] = exp2_fast(z.x), e[j + 1] = exp2_fast(z.y);
+                            l[x][0] += e[j], l[x][1] += e[j + 1];
                         }
                         pf[step][x][0] = transposed8(pack2<false>(e[0], e[1]));
                         pf[step][x][1] = transposed8(pack2<false>(e[2], e[3]));
@@ -764,13 +771,22 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
                 } else {
                     if (!wait.warp(full, joined & 1)) ok = false;
                     if (!ok) break;
-                    sums.join(at, rows);
+                    sums.join(at, rows, c);
                     if (!first_round || part == 0) warp_arrive(smem_addr(&aux.join_free[place]));
                 }
             }
             joined++;
             if (!ok) break;
             if (gone) continue;
+#pragma unroll
+            for (int x = 0; x < NT; x++)
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    // in units of the call's scale from here on.  (The thread's numbers anew: kept in registers over the tiles they spill, and the
+                    // long decode batch takes 6 us more.)
+                    const uint32_t e = aux.size[(threadIdx.x >> 5) - F::kLoaders][8 * x + 2 * (threadIdx.x & 3) + i];
+                    m[x][i] = l[x][i] > 0.0f ? m[x][i] * __uint_as_float(e << 23) : -INFINITY;
+                }
             if (!w.whole()) {
                 // the last of the CTA's heads to be in the workspace counts the piece; who counts the last one joins them all in the end
                 const Cut cut(line, w.pos - w.at.off, unit_cost(w.u));
@@ -807,7 +823,7 @@ attention_q4_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
 #pragma unroll
                     for (int k = 0; k < D / 64; k++)
                         if (n * (D / 8) < dv) reinterpret_cast<uint4 *>(to)[n * (D / 64) + k] = make_uint4(z[4 * k], z[4 * k + 1], z[4 * k + 2], z[4 * k + 3]);
-                    if (n == 0 && lse) *lse = lse_of(m[x][i], l[x][i]);
+                    if (n == 0 && lse) *lse = lse_of(p, m[x][i], l[x][i]);
                 }
         } while (next_unit());
         // ---- cut units: the CTA that brought the last piece joins them, in the order of the keys; of many pieces the last of every

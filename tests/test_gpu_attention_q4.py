@@ -7,9 +7,9 @@ import pytest
 import torch
 
 from paged_kv_cache_81_gb300 import pagedkv as K
-from tests.attention_support import NAN, close
+from tests.attention_support import NAN, close, hidden
 from tests.q4_support import Q4Batch, check, reference
-from tests.rotate_support import held, plane, quantised, q4_pages, rotated
+from tests.rotate_support import U, VALUES, held, packed, plane, quantised, q4_pages, rotated
 
 pytestmark = pytest.mark.gpu
 
@@ -165,6 +165,67 @@ def test_queries_of_very_different_sizes(tokens, dim):
     b.q_cpu = q.to(BF)
     b.q = b.q_cpu.cuda()
     check(b, scale=2.0 ** -62)
+
+
+def large_scores(q_lens, kv_lens, heads, kv_heads, dim, dtype, seed):
+    """A batch whose products q . K are 2752512 or -2752512 and a whole number of up to 108 beside it: exact in 32 bits, at any scale."""
+    b = Q4Batch(q_lens, kv_lens, heads, kv_heads, dim, dtype=dtype, seed=seed)
+    g = torch.Generator().manual_seed(seed)
+    for r, n in enumerate(kv_lens):
+        code = torch.zeros(n, kv_heads, dim, dtype=torch.long)
+        code[..., 0] = 7
+        code[..., 16:32] = torch.randint(0, 16, (n, kv_heads, 16), generator=g)
+        unit = torch.ones(n, kv_heads, dim // 16)
+        unit[..., 0] = 448.0
+        unit = unit.to(torch.float8_e4m3fn)
+        j = torch.arange(n)
+        b.tensors[0][b.table_cpu[r, j // 16].long(), j % 16] = packed(code, unit.view(torch.uint8)).cuda()
+        b.rows[0][r] = VALUES[code] * unit.double().repeat_interleave(16, -1)
+    q = torch.zeros(sum(q_lens), heads, dim)
+    q[..., 0], q[..., 16], q[..., 17] = 1024.0, 2.0, 16.0
+    q[1::3, :, 0] *= -1
+    if dtype == BF:
+        q[:, 1::2] *= 2.0 ** 20  # another power of two is taken off these rows
+    b.q_cpu = q.to(dtype)
+    b.q = b.q_cpu.cuda()
+    return b
+
+
+@pytest.mark.parametrize("scale", [0.125, 1.0, 3.0, 6.0, 16.0, 1024.0, 2.0 ** 40, 1e30])
+@pytest.mark.parametrize("q_lens,kv_lens,heads", [([1], [3000], 8), ([3], [3000], 8), ([1] * 30, [150 + 7 * i for i in range(30)], 4), ([100], [3000], 4),
+                                                  ([60, 9] * 10, [150, 70] * 10, 4)])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_scores_of_any_size(scale, q_lens, kv_lens, heads, dim, dtype):
+    """Finite scores up to 3e36: weights that neither pass what fp16 holds nor vanish, out of the differences alone.
+
+    The products are exact. A weight's exponent, c (s - m) + 7, is off by the rounding of c, of the product and of the sum, each 2^-24 of at
+    most 45 (what weighs less is lost anyway), and 2^x by 2^-22: 2^-16 in all covers it twice over."""
+    b = large_scores(q_lens, kv_lens, heads, 2, dim, dtype, seed=len(q_lens) + dim)
+    rows = scale * 2.0 ** -20 if dtype == BF else scale  # of the rows that are 2^20 times as large
+    K.kv_get_last_error(clear=True)
+    for s in {scale, rows}:
+        if s < 1e-30:
+            continue
+        out, lse = b.run(s)
+        at = 0
+        for k, v, m in zip(*b.rows, q_lens):
+            x, n, group = b.q_cpu[at:at + m].double(), k.shape[0], heads // 2
+            kd, vd = k.repeat_interleave(group, 1), v.repeat_interleave(group, 1)
+            z = torch.einsum("mhd,nhd->mhn", x, kd) * float(torch.tensor(s, dtype=torch.float32))
+            hide = hidden(m, n, True, 0)[:, None]
+            z = z.masked_fill(hide, -math.inf)
+            top = z.amax(-1, keepdim=True)
+            p = torch.exp(z - top)
+            total = p.sum(-1, keepdim=True)
+            p /= total
+            o, mag = (torch.einsum("mhn,nhd->mhd", p, y) for y in (vd, vd.abs()))
+            want = (top + total.log())[..., 0]
+            close(out[at:at + m], o, U[dtype] * o.abs() * 1.01 + (2.0 ** -11 * 1.01 + 2.0 ** -16) * mag + n * 2.0 ** -25 * vd.abs().max(), "out")
+            fine = want.abs() < 3e38  # the others are no 32-bit numbers
+            close(lse[at:at + m][fine.cuda()], want[fine], 2.0 ** -22 * want[fine].abs() + 2.0 ** -15, "lse")
+            at += m
+    assert K.kv_get_last_error(clear=True) == 0
 
 
 def test_growing_scores_rescale():
