@@ -875,8 +875,6 @@ int launch_kernel(FewParams p, const DeviceInfo *dev, cudaStream_t s)
         return st != KV_OK ? st : load_kernels(kernel);
     }
     const int all = p.heads_all, heads = p.unit_heads;
-    p.tile = 16 * p.split * F::kSteps;
-    p.piece_rows = piece_rows(p.k.desc->block_size, p.tile < 256 ? p.tile : 256);
     // A run of rows ends on a multiple of 128 bytes, where a TMA may begin; its rows lie 32 or 96 bytes off one where that allows it.
     const auto pitch = [&](int bytes) {
         const int step = p.piece_rows >= 4 ? 64 : 128 / p.piece_rows, off = p.piece_rows >= 4 ? 32 : 0;
@@ -901,11 +899,20 @@ int launch_kernel(FewParams p, const DeviceInfo *dev, cudaStream_t s)
         }
         return l;
     };
-    p.kl = place(p.k);
-    p.vl = place(p.v);
+    uint32_t pair, join;
+    const auto fit = [&] {
+        p.tile = 16 * p.split * F::kSteps;
+        p.piece_rows = piece_rows(p.k.desc->block_size, p.tile < 256 ? p.tile : 256);
+        p.kl = place(p.k);
+        p.vl = place(p.v);
+        pair = (uint32_t)(p.kl.bytes + p.vl.bytes), join = ((uint32_t)(heads * p.split / 2) * Sums<D, NT>::kShared * 4 + 127) & ~127u;
+        p.slots = (int)((kAll - kFixed - join - 128) / pair);
+    };
+    fit();
+    // One head of several in pages of an odd size (key heads in a prime number): codes and scales of single rows take 128 bytes each, and the
+    // 512 keys of all warps 256 KB.  Half of the warps then.
+    while (!H && p.slots < 1 && p.split > 1) p.split /= 2, fit();
     p.order = order_of(p.kl.codes);
-    const uint32_t pair = (uint32_t)(p.kl.bytes + p.vl.bytes), join = ((uint32_t)(heads * p.split / 2) * Sums<D, NT>::kShared * 4 + 127) & ~127u;
-    p.slots = (int)((kAll - kFixed - join - 128) / pair);
     if (p.slots > kMaxSlots) p.slots = kMaxSlots;
     if (p.slots < 1 || dev->num_sms * 2 * 4 > kCounterBytes) return KV_ERR_UNSUPPORTED;
     CUtensorMap map[4];

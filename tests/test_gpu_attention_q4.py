@@ -47,6 +47,15 @@ def test_pages(block, layout, long):
     check(Q4Batch([1, 2, long], [400, 9, 390], 4, 1, 64, block=block, layout=layout, seed=block))
 
 
+@pytest.mark.parametrize("kv_heads", [11, 13, 17, 19])
+@pytest.mark.parametrize("block", [1, 3, 17])
+@pytest.mark.parametrize("rows", [1, 8, 12, 16, 32])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_heads_that_come_one_by_one_in_odd_pages(kv_heads, block, rows, dim):
+    """Key heads in a prime number, more than a block takes together, whose rows come one by one."""
+    check(Q4Batch([rows // 4 or 1] * 3, [600, 33, 1100], kv_heads * min(rows, 4), kv_heads, dim, block=block, dtype=FP if rows == 12 else BF, seed=rows))
+
+
 @pytest.mark.parametrize("causal,window", [(False, 0), (True, 0), (True, 1), (True, 2), (True, 100), (True, 128), (True, 129), (True, 5000)])
 @pytest.mark.parametrize("long", [4, 200])
 def test_masks(causal, window, long):
