@@ -270,8 +270,9 @@ __device__ __forceinline__ void store_rows32(char *to, const float (&o)[32], flo
     }
 }
 
-// Launch attributes of every attention kernel, set once per device (kv_runtime.cu).
+// Launch attributes of every attention kernel, set once per device (kv_runtime.cu): those over 16 bits, those over 4.
 int prepare_attention(const DeviceInfo &dev);
+int prepare_attention_q4(const DeviceInfo &dev);
 int preload_attention_kernels();  // kv_attention.cu
 int preload_latent_kernels();     // kv_latent.cu
 int preload_expand_kernels();     // kv_expand.cu

@@ -52,7 +52,7 @@ int kv_attention_q4(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_
     const DeviceInfo *dev = current_device();
     if (dev == nullptr) return KV_ERR_CUDA;
     if (workspace_bytes < attention_workspace(dev->num_sms)) return KV_ERR_RANGE;
-    if ((st = prepare_attention(*dev)) != KV_OK) return st;
+    if ((st = prepare_attention_q4(*dev)) != KV_OK) return st;
     p.b.err = dev->err_word;
     const auto plane = [](const kv_cache_desc *c, int tensor, int which, int dim) {
         return Q4Plane{c->base[tensor] + (which ? (uint64_t)c->plane_stride : 0), c, dim};

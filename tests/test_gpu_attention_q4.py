@@ -2,6 +2,9 @@
 from __future__ import annotations
 
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -388,6 +391,31 @@ def test_streams_and_graphs(heads):
         for out, lse in outs:
             close(out, o, to, "out")
             close(lse, l, tl, "lse")
+
+
+_FIRST_CALLS = """
+import torch
+from paged_kv_cache_81_gb300 import pagedkv as K
+from tests.attention_support import Batch
+from tests.q4_support import Q4Batch
+a, b = Batch([1, 2], [50, 60], 4, 2, 64), Q4Batch([1, 2], [50, 60], 4, 2, 64)
+ws = K.kv_attention_workspace()
+outs = [torch.empty(3, 4, 64, dtype=torch.bfloat16, device="cuda"), torch.empty(3, 4, device="cuda")]
+free = []
+for run in (a.run, b.run):
+    run(0.1, workspace=ws, out=outs[0], lse=outs[1])
+    torch.cuda.synchronize()
+    free.append(torch.cuda.mem_get_info()[0])
+print(free[0] - free[1])
+"""
+
+
+def test_16_bit_calls_do_not_load_the_kernels_over_4_bits():
+    """A process whose first attention call is over 16 bits: the kernels over 4 bits take their memory (and time) with their own first call."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
+    assert int(r.stdout) > 0
 
 
 def test_python_refusals():
