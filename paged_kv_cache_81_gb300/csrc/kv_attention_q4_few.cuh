@@ -36,7 +36,6 @@ namespace pkv {
 namespace {
 
 constexpr int kLeast = 2;     // tiles of a piece of a unit, at least
-constexpr int kMaxHeads = 16;  // key heads of a unit
 constexpr int kMaxSlots = 8;
 constexpr float kNothing = -3e38f;  // the reference of a row that has seen no key yet: a number, so that a hidden score less it is -inf still
 constexpr int kMany = 12;     // pieces of a unit from which on they are joined in two stages
@@ -935,11 +934,12 @@ template <int D, int NT>
 int launch_few(FewParams &p, const DeviceInfo *dev, cudaStream_t s)
 {
     constexpr int kWarps = Few<D, NT, 0>::kWarps;
+    // by the logarithm of the heads; those of 8 warps end at 8
     int (*const full[])(FewParams, const DeviceInfo *, cudaStream_t) = {launch_kernel<D, NT, 1>, launch_kernel<D, NT, 2>, launch_kernel<D, NT, 4>,
-                                                                       launch_kernel<D, NT, 8>, launch_kernel<D, NT, kWarps>};
+                                                                       launch_kernel<D, NT, 8>, kWarps > 8 ? launch_kernel<D, NT, kWarps> : nullptr};
     if (dev == nullptr) {
         int st = launch_kernel<D, NT, 0>(p, dev, s);
-        for (int i = 0; st == KV_OK && i < 5; i++) st = full[i](p, dev, s);
+        for (int i = 0; st == KV_OK && i < 5 && full[i]; i++) st = full[i](p, dev, s);
         return st;
     }
     const int all = p.heads_all;

@@ -49,13 +49,6 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t b)
     return v;
 }
 
-__device__ __forceinline__ float2 f16x2_to_f32(uint32_t v)
-{
-    float2 f;
-    asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(f.x), "=f"(f.y) : "r"(v));
-    return f;
-}
-
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
 {
     uint32_t v;
