@@ -580,7 +580,7 @@ typedef struct {
 } kv_rope_scaling;
 
 /* The frequencies as kv_rope takes them, into HOST memory (rot_dim / 2 numbers), and the magnitude (may be NULL).
- * scaling may be NULL (KV_ROPE_PLAIN).  rot_dim even, base > 1. */
+ * scaling may be NULL (KV_ROPE_PLAIN).  rot_dim even, base > 1; frequencies that are no finite 64-bit numbers are refused. */
 KV_API int kv_rope_frequencies(int32_t rot_dim, double base, const kv_rope_scaling *scaling, uint64_t *turns_out, float *magnitude_out);
 
 /*

@@ -722,15 +722,19 @@ int kv_rope_frequencies(int32_t rot_dim, double base, const kv_rope_scaling *sca
         low = std::fmax(std::floor(d * std::log(length / (scaling->fast * kTurn)) / (2.0 * std::log(base))), 0.0);
         high = std::fmin(std::ceil(d * std::log(length / (scaling->slow * kTurn)) / (2.0 * std::log(base))), d - 1.0);
     }
-    for (int i = 0; i < rot_dim / 2; i++) {
+    const auto frequency = [&](int i) {
         double w = std::pow(base, -2.0 * i / d), mix = 1.0;  // mix: how much of the frequency stays as it is
         if (kind == KV_ROPE_LINEAR) mix = 0.0;
         if (kind == KV_ROPE_BANDS) mix = (length * w / kTurn - scaling->slow) / (scaling->fast - scaling->slow);
         if (kind == KV_ROPE_YARN) mix = 1.0 - (i - low) / std::fmax(high - low, 1e-3);
         mix = std::fmin(std::fmax(mix, 0.0), 1.0);
-        if (kind != KV_ROPE_BASE) w = w * mix + w / f * (1.0 - mix);
-        // of a turn: below 2^64, as w is at most 1 (or 1 / f)
-        const double t = std::nearbyint(std::ldexp(std::fmod(w / kTurn, 1.0), 64));
+        return kind == KV_ROPE_BASE ? w : w * mix + w / f * (1.0 - mix);
+    };
+    for (int i = 0; i < rot_dim / 2; i++)  // a factor near 0 takes them out of 64 bits
+        if (!std::isfinite(frequency(i))) return KV_ERR_INVALID_ARG;
+    for (int i = 0; i < rot_dim / 2; i++) {
+        // of a turn, whole ones dropped
+        const double t = std::nearbyint(std::ldexp(std::fmod(frequency(i) / kTurn, 1.0), 64));
         turns_out[i] = t >= 18446744073709551616.0 ? 0 : (uint64_t)t;
     }
     if (magnitude_out) *magnitude_out = (float)(kind == KV_ROPE_YARN && f > 1.0 ? 0.1 * std::log(f) + 1.0 : 1.0);

@@ -76,6 +76,20 @@ def test_frequencies_refused(lib):
         K.kv_rope_frequencies(64, scaling="other")
 
 
+def test_frequencies_that_are_no_numbers(lib):
+    """Factors so small that a frequency (or the changed base) leaves 64-bit floating point: no such frequency has a fraction of a turn."""
+    for kw in (dict(scaling="linear", factor=1e-310), dict(scaling="bands", factor=1e-310), dict(scaling="yarn", factor=1e-310)):
+        with pytest.raises(K.KvError):
+            K.kv_rope_frequencies(64, 10000.0, **kw)
+    with pytest.raises(K.KvError):
+        K.kv_rope_frequencies(4, 10000.0, scaling="base", factor=1e-200)
+    out = (ctypes.c_uint64 * 2)(7, 7)
+    assert lib.kv_rope_frequencies(4, 10000.0, ctypes.byref(K.KvRopeScaling(1, 1e-310, 4096.0, 32.0, 1.0)), out, None) == ARG
+    assert list(out) == [7, 7]  # left as they were
+    turns, _ = K.kv_rope_frequencies(4, 10000.0, scaling="base", factor=1e200)  # the slowest pair slows down to nothing
+    assert turns.tolist()[1] == 0 and radians(turns)[0] == pytest.approx(1.0, rel=2.0 ** -48)
+
+
 def rope(rot=64, offset=0, inter=0, m=1.0, turns=0x1000):
     return K.KvRope(turns, rot, offset, inter, m)
 
