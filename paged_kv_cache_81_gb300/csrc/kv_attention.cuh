@@ -9,7 +9,6 @@
 
 namespace pkv {
 
-constexpr bool kOneJoin = PKV_ONE_JOIN;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int64_t kCounterBytes = KV_ATTENTION_ZEROED_BYTES;  // arrival counts of cut units, zero between calls
 
@@ -98,6 +97,8 @@ struct Output {
     float values = 1.0f;  // what outputs are multiplied by at the end
 };
 
+inline namespace PKV_FORM {
+
 // Joins rows [row0, row0 + rows) of a cut unit from fragments of `stride` floats, or (at.sum) adds fragments up to a
 // new one, in an inner part's odd slot.  A fragment
 // holds its accumulators four columns at a time, [DV / 4][stat rows][4], so that writing (a thread a row)
@@ -185,7 +186,7 @@ __device__ PKV_APART void join_rows(const Output p, const Pieces at, int half, i
     };
     // what the registers beside the tile loop hold; two fragments (a long unit's usual cut) in four trips a row instead
     // of eight: three prefill chunks of 500 to 2000 tokens 117 us, so 114.5
-    if (kOneJoin)  // inlined: short
+    if (PKV_ONE_JOIN)  // inlined: short
         columns(std::integral_constant<int, 4>(), std::integral_constant<int, 2>());
     else if (quads <= 4)
         columns(std::integral_constant<int, 4>(), std::integral_constant<int, 6>());
@@ -228,6 +229,8 @@ __device__ __forceinline__ void join_unit(const Output &p, float *ws, const Cut 
         if (!sum) return;
     }
 }
+
+}  // namespace PKV_FORM
 
 // 32 accumulator columns of a row into its fragment, as join_rows reads them.
 __device__ __forceinline__ void store_fragment32(float *part, int rows, int row, int q, const float (&f)[32])

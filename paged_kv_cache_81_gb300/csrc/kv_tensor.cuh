@@ -14,12 +14,15 @@
 #include "kv_async.cuh"
 #include "kv_common.cuh"
 
-// Code that is called seldom and kept out of its callers' registers.  A kernel that changes its warps' registers cannot call.
+// Code that is called seldom and kept out of its callers' registers.  A kernel that changes its warps' registers cannot call.  What is
+// compiled in either form has a name for each, in the namespace PKV_FORM.
 #ifndef PKV_APART
 #define PKV_APART __noinline__
 #define PKV_ONE_JOIN 0
+#define PKV_FORM called
 #else
 #define PKV_ONE_JOIN 1
+#define PKV_FORM inlined
 #endif
 
 namespace pkv {
@@ -29,6 +32,7 @@ namespace pkv {
 // given up (a word in shared memory) and sets KV_DERR_TIMEOUT; every other wait of the CTA then
 // returns at once, the roles leave their loops, and the CTA ends through its common exit.
 // ---------------------------------------------------------------------------
+inline namespace PKV_FORM {
 struct Waiter {
     volatile int *gave_up;
     int *err;
@@ -83,6 +87,7 @@ struct Waiter {
         return __all_sync(0xffffffffu, a && b && c) || (warp(bar0, parity0) && warp(bar1, parity1) && warp(bar2, parity2));
     }
 };
+}  // namespace PKV_FORM
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar)
 {
