@@ -41,8 +41,9 @@ int kv_attention_q4(const kv_attn_desc *d, const kv_attn_batch *batch, const kv_
     if (workspace == nullptr) return KV_ERR_INVALID_ARG;
     if (!aligned16(workspace) || ((uintptr_t)lse & 3u)) return KV_ERR_ALIGN;
     // By the rows (tokens times query heads of a key head) that a request has on average.  Each side measured, 16 requests of 8000 with 8 key
-    // heads of 128 in bf16, groups of 4: 8 rows in units of 8 46 us, of 16 57; 16 rows with few rows' kernel 67, many rows' 104; 20 rows 95 and 106;
-    // 32 rows 98 and 106; 36 rows 124 and 111.  (64 requests of 2000: 32 rows 97 and 127, 48 rows 137 and 131; one of 120000: 32 rows 89 and 104.)
+    // heads of 128 in bf16, groups of 4: 8 rows in units of 8 46 us, of 16 57; 16 rows with few rows' kernel 66, many rows' 104; 20 rows 93 and 106;
+    // 32 rows 96 and 106; 36 rows 122 and 111.  (64 requests of 2000: 32 rows 94 and 127, 48 rows 133 and 131; one of 120000: 32 rows 104 and 105.)
+    // One kernel a call: 200 decoding requests of 1000 to 4000 take 114 us, a chunk of 1024 tokens over 8192 135 (of 4096 368), in one call 681 (806).
     const bool many = batch->n_tokens * group > 32ll * batch->n_reqs;
     const int rows = batch->n_tokens * group <= 8ll * batch->n_reqs ? 8 : 16;
     Q4Params p = {};

@@ -9,14 +9,14 @@
 // tcgen05 product would want them written to shared memory, twice the bytes of the cache's 16-bit rows a cycle
 // (82 in and 82 out of 128), or both operands in 4 bits, which queries and weights are not.
 //
-// Measured: 64 requests of 4096 to 12288 tokens, 32 heads over 8 of 128, pages of 16: 113 us, 82% of the copy rate: about 98% between the
-// first tile and the last, 8 us before and 5 to 12 after (ends of pieces, joins); with 16 key heads 213 us, 86%.  The integer pipe is half
-// taken, by codes.  12 rows over 64 requests of 8000: 152 us, 59%: two products of 8 rows, twice the exponentials.
+// Measured: 64 requests of 4096 to 12288 tokens, 32 heads over 8 of 128, pages of 16: 114 us, 81% of the copy rate: about 98% between the
+// first tile and the last, 8 us before and 5 to 12 after (ends of pieces, joins); with 16 key heads 212 us, 87%.  The integer pipe is half
+// taken, by codes.  12 rows over 64 requests of 8000: 150 us, 59%: two products of 8 rows, twice the exponentials.
 //
 // Queries are brought to [1, 2) by a power of two a row and held in fp16, weights are fp16, 2^7 times as large (kv_tensor.cuh,
 // weight_offset); sums are in 32 bits.  The reference m of a row's weights is one of its scores, as the product left them, and is taken off
 // before the product with c: 2^(c (s - m) + 7) with s - m <= 8 / c, which stays below fp16's 2^16 whatever the size of s.  (With c s and c m rounded
-// by themselves it did not from scaled scores of 10^7 on.)
+// by themselves it did not from scaled scores of 10^7 on; the long decode batch takes 1 us more so, twelve rows 2 us less.)
 //
 // One persistent CTA per SM; a unit is one request's rows of as many key heads as there are warps for, or fewer (launch_few).
 //   warps 0, 1 (to 3)  bring rows of keys and of values by TMA, one for each run of slots inside a page, into rings of tiles
@@ -947,8 +947,9 @@ int launch_few(FewParams &p, const DeviceInfo *dev, cudaStream_t s)
     while (all % heads) heads--;
     // A unit of few heads lies in fewer pieces, of fewer bytes, when many CTAs share a request: joining them is bound by what one SM reads
     // (45 GB/s).  But rows that come apart into heads cost more to load, so that this pays for short contexts only.  8 key heads of 128
-    // and a unit of 8, 4, 2 of them, one request of 120000 and of 8000: 12 rows 74, 64, 58 and 40, 28, 22 us; 8 rows 53, 49, 50 and 30, 21, 19
-    // us; eight requests of 15000: 62, 59, 58 and 46, 47, 51; 64 requests of 8000: 12 rows 152, 177, 245, 4 rows 113, 181, 244.
+    // and a unit of 8, 4, 2 of them, one request of 120000 and of 8000: 12 rows 72, 61, 56 and 40, 26, 21 us; 8 rows 52, 49, 49 and 29, 22, 20
+    // us; eight requests of 15000: 61, 60, 66 and 46, 51, 62; 64 requests of 8000: 12 rows 150, 198, 263, 4 rows 110, 176, 248.
+    // The lengths are on the device, so the table's width stands for them: two requests of 8000, 12 rows, take 21 us, under a table for 128000 41.
     constexpr int kPieces = NT == 1 ? 40 : 10;            // of a unit, above which it gets fewer heads
     constexpr int64_t kShort = NT == 1 ? 6144 : 10240;    // keys times heads an SM, up to which (where the two would meet for one request)
     const int64_t seen = p.b.window ? std::min<int64_t>(p.b.max_tokens, (int64_t)p.b.window + p.b.n_tokens) : p.b.max_tokens;

@@ -17,8 +17,8 @@
 //
 // Measured (8 prompts of 1000 to 2000 tokens, 32 heads and 8 key heads of 128): 51 us in 16 bits, 6.1 TB/s of a measured 6.65; a CTA
 // that takes one token and loads after its angles 84.  8000 tokens of 20 heads of 192, 64 of them turned: 18.5 us, 6.65 TB/s.  Into 4 bits
-// 65 us (111), 5.0 TB/s, two thirds of the issue slots taken by the exact products and the rounding.  Two numbers an instruction
-// (f32x2) took 8 % off it.  Pieces are copied to shared memory rather than loaded ahead into registers: the copies of values from one
+// 66 us (111), 5.0 TB/s, 59 where the values held are not wanted: 2.6 of 4 instructions a cycle, of the exact products and the rounding, the
+// rest waits at a token's barrier.  Two numbers an instruction (f32x2) took 8 % off it.  Pieces are copied to shared memory rather than loaded ahead into registers: the copies of values from one
 // iteration to the next waited for them (4 bits 86).  The table of angles lies in shared memory and a warp finds the places of 32 tokens
 // at once, as loads that depend on one another took longer than the rest of an iteration (4 bits 86, 16 bits 56).
 #include <algorithm>
