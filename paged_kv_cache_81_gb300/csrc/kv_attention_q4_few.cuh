@@ -14,7 +14,8 @@
 // taken, by codes.  12 rows over 64 requests of 8000: 150 us, 59%: two products of 8 rows, twice the exponentials.
 //
 // Queries are brought to [1, 2) by a power of two a row and held in fp16, weights are fp16, 2^7 times as large (kv_tensor.cuh,
-// weight_offset); sums are in 32 bits.  The reference m of a row's weights is one of its scores, as the product left them, and is taken off
+// weight_offset); sums are in 32 bits.  fp16 since a product's operands have one type, and codes times scales are exact in it but not in bf16; a
+// second product for what the rounding of weights leaves would double the second half of the work.  The reference m of a row's weights is one of its scores, as the product left them, and is taken off
 // before the product with c: 2^(c (s - m) + 7) with s - m <= 8 / c, which stays below fp16's 2^16 whatever the size of s.  (With c s and c m rounded
 // by themselves it did not from scaled scores of 10^7 on; the long decode batch takes 1 us more so, twelve rows 2 us less.)
 //
